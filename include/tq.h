@@ -393,6 +393,190 @@ tq_status tq_decode_attn(const tq_attn_args* args, const tq_codec* k_codec,
 tq_status tq_decode_attn_noalloc(const tq_attn_args* args, const tq_codec* k_codec,
                                  const tq_codec* v_codec, void* stream);
 
+/*
+ * Rotary positions and append.  For each layer, sequence b and new token
+ * t < T_b (T_b = min(max(q_lens[b], 0), t_q), or t_q without q_lens): the
+ * queries are rotated into q_out, the keys rotated into ring slot
+ * (tail_start + tail_len + t) % tail_cap and the values copied into the same
+ * slot; tail_len_out receives tail_len + T_b.  Of a head's coordinates the
+ * rot_dim from rot_start on turn in rot_dim/2 pairs: pair p joins coordinates
+ * rot_start + p and rot_start + rot_dim/2 + p, or, with pair_adjacent,
+ * rot_start + 2p and rot_start + 2p + 1; it turns by the angle
+ * positions[pair_axis[p]][b][t] * inv_freq[p]:
+ *   y0 = rot_scale (x0 cos - x1 sin),  y1 = rot_scale (x1 cos + x0 sin),
+ * in f32 from an angle reduced exactly (positions of any size and sign), each
+ * output rounded once to bf16.  The other coordinates are copied.  Several
+ * axes (time, height, width) are several rows of `positions`.
+ * A sequence whose new tokens do not fit the ring (tail_len + T_b > tail_cap,
+ * or a tail_len outside [0, tail_cap]) is not appended and keeps its tail_len,
+ * as tq_evict leaves a full record array; its queries are still rotated.
+ * Rows t >= T_b of q_out and ring slots of no new token are not touched.
+ */
+#define TQ_MAX_AXES 4
+typedef struct {
+  int32_t n_layers, batch, t_q, n_q_heads, n_kv_heads, head_dim;
+  /* bf16, element (l, b, t, h, j) at x + l*layer_stride + b*batch_stride +
+   * t*token_stride + h*head_dim + j; 16-byte aligned, strides multiples of 8.
+   * k and v share theirs.  q may be NULL (n_q_heads 0).  v and v_tail are NULL
+   * together where keys and values share one ring. */
+  const void* q;
+  const void* k;
+  const void* v;
+  int64_t q_layer_stride, q_batch_stride, q_token_stride;
+  int64_t kv_layer_stride, kv_batch_stride, kv_token_stride;
+  void* q_out; /* may be q, with the same strides */
+  int64_t q_out_layer_stride, q_out_batch_stride, q_out_token_stride;
+  const int32_t* q_lens;    /* device [batch]; NULL = t_q everywhere */
+  const int32_t* positions; /* device [n_axes][batch][t_q] */
+  int32_t n_axes;           /* 1..TQ_MAX_AXES */
+  int32_t rot_start;        /* multiple of 8 */
+  int32_t rot_dim;          /* multiple of 16, >= 0 (0: nothing turns) */
+  int32_t pair_adjacent;
+  const float* inv_freq;    /* device f32 [rot_dim/2], finite */
+  uint8_t pair_axis[256];   /* axis of pair p, below n_axes */
+  float rot_scale;          /* finite */
+  /* ring: bf16 [L][B][Hkv][tail_cap][d], as in tq_evict_args */
+  void* k_tail;
+  void* v_tail;
+  int64_t tail_layer_stride;
+  int32_t tail_cap;
+  const int32_t* tail_start; /* device [L][B]; NULL = 0 */
+  const int32_t* tail_len;   /* device [L][B] */
+  int32_t* tail_len_out;     /* device [L][B]; may be tail_len (then one more small launch) */
+  /* accumulated weights (tq_attn_mass), optional: the new tokens' entries
+   * 128 n_chunks + tail_len + t (those below mass_cap) start at 0 */
+  float* mass;
+  int64_t mass_layer_stride;
+  int32_t mass_cap;
+  const int32_t* n_chunks;   /* device [L][B]; NULL = 0 */
+} tq_append_args;
+
+tq_status tq_append(const tq_append_args* args, void* stream);
+
+/*
+ * Queries of up to t_q new tokens per sequence against a cache.  With
+ * total = 128 n_chunks + tail_len (the new tokens' own keys included) query t
+ * of sequence b sees the tokens of index < total, and when `causal` is set of
+ * index <= total - T_b + t only: the newest T_b tokens are the queries' own.
+ * T_b and q_lens as in tq_append.
+ */
+typedef struct {
+  int32_t n_layers, batch, t_q, n_q_heads, n_kv_heads, head_dim;
+  float scale;   /* softmax scale applied to q . k */
+  float softcap; /* as in tq_attn_args; 0 = none */
+  int32_t causal;
+  /* bf16, element (l, b, t, h, j) at x + l*layer_stride + b*batch_stride +
+   * t*token_stride + h*head_dim + j; 16-byte aligned, strides multiples of 8 */
+  const void* q;
+  int64_t q_layer_stride, q_batch_stride, q_token_stride;
+  void* out; /* tq_prefill_attn only (tq_attn_mass ignores it) */
+  int64_t out_layer_stride, out_batch_stride, out_token_stride;
+  const int32_t* q_lens; /* device [batch]; NULL = t_q everywhere */
+  /* the cache, as in tq_attn_args (records may be NULL with n_chunks and
+   * block_table; the ring may be NULL with tail_len and tail_start).
+   * tq_attn_mass reads no values: v_rec and v_tail may be NULL there. */
+  const void* k_rec;
+  const void* v_rec;
+  int64_t k_rec_layer_stride, v_rec_layer_stride;
+  int32_t rec_cap;
+  const void* k_tail;
+  const void* v_tail;
+  int64_t tail_layer_stride;
+  int32_t tail_cap;
+  const int32_t* n_chunks;
+  const int32_t* tail_start;
+  const int32_t* tail_len;
+  int32_t max_chunks; /* host upper bound of n_chunks */
+  int32_t max_tail;   /* host upper bound of tail_len */
+  const int32_t* block_table;
+  int32_t table_stride;
+  int32_t splits; /* context splits per row tile; 0 = automatic */
+} tq_query_args;
+
+/*
+ * Attention of several query tokens per sequence over records and ring:
+ *   out[l][b][t][h] = sum_i softmax_i(cap(scale q . k_i)) v_i
+ * over the tokens that query sees, rounded once to bf16.  The records are
+ * dequantised to f16 (centroids and rotated queries each within half an f16
+ * step, f32 accumulation and softmax statistics, weights rounded to f16; the
+ * ring's bf16 keys, values and queries enter exactly, its weights rounded to
+ * bf16): the output is within bf16's own precision of the exact sum.  A row
+ * that sees no token is zero; rows t >= T_b are not touched.
+ * workspace: device, 256-byte aligned; contents need no initialisation.
+ * Calls that overlap on the GPU need workspaces of their own.
+ */
+size_t tq_prefill_attn_workspace_size(const tq_query_args* args, const tq_codec* k_codec,
+                                      const tq_codec* v_codec);
+tq_status tq_prefill_attn(const tq_query_args* args, const tq_codec* k_codec, const tq_codec* v_codec,
+                          void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Accumulated attention weight.  For every cached token i of (l, b, kv head h):
+ *   mass = decay * mass + sum over the kv head's query heads and the T_b
+ *          queries of softmax_i(cap(scale q . k_i))
+ * at mass + l*mass_layer_stride + (b*n_kv_heads + h)*mass_cap + i, f32; a
+ * record's token 128 c + s comes first, the ring's tokens follow from
+ * 128 n_chunks on, so that tq_evict moves no entry.  Entries of index >= total
+ * are not touched.  mass_cap >= 128 max_chunks + max_tail.  Sums run in a
+ * fixed order (no atomics).  decay: finite, >= 0.
+ */
+size_t tq_attn_mass_workspace_size(const tq_query_args* args, const tq_codec* k_codec);
+tq_status tq_attn_mass(const tq_query_args* args, const tq_codec* k_codec, float* mass,
+                       int64_t mass_layer_stride, int32_t mass_cap, float decay, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * Eviction by accumulated weight.  Of the 128 n compressed tokens of every
+ * (layer, sequence, kv head) the min(n, keep_chunks) * 128 tokens remain that
+ * are among the first `sink` or the newest `recent` of them, or have the
+ * largest mass after those (ties, and NaN below every number: the lower index
+ * stays), in their order: record r of the destination holds tokens
+ * 128 r .. 128 r + 127 of those that remain, codes, scales and side lists bit
+ * for bit (a side list that outgrows outlier_cap drops the entries that do not
+ * fit, as tq_encode does).  Every kv head chooses its own tokens.  mass moves
+ * along, the ring's entries behind it; n_chunks_dst = min(n, keep_chunks).
+ * The ring itself, tail_start and tail_len stay as they are.
+ *
+ * In place (k_dst == k_rec, and v_dst, mass_dst, n_chunks_dst likewise equal
+ * to their sources, dst fields of the layout ignored): the entries of mass
+ * behind the remaining tokens become 0, dropped records keep their bytes;
+ * with a block table every block named must belong to one sequence only.
+ * Out of place: the destination must not overlap the source; only records
+ * below n_chunks_dst and entries of remaining tokens are written.
+ */
+typedef struct {
+  int32_t n_layers, batch, n_kv_heads;
+  void* k_rec; /* records as in tq_evict_args */
+  void* v_rec; /* may equal k_rec: keys and values share records */
+  int64_t k_rec_layer_stride, v_rec_layer_stride;
+  int32_t rec_cap;
+  const int32_t* block_table;
+  int32_t table_stride;
+  void* k_dst;
+  void* v_dst;
+  int64_t k_dst_layer_stride, v_dst_layer_stride;
+  int32_t dst_cap;
+  const int32_t* dst_table; /* block table of the destination; NULL = contiguous */
+  int32_t dst_table_stride;
+  float* mass;     /* f32 at mass + l*mass_layer_stride + (b*n_kv_heads + h)*mass_cap + i */
+  float* mass_dst;
+  int64_t mass_layer_stride, mass_dst_layer_stride;
+  int32_t mass_cap, mass_dst_cap; /* >= 128 max_chunks + max_tail; >= 128 keep_chunks + max_tail */
+  int32_t* n_chunks;       /* device [L][B] */
+  int32_t* n_chunks_dst;
+  const int32_t* tail_len; /* device [L][B]; NULL = 0 */
+  int32_t max_chunks, max_tail; /* host upper bounds */
+  int32_t keep_chunks;     /* >= 1 */
+  int32_t sink, recent;    /* >= 0, sink + recent <= 128 keep_chunks */
+  int32_t* kept;           /* optional, device [L][B][Hkv][128 keep_chunks]: the index each
+                              remaining token had; entries of no token are not touched */
+} tq_evict_mass_args;
+
+size_t tq_evict_mass_workspace_size(const tq_evict_mass_args* args, const tq_codec* k_codec,
+                                    const tq_codec* v_codec);
+tq_status tq_evict_mass(const tq_evict_mass_args* args, const tq_codec* k_codec, const tq_codec* v_codec,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -58,6 +58,48 @@ class tq_attn_plan(ctypes.Structure):
                 ("warps_per_cta", c_i32), ("workspace_bytes", c_u64)]
 
 
+class tq_append_args(ctypes.Structure):
+    _fields_ = [("n_layers", c_i32), ("batch", c_i32), ("t_q", c_i32), ("n_q_heads", c_i32), ("n_kv_heads", c_i32),
+                ("head_dim", c_i32), ("q", c_p), ("k", c_p), ("v", c_p),
+                ("q_layer_stride", c_i64), ("q_batch_stride", c_i64), ("q_token_stride", c_i64),
+                ("kv_layer_stride", c_i64), ("kv_batch_stride", c_i64), ("kv_token_stride", c_i64),
+                ("q_out", c_p), ("q_out_layer_stride", c_i64), ("q_out_batch_stride", c_i64),
+                ("q_out_token_stride", c_i64),
+                ("q_lens", c_p), ("positions", c_p), ("n_axes", c_i32), ("rot_start", c_i32), ("rot_dim", c_i32),
+                ("pair_adjacent", c_i32), ("inv_freq", c_p), ("pair_axis", ctypes.c_uint8 * 256),
+                ("rot_scale", c_f32),
+                ("k_tail", c_p), ("v_tail", c_p), ("tail_layer_stride", c_i64), ("tail_cap", c_i32),
+                ("tail_start", c_p), ("tail_len", c_p), ("tail_len_out", c_p),
+                ("mass", c_p), ("mass_layer_stride", c_i64), ("mass_cap", c_i32), ("n_chunks", c_p)]
+
+
+class tq_query_args(ctypes.Structure):
+    _fields_ = [("n_layers", c_i32), ("batch", c_i32), ("t_q", c_i32), ("n_q_heads", c_i32), ("n_kv_heads", c_i32),
+                ("head_dim", c_i32), ("scale", c_f32), ("softcap", c_f32), ("causal", c_i32),
+                ("q", c_p), ("q_layer_stride", c_i64), ("q_batch_stride", c_i64), ("q_token_stride", c_i64),
+                ("out", c_p), ("out_layer_stride", c_i64), ("out_batch_stride", c_i64), ("out_token_stride", c_i64),
+                ("q_lens", c_p),
+                ("k_rec", c_p), ("v_rec", c_p), ("k_rec_layer_stride", c_i64), ("v_rec_layer_stride", c_i64),
+                ("rec_cap", c_i32),
+                ("k_tail", c_p), ("v_tail", c_p), ("tail_layer_stride", c_i64), ("tail_cap", c_i32),
+                ("n_chunks", c_p), ("tail_start", c_p), ("tail_len", c_p),
+                ("max_chunks", c_i32), ("max_tail", c_i32), ("block_table", c_p), ("table_stride", c_i32),
+                ("splits", c_i32)]
+
+
+class tq_evict_mass_args(ctypes.Structure):
+    _fields_ = [("n_layers", c_i32), ("batch", c_i32), ("n_kv_heads", c_i32),
+                ("k_rec", c_p), ("v_rec", c_p), ("k_rec_layer_stride", c_i64), ("v_rec_layer_stride", c_i64),
+                ("rec_cap", c_i32), ("block_table", c_p), ("table_stride", c_i32),
+                ("k_dst", c_p), ("v_dst", c_p), ("k_dst_layer_stride", c_i64), ("v_dst_layer_stride", c_i64),
+                ("dst_cap", c_i32), ("dst_table", c_p), ("dst_table_stride", c_i32),
+                ("mass", c_p), ("mass_dst", c_p), ("mass_layer_stride", c_i64), ("mass_dst_layer_stride", c_i64),
+                ("mass_cap", c_i32), ("mass_dst_cap", c_i32),
+                ("n_chunks", c_p), ("n_chunks_dst", c_p), ("tail_len", c_p),
+                ("max_chunks", c_i32), ("max_tail", c_i32), ("keep_chunks", c_i32), ("sink", c_i32),
+                ("recent", c_i32), ("kept", c_p)]
+
+
 ATTN_KERNELS = {0: "none", 1: "cuda_core", 2: "cuda_core_warp", 3: "mma", 4: "mma512", 5: "tcgen05"}
 
 _SIGS = {
@@ -86,6 +128,18 @@ _SIGS = {
                                               ctypes.POINTER(tq_codec), c_p]),
     "tq_decode_attn_plan": (ctypes.c_int, [ctypes.POINTER(tq_attn_args), ctypes.POINTER(tq_codec),
                                            ctypes.POINTER(tq_codec), ctypes.POINTER(tq_attn_plan)]),
+    "tq_append": (ctypes.c_int, [ctypes.POINTER(tq_append_args), c_p]),
+    "tq_prefill_attn_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(tq_query_args), ctypes.POINTER(tq_codec),
+                                                         ctypes.POINTER(tq_codec)]),
+    "tq_prefill_attn": (ctypes.c_int, [ctypes.POINTER(tq_query_args), ctypes.POINTER(tq_codec),
+                                       ctypes.POINTER(tq_codec), c_p, ctypes.c_size_t, c_p]),
+    "tq_attn_mass_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(tq_query_args), ctypes.POINTER(tq_codec)]),
+    "tq_attn_mass": (ctypes.c_int, [ctypes.POINTER(tq_query_args), ctypes.POINTER(tq_codec), c_p, c_i64, c_i32,
+                                    c_f32, c_p, ctypes.c_size_t, c_p]),
+    "tq_evict_mass_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(tq_evict_mass_args), ctypes.POINTER(tq_codec),
+                                                       ctypes.POINTER(tq_codec)]),
+    "tq_evict_mass": (ctypes.c_int, [ctypes.POINTER(tq_evict_mass_args), ctypes.POINTER(tq_codec),
+                                     ctypes.POINTER(tq_codec), c_p, ctypes.c_size_t, c_p]),
 }
 
 NOALLOC_WORKSPACE_BYTES = 8 << 20
@@ -373,4 +427,331 @@ def decode_attn(*, k_codec=None, v_codec=None, workspace=None, stream=None, **kw
     if workspace is None or workspace.numel() < need:
         workspace = torch.empty(need, dtype=torch.uint8, device=kw["q"].device)
     tq_decode_attn(a, k_codec, v_codec, workspace, stream)
+    return workspace
+
+
+# ---------------------------------------------------------------------------
+# several new tokens: append, prefill attention, accumulated weights, eviction
+# ---------------------------------------------------------------------------
+def _need(ok, why: str):
+    if not ok:
+        raise ValueError(why)
+
+
+def _check_tensors(dtype_of: dict):
+    """Every tensor given is of its dtype, on one CUDA device, which is the current one."""
+    import torch
+    dev = torch.device("cuda", torch.cuda.current_device()) if torch.cuda.is_available() else None
+    for name, (t, dtype) in dtype_of.items():
+        if t is not None:
+            _need(t.dtype == dtype, f"{name}: expected {dtype}, got {t.dtype}")
+            _need(dev is None or t.device == dev, f"{name} is on {t.device}, not on the current device {dev}")
+
+
+def _heads_packed(t, name: str, d: int):
+    """(layer, batch, token) strides of a [L, B, T, heads, d] view whose heads and dims are packed."""
+    _need(t.dim() == 5 and t.stride(4) == 1 and (t.shape[3] == 1 or t.stride(3) == d),
+          f"{name}: expected [L, B, T, heads, d] with heads and dims packed")
+    return t.stride(0), t.stride(1), t.stride(2)
+
+
+def _ring_cap(t, name: str):
+    L, B, H, cap, d = t.shape
+    _need(t.stride(4) == 1 and t.stride(3) == d and (H == 1 or t.stride(2) == cap * d) and
+          (B == 1 or t.stride(1) == H * cap * d), f"{name}: a layer's ring [B, Hkv, cap, d] must be contiguous")
+    return cap
+
+
+def _counts(t, name: str, L: int, B: int):
+    _need(t is None or (t.is_contiguous() and tuple(t.shape) == (L, B)), f"{name}: expected contiguous int32 [{L}, {B}]")
+
+
+def rope_pair_axis(sections, interleaved: bool = False):
+    """Axis of every frequency pair for `sections` (pairs per axis): each axis turns its own run of
+    frequencies, or, interleaved, the axes take turns (0, 1, 2, 0, 1, 2, ...) until a section is used up."""
+    if not interleaved:
+        return [a for a, n in enumerate(sections) for _ in range(n)]
+    left, out = list(sections), []
+    while any(left):
+        for a in range(len(left)):
+            if left[a]:
+                left[a] -= 1
+                out.append(a)
+    return out
+
+
+def make_append_args(*, k, k_tail, tail_len, tail_len_out=None, v=None, v_tail=None, q=None, q_out=None,
+                     positions=None, inv_freq=None, pair_axis=None, rot_start: int = 0, pair_adjacent: bool = False,
+                     rot_scale: float = 1.0, tail_start=None, q_lens=None, mass=None, n_chunks=None) -> tq_append_args:
+    """tq_append_args from tensors.  q, k, v, q_out: bf16 views [L, B, T, heads, d] (heads and dims packed;
+    k and v with equal strides); k_tail, v_tail: bf16 [L, B, Hkv, cap, d] (v and v_tail None where keys and
+    values share a ring); positions: int32 [axes, B, T]; inv_freq: f32 [pairs], 2 * pairs coordinates from
+    rot_start on turn; pair_axis: axis of each pair (default 0; rope_pair_axis); counters int32 [L, B]
+    (tail_len_out defaults to tail_len); mass: f32 [L, B, Hkv, cap]."""
+    import torch
+    i32, f32, bf = torch.int32, torch.float32, torch.bfloat16
+    _check_tensors(dict(q=(q, bf), k=(k, bf), v=(v, bf), q_out=(q_out, bf), k_tail=(k_tail, bf), v_tail=(v_tail, bf),
+                        positions=(positions, i32), inv_freq=(inv_freq, f32), tail_start=(tail_start, i32),
+                        tail_len=(tail_len, i32), tail_len_out=(tail_len_out, i32), q_lens=(q_lens, i32),
+                        mass=(mass, f32), n_chunks=(n_chunks, i32)))
+    L, B, T, Hkv, d = k.shape
+    a = tq_append_args()
+    a.n_layers, a.batch, a.t_q, a.n_kv_heads, a.head_dim = L, B, T, Hkv, d
+    a.k, (a.kv_layer_stride, a.kv_batch_stride, a.kv_token_stride) = k.data_ptr(), _heads_packed(k, "k", d)
+    if v is not None:
+        _need(v.shape == k.shape and _heads_packed(v, "v", d) == _heads_packed(k, "k", d),
+              "v: expected k's shape and strides")
+        a.v = v.data_ptr()
+    if q is not None:
+        _need(q_out is not None and q_out.shape == q.shape and q.shape[:3] == k.shape[:3] and q.shape[4] == d,
+              "q, q_out: expected [L, B, T, Hq, d] like k")
+        a.n_q_heads = q.shape[3]
+        a.q, (a.q_layer_stride, a.q_batch_stride, a.q_token_stride) = q.data_ptr(), _heads_packed(q, "q", d)
+        a.q_out = q_out.data_ptr()
+        a.q_out_layer_stride, a.q_out_batch_stride, a.q_out_token_stride = _heads_packed(q_out, "q_out", d)
+    _need(tuple(k_tail.shape[:3]) == (L, B, Hkv) and k_tail.shape[4] == d, "k_tail: expected [L, B, Hkv, cap, d]")
+    a.tail_cap = _ring_cap(k_tail, "k_tail")
+    a.k_tail, a.tail_layer_stride = k_tail.data_ptr(), k_tail.stride(0)
+    if v_tail is not None:
+        _need(v_tail.shape == k_tail.shape and v_tail.stride() == k_tail.stride(), "v_tail: expected k_tail's layout")
+        a.v_tail = v_tail.data_ptr()
+    if inv_freq is not None:
+        n = inv_freq.numel()
+        _need(inv_freq.is_contiguous() and 0 < 2 * n <= d, "inv_freq: expected contiguous f32 [pairs], 2 * pairs <= d")
+        _need(positions is not None and positions.is_contiguous() and positions.dim() == 3 and
+              tuple(positions.shape[1:]) == (B, T), "positions: expected contiguous int32 [axes, B, T]")
+        axis = [0] * n if pair_axis is None else [int(x) for x in pair_axis]
+        _need(len(axis) == n and all(0 <= x < 256 for x in axis), "pair_axis: expected one axis for each pair")
+        a.n_axes, a.rot_dim, a.rot_start = positions.shape[0], 2 * n, rot_start
+        a.positions, a.inv_freq = positions.data_ptr(), inv_freq.data_ptr()
+        a.pair_axis[:n] = axis
+    a.pair_adjacent, a.rot_scale = int(pair_adjacent), rot_scale
+    out = tail_len if tail_len_out is None else tail_len_out
+    for name, t in (("tail_start", tail_start), ("tail_len", tail_len), ("tail_len_out", out), ("n_chunks", n_chunks)):
+        _counts(t, name, L, B)
+    _need(q_lens is None or (q_lens.is_contiguous() and tuple(q_lens.shape) == (B,)), "q_lens: expected int32 [B]")
+    a.tail_start, a.tail_len, a.tail_len_out = _ptr(tail_start), tail_len.data_ptr(), out.data_ptr()
+    a.q_lens, a.n_chunks = _ptr(q_lens), _ptr(n_chunks)
+    if mass is not None:
+        a.mass, a.mass_layer_stride, a.mass_cap = mass.data_ptr(), *_mass_layout(mass, L, B, Hkv)
+    a._tensors = (q, k, v, q_out, positions, inv_freq, k_tail, v_tail, tail_start, tail_len, out, q_lens, mass,
+                  n_chunks)
+    return a
+
+
+def _mass_layout(mass, L: int, B: int, Hkv: int):
+    cap = mass.shape[-1]
+    _need(tuple(mass.shape[:3]) == (L, B, Hkv) and mass.dim() == 4 and mass.stride(3) == 1 and
+          (Hkv == 1 or mass.stride(2) == cap) and (B == 1 or mass.stride(1) == Hkv * cap),
+          "mass: expected f32 [L, B, Hkv, cap], contiguous within a layer")
+    return mass.stride(0), cap
+
+
+def tq_append(args: tq_append_args, stream=None):
+    """Rotate queries and keys and append keys and values to the ring (include/tq.h)."""
+    _check("tq_append", load().tq_append(ctypes.byref(args), _stream(stream)))
+
+
+def make_query_args(*, q, scale: float, out=None, softcap: float = 0.0, causal: bool = True, q_lens=None, k_rec=None,
+                    v_rec=None, k_tail=None, v_tail=None, n_chunks=None, tail_start=None, tail_len=None,
+                    max_chunks: int = 0, max_tail: int = 0, block_table=None, splits: int = 0,
+                    n_kv_heads: int | None = None) -> tq_query_args:
+    """tq_query_args from tensors.  q, out: bf16 views [L, B, T, Hq, d] (heads and dims packed; out for
+    tq_prefill_attn); the cache as for make_attn_args; q_lens: int32 [B]."""
+    import torch
+    i32, bf = torch.int32, torch.bfloat16
+    _check_tensors(dict(q=(q, bf), out=(out, bf), k_rec=(k_rec, torch.uint8), v_rec=(v_rec, torch.uint8),
+                        k_tail=(k_tail, bf), v_tail=(v_tail, bf), n_chunks=(n_chunks, i32),
+                        tail_start=(tail_start, i32), tail_len=(tail_len, i32), q_lens=(q_lens, i32),
+                        block_table=(block_table, i32)))
+    L, B, T, Hq, d = q.shape
+    a = tq_query_args()
+    a.n_layers, a.batch, a.t_q, a.n_q_heads, a.head_dim = L, B, T, Hq, d
+    a.scale, a.softcap, a.causal, a.splits = scale, softcap, int(causal), splits
+    a.q, (a.q_layer_stride, a.q_batch_stride, a.q_token_stride) = q.data_ptr(), _heads_packed(q, "q", d)
+    if out is not None:
+        _need(out.shape == q.shape, "out: expected q's shape")
+        a.out, (a.out_layer_stride, a.out_batch_stride, a.out_token_stride) = (out.data_ptr(),
+                                                                              _heads_packed(out, "out", d))
+    paged = block_table is not None
+    src = k_rec if k_rec is not None else k_tail
+    Hkv = n_kv_heads if n_kv_heads is not None else (src.shape[2] if src is not None else Hq)
+    a.n_kv_heads = Hkv
+    for r, name in ((k_rec, "k_rec"), (v_rec, "v_rec")):
+        if r is not None:
+            lead = (r.shape[0], r.shape[2]) if paged else (r.shape[0], r.shape[1], r.shape[2])
+            _need(lead == ((L, Hkv) if paged else (L, B, Hkv)) and (r.shape[0] == 0 or r[0].is_contiguous()),
+                  f"{name}: expected records [L, B, Hkv, cap, bytes] or a pool [L, blocks, Hkv, bytes], "
+                  "contiguous within a layer")
+    if k_rec is not None:
+        a.k_rec, a.k_rec_layer_stride = k_rec.data_ptr(), k_rec.stride(0)
+        a.rec_cap = k_rec.shape[1] if paged else k_rec.shape[3]
+    if v_rec is not None:
+        _need(k_rec is not None and v_rec.shape[:-1] == k_rec.shape[:-1], "v_rec: expected k_rec's layout")
+        a.v_rec, a.v_rec_layer_stride = v_rec.data_ptr(), v_rec.stride(0)
+    if paged:
+        _need(block_table.is_contiguous() and block_table.dim() == 2 and block_table.shape[0] == B,
+              "block_table: expected contiguous int32 [B, stride]")
+        a.block_table, a.table_stride = block_table.data_ptr(), block_table.shape[1]
+    if k_tail is not None:
+        _need(tuple(k_tail.shape[:3]) == (L, B, Hkv) and k_tail.shape[4] == d, "k_tail: expected [L, B, Hkv, cap, d]")
+        a.k_tail, a.tail_layer_stride, a.tail_cap = k_tail.data_ptr(), k_tail.stride(0), _ring_cap(k_tail, "k_tail")
+    if v_tail is not None:
+        _need(k_tail is not None and v_tail.shape == k_tail.shape and v_tail.stride() == k_tail.stride(),
+              "v_tail: expected k_tail's layout")
+        a.v_tail = v_tail.data_ptr()
+    for name, t in (("n_chunks", n_chunks), ("tail_start", tail_start), ("tail_len", tail_len)):
+        _counts(t, name, L, B)
+    _need(q_lens is None or (q_lens.is_contiguous() and tuple(q_lens.shape) == (B,)), "q_lens: expected int32 [B]")
+    a.n_chunks, a.tail_start, a.tail_len, a.q_lens = _ptr(n_chunks), _ptr(tail_start), _ptr(tail_len), _ptr(q_lens)
+    a.max_chunks, a.max_tail = max_chunks, max_tail
+    a._tensors = (q, out, k_rec, v_rec, k_tail, v_tail, n_chunks, tail_start, tail_len, q_lens, block_table)
+    return a
+
+
+def _raw(codec):
+    return None if codec is None else ctypes.byref(codec.c)
+
+
+def _check_records(codec, rec, name: str):
+    _need(codec is None or rec is None or rec.shape[-1] == codec.record_bytes,
+          f"{name}: records are not of the codec's {codec.record_bytes if codec else 0} bytes")
+
+
+def tq_prefill_attn_workspace_size(args: tq_query_args, k_codec: Codec | None, v_codec: Codec | None) -> int:
+    n = load().tq_prefill_attn_workspace_size(ctypes.byref(args), _raw(k_codec), _raw(v_codec))
+    if n == 0:
+        raise TqError("tq_prefill_attn_workspace_size", TQ_ERR_INVALID_ARG)
+    return int(n)
+
+
+def tq_prefill_attn(args: tq_query_args, k_codec: Codec | None, v_codec: Codec | None, workspace, stream=None):
+    """Attention of several query tokens per sequence over records and ring, bf16 out (include/tq.h)."""
+    _check("tq_prefill_attn", load().tq_prefill_attn(ctypes.byref(args), _raw(k_codec), _raw(v_codec), _ptr(workspace),
+                                                     workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def prefill_attn(*, k_codec=None, v_codec=None, workspace=None, stream=None, **kw):
+    """Convenience: build the arguments, size/allocate the workspace if not given, run."""
+    import torch
+    _check_records(k_codec, kw.get("k_rec"), "k_rec")
+    _check_records(v_codec, kw.get("v_rec"), "v_rec")
+    a = make_query_args(**kw)
+    need = tq_prefill_attn_workspace_size(a, k_codec, v_codec)
+    if workspace is None or workspace.numel() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=kw["q"].device)
+    tq_prefill_attn(a, k_codec, v_codec, workspace, stream)
+    return workspace
+
+
+def tq_attn_mass_workspace_size(args: tq_query_args, k_codec: Codec | None) -> int:
+    n = load().tq_attn_mass_workspace_size(ctypes.byref(args), _raw(k_codec))
+    if n == 0:
+        raise TqError("tq_attn_mass_workspace_size", TQ_ERR_INVALID_ARG)
+    return int(n)
+
+
+def tq_attn_mass(args: tq_query_args, k_codec: Codec | None, mass, workspace, decay: float = 1.0, stream=None):
+    """mass (f32 [L, B, Hkv, cap]) = decay * mass + the attention weight each cached token receives
+    from the queries (include/tq.h)."""
+    stride, cap = _mass_layout(mass, args.n_layers, args.batch, args.n_kv_heads)
+    _check("tq_attn_mass", load().tq_attn_mass(ctypes.byref(args), _raw(k_codec), _ptr(mass), stride, cap, decay,
+                                               _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                               _stream(stream)))
+
+
+def attn_mass(*, mass, k_codec=None, decay: float = 1.0, workspace=None, stream=None, **kw):
+    """Convenience: build the arguments, size/allocate the workspace if not given, run."""
+    import torch
+    _check_tensors(dict(mass=(mass, torch.float32)))
+    _check_records(k_codec, kw.get("k_rec"), "k_rec")
+    a = make_query_args(**kw)
+    need = tq_attn_mass_workspace_size(a, k_codec)
+    if workspace is None or workspace.numel() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=kw["q"].device)
+    tq_attn_mass(a, k_codec, mass, workspace, decay, stream)
+    return workspace
+
+
+def make_evict_mass_args(*, k_rec, v_rec, mass, n_chunks, max_chunks: int, keep_chunks: int, k_dst=None, v_dst=None,
+                         mass_dst=None, n_chunks_dst=None, tail_len=None, max_tail: int = 0, sink: int = 0,
+                         recent: int = 0, kept=None, block_table=None, dst_table=None) -> tq_evict_mass_args:
+    """tq_evict_mass_args from tensors: records as for make_evict_args (v_rec may be k_rec), mass f32
+    [L, B, Hkv, cap]; without k_dst, v_dst, mass_dst, n_chunks_dst the cache is compacted in place;
+    kept: optional int32 [L, B, Hkv, 128 * keep_chunks]."""
+    import torch
+    i32, f32, u8 = torch.int32, torch.float32, torch.uint8
+    dst = (k_dst, v_dst, mass_dst, n_chunks_dst)
+    _need(all(t is None for t in dst) or all(t is not None for t in dst),
+          "k_dst, v_dst, mass_dst and n_chunks_dst go together")
+    in_place = k_dst is None
+    _need(not in_place or dst_table is None, "dst_table: only out of place")
+    if in_place:
+        k_dst, v_dst, mass_dst, n_chunks_dst, dst_table = k_rec, v_rec, mass, n_chunks, block_table
+    _check_tensors(dict(k_rec=(k_rec, u8), v_rec=(v_rec, u8), k_dst=(k_dst, u8), v_dst=(v_dst, u8), mass=(mass, f32),
+                        mass_dst=(mass_dst, f32), n_chunks=(n_chunks, i32), n_chunks_dst=(n_chunks_dst, i32),
+                        tail_len=(tail_len, i32), kept=(kept, i32), block_table=(block_table, i32),
+                        dst_table=(dst_table, i32)))
+    L, B, Hkv = mass.shape[:3]
+    a = tq_evict_mass_args()
+    a.n_layers, a.batch, a.n_kv_heads = L, B, Hkv
+    for rec, table, name in ((k_rec, block_table, "k_rec"), (v_rec, block_table, "v_rec"), (k_dst, dst_table, "k_dst"),
+                             (v_dst, dst_table, "v_dst")):
+        lead = (rec.shape[0], rec.shape[2]) if table is not None else tuple(rec.shape[:3])
+        _need(lead == ((L, Hkv) if table is not None else (L, B, Hkv)) and rec[0].is_contiguous(),
+              f"{name}: expected records [L, B, Hkv, cap, bytes] or a pool [L, blocks, Hkv, bytes], "
+              "contiguous within a layer")
+    _need(v_rec.shape[:-1] == k_rec.shape[:-1] and v_dst.shape[:-1] == k_dst.shape[:-1],
+          "key and value records: expected one layout")
+    _need(k_dst.shape[-1] == k_rec.shape[-1] and v_dst.shape[-1] == v_rec.shape[-1],
+          "destination records: expected the source's size")
+    a.k_rec, a.v_rec, a.k_dst, a.v_dst = (t.data_ptr() for t in (k_rec, v_rec, k_dst, v_dst))
+    a.k_rec_layer_stride, a.v_rec_layer_stride = k_rec.stride(0), v_rec.stride(0)
+    a.k_dst_layer_stride, a.v_dst_layer_stride = k_dst.stride(0), v_dst.stride(0)
+    a.rec_cap = k_rec.shape[1] if block_table is not None else k_rec.shape[3]
+    a.dst_cap = k_dst.shape[1] if dst_table is not None else k_dst.shape[3]
+    for table, name in ((block_table, "block_table"), (dst_table, "dst_table")):
+        _need(table is None or (table.is_contiguous() and table.dim() == 2 and table.shape[0] == B),
+              f"{name}: expected contiguous int32 [B, stride]")
+    if block_table is not None:
+        a.block_table, a.table_stride = block_table.data_ptr(), block_table.shape[1]
+    if dst_table is not None:
+        a.dst_table, a.dst_table_stride = dst_table.data_ptr(), dst_table.shape[1]
+    a.mass, a.mass_layer_stride, a.mass_cap = mass.data_ptr(), *_mass_layout(mass, L, B, Hkv)
+    a.mass_dst, a.mass_dst_layer_stride, a.mass_dst_cap = mass_dst.data_ptr(), *_mass_layout(mass_dst, L, B, Hkv)
+    for name, t in (("n_chunks", n_chunks), ("n_chunks_dst", n_chunks_dst), ("tail_len", tail_len)):
+        _counts(t, name, L, B)
+    a.n_chunks, a.n_chunks_dst, a.tail_len = n_chunks.data_ptr(), n_chunks_dst.data_ptr(), _ptr(tail_len)
+    _need(kept is None or (kept.is_contiguous() and tuple(kept.shape) == (L, B, Hkv, CHUNK * keep_chunks)),
+          "kept: expected contiguous int32 [L, B, Hkv, 128 * keep_chunks]")
+    a.kept = _ptr(kept)
+    a.max_chunks, a.max_tail, a.keep_chunks, a.sink, a.recent = max_chunks, max_tail, keep_chunks, sink, recent
+    a._tensors = (k_rec, v_rec, k_dst, v_dst, mass, mass_dst, n_chunks, n_chunks_dst, tail_len, kept, block_table,
+                  dst_table)
+    return a
+
+
+def tq_evict_mass_workspace_size(args: tq_evict_mass_args, k_codec: Codec, v_codec: Codec | None) -> int:
+    n = load().tq_evict_mass_workspace_size(ctypes.byref(args), _raw(k_codec), _raw(v_codec))
+    if n == 0:
+        raise TqError("tq_evict_mass_workspace_size", TQ_ERR_INVALID_ARG)
+    return int(n)
+
+
+def tq_evict_mass(args: tq_evict_mass_args, k_codec: Codec, v_codec: Codec | None, workspace, stream=None):
+    """Keep the tokens of the largest accumulated weight and compact the records (include/tq.h)."""
+    _check("tq_evict_mass", load().tq_evict_mass(ctypes.byref(args), _raw(k_codec), _raw(v_codec), _ptr(workspace),
+                                                 workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def evict_mass(*, k_codec, v_codec=None, workspace=None, stream=None, **kw):
+    """Convenience: build the arguments, size/allocate the workspace if not given, run."""
+    import torch
+    _check_records(k_codec, kw["k_rec"], "k_rec")
+    _check_records(v_codec, kw["v_rec"], "v_rec")
+    a = make_evict_mass_args(**kw)
+    need = tq_evict_mass_workspace_size(a, k_codec, v_codec)
+    if workspace is None or workspace.numel() < need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=kw["k_rec"].device)
+    tq_evict_mass(a, k_codec, v_codec, workspace, stream)
     return workspace

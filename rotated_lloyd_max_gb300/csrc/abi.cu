@@ -8,7 +8,7 @@
 #include <cstring>
 
 #include "../../include/tq.h"
-#include "tq_params.h"
+#include "cache_params.h"
 
 using namespace tq;
 
@@ -296,6 +296,11 @@ Route route_of(const Plan& pl) {
 }  // namespace
 
 namespace tq {
+
+// shared with abi_cache.cu
+tq_status resolve_codec_dev(const tq_codec* c, CodecDev* o) { return resolve_codec(c, o); }
+int sm_count() { return num_sms(); }
+int max_dynamic_smem() { return max_dyn_smem(); }
 
 void attn_smem_layout(AttnParams& p, int D, int GT) {
   const int GTP = GT == 6 ? 8 : GT;

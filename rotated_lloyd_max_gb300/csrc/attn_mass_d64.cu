@@ -1,0 +1,10 @@
+// Accumulated attention weight at head dim 64 (kernel: attn_mass.cuh).
+#include "attn_mass.cuh"
+
+namespace tq {
+
+cudaError_t launch_attn_mass_d64(const MassParams& mp, int NT, cudaStream_t s) {
+  return attn_mass_launch_d<64>(mp, NT, s);
+}
+
+}  // namespace tq

@@ -1,0 +1,103 @@
+// Kernel parameter blocks of the append, the eviction by accumulated weight
+// and the several-query calls, shared between the C ABI (abi_cache.cu) and the
+// kernels.  Host-visible plain structs.
+#pragma once
+
+#include "../../include/tq.h"
+#include "tq_params.h"
+
+namespace tq {
+
+struct AppendParams {
+  int L, B, T, Hq, Hkv, D;
+  int heads;          // heads of a token this launch handles: queries, keys, values (unless shared)
+  int group;          // heads per CTA
+  int tile, tiles;    // tokens per CTA; token tiles per (layer, sequence)
+  FastDiv units;      // division by group * (d / 16)
+  const uint16_t *q, *k, *v;
+  int64_t q_ls, q_bs, q_ts, kv_ls, kv_bs, kv_ts;
+  uint16_t* q_out;
+  int64_t o_ls, o_bs, o_ts;
+  const int32_t* q_lens;
+  const int32_t* positions;
+  int rot_start, rot_dim, adjacent;
+  const float* inv_freq;
+  uint8_t pair_axis[256];
+  float rot_scale;
+  uint16_t *k_tail, *v_tail;
+  int64_t tail_ls;
+  int tail_cap;
+  const int32_t* tail_start;
+  const int32_t* tail_len;
+  int32_t* tail_len_out;
+  int in_place;       // tail_len_out == tail_len: a launch of its own moves the counters
+  float* mass;
+  int64_t mass_ls;
+  int mass_cap;
+  const int32_t* n_chunks;
+};
+
+struct EvictMassParams {
+  int L, B, Hkv;
+  CodecDev kc, vc;
+  int shared;
+  const uint8_t *k_rec, *v_rec;
+  int64_t k_ls, v_ls;
+  int rec_cap;
+  const int32_t* table;
+  int table_stride, rec_limit;
+  uint8_t *k_dst, *v_dst;
+  int64_t kd_ls, vd_ls;
+  int dst_cap;
+  const int32_t* dst_table;
+  int dst_table_stride;
+  const float* mass;
+  float* mass_dst;
+  int64_t mass_ls, mass_dst_ls;
+  int mass_cap, mass_dst_cap;
+  const int32_t* n_chunks;
+  int32_t* n_chunks_dst;
+  const int32_t* tail_len;
+  int max_chunks, max_tail, keep, sink, recent;
+  int slots;       // records a stream can keep: min(keep, max_chunks)
+  int in_place;
+  int32_t* kept;   // caller's list or null
+  // workspace
+  int32_t* list;   // [streams][128 slots] source index of each remaining token
+  int32_t* counts; // [L * B] records before
+};
+
+struct QueryParams {
+  int L, B, T, Hq, Hkv, G, D;
+  float sscale;       // softmax scale * log2(e)
+  float scap, iscap;  // logit soft cap * log2(e) and its reciprocal; 0, 0 = no cap
+  int causal;
+  const uint16_t* q;
+  int64_t q_ls, q_bs, q_ts;
+  const int32_t* q_lens;
+  const uint8_t *krec, *vrec;
+  int64_t krec_ls, vrec_ls;
+  int rec_cap;
+  const int32_t* table;
+  int table_stride, rec_limit;
+  CodecDev kc, vc;
+  int shared_kv;
+  const uint16_t *ktail, *vtail;
+  int64_t tail_ls;
+  int tail_cap;
+  const int32_t* n_chunks;
+  const int32_t* tail_start;
+  const int32_t* tail_len;
+  int max_chunks, max_tail;
+};
+
+cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
+cudaError_t launch_append_commit(const AppendParams& p, cudaStream_t s);
+cudaError_t launch_evict_mass(const EvictMassParams& p, cudaStream_t s);
+
+// abi.cu
+int sm_count();
+int max_dynamic_smem();
+tq_status resolve_codec_dev(const tq_codec* c, CodecDev* o);
+
+}  // namespace tq

@@ -1,0 +1,391 @@
+// Eviction by accumulated attention weight: of the 128 n compressed tokens of
+// a stream (layer, sequence, kv head) the 128 n' of the largest weight stay,
+// in their order, and their records are compacted.
+//
+// mass_select_kernel finds the threshold by a radix selection over the
+// weights' bits, mapped to integers of the same order: three passes of 11, 11
+// and 10 bits, each a histogram of the keys that share the digits found so far.
+// A cluster of CTAs holds one stream: every CTA keeps the keys of its run of
+// tokens in shared memory (they are read from memory once), histograms meet
+// through distributed shared memory, and ballots give each remaining token
+// its rank, so that ties fall to the lower index and the list comes out in
+// order without a sort.
+//
+// mass_compact_kernel moves what remains: scales and code rows (16 bytes a
+// thread, or 8 where a row is no multiple of 16), side lists re-based, weights
+// behind their tokens.  The destination index of a token is never above its
+// source index.  In place, a cluster therefore walks one stream in waves of
+// ascending records: all its CTAs gather a wave into registers, meet at the
+// cluster barrier, and write it; what a wave overwrites no later wave reads.
+// Out of place nothing orders the records and a CTA takes one each.  Both
+// are bound by memory: every remaining record is read and written once.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+#include <type_traits>
+
+#include "cache_params.h"
+#include "tq_common.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace tq {
+
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
+constexpr int kSelBins = 2048;
+constexpr int kMoveThreads = 256;
+constexpr int kMoveUnits = 8;   // 16-byte units a thread may hold: 128 rows of 256 bytes at most
+constexpr int kMoveCluster = 8;
+
+// order-preserving image of a weight; NaN below every number, -0 equal to 0
+__device__ __forceinline__ uint32_t mass_key(float m) {
+  if (m != m) return 0u;
+  const uint32_t u = __float_as_uint(m + 0.f);
+  return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+}
+
+struct SelShared {
+  uint32_t hist[2][kSelBins];
+  uint32_t warp_sum[kSelWarps];
+  uint32_t digit, left;
+  uint32_t gt[kSelWarps], eq[kSelWarps];
+  uint32_t cta_gt, cta_eq;
+};
+
+// CACHED: the CTA's keys stay in shared memory (otherwise each pass reads the weights again)
+template <bool CACHED>
+__global__ void __launch_bounds__(kSelThreads) mass_select_kernel(const __grid_constant__ EvictMassParams p) {
+  __shared__ SelShared sh;
+  extern __shared__ uint32_t keys[];
+  cg::cluster_group cl = cg::this_cluster();
+  const int C = cl.num_blocks(), rank = cl.block_rank();
+  const int64_t stream = blockIdx.x / C;
+  const int h = stream % p.Hkv, lb = stream / p.Hkv, l = lb / p.B, b = lb % p.B;
+  const int n = min(max(p.n_chunks[lb], 0), min(p.max_chunks, p.rec_limit));
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (h == 0 && rank == 0 && tid == 0) p.counts[lb] = n;
+  const int N = n * kChunk, K = min(n, p.keep) * kChunk;
+  int32_t* list = p.list + stream * (int64_t)p.slots * kChunk;
+  int32_t* kept = p.kept ? p.kept + stream * (int64_t)p.keep * kChunk : nullptr;
+  auto keep_token = [&](uint32_t at, int token) {
+    list[at] = token;
+    if (kept) kept[at] = token;
+  };
+  if (n <= p.keep) {  // everything stays
+    for (int i = rank * kSelThreads + tid; i < N; i += C * kSelThreads) keep_token(i, i);
+    return;
+  }
+  const float* mass = p.mass + l * p.mass_ls + ((int64_t)b * p.Hkv + h) * p.mass_cap;
+  const int slice = (n + C - 1) / C * kChunk;
+  const int first = min(rank * slice, N), count = min(slice, N - first);
+  auto load_key = [&](int i) -> uint32_t {
+    const int at = first + i;
+    return at < p.sink || at >= N - p.recent ? 0xFFFFFFFFu : mass_key(mass[at]);
+  };
+  auto key_at = [&](int i) -> uint32_t { return CACHED ? keys[i] : load_key(i); };
+  uint32_t prefix = 0, mask = 0, want = K;
+#pragma unroll 1
+  for (int pass = 0; pass < 3; ++pass) {
+    const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+    uint32_t* hist = sh.hist[pass & 1];
+    for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+    for (int i = tid; i < count; i += kSelThreads) {
+      uint32_t key;
+      if (CACHED && pass == 0) {
+        key = load_key(i);
+        keys[i] = key;
+      } else {
+        key = key_at(i);
+      }
+      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1u);
+    }
+    cl.sync();
+    // thread t sums bins 4t .. 4t + 3 of every CTA's histogram; the digit is
+    // the largest whose count of keys at or above it reaches `want`
+    uint32_t c[4] = {0, 0, 0, 0};
+    for (int r = 0; r < C; ++r) {
+      const uint4 v = *reinterpret_cast<const uint4*>(cl.map_shared_rank(hist, r) + 4 * tid);
+      c[0] += v.x; c[1] += v.y; c[2] += v.z; c[3] += v.w;
+    }
+    const uint32_t mine = c[0] + c[1] + c[2] + c[3];
+    uint32_t up = mine;  // inclusive sum over this lane and those above it
+#pragma unroll
+    for (int m = 1; m < 32; m <<= 1) {
+      const uint32_t o = __shfl_down_sync(0xffffffffu, up, m);
+      if (lane + m < 32) up += o;
+    }
+    if (lane == 0) sh.warp_sum[warp] = up;
+    __syncthreads();
+    uint32_t above = up - mine;
+    for (int w = warp + 1; w < kSelWarps; ++w) above += sh.warp_sum[w];
+    if (above < want && above + mine >= want) {
+      int k = 3;
+      while (above + c[k] < want) above += c[k--];
+      sh.digit = 4 * tid + k;
+      sh.left = want - above;
+    }
+    __syncthreads();
+    prefix |= sh.digit << shift;
+    mask |= (uint32_t)(bins - 1) << shift;
+    want = sh.left;
+  }
+  // prefix is the smallest key that stays, `want` of its ties do
+  const int run = (count + kSelThreads - 1) / kSelThreads * 32;  // tokens of a warp, contiguous
+  const int w0 = min(warp * run, count), w1 = min(w0 + run, count);
+  uint32_t gt = 0, eq = 0;
+  for (int i = w0 + lane; i < w1; i += 32) {
+    const uint32_t key = key_at(i);
+    gt += key > prefix;
+    eq += key == prefix;
+  }
+  gt = __reduce_add_sync(0xffffffffu, gt);
+  eq = __reduce_add_sync(0xffffffffu, eq);
+  if (lane == 0) {
+    sh.gt[warp] = gt;
+    sh.eq[warp] = eq;
+  }
+  __syncthreads();
+  if (tid == 0) {
+    uint32_t a = 0, e = 0;
+    for (int w = 0; w < kSelWarps; ++w) {
+      a += sh.gt[w];
+      e += sh.eq[w];
+    }
+    sh.cta_gt = a;
+    sh.cta_eq = e;
+  }
+  cl.sync();
+  uint32_t gt0 = 0, eq0 = 0;  // before this warp's run
+  for (int r = 0; r < rank; ++r) {
+    gt0 += *cl.map_shared_rank(&sh.cta_gt, r);
+    eq0 += *cl.map_shared_rank(&sh.cta_eq, r);
+  }
+  for (int w = 0; w < warp; ++w) {
+    gt0 += sh.gt[w];
+    eq0 += sh.eq[w];
+  }
+  for (int i0 = w0; i0 < w1; i0 += 32) {
+    const int i = i0 + lane;
+    const uint32_t key = i < w1 ? key_at(i) : 0u;
+    const bool g = i < w1 && key > prefix, e = i < w1 && key == prefix;
+    const uint32_t bg = __ballot_sync(0xffffffffu, g), be = __ballot_sync(0xffffffffu, e);
+    const uint32_t lower = (1u << lane) - 1u;
+    const uint32_t gb = gt0 + __popc(bg & lower), eb = eq0 + __popc(be & lower);
+    if (g || (e && eb < want)) keep_token(gb + min(eb, want), first + i);
+    gt0 += __popc(bg);
+    eq0 += __popc(be);
+  }
+  cl.sync();  // no CTA leaves while another reads its counters
+}
+
+// ----------------------------------------------------------------- compaction
+struct MoveShared {
+  int64_t at[kChunk];   // byte offset of each slot's source record
+  int src[kChunk];      // its slot there
+  int off[kChunk + 1];  // side list: entries before each slot in the destination
+  int from[kChunk];     // and before it in the source
+  int warp_sum[4];
+};
+
+// One destination record: gathered into registers (entries into shared
+// memory), then, after `meet` (the cluster's barrier in place), written.
+template <int UNIT, bool OUTL, class Src, class Meet>
+__device__ __forceinline__ void move_record(const CodecDev& c, const uint8_t* base, Src&& src_of, uint8_t* dst,
+                                            const int32_t* list, bool live, int r, bool in_place, MoveShared& sh,
+                                            uint32_t* ent, Meet&& meet) {
+  using V = typename std::conditional<UNIT == 16, uint4, uint2>::type;
+  const int tid = threadIdx.x;
+  const int row = c.off_norm / kChunk, upr = row / UNIT, units = kChunk * upr;
+  bool moves = false;
+  if (live && tid < kChunk) {
+    const int s = list[r * kChunk + tid];
+    sh.at[tid] = src_of(s / kChunk);
+    sh.src[tid] = s % kChunk;
+    moves = s != r * kChunk + tid;
+  }
+  // in place, a record whose tokens all stay where they are is left alone
+  const bool go = __syncthreads_or(moves) || (live && !in_place);
+  const bool lists = OUTL && c.has_outl;
+  V buf[kMoveUnits * 16 / UNIT];
+  float scale = 0.f;
+  if (go) {
+#pragma unroll
+    for (int k = 0; k < kMoveUnits * 16 / UNIT; ++k) {
+      const int u = tid + k * kMoveThreads;
+      if (u < units) {
+        const int slot = u / upr, part = u % upr;
+        buf[k] = *reinterpret_cast<const V*>(base + sh.at[slot] + sh.src[slot] * row + part * UNIT);
+      }
+    }
+    if (tid < kChunk) scale = *reinterpret_cast<const float*>(base + sh.at[tid] + c.off_norm + 4 * sh.src[tid]);
+    if (lists) {
+      int cnt = 0;
+      if (tid < kChunk) {
+        const uint8_t* cs = base + sh.at[tid] + c.off_count;
+        const int s = sh.src[tid];
+        int before = 0;
+        for (int w = 0; w < kChunk / 4; ++w) {  // entries of the slots in front
+          uint32_t v = reinterpret_cast<const uint32_t*>(cs)[w];
+          const int inside = s - 4 * w;
+          if (inside < 4) v &= inside > 0 ? (1u << (8 * inside)) - 1u : 0u;
+          before = __dp4a(v, 0x01010101u, (uint32_t)before);
+        }
+        cnt = min((int)cs[s], max(c.cap - before, 0));
+        sh.from[tid] = before;
+        int inc = cnt;
+        for (int m = 1; m < 32; m <<= 1) {
+          const int o = __shfl_up_sync(0xffffffffu, inc, m);
+          if ((tid & 31) >= m) inc += o;
+        }
+        sh.off[tid + 1] = inc;
+        if ((tid & 31) == 31) sh.warp_sum[tid >> 5] = inc;
+      }
+      __syncthreads();
+      if (tid < kChunk) {
+        int add = 0;
+        for (int w = 0; w < (tid >> 5); ++w) add += sh.warp_sum[w];
+        sh.off[tid + 1] = min(sh.off[tid + 1] + add, c.cap);  // entries past the capacity are dropped
+        if (tid == 0) sh.off[0] = 0;
+      }
+      __syncthreads();
+      for (int slot = tid >> 5; slot < kChunk; slot += kMoveThreads / 32) {
+        const int o = sh.off[slot], m = sh.off[slot + 1] - o;
+        const uint32_t* es = reinterpret_cast<const uint32_t*>(base + sh.at[slot] + c.off_entries) + sh.from[slot];
+        for (int e = tid & 31; e < m; e += 32) ent[o + e] = es[e];
+      }
+      __syncthreads();
+    }
+  }
+  meet();
+  if (go) {
+#pragma unroll
+    for (int k = 0; k < kMoveUnits * 16 / UNIT; ++k) {
+      const int u = tid + k * kMoveThreads;
+      if (u < units) *reinterpret_cast<V*>(dst + u * UNIT) = buf[k];
+    }
+    if (tid < kChunk) reinterpret_cast<float*>(dst + c.off_norm)[tid] = scale;
+    if (lists) {
+      if (tid < kChunk) dst[c.off_count + tid] = (uint8_t)(sh.off[tid + 1] - sh.off[tid]);
+      uint32_t* ed = reinterpret_cast<uint32_t*>(dst + c.off_entries);
+      for (int e = tid; e < sh.off[kChunk]; e += kMoveThreads) ed[e] = ent[e];
+    }
+  }
+  __syncthreads();  // the bookkeeping block is free again
+}
+
+template <int UNIT, bool OUTL, bool INPLACE>
+__global__ void __launch_bounds__(kMoveThreads) mass_compact_kernel(const __grid_constant__ EvictMassParams p) {
+  __shared__ MoveShared sh;
+  extern __shared__ uint32_t ent[];
+  const int job = blockIdx.z;  // 0: keys, 1: values, 2: weights
+  const int64_t stream = blockIdx.y;
+  const int h = stream % p.Hkv, lb = stream / p.Hkv, l = lb / p.B, b = lb % p.B;
+  const int n = p.counts[lb], left = min(n, p.keep);
+  const int32_t* list = p.list + stream * (int64_t)p.slots * kChunk;
+  const int tid = threadIdx.x;
+  if (job == 0 && h == 0 && blockIdx.x == 0 && tid == 0) p.n_chunks_dst[lb] = left;
+  if (INPLACE && n <= p.keep) return;  // nothing moves (the whole cluster leaves)
+  if (job == 1 && p.shared) return;
+  const int C = INPLACE ? kMoveCluster : 1;
+  if (job == 2) {
+    const int len = p.tail_len ? min(max(p.tail_len[lb], 0), p.max_tail) : 0;
+    const float* m = p.mass + l * p.mass_ls + ((int64_t)b * p.Hkv + h) * p.mass_cap;
+    float* d = p.mass_dst + l * p.mass_dst_ls + ((int64_t)b * p.Hkv + h) * p.mass_dst_cap;
+    const int live = left * kChunk, all = live + len, was = n * kChunk;
+    auto source = [&](int i) { return i < live ? list[i] : was + (i - live); };
+    constexpr int PER = 8;
+    const int step = (int)gridDim.x * kMoveThreads * PER;
+    for (int i0 = 0; i0 < all; i0 += step) {
+      float v[PER];
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        const int i = i0 + (blockIdx.x * PER + k) * kMoveThreads + tid;
+        v[k] = i < all ? m[source(i)] : 0.f;
+      }
+      if constexpr (INPLACE) cg::this_cluster().sync();
+#pragma unroll
+      for (int k = 0; k < PER; ++k) {
+        const int i = i0 + (blockIdx.x * PER + k) * kMoveThreads + tid;
+        if (i < all) d[i] = v[k];
+      }
+    }
+    if (INPLACE)
+      for (int i = all + blockIdx.x * kMoveThreads + tid; i < was + len; i += C * kMoveThreads) d[i] = 0.f;
+    return;
+  }
+  const CodecDev& c = job == 0 ? p.kc : p.vc;
+  const uint8_t* base = (job == 0 ? p.k_rec + l * p.k_ls : p.v_rec + l * p.v_ls);
+  uint8_t* dbase = (job == 0 ? p.k_dst + l * p.kd_ls : p.v_dst + l * p.vd_ls);
+  auto src_of = [&](int r) { return rec_offset(p.table, p.table_stride, p.rec_cap, p.Hkv, b, h, r, c.rec_bytes); };
+  for (int r0 = INPLACE ? 0 : (int)blockIdx.x; r0 < left; r0 += INPLACE ? C : (int)gridDim.x) {
+    const int r = INPLACE ? r0 + (int)blockIdx.x : r0;
+    const bool live = r < left;
+    uint8_t* dst =
+        dbase + rec_offset(p.dst_table, p.dst_table_stride, p.dst_cap, p.Hkv, b, h, live ? r : 0, c.rec_bytes);
+    move_record<UNIT, OUTL>(c, base, src_of, dst, list, live, r, INPLACE, sh, ent, [&] {
+      if constexpr (INPLACE) cg::this_cluster().sync();
+    });
+  }
+}
+
+template <int UNIT, bool OUTL, bool INPLACE>
+static cudaError_t compact_launch(const EvictMassParams& p, cudaStream_t s) {
+  auto kern = mass_compact_kernel<UNIT, OUTL, INPLACE>;
+  int cap = 0;
+  if (OUTL) cap = std::min(std::max(p.kc.has_outl ? p.kc.cap : 0, p.vc.has_outl ? p.vc.cap : 0), kChunk * 255);
+  const int smem = 4 * cap;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(INPLACE ? kMoveCluster : p.slots, p.L * p.B * p.Hkv, 3);
+  cfg.blockDim = dim3(kMoveThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = kMoveCluster;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = INPLACE ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+template <int UNIT, bool OUTL>
+static cudaError_t compact_pick(const EvictMassParams& p, cudaStream_t s) {
+  return p.in_place ? compact_launch<UNIT, OUTL, true>(p, s) : compact_launch<UNIT, OUTL, false>(p, s);
+}
+
+cudaError_t launch_evict_mass(const EvictMassParams& p, cudaStream_t s) {
+  // about 4096 tokens a CTA, at most 8 CTAs (the portable cluster size)
+  int C = 1;
+  while (C < 8 && p.max_chunks > 32 * C) C *= 2;
+  const int smem = (p.max_chunks + C - 1) / C * kChunk * 4;
+  const bool cached = smem <= 160 * 1024;
+  auto kern = cached ? mass_select_kernel<true> : mass_select_kernel<false>;
+  if (cached && smem > 24 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)((int64_t)p.L * p.B * p.Hkv * C));
+  cfg.blockDim = dim3(kSelThreads);
+  cfg.dynamicSmemBytes = cached ? smem : 0;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = C;
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
+  if (e != cudaSuccess) return e;
+  const bool outl = p.kc.has_outl || p.vc.has_outl;
+  const bool wide = p.kc.off_norm / kChunk % 16 == 0 && p.vc.off_norm / kChunk % 16 == 0;
+  if (outl) return wide ? compact_pick<16, true>(p, s) : compact_pick<8, true>(p, s);
+  return wide ? compact_pick<16, false>(p, s) : compact_pick<8, false>(p, s);
+}
+
+}  // namespace tq
