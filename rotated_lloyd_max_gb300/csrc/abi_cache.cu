@@ -233,19 +233,40 @@ tq_status prefill_plan(const tq_query_args* a, const tq_codec* kcod, const tq_co
   pp.rows = pp.q.T * pp.q.G;
   pp.tiles = (int)cdiv(pp.rows, bm);
   const int64_t units = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv;
-  // enough CTAs for two waves of two per SM; a split keeps at least two
-  // records or 256 ring tokens, and a row at most 64 partials of either kind
-  const int64_t want = a->splits > 0 ? a->splits : cdiv(4ll * sm_count(), units * pp.tiles);
-  if (pp.q.max_chunks > 0) {
-    const int64_t s = std::min<int64_t>(std::min<int64_t>(want, 64), a->splits > 0 ? pp.q.max_chunks : cdiv(pp.q.max_chunks, 2));
-    pp.cps = (int)cdiv(pp.q.max_chunks, s);
-    pp.Sc = (int)cdiv(pp.q.max_chunks, pp.cps);
-  }
-  if (pp.q.max_tail > 0) {
-    const int64_t t = cdiv(pp.q.max_tail, 64);
-    const int64_t s = std::min<int64_t>(std::min<int64_t>(want, 64), a->splits > 0 ? t : cdiv(t, 4));
-    pp.tps = (int)(64 * cdiv(t, s));
-    pp.St = (int)cdiv(pp.q.max_tail, pp.tps);
+  const int64_t sms = sm_count(), U = units * pp.tiles;
+  if (d <= 128) {
+    // one CTA per SM: the split count that minimises waves x 128-token tiles
+    // per split, four tiles' worth of set-up and epilogue included, and the
+    // partials' traffic (about 0.03 tiles per CTA)
+    const int64_t ring = cdiv(pp.q.max_tail, TQ_CHUNK), most = std::max<int64_t>(pp.q.max_chunks, ring);
+    double best = 1e300;
+    for (int64_t per = 1, s = most; per <= most; per = s > 1 ? cdiv(most, --s) : most + 1) {
+      if (a->splits > 0 && s != std::min<int64_t>(a->splits, most)) continue;
+      const int64_t ctas = U * (cdiv(pp.q.max_chunks, per) + cdiv(ring, per));
+      const double cost = (double)cdiv(ctas, sms) * (double)(per + 4) + 0.03 * (double)ctas;
+      if (cost < best) {
+        best = cost;
+        pp.cps = (int)per;
+        pp.Sc = (int)cdiv(pp.q.max_chunks, per);
+        pp.tps = (int)(TQ_CHUNK * per);
+        pp.St = (int)cdiv(ring, per);
+      }
+    }
+  } else {
+    // enough CTAs for four waves of one per SM; a split keeps at least two
+    // records or 256 ring tokens, and a row at most 64 partials of either kind
+    const int64_t want = a->splits > 0 ? a->splits : cdiv(4 * sms, U);
+    if (pp.q.max_chunks > 0) {
+      const int64_t s = std::min<int64_t>(std::min<int64_t>(want, 64), a->splits > 0 ? pp.q.max_chunks : cdiv(pp.q.max_chunks, 2));
+      pp.cps = (int)cdiv(pp.q.max_chunks, s);
+      pp.Sc = (int)cdiv(pp.q.max_chunks, pp.cps);
+    }
+    if (pp.q.max_tail > 0) {
+      const int64_t t = cdiv(pp.q.max_tail, 64);
+      const int64_t s = std::min<int64_t>(std::min<int64_t>(want, 64), a->splits > 0 ? t : cdiv(t, 4));
+      pp.tps = (int)(64 * cdiv(t, s));
+      pp.St = (int)cdiv(pp.q.max_tail, pp.tps);
+    }
   }
   if ((int64_t)pp.tiles * std::max(pp.Sc, pp.St) > 0x7FFFFFFFll || units * pp.rows > (1ll << 32)) return TQ_ERR_UNSUPPORTED;
   pp.out = (uint16_t*)a->out;

@@ -31,7 +31,6 @@ struct PrefillParams {
   uint16_t* out;
   int64_t o_ls, o_bs, o_ts;
   float inv_sqrt_d;
-  int* status;
 };
 
 // Tile shapes: BM rows (16 per row warp), CW warps side by side over the output columns
@@ -110,6 +109,15 @@ __device__ __forceinline__ uint4 decode8(uint32_t w, const Planes& pl) {
 }
 
 constexpr float kTableScale = 32768.f;  // 2^15
+
+__device__ __forceinline__ uint32_t pack2_f16(float a, float b) {
+  const __half2 v = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+__device__ __forceinline__ uint32_t pack2_bf16(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 
 template <int D, bool DENSE>
 __global__ void __launch_bounds__(256) prefill_kernel(const __grid_constant__ PrefillParams pp) {

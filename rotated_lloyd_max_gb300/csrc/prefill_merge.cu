@@ -29,6 +29,7 @@ __global__ void __launch_bounds__(kThreads) prefill_merge_kernel(const __grid_co
   for (int e = 0; e < E; ++e) c[e] = d[e] = 0.f;
   for (int s = 0; s < S; ++s) {
     const float2 v = ml[s];
+    if (v.y != v.y) W = v.y;  // a split that gave up: the row comes out NaN
     if (!(v.y > 0.f)) continue;
     const float w = exp2f(v.x - M);
     W = fmaf(w, v.y, W);
@@ -49,7 +50,7 @@ __global__ void __launch_bounds__(kThreads) prefill_merge_kernel(const __grid_co
     fwht_regs<E>(c);
     fwht_lanes<E>(c, lane, 32);
   }
-  const float iw = W > 0.f ? 1.f / W : 0.f;  // a row that sees no token is zero
+  const float iw = W > 0.f || W != W ? 1.f / W : 0.f;  // a row that sees no token is zero
   uint16_t* out = pp.out + l * pp.o_ls + b * pp.o_bs + (int64_t)tok * pp.o_ts + (int64_t)(h * p.G + row % p.G) * D +
                   lane * E;
 #pragma unroll

@@ -1,0 +1,542 @@
+// Attention of several query tokens per sequence on the fifth-generation
+// tensor cores (tcgen05, accumulators in tensor memory), head dims 64 and 128.
+//
+// A CTA keeps 256 query rows (two M = 128 tiles; row = token * G + head, so any
+// group size fills them) and walks a run of 128-token tiles: records, or the
+// ring's tokens.  Scores S = Q~ K^T (A and B from shared memory) and outputs
+// O += P V (P from tensor memory, V from shared memory) accumulate in f32:
+// columns 0-255 hold S of the two tiles, which the softmax replaces by P in
+// half as many, columns 256.. hold O.
+//
+// Operands of the records are f16: q~ 2^s (s per row), and centroid * scale
+// with the token's scale folded in, n 2^-(E+1) as f16 with E the exponent of
+// the largest scale of the CTA's run (read ahead; values below 2^-24 of the
+// largest round to zero), so that a logit needs one multiply-add and a weight
+// none.  The ring's operands are bf16 as they are.  The softmax subtracts a
+// reference that follows the maximum only when it is passed by 2^8, so O is
+// rescaled rarely, by the warps that own the rows.
+//
+// Warps: 0-3 and 4-7 softmax of tile 0 and 1 (a thread per row), 8-15 decode
+// records (or copy ring tokens) into two stages each of key and value tiles,
+// 16 issues MMAs.  A tile's MMAs run P V(i) then Q K(i+1), and the two tiles
+// alternate, so that one tile's softmax runs under the other's MMAs.  Every
+// wait is bounded; a CTA whose wait expired leaves NaN statistics, so that its
+// rows come out NaN.
+#pragma once
+
+#include "prefill.cuh"
+#include "umma.cuh"
+
+namespace tq {
+
+constexpr int kPfSoft = 8, kPfLoad = 8;  // softmax and loading warps
+constexpr int kPfThreads = 32 * (kPfSoft + kPfLoad + 1);
+constexpr int kPfRows = 256;
+
+template <int D>
+struct PfCfg {
+  static constexpr int TILE = 128 * D * 2;      // bytes of a 128-row operand tile
+  static constexpr int Q = 0, K = 2 * TILE, V = 4 * TILE, MISC = 6 * TILE;
+  static constexpr int SMEM = MISC + 2560 + 1024;  // + bookkeeping + alignment slack
+};
+
+struct PfMisc {
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2], fin;
+  uint32_t tbase;
+  int abort_;
+  float red[2][17];
+  float qf[kPfRows];  // logit factor of a row
+  int lim[kPfRows];   // tokens it sees, counted from the run's origin
+};
+static_assert(sizeof(PfMisc) <= 2560, "bookkeeping block");
+
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(
+          taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+// D (tensor memory) += A (tensor memory) * B (shared memory)
+__device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                            uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+constexpr uint32_t kIdescBf16 = (1u << 7) | (1u << 10);  // bf16 A and B
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, __half2 b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), b);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// eight codes of a packed row as nibbles; w holds the bytes that a lane loaded for them
+template <int B>
+__device__ __forceinline__ uint32_t load_codes(const uint8_t* row, int u) {
+  if constexpr (B == 4) return __ldg(reinterpret_cast<const uint32_t*>(row) + u);
+  else if constexpr (B == 2) return __ldg(reinterpret_cast<const uint16_t*>(row) + u);
+  else if constexpr (B == 1) return __ldg(row + u);
+  else {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(row) + ((3 * u) >> 2);
+    return __funnelshift_r(__ldg(w), __ldg(w + 1), 8 * ((3 * u) & 3));
+  }
+}
+// centroids of up to 16 levels as byte planes; with 8 levels or fewer one lookup a plane is enough
+template <int B>
+__device__ __forceinline__ uint4 decode_codes(uint32_t x, const Planes& pl) {
+  if constexpr (B == 4) return decode8(x, pl);
+  if constexpr (B == 3) x = spread3(x);
+  if constexpr (B == 2) {
+    x &= 0xFFFFu;
+    x = (x | (x << 8)) & 0x00FF00FFu;
+    x = (x | (x << 4)) & 0x0F0F0F0Fu;
+    x = (x | (x << 2)) & 0x33333333u;
+  }
+  if constexpr (B == 1) {
+    x &= 0xFFu;
+    x = (x | (x << 12)) & 0x000F000Fu;
+    x = (x | (x << 6)) & 0x03030303u;
+    x = (x | (x << 3)) & 0x11111111u;
+  }
+  const uint32_t y = x >> 16;
+  const uint32_t a0 = __byte_perm(pl.lo[0], pl.lo[1], x), b0 = __byte_perm(pl.hi[0], pl.hi[1], x);
+  const uint32_t a1 = __byte_perm(pl.lo[0], pl.lo[1], y), b1 = __byte_perm(pl.hi[0], pl.hi[1], y);
+  return make_uint4(__byte_perm(a0, b0, 0x5140), __byte_perm(a0, b0, 0x7362), __byte_perm(a1, b1, 0x5140),
+                    __byte_perm(a1, b1, 0x7362));
+}
+
+// One record's keys or values into a stage: warp w of the eight takes tokens
+// 16 w .. 16 w + 15, a lane eight codes (16 bytes of f16) at a time.
+template <int D, int B>
+__device__ __forceinline__ void decode_tile(const CodecDev& c, const uint8_t* rec, const Planes& pl, float nscale,
+                                            unsigned char* st, int w, int lane) {
+  constexpr int CH = D / 8, PER = 16 * CH / 32;  // chunks per row, per lane
+  const int rb = D * B / 8;
+  uint32_t x[PER];
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int i = lane + 32 * k;
+    x[k] = load_codes<B>(rec + (16 * w + i / CH) * rb, i % CH);
+  }
+  const float n = __ldg(reinterpret_cast<const float*>(rec + c.off_norm) + 16 * w + (lane & 15)) * nscale;
+#pragma unroll
+  for (int k = 0; k < PER; ++k) {
+    const int i = lane + 32 * k, row = i / CH, ch = i % CH;
+    const __half2 s = __float2half2_rn(__shfl_sync(0xffffffffu, n, row));
+    uint4 v = decode_codes<B>(x[k], pl);
+    v = make_uint4(hmul2(v.x, s), hmul2(v.y, s), hmul2(v.z, s), hmul2(v.w, s));
+    *reinterpret_cast<uint4*>(st + (ch >> 3) * 16384 + sw128_off(16 * w + row, ch & 7)) = v;
+  }
+  if (c.has_outl) {  // the warp's tokens' side lists replace their coordinates
+    const uint32_t* cw = reinterpret_cast<const uint32_t*>(rec + c.off_count);
+    const int slot = 16 * w + (lane & 15);
+    int from = 0;
+    for (int q = 0; q < 4 * w; ++q) from = __dp4a(__ldg(cw + q), 0x01010101u, (uint32_t)from);
+    const int mine = __ldg(rec + c.off_count + slot);
+    int inc = mine;
+#pragma unroll
+    for (int m = 1; m < 16; m <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, inc, m, 16);
+      if ((lane & 15) >= m) inc += o;
+    }
+    from += inc - mine;
+    const int cnt = min(mine, max(c.cap - from, 0));
+    const uint32_t* ent = reinterpret_cast<const uint32_t*>(rec + c.off_entries);
+    __syncwarp();
+#pragma unroll 1
+    for (int row = 0; row < 16; ++row) {
+      const int f = __shfl_sync(0xffffffffu, from, row), m = __shfl_sync(0xffffffffu, cnt, row);
+      const float s = __shfl_sync(0xffffffffu, n, row) * kTableScale;
+      for (int e = lane; e < m; e += 32) {
+        const uint32_t en = __ldg(ent + f + e);
+        const int j = en & (D - 1);
+        *reinterpret_cast<__half*>(st + (j >> 6) * 16384 + sw128_off(16 * w + row, (j >> 3) & 7) + 2 * (j & 7)) =
+            __float2half_rn(bf16_hi(en) * s);
+      }
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void decode_tile_b(const CodecDev& c, const uint8_t* rec, const Planes& pl, float nscale,
+                                              unsigned char* st, int w, int lane) {
+  switch (c.bits) {
+    case 1: decode_tile<D, 1>(c, rec, pl, nscale, st, w, lane); break;
+    case 2: decode_tile<D, 2>(c, rec, pl, nscale, st, w, lane); break;
+    case 3: decode_tile<D, 3>(c, rec, pl, nscale, st, w, lane); break;
+    default: decode_tile<D, 4>(c, rec, pl, nscale, st, w, lane); break;
+  }
+}
+
+template <int D, bool DENSE>
+__device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsigned char* sm, int tile, int split) {
+  using C = PfCfg<D>;
+  const QueryParams& p = pp.q;
+  PfMisc& ms = *reinterpret_cast<PfMisc*>(sm + C::MISC);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int h = blockIdx.y % p.Hkv, b = blockIdx.y / p.Hkv, l = blockIdx.z;
+  const int S = pp.Sc + pp.St;
+  const int lb = l * p.B + b;
+  const int64_t unit = (int64_t)lb * p.Hkv + h;
+  const CacheLen cl = cache_len(p, lb);
+  const int tb = query_len(p, b);
+  const int r0 = tile * kPfRows, rn = min(kPfRows, tb * p.G - r0);
+  if (rn <= 0) return;
+  const int base = DENSE ? cl.n * kChunk : 0;
+  const int top = row_limit(p, cl, tb, r0 + rn - 1) - base;
+  const int k0 = split * (DENSE ? pp.tps : pp.cps * kChunk);
+  const int k1 = min(min(k0 + (DENSE ? pp.tps : pp.cps * kChunk), DENSE ? cl.len : cl.n * kChunk), top);
+  const int sidx = DENSE ? pp.Sc + split : split;
+  const int64_t wrow = unit * pp.rows + r0;
+  if (k0 >= k1) {
+    for (int r = tid; r < rn; r += kPfThreads) pp.ws_ml[(wrow + r) * S + sidx] = make_float2(-INFINITY, 0.f);
+    return;
+  }
+  const int n = (k1 - k0 + kChunk - 1) / kChunk;  // 128-token tiles
+  const int nt = rn > 128 ? 2 : 1;                // row tiles in use
+  const int c0 = k0 / kChunk;
+  const uint8_t* kl = p.krec + l * p.krec_ls;
+  const uint8_t* vl = p.vrec + l * p.vrec_ls;
+  auto rec_at = [&](bool key, int c) {
+    const int bytes = key ? p.kc.rec_bytes : p.vc.rec_bytes;
+    return (key ? kl : vl) + rec_offset(p.table, p.table_stride, p.rec_cap, p.Hkv, b, h, c, bytes);
+  };
+
+  // ---------------------------------------------------------------- set-up
+  if (tid == 0) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ms.k_full[i], kPfLoad);
+      mbar_init(&ms.v_full[i], kPfLoad);
+      mbar_init(&ms.k_empty[i], 1);
+      mbar_init(&ms.v_empty[i], 1);
+      mbar_init(&ms.s_full[i], 1);
+      mbar_init(&ms.p_full[i], 4);
+      mbar_init(&ms.o_done[i], 1);
+    }
+    mbar_init(&ms.fin, 1);
+    ms.abort_ = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  if (warp == kPfSoft + kPfLoad) tmem_alloc(&ms.tbase, 512);
+  if constexpr (!DENSE) {  // the run's largest scales
+    float mk = 0.f, mv = 0.f;
+    for (int i = tid; i < n * kChunk; i += kPfThreads) {
+      mk = fmaxf(mk, fabsf(__ldg(reinterpret_cast<const float*>(rec_at(true, c0 + i / kChunk) + p.kc.off_norm) + i % kChunk)));
+      mv = fmaxf(mv, fabsf(__ldg(reinterpret_cast<const float*>(rec_at(false, c0 + i / kChunk) + p.vc.off_norm) + i % kChunk)));
+    }
+    mk = warp_max(mk);
+    mv = warp_max(mv);
+    if (lane == 0) {
+      ms.red[0][warp] = mk;
+      ms.red[1][warp] = mv;
+    }
+    __syncthreads();
+  }
+  float ek = 1.f, ev = 1.f;  // 2^-(E+1) of keys and values
+  if constexpr (!DENSE) {
+    float mk = ms.red[0][0], mv = ms.red[1][0];
+    for (int w = 1; w < 17; ++w) {
+      mk = fmaxf(mk, ms.red[0][w]);
+      mv = fmaxf(mv, ms.red[1][w]);
+    }
+    ek = pow2i(-1 - exp_of(mk));
+    ev = pow2i(-1 - exp_of(mv));
+  }
+  {  // query rows, a warp each: lane holds D / 32 coordinates
+    constexpr int E = D / 32;
+    const float sgn = p.sscale < 0.f ? -1.f : 1.f;
+    for (int r = warp; r < 128 * nt; r += kPfThreads / 32) {
+      const int row = r0 + r;
+      float x[E];
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[e] = 0.f;
+      if (r < rn) {
+        const uint16_t* qp = p.q + l * p.q_ls + b * p.q_bs + (int64_t)(row / p.G) * p.q_ts +
+                             (int64_t)(h * p.G + row % p.G) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; e += 2) {
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(qp + e);
+          x[e] = bf16_lo(w) * sgn;
+          x[e + 1] = bf16_hi(w) * sgn;
+        }
+      }
+      float f = fabsf(p.sscale);
+      uint32_t w[E / 2];
+      if constexpr (DENSE) {
+#pragma unroll
+        for (int e = 0; e < E; e += 2) w[e / 2] = pack2_bf16(x[e], x[e + 1]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int j = lane * E + e;
+          if ((p.kc.signs[j >> 5] >> (j & 31)) & 1u) x[e] = -x[e];
+        }
+        fwht_regs<E>(x);
+        fwht_lanes<E>(x, lane, 32);
+        float mx = 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          x[e] *= inv_sqrt_dim<D>();
+          mx = fmaxf(mx, fabsf(x[e]));
+        }
+        mx = warp_max(mx);
+        const int s = mx > 0.f ? 13 - exp_of(mx) : 0;
+        const float sc = pow2i(s);
+        f = f * pow2i(-15 - s) * (1.f / ek);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) w[e / 2] = pack2_f16(x[e] * sc, x[e + 1] * sc);
+      }
+      const int j = lane * E;
+      unsigned char* dst = sm + C::Q + (r >> 7) * C::TILE + (j >> 6) * 16384 + sw128_off(r & 127, (j >> 3) & 7) + 2 * (j & 7);
+      if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
+      else *reinterpret_cast<uint32_t*>(dst) = w[0];
+      if (lane == 0) {
+        ms.qf[r] = f;
+        ms.lim[r] = r < rn ? row_limit(p, cl, tb, row) - base - k0 : 0x7FFFFFFF;
+      }
+    }
+  }
+  fence_async_smem();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tb0 = ms.tbase;
+  volatile int* abort_f = &ms.abort_;
+
+  if (warp == kPfSoft + kPfLoad) {
+    // ---------------------------------------------------------------- MMA issue
+    if (lane == 0) {
+      constexpr uint32_t T = DENSE ? kIdescBf16 : 0u;
+      constexpr uint32_t IS = idesc_f16(128, 128, false, false) | T;
+      constexpr uint32_t IV = idesc_f16(128, D, false, true) | T;
+      const uint64_t dQ = sdesc_sw128(smem_u32(sm + C::Q), 16, 1024);
+      const uint64_t dK = sdesc_sw128(smem_u32(sm + C::K), 16, 1024);
+      const uint64_t dV = sdesc_sw128(smem_u32(sm + C::V), 16384, 1024);
+      constexpr uint64_t TS = C::TILE / 16;
+      auto scores = [&](int t, int i) {
+        const uint64_t a = dQ + t * TS, bk = dK + (i & 1) * TS;
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          const uint64_t o = (ks >> 2) * 1024 + 2 * (ks & 3);
+          umma_f16(tb0 + 128 * t, a + o, bk + o, IS, ks != 0);
+        }
+        umma_commit(&ms.s_full[t]);
+      };
+      mbar_wait(&ms.k_full[0], 0, abort_f);
+      tc_fence_after();
+      for (int t = 0; t < nt; ++t) scores(t, 0);
+      umma_commit(&ms.k_empty[0]);
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        for (int t = 0; t < nt; ++t) {
+          if (t == 0) mbar_wait(&ms.v_full[i & 1], (i >> 1) & 1, abort_f);
+          mbar_wait(&ms.p_full[t], i & 1, abort_f);
+          tc_fence_after();
+          const uint64_t bv = dV + (i & 1) * TS;
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            umma_f16_ts(tb0 + 256 + D * t, tb0 + 128 * t + 8 * ks, bv + 128 * ks, IV, i > 0 || ks > 0);
+          umma_commit(&ms.o_done[t]);
+          if (t == nt - 1) umma_commit(&ms.v_empty[i & 1]);
+          if (i + 1 < n) {
+            if (t == 0) mbar_wait(&ms.k_full[(i + 1) & 1], ((i + 1) >> 1) & 1, abort_f);
+            mbar_wait(&ms.o_done[t], i & 1, abort_f);  // P is read before S takes its columns
+            tc_fence_after();
+            scores(t, i + 1);
+            if (t == nt - 1) umma_commit(&ms.k_empty[(i + 1) & 1]);
+          }
+        }
+      }
+      umma_commit(&ms.fin);
+    }
+    __syncwarp();
+  } else if (warp >= kPfSoft) {
+    // ---------------------------------------------------------------- keys and values
+    const int w = warp - kPfSoft;
+    if constexpr (DENSE) {
+      constexpr int CH = D / 8, PER = 16 * CH / 32;
+      const int cap = p.tail_cap;
+      const int start = p.tail_start ? ((p.tail_start[lb] % cap) + cap) % cap : 0;
+      const int64_t ring = l * p.tail_ls + (int64_t)(b * p.Hkv + h) * cap * D;
+      for (int i = 0; i < n; ++i) {
+        const int s = i & 1, ph = ((i >> 1) & 1) ^ 1;
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv) {
+          const uint16_t* src = (kv ? p.vtail : p.ktail) + ring;
+          mbar_wait(kv ? &ms.v_empty[s] : &ms.k_empty[s], ph, abort_f);
+          unsigned char* st = sm + (kv ? C::V : C::K) + s * C::TILE;
+#pragma unroll
+          for (int k = 0; k < PER; ++k) {
+            const int x = lane + 32 * k, row = 16 * w + x / CH, ch = x % CH;
+            const int tok = min(k0 + i * kChunk + row, cl.len - 1);
+            cp_async16(st + (ch >> 3) * 16384 + sw128_off(row, ch & 7),
+                       src + (int64_t)((start + (int64_t)tok) % cap) * D + 8 * ch);
+          }
+          cp_async_commit();
+          if (kv) {  // the keys have landed, then the values
+            cp_async_wait<1>();
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.k_full[s]);
+            cp_async_wait<0>();
+            fence_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ms.v_full[s]);
+          }
+        }
+      }
+    } else {
+      const Planes kpl = make_planes(p.kc, kTableScale), vpl = make_planes(p.vc, kTableScale);
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const int s = i & 1, ph = ((i >> 1) & 1) ^ 1;
+        mbar_wait(&ms.k_empty[s], ph, abort_f);
+        decode_tile_b<D>(p.kc, rec_at(true, c0 + i), kpl, ek, sm + C::K + s * C::TILE, w, lane);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.k_full[s]);
+        mbar_wait(&ms.v_empty[s], ph, abort_f);
+        decode_tile_b<D>(p.vc, rec_at(false, c0 + i), vpl, ev, sm + C::V + s * C::TILE, w, lane);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.v_full[s]);
+      }
+    }
+  } else if ((warp >> 2) < nt) {
+    // ---------------------------------------------------------------- softmax: a thread per row
+    const int t = warp >> 2, q = warp & 3, r = 128 * t + 32 * q + lane;
+    const uint32_t lrow = (uint32_t)(32 * q) << 16;
+    const uint32_t tS = tb0 + 128 * t + lrow, tO = tb0 + 256 + D * t + lrow;
+    const float f = ms.qf[r];
+    const int lim = ms.lim[r];
+    float mref = -INFINITY, lsum = 0.f;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      mbar_wait(&ms.s_full[t], i & 1, abort_f);
+      tc_fence_after();
+      const int seen = lim - i * kChunk;  // columns below it
+      const bool edge = __any_sync(0xffffffffu, seen < kChunk);
+      float mx = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t a[32];
+        tmem_ld32(tS + 32 * c, a);
+        tmem_ld_wait();
+        if (edge) {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) mx = fmaxf(mx, 32 * c + j < seen ? __uint_as_float(a[j]) : -INFINITY);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(a[j]));
+        }
+      }
+      float tm = mx > -INFINITY ? mx * f : -INFINITY;
+      if (p.scap > 0.f) tm = soft_cap(tm, p.scap, p.iscap);
+      if (__any_sync(0xffffffffu, tm > mref + 8.f)) {
+        const float mn = tm > mref + 8.f ? tm : mref;
+        const float al = mref > -INFINITY ? ex2(mref - mn) : 0.f;  // 1 where the reference stays
+        const float sc = mn > -INFINITY ? al : 1.f;
+        lsum *= sc;
+        mref = mn;
+        if (i > 0) {  // P V(i - 1) is complete: the scores of this tile were issued after it
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t o[32];
+            tmem_ld32(tO + 32 * c, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * sc);
+            tmem_st32(tO + 32 * c, o);
+          }
+        }
+      }
+      const float ref = mref > -INFINITY ? mref : 0.f;
+      const float2 f2v = f2(f, f), m2 = f2(-ref, -ref);
+      float2 sum = f2(0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t a[32], w[16];
+        tmem_ld32(tS + 32 * c, a);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) {
+          float2 v = f2(__uint_as_float(a[j]), __uint_as_float(a[j + 1]));
+          if (p.scap > 0.f) {
+            v = f2(soft_cap(v.x * f, p.scap, p.iscap) - ref, soft_cap(v.y * f, p.scap, p.iscap) - ref);
+          } else {
+            v = fma2(v, f2v, m2);
+          }
+          v = f2(ex2(v.x), ex2(v.y));
+          if (edge) {
+            if (32 * c + j >= seen) v.x = 0.f;
+            if (32 * c + j + 1 >= seen) v.y = 0.f;
+          }
+          sum = add2(sum, v);
+          w[j / 2] = DENSE ? pack2_bf16(v.x, v.y) : pack2_f16(v.x, v.y);
+        }
+        tmem_st16(tS + 16 * c, w);  // over columns of S that are read
+      }
+      lsum += sum.x + sum.y;
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ms.p_full[t]);
+    }
+    mbar_wait(&ms.o_done[t], (n - 1) & 1, abort_f);
+    tc_fence_after();
+    const float un = DENSE ? 1.f : pow2i(-15) * (1.f / ev);
+    float* dst = pp.ws_acc + ((wrow + r) * S + sidx) * D;
+#pragma unroll
+    for (int c = 0; c < D / 32; ++c) {
+      uint32_t o[32];
+      tmem_ld32(tO + 32 * c, o);
+      tmem_ld_wait();
+      if (r < rn) {
+#pragma unroll
+        for (int j = 0; j < 32; j += 4)
+          *reinterpret_cast<float4*>(dst + 32 * c + j) =
+              make_float4(__uint_as_float(o[j]) * un, __uint_as_float(o[j + 1]) * un, __uint_as_float(o[j + 2]) * un,
+                          __uint_as_float(o[j + 3]) * un);
+      }
+    }
+    if (r < rn) {
+      const float bad = __int_as_float(0x7fc00000);
+      pp.ws_ml[(wrow + r) * S + sidx] = *abort_f ? make_float2(bad, bad)
+                                        : lsum > 0.f ? make_float2(mref, lsum) : make_float2(-INFINITY, 0.f);
+    }
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (warp == kPfSoft + kPfLoad) {
+    volatile int drain = 0;  // every MMA has completed, whatever the abort flag says
+    mbar_wait(&ms.fin, 0, &drain);
+    tc_fence_after();
+    tmem_dealloc(tb0, 512);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kPfThreads, 1) prefill_umma_kernel(const __grid_constant__ PrefillParams pp) {
+  extern __shared__ __align__(1024) unsigned char smraw[];
+  unsigned char* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
+  const int S = pp.Sc + pp.St, split = blockIdx.x % S, tile = blockIdx.x / S;
+  if (split < pp.Sc) prefill_umma_body<D, false>(pp, sm, tile, split);
+  else prefill_umma_body<D, true>(pp, sm, tile, split - pp.Sc);
+}
+
+template <int D>
+cudaError_t prefill_umma_launch(const PrefillParams& pp, cudaStream_t s) {
+  if (pp.Sc + pp.St == 0) return cudaSuccess;
+  const cudaError_t e =
+      cudaFuncSetAttribute(prefill_umma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PfCfg<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  const dim3 grid(pp.tiles * (pp.Sc + pp.St), pp.q.B * pp.q.Hkv, pp.q.L);
+  prefill_umma_kernel<D><<<grid, kPfThreads, PfCfg<D>::SMEM, s>>>(pp);
+  return cudaGetLastError();
+}
+
+}  // namespace tq
