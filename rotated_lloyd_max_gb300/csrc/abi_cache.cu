@@ -274,7 +274,8 @@ tq_status prefill_plan(const tq_query_args* a, const tq_codec* kcod, const tq_co
   pp.o_bs = a->out_batch_stride;
   pp.o_ts = a->out_token_stride;
   pp.inv_sqrt_d = (float)(1.0 / std::sqrt((double)d));
-  const size_t parts = (size_t)(units * pp.rows) * (pp.Sc + pp.St);
+  // partials: every row, or at head dims 64 and 128 whole tiles of 128 rows
+  const size_t parts = (size_t)(units * (d <= 128 ? cdiv(pp.rows, 128) * 128 : pp.rows)) * (pp.Sc + pp.St);
   pl->ml_off = pad256(parts * d * 4);
   pl->bytes = pl->ml_off + pad256(parts * 8) + 256;
   return TQ_OK;

@@ -16,12 +16,18 @@
 // reference that follows the maximum only when it is passed by 2^8, so O is
 // rescaled rarely, by the warps that own the rows.
 //
-// Warps: 0-3 and 4-7 softmax of tile 0 and 1 (a thread per row), 8-15 decode
+// Warps: 0-3 and 4-7 softmax of tile 0 and 1 (a thread per row), 8-23 decode
 // records (or copy ring tokens) into two stages each of key and value tiles,
-// 16 issues MMAs.  A tile's MMAs run P V(i) then Q K(i+1), and the two tiles
-// alternate, so that one tile's softmax runs under the other's MMAs.  Every
-// wait is bounded; a CTA whose wait expired leaves NaN statistics, so that its
-// rows come out NaN.
+// 24 issues MMAs.  A tile's MMAs run P V(i) then Q K(i+1), and the two tiles
+// alternate, so that one tile's softmax runs under the other's MMAs.  The
+// decoding warps give registers to the softmax warps.  Every wait is bounded; a
+// CTA whose wait expired leaves NaN statistics, so that its rows come out NaN.
+//
+// The rotation of the queries is a product with the signed Hadamard matrix
+// (+-1, exact in bf16, as the queries are), one more MMA per tile.
+//
+// Partials lie as [128-row tile][split][D / 4][128 rows][4], so that the
+// thread that owns a row writes 16 bytes beside its neighbours'.
 #pragma once
 
 #include "prefill.cuh"
@@ -29,26 +35,39 @@
 
 namespace tq {
 
-constexpr int kPfSoft = 8, kPfLoad = 8;  // softmax and loading warps
+constexpr int kPfSoft = 8, kPfLoad = 16;  // softmax and loading warps
 constexpr int kPfThreads = 32 * (kPfSoft + kPfLoad + 1);
 constexpr int kPfRows = 256;
+// Registers per thread: 72 at launch (25 warps: seven on one of the SM's four
+// partitions), then 104 for the softmax and 56 for the decoding warps, no more
+// in sum than at launch: 8 x 104 + 16 x 56 + 72 <= 25 x 72.
+constexpr int kPfLaunchRegs = 72, kPfSoftRegs = 104, kPfLoadRegs = 56;
+static_assert(kPfSoft * kPfSoftRegs + kPfLoad * kPfLoadRegs + kPfLaunchRegs <= (kPfSoft + kPfLoad + 1) * kPfLaunchRegs,
+              "the registers that some warps take, others gave");
 
 template <int D>
 struct PfCfg {
   static constexpr int TILE = 128 * D * 2;      // bytes of a 128-row operand tile
   static constexpr int Q = 0, K = 2 * TILE, V = 4 * TILE, MISC = 6 * TILE;
-  static constexpr int SMEM = MISC + 2560 + 1024;  // + bookkeeping + alignment slack
+  static constexpr int SMEM = MISC + 1024 + 1024;  // + bookkeeping + alignment slack
 };
 
 struct PfMisc {
-  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2], fin;
+  uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_full[2], o_done[2], rot, fin;
   uint32_t tbase;
   int abort_;
-  float red[2][17];
-  float qf[kPfRows];  // logit factor of a row
-  int lim[kPfRows];   // tokens it sees, counted from the run's origin
+  float red[2][kPfThreads / 32];
 };
-static_assert(sizeof(PfMisc) <= 2560, "bookkeeping block");
+static_assert(sizeof(PfMisc) <= 1024, "bookkeeping block");
+
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -66,6 +85,12 @@ __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, ui
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
+}
+// true in one lane of a converged warp, in a form that keeps the MMA loop's operands in uniform registers
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
 }
 constexpr uint32_t kIdescBf16 = (1u << 7) | (1u << 10);  // bf16 A and B
 
@@ -109,66 +134,85 @@ __device__ __forceinline__ uint4 decode_codes(uint32_t x, const Planes& pl) {
                     __byte_perm(a1, b1, 0x7362));
 }
 
-// One record's keys or values into a stage: warp w of the eight takes tokens
-// 16 w .. 16 w + 15, a lane eight codes (16 bytes of f16) at a time.
-template <int D, int B>
-__device__ __forceinline__ void decode_tile(const CodecDev& c, const uint8_t* rec, const Planes& pl, float nscale,
-                                            unsigned char* st, int w, int lane) {
-  constexpr int CH = D / 8, PER = 16 * CH / 32;  // chunks per row, per lane
-  const int rb = D * B / 8;
+// One record's keys or values into a stage: warp w of the sixteen takes tokens
+// 8 w .. 8 w + 7, a lane eight codes (16 bytes of f16) at a time.  The
+// packed words of the next tile are loaded before this one's are decoded.
+template <int D>
+struct Packed {
+  static constexpr int CH = D / 8, PER = 8 * CH / 32;  // chunks per row, per lane
   uint32_t x[PER];
+  float n;
+};
+template <int D, int B>
+__device__ __forceinline__ void load_packed(const CodecDev& c, const uint8_t* rec, int w, int lane, Packed<D>& k) {
+  using P = Packed<D>;
+  const uint8_t* rows = rec + 8 * w * (D * B / 8);
 #pragma unroll
-  for (int k = 0; k < PER; ++k) {
-    const int i = lane + 32 * k;
-    x[k] = load_codes<B>(rec + (16 * w + i / CH) * rb, i % CH);
-  }
-  const float n = __ldg(reinterpret_cast<const float*>(rec + c.off_norm) + 16 * w + (lane & 15)) * nscale;
+  for (int i = 0; i < P::PER; ++i)
+    k.x[i] = load_codes<B>(rows + ((lane + 32 * i) / P::CH) * (D * B / 8), (lane + 32 * i) % P::CH);
+  k.n = __ldg(reinterpret_cast<const float*>(rec + c.off_norm) + 8 * w + (lane & 7));
+}
+template <int D, int B>
+__device__ __forceinline__ void store_decoded(const Packed<D>& k, float n, const Planes& pl, unsigned char* st, int w,
+                                              int lane) {
+  using P = Packed<D>;
 #pragma unroll
-  for (int k = 0; k < PER; ++k) {
-    const int i = lane + 32 * k, row = i / CH, ch = i % CH;
+  for (int i = 0; i < P::PER; ++i) {
+    const int row = (lane + 32 * i) / P::CH, ch = (lane + 32 * i) % P::CH;
     const __half2 s = __float2half2_rn(__shfl_sync(0xffffffffu, n, row));
-    uint4 v = decode_codes<B>(x[k], pl);
+    uint4 v = decode_codes<B>(k.x[i], pl);
     v = make_uint4(hmul2(v.x, s), hmul2(v.y, s), hmul2(v.z, s), hmul2(v.w, s));
-    *reinterpret_cast<uint4*>(st + (ch >> 3) * 16384 + sw128_off(16 * w + row, ch & 7)) = v;
+    *reinterpret_cast<uint4*>(st + (ch >> 3) * 16384 + sw128_off(8 * w + row, ch & 7)) = v;
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void load_tile(const CodecDev& c, const uint8_t* rec, int w, int lane, Packed<D>& k) {
+  switch (c.bits) {
+    case 1: load_packed<D, 1>(c, rec, w, lane, k); break;
+    case 2: load_packed<D, 2>(c, rec, w, lane, k); break;
+    case 3: load_packed<D, 3>(c, rec, w, lane, k); break;
+    default: load_packed<D, 4>(c, rec, w, lane, k); break;
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void decode_tile(const CodecDev& c, const uint8_t* rec, const Packed<D>& k, const Planes& pl,
+                                            float nscale, unsigned char* st, int w, int lane) {
+  const float n = k.n * nscale;
+  switch (c.bits) {
+    case 1: store_decoded<D, 1>(k, n, pl, st, w, lane); break;
+    case 2: store_decoded<D, 2>(k, n, pl, st, w, lane); break;
+    case 3: store_decoded<D, 3>(k, n, pl, st, w, lane); break;
+    default: store_decoded<D, 4>(k, n, pl, st, w, lane); break;
   }
   if (c.has_outl) {  // the warp's tokens' side lists replace their coordinates
     const uint32_t* cw = reinterpret_cast<const uint32_t*>(rec + c.off_count);
-    const int slot = 16 * w + (lane & 15);
+    const int slot = 8 * w + (lane & 7);
     int from = 0;
-    for (int q = 0; q < 4 * w; ++q) from = __dp4a(__ldg(cw + q), 0x01010101u, (uint32_t)from);
+    for (int q = 0; q < 2 * w; ++q) from = __dp4a(__ldg(cw + q), 0x01010101u, (uint32_t)from);
     const int mine = __ldg(rec + c.off_count + slot);
     int inc = mine;
 #pragma unroll
-    for (int m = 1; m < 16; m <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, inc, m, 16);
-      if ((lane & 15) >= m) inc += o;
+    for (int m = 1; m < 8; m <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, inc, m, 8);
+      if ((lane & 7) >= m) inc += o;
     }
     from += inc - mine;
     const int cnt = min(mine, max(c.cap - from, 0));
     const uint32_t* ent = reinterpret_cast<const uint32_t*>(rec + c.off_entries);
     __syncwarp();
 #pragma unroll 1
-    for (int row = 0; row < 16; ++row) {
+    for (int row = 0; row < 8; ++row) {
       const int f = __shfl_sync(0xffffffffu, from, row), m = __shfl_sync(0xffffffffu, cnt, row);
       const float s = __shfl_sync(0xffffffffu, n, row) * kTableScale;
       for (int e = lane; e < m; e += 32) {
         const uint32_t en = __ldg(ent + f + e);
         const int j = en & (D - 1);
-        *reinterpret_cast<__half*>(st + (j >> 6) * 16384 + sw128_off(16 * w + row, (j >> 3) & 7) + 2 * (j & 7)) =
+        *reinterpret_cast<__half*>(st + (j >> 6) * 16384 + sw128_off(8 * w + row, (j >> 3) & 7) + 2 * (j & 7)) =
             __float2half_rn(bf16_hi(en) * s);
       }
     }
-  }
-}
-
-template <int D>
-__device__ __forceinline__ void decode_tile_b(const CodecDev& c, const uint8_t* rec, const Planes& pl, float nscale,
-                                              unsigned char* st, int w, int lane) {
-  switch (c.bits) {
-    case 1: decode_tile<D, 1>(c, rec, pl, nscale, st, w, lane); break;
-    case 2: decode_tile<D, 2>(c, rec, pl, nscale, st, w, lane); break;
-    case 3: decode_tile<D, 3>(c, rec, pl, nscale, st, w, lane); break;
-    default: decode_tile<D, 4>(c, rec, pl, nscale, st, w, lane); break;
   }
 }
 
@@ -191,9 +235,11 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
   const int k0 = split * (DENSE ? pp.tps : pp.cps * kChunk);
   const int k1 = min(min(k0 + (DENSE ? pp.tps : pp.cps * kChunk), DENSE ? cl.len : cl.n * kChunk), top);
   const int sidx = DENSE ? pp.Sc + split : split;
-  const int64_t wrow = unit * pp.rows + r0;
+  // partials of the CTA's first 128-row tile (a second one follows S blocks later)
+  const int64_t blk = ((unit * ((pp.rows + 127) / 128) + 2 * tile) * S + sidx) * 128;
   if (k0 >= k1) {
-    for (int r = tid; r < rn; r += kPfThreads) pp.ws_ml[(wrow + r) * S + sidx] = make_float2(-INFINITY, 0.f);
+    for (int r = tid; r < rn; r += kPfThreads)
+      pp.ws_ml[blk + (r >> 7) * S * 128 + (r & 127)] = make_float2(-INFINITY, 0.f);
     return;
   }
   const int n = (k1 - k0 + kChunk - 1) / kChunk;  // 128-token tiles
@@ -217,6 +263,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
       mbar_init(&ms.p_full[i], 4);
       mbar_init(&ms.o_done[i], 1);
     }
+    mbar_init(&ms.rot, 1);
     mbar_init(&ms.fin, 1);
     ms.abort_ = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -224,9 +271,12 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
   if (warp == kPfSoft + kPfLoad) tmem_alloc(&ms.tbase, 512);
   if constexpr (!DENSE) {  // the run's largest scales
     float mk = 0.f, mv = 0.f;
-    for (int i = tid; i < n * kChunk; i += kPfThreads) {
-      mk = fmaxf(mk, fabsf(__ldg(reinterpret_cast<const float*>(rec_at(true, c0 + i / kChunk) + p.kc.off_norm) + i % kChunk)));
-      mv = fmaxf(mv, fabsf(__ldg(reinterpret_cast<const float*>(rec_at(false, c0 + i / kChunk) + p.vc.off_norm) + i % kChunk)));
+    for (int i = tid; i < n * (kChunk / 4); i += kPfThreads) {
+      const int c = c0 + i / (kChunk / 4), o = i % (kChunk / 4);
+      const float4 x = __ldg(reinterpret_cast<const float4*>(rec_at(true, c) + p.kc.off_norm) + o);
+      const float4 y = __ldg(reinterpret_cast<const float4*>(rec_at(false, c) + p.vc.off_norm) + o);
+      mk = fmaxf(mk, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
+      mv = fmaxf(mv, fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w))));
     }
     mk = warp_max(mk);
     mv = warp_max(mv);
@@ -234,69 +284,30 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
       ms.red[0][warp] = mk;
       ms.red[1][warp] = mv;
     }
-    __syncthreads();
   }
-  float ek = 1.f, ev = 1.f;  // 2^-(E+1) of keys and values
-  if constexpr (!DENSE) {
-    float mk = ms.red[0][0], mv = ms.red[1][0];
-    for (int w = 1; w < 17; ++w) {
-      mk = fmaxf(mk, ms.red[0][w]);
-      mv = fmaxf(mv, ms.red[1][w]);
+  {  // queries, bf16 as they are (the softmax scale's sign folded in)
+    constexpr int CH = D / 8;
+    const uint32_t flip = p.sscale < 0.f ? 0x80008000u : 0u;
+    for (int i = tid; i < 128 * nt * CH; i += kPfThreads) {
+      const int r = i / CH, ch = i % CH, row = r0 + r;
+      uint4 v = make_uint4(0, 0, 0, 0);
+      if (r < rn)
+        v = __ldg(reinterpret_cast<const uint4*>(p.q + l * p.q_ls + b * p.q_bs + (int64_t)(row / p.G) * p.q_ts +
+                                                 (int64_t)(h * p.G + row % p.G) * D) + ch);
+      v = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
+      *reinterpret_cast<uint4*>(sm + C::Q + (r >> 7) * C::TILE + (ch >> 3) * 16384 + sw128_off(r & 127, ch & 7)) = v;
     }
-    ek = pow2i(-1 - exp_of(mk));
-    ev = pow2i(-1 - exp_of(mv));
-  }
-  {  // query rows, a warp each: lane holds D / 32 coordinates
-    constexpr int E = D / 32;
-    const float sgn = p.sscale < 0.f ? -1.f : 1.f;
-    for (int r = warp; r < 128 * nt; r += kPfThreads / 32) {
-      const int row = r0 + r;
-      float x[E];
+    if constexpr (!DENSE) {  // signed Hadamard matrix: row n, column k: (-1)^popc(n & k) s_k
+      for (int i = tid; i < D * CH; i += kPfThreads) {
+        const int n_ = i / CH, ch = i % CH;
+        const uint32_t sg = (p.kc.signs[ch >> 2] >> (8 * (ch & 3))) ^ (__popc((n_ >> 3) & ch) & 1 ? 0xFFu : 0u);
+        uint32_t w[4];
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = 0.f;
-      if (r < rn) {
-        const uint16_t* qp = p.q + l * p.q_ls + b * p.q_bs + (int64_t)(row / p.G) * p.q_ts +
-                             (int64_t)(h * p.G + row % p.G) * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; e += 2) {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(qp + e);
-          x[e] = bf16_lo(w) * sgn;
-          x[e + 1] = bf16_hi(w) * sgn;
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t s0 = (sg >> (2 * j)) ^ __popc(n_ & (2 * j)), s1 = (sg >> (2 * j + 1)) ^ __popc(n_ & (2 * j + 1));
+          w[j] = 0x3F803F80u | ((s0 & 1u) << 15) | ((s1 & 1u) << 31);
         }
-      }
-      float f = fabsf(p.sscale);
-      uint32_t w[E / 2];
-      if constexpr (DENSE) {
-#pragma unroll
-        for (int e = 0; e < E; e += 2) w[e / 2] = pack2_bf16(x[e], x[e + 1]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const int j = lane * E + e;
-          if ((p.kc.signs[j >> 5] >> (j & 31)) & 1u) x[e] = -x[e];
-        }
-        fwht_regs<E>(x);
-        fwht_lanes<E>(x, lane, 32);
-        float mx = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          x[e] *= inv_sqrt_dim<D>();
-          mx = fmaxf(mx, fabsf(x[e]));
-        }
-        mx = warp_max(mx);
-        const int s = mx > 0.f ? 13 - exp_of(mx) : 0;
-        const float sc = pow2i(s);
-        f = f * pow2i(-15 - s) * (1.f / ek);
-#pragma unroll
-        for (int e = 0; e < E; e += 2) w[e / 2] = pack2_f16(x[e] * sc, x[e + 1] * sc);
-      }
-      const int j = lane * E;
-      unsigned char* dst = sm + C::Q + (r >> 7) * C::TILE + (j >> 6) * 16384 + sw128_off(r & 127, (j >> 3) & 7) + 2 * (j & 7);
-      if constexpr (E == 4) *reinterpret_cast<uint2*>(dst) = make_uint2(w[0], w[1]);
-      else *reinterpret_cast<uint32_t*>(dst) = w[0];
-      if (lane == 0) {
-        ms.qf[r] = f;
-        ms.lim[r] = r < rn ? row_limit(p, cl, tb, row) - base - k0 : 0x7FFFFFFF;
+        *reinterpret_cast<uint4*>(sm + C::K + (ch >> 3) * 16384 + sw128_off(n_, ch & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
       }
     }
   }
@@ -304,12 +315,69 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tb0 = ms.tbase;
   volatile int* abort_f = &ms.abort_;
+  float ek = 1.f, ev = 1.f;  // 2^-(E+1) of keys and values
+  float f = fabsf(p.sscale);  // logit factor of the thread's row (softmax warps)
+  if constexpr (!DENSE) {
+    float mk = ms.red[0][lane < kPfThreads / 32 ? lane : 0], mv = ms.red[1][lane < kPfThreads / 32 ? lane : 0];
+    ek = pow2i(-1 - exp_of(warp_max(mk)));
+    ev = pow2i(-1 - exp_of(warp_max(mv)));
+    // rotation: scores' columns receive Q H, which return to the Q tiles as f16
+    if (warp == kPfSoft + kPfLoad) {
+      if (elect_one()) {
+        const uint64_t dQ = sdesc_sw128(smem_u32(sm + C::Q), 16, 1024), dH = sdesc_sw128(smem_u32(sm + C::K), 16, 1024);
+        for (int t = 0; t < nt; ++t)
+#pragma unroll
+          for (int ks = 0; ks < D / 16; ++ks) {
+            const uint64_t o = (ks >> 2) * 1024 + 2 * (ks & 3);
+            umma_f16(ms.tbase + 128 * t, dQ + t * (C::TILE / 16) + o, dH + o,
+                     idesc_f16(128, D, false, false) | kIdescBf16, ks != 0);
+          }
+        umma_commit(&ms.rot);
+      }
+      __syncwarp();
+    } else if (warp < 4 * nt) {
+      mbar_wait(&ms.rot, 0, abort_f);
+      tc_fence_after();
+      const uint32_t tS = ms.tbase + 128 * (warp >> 2) + ((uint32_t)(32 * (warp & 3)) << 16);
+      float mx = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t a[32];
+        tmem_ld32(tS + 32 * c, a);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) mx = fmaxf(mx, fabsf(__uint_as_float(a[j])));
+      }
+      mx *= inv_sqrt_dim<D>();
+      const int s = mx > 0.f ? 13 - exp_of(mx) : 0;  // largest in [2^13, 2^14)
+      const float sc = pow2i(s) * inv_sqrt_dim<D>();
+      f *= pow2i(-15 - s) * (1.f / ek);
+      const int r = 32 * (warp & 3) + lane;
+      unsigned char* dst = sm + C::Q + (warp >> 2) * C::TILE;
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t a[32], w[16];
+        tmem_ld32(tS + 32 * c, a);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; j += 2) w[j / 2] = pack2_f16(__uint_as_float(a[j]) * sc, __uint_as_float(a[j + 1]) * sc);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          *reinterpret_cast<uint4*>(dst + (c >> 1) * 16384 + sw128_off(r, 4 * (c & 1) + k)) =
+              make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
+      }
+      fence_async_smem();
+      tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+  }
+  const uint32_t tb0 = ms.tbase;
 
   if (warp == kPfSoft + kPfLoad) {
     // ---------------------------------------------------------------- MMA issue
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t T = DENSE ? kIdescBf16 : 0u;
       constexpr uint32_t IS = idesc_f16(128, 128, false, false) | T;
       constexpr uint32_t IV = idesc_f16(128, D, false, true) | T;
@@ -356,9 +424,10 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
     __syncwarp();
   } else if (warp >= kPfSoft) {
     // ---------------------------------------------------------------- keys and values
+    regs_down<kPfLoadRegs>();
     const int w = warp - kPfSoft;
     if constexpr (DENSE) {
-      constexpr int CH = D / 8, PER = 16 * CH / 32;
+      constexpr int CH = D / 8, PER = 8 * CH / 32;
       const int cap = p.tail_cap;
       const int start = p.tail_start ? ((p.tail_start[lb] % cap) + cap) % cap : 0;
       const int64_t ring = l * p.tail_ls + (int64_t)(b * p.Hkv + h) * cap * D;
@@ -371,7 +440,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
           unsigned char* st = sm + (kv ? C::V : C::K) + s * C::TILE;
 #pragma unroll
           for (int k = 0; k < PER; ++k) {
-            const int x = lane + 32 * k, row = 16 * w + x / CH, ch = x % CH;
+            const int x = lane + 32 * k, row = 8 * w + x / CH, ch = x % CH;
             const int tok = min(k0 + i * kChunk + row, cl.len - 1);
             cp_async16(st + (ch >> 3) * 16384 + sw128_off(row, ch & 7),
                        src + (int64_t)((start + (int64_t)tok) % cap) * D + 8 * ch);
@@ -391,28 +460,35 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
       }
     } else {
       const Planes kpl = make_planes(p.kc, kTableScale), vpl = make_planes(p.vc, kTableScale);
+      Packed<D> xk, xv;
+      load_tile<D>(p.kc, rec_at(true, c0), w, lane, xk);
+      load_tile<D>(p.vc, rec_at(false, c0), w, lane, xv);
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
         const int s = i & 1, ph = ((i >> 1) & 1) ^ 1;
         mbar_wait(&ms.k_empty[s], ph, abort_f);
-        decode_tile_b<D>(p.kc, rec_at(true, c0 + i), kpl, ek, sm + C::K + s * C::TILE, w, lane);
+        decode_tile<D>(p.kc, rec_at(true, c0 + i), xk, kpl, ek, sm + C::K + s * C::TILE, w, lane);
+        if (i + 1 < n) load_tile<D>(p.kc, rec_at(true, c0 + i + 1), w, lane, xk);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.k_full[s]);
         mbar_wait(&ms.v_empty[s], ph, abort_f);
-        decode_tile_b<D>(p.vc, rec_at(false, c0 + i), vpl, ev, sm + C::V + s * C::TILE, w, lane);
+        decode_tile<D>(p.vc, rec_at(false, c0 + i), xv, vpl, ev, sm + C::V + s * C::TILE, w, lane);
+        if (i + 1 < n) load_tile<D>(p.vc, rec_at(false, c0 + i + 1), w, lane, xv);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.v_full[s]);
       }
     }
-  } else if ((warp >> 2) < nt) {
+  } else {
     // ---------------------------------------------------------------- softmax: a thread per row
+    regs_up<kPfSoftRegs>();
+    if ((warp >> 2) < nt) {
     const int t = warp >> 2, q = warp & 3, r = 128 * t + 32 * q + lane;
     const uint32_t lrow = (uint32_t)(32 * q) << 16;
     const uint32_t tS = tb0 + 128 * t + lrow, tO = tb0 + 256 + D * t + lrow;
-    const float f = ms.qf[r];
-    const int lim = ms.lim[r];
+    // tokens it sees, counted from the run's first; rows of no query see everything
+    const int lim = r < rn ? row_limit(p, cl, tb, r0 + r) - base - k0 : 0x7FFFFFFF;
     float mref = -INFINITY, lsum = 0.f;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
@@ -420,7 +496,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
       tc_fence_after();
       const int seen = lim - i * kChunk;  // columns below it
       const bool edge = __any_sync(0xffffffffu, seen < kChunk);
-      float mx = -INFINITY;
+      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t a[32];
@@ -428,12 +504,13 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
         tmem_ld_wait();
         if (edge) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) mx = fmaxf(mx, 32 * c + j < seen ? __uint_as_float(a[j]) : -INFINITY);
+          for (int j = 0; j < 32; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], 32 * c + j < seen ? __uint_as_float(a[j]) : -INFINITY);
         } else {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(a[j]));
+          for (int j = 0; j < 32; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(a[j]));
         }
       }
+      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
       float tm = mx > -INFINITY ? mx * f : -INFINITY;
       if (p.scap > 0.f) tm = soft_cap(tm, p.scap, p.iscap);
       if (__any_sync(0xffffffffu, tm > mref + 8.f)) {
@@ -489,7 +566,8 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
     mbar_wait(&ms.o_done[t], (n - 1) & 1, abort_f);
     tc_fence_after();
     const float un = DENSE ? 1.f : pow2i(-15) * (1.f / ev);
-    float* dst = pp.ws_acc + ((wrow + r) * S + sidx) * D;
+    const int64_t at = blk + (int64_t)t * S * 128;
+    float4* dst = reinterpret_cast<float4*>(pp.ws_acc) + at * (D / 4) + (r & 127);
 #pragma unroll
     for (int c = 0; c < D / 32; ++c) {
       uint32_t o[32];
@@ -498,17 +576,18 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
       if (r < rn) {
 #pragma unroll
         for (int j = 0; j < 32; j += 4)
-          *reinterpret_cast<float4*>(dst + 32 * c + j) =
+          dst[(8 * c + j / 4) * 128] =
               make_float4(__uint_as_float(o[j]) * un, __uint_as_float(o[j + 1]) * un, __uint_as_float(o[j + 2]) * un,
                           __uint_as_float(o[j + 3]) * un);
       }
     }
     if (r < rn) {
       const float bad = __int_as_float(0x7fc00000);
-      pp.ws_ml[(wrow + r) * S + sidx] = *abort_f ? make_float2(bad, bad)
-                                        : lsum > 0.f ? make_float2(mref, lsum) : make_float2(-INFINITY, 0.f);
+      pp.ws_ml[at + (r & 127)] = *abort_f ? make_float2(bad, bad)
+                                 : lsum > 0.f ? make_float2(mref, lsum) : make_float2(-INFINITY, 0.f);
     }
     tc_fence_before();
+    }
   }
   __syncthreads();
   if (warp == kPfSoft + kPfLoad) {
@@ -531,9 +610,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_umma_kernel(const __gri
 template <int D>
 cudaError_t prefill_umma_launch(const PrefillParams& pp, cudaStream_t s) {
   if (pp.Sc + pp.St == 0) return cudaSuccess;
-  const cudaError_t e =
-      cudaFuncSetAttribute(prefill_umma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PfCfg<D>::SMEM);
+  cudaError_t e = cudaFuncSetAttribute(prefill_umma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PfCfg<D>::SMEM);
   if (e != cudaSuccess) return e;
+  // the split of the registers counts on this many at launch
+  cudaFuncAttributes fa;
+  if ((e = cudaFuncGetAttributes(&fa, prefill_umma_kernel<D>)) != cudaSuccess) return e;
+  if (fa.numRegs != kPfLaunchRegs) return cudaErrorInvalidConfiguration;
   const dim3 grid(pp.tiles * (pp.Sc + pp.St), pp.q.B * pp.q.Hkv, pp.q.L);
   prefill_umma_kernel<D><<<grid, kPfThreads, PfCfg<D>::SMEM, s>>>(pp);
   return cudaGetLastError();
