@@ -235,21 +235,27 @@ tq_status prefill_plan(const tq_query_args* a, const tq_codec* kcod, const tq_co
   const int64_t units = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv;
   const int64_t sms = sm_count(), U = units * pp.tiles;
   if (d <= 128) {
-    // one CTA per SM: the split count that minimises waves x 128-token tiles
-    // per split, four tiles' worth of set-up and epilogue included, and the
-    // partials' traffic (about 0.03 tiles per CTA)
+    // One CTA per SM.  The split count that minimises, in 128-token tiles' time:
+    // waves of records' CTAs with six tiles' worth of set-up and epilogue each,
+    // the ring's CTAs in the last wave's idle SMs or after it, and the partials'
+    // traffic (about 0.03 tiles per CTA).
     const int64_t ring = cdiv(pp.q.max_tail, TQ_CHUNK), most = std::max<int64_t>(pp.q.max_chunks, ring);
     double best = 1e300;
-    for (int64_t per = 1, s = most; per <= most; per = s > 1 ? cdiv(most, --s) : most + 1) {
-      if (a->splits > 0 && s != std::min<int64_t>(a->splits, most)) continue;
-      const int64_t ctas = U * (cdiv(pp.q.max_chunks, per) + cdiv(ring, per));
-      const double cost = (double)cdiv(ctas, sms) * (double)(per + 4) + 0.03 * (double)ctas;
+    for (int64_t s = 1; s <= std::min<int64_t>(most, 128); ++s) {
+      if (a->splits > 0 && s != std::min<int64_t>(a->splits, std::min<int64_t>(most, 128))) continue;
+      const int64_t per = cdiv(most, s);
+      const int64_t sc = cdiv(pp.q.max_chunks, per), st = cdiv(ring, per);
+      const int64_t waves = cdiv(U * sc, sms);
+      const double one = (double)(sc ? cdiv(pp.q.max_chunks, sc) : 0) + 6, rest = (double)(st ? cdiv(ring, st) : 0) + 6;
+      const double idle = (double)(waves * sms - U * sc) * one, dense = (double)(U * st) * rest;
+      double cost = (double)waves * one + 0.03 * (double)(U * (sc + st));
+      if (dense > 0.9 * idle) cost += std::max(rest, (dense - 0.9 * idle) / (double)sms);
       if (cost < best) {
         best = cost;
         pp.cps = (int)per;
-        pp.Sc = (int)cdiv(pp.q.max_chunks, per);
+        pp.Sc = (int)sc;
         pp.tps = (int)(TQ_CHUNK * per);
-        pp.St = (int)cdiv(ring, per);
+        pp.St = (int)st;
       }
     }
   } else {
@@ -268,7 +274,7 @@ tq_status prefill_plan(const tq_query_args* a, const tq_codec* kcod, const tq_co
       pp.St = (int)cdiv(pp.q.max_tail, pp.tps);
     }
   }
-  if ((int64_t)pp.tiles * std::max(pp.Sc, pp.St) > 0x7FFFFFFFll || units * pp.rows > (1ll << 32)) return TQ_ERR_UNSUPPORTED;
+  if (U * (pp.Sc + pp.St) > 0x7FFFFFFFll || units * pp.rows > (1ll << 32)) return TQ_ERR_UNSUPPORTED;
   pp.out = (uint16_t*)a->out;
   pp.o_ls = a->out_layer_stride;
   pp.o_bs = a->out_batch_stride;

@@ -16,9 +16,9 @@
 // reference that follows the maximum only when it is passed by 2^8, so O is
 // rescaled rarely, by the warps that own the rows.
 //
-// Warps: 0-3 and 4-7 softmax of tile 0 and 1 (a thread per row), 8-23 decode
+// Warps: 0-3 and 4-7 softmax of tile 0 and 1 (a thread per row), 8-15 decode
 // records (or copy ring tokens) into two stages each of key and value tiles,
-// 24 issues MMAs.  A tile's MMAs run P V(i) then Q K(i+1), and the two tiles
+// 16 issues MMAs.  A tile's MMAs run P V(i) then Q K(i+1), and the two tiles
 // alternate, so that one tile's softmax runs under the other's MMAs.  The
 // decoding warps give registers to the softmax warps.  Every wait is bounded; a
 // CTA whose wait expired leaves NaN statistics, so that its rows come out NaN.
@@ -35,20 +35,22 @@
 
 namespace tq {
 
-constexpr int kPfSoft = 8, kPfLoad = 16;  // softmax and loading warps
+constexpr int kPfSoft = 8, kPfLoad = 8;  // softmax and loading warps
 constexpr int kPfThreads = 32 * (kPfSoft + kPfLoad + 1);
 constexpr int kPfRows = 256;
-// Registers per thread: 72 at launch (25 warps: seven on one of the SM's four
-// partitions), then 104 for the softmax and 56 for the decoding warps, no more
-// in sum than at launch: 8 x 104 + 16 x 56 + 72 <= 25 x 72.
-constexpr int kPfLaunchRegs = 72, kPfSoftRegs = 104, kPfLoadRegs = 56;
+constexpr float kPfMargin = 13.f;  // log2 of the largest weight kept against an old reference
+
+// Registers per thread: 96 at launch (17 warps: five on one of the SM's four
+// partitions), then 120 for the softmax and 72 for the decoding warps, no more
+// in sum than at launch.
+constexpr int kPfLaunchRegs = 96, kPfSoftRegs = 120, kPfLoadRegs = 72;
 static_assert(kPfSoft * kPfSoftRegs + kPfLoad * kPfLoadRegs + kPfLaunchRegs <= (kPfSoft + kPfLoad + 1) * kPfLaunchRegs,
               "the registers that some warps take, others gave");
 
 template <int D>
 struct PfCfg {
   static constexpr int TILE = 128 * D * 2;      // bytes of a 128-row operand tile
-  static constexpr int Q = 0, K = 2 * TILE, V = 4 * TILE, MISC = 6 * TILE;
+  static constexpr int Q = 0, K = 2 * TILE, V = 4 * TILE, LUT = 6 * TILE, MISC = LUT + 32768;
   static constexpr int SMEM = MISC + 1024 + 1024;  // + bookkeeping + alignment slack
 };
 
@@ -60,6 +62,11 @@ struct PfMisc {
 };
 static_assert(sizeof(PfMisc) <= 1024, "bookkeeping block");
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 template <int N>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -76,6 +83,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr));
 }
 // D (tensor memory) += A (tensor memory) * B (shared memory)
 __device__ __forceinline__ void umma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
@@ -99,17 +113,6 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, __half2 b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// eight codes of a packed row as nibbles; w holds the bytes that a lane loaded for them
-template <int B>
-__device__ __forceinline__ uint32_t load_codes(const uint8_t* row, int u) {
-  if constexpr (B == 4) return __ldg(reinterpret_cast<const uint32_t*>(row) + u);
-  else if constexpr (B == 2) return __ldg(reinterpret_cast<const uint16_t*>(row) + u);
-  else if constexpr (B == 1) return __ldg(row + u);
-  else {
-    const uint32_t* w = reinterpret_cast<const uint32_t*>(row) + ((3 * u) >> 2);
-    return __funnelshift_r(__ldg(w), __ldg(w + 1), 8 * ((3 * u) & 3));
-  }
-}
 // centroids of up to 16 levels as byte planes; with 8 levels or fewer one lookup a plane is enough
 template <int B>
 __device__ __forceinline__ uint4 decode_codes(uint32_t x, const Planes& pl) {
@@ -134,82 +137,127 @@ __device__ __forceinline__ uint4 decode_codes(uint32_t x, const Planes& pl) {
                     __byte_perm(a1, b1, 0x7362));
 }
 
-// One record's keys or values into a stage: warp w of the sixteen takes tokens
-// 8 w .. 8 w + 7, a lane eight codes (16 bytes of f16) at a time.  The
+// One record's keys or values into a stage: warp w of the eight takes tokens
+// 16 w .. 16 w + 15, a lane eight codes (16 bytes of f16) at a time.  The
 // packed words of the next tile are loaded before this one's are decoded.
 template <int D>
 struct Packed {
-  static constexpr int CH = D / 8, PER = 8 * CH / 32;  // chunks per row, per lane
+  static constexpr int CH = D / 8, PER = 16 * CH / 32;  // chunks per row, per lane
   uint32_t x[PER];
   float n;
 };
+// rec points at the record's rows of this lane: token 16 w + lane / CH, codes 8 (lane % CH) ..
 template <int D, int B>
-__device__ __forceinline__ void load_packed(const CodecDev& c, const uint8_t* rec, int w, int lane, Packed<D>& k) {
+__device__ __forceinline__ void load_packed(const uint8_t* rec, Packed<D>& k) {
   using P = Packed<D>;
-  const uint8_t* rows = rec + 8 * w * (D * B / 8);
+  constexpr int STEP = 32 / P::CH * (D * B / 8);  // bytes between a lane's chunks
 #pragma unroll
-  for (int i = 0; i < P::PER; ++i)
-    k.x[i] = load_codes<B>(rows + ((lane + 32 * i) / P::CH) * (D * B / 8), (lane + 32 * i) % P::CH);
-  k.n = __ldg(reinterpret_cast<const float*>(rec + c.off_norm) + 8 * w + (lane & 7));
+  for (int i = 0; i < P::PER; ++i) {
+    if constexpr (B == 4) k.x[i] = __ldg(reinterpret_cast<const uint32_t*>(rec + i * STEP));
+    else if constexpr (B == 2) k.x[i] = __ldg(reinterpret_cast<const uint16_t*>(rec + i * STEP));
+    else if constexpr (B == 1) k.x[i] = __ldg(rec + i * STEP);
+    else {  // the two words around three bytes (the second may lie past the row, inside the record)
+      const uint32_t o = (uint32_t)reinterpret_cast<uintptr_t>(rec) & 3u;
+      const uint32_t* w = reinterpret_cast<const uint32_t*>(rec - o + i * STEP);
+      k.x[i] = __funnelshift_r(__ldg(w), __ldg(w + 1), 8 * o);
+    }
+  }
 }
-template <int D, int B>
-__device__ __forceinline__ void store_decoded(const Packed<D>& k, float n, const Planes& pl, unsigned char* st, int w,
-                                              int lane) {
+// LUT: pairs of 4-bit codes by one shared-memory lookup in a table with a copy per
+// lane (entry e at 128 e + 4 lane, no bank conflicts), two logic operations a
+// pair where the byte planes take six a pair.
+template <int D, int B, bool LUT>
+__device__ __forceinline__ void store_decoded(const Packed<D>& k, float n, const Planes& pl, const unsigned char* lut,
+                                              unsigned char* st, int w, int lane) {
   using P = Packed<D>;
+  const uint32_t n2 = pack2_f16(n, n);
+  st += w * 2048;
+  const uint32_t lo = 4 * lane;
 #pragma unroll
   for (int i = 0; i < P::PER; ++i) {
     const int row = (lane + 32 * i) / P::CH, ch = (lane + 32 * i) % P::CH;
-    const __half2 s = __float2half2_rn(__shfl_sync(0xffffffffu, n, row));
-    uint4 v = decode_codes<B>(k.x[i], pl);
+    const uint32_t sw = __shfl_sync(0xffffffffu, n2, row);
+    const __half2 s = *reinterpret_cast<const __half2*>(&sw);
+    uint4 v;
+    if constexpr (LUT) {
+      const uint32_t x = k.x[i];
+      v.x = *reinterpret_cast<const uint32_t*>(lut + (((x << 7) & 0x7F80u) | lo));
+      v.y = *reinterpret_cast<const uint32_t*>(lut + (((x >> 1) & 0x7F80u) | lo));
+      v.z = *reinterpret_cast<const uint32_t*>(lut + (((x >> 9) & 0x7F80u) | lo));
+      v.w = *reinterpret_cast<const uint32_t*>(lut + (((x >> 17) & 0x7F80u) | lo));
+    } else {
+      v = decode_codes<B>(k.x[i], pl);
+    }
     v = make_uint4(hmul2(v.x, s), hmul2(v.y, s), hmul2(v.z, s), hmul2(v.w, s));
-    *reinterpret_cast<uint4*>(st + (ch >> 3) * 16384 + sw128_off(8 * w + row, ch & 7)) = v;
+    *reinterpret_cast<uint4*>(st + (ch >> 3) * 16384 + row * 128 + (((ch ^ row) & 7) << 4)) = v;
   }
 }
 
+// Where a lane reads one codec's records: its rows and its token's scale.
+struct RecSource {
+  const uint8_t* layer;  // the layer's records
+  const uint8_t* next;   // next record of the run
+  int rows, bytes, bits, norm;
+};
 template <int D>
-__device__ __forceinline__ void load_tile(const CodecDev& c, const uint8_t* rec, int w, int lane, Packed<D>& k) {
-  switch (c.bits) {
-    case 1: load_packed<D, 1>(c, rec, w, lane, k); break;
-    case 2: load_packed<D, 2>(c, rec, w, lane, k); break;
-    case 3: load_packed<D, 3>(c, rec, w, lane, k); break;
-    default: load_packed<D, 4>(c, rec, w, lane, k); break;
+__device__ __forceinline__ RecSource rec_source(const CodecDev& c, const uint8_t* layer, int w, int lane) {
+  constexpr int CH = D / 8;
+  RecSource r;
+  r.layer = r.next = layer;
+  r.bits = c.bits;
+  r.bytes = c.rec_bytes;
+  r.rows = (16 * w + lane / CH) * (D * c.bits / 8) + lane % CH * c.bits;
+  r.norm = c.off_norm + 4 * (16 * w + (lane & 15));
+  return r;
+}
+template <int D>
+__device__ __forceinline__ void load_tile(const RecSource& r, Packed<D>& k) {
+  const uint8_t* at = r.next + r.rows;
+  switch (r.bits) {
+    case 1: load_packed<D, 1>(at, k); break;
+    case 2: load_packed<D, 2>(at, k); break;
+    case 3: load_packed<D, 3>(at, k); break;
+    default: load_packed<D, 4>(at, k); break;
   }
+  k.n = __ldg(reinterpret_cast<const float*>(r.next + r.norm));
 }
 
 template <int D>
 __device__ __forceinline__ void decode_tile(const CodecDev& c, const uint8_t* rec, const Packed<D>& k, const Planes& pl,
-                                            float nscale, unsigned char* st, int w, int lane) {
+                                            const unsigned char* lut, float nscale, unsigned char* st, int w, int lane) {
   const float n = k.n * nscale;
   switch (c.bits) {
-    case 1: store_decoded<D, 1>(k, n, pl, st, w, lane); break;
-    case 2: store_decoded<D, 2>(k, n, pl, st, w, lane); break;
-    case 3: store_decoded<D, 3>(k, n, pl, st, w, lane); break;
-    default: store_decoded<D, 4>(k, n, pl, st, w, lane); break;
+    case 1: store_decoded<D, 1, false>(k, n, pl, lut, st, w, lane); break;
+    case 2: store_decoded<D, 2, false>(k, n, pl, lut, st, w, lane); break;
+    case 3: store_decoded<D, 3, false>(k, n, pl, lut, st, w, lane); break;
+    default:
+      if (lut) store_decoded<D, 4, true>(k, n, pl, lut, st, w, lane);
+      else store_decoded<D, 4, false>(k, n, pl, lut, st, w, lane);
   }
   if (c.has_outl) {  // the warp's tokens' side lists replace their coordinates
     const uint32_t* cw = reinterpret_cast<const uint32_t*>(rec + c.off_count);
-    const int slot = 8 * w + (lane & 7);
+    const int slot = 16 * w + (lane & 15);
     int from = 0;
-    for (int q = 0; q < 2 * w; ++q) from = __dp4a(__ldg(cw + q), 0x01010101u, (uint32_t)from);
+    for (int q = 0; q < 4 * w; ++q) from = __dp4a(__ldg(cw + q), 0x01010101u, (uint32_t)from);
     const int mine = __ldg(rec + c.off_count + slot);
     int inc = mine;
 #pragma unroll
-    for (int m = 1; m < 8; m <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, inc, m, 8);
-      if ((lane & 7) >= m) inc += o;
+    for (int m = 1; m < 16; m <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, inc, m, 16);
+      if ((lane & 15) >= m) inc += o;
     }
     from += inc - mine;
     const int cnt = min(mine, max(c.cap - from, 0));
     const uint32_t* ent = reinterpret_cast<const uint32_t*>(rec + c.off_entries);
     __syncwarp();
 #pragma unroll 1
-    for (int row = 0; row < 8; ++row) {
+    for (int row = 0; row < 16; ++row) {
       const int f = __shfl_sync(0xffffffffu, from, row), m = __shfl_sync(0xffffffffu, cnt, row);
       const float s = __shfl_sync(0xffffffffu, n, row) * kTableScale;
       for (int e = lane; e < m; e += 32) {
         const uint32_t en = __ldg(ent + f + e);
         const int j = en & (D - 1);
-        *reinterpret_cast<__half*>(st + (j >> 6) * 16384 + sw128_off(8 * w + row, (j >> 3) & 7) + 2 * (j & 7)) =
+        *reinterpret_cast<__half*>(st + (j >> 6) * 16384 + sw128_off(16 * w + row, (j >> 3) & 7) + 2 * (j & 7)) =
             __float2half_rn(bf16_hi(en) * s);
       }
     }
@@ -217,15 +265,14 @@ __device__ __forceinline__ void decode_tile(const CodecDev& c, const uint8_t* re
 }
 
 template <int D, bool DENSE>
-__device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsigned char* sm, int tile, int split) {
+__device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsigned char* sm, int64_t unit, int tile,
+                                                  int split) {
   using C = PfCfg<D>;
   const QueryParams& p = pp.q;
   PfMisc& ms = *reinterpret_cast<PfMisc*>(sm + C::MISC);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.y % p.Hkv, b = blockIdx.y / p.Hkv, l = blockIdx.z;
+  const int h = (int)(unit % p.Hkv), lb = (int)(unit / p.Hkv), b = lb % p.B, l = lb / p.B;
   const int S = pp.Sc + pp.St;
-  const int lb = l * p.B + b;
-  const int64_t unit = (int64_t)lb * p.Hkv + h;
   const CacheLen cl = cache_len(p, lb);
   const int tb = query_len(p, b);
   const int r0 = tile * kPfRows, rn = min(kPfRows, tb * p.G - r0);
@@ -269,6 +316,12 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kPfSoft + kPfLoad) tmem_alloc(&ms.tbase, 512);
+  bool vtable = false;  // the values are decoded through the lookup table
+  if constexpr (!DENSE) {
+    vtable = p.vc.bits == 4;
+    if (p.kc.bits == 4)
+      for (int k = 8; k < 16; ++k) vtable = vtable && p.kc.centroids[k] == p.vc.centroids[k];  // tables are symmetric
+  }
   if constexpr (!DENSE) {  // the run's largest scales
     float mk = 0.f, mv = 0.f;
     for (int i = tid; i < n * (kChunk / 4); i += kPfThreads) {
@@ -296,6 +349,16 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
                                                  (int64_t)(h * p.G + row % p.G) * D) + ch);
       v = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
       *reinterpret_cast<uint4*>(sm + C::Q + (r >> 7) * C::TILE + (ch >> 3) * 16384 + sw128_off(r & 127, ch & 7)) = v;
+    }
+    if constexpr (!DENSE) {
+      // lookup table of the 4-bit codec (the keys', and the values' where it is the same)
+      const CodecDev& c4 = p.kc.bits == 4 ? p.kc : p.vc;
+      if (c4.bits == 4)
+        for (int i = tid; i < 256; i += kPfThreads) {
+          const uint32_t v = pack2_f16(c4.centroids[i & 15] * kTableScale, c4.centroids[i >> 4] * kTableScale);
+#pragma unroll
+          for (int k = 0; k < 8; ++k) reinterpret_cast<uint4*>(sm + C::LUT + 128 * i)[(k + i) & 7] = make_uint4(v, v, v, v);
+        }
     }
     if constexpr (!DENSE) {  // signed Hadamard matrix: row n, column k: (-1)^popc(n & k) s_k
       for (int i = tid; i < D * CH; i += kPfThreads) {
@@ -337,7 +400,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
       }
       __syncwarp();
     } else if (warp < 4 * nt) {
-      mbar_wait(&ms.rot, 0, abort_f);
+      mbar_wait_idle(&ms.rot, 0, abort_f);
       tc_fence_after();
       const uint32_t tS = ms.tbase + 128 * (warp >> 2) + ((uint32_t)(32 * (warp & 3)) << 16);
       float mx = 0.f;
@@ -394,15 +457,15 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
         }
         umma_commit(&ms.s_full[t]);
       };
-      mbar_wait(&ms.k_full[0], 0, abort_f);
+      mbar_wait_idle(&ms.k_full[0], 0, abort_f);
       tc_fence_after();
       for (int t = 0; t < nt; ++t) scores(t, 0);
       umma_commit(&ms.k_empty[0]);
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
         for (int t = 0; t < nt; ++t) {
-          if (t == 0) mbar_wait(&ms.v_full[i & 1], (i >> 1) & 1, abort_f);
-          mbar_wait(&ms.p_full[t], i & 1, abort_f);
+          if (t == 0) mbar_wait_idle(&ms.v_full[i & 1], (i >> 1) & 1, abort_f);
+          mbar_wait_idle(&ms.p_full[t], i & 1, abort_f);
           tc_fence_after();
           const uint64_t bv = dV + (i & 1) * TS;
 #pragma unroll
@@ -411,8 +474,8 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
           umma_commit(&ms.o_done[t]);
           if (t == nt - 1) umma_commit(&ms.v_empty[i & 1]);
           if (i + 1 < n) {
-            if (t == 0) mbar_wait(&ms.k_full[(i + 1) & 1], ((i + 1) >> 1) & 1, abort_f);
-            mbar_wait(&ms.o_done[t], i & 1, abort_f);  // P is read before S takes its columns
+            if (t == 0) mbar_wait_idle(&ms.k_full[(i + 1) & 1], ((i + 1) >> 1) & 1, abort_f);
+            mbar_wait_idle(&ms.o_done[t], i & 1, abort_f);  // P is read before S takes its columns
             tc_fence_after();
             scores(t, i + 1);
             if (t == nt - 1) umma_commit(&ms.k_empty[(i + 1) & 1]);
@@ -427,7 +490,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
     regs_down<kPfLoadRegs>();
     const int w = warp - kPfSoft;
     if constexpr (DENSE) {
-      constexpr int CH = D / 8, PER = 8 * CH / 32;
+      constexpr int CH = D / 8, PER = 16 * CH / 32;
       const int cap = p.tail_cap;
       const int start = p.tail_start ? ((p.tail_start[lb] % cap) + cap) % cap : 0;
       const int64_t ring = l * p.tail_ls + (int64_t)(b * p.Hkv + h) * cap * D;
@@ -436,11 +499,11 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv) {
           const uint16_t* src = (kv ? p.vtail : p.ktail) + ring;
-          mbar_wait(kv ? &ms.v_empty[s] : &ms.k_empty[s], ph, abort_f);
+          mbar_wait_idle(kv ? &ms.v_empty[s] : &ms.k_empty[s], ph, abort_f);
           unsigned char* st = sm + (kv ? C::V : C::K) + s * C::TILE;
 #pragma unroll
           for (int k = 0; k < PER; ++k) {
-            const int x = lane + 32 * k, row = 8 * w + x / CH, ch = x % CH;
+            const int x = lane + 32 * k, row = 16 * w + x / CH, ch = x % CH;
             const int tok = min(k0 + i * kChunk + row, cl.len - 1);
             cp_async16(st + (ch >> 3) * 16384 + sw128_off(row, ch & 7),
                        src + (int64_t)((start + (int64_t)tok) % cap) * D + 8 * ch);
@@ -460,21 +523,36 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
       }
     } else {
       const Planes kpl = make_planes(p.kc, kTableScale), vpl = make_planes(p.vc, kTableScale);
+      const unsigned char* klut = p.kc.bits == 4 ? sm + C::LUT : nullptr;
+      const unsigned char* vlut = vtable ? sm + C::LUT : nullptr;
+      RecSource ks = rec_source<D>(p.kc, kl, w, lane), vs = rec_source<D>(p.vc, vl, w, lane);
+      auto seek = [&](RecSource& r, int c) {  // contiguous records follow one another
+        if (p.table || c == c0) r.next = r.layer + rec_offset(p.table, p.table_stride, p.rec_cap, p.Hkv, b, h, c, r.bytes);
+        else r.next += r.bytes;
+      };
       Packed<D> xk, xv;
-      load_tile<D>(p.kc, rec_at(true, c0), w, lane, xk);
-      load_tile<D>(p.vc, rec_at(false, c0), w, lane, xv);
+      seek(ks, c0);
+      load_tile<D>(ks, xk);
+      seek(vs, c0);
+      load_tile<D>(vs, xv);
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
         const int s = i & 1, ph = ((i >> 1) & 1) ^ 1;
-        mbar_wait(&ms.k_empty[s], ph, abort_f);
-        decode_tile<D>(p.kc, rec_at(true, c0 + i), xk, kpl, ek, sm + C::K + s * C::TILE, w, lane);
-        if (i + 1 < n) load_tile<D>(p.kc, rec_at(true, c0 + i + 1), w, lane, xk);
+        mbar_wait_idle(&ms.k_empty[s], ph, abort_f);
+        decode_tile<D>(p.kc, ks.next, xk, kpl, klut, ek, sm + C::K + s * C::TILE, w, lane);
+        if (i + 1 < n) {
+          seek(ks, c0 + i + 1);
+          load_tile<D>(ks, xk);
+        }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.k_full[s]);
-        mbar_wait(&ms.v_empty[s], ph, abort_f);
-        decode_tile<D>(p.vc, rec_at(false, c0 + i), xv, vpl, ev, sm + C::V + s * C::TILE, w, lane);
-        if (i + 1 < n) load_tile<D>(p.vc, rec_at(false, c0 + i + 1), w, lane, xv);
+        mbar_wait_idle(&ms.v_empty[s], ph, abort_f);
+        decode_tile<D>(p.vc, vs.next, xv, vpl, vlut, ev, sm + C::V + s * C::TILE, w, lane);
+        if (i + 1 < n) {
+          seek(vs, c0 + i + 1);
+          load_tile<D>(vs, xv);
+        }
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.v_full[s]);
@@ -492,83 +570,103 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
     float mref = -INFINITY, lsum = 0.f;
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
-      mbar_wait(&ms.s_full[t], i & 1, abort_f);
+      mbar_wait_idle(&ms.s_full[t], i & 1, abort_f);
       tc_fence_after();
       const int seen = lim - i * kChunk;  // columns below it
       const bool edge = __any_sync(0xffffffffu, seen < kChunk);
-      float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t a[32];
-        tmem_ld32(tS + 32 * c, a);
-        tmem_ld_wait();
-        if (edge) {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], 32 * c + j < seen ? __uint_as_float(a[j]) : -INFINITY);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 32; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], __uint_as_float(a[j]));
-        }
-      }
-      const float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-      float tm = mx > -INFINITY ? mx * f : -INFINITY;
-      if (p.scap > 0.f) tm = soft_cap(tm, p.scap, p.iscap);
-      if (__any_sync(0xffffffffu, tm > mref + 8.f)) {
-        const float mn = tm > mref + 8.f ? tm : mref;
-        const float al = mref > -INFINITY ? ex2(mref - mn) : 0.f;  // 1 where the reference stays
-        const float sc = mn > -INFINITY ? al : 1.f;
-        lsum *= sc;
-        mref = mn;
-        if (i > 0) {  // P V(i - 1) is complete: the scores of this tile were issued after it
-#pragma unroll
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t o[32];
-            tmem_ld32(tO + 32 * c, o);
-            tmem_ld_wait();
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * sc);
-            tmem_st32(tO + 32 * c, o);
-          }
-        }
-      }
-      const float ref = mref > -INFINITY ? mref : 0.f;
-      const float2 f2v = f2(f, f), m2 = f2(-ref, -ref);
+      uint32_t w[64];  // weights as pairs; chunk c of S becomes columns 16 c .. 16 c + 15
+      float mx = -INFINITY;
       float2 sum = f2(0.f, 0.f);
+      bool again = edge || mref == -INFINITY || p.scap > 0.f;
+      if (!__any_sync(0xffffffffu, again)) {
+        // weights against the reference as it stands; the maximum is found on the way
+        const float2 f2v = f2(f, f), m2 = f2(-mref, -mref);
+        float x0 = -INFINITY;
+        uint32_t a[2][16];
+        tmem_ld16(tS, a[0]);
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t a[32], w[16];
-        tmem_ld32(tS + 32 * c, a);
-        tmem_ld_wait();
+        for (int c = 0; c < 8; ++c) {
+          tmem_ld_wait();
+          if (c < 7) tmem_ld16(tS + 16 * (c + 1), a[(c + 1) & 1]);
 #pragma unroll
-        for (int j = 0; j < 32; j += 2) {
-          float2 v = f2(__uint_as_float(a[j]), __uint_as_float(a[j + 1]));
-          if (p.scap > 0.f) {
-            v = f2(soft_cap(v.x * f, p.scap, p.iscap) - ref, soft_cap(v.y * f, p.scap, p.iscap) - ref);
-          } else {
-            v = fma2(v, f2v, m2);
+          for (int j = 0; j < 16; j += 2) {
+            float2 v = fma2(f2(__uint_as_float(a[c & 1][j]), __uint_as_float(a[c & 1][j + 1])), f2v, m2);
+            x0 = max3(x0, v.x, v.y);
+            v = f2(ex2(v.x), ex2(v.y));
+            sum = add2(sum, v);
+            w[8 * c + j / 2] = DENSE ? pack2_bf16(v.x, v.y) : pack2_f16(v.x, v.y);
           }
-          v = f2(ex2(v.x), ex2(v.y));
-          if (edge) {
-            if (32 * c + j >= seen) v.x = 0.f;
-            if (32 * c + j + 1 >= seen) v.y = 0.f;
-          }
-          sum = add2(sum, v);
-          w[j / 2] = DENSE ? pack2_bf16(v.x, v.y) : pack2_f16(v.x, v.y);
         }
-        tmem_st16(tS + 16 * c, w);  // over columns of S that are read
+        again = x0 > kPfMargin;
+      }
+      if (__any_sync(0xffffffffu, again)) {
+        // a new reference for the rows that passed theirs by the margin (or have none yet):
+        // find the maximum, rescale, and form the weights again
+        again = false;
+        sum = f2(0.f, 0.f);
+#pragma unroll 1
+        for (int c = 0; c < 8; ++c) {
+          uint32_t a[16];
+          tmem_ld16(tS + 16 * c, a);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; ++j) mx = fmaxf(mx, 16 * c + j < seen ? __uint_as_float(a[j]) : -INFINITY);
+        }
+        float tm = mx > -INFINITY ? mx * f : -INFINITY;
+        if (p.scap > 0.f) tm = soft_cap(tm, p.scap, p.iscap);
+        if (__any_sync(0xffffffffu, tm > mref + kPfMargin)) {
+          const float mn = tm > mref + kPfMargin ? tm : mref;
+          const float al = mref > -INFINITY ? ex2(mref - mn) : 0.f;  // 1 where the reference stays
+          const float sc = mn > -INFINITY ? al : 1.f;
+          lsum *= sc;
+          mref = mn;
+          if (i > 0) {  // P V(i - 1) is complete: the scores of this tile were issued after it
+#pragma unroll 1
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t o[16];
+              tmem_ld16(tO + 16 * c, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * sc);
+              tmem_st16(tO + 16 * c, o);
+            }
+          }
+        }
+        const float ref = mref > -INFINITY ? mref : 0.f;
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t a[16];
+          tmem_ld16(tS + 16 * c, a);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 16; j += 2) {
+            float2 v = f2(__uint_as_float(a[j]) * f, __uint_as_float(a[j + 1]) * f);
+            if (p.scap > 0.f) v = f2(soft_cap(v.x, p.scap, p.iscap), soft_cap(v.y, p.scap, p.iscap));
+            v = f2(16 * c + j < seen ? ex2(v.x - ref) : 0.f, 16 * c + j + 1 < seen ? ex2(v.y - ref) : 0.f);
+            sum = add2(sum, v);
+            w[8 * c + j / 2] = DENSE ? pack2_bf16(v.x, v.y) : pack2_f16(v.x, v.y);
+          }
+        }
       }
       lsum += sum.x + sum.y;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t u[16];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) u[j] = w[16 * c + j];
+        tmem_st16(tS + 16 * c, u);
+      }
       tmem_st_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.p_full[t]);
     }
-    mbar_wait(&ms.o_done[t], (n - 1) & 1, abort_f);
+    mbar_wait_idle(&ms.o_done[t], (n - 1) & 1, abort_f);
     tc_fence_after();
     const float un = DENSE ? 1.f : pow2i(-15) * (1.f / ev);
     const int64_t at = blk + (int64_t)t * S * 128;
     float4* dst = reinterpret_cast<float4*>(pp.ws_acc) + at * (D / 4) + (r & 127);
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
       uint32_t o[32];
       tmem_ld32(tO + 32 * c, o);
@@ -592,7 +690,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
   __syncthreads();
   if (warp == kPfSoft + kPfLoad) {
     volatile int drain = 0;  // every MMA has completed, whatever the abort flag says
-    mbar_wait(&ms.fin, 0, &drain);
+    mbar_wait_idle(&ms.fin, 0, &drain);
     tc_fence_after();
     tmem_dealloc(tb0, 512);
   }
@@ -602,9 +700,12 @@ template <int D>
 __global__ void __launch_bounds__(kPfThreads, 1) prefill_umma_kernel(const __grid_constant__ PrefillParams pp) {
   extern __shared__ __align__(1024) unsigned char smraw[];
   unsigned char* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
-  const int S = pp.Sc + pp.St, split = blockIdx.x % S, tile = blockIdx.x / S;
-  if (split < pp.Sc) prefill_umma_body<D, false>(pp, sm, tile, split);
-  else prefill_umma_body<D, true>(pp, sm, tile, split - pp.Sc);
+  // records first, the ring's shorter runs behind them
+  const int64_t U = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv * pp.tiles;
+  const int split = (int)(blockIdx.x / U), tile = (int)(blockIdx.x % U % pp.tiles);
+  const int64_t unit = blockIdx.x % U / pp.tiles;
+  if (split < pp.Sc) prefill_umma_body<D, false>(pp, sm, unit, tile, split);
+  else prefill_umma_body<D, true>(pp, sm, unit, tile, split - pp.Sc);
 }
 
 template <int D>
@@ -616,8 +717,8 @@ cudaError_t prefill_umma_launch(const PrefillParams& pp, cudaStream_t s) {
   cudaFuncAttributes fa;
   if ((e = cudaFuncGetAttributes(&fa, prefill_umma_kernel<D>)) != cudaSuccess) return e;
   if (fa.numRegs != kPfLaunchRegs) return cudaErrorInvalidConfiguration;
-  const dim3 grid(pp.tiles * (pp.Sc + pp.St), pp.q.B * pp.q.Hkv, pp.q.L);
-  prefill_umma_kernel<D><<<grid, kPfThreads, PfCfg<D>::SMEM, s>>>(pp);
+  const int64_t grid = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv * pp.tiles * (pp.Sc + pp.St);
+  prefill_umma_kernel<D><<<(unsigned)grid, kPfThreads, PfCfg<D>::SMEM, s>>>(pp);
   return cudaGetLastError();
 }
 
