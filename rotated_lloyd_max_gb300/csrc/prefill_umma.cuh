@@ -16,9 +16,9 @@
 // reference that follows the maximum only when it is passed by 2^8, so O is
 // rescaled rarely, by the warps that own the rows.
 //
-// Warps: 0-3 and 4-7 softmax of tile 0 and 1 (a thread per row), 8-15 decode
+// Warps: 0-3 and 4-7 softmax of tile 0 and 1 (a thread per row), 8-23 decode
 // records (or copy ring tokens) into two stages each of key and value tiles,
-// 16 issues MMAs.  A tile's MMAs run P V(i) then Q K(i+1), and the two tiles
+// 24 issues MMAs.  A tile's MMAs run P V(i) then Q K(i+1), and the two tiles
 // alternate, so that one tile's softmax runs under the other's MMAs.  The
 // decoding warps give registers to the softmax warps.  Every wait is bounded; a
 // CTA whose wait expired leaves NaN statistics, so that its rows come out NaN.
@@ -35,15 +35,17 @@
 
 namespace tq {
 
-constexpr int kPfSoft = 8, kPfLoad = 8;  // softmax and loading warps
+constexpr int kPfSoft = 8, kPfLoad = 16;  // softmax and loading warps
 constexpr int kPfThreads = 32 * (kPfSoft + kPfLoad + 1);
 constexpr int kPfRows = 256;
+constexpr int kPfTok = 128 / kPfLoad;  // tokens of a tile that a loading warp decodes
 constexpr float kPfMargin = 13.f;  // log2 of the largest weight kept against an old reference
 
-// Registers per thread: 96 at launch (17 warps: five on one of the SM's four
-// partitions), then 120 for the softmax and 72 for the decoding warps, no more
-// in sum than at launch.
-constexpr int kPfLaunchRegs = 96, kPfSoftRegs = 120, kPfLoadRegs = 72;
+// Registers per thread: 72 at launch (25 warps: seven on one of the SM's four
+// partitions), then 104 for the softmax and 56 for the decoding warps, no more
+// in sum than at launch.  Sixteen decoding warps rather than eight: what they do
+// is short dependent chains (1024 tokens over 32768 cached: 652 us against 817).
+constexpr int kPfLaunchRegs = 72, kPfSoftRegs = 104, kPfLoadRegs = 56;
 static_assert(kPfSoft * kPfSoftRegs + kPfLoad * kPfLoadRegs + kPfLaunchRegs <= (kPfSoft + kPfLoad + 1) * kPfLaunchRegs,
               "the registers that some warps take, others gave");
 
@@ -137,16 +139,16 @@ __device__ __forceinline__ uint4 decode_codes(uint32_t x, const Planes& pl) {
                     __byte_perm(a1, b1, 0x7362));
 }
 
-// One record's keys or values into a stage: warp w of the eight takes tokens
-// 16 w .. 16 w + 15, a lane eight codes (16 bytes of f16) at a time.  The
+// One record's keys or values into a stage: warp w takes its kPfTok tokens
+// from kPfTok w on, a lane eight codes (16 bytes of f16) at a time.  The
 // packed words of the next tile are loaded before this one's are decoded.
 template <int D>
 struct Packed {
-  static constexpr int CH = D / 8, PER = 16 * CH / 32;  // chunks per row, per lane
+  static constexpr int CH = D / 8, PER = kPfTok * CH / 32;  // chunks per row, per lane
   uint32_t x[PER];
   float n;
 };
-// rec points at the record's rows of this lane: token 16 w + lane / CH, codes 8 (lane % CH) ..
+// rec points at the record's rows of this lane: token kPfTok w + lane / CH, codes 8 (lane % CH) ..
 template <int D, int B>
 __device__ __forceinline__ void load_packed(const uint8_t* rec, Packed<D>& k) {
   using P = Packed<D>;
@@ -171,7 +173,7 @@ __device__ __forceinline__ void store_decoded(const Packed<D>& k, float n, const
                                               unsigned char* st, int w, int lane) {
   using P = Packed<D>;
   const uint32_t n2 = pack2_f16(n, n);
-  st += w * 2048;
+  st += w * kPfTok * 128;
   const uint32_t lo = 4 * lane;
 #pragma unroll
   for (int i = 0; i < P::PER; ++i) {
@@ -206,8 +208,8 @@ __device__ __forceinline__ RecSource rec_source(const CodecDev& c, const uint8_t
   r.layer = r.next = layer;
   r.bits = c.bits;
   r.bytes = c.rec_bytes;
-  r.rows = (16 * w + lane / CH) * (D * c.bits / 8) + lane % CH * c.bits;
-  r.norm = c.off_norm + 4 * (16 * w + (lane & 15));
+  r.rows = (kPfTok * w + lane / CH) * (D * c.bits / 8) + lane % CH * c.bits;
+  r.norm = c.off_norm + 4 * (kPfTok * w + lane % kPfTok);
   return r;
 }
 template <int D>
@@ -236,28 +238,28 @@ __device__ __forceinline__ void decode_tile(const CodecDev& c, const uint8_t* re
   }
   if (c.has_outl) {  // the warp's tokens' side lists replace their coordinates
     const uint32_t* cw = reinterpret_cast<const uint32_t*>(rec + c.off_count);
-    const int slot = 16 * w + (lane & 15);
+    const int slot = kPfTok * w + lane % kPfTok;
     int from = 0;
-    for (int q = 0; q < 4 * w; ++q) from = __dp4a(__ldg(cw + q), 0x01010101u, (uint32_t)from);
+    for (int q = 0; q < kPfTok / 4 * w; ++q) from = __dp4a(__ldg(cw + q), 0x01010101u, (uint32_t)from);
     const int mine = __ldg(rec + c.off_count + slot);
     int inc = mine;
 #pragma unroll
-    for (int m = 1; m < 16; m <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, inc, m, 16);
-      if ((lane & 15) >= m) inc += o;
+    for (int m = 1; m < kPfTok; m <<= 1) {
+      const int o = __shfl_up_sync(0xffffffffu, inc, m, kPfTok);
+      if (lane % kPfTok >= m) inc += o;
     }
     from += inc - mine;
     const int cnt = min(mine, max(c.cap - from, 0));
     const uint32_t* ent = reinterpret_cast<const uint32_t*>(rec + c.off_entries);
     __syncwarp();
 #pragma unroll 1
-    for (int row = 0; row < 16; ++row) {
+    for (int row = 0; row < kPfTok; ++row) {
       const int f = __shfl_sync(0xffffffffu, from, row), m = __shfl_sync(0xffffffffu, cnt, row);
       const float s = __shfl_sync(0xffffffffu, n, row) * kTableScale;
       for (int e = lane; e < m; e += 32) {
         const uint32_t en = __ldg(ent + f + e);
         const int j = en & (D - 1);
-        *reinterpret_cast<__half*>(st + (j >> 6) * 16384 + sw128_off(16 * w + row, (j >> 3) & 7) + 2 * (j & 7)) =
+        *reinterpret_cast<__half*>(st + (j >> 6) * 16384 + sw128_off(kPfTok * w + row, (j >> 3) & 7) + 2 * (j & 7)) =
             __float2half_rn(bf16_hi(en) * s);
       }
     }
@@ -490,7 +492,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
     regs_down<kPfLoadRegs>();
     const int w = warp - kPfSoft;
     if constexpr (DENSE) {
-      constexpr int CH = D / 8, PER = 16 * CH / 32;
+      constexpr int CH = D / 8, PER = kPfTok * CH / 32;
       const int cap = p.tail_cap;
       const int start = p.tail_start ? ((p.tail_start[lb] % cap) + cap) % cap : 0;
       const int64_t ring = l * p.tail_ls + (int64_t)(b * p.Hkv + h) * cap * D;
@@ -503,7 +505,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
           unsigned char* st = sm + (kv ? C::V : C::K) + s * C::TILE;
 #pragma unroll
           for (int k = 0; k < PER; ++k) {
-            const int x = lane + 32 * k, row = 16 * w + x / CH, ch = x % CH;
+            const int x = lane + 32 * k, row = kPfTok * w + x / CH, ch = x % CH;
             const int tok = min(k0 + i * kChunk + row, cl.len - 1);
             cp_async16(st + (ch >> 3) * 16384 + sw128_off(row, ch & 7),
                        src + (int64_t)((start + (int64_t)tok) % cap) * D + 8 * ch);
