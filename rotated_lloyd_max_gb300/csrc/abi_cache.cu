@@ -7,6 +7,7 @@
 #include <cstdint>
 #include <cstring>
 
+#include "attn_mass_few.cuh"
 #include "prefill.cuh"
 
 using namespace tq;
@@ -15,6 +16,7 @@ namespace tq {
 
 #define TQ_DECL_DIM(d)                                                        \
   cudaError_t launch_attn_mass_d##d(const MassParams& mp, int NT, cudaStream_t s); \
+  cudaError_t launch_attn_mass_few_d##d(const MassParams& mp, cudaStream_t s); \
   cudaError_t launch_prefill_d##d(const PrefillParams& pp, cudaStream_t s);   \
   int prefill_rows_d##d();
 TQ_DECL_DIM(64)
@@ -23,6 +25,7 @@ TQ_DECL_DIM(256)
 TQ_DECL_DIM(512)
 #undef TQ_DECL_DIM
 cudaError_t launch_prefill_merge(const PrefillParams& pp, cudaStream_t s);
+cudaError_t launch_attn_mass_add(const MassParams& mp, cudaStream_t s);
 
 }  // namespace tq
 
@@ -289,45 +292,84 @@ tq_status prefill_plan(const tq_query_args* a, const tq_codec* kcod, const tq_co
 
 struct MassPlan {
   MassParams mp;
-  int NT;
-  size_t frag, fragd, qsc, qrot, bytes;
+  bool few;  // at most eight query rows: the logits are kept
+  int NT;    // else rows per block / 8
+  size_t ml, frag, fragd, qsc, qrot, logits, bytes;
 };
 
 tq_status mass_plan(const tq_query_args* a, const tq_codec* kcod, MassPlan* pl) {
+  std::memset(pl, 0, sizeof(*pl));
   MassParams& mp = pl->mp;
-  std::memset(&mp, 0, sizeof(mp));
   const tq_status st = query_params(a, kcod, nullptr, false, &mp.q);
   if (st != TQ_OK) return st;
   const QueryParams& q = mp.q;
   const bool outl = q.krec && q.kc.has_outl;
   mp.rows = q.T * q.G;
-  pl->NT = mp.rows <= 8 ? 1 : outl ? 2 : 8;
-  const int R = 8 * pl->NT;
-  mp.nrb = (int)cdiv(mp.rows, R);
-  const int64_t units = (int64_t)q.L * q.B * q.Hkv;
-  // CTAs of the first pass for about two waves of four per SM; at most 32
-  // records or ring tiles of 128 tokens a split (their sums sit in shared memory)
-  const int64_t want = a->splits > 0 ? a->splits : cdiv(8ll * sm_count(), units * mp.nrb);
-  if (q.max_chunks > 0) {
-    mp.cps = (int)std::min<int64_t>(32, cdiv(q.max_chunks, std::min<int64_t>(want, q.max_chunks)));
-    mp.Sc = (int)cdiv(q.max_chunks, mp.cps);
-  }
-  if (q.max_tail > 0) {
-    const int64_t t = cdiv(q.max_tail, TQ_CHUNK);
-    const int64_t per = std::min<int64_t>(32, cdiv(t, std::min<int64_t>(want, t)));
+  const int64_t units = (int64_t)q.L * q.B * q.Hkv, sms = sm_count();
+  const int bits = q.krec ? q.kc.bits : 1;
+  pl->few = mp.rows <= 8;
+  const int64_t ring = cdiv(q.max_tail, TQ_CHUNK);
+  if (pl->few) {
+    mp.nrb = 1;
+    mp.pitch = mp.rows <= 1 ? 1 : mp.rows <= 2 ? 2 : mp.rows <= 4 ? 4 : 8;
+    attn_mass_few_layout(mp, q.D, bits, outl);
+    // CTAs per SM by shared memory (four at the widest table); the split count
+    // that minimises waves x records per split, three records' worth of set-up included
+    const int64_t slots = sms * std::max<int64_t>(1, std::min<int64_t>(5, max_dynamic_smem() / (mp.sm_total + 1024)));
+    const int64_t most = std::max<int64_t>(q.max_chunks, ring);
+    int64_t best = INT64_MAX, per = 1;
+    for (int64_t s = 1; s <= std::min<int64_t>(most, 512); ++s) {
+      if (a->splits > 0 && s != std::min<int64_t>(a->splits, std::min<int64_t>(most, 512))) continue;
+      const int64_t c = cdiv(most, s);
+      const int64_t cost = cdiv(units * (cdiv(q.max_chunks, c) + cdiv(ring, c)), slots) * (c + 3);
+      if (cost < best) {
+        best = cost;
+        per = c;
+      }
+    }
+    mp.cps = (int)per;
+    mp.Sc = (int)cdiv(q.max_chunks, per);
     mp.tps = (int)(TQ_CHUNK * per);
-    mp.St = (int)cdiv(q.max_tail, mp.tps);
+    mp.St = (int)cdiv(ring, per);
+  } else {
+    pl->NT = outl ? 2 : mp.rows <= 32 ? 4 : 8;
+    mp.nrb = (int)cdiv(mp.rows, 8 * pl->NT);
+    // CTAs of the first pass for about two waves of four per SM; at most 32
+    // records or ring tiles of 128 tokens a split (their sums sit in shared memory)
+    const int64_t want = a->splits > 0 ? a->splits : cdiv(8 * sms, units * mp.nrb);
+    if (q.max_chunks > 0) {
+      mp.cps = (int)std::min<int64_t>(32, cdiv(q.max_chunks, std::min<int64_t>(want, q.max_chunks)));
+      mp.Sc = (int)cdiv(q.max_chunks, mp.cps);
+    }
+    if (q.max_tail > 0) {
+      const int64_t per = std::min<int64_t>(32, cdiv(ring, std::min<int64_t>(want, ring)));
+      mp.tps = (int)(TQ_CHUNK * per);
+      mp.St = (int)cdiv(q.max_tail, mp.tps);
+    }
+    attn_mass_layout(mp, q.D, bits, pl->NT, outl);
   }
   const int S = mp.Sc + mp.St;
   if ((int64_t)S * mp.nrb > 0x7FFFFFFFll) return TQ_ERR_UNSUPPORTED;
-  attn_mass_layout(mp, q.D, q.krec ? q.kc.bits : 1, pl->NT, outl);
   if (mp.sm_total > max_dynamic_smem()) return TQ_ERR_UNSUPPORTED;
-  const size_t blocks = (size_t)units * mp.nrb, frags = blocks * (q.D / 16) * pl->NT * 32;
-  pl->frag = pad256(blocks * R * S * 8);
-  pl->fragd = pl->frag + pad256(frags * 16);
-  pl->qsc = pl->fragd + pad256(frags * 8);
-  pl->qrot = pl->qsc + pad256(blocks * R * 4);
-  pl->bytes = pl->qrot + (outl ? pad256(blocks * R * q.D * 4) : 0) + 256;
+  size_t off = 0;
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += pad256(bytes);
+    return at;
+  };
+  if (pl->few) {
+    pl->ml = take((size_t)units * S * 8 * 8);
+    pl->logits = take((size_t)units * (q.max_chunks * (size_t)TQ_CHUNK + (size_t)mp.St * mp.tps) * mp.pitch * 4);
+  } else {
+    const int R = 8 * pl->NT;
+    const size_t blocks = (size_t)units * mp.nrb, frags = blocks * (q.D / 16) * pl->NT * 32;
+    pl->ml = take(blocks * R * S * 8);
+    pl->frag = take(frags * 16);
+    pl->fragd = take(frags * 8);
+    pl->qsc = take(blocks * R * 4);
+    pl->qrot = take(outl ? blocks * R * q.D * 4 : 0);
+  }
+  pl->bytes = off + 256;
   return TQ_OK;
 }
 
@@ -482,7 +524,8 @@ tq_status tq_attn_mass(const tq_query_args* a, const tq_codec* k_codec, float* m
   if (workspace_bytes < pl.bytes) return TQ_ERR_WORKSPACE;
   if (mp.Sc + mp.St == 0) return TQ_OK;  // no token to weigh
   char* ws = (char*)workspace;
-  mp.ml = (float2*)ws;
+  mp.ml = (float2*)(ws + pl.ml);
+  mp.logits = (float*)(ws + pl.logits);
   mp.frag = (uint4*)(ws + pl.frag);
   mp.fragd = (uint2*)(ws + pl.fragd);
   mp.qsc = (float*)(ws + pl.qsc);
@@ -492,8 +535,18 @@ tq_status tq_attn_mass(const tq_query_args* a, const tq_codec* k_codec, float* m
   mp.mass_cap = mass_cap;
   mp.decay = decay;
   cudaStream_t s = (cudaStream_t)stream;
+  cudaError_t e;
+  if (pl.few) {
+    switch (mp.q.D) {
+      case 64: e = launch_attn_mass_few_d64(mp, s); break;
+      case 128: e = launch_attn_mass_few_d128(mp, s); break;
+      case 256: e = launch_attn_mass_few_d256(mp, s); break;
+      default: e = launch_attn_mass_few_d512(mp, s); break;
+    }
+    if (e != cudaSuccess) return TQ_ERR_CUDA;
+    return launch_attn_mass_add(mp, s) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+  }
   for (mp.pass = 0; mp.pass < 2; ++mp.pass) {
-    cudaError_t e;
     switch (mp.q.D) {
       case 64: e = launch_attn_mass_d64(mp, pl.NT, s); break;
       case 128: e = launch_attn_mass_d128(mp, pl.NT, s); break;

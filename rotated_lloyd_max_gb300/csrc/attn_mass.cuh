@@ -41,6 +41,8 @@ struct MassParams {
   uint2* fragd;       // the same for the ring: bf16 queries as they are
   float* qsc;         // [units][nrb * 8 NT] score scales
   float* qrot;        // [units][nrb][D][8 NT] rotated queries (side lists only)
+  int pitch;          // few rows: logits kept per token (rows padded to a power of two)
+  float* logits;      // [units][records' then the ring's tokens][pitch]
   float* mass;
   int64_t mass_ls;
   int mass_cap;
@@ -83,6 +85,10 @@ struct MassMisc {
   float2 part[4][8 * NT]; // the warps' statistics (pass 0)
 };
 
+__device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
+  const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
 // a logit in log2 units, -inf past the row's limit
 __device__ __forceinline__ float mass_logit(const QueryParams& p, float acc, float f, bool seen) {
   float t = acc * f;
@@ -477,12 +483,12 @@ cudaError_t attn_mass_launch_t(const MassParams& mp, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-// rows per block: 8 for a single decode step's few heads, else 64 (32 with side
-// lists, whose corrections keep the rotated queries in shared memory as f32)
+// row blocks of 32 for up to 32 rows, else of 64; of 16 with side lists, whose
+// corrections keep the rotated queries in shared memory as f32
 template <int D, int KB>
 cudaError_t attn_mass_launch_kb(const MassParams& mp, int NT, cudaStream_t s) {
-  if (mp.q.kc.has_outl) return NT == 1 ? attn_mass_launch_t<D, KB, 1, true>(mp, s) : attn_mass_launch_t<D, KB, 2, true>(mp, s);
-  return NT == 1 ? attn_mass_launch_t<D, KB, 1, false>(mp, s) : attn_mass_launch_t<D, KB, 8, false>(mp, s);
+  if (mp.q.kc.has_outl) return attn_mass_launch_t<D, KB, 2, true>(mp, s);
+  return NT == 4 ? attn_mass_launch_t<D, KB, 4, false>(mp, s) : attn_mass_launch_t<D, KB, 8, false>(mp, s);
 }
 
 template <int D>
