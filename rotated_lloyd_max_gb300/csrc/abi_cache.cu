@@ -25,6 +25,9 @@ TQ_DECL_DIM(256)
 TQ_DECL_DIM(512)
 #undef TQ_DECL_DIM
 cudaError_t launch_prefill_merge(const PrefillParams& pp, cudaStream_t s);
+cudaError_t launch_attn_mass_umma_d64(const MassParams& mp, cudaStream_t s);
+cudaError_t launch_attn_mass_umma_d128(const MassParams& mp, cudaStream_t s);
+constexpr int kMassUmmaPer = 48;  // 128-token tiles of a split of theirs at most
 cudaError_t launch_attn_mass_add(const MassParams& mp, cudaStream_t s);
 
 }  // namespace tq
@@ -293,6 +296,7 @@ tq_status prefill_plan(const tq_query_args* a, const tq_codec* kcod, const tq_co
 struct MassPlan {
   MassParams mp;
   bool few;  // at most eight query rows: the logits are kept
+  bool umma; // many rows at head dims 64 and 128: tcgen05, blocks of 128 rows
   int NT;    // else rows per block / 8
   size_t ml, frag, fragd, qsc, qrot, logits, bytes;
 };
@@ -308,6 +312,8 @@ tq_status mass_plan(const tq_query_args* a, const tq_codec* kcod, MassPlan* pl) 
   const int64_t units = (int64_t)q.L * q.B * q.Hkv, sms = sm_count();
   const int bits = q.krec ? q.kc.bits : 1;
   pl->few = mp.rows <= 8;
+  // 128 rows cost the tensor cores as much as 40 do on mma.sync (four times slower a product)
+  pl->umma = mp.rows > 40 && q.D <= 128;
   const int64_t ring = cdiv(q.max_tail, TQ_CHUNK);
   if (pl->few) {
     mp.nrb = 1;
@@ -326,6 +332,27 @@ tq_status mass_plan(const tq_query_args* a, const tq_codec* kcod, MassPlan* pl) 
         best = cost;
         per = c;
       }
+    }
+    mp.cps = (int)per;
+    mp.Sc = (int)cdiv(q.max_chunks, per);
+    mp.tps = (int)(TQ_CHUNK * per);
+    mp.St = (int)cdiv(ring, per);
+  } else if (pl->umma) {
+    // one CTA per SM: the split count that minimises waves x tiles per split in
+    // both passes (row tiles are CTAs in the first and a loop in the second),
+    // six tiles' worth of set-up per row tile included
+    mp.nrb = (int)cdiv(mp.rows, 128);
+    const int64_t most = std::max<int64_t>(std::max<int64_t>(q.max_chunks, ring), 1);
+    int64_t best = INT64_MAX, per = 1;
+    for (int64_t s = cdiv(most, kMassUmmaPer); s <= most; ++s) {
+      if (a->splits > 0 && s != std::max(cdiv(most, kMassUmmaPer), std::min<int64_t>(a->splits, most))) continue;
+      const int64_t c = cdiv(most, s), ctas = units * (cdiv(q.max_chunks, c) + cdiv(ring, c));
+      const int64_t cost = cdiv(ctas * mp.nrb, sms) * (c + 6) + cdiv(ctas, sms) * mp.nrb * (c + 6);
+      if (cost < best) {
+        best = cost;
+        per = c;
+      }
+      if (s > 512) break;
     }
     mp.cps = (int)per;
     mp.Sc = (int)cdiv(q.max_chunks, per);
@@ -360,6 +387,8 @@ tq_status mass_plan(const tq_query_args* a, const tq_codec* kcod, MassPlan* pl) 
   if (pl->few) {
     pl->ml = take((size_t)units * S * 8 * 8);
     pl->logits = take((size_t)units * (q.max_chunks * (size_t)TQ_CHUNK + (size_t)mp.St * mp.tps) * mp.pitch * 4);
+  } else if (pl->umma) {
+    pl->ml = take((size_t)units * mp.nrb * S * 128 * 8);
   } else {
     const int R = 8 * pl->NT;
     const size_t blocks = (size_t)units * mp.nrb, frags = blocks * (q.D / 16) * pl->NT * 32;
@@ -547,7 +576,9 @@ tq_status tq_attn_mass(const tq_query_args* a, const tq_codec* k_codec, float* m
     return launch_attn_mass_add(mp, s) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
   }
   for (mp.pass = 0; mp.pass < 2; ++mp.pass) {
-    switch (mp.q.D) {
+    switch (pl.umma ? -mp.q.D : mp.q.D) {
+      case -64: e = launch_attn_mass_umma_d64(mp, s); break;
+      case -128: e = launch_attn_mass_umma_d128(mp, s); break;
       case 64: e = launch_attn_mass_d64(mp, pl.NT, s); break;
       case 128: e = launch_attn_mass_d128(mp, pl.NT, s); break;
       case 256: e = launch_attn_mass_d256(mp, pl.NT, s); break;

@@ -224,6 +224,35 @@ __device__ __forceinline__ void load_tile(const RecSource& r, Packed<D>& k) {
   k.n = __ldg(reinterpret_cast<const float*>(r.next + r.norm));
 }
 
+// The side lists of the warp's tokens: put(row, coordinate, value, the token's n)
+// for each entry, after the warp has written the rows; entries past the capacity are not read.
+template <int D, class Put>
+__device__ __forceinline__ void side_list(const CodecDev& c, const uint8_t* rec, int w, int lane, float n, Put&& put) {
+  const uint32_t* cw = reinterpret_cast<const uint32_t*>(rec + c.off_count);
+  int from = 0;
+  for (int q = 0; q < kPfTok / 4 * w; ++q) from = __dp4a(__ldg(cw + q), 0x01010101u, (uint32_t)from);
+  const int mine = __ldg(rec + c.off_count + kPfTok * w + lane % kPfTok);
+  int inc = mine;
+#pragma unroll
+  for (int m = 1; m < kPfTok; m <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, inc, m, kPfTok);
+    if (lane % kPfTok >= m) inc += o;
+  }
+  from += inc - mine;
+  const int cnt = min(mine, max(c.cap - from, 0));
+  const uint32_t* ent = reinterpret_cast<const uint32_t*>(rec + c.off_entries);
+  __syncwarp();
+#pragma unroll 1
+  for (int row = 0; row < kPfTok; ++row) {
+    const int f = __shfl_sync(0xffffffffu, from, row), m = __shfl_sync(0xffffffffu, cnt, row);
+    const float s = __shfl_sync(0xffffffffu, n, row);
+    for (int e = lane; e < m; e += 32) {
+      const uint32_t en = __ldg(ent + f + e);
+      put(row, (int)(en & (D - 1)), bf16_hi(en), s);
+    }
+  }
+}
+
 template <int D>
 __device__ __forceinline__ void decode_tile(const CodecDev& c, const uint8_t* rec, const Packed<D>& k, const Planes& pl,
                                             const unsigned char* lut, float nscale, unsigned char* st, int w, int lane) {
@@ -236,34 +265,11 @@ __device__ __forceinline__ void decode_tile(const CodecDev& c, const uint8_t* re
       if (lut) store_decoded<D, 4, true>(k, n, pl, lut, st, w, lane);
       else store_decoded<D, 4, false>(k, n, pl, lut, st, w, lane);
   }
-  if (c.has_outl) {  // the warp's tokens' side lists replace their coordinates
-    const uint32_t* cw = reinterpret_cast<const uint32_t*>(rec + c.off_count);
-    const int slot = kPfTok * w + lane % kPfTok;
-    int from = 0;
-    for (int q = 0; q < kPfTok / 4 * w; ++q) from = __dp4a(__ldg(cw + q), 0x01010101u, (uint32_t)from);
-    const int mine = __ldg(rec + c.off_count + slot);
-    int inc = mine;
-#pragma unroll
-    for (int m = 1; m < kPfTok; m <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, inc, m, kPfTok);
-      if (lane % kPfTok >= m) inc += o;
-    }
-    from += inc - mine;
-    const int cnt = min(mine, max(c.cap - from, 0));
-    const uint32_t* ent = reinterpret_cast<const uint32_t*>(rec + c.off_entries);
-    __syncwarp();
-#pragma unroll 1
-    for (int row = 0; row < kPfTok; ++row) {
-      const int f = __shfl_sync(0xffffffffu, from, row), m = __shfl_sync(0xffffffffu, cnt, row);
-      const float s = __shfl_sync(0xffffffffu, n, row) * kTableScale;
-      for (int e = lane; e < m; e += 32) {
-        const uint32_t en = __ldg(ent + f + e);
-        const int j = en & (D - 1);
-        *reinterpret_cast<__half*>(st + (j >> 6) * 16384 + sw128_off(kPfTok * w + row, (j >> 3) & 7) + 2 * (j & 7)) =
-            __float2half_rn(bf16_hi(en) * s);
-      }
-    }
-  }
+  if (c.has_outl)
+    side_list<D>(c, rec, w, lane, n, [&](int row, int j, float y, float nr) {
+      *reinterpret_cast<__half*>(st + (j >> 6) * 16384 + sw128_off(kPfTok * w + row, (j >> 3) & 7) + 2 * (j & 7)) =
+          __float2half_rn(y * nr * kTableScale);
+    });
 }
 
 template <int D, bool DENSE>

@@ -81,6 +81,11 @@ CASES = {
     "ring_only": dict(d=128, G=4, T=10, n=0, tail=200),
     "queries_in_the_records": dict(d=128, G=3, T=150, n=3, tail=60),
     "more_queries_than_tokens": dict(d=64, G=2, T=50, n=0, tail=20),
+    "window_softcap": dict(d=128, G=4, T=12, softcap=3.0, n=3),
+    "window_paged_two_bits": dict(d=64, G=3, T=50, kb=2, paged=True, n=6, B=3, L=2),
+    "window_one_bit": dict(d=128, G=8, T=20, kb=1, n=5, tail=10),
+    "twenty_rows": dict(d=128, G=4, T=5, n=4, kb=3),
+    "nobody_asks_a_window": dict(d=64, G=8, T=9, lens=[0, 9]),
     "nobody_asks": dict(d=64, G=2, T=4, lens=[0, 0]),
 }
 
@@ -92,6 +97,31 @@ def test_mass_against_the_formula(tq, orc, name, splits):
     call = {k: kw.pop(k) for k in ("G", "T", "lens", "causal", "softcap") if k in kw}
     c = Cache(tq, orc, T=kw.pop("T_out", 0.0), seed=13, **kw)
     _check(tq, c, splits=splits, **call)
+
+
+@pytest.mark.parametrize("T", [1, 7, 30])
+def test_a_negative_scale(tq, orc, T):
+    """The softmax scale's sign belongs to the logits on every route (few rows, some, many)."""
+    import torch
+    c = Cache(tq, orc, B=1, Hkv=1, d=128, n=3, tail=30, seed=29)
+    q = queries(1, 1, T, 3, 128, 5)
+    mass = torch.zeros((1, 1, 1, 128 * 3 + 30), device="cuda")
+    tq.attn_mass(k_codec=c.kc, mass=mass, q=tl.to_bf16_tensor(q, "cuda"), scale=-1.0, **c.kw(values=False))
+    qf = synth.bf16_bits_to_f32(q).astype(np.float64)
+    want = sum(weights(qf[0, 0, :, i], c.vectors("k", 0, 0, 0), T, 128 * 3 + 30, True, 0.0, -1.0).sum(0) for i in range(3))
+    assert np.abs(mass.cpu().numpy()[0, 0, 0] - want).max() <= 1e-4 * want.max()
+
+
+@pytest.mark.parametrize("T", [1, 7, 30])
+def test_huge_logits(tq, orc, T):
+    """Logits of hundreds: one token takes each row's weight, nothing overflows."""
+    import torch
+    c = Cache(tq, orc, B=1, Hkv=1, d=128, n=4, tail=20, seed=30)
+    q = queries(1, 1, T, 3, 128, 6, gain=100.0)
+    mass = torch.zeros((1, 1, 1, 128 * 4 + 20), device="cuda")
+    tq.attn_mass(k_codec=c.kc, mass=mass, q=tl.to_bf16_tensor(q, "cuda"), scale=1.0, **c.kw(values=False))
+    got = mass.cpu().numpy()[0, 0, 0].astype(np.float64)
+    assert np.isfinite(got).all() and abs(got.sum() / (3 * T) - 1) <= 2.0 ** -12
 
 
 def test_every_query_gives_a_weight_of_one(tq, orc):
