@@ -240,44 +240,27 @@ tq_status prefill_plan(const tq_query_args* a, const tq_codec* kcod, const tq_co
   pp.tiles = (int)cdiv(pp.rows, bm);
   const int64_t units = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv;
   const int64_t sms = sm_count(), U = units * pp.tiles;
-  if (d <= 128) {
-    // One CTA per SM.  The split count that minimises, in 128-token tiles' time:
-    // waves of records' CTAs with six tiles' worth of set-up and epilogue each,
-    // the ring's CTAs in the last wave's idle SMs or after it, and the partials'
-    // traffic (about 0.03 tiles per CTA).
-    const int64_t ring = cdiv(pp.q.max_tail, TQ_CHUNK), most = std::max<int64_t>(pp.q.max_chunks, ring);
-    double best = 1e300;
-    for (int64_t s = 1; s <= std::min<int64_t>(most, 128); ++s) {
-      if (a->splits > 0 && s != std::min<int64_t>(a->splits, std::min<int64_t>(most, 128))) continue;
-      const int64_t per = cdiv(most, s);
-      const int64_t sc = cdiv(pp.q.max_chunks, per), st = cdiv(ring, per);
-      const int64_t waves = cdiv(U * sc, sms);
-      const double one = (double)(sc ? cdiv(pp.q.max_chunks, sc) : 0) + 6, rest = (double)(st ? cdiv(ring, st) : 0) + 6;
-      const double idle = (double)(waves * sms - U * sc) * one, dense = (double)(U * st) * rest;
-      double cost = (double)waves * one + 0.03 * (double)(U * (sc + st));
-      if (dense > 0.9 * idle) cost += std::max(rest, (dense - 0.9 * idle) / (double)sms);
-      if (cost < best) {
-        best = cost;
-        pp.cps = (int)per;
-        pp.Sc = (int)sc;
-        pp.tps = (int)(TQ_CHUNK * per);
-        pp.St = (int)st;
-      }
-    }
-  } else {
-    // enough CTAs for four waves of one per SM; a split keeps at least two
-    // records or 256 ring tokens, and a row at most 64 partials of either kind
-    const int64_t want = a->splits > 0 ? a->splits : cdiv(4 * sms, U);
-    if (pp.q.max_chunks > 0) {
-      const int64_t s = std::min<int64_t>(std::min<int64_t>(want, 64), a->splits > 0 ? pp.q.max_chunks : cdiv(pp.q.max_chunks, 2));
-      pp.cps = (int)cdiv(pp.q.max_chunks, s);
-      pp.Sc = (int)cdiv(pp.q.max_chunks, pp.cps);
-    }
-    if (pp.q.max_tail > 0) {
-      const int64_t t = cdiv(pp.q.max_tail, 64);
-      const int64_t s = std::min<int64_t>(std::min<int64_t>(want, 64), a->splits > 0 ? t : cdiv(t, 4));
-      pp.tps = (int)(64 * cdiv(t, s));
-      pp.St = (int)cdiv(pp.q.max_tail, pp.tps);
+  // One CTA per SM.  The split count that minimises, in 128-token tiles' time:
+  // waves of records' CTAs with six tiles' worth of set-up and epilogue each,
+  // the ring's CTAs in the last wave's idle SMs or after it, and the partials'
+  // traffic (about 0.03 tiles per CTA).
+  const int64_t ring = cdiv(pp.q.max_tail, TQ_CHUNK), most = std::max<int64_t>(pp.q.max_chunks, ring);
+  double best = 1e300;
+  for (int64_t s = 1; s <= std::min<int64_t>(most, 128); ++s) {
+    if (a->splits > 0 && s != std::min<int64_t>(a->splits, std::min<int64_t>(most, 128))) continue;
+    const int64_t per = cdiv(most, s);
+    const int64_t sc = cdiv(pp.q.max_chunks, per), st = cdiv(ring, per);
+    const int64_t waves = cdiv(U * sc, sms);
+    const double one = (double)(sc ? cdiv(pp.q.max_chunks, sc) : 0) + 6, rest = (double)(st ? cdiv(ring, st) : 0) + 6;
+    const double idle = (double)(waves * sms - U * sc) * one, dense = (double)(U * st) * rest;
+    double cost = (double)waves * one + 0.03 * (double)(U * (sc + st));
+    if (dense > 0.9 * idle) cost += std::max(rest, (dense - 0.9 * idle) / (double)sms);
+    if (cost < best) {
+      best = cost;
+      pp.cps = (int)per;
+      pp.Sc = (int)sc;
+      pp.tps = (int)(TQ_CHUNK * per);
+      pp.St = (int)st;
     }
   }
   if (U * (pp.Sc + pp.St) > 0x7FFFFFFFll || units * pp.rows > (1ll << 32)) return TQ_ERR_UNSUPPORTED;

@@ -352,13 +352,13 @@ __device__ __forceinline__ void mass_umma_body(const MassParams& mp, unsigned ch
               *reinterpret_cast<uint16_t*>(d + C::TILE) = 0;
             });
           }
+          fence_async_smem();  // before the next loads, which it would wait for
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&ms.k_full[g & 1]);
           if (i + 1 < n) {
             seek(c0 + i + 1);
             load_tile<D>(ks, xk);
           }
-          fence_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&ms.k_full[g & 1]);
         }
       }
     } else {

@@ -31,8 +31,9 @@ namespace cg = cooperative_groups;
 
 namespace tq {
 
-constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
+constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 2048;
+constexpr int kBatch = 8;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveUnits = 8;   // 16-byte units a thread may hold: 128 rows of 256 bytes at most
 constexpr int kMoveCluster = 8;
@@ -45,20 +46,22 @@ __device__ __forceinline__ uint32_t mass_key(float m) {
 }
 
 struct SelShared {
-  uint32_t hist[2][kSelBins];
+  uint32_t hist[2][kSelBins], total[kSelBins], more[kSelBins];
   uint32_t warp_sum[kSelWarps];
   uint32_t digit, left;
   uint32_t gt[kSelWarps], eq[kSelWarps];
   uint32_t cta_gt, cta_eq;
 };
 
-// CACHED: the CTA's keys stay in shared memory (otherwise each pass reads the weights again)
-template <bool CACHED>
-__global__ void __launch_bounds__(kSelThreads) mass_select_kernel(const __grid_constant__ EvictMassParams p) {
+// CACHED: the CTA's keys stay in shared memory (otherwise each pass reads the
+// weights again).  CLUSTER: several CTAs hold a stream; their histograms meet
+// slice by slice, CTA r summing the r-th slice of the bins over all of them.
+template <bool CACHED, bool CLUSTER>
+__global__ void __launch_bounds__(kSelThreads, 1) mass_select_kernel(const __grid_constant__ EvictMassParams p) {
   __shared__ SelShared sh;
   extern __shared__ uint32_t keys[];
   cg::cluster_group cl = cg::this_cluster();
-  const int C = cl.num_blocks(), rank = cl.block_rank();
+  const int C = CLUSTER ? (int)cl.num_blocks() : 1, rank = CLUSTER ? (int)cl.block_rank() : 0;
   const int64_t stream = blockIdx.x / C;
   const int h = stream % p.Hkv, lb = stream / p.Hkv, l = lb / p.B, b = lb % p.B;
   const int n = min(max(p.n_chunks[lb], 0), min(p.max_chunks, p.rec_limit));
@@ -88,27 +91,52 @@ __global__ void __launch_bounds__(kSelThreads) mass_select_kernel(const __grid_c
   for (int pass = 0; pass < 3; ++pass) {
     const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
     uint32_t* hist = sh.hist[pass & 1];
-    for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
-    __syncthreads();
-    for (int i = tid; i < count; i += kSelThreads) {
-      uint32_t key;
-      if (CACHED && pass == 0) {
-        key = load_key(i);
-        keys[i] = key;
-      } else {
-        key = key_at(i);
+    if (pass == 0) {
+      // the leading digits of weights are few (their exponents): four copies of
+      // the histogram, a quarter of the lanes each, keep the atomics from queueing
+      uint32_t* all = sh.hist[0];  // hist[0], hist[1], total, more lie one behind another
+      for (int i = tid; i < 4 * kSelBins; i += kSelThreads) all[i] = 0;
+      __syncthreads();
+      for (int i0 = tid; i0 < count; i0 += kBatch * kSelThreads) {  // a batch's loads in flight together
+        uint32_t key[kBatch];
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          if (i0 + k * kSelThreads < count) key[k] = load_key(i0 + k * kSelThreads);
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k)
+          if (i0 + k * kSelThreads < count) {
+            if (CACHED) keys[i0 + k * kSelThreads] = key[k];
+            atomicAdd(&all[(lane & 3) * kSelBins + (key[k] >> 21)], 1u);
+          }
       }
-      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1u);
+      __syncthreads();
+      for (int i = tid; i < kSelBins; i += kSelThreads)
+        all[i] += (all[kSelBins + i] + all[2 * kSelBins + i]) + all[3 * kSelBins + i];
+    } else {
+      for (int i = tid; i < kSelBins; i += kSelThreads) hist[i] = 0;
+      __syncthreads();
+#pragma unroll 8
+      for (int i = tid; i < count; i += kSelThreads) {
+        const uint32_t key = key_at(i);
+        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & (bins - 1)], 1u);
+      }
     }
-    cl.sync();
-    // thread t sums bins 4t .. 4t + 3 of every CTA's histogram; the digit is
-    // the largest whose count of keys at or above it reaches `want`
-    uint32_t c[4] = {0, 0, 0, 0};
-    for (int r = 0; r < C; ++r) {
-      const uint4 v = *reinterpret_cast<const uint4*>(cl.map_shared_rank(hist, r) + 4 * tid);
-      c[0] += v.x; c[1] += v.y; c[2] += v.z; c[3] += v.w;
+    if constexpr (CLUSTER) {  // the slice's totals go back to every CTA's second copy
+      cl.sync();
+      const int per = kSelBins / C;
+      for (int i = tid; i < per; i += kSelThreads) {
+        uint32_t sum = 0;
+        for (int r = 0; r < C; ++r) sum += cl.map_shared_rank(hist, r)[rank * per + i];
+        for (int r = 0; r < C; ++r) cl.map_shared_rank(sh.total, r)[rank * per + i] = sum;
+      }
+      cl.sync();
+    } else {
+      __syncthreads();
     }
-    const uint32_t mine = c[0] + c[1] + c[2] + c[3];
+    // thread t holds bins 2t, 2t + 1; the digit is the largest whose count of
+    // keys at or above it reaches `want`
+    const uint32_t* tot = CLUSTER ? sh.total : hist;
+    const uint32_t b0 = tot[2 * tid], b1 = tot[2 * tid + 1], mine = b0 + b1;
     uint32_t up = mine;  // inclusive sum over this lane and those above it
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
@@ -118,12 +146,14 @@ __global__ void __launch_bounds__(kSelThreads) mass_select_kernel(const __grid_c
     if (lane == 0) sh.warp_sum[warp] = up;
     __syncthreads();
     uint32_t above = up - mine;
-    for (int w = warp + 1; w < kSelWarps; ++w) above += sh.warp_sum[w];
+    {
+      const uint32_t others = lane > warp ? sh.warp_sum[lane] : 0u;  // 32 warps
+      above += __reduce_add_sync(0xffffffffu, others);
+    }
     if (above < want && above + mine >= want) {
-      int k = 3;
-      while (above + c[k] < want) above += c[k--];
-      sh.digit = 4 * tid + k;
-      sh.left = want - above;
+      const bool upper = above + b1 >= want;
+      sh.digit = 2 * tid + (upper ? 1 : 0);
+      sh.left = want - above - (upper ? 0 : b1);
     }
     __syncthreads();
     prefix |= sh.digit << shift;
@@ -134,6 +164,7 @@ __global__ void __launch_bounds__(kSelThreads) mass_select_kernel(const __grid_c
   const int run = (count + kSelThreads - 1) / kSelThreads * 32;  // tokens of a warp, contiguous
   const int w0 = min(warp * run, count), w1 = min(w0 + run, count);
   uint32_t gt = 0, eq = 0;
+#pragma unroll 8
   for (int i = w0 + lane; i < w1; i += 32) {
     const uint32_t key = key_at(i);
     gt += key > prefix;
@@ -146,25 +177,21 @@ __global__ void __launch_bounds__(kSelThreads) mass_select_kernel(const __grid_c
     sh.eq[warp] = eq;
   }
   __syncthreads();
-  if (tid == 0) {
-    uint32_t a = 0, e = 0;
-    for (int w = 0; w < kSelWarps; ++w) {
-      a += sh.gt[w];
-      e += sh.eq[w];
+  // before this warp's run: the warps in front, and the CTAs in front
+  uint32_t gt0 = __reduce_add_sync(0xffffffffu, lane < warp ? sh.gt[lane] : 0u);
+  uint32_t eq0 = __reduce_add_sync(0xffffffffu, lane < warp ? sh.eq[lane] : 0u);
+  if constexpr (CLUSTER) {
+    if (tid == kSelThreads - 1) {
+      sh.cta_gt = gt0 + sh.gt[warp];
+      sh.cta_eq = eq0 + sh.eq[warp];
     }
-    sh.cta_gt = a;
-    sh.cta_eq = e;
+    cl.sync();
+    for (int r = 0; r < rank; ++r) {
+      gt0 += *cl.map_shared_rank(&sh.cta_gt, r);
+      eq0 += *cl.map_shared_rank(&sh.cta_eq, r);
+    }
   }
-  cl.sync();
-  uint32_t gt0 = 0, eq0 = 0;  // before this warp's run
-  for (int r = 0; r < rank; ++r) {
-    gt0 += *cl.map_shared_rank(&sh.cta_gt, r);
-    eq0 += *cl.map_shared_rank(&sh.cta_eq, r);
-  }
-  for (int w = 0; w < warp; ++w) {
-    gt0 += sh.gt[w];
-    eq0 += sh.eq[w];
-  }
+#pragma unroll 4
   for (int i0 = w0; i0 < w1; i0 += 32) {
     const int i = i0 + lane;
     const uint32_t key = i < w1 ? key_at(i) : 0u;
@@ -176,7 +203,7 @@ __global__ void __launch_bounds__(kSelThreads) mass_select_kernel(const __grid_c
     gt0 += __popc(bg);
     eq0 += __popc(be);
   }
-  cl.sync();  // no CTA leaves while another reads its counters
+  if constexpr (CLUSTER) cl.sync();  // no CTA leaves while another reads its counters
 }
 
 // ----------------------------------------------------------------- compaction
@@ -329,6 +356,68 @@ __global__ void __launch_bounds__(kMoveThreads) mass_compact_kernel(const __grid
   }
 }
 
+// Out of place without side lists nothing ties the tokens of a record together:
+// a warp takes 32 of them, a lane each for its source and scale, and the lanes
+// together for the code rows, with every load of a task in flight at once and no
+// barrier.
+template <int UNIT>
+__global__ void __launch_bounds__(kMoveThreads) mass_move_kernel(const __grid_constant__ EvictMassParams p) {
+  using V = typename std::conditional<UNIT == 16, uint4, uint2>::type;
+  const int64_t stream = blockIdx.y;
+  const int h = stream % p.Hkv, lb = stream / p.Hkv, l = lb / p.B, b = lb % p.B;
+  const int n = p.counts[lb], left = min(n, p.keep);
+  const int32_t* list = p.list + stream * (int64_t)p.slots * kChunk;
+  const int tid = threadIdx.x, lane = tid & 31;
+  if (h == 0 && blockIdx.x == 0 && tid == 0) p.n_chunks_dst[lb] = left;
+  const int i0 = (blockIdx.x * kMoveThreads + tid) & ~31;  // the warp's first token
+  const int live = left * kChunk;
+  // weights: the remaining tokens' and the ring's behind them
+  const int len = p.tail_len ? min(max(p.tail_len[lb], 0), p.max_tail) : 0;
+  const float* m = p.mass + l * p.mass_ls + ((int64_t)b * p.Hkv + h) * p.mass_cap;
+  float* d = p.mass_dst + l * p.mass_dst_ls + ((int64_t)b * p.Hkv + h) * p.mass_dst_cap;
+  const int i = i0 + lane;
+  if (i0 >= live) {
+    if (i < live + len) d[i] = m[n * kChunk + (i - live)];
+    return;
+  }
+  const int src = list[i];
+  const float w = m[src];
+  const int sc = src / kChunk, slot = src % kChunk, r = i0 / kChunk;
+  auto move = [&](const CodecDev& c, const uint8_t* base, uint8_t* dbase) {
+    const uint8_t* rec = base + rec_offset(p.table, p.table_stride, p.rec_cap, p.Hkv, b, h, sc, c.rec_bytes);
+    uint8_t* dst = dbase + rec_offset(p.dst_table, p.dst_table_stride, p.dst_cap, p.Hkv, b, h, r, c.rec_bytes);
+    const int row = c.off_norm / kChunk, upr = row / UNIT;
+    const int inv = (65536 + upr - 1) / upr;  // u / upr = u inv >> 16 for u < 1024
+    const float scale = *reinterpret_cast<const float*>(rec + c.off_norm + 4 * slot);
+    const uint64_t from = (uint64_t)(rec + slot * row);
+    const int first = (i0 % kChunk) * row;
+    for (int k0 = 0; k0 < upr; k0 += 4) {
+      V v[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int u = lane + 32 * (k0 + k), q = u * inv >> 16;
+        const uint64_t a = __shfl_sync(0xffffffffu, from, q & 31);
+        if (k0 + k < upr) v[k] = *reinterpret_cast<const V*>(a + (u - q * upr) * UNIT);
+      }
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        if (k0 + k < upr) *reinterpret_cast<V*>(dst + first + (lane + 32 * (k0 + k)) * UNIT) = v[k];
+    }
+    reinterpret_cast<float*>(dst + c.off_norm)[i % kChunk] = scale;
+  };
+  move(p.kc, p.k_rec + l * p.k_ls, p.k_dst + l * p.kd_ls);
+  if (!p.shared) move(p.vc, p.v_rec + l * p.v_ls, p.v_dst + l * p.vd_ls);
+  d[i] = w;
+}
+
+template <int UNIT>
+static cudaError_t move_launch(const EvictMassParams& p, cudaStream_t s) {
+  const int64_t tokens = (int64_t)p.slots * kChunk + p.max_tail;
+  const dim3 grid((unsigned)((tokens + kMoveThreads - 1) / kMoveThreads), p.L * p.B * p.Hkv);
+  mass_move_kernel<UNIT><<<grid, kMoveThreads, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
 template <int UNIT, bool OUTL, bool INPLACE>
 static cudaError_t compact_launch(const EvictMassParams& p, cudaStream_t s) {
   auto kern = mass_compact_kernel<UNIT, OUTL, INPLACE>;
@@ -355,22 +444,30 @@ static cudaError_t compact_launch(const EvictMassParams& p, cudaStream_t s) {
 
 template <int UNIT, bool OUTL>
 static cudaError_t compact_pick(const EvictMassParams& p, cudaStream_t s) {
-  return p.in_place ? compact_launch<UNIT, OUTL, true>(p, s) : compact_launch<UNIT, OUTL, false>(p, s);
+  if (p.in_place) return compact_launch<UNIT, OUTL, true>(p, s);
+  if constexpr (OUTL) return compact_launch<UNIT, OUTL, false>(p, s);
+  else return move_launch<UNIT>(p, s);
 }
 
 cudaError_t launch_evict_mass(const EvictMassParams& p, cudaStream_t s) {
-  // about 4096 tokens a CTA, at most 8 CTAs (the portable cluster size)
+  // One CTA a stream, or several (a cluster of at most 8) where the streams do
+  // not fill the SMs and a CTA keeps 4096 tokens, or where one CTA's shared
+  // memory does not hold the keys.  (256 streams of 32768 tokens: 8 CTAs each
+  // took 217 us, mostly for meetings of the histograms.)
+  const int64_t streams = (int64_t)p.L * p.B * p.Hkv;
+  auto bytes = [&](int c) { return (p.max_chunks + c - 1) / c * kChunk * 4; };
   int C = 1;
-  while (C < 8 && p.max_chunks > 32 * C) C *= 2;
-  const int smem = (p.max_chunks + C - 1) / C * kChunk * 4;
-  const bool cached = smem <= 160 * 1024;
-  auto kern = cached ? mass_select_kernel<true> : mass_select_kernel<false>;
-  if (cached && smem > 24 * 1024) {
+  while (C < 8 && ((p.max_chunks > 32 * C && streams * C < sm_count()) || bytes(C) > 192 * 1024)) C *= 2;
+  const int smem = bytes(C);
+  const bool cached = smem <= 192 * 1024;
+  auto kern = C > 1 ? (cached ? mass_select_kernel<true, true> : mass_select_kernel<false, true>)
+                    : (cached ? mass_select_kernel<true, false> : mass_select_kernel<false, false>);
+  if (cached) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((int64_t)p.L * p.B * p.Hkv * C));
+  cfg.gridDim = dim3((unsigned)(streams * C));
   cfg.blockDim = dim3(kSelThreads);
   cfg.dynamicSmemBytes = cached ? smem : 0;
   cfg.stream = s;
@@ -379,7 +476,7 @@ cudaError_t launch_evict_mass(const EvictMassParams& p, cudaStream_t s) {
   at[0].val.clusterDim.x = C;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = C > 1 ? 1 : 0;
   cudaError_t e = cudaLaunchKernelEx(&cfg, kern, p);
   if (e != cudaSuccess) return e;
   const bool outl = p.kc.has_outl || p.vc.has_outl;

@@ -548,22 +548,22 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
         const int s = i & 1, ph = ((i >> 1) & 1) ^ 1;
         mbar_wait_idle(&ms.k_empty[s], ph, abort_f);
         decode_tile<D>(p.kc, ks.next, xk, kpl, klut, ek, sm + C::K + s * C::TILE, w, lane);
+        fence_async_smem();  // before the next loads, which it would wait for
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.k_full[s]);
         if (i + 1 < n) {
           seek(ks, c0 + i + 1);
           load_tile<D>(ks, xk);
         }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ms.k_full[s]);
         mbar_wait_idle(&ms.v_empty[s], ph, abort_f);
         decode_tile<D>(p.vc, vs.next, xv, vpl, vlut, ev, sm + C::V + s * C::TILE, w, lane);
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ms.v_full[s]);
         if (i + 1 < n) {
           seek(vs, c0 + i + 1);
           load_tile<D>(vs, xv);
         }
-        fence_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ms.v_full[s]);
       }
     }
   } else {

@@ -160,6 +160,8 @@ CASES = {
     "side_lists_shared": dict(d=64, kb=3, T=1.5, shared=True, n=6, keep=2),
     "paged": dict(d=128, n=6, keep=4, B=3, L=2, paged=True),
     "no_ring": dict(d=128, n=5, keep=2, tail=0, cap=8),
+    "thirty_two_records": dict(d=64, n=32, keep=16, B=1, sink=4, recent=30),
+    "forty_records": dict(d=64, kb=2, vb=2, n=40, keep=7, B=1, Hkv=3),
     "many_records": dict(d=64, kb=1, vb=1, n=300, keep=170, B=1, Hkv=1, sink=4, recent=64),
 }
 
