@@ -6,9 +6,10 @@
 //   O^T[coord][row] += V^T P    (A: 128 coordinates of the decoded tokens,
 //                                MN-major; B: P [token][row], MN-major)
 // A thread owns a token (its lane) for the softmax and a coordinate for the
-// outputs.  Operands, scales and the reference of the softmax are those of the
-// narrower kernel (prefill_umma.cuh): f16 centroids with the token's scale
-// folded in, bf16 for the ring's tokens.
+// outputs, so that a token's scales are one factor of its thread's logits and one
+// of its weights, and decoding is a table lookup and nothing else.  References
+// of the softmax as in the narrower kernel (prefill_umma.cuh); the ring's
+// tokens are bf16 operands.
 //
 // Tokens are decoded in chunks of 64 coordinates (16 KB) into a ring of eight,
 // sixteen warps in groups of four, a group a chunk.  Where keys and values share
@@ -72,11 +73,10 @@ __device__ __forceinline__ float transpose_reduce32(float (&v)[32], int lane) {
 // 32 w .. 32 w + 31, a lane eight codes of every fourth token.
 struct Chunk {
   uint32_t x[8];
-  float n;
 };
+// at: the lane's first token, codes of chunk c
 template <int D, int B>
-__device__ __forceinline__ void load_chunk(const uint8_t* rec, int c, int w, int lane, Chunk& k) {
-  const uint8_t* at = rec + (32 * w + (lane >> 3)) * (D * B / 8) + (8 * c + (lane & 7)) * B;
+__device__ __forceinline__ void load_chunk(const uint8_t* at, Chunk& k) {
   constexpr int STEP = 4 * (D * B / 8);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -91,37 +91,69 @@ __device__ __forceinline__ void load_chunk(const uint8_t* rec, int c, int w, int
   }
 }
 template <int D>
-__device__ __forceinline__ void load_chunk_b(const CodecDev& cd, const uint8_t* rec, int c, int w, int lane, Chunk& k) {
-  switch (cd.bits) {
-    case 1: load_chunk<D, 1>(rec, c, w, lane, k); break;
-    case 2: load_chunk<D, 2>(rec, c, w, lane, k); break;
-    case 3: load_chunk<D, 3>(rec, c, w, lane, k); break;
-    default: load_chunk<D, 4>(rec, c, w, lane, k); break;
+__device__ __forceinline__ void load_chunk_b(int bits, const uint8_t* at, Chunk& k) {
+  switch (bits) {
+    case 1: load_chunk<D, 1>(at, k); break;
+    case 2: load_chunk<D, 2>(at, k); break;
+    case 3: load_chunk<D, 3>(at, k); break;
+    default: load_chunk<D, 4>(at, k); break;
   }
-  k.n = __ldg(reinterpret_cast<const float*>(rec + cd.off_norm) + 32 * w + lane);
 }
-// LUT: 4-bit pairs through a table of 16 copies (entry e at 64 e + 4 (lane % 16))
+// four 4-bit codes (16 bits) -> f16 pairs through the byte planes
+__device__ __forceinline__ void half_planes(uint32_t sel, const Planes& pl, uint32_t& x, uint32_t& y) {
+  const uint32_t s7 = sel & 0x7777u, pick = 0x3210u + ((sel >> 3) & 0x1111u) * 4u;
+  const uint32_t a = __byte_perm(__byte_perm(pl.lo[0], pl.lo[1], s7), __byte_perm(pl.lo[2], pl.lo[3], s7), pick);
+  const uint32_t b = __byte_perm(__byte_perm(pl.hi[0], pl.hi[1], s7), __byte_perm(pl.hi[2], pl.hi[3], s7), pick);
+  x = __byte_perm(a, b, 0x5140);
+  y = __byte_perm(a, b, 0x7362);
+}
+// LUT: half of the 4-bit codes through a table of 16 copies (a pair's entry e at
+// 64 e + 4 (lane % 16)), half through the planes: the lookups alone queue for
+// shared memory (two lanes meet in a bank), the planes alone for the ALUs.
 template <int B, bool LUT>
-__device__ __forceinline__ void store_chunk(const Chunk& k, float n, const Planes& pl, const unsigned char* lut,
+__device__ __forceinline__ void store_chunk(const Chunk& k, const Planes& pl, const unsigned char* lut,
                                             unsigned char* st, int w, int lane) {
-  const uint32_t n2 = pack2_f16(n, n), lo = 4 * (lane & 15);
+  const uint32_t lo = 4 * (lane & 15);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int row = 4 * i + (lane >> 3);
-    const uint32_t sw = __shfl_sync(0xffffffffu, n2, row);
-    const __half2 s = *reinterpret_cast<const __half2*>(&sw);
     uint4 v;
     if constexpr (LUT) {
       const uint32_t x = k.x[i];
       v.x = *reinterpret_cast<const uint32_t*>(lut + (((x << 6) & 0x3FC0u) | lo));
       v.y = *reinterpret_cast<const uint32_t*>(lut + (((x >> 2) & 0x3FC0u) | lo));
-      v.z = *reinterpret_cast<const uint32_t*>(lut + (((x >> 10) & 0x3FC0u) | lo));
-      v.w = *reinterpret_cast<const uint32_t*>(lut + (((x >> 18) & 0x3FC0u) | lo));
+      half_planes(x >> 16, pl, v.z, v.w);
     } else {
       v = decode_codes<B>(k.x[i], pl);
     }
-    v = make_uint4(hmul2(v.x, s), hmul2(v.y, s), hmul2(v.z, s), hmul2(v.w, s));
     *reinterpret_cast<uint4*>(st + sw128_off(32 * w + row, lane & 7)) = v;
+  }
+}
+
+__device__ __forceinline__ void store_chunk_b(int bits, const Chunk& k, const Planes& pl, const unsigned char* lut,
+                                              unsigned char* st, int w, int lane) {
+  switch (bits) {
+    case 1: store_chunk<1, false>(k, pl, lut, st, w, lane); break;
+    case 2: store_chunk<2, false>(k, pl, lut, st, w, lane); break;
+    case 3: store_chunk<3, false>(k, pl, lut, st, w, lane); break;
+    default:
+      if (lut) store_chunk<4, true>(k, pl, lut, st, w, lane);
+      else store_chunk<4, false>(k, pl, lut, st, w, lane);
+  }
+}
+// side list entries of chunk c's coordinates, a lane a token
+template <int D>
+__device__ __forceinline__ void patch_chunk(const CodecDev& cd, const uint8_t* rec, int c, unsigned char* st, int w,
+                                            int lane) {
+  const int e = slot_entries(rec + cd.off_count, w, lane), from = e >> 8, cnt = min(e & 255, max(cd.cap - from, 0));
+  const uint32_t* ent = reinterpret_cast<const uint32_t*>(rec + cd.off_entries) + from;
+  __syncwarp();
+  for (int i = 0; i < cnt; ++i) {
+    const uint32_t en = __ldg(ent + i);
+    const int j = en & (D - 1);
+    if ((j >> 6) == c)
+      *reinterpret_cast<__half*>(st + sw128_off(32 * w + lane, (j >> 3) & 7) + 2 * (j & 7)) =
+          __float2half_rn(bf16_hi(en) * kTableScale);
   }
 }
 
@@ -176,20 +208,13 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
     vtable = p.vc.bits == 4;
     if (p.kc.bits == 4)
       for (int k = 8; k < 16; ++k) vtable = vtable && p.kc.centroids[k] == p.vc.centroids[k];
-    float mk = 0.f, mv = 0.f;  // the run's largest scales
+    float mv = 0.f;  // the run's largest value scale
     for (int i = tid; i < n * (kChunk / 4); i += kPwThreads) {
-      const int c = c0 + i / (kChunk / 4), o = i % (kChunk / 4);
-      const float4 x = __ldg(reinterpret_cast<const float4*>(rec_at(true, c) + p.kc.off_norm) + o);
-      const float4 y = __ldg(reinterpret_cast<const float4*>(rec_at(false, c) + p.vc.off_norm) + o);
-      mk = fmaxf(mk, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
+      const float4 y = __ldg(reinterpret_cast<const float4*>(rec_at(false, c0 + i / (kChunk / 4)) + p.vc.off_norm) + i % (kChunk / 4));
       mv = fmaxf(mv, fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w))));
     }
-    mk = warp_max(mk);
     mv = warp_max(mv);
-    if (lane == 0) {
-      ms.red[0][warp] = mk;
-      ms.red[1][warp] = mv;
-    }
+    if (lane == 0) ms.red[0][warp] = mv;
     const CodecDev& c4 = p.kc.bits == 4 ? p.kc : p.vc;
     if (c4.bits == 4)
       for (int i = tid; i < 256 * 16; i += kPwThreads)
@@ -197,11 +222,8 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
             pack2_f16(c4.centroids[(i >> 4) & 15] * kTableScale, c4.centroids[i >> 8] * kTableScale);
     __syncthreads();
   }
-  float ek = 1.f, ev = 1.f;
-  if constexpr (!DENSE) {
-    ek = pow2i(-1 - exp_of(warp_max(ms.red[0][lane < 21 ? lane : 0])));
-    ev = pow2i(-1 - exp_of(warp_max(ms.red[1][lane < 21 ? lane : 0])));
-  }
+  float ev = 1.f;  // 2^-(E+1) of the values' scales: weights times scales stay in f16's range
+  if constexpr (!DENSE) ev = pow2i(-1 - exp_of(warp_max(ms.red[0][lane < 21 ? lane : 0])));
   {  // query rows, a warp each; lane holds E coordinates
     const float sgn = p.sscale < 0.f ? -1.f : 1.f;
     for (int r = warp; r < kPwRows; r += kPwThreads / 32) {
@@ -245,7 +267,7 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
         mx = warp_max(mx);
         const int s = mx > 0.f ? 13 - exp_of(mx) : 0;
         const float sc = pow2i(s);
-        f = f * pow2i(-15 - s) * (1.f / ek);
+        f *= pow2i(-15 - s);
 #pragma unroll
         for (int e = 0; e < E; e += 2) w[e / 2] = pack2_f16(x[e] * sc, x[e + 1] * sc);
       }
@@ -279,41 +301,38 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
       const uint64_t dQ = sdesc_sw128(smem_u32(sm + C::Q), 16, 1024);
       const uint64_t dK = sdesc_sw128(smem_u32(sm + C::RING), 16, 1024);
       const uint64_t dP = sdesc_sw128(smem_u32(sm + C::P), 1024, 1024);
-      uint32_t g = 0;  // chunks taken from the ring
+      const uint64_t dV = sdesc_sw128(smem_u32(sm + C::RING), 16384, 1024);
+      // slots and parities of a record's chunks: one record in turn takes NCH slots
+      // where keys are the values, else 2 NCH (all of them, twice at head dim 512)
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
-#pragma unroll 1
+        const uint32_t q0 = i * perrec, s0 = q0 % kPwSlots, p0 = (q0 / kPwSlots) & 1;
+        const uint32_t q1 = one ? q0 : q0 + NCH, s1 = q1 % kPwSlots, p1 = (q1 / kPwSlots) & 1;
+        const uint64_t a0 = dK + s0 * 1024, v0 = dV + s1 * 1024;
+#pragma unroll
         for (int c = 0; c < NCH; ++c) {
-          const uint32_t q = one ? (uint32_t)(i * NCH + c) : g, s = q % kPwSlots;
-          mbar_wait_idle(&ms.full[s], (q / kPwSlots) & 1, abort_f);
+          mbar_wait_idle(&ms.full[s0 + c], p0, abort_f);
           tc_fence_after();
 #pragma unroll
-          for (int ks = 0; ks < 4; ++ks)
-            umma_f16(tS, dK + s * 1024 + 2 * ks, dQ + c * 512 + 2 * ks, IS, (c | ks) != 0);
-          if (!one) {
-            umma_commit(&ms.empty[s]);
-            ++g;
-          }
+          for (int ks = 0; ks < 4; ++ks) umma_f16(tS, a0 + c * 1024 + 2 * ks, dQ + c * 512 + 2 * ks, IS, (c | ks) != 0);
+          if (!one) umma_commit(&ms.empty[s0 + c]);
         }
         umma_commit(&ms.s_full);
         mbar_wait_idle(&ms.p_full, i & 1, abort_f);
         tc_fence_after();
-#pragma unroll 1
+#pragma unroll
         for (int j = 0; j < NBL; ++j) {
           // a block of 128 coordinates: two chunks, 64 coordinates (M rows) apart in the ring
-          const uint32_t q = one ? (uint32_t)(i * NCH + 2 * j) : g, s = q % kPwSlots;
           if (!one) {
-            mbar_wait_idle(&ms.full[s], (q / kPwSlots) & 1, abort_f);
-            mbar_wait_idle(&ms.full[s + 1], ((q + 1) / kPwSlots) & 1, abort_f);
+            mbar_wait_idle(&ms.full[s1 + 2 * j], p1, abort_f);
+            mbar_wait_idle(&ms.full[s1 + 2 * j + 1], p1, abort_f);
             tc_fence_after();
           }
-          const uint64_t dV = sdesc_sw128(smem_u32(sm + C::RING) + s * 16384, 16384, 1024);
 #pragma unroll
           for (int ks = 0; ks < 8; ++ks)
-            umma_f16(tO + 64 * j, dV + 128 * ks, dP + 128 * ks, IV, i > 0 || ks > 0);
-          umma_commit(&ms.empty[s]);
-          umma_commit(&ms.empty[s + 1]);
-          g += 2;
+            umma_f16(tO + 64 * j, v0 + j * 2048 + 128 * ks, dP + 128 * ks, IV, i > 0 || ks > 0);
+          umma_commit(&ms.empty[s1 + 2 * j]);
+          umma_commit(&ms.empty[s1 + 2 * j + 1]);
         }
         umma_commit(&ms.o_done);
       }
@@ -346,49 +365,58 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
         if (lane == 0) mbar_arrive(&ms.full[s]);
       }
     } else {
+      // a group's chunks of a record: c = grp, grp + 4, .. of the keys, then of the
+      // values where those are apart; the same chunk of the next record is loaded
+      // as soon as one is stored
+      constexpr int PER = NCH / 4;
       const Planes kpl = make_planes(p.kc, kTableScale), vpl = make_planes(p.vc, kTableScale);
       const unsigned char* klut = p.kc.bits == 4 ? sm + C::LUT : nullptr;
       const unsigned char* vlut = vtable ? sm + C::LUT : nullptr;
-      Chunk cur;
-      auto load = [&](int q) {
-        const int x = q % perrec;
-        load_chunk_b<D>(x >= NCH ? p.vc : p.kc, rec_at(x < NCH, c0 + q / perrec), x % NCH, w, lane, cur);
-      };
-      load(grp);
-#pragma unroll 1
-      for (int q = grp; q < total; q += 4) {
-        const int x = q % perrec, c = x % NCH, s = q % kPwSlots;
-        const bool key = x < NCH;
-        const CodecDev& cd = key ? p.kc : p.vc;
-        const unsigned char* lut = key ? klut : vlut;
-        const float nr = cur.n * (key ? ek : ev);
-        mbar_wait_idle(&ms.empty[s], ((q / kPwSlots) & 1) ^ 1, abort_f);
-        unsigned char* st = sm + C::RING + s * 16384;
-        switch (cd.bits) {
-          case 1: store_chunk<1, false>(cur, nr, key ? kpl : vpl, lut, st, w, lane); break;
-          case 2: store_chunk<2, false>(cur, nr, key ? kpl : vpl, lut, st, w, lane); break;
-          case 3: store_chunk<3, false>(cur, nr, key ? kpl : vpl, lut, st, w, lane); break;
-          default:
-            if (lut) store_chunk<4, true>(cur, nr, key ? kpl : vpl, lut, st, w, lane);
-            else store_chunk<4, false>(cur, nr, key ? kpl : vpl, lut, st, w, lane);
-        }
-        if (cd.has_outl) {  // side lists: entries of this chunk's coordinates (in the order of their indices)
-          const uint8_t* rec = rec_at(key, c0 + q / perrec);
-          const int e = slot_entries(rec + cd.off_count, w, lane), from = e >> 8, cnt = min(e & 255, max(cd.cap - from, 0));
-          const uint32_t* ent = reinterpret_cast<const uint32_t*>(rec + cd.off_entries) + from;
-          __syncwarp();
-          for (int k = 0; k < cnt; ++k) {  // lane: token 32 w + lane
-            const uint32_t en = __ldg(ent + k);
-            const int j = en & (D - 1);
-            if ((j >> 6) == c)
-              *reinterpret_cast<__half*>(st + sw128_off(32 * w + lane, (j >> 3) & 7) + 2 * (j & 7)) =
-                  __float2half_rn(bf16_hi(en) * nr * kTableScale);
-          }
-        }
+      const int kbits = p.kc.bits, vbits = p.vc.bits;
+      const int kat = (32 * w + (lane >> 3)) * (D * kbits / 8) + (8 * grp + (lane & 7)) * kbits;
+      const int vat = (32 * w + (lane >> 3)) * (D * vbits / 8) + (8 * grp + (lane & 7)) * vbits;
+      Chunk kx[PER], vx[PER];
+      const uint8_t *krec = rec_at(true, c0), *vrec = rec_at(false, c0);
+#pragma unroll
+      for (int x = 0; x < PER; ++x) {
+        load_chunk_b<D>(kbits, krec + kat + 32 * x * kbits, kx[x]);
+        if (!one) load_chunk_b<D>(vbits, vrec + vat + 32 * x * vbits, vx[x]);
+      }
+      uint32_t q = grp;
+      auto hand_over = [&](uint32_t s) {
         fence_async_smem();  // before the next loads, which it would wait for
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.full[s]);
-        if (q + 4 < total) load(q + 4);
+        q += 4;
+      };
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {
+        const bool more = i + 1 < n;
+        const uint8_t* knext = more ? rec_at(true, c0 + i + 1) : krec;
+#pragma unroll
+        for (int x = 0; x < PER; ++x) {
+          const uint32_t s = q % kPwSlots;
+          mbar_wait_idle(&ms.empty[s], ((q / kPwSlots) & 1) ^ 1, abort_f);
+          unsigned char* st = sm + C::RING + s * 16384;
+          store_chunk_b(kbits, kx[x], kpl, klut, st, w, lane);
+          if (p.kc.has_outl) patch_chunk<D>(p.kc, krec, grp + 4 * x, st, w, lane);
+          hand_over(s);
+          if (more) load_chunk_b<D>(kbits, knext + kat + 32 * x * kbits, kx[x]);
+        }
+        krec = knext;
+        if (one) continue;
+        const uint8_t* vnext = more ? rec_at(false, c0 + i + 1) : vrec;
+#pragma unroll
+        for (int x = 0; x < PER; ++x) {
+          const uint32_t s = q % kPwSlots;
+          mbar_wait_idle(&ms.empty[s], ((q / kPwSlots) & 1) ^ 1, abort_f);
+          unsigned char* st = sm + C::RING + s * 16384;
+          store_chunk_b(vbits, vx[x], vpl, vlut, st, w, lane);
+          if (p.vc.has_outl) patch_chunk<D>(p.vc, vrec, grp + 4 * x, st, w, lane);
+          hand_over(s);
+          if (more) load_chunk_b<D>(vbits, vnext + vat + 32 * x * vbits, vx[x]);
+        }
+        vrec = vnext;
       }
     }
   } else {
@@ -399,8 +427,18 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
 #pragma unroll
     for (int m = 16; m; m >>= 1) low = min(low, __shfl_xor_sync(0xffffffffu, low, m));
     float lacc[2] = {0.f, 0.f};  // sums of rows lane and 32 + lane over this warp's tokens
+    auto scale_at = [&](bool key, int i) {
+      if constexpr (DENSE) return 1.f;
+      return __ldg(reinterpret_cast<const float*>(rec_at(key, c0 + i) + (key ? p.kc.off_norm : p.vc.off_norm)) + tok);
+    };
+    float nk1 = scale_at(true, 0), nv1 = scale_at(false, 0);
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
+      const float nk = nk1, nv = nv1 * ev;  // the token's scales
+      if (i + 1 < n) {
+        nk1 = scale_at(true, i + 1);
+        nv1 = scale_at(false, i + 1);
+      }
       mbar_wait_idle(&ms.s_full, i & 1, abort_f);
       tc_fence_after();
       const int at = i * kChunk + tok;
@@ -413,10 +451,10 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
 #pragma unroll
         for (int j = 0; j < 32; j += 4) {
           const float4 f = *reinterpret_cast<const float4*>(&ms.qf[32 * hh + j]);
-          t[j] = __uint_as_float(a[j]) * f.x;
-          t[j + 1] = __uint_as_float(a[j + 1]) * f.y;
-          t[j + 2] = __uint_as_float(a[j + 2]) * f.z;
-          t[j + 3] = __uint_as_float(a[j + 3]) * f.w;
+          t[j] = __uint_as_float(a[j]) * nk * f.x;
+          t[j + 1] = __uint_as_float(a[j + 1]) * nk * f.y;
+          t[j + 2] = __uint_as_float(a[j + 2]) * nk * f.z;
+          t[j + 3] = __uint_as_float(a[j + 3]) * nk * f.w;
         }
         if (p.scap > 0.f) {
 #pragma unroll
@@ -427,21 +465,49 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
           for (int j = 0; j < 32; ++j) t[j] = at < ms.lim[32 * hh + j] ? t[j] : -INFINITY;
         }
       };
-      bool need = false;
-#pragma unroll 1
-      for (int hh = 0; hh < 2; ++hh) {
-        float t[32];
-        logits(hh, t);
+      // weights against the references as they stand (the unscaled ones, rounded, are
+      // kept for the sums); a logit that passes its reference by the margin (or
+      // finds none yet) sends the record to the slow path.  The outputs of the
+      // record before are in: the scores were issued behind them.
+      uint32_t w[32];
+      auto put = [&](int hh, int j, const float2 (&x)[4]) {  // rows 32 hh + j .. + 7
+        uint32_t u[4];
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 r = *reinterpret_cast<const float4*>(&ms.ref[32 * hh + j]);
-          need |= t[j] > r.x + kPfMargin || t[j + 1] > r.y + kPfMargin || t[j + 2] > r.z + kPfMargin || t[j + 3] > r.w + kPfMargin;
+        for (int k = 0; k < 4; ++k) {
+          w[16 * hh + j / 2 + k] = DENSE ? pack2_bf16(x[k].x, x[k].y) : pack2_f16(x[k].x, x[k].y);
+          const float2 y = mul2(x[k], f2(nv, nv));
+          u[k] = DENSE ? w[16 * hh + j / 2 + k] : pack2_f16(y.x, y.y);
+        }
+        *reinterpret_cast<uint4*>(sm + C::P + sw128_off(tok, 4 * hh + j / 8)) = make_uint4(u[0], u[1], u[2], u[3]);
+      };
+      float over = -INFINITY;
+      const bool plain = !edge && !(p.scap > 0.f);
+      if (plain) {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t a[32];
+          tmem_ld32(tS + lrow + 32 * hh, a);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            float2 x[4];
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+              const float4 f = *reinterpret_cast<const float4*>(&ms.qf[32 * hh + j + 2 * k]);
+              const float4 r = *reinterpret_cast<const float4*>(&ms.ref[32 * hh + j + 2 * k]);
+              const float2 A = mul2(f2(__uint_as_float(a[j + 2 * k]), __uint_as_float(a[j + 2 * k + 1])), f2(nk, nk));
+              const float2 B = mul2(f2(__uint_as_float(a[j + 2 * k + 2]), __uint_as_float(a[j + 2 * k + 3])), f2(nk, nk));
+              x[k] = fma2(A, f2(f.x, f.y), f2(-r.x, -r.y));
+              x[k + 1] = fma2(B, f2(f.z, f.w), f2(-r.z, -r.w));
+              over = max3(max3(over, x[k].x, x[k].y), x[k + 1].x, x[k + 1].y);
+              x[k] = f2(ex2(x[k].x), ex2(x[k].y));
+              x[k + 1] = f2(ex2(x[k + 1].x), ex2(x[k + 1].y));
+            }
+            put(hh, j, x);
+          }
         }
       }
-      if (i > 0) {  // P of the record before is read, its outputs are in
-        mbar_wait_idle(&ms.o_done, (i - 1) & 1, abort_f);
-        tc_fence_after();
-      }
+      const bool need = !plain || over > kPfMargin;
       if (bar_soft_or(need)) {
         // new references for the rows that passed theirs; their outputs and sums rescaled
 #pragma unroll 1
@@ -479,32 +545,39 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
           tmem_st_wait();
         }
         bar_soft();  // the factors are read before the reductions' space is used again
-      }
-#pragma unroll 1
-      for (int hh = 0; hh < 2; ++hh) {
-        float t[32];
-        logits(hh, t);
-        uint32_t w[16];
 #pragma unroll
-        for (int j = 0; j < 32; j += 4) {
-          const float4 r = *reinterpret_cast<const float4*>(&ms.ref[32 * hh + j]);
-          t[j] = ex2(t[j] - (r.x > -INFINITY ? r.x : 0.f));
-          t[j + 1] = ex2(t[j + 1] - (r.y > -INFINITY ? r.y : 0.f));
-          t[j + 2] = ex2(t[j + 2] - (r.z > -INFINITY ? r.z : 0.f));
-          t[j + 3] = ex2(t[j + 3] - (r.w > -INFINITY ? r.w : 0.f));
-          w[j / 2] = DENSE ? pack2_bf16(t[j], t[j + 1]) : pack2_f16(t[j], t[j + 1]);
-          w[j / 2 + 1] = DENSE ? pack2_bf16(t[j + 2], t[j + 3]) : pack2_f16(t[j + 2], t[j + 3]);
+        for (int hh = 0; hh < 2; ++hh) {
+          float t[32];
+          logits(hh, t);
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            float2 x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float2 r = *reinterpret_cast<const float2*>(&ms.ref[32 * hh + j + 2 * k]);
+              x[k] = f2(ex2(t[j + 2 * k] - (r.x > -INFINITY ? r.x : 0.f)), ex2(t[j + 2 * k + 1] - (r.y > -INFINITY ? r.y : 0.f)));
+            }
+            put(hh, j, x);
+          }
         }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-          *reinterpret_cast<uint4*>(sm + C::P + sw128_off(tok, 4 * hh + k)) =
-              make_uint4(w[4 * k], w[4 * k + 1], w[4 * k + 2], w[4 * k + 3]);
-        lacc[hh] += transpose_reduce32<false>(t, lane);
       }
       fence_async_smem();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&ms.p_full);
+      // the sums, of the weights as rounded, while the outputs are multiplied
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        float t[32];
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const uint32_t v = w[16 * hh + j];
+          const float2 x = DENSE ? f2(bf16_lo(v), bf16_hi(v)) : __half22float2(*reinterpret_cast<const __half2*>(&v));
+          t[2 * j] = x.x;
+          t[2 * j + 1] = x.y;
+        }
+        lacc[hh] += transpose_reduce32<false>(t, lane);
+      }
     }
     mbar_wait_idle(&ms.o_done, (n - 1) & 1, abort_f);
     tc_fence_after();
