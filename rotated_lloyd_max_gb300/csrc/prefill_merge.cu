@@ -27,6 +27,7 @@ __global__ void __launch_bounds__(kThreads) prefill_merge_kernel(const __grid_co
   float c[E], d[E], W = 0.f;
 #pragma unroll
   for (int e = 0; e < E; ++e) c[e] = d[e] = 0.f;
+#pragma unroll 2
   for (int s = 0; s < S; ++s) {
     const float2 v = ml[s];
     if (v.y != v.y) W = v.y;  // a split that gave up: the row comes out NaN
@@ -64,52 +65,83 @@ __global__ void __launch_bounds__(kThreads) prefill_merge_kernel(const __grid_co
   }
 }
 
-// Merge of the tcgen05 kernel's partials, [tile][split][D / 4][128 rows][4]: a
-// CTA per 128-row tile, four threads per row with D / 4 coordinates each (the
-// transform's last two stages cross them), so that a warp reads eight rows'
-// 16-byte pieces side by side.
-template <int D>
-__global__ void __launch_bounds__(512) prefill_merge_tiles_kernel(const __grid_constant__ PrefillParams pp) {
-  constexpr int E = D / 4;
+// Merge of the narrow kernel's partials, [tile][split][D / 4][128 rows][4]: four
+// threads per row with D / 4 coordinates each (the transform's last two stages
+// cross them), so that a warp reads eight rows' 16-byte pieces side by side.
+// A CTA takes 256 / (4 SL) rows; with SL > 1 the splits of a row are shared by SL
+// groups of threads, whose sums meet in shared memory (a few rows with many
+// splits would otherwise wait for one load after another: 30 rows of 18 splits
+// 30 us with SL = 1).
+template <int D, int SL>
+__global__ void __launch_bounds__(256) prefill_merge_tiles_kernel(const __grid_constant__ PrefillParams pp) {
+  constexpr int E = D / 4, ROWS = 256 / (4 * SL);
+  __shared__ float part[SL > 1 ? (SL - 1) * 4 * ROWS : 1][E + 1];
+  __shared__ float wsum[SL > 1 ? SL * 4 * ROWS : 1];
   const QueryParams& p = pp.q;
-  const int tid = threadIdx.x, r = tid >> 2, qd = tid & 3;
-  const int ntile = (pp.rows + 127) / 128, tile = blockIdx.x % ntile;
-  const int64_t unit = blockIdx.x / ntile;
+  const int tid = threadIdx.x, qd = tid & 3, sl = SL > 1 ? tid / (4 * ROWS) : 0, lr = (tid >> 2) % ROWS;
+  const int ntile = (pp.rows + 127) / 128, per = 128 / ROWS;  // CTAs of a tile
+  const int64_t blk = blockIdx.x / per;
+  const int r = (int)(blockIdx.x % per) * ROWS + lr;
+  const int tile = (int)(blk % ntile);
+  const int64_t unit = blk / ntile;
   const int row = tile * 128 + r, tok = row / p.G;
   const int h = (int)(unit % p.Hkv), lb = (int)(unit / p.Hkv), b = lb % p.B, l = lb / p.B;
   const int tb = query_len(p, b);
-  if (tile * 128 >= tb * p.G) return;
-  const bool live = row < pp.rows && tok < tb;
+  if (tile * 128 + (int)(blockIdx.x % per) * ROWS >= tb * p.G) return;
+  const bool live = row < tb * p.G;
   const int S = pp.Sc + pp.St;
-  const float2* ml = pp.ws_ml + (int64_t)blockIdx.x * S * 128 + r;
-  const float4* acc = reinterpret_cast<const float4*>(pp.ws_acc) + ((int64_t)blockIdx.x * S * (D / 4) + qd * (E / 4)) * 128 + r;
+  const float2* ml = pp.ws_ml + blk * S * 128 + r;
+  const float4* acc = reinterpret_cast<const float4*>(pp.ws_acc) + (blk * S * (D / 4) + qd * (E / 4)) * 128 + r;
   float M = -INFINITY, W = 0.f;
-  if (live)
+  if (live) {
+#pragma unroll 4
     for (int s = 0; s < S; ++s) {
       const float2 v = ml[s * 128];
-      if (v.y > 0.f) M = fmaxf(M, v.x);
+      M = fmaxf(M, v.y > 0.f ? v.x : -INFINITY);
     }
+  }
+  // the records' splits, then (in a second round) the ring's: sum of w x over this thread's share
   float c[E];
+  auto round = [&](int s0, int s1) {
+#pragma unroll 2
+    for (int s = s0 + sl; s < s1; s += SL) {
+      const float2 v = live ? ml[s * 128] : make_float2(0.f, 0.f);
+      if (v.y != v.y) W = v.y;  // a split that gave up: the row comes out NaN
+      const bool on = v.y > 0.f;
+      const float w = on ? exp2f(v.x - M) : 0.f;
+      W = on ? fmaf(w, v.y, W) : W;
+      const float4* a = acc + (int64_t)s * (D / 4) * 128;
 #pragma unroll
-  for (int e = 0; e < E; ++e) c[e] = 0.f;
-  auto add = [&](int s) {
-    const float2 v = live ? ml[s * 128] : make_float2(0.f, 0.f);
-    if (v.y != v.y) W = v.y;  // a split that gave up: the row comes out NaN
-    if (!(v.y > 0.f)) return;
-    const float w = exp2f(v.x - M);
-    W = fmaf(w, v.y, W);
-    const float4* a = acc + (int64_t)s * (D / 4) * 128;
-#pragma unroll
-    for (int k = 0; k < E / 4; ++k) {
-      const float4 x = a[k * 128];
-      c[4 * k] = fmaf(w, x.x, c[4 * k]);
-      c[4 * k + 1] = fmaf(w, x.y, c[4 * k + 1]);
-      c[4 * k + 2] = fmaf(w, x.z, c[4 * k + 2]);
-      c[4 * k + 3] = fmaf(w, x.w, c[4 * k + 3]);
+      for (int k = 0; k < E / 4; ++k) {
+        const float4 x = on ? a[k * 128] : make_float4(0.f, 0.f, 0.f, 0.f);  // an empty split wrote nothing
+        c[4 * k] = fmaf(w, x.x, c[4 * k]);
+        c[4 * k + 1] = fmaf(w, x.y, c[4 * k + 1]);
+        c[4 * k + 2] = fmaf(w, x.z, c[4 * k + 2]);
+        c[4 * k + 3] = fmaf(w, x.w, c[4 * k + 3]);
+      }
     }
   };
+  auto join = [&] {  // group 0 gathers the other groups' sums
+    if constexpr (SL > 1) {
+      const int at = 4 * lr + qd;
+      __syncthreads();
+      if (sl > 0) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) part[(sl - 1) * 4 * ROWS + at][e] = c[e];
+      }
+      __syncthreads();
+      if (sl == 0) {
+        for (int g = 0; g < SL - 1; ++g)
+#pragma unroll
+          for (int e = 0; e < E; ++e) c[e] += part[g * 4 * ROWS + at][e];
+      }
+    }
+  };
+#pragma unroll
+  for (int e = 0; e < E; ++e) c[e] = 0.f;
   if (pp.Sc > 0) {
-    for (int s = 0; s < pp.Sc; ++s) add(s);
+    round(0, pp.Sc);
+    join();
     __syncwarp();
     fwht_regs<E>(c);
     fwht_lanes<E>(c, tid & 31, 4);
@@ -117,9 +149,17 @@ __global__ void __launch_bounds__(512) prefill_merge_tiles_kernel(const __grid_c
     for (int e = 0; e < E; ++e) {
       const int j = qd * E + e;
       c[e] *= ((p.vc.signs[j >> 5] >> (j & 31)) & 1u) ? -pp.inv_sqrt_d : pp.inv_sqrt_d;
+      if (sl > 0) c[e] = 0.f;
     }
   }
-  for (int s = pp.Sc; s < S; ++s) add(s);
+  round(pp.Sc, S);
+  join();
+  if constexpr (SL > 1) {
+    wsum[tid] = W;
+    __syncthreads();
+    if (sl > 0) return;
+    for (int g = 1; g < SL; ++g) W += wsum[g * 4 * ROWS + 4 * lr + qd];
+  }
   if (!live) return;
   const float iw = W > 0.f || W != W ? 1.f / W : 0.f;  // a row that sees no token is zero
   uint16_t* out = pp.out + l * pp.o_ls + b * pp.o_bs + (int64_t)tok * pp.o_ts + (int64_t)(h * p.G + row % p.G) * D + qd * E;
@@ -130,13 +170,19 @@ __global__ void __launch_bounds__(512) prefill_merge_tiles_kernel(const __grid_c
                    pack2_bf16(c[e + 4] * iw, c[e + 5] * iw), pack2_bf16(c[e + 6] * iw, c[e + 7] * iw));
 }
 
+template <int D>
+static void merge_tiles_launch(const PrefillParams& pp, int64_t tiles, cudaStream_t s) {
+  if (pp.Sc + pp.St > 6) prefill_merge_tiles_kernel<D, 8><<<(unsigned)(tiles * 16), 256, 0, s>>>(pp);
+  else prefill_merge_tiles_kernel<D, 1><<<(unsigned)(tiles * 2), 256, 0, s>>>(pp);
+}
+
 cudaError_t launch_prefill_merge(const PrefillParams& pp, cudaStream_t s) {
   const int64_t rows = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv * pp.rows;
   const unsigned grid = (unsigned)((rows + 3) / 4);
-  const unsigned tiles = (unsigned)((int64_t)pp.q.L * pp.q.B * pp.q.Hkv * ((pp.rows + 127) / 128));
+  const int64_t tiles = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv * ((pp.rows + 127) / 128);
   switch (pp.q.D) {
-    case 64: prefill_merge_tiles_kernel<64><<<tiles, 512, 0, s>>>(pp); break;
-    case 128: prefill_merge_tiles_kernel<128><<<tiles, 512, 0, s>>>(pp); break;
+    case 64: merge_tiles_launch<64>(pp, tiles, s); break;
+    case 128: merge_tiles_launch<128>(pp, tiles, s); break;
     case 256: prefill_merge_kernel<256><<<grid, kThreads, 0, s>>>(pp); break;
     case 512: prefill_merge_kernel<512><<<grid, kThreads, 0, s>>>(pp); break;
     default: return cudaErrorInvalidValue;

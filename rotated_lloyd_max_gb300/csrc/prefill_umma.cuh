@@ -39,7 +39,9 @@ constexpr int kPfSoft = 8, kPfLoad = 16;  // softmax and loading warps
 constexpr int kPfThreads = 32 * (kPfSoft + kPfLoad + 1);
 constexpr int kPfRows = 256;
 constexpr int kPfTok = 128 / kPfLoad;  // tokens of a tile that a loading warp decodes
-constexpr float kPfMargin = 13.f;  // log2 of the largest weight kept against an old reference
+// log2 of the largest weight kept against an old reference, and how far a new
+// one is put above the maximum it was found for
+constexpr float kPfMargin = 15.f, kPfAbove = 4.f;
 
 // Registers per thread: 72 at launch (25 warps: seven on one of the SM's four
 // partitions), then 104 for the softmax and 56 for the decoding warps, no more
@@ -623,7 +625,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
         float tm = mx > -INFINITY ? mx * f : -INFINITY;
         if (p.scap > 0.f) tm = soft_cap(tm, p.scap, p.iscap);
         if (__any_sync(0xffffffffu, tm > mref + kPfMargin)) {
-          const float mn = tm > mref + kPfMargin ? tm : mref;
+          const float mn = tm > mref + kPfMargin ? tm + kPfAbove : mref;
           const float al = mref > -INFINITY ? ex2(mref - mn) : 0.f;  // 1 where the reference stays
           const float sc = mn > -INFINITY ? al : 1.f;
           lsum *= sc;

@@ -521,7 +521,7 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
         if (tid < 64) {
           const float mx = fmaxf(fmaxf(ms.red[0][tid], ms.red[1][tid]), fmaxf(ms.red[2][tid], ms.red[3][tid]));
           const float mo = ms.ref[tid];
-          mn = mx > mo + kPfMargin ? mx : mo;
+          mn = mx > mo + kPfMargin ? mx + kPfAbove : mo;
           sc = mo > -INFINITY ? ex2(mo - mn) : mn > -INFINITY ? 0.f : 1.f;
         }
         bar_soft();
