@@ -179,10 +179,17 @@ def _check(fn: str, status: int):
         raise TqError(fn, status)
 
 
+_raw_stream = None  # torch's handle of the current stream by device (a Stream object costs microseconds)
+
+
 def _stream(stream):
+    global _raw_stream
     import torch
     if stream is None:
-        return c_p(torch.cuda.current_stream().cuda_stream)
+        if _raw_stream is None:
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                                  lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+        return c_p(_raw_stream(torch.cuda.current_device()))
     if isinstance(stream, int):
         return c_p(stream)
     return c_p(stream.cuda_stream)
@@ -448,6 +455,14 @@ def _check_tensors(dtype_of: dict):
             _need(dev is None or t.device == dev, f"{name} is on {t.device}, not on the current device {dev}")
 
 
+def _ready(args, workspace=None):
+    """The call runs where its tensors are (they may have been checked under another current device)."""
+    import torch
+    dev = args._tensors[args._lead].device.index
+    _need(dev == torch.cuda.current_device(), f"the tensors are on device {dev}, not on the current one")
+    _need(workspace is None or workspace.get_device() == dev, "the workspace is on another device")
+
+
 def _heads_packed(t, name: str, d: int):
     """(layer, batch, token) strides of a [L, B, T, heads, d] view whose heads and dims are packed."""
     _need(t.dim() == 5 and t.stride(4) == 1 and (t.shape[3] == 1 or t.stride(3) == d),
@@ -534,6 +549,7 @@ def make_append_args(*, k, k_tail, tail_len, tail_len_out=None, v=None, v_tail=N
     a.q_lens, a.n_chunks = _ptr(q_lens), _ptr(n_chunks)
     if mass is not None:
         a.mass, a.mass_layer_stride, a.mass_cap = mass.data_ptr(), *_mass_layout(mass, L, B, Hkv)
+    a._lead = 1
     a._tensors = (q, k, v, q_out, positions, inv_freq, k_tail, v_tail, tail_start, tail_len, out, q_lens, mass,
                   n_chunks)
     return a
@@ -549,6 +565,7 @@ def _mass_layout(mass, L: int, B: int, Hkv: int):
 
 def tq_append(args: tq_append_args, stream=None):
     """Rotate queries and keys and append keys and values to the ring (include/tq.h)."""
+    _ready(args)
     _check("tq_append", load().tq_append(ctypes.byref(args), _stream(stream)))
 
 
@@ -579,8 +596,9 @@ def make_query_args(*, q, scale: float, out=None, softcap: float = 0.0, causal: 
     a.n_kv_heads = Hkv
     for r, name in ((k_rec, "k_rec"), (v_rec, "v_rec")):
         if r is not None:
-            lead = (r.shape[0], r.shape[2]) if paged else (r.shape[0], r.shape[1], r.shape[2])
-            _need(lead == ((L, Hkv) if paged else (L, B, Hkv)) and (r.shape[0] == 0 or r[0].is_contiguous()),
+            lead = (r.shape[0], r.shape[2]) if paged else tuple(r.shape[:3])
+            _need(r.dim() == (4 if paged else 5) and lead == ((L, Hkv) if paged else (L, B, Hkv)) and
+                  r[0].is_contiguous(),
                   f"{name}: expected records [L, B, Hkv, cap, bytes] or a pool [L, blocks, Hkv, bytes], "
                   "contiguous within a layer")
     if k_rec is not None:
@@ -605,6 +623,7 @@ def make_query_args(*, q, scale: float, out=None, softcap: float = 0.0, causal: 
     _need(q_lens is None or (q_lens.is_contiguous() and tuple(q_lens.shape) == (B,)), "q_lens: expected int32 [B]")
     a.n_chunks, a.tail_start, a.tail_len, a.q_lens = _ptr(n_chunks), _ptr(tail_start), _ptr(tail_len), _ptr(q_lens)
     a.max_chunks, a.max_tail = max_chunks, max_tail
+    a._lead = 0
     a._tensors = (q, out, k_rec, v_rec, k_tail, v_tail, n_chunks, tail_start, tail_len, q_lens, block_table)
     return a
 
@@ -627,6 +646,7 @@ def tq_prefill_attn_workspace_size(args: tq_query_args, k_codec: Codec | None, v
 
 def tq_prefill_attn(args: tq_query_args, k_codec: Codec | None, v_codec: Codec | None, workspace, stream=None):
     """Attention of several query tokens per sequence over records and ring, bf16 out (include/tq.h)."""
+    _ready(args, workspace)
     _check("tq_prefill_attn", load().tq_prefill_attn(ctypes.byref(args), _raw(k_codec), _raw(v_codec), _ptr(workspace),
                                                      workspace.numel() * workspace.element_size(), _stream(stream)))
 
@@ -654,6 +674,7 @@ def tq_attn_mass_workspace_size(args: tq_query_args, k_codec: Codec | None) -> i
 def tq_attn_mass(args: tq_query_args, k_codec: Codec | None, mass, workspace, decay: float = 1.0, stream=None):
     """mass (f32 [L, B, Hkv, cap]) = decay * mass + the attention weight each cached token receives
     from the queries (include/tq.h)."""
+    _ready(args, workspace)
     stride, cap = _mass_layout(mass, args.n_layers, args.batch, args.n_kv_heads)
     _check("tq_attn_mass", load().tq_attn_mass(ctypes.byref(args), _raw(k_codec), _ptr(mass), stride, cap, decay,
                                                _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -698,7 +719,8 @@ def make_evict_mass_args(*, k_rec, v_rec, mass, n_chunks, max_chunks: int, keep_
     for rec, table, name in ((k_rec, block_table, "k_rec"), (v_rec, block_table, "v_rec"), (k_dst, dst_table, "k_dst"),
                              (v_dst, dst_table, "v_dst")):
         lead = (rec.shape[0], rec.shape[2]) if table is not None else tuple(rec.shape[:3])
-        _need(lead == ((L, Hkv) if table is not None else (L, B, Hkv)) and rec[0].is_contiguous(),
+        _need(rec.dim() == (5 if table is None else 4) and
+              lead == ((L, Hkv) if table is not None else (L, B, Hkv)) and rec[0].is_contiguous(),
               f"{name}: expected records [L, B, Hkv, cap, bytes] or a pool [L, blocks, Hkv, bytes], "
               "contiguous within a layer")
     _need(v_rec.shape[:-1] == k_rec.shape[:-1] and v_dst.shape[:-1] == k_dst.shape[:-1],
@@ -726,6 +748,7 @@ def make_evict_mass_args(*, k_rec, v_rec, mass, n_chunks, max_chunks: int, keep_
           "kept: expected contiguous int32 [L, B, Hkv, 128 * keep_chunks]")
     a.kept = _ptr(kept)
     a.max_chunks, a.max_tail, a.keep_chunks, a.sink, a.recent = max_chunks, max_tail, keep_chunks, sink, recent
+    a._lead = 0
     a._tensors = (k_rec, v_rec, k_dst, v_dst, mass, mass_dst, n_chunks, n_chunks_dst, tail_len, kept, block_table,
                   dst_table)
     return a
@@ -740,6 +763,7 @@ def tq_evict_mass_workspace_size(args: tq_evict_mass_args, k_codec: Codec, v_cod
 
 def tq_evict_mass(args: tq_evict_mass_args, k_codec: Codec, v_codec: Codec | None, workspace, stream=None):
     """Keep the tokens of the largest accumulated weight and compact the records (include/tq.h)."""
+    _ready(args, workspace)
     _check("tq_evict_mass", load().tq_evict_mass(ctypes.byref(args), _raw(k_codec), _raw(v_codec), _ptr(workspace),
                                                  workspace.numel() * workspace.element_size(), _stream(stream)))
 

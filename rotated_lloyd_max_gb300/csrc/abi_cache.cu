@@ -477,6 +477,10 @@ tq_status evict_mass_params(const tq_evict_mass_args* a, const tq_codec* kcod, c
   return TQ_OK;
 }
 
+size_t evict_mass_bytes(const EvictMassParams& p) {
+  return pad256((size_t)p.L * p.B * 4) + pad256((size_t)p.L * p.B * p.Hkv * p.slots * TQ_CHUNK * 4) + 256;
+}
+
 }  // namespace
 
 extern "C" {
@@ -575,7 +579,7 @@ tq_status tq_attn_mass(const tq_query_args* a, const tq_codec* k_codec, float* m
 size_t tq_evict_mass_workspace_size(const tq_evict_mass_args* a, const tq_codec* k_codec, const tq_codec* v_codec) {
   EvictMassParams p;
   if (evict_mass_params(a, k_codec, v_codec, &p) != TQ_OK) return 0;
-  return pad256((size_t)p.L * p.B * 4) + pad256((size_t)p.L * p.B * p.Hkv * p.slots * TQ_CHUNK * 4) + 256;
+  return evict_mass_bytes(p);
 }
 
 tq_status tq_evict_mass(const tq_evict_mass_args* a, const tq_codec* k_codec, const tq_codec* v_codec, void* workspace,
@@ -584,7 +588,7 @@ tq_status tq_evict_mass(const tq_evict_mass_args* a, const tq_codec* k_codec, co
   const tq_status st = evict_mass_params(a, k_codec, v_codec, &p);
   if (st != TQ_OK) return st;
   if (!workspace || !aligned(workspace, 256)) return TQ_ERR_INVALID_ARG;
-  if (workspace_bytes < tq_evict_mass_workspace_size(a, k_codec, v_codec)) return TQ_ERR_WORKSPACE;
+  if (workspace_bytes < evict_mass_bytes(p)) return TQ_ERR_WORKSPACE;
   p.counts = (int32_t*)workspace;
   p.list = (int32_t*)((char*)workspace + pad256((size_t)p.L * p.B * 4));
   return launch_evict_mass(p, (cudaStream_t)stream) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;

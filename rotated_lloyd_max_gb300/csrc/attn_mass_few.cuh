@@ -350,8 +350,10 @@ inline void attn_mass_few_layout(MassParams& mp, int D, int KB, bool outl) {
 template <int D, int KB, bool OUTL>
 cudaError_t attn_mass_few_launch_t(const MassParams& mp, cudaStream_t s) {
   auto kern = attn_mass_few_kernel<D, KB, OUTL>;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, mp.sm_total);
-  if (e != cudaSuccess) return e;
+  if (mp.sm_total > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, mp.sm_total);
+    if (e != cudaSuccess) return e;
+  }
   kern<<<dim3(mp.Sc + mp.St, mp.q.B * mp.q.Hkv, mp.q.L), kThreads, mp.sm_total, s>>>(mp);
   return cudaGetLastError();
 }

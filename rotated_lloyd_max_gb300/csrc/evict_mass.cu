@@ -462,7 +462,7 @@ cudaError_t launch_evict_mass(const EvictMassParams& p, cudaStream_t s) {
   const bool cached = smem <= 192 * 1024;
   auto kern = C > 1 ? (cached ? mass_select_kernel<true, true> : mass_select_kernel<false, true>)
                     : (cached ? mass_select_kernel<true, false> : mass_select_kernel<false, false>);
-  if (cached) {
+  if (cached && smem + (int)sizeof(SelShared) > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
