@@ -10,6 +10,7 @@ constexpr int kAddThreads = 256, kAddTokens = 4;  // tokens per thread
 template <int P>
 __global__ void __launch_bounds__(kAddThreads) attn_mass_add_kernel(const __grid_constant__ MassParams mp) {
   __shared__ float lse[8];
+  pdl_wait();
   const QueryParams& p = mp.q;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.y % p.Hkv, b = blockIdx.y / p.Hkv, l = blockIdx.z;
@@ -68,13 +69,12 @@ cudaError_t launch_attn_mass_add(const MassParams& mp, cudaStream_t s) {
   const int most = mp.q.max_chunks * kChunk + mp.q.max_tail;
   const dim3 grid((most + kAddThreads * kAddTokens - 1) / (kAddThreads * kAddTokens), mp.q.B * mp.q.Hkv, mp.q.L);
   switch (mp.pitch) {
-    case 1: attn_mass_add_kernel<1><<<grid, kAddThreads, 0, s>>>(mp); break;
-    case 2: attn_mass_add_kernel<2><<<grid, kAddThreads, 0, s>>>(mp); break;
-    case 4: attn_mass_add_kernel<4><<<grid, kAddThreads, 0, s>>>(mp); break;
-    case 8: attn_mass_add_kernel<8><<<grid, kAddThreads, 0, s>>>(mp); break;
+    case 1: return launch_after(attn_mass_add_kernel<1>, grid, kAddThreads, 0, s, 1, mp);
+    case 2: return launch_after(attn_mass_add_kernel<2>, grid, kAddThreads, 0, s, 1, mp);
+    case 4: return launch_after(attn_mass_add_kernel<4>, grid, kAddThreads, 0, s, 1, mp);
+    case 8: return launch_after(attn_mass_add_kernel<8>, grid, kAddThreads, 0, s, 1, mp);
     default: return cudaErrorInvalidValue;
   }
-  return cudaGetLastError();
 }
 
 }  // namespace tq

@@ -37,6 +37,7 @@ __global__ void __launch_bounds__(kThreads) attn_mass_few_kernel(const __grid_co
   constexpr int NB = STEP * KB, NW = (NB + 31) / 32;
   constexpr bool AL = NB % 32 == 0;
   const QueryParams& p = mp.q;
+  pdl_start();
   extern __shared__ __align__(128) unsigned char sm[];
   uint4* qfrag = reinterpret_cast<uint4*>(sm + mp.sm_frag);
   uint2* qfragd = reinterpret_cast<uint2*>(sm + mp.sm_frag);

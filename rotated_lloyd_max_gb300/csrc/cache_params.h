@@ -95,6 +95,37 @@ cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
 cudaError_t launch_append_commit(const AppendParams& p, cudaStream_t s);
 cudaError_t launch_evict_mass(const EvictMassParams& p, cudaStream_t s);
 
+#ifdef __CUDACC__
+// Programmatic dependent launch between the kernels of one call: the second is
+// launched while the first runs and waits on the device for its end, which
+// hides a launch's latency (1 to 2 us of the short calls).  Every thread of the
+// second kernel waits before anything else, so that its end is never before the
+// first one's.  pdl_start: from here
+// on the next kernel may be made resident; pdl_wait: the kernel before has
+// ended and what it wrote is visible.
+__device__ __forceinline__ void pdl_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <class... Args>
+inline cudaError_t launch_after(void (*kern)(Args...), dim3 grid, int block, int smem, cudaStream_t s, int cluster,
+                                const Args&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+#endif
+
 // abi.cu
 int sm_count();
 int max_dynamic_smem();

@@ -60,6 +60,7 @@ template <bool CACHED, bool CLUSTER>
 __global__ void __launch_bounds__(kSelThreads, 1) mass_select_kernel(const __grid_constant__ EvictMassParams p) {
   __shared__ SelShared sh;
   extern __shared__ uint32_t keys[];
+  pdl_start();
   cg::cluster_group cl = cg::this_cluster();
   const int C = CLUSTER ? (int)cl.num_blocks() : 1, rank = CLUSTER ? (int)cl.block_rank() : 0;
   const int64_t stream = blockIdx.x / C;
@@ -306,6 +307,7 @@ __global__ void __launch_bounds__(kMoveThreads) mass_compact_kernel(const __grid
   __shared__ MoveShared sh;
   extern __shared__ uint32_t ent[];
   const int job = blockIdx.z;  // 0: keys, 1: values, 2: weights
+  pdl_wait();
   const int64_t stream = blockIdx.y;
   const int h = stream % p.Hkv, lb = stream / p.Hkv, l = lb / p.B, b = lb % p.B;
   const int n = p.counts[lb], left = min(n, p.keep);
@@ -363,6 +365,7 @@ __global__ void __launch_bounds__(kMoveThreads) mass_compact_kernel(const __grid
 template <int UNIT>
 __global__ void __launch_bounds__(kMoveThreads) mass_move_kernel(const __grid_constant__ EvictMassParams p) {
   using V = typename std::conditional<UNIT == 16, uint4, uint2>::type;
+  pdl_wait();
   const int64_t stream = blockIdx.y;
   const int h = stream % p.Hkv, lb = stream / p.Hkv, l = lb / p.B, b = lb % p.B;
   const int n = p.counts[lb], left = min(n, p.keep);
@@ -414,8 +417,7 @@ template <int UNIT>
 static cudaError_t move_launch(const EvictMassParams& p, cudaStream_t s) {
   const int64_t tokens = (int64_t)p.slots * kChunk + p.max_tail;
   const dim3 grid((unsigned)((tokens + kMoveThreads - 1) / kMoveThreads), p.L * p.B * p.Hkv);
-  mass_move_kernel<UNIT><<<grid, kMoveThreads, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_after(mass_move_kernel<UNIT>, grid, kMoveThreads, 0, s, 1, p);
 }
 
 template <int UNIT, bool OUTL, bool INPLACE>
@@ -428,18 +430,8 @@ static cudaError_t compact_launch(const EvictMassParams& p, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(INPLACE ? kMoveCluster : p.slots, p.L * p.B * p.Hkv, 3);
-  cfg.blockDim = dim3(kMoveThreads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = kMoveCluster;
-  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = INPLACE ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, p);
+  return launch_after(kern, dim3(INPLACE ? kMoveCluster : p.slots, p.L * p.B * p.Hkv, 3), kMoveThreads, smem, s,
+                      INPLACE ? kMoveCluster : 1, p);
 }
 
 template <int UNIT, bool OUTL>

@@ -9,6 +9,7 @@ namespace tq {
 template <int D>
 __global__ void __launch_bounds__(kThreads) prefill_merge_kernel(const __grid_constant__ PrefillParams pp) {
   constexpr int E = D / 32;
+  pdl_wait();
   const QueryParams& p = pp.q;
   const int lane = threadIdx.x & 31;
   const int64_t wrow = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
@@ -77,6 +78,7 @@ __global__ void __launch_bounds__(256) prefill_merge_tiles_kernel(const __grid_c
   constexpr int E = D / 4, ROWS = 256 / (4 * SL);
   __shared__ float part[SL > 1 ? (SL - 1) * 4 * ROWS : 1][E + 1];
   __shared__ float wsum[SL > 1 ? SL * 4 * ROWS : 1];
+  pdl_wait();
   const QueryParams& p = pp.q;
   const int tid = threadIdx.x, qd = tid & 3, sl = SL > 1 ? tid / (4 * ROWS) : 0, lr = (tid >> 2) % ROWS;
   const int ntile = (pp.rows + 127) / 128, per = 128 / ROWS;  // CTAs of a tile
@@ -171,9 +173,9 @@ __global__ void __launch_bounds__(256) prefill_merge_tiles_kernel(const __grid_c
 }
 
 template <int D>
-static void merge_tiles_launch(const PrefillParams& pp, int64_t tiles, cudaStream_t s) {
-  if (pp.Sc + pp.St > 6) prefill_merge_tiles_kernel<D, 8><<<(unsigned)(tiles * 16), 256, 0, s>>>(pp);
-  else prefill_merge_tiles_kernel<D, 1><<<(unsigned)(tiles * 2), 256, 0, s>>>(pp);
+static cudaError_t merge_tiles_launch(const PrefillParams& pp, int64_t tiles, cudaStream_t s) {
+  if (pp.Sc + pp.St > 6) return launch_after(prefill_merge_tiles_kernel<D, 8>, dim3((unsigned)(tiles * 16)), 256, 0, s, 1, pp);
+  return launch_after(prefill_merge_tiles_kernel<D, 1>, dim3((unsigned)(tiles * 2)), 256, 0, s, 1, pp);
 }
 
 cudaError_t launch_prefill_merge(const PrefillParams& pp, cudaStream_t s) {
@@ -181,13 +183,12 @@ cudaError_t launch_prefill_merge(const PrefillParams& pp, cudaStream_t s) {
   const unsigned grid = (unsigned)((rows + 3) / 4);
   const int64_t tiles = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv * ((pp.rows + 127) / 128);
   switch (pp.q.D) {
-    case 64: merge_tiles_launch<64>(pp, tiles, s); break;
-    case 128: merge_tiles_launch<128>(pp, tiles, s); break;
-    case 256: prefill_merge_kernel<256><<<grid, kThreads, 0, s>>>(pp); break;
-    case 512: prefill_merge_kernel<512><<<grid, kThreads, 0, s>>>(pp); break;
+    case 64: return merge_tiles_launch<64>(pp, tiles, s);
+    case 128: return merge_tiles_launch<128>(pp, tiles, s);
+    case 256: return launch_after(prefill_merge_kernel<256>, dim3(grid), kThreads, 0, s, 1, pp);
+    case 512: return launch_after(prefill_merge_kernel<512>, dim3(grid), kThreads, 0, s, 1, pp);
     default: return cudaErrorInvalidValue;
   }
-  return cudaGetLastError();
 }
 
 }  // namespace tq

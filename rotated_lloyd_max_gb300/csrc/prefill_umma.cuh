@@ -708,6 +708,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
 
 template <int D>
 __global__ void __launch_bounds__(kPfThreads, 1) prefill_umma_kernel(const __grid_constant__ PrefillParams pp) {
+  pdl_start();
   extern __shared__ __align__(1024) unsigned char smraw[];
   unsigned char* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
   // records first, the ring's shorter runs behind them

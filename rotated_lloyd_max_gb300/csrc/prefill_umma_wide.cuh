@@ -615,6 +615,7 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
 
 template <int D>
 __global__ void __launch_bounds__(kPwThreads, 1) prefill_wide_kernel(const __grid_constant__ PrefillParams pp) {
+  pdl_start();
   extern __shared__ __align__(1024) unsigned char smraw[];
   unsigned char* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
   const int64_t U = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv * pp.tiles;
