@@ -496,12 +496,19 @@ typedef struct {
 /*
  * Attention of several query tokens per sequence over records and ring:
  *   out[l][b][t][h] = sum_i softmax_i(cap(scale q . k_i)) v_i
- * over the tokens that query sees, rounded once to bf16.  The records are
- * dequantised to f16 (centroids and rotated queries each within half an f16
- * step, f32 accumulation and softmax statistics, weights rounded to f16; the
- * ring's bf16 keys, values and queries enter exactly, its weights rounded to
- * bf16): the output is within bf16's own precision of the exact sum.  A row
- * that sees no token is zero; rows t >= T_b are not touched.
+ * over the tokens that query sees, rounded once to bf16.  The records'
+ * operands are f16 (centroids, rotated queries, weights, and at head dims 64
+ * and 128 the per-vector scales, each within half an f16 step; f32
+ * accumulation and softmax statistics); the ring's bf16 keys, values and
+ * queries enter exactly, its weights rounded to bf16: the output is within
+ * bf16's own precision of the exact sum.  Scales below 2^-24 of the largest
+ * one of the same context split round to zero.  A row that sees no token is
+ * zero; rows t >= T_b are not touched.  Slots and records that hold no token
+ * are never read, and keys of tokens a query does not see do not touch its row,
+ * whatever they hold; the VALUES of all tokens below total have to be finite
+ * (a weight of zero times an infinity is NaN, for a later query's token too).
+ * The kernels bound every internal wait (about two seconds); if one expires (a
+ * fault of the device, not of the arguments) the rows concerned are NaN.
  * workspace: device, 256-byte aligned; contents need no initialisation.
  * Calls that overlap on the GPU need workspaces of their own.
  */
@@ -518,7 +525,10 @@ tq_status tq_prefill_attn(const tq_query_args* args, const tq_codec* k_codec, co
  * record's token 128 c + s comes first, the ring's tokens follow from
  * 128 n_chunks on, so that tq_evict moves no entry.  Entries of index >= total
  * are not touched.  mass_cap >= 128 max_chunks + max_tail.  Sums run in a
- * fixed order (no atomics).  decay: finite, >= 0.
+ * fixed order (no atomics); logits are f32-accurate (operands of 22 bits or
+ * exact), on every route: up to 8 rows (query heads of a kv head x t_q), up to
+ * 40 or head dims 256 and 512 (mma.sync), more (tcgen05; a wait of its that
+ * expires leaves NaN).  decay: finite, >= 0.  workspace as for tq_prefill_attn.
  */
 size_t tq_attn_mass_workspace_size(const tq_query_args* args, const tq_codec* k_codec);
 tq_status tq_attn_mass(const tq_query_args* args, const tq_codec* k_codec, float* mass,

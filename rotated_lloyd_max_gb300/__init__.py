@@ -465,9 +465,9 @@ def _ready(args, workspace=None):
 
 def _heads_packed(t, name: str, d: int):
     """(layer, batch, token) strides of a [L, B, T, heads, d] view whose heads and dims are packed."""
-    _need(t.dim() == 5 and t.stride(4) == 1 and (t.shape[3] == 1 or t.stride(3) == d),
+    _need(t.dim() == 5 and t.shape[4] == d and t.stride(4) == 1 and (t.shape[3] == 1 or t.stride(3) == d),
           f"{name}: expected [L, B, T, heads, d] with heads and dims packed")
-    return t.stride(0), t.stride(1), t.stride(2)
+    return tuple(t.stride(i) if t.shape[i] > 1 else 0 for i in range(3))
 
 
 def _ring_cap(t, name: str):
@@ -526,7 +526,7 @@ def make_append_args(*, k, k_tail, tail_len, tail_len_out=None, v=None, v_tail=N
         a.q_out_layer_stride, a.q_out_batch_stride, a.q_out_token_stride = _heads_packed(q_out, "q_out", d)
     _need(tuple(k_tail.shape[:3]) == (L, B, Hkv) and k_tail.shape[4] == d, "k_tail: expected [L, B, Hkv, cap, d]")
     a.tail_cap = _ring_cap(k_tail, "k_tail")
-    a.k_tail, a.tail_layer_stride = k_tail.data_ptr(), k_tail.stride(0)
+    a.k_tail, a.tail_layer_stride = k_tail.data_ptr(), _layer_stride(k_tail)
     if v_tail is not None:
         _need(v_tail.shape == k_tail.shape and v_tail.stride() == k_tail.stride(), "v_tail: expected k_tail's layout")
         a.v_tail = v_tail.data_ptr()
@@ -555,12 +555,16 @@ def make_append_args(*, k, k_tail, tail_len, tail_len_out=None, v=None, v_tail=N
     return a
 
 
+def _layer_stride(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else 0
+
+
 def _mass_layout(mass, L: int, B: int, Hkv: int):
     cap = mass.shape[-1]
     _need(tuple(mass.shape[:3]) == (L, B, Hkv) and mass.dim() == 4 and mass.stride(3) == 1 and
           (Hkv == 1 or mass.stride(2) == cap) and (B == 1 or mass.stride(1) == Hkv * cap),
           "mass: expected f32 [L, B, Hkv, cap], contiguous within a layer")
-    return mass.stride(0), cap
+    return _layer_stride(mass), cap
 
 
 def tq_append(args: tq_append_args, stream=None):
@@ -602,18 +606,18 @@ def make_query_args(*, q, scale: float, out=None, softcap: float = 0.0, causal: 
                   f"{name}: expected records [L, B, Hkv, cap, bytes] or a pool [L, blocks, Hkv, bytes], "
                   "contiguous within a layer")
     if k_rec is not None:
-        a.k_rec, a.k_rec_layer_stride = k_rec.data_ptr(), k_rec.stride(0)
+        a.k_rec, a.k_rec_layer_stride = k_rec.data_ptr(), _layer_stride(k_rec)
         a.rec_cap = k_rec.shape[1] if paged else k_rec.shape[3]
     if v_rec is not None:
         _need(k_rec is not None and v_rec.shape[:-1] == k_rec.shape[:-1], "v_rec: expected k_rec's layout")
-        a.v_rec, a.v_rec_layer_stride = v_rec.data_ptr(), v_rec.stride(0)
+        a.v_rec, a.v_rec_layer_stride = v_rec.data_ptr(), _layer_stride(v_rec)
     if paged:
         _need(block_table.is_contiguous() and block_table.dim() == 2 and block_table.shape[0] == B,
               "block_table: expected contiguous int32 [B, stride]")
         a.block_table, a.table_stride = block_table.data_ptr(), block_table.shape[1]
     if k_tail is not None:
         _need(tuple(k_tail.shape[:3]) == (L, B, Hkv) and k_tail.shape[4] == d, "k_tail: expected [L, B, Hkv, cap, d]")
-        a.k_tail, a.tail_layer_stride, a.tail_cap = k_tail.data_ptr(), k_tail.stride(0), _ring_cap(k_tail, "k_tail")
+        a.k_tail, a.tail_layer_stride, a.tail_cap = k_tail.data_ptr(), _layer_stride(k_tail), _ring_cap(k_tail, "k_tail")
     if v_tail is not None:
         _need(k_tail is not None and v_tail.shape == k_tail.shape and v_tail.stride() == k_tail.stride(),
               "v_tail: expected k_tail's layout")
@@ -675,6 +679,9 @@ def tq_attn_mass(args: tq_query_args, k_codec: Codec | None, mass, workspace, de
     """mass (f32 [L, B, Hkv, cap]) = decay * mass + the attention weight each cached token receives
     from the queries (include/tq.h)."""
     _ready(args, workspace)
+    import torch
+    _need(mass.dtype == torch.float32 and mass.device == args._tensors[0].device,
+          "mass: expected f32 on the queries' device")
     stride, cap = _mass_layout(mass, args.n_layers, args.batch, args.n_kv_heads)
     _check("tq_attn_mass", load().tq_attn_mass(ctypes.byref(args), _raw(k_codec), _ptr(mass), stride, cap, decay,
                                                _ptr(workspace), workspace.numel() * workspace.element_size(),
@@ -728,8 +735,8 @@ def make_evict_mass_args(*, k_rec, v_rec, mass, n_chunks, max_chunks: int, keep_
     _need(k_dst.shape[-1] == k_rec.shape[-1] and v_dst.shape[-1] == v_rec.shape[-1],
           "destination records: expected the source's size")
     a.k_rec, a.v_rec, a.k_dst, a.v_dst = (t.data_ptr() for t in (k_rec, v_rec, k_dst, v_dst))
-    a.k_rec_layer_stride, a.v_rec_layer_stride = k_rec.stride(0), v_rec.stride(0)
-    a.k_dst_layer_stride, a.v_dst_layer_stride = k_dst.stride(0), v_dst.stride(0)
+    a.k_rec_layer_stride, a.v_rec_layer_stride = _layer_stride(k_rec), _layer_stride(v_rec)
+    a.k_dst_layer_stride, a.v_dst_layer_stride = _layer_stride(k_dst), _layer_stride(v_dst)
     a.rec_cap = k_rec.shape[1] if block_table is not None else k_rec.shape[3]
     a.dst_cap = k_dst.shape[1] if dst_table is not None else k_dst.shape[3]
     for table, name in ((block_table, "block_table"), (dst_table, "dst_table")):

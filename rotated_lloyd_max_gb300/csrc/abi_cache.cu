@@ -49,7 +49,7 @@ tq_status append_params(const tq_append_args* a, AppendParams* p) {
   const int d = a->head_dim;
   if (!dim_ok(d)) return TQ_ERR_UNSUPPORTED;
   if (a->n_layers <= 0 || a->batch <= 0 || a->t_q <= 0 || a->n_q_heads < 0 || a->n_kv_heads <= 0 ||
-      a->n_q_heads > 65535 || a->n_kv_heads > 65535)
+      a->n_q_heads > 16384 || a->n_kv_heads > 16384)
     return TQ_ERR_INVALID_ARG;
   if (!a->k || !a->k_tail || !a->tail_len || !a->tail_len_out || a->tail_cap <= 0) return TQ_ERR_INVALID_ARG;
   if ((a->v == nullptr) != (a->v_tail == nullptr) || (a->q != nullptr) != (a->n_q_heads > 0) ||

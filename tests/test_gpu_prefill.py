@@ -153,3 +153,65 @@ def test_captured_and_replayed(tq, orc):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, eager)
+
+
+@pytest.mark.parametrize("d,G,shared", [(64, 3, False), (128, 5, False), (512, 4, False)])
+def test_keys_a_query_does_not_see_may_be_anything(tq, orc, d, G, shared):
+    """Later new tokens' keys hold infinities and NaN: the queries before them are as with clean ones."""
+    import torch
+    c = Cache(tq, orc, B=1, Hkv=2, d=d, kb=3, vb=3, n=2, tail=50, seed=11)
+    T = 20
+    q = queries(1, 1, T, 2 * G, d, 3)
+    clean = _run(tq, c, q, None, G)
+    for back, bad in ((0, math.nan), (1, math.inf), (4, -math.inf)):
+        slot = (int(c.start[0, 0]) + 50 - 1 - back) % c.cap
+        c.ring["k"][0, 0, :, slot] = bad
+    out = _run(tq, c, q, None, G)
+    assert torch.equal(out[0, 0, : T - 5], clean[0, 0, : T - 5])
+
+
+def test_broadcast_and_strided_queries(tq, orc):
+    """Queries shared by the sequences (batch stride 0), a fused projection's view, one kv head."""
+    import torch
+    c = Cache(tq, orc, B=3, Hkv=1, d=64, kb=2, vb=2, n=2, tail=40, lens=([2, 2, 2], [40, 40, 40]), seed=12)
+    wide = tl.to_bf16_tensor(queries(1, 1, 6, 9, 64, 4), "cuda")
+    view = wide[:, :, :, 2:7].expand(1, 3, 6, 5, 64)
+    out, ref = torch.empty((1, 3, 6, 5, 64), dtype=torch.bfloat16, device="cuda"), None
+    tq.prefill_attn(k_codec=c.kc, v_codec=c.vc, q=view, out=out, scale=1.0, **c.kw())
+    ref = torch.empty_like(out)
+    tq.prefill_attn(k_codec=c.kc, v_codec=c.vc, q=view.contiguous(), out=ref, scale=1.0, **c.kw())
+    assert torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("scale", [-1.0, 0.0])
+@pytest.mark.parametrize("d", [64, 256])
+def test_negative_and_zero_scales(tq, orc, d, scale):
+    c = Cache(tq, orc, B=1, Hkv=1, d=d, kb=4, vb=2, n=2, tail=30, seed=14)
+    q = queries(1, 1, 4, 3, d, 5)
+    out = _run(tq, c, q, None, 3, scale=scale)
+    qf = synth.bf16_bits_to_f32(q).astype(np.float64)
+    got = synth.bf16_bits_to_f32(tl.bf16_tensor_bits(out.contiguous())).astype(np.float64)
+    k, v = c.vectors("k", 0, 0, 0), c.vectors("v", 0, 0, 0)
+    for i in range(3):
+        want = weights(qf[0, 0, :, i], k, 4, 286, True, 0.0, scale) @ v
+        assert np.linalg.norm(got[0, 0, :, i] - want) <= 2.0 ** -7 * np.linalg.norm(want)
+
+
+def test_growing_logits_move_the_reference(tq, orc):
+    """Keys whose scales grow by records: every record passes the reference of those before by far."""
+    import torch
+    for d, kb in ((128, 4), (512, 3)):
+        c = Cache(tq, orc, B=1, Hkv=1, d=d, kb=kb, vb=4, n=6, tail=9, seed=15)
+        off = 128 * d * kb // 8
+        sc = c.rec["k"][0, 0, 0, :, off:off + 512].contiguous().view(torch.float32)
+        c.rec["k"][0, 0, 0, :, off:off + 512] = (sc * torch.tensor([0.1, 1, 3, 6, 9, 12], device="cuda")[:, None]).view(torch.uint8)
+        c._host["k"] = c.rec["k"].cpu().numpy()
+        q = queries(1, 1, 7, 4, d, 16)
+        out = _run(tq, c, q, None, 4, splits=1)
+        qf = synth.bf16_bits_to_f32(q).astype(np.float64)
+        got = synth.bf16_bits_to_f32(tl.bf16_tensor_bits(out.contiguous())).astype(np.float64)
+        k, v = c.vectors("k", 0, 0, 0), c.vectors("v", 0, 0, 0)
+        # a logit of up to 60 is off by 2^-12 of itself: 2^-6 of a weight, and so of the output
+        for i in range(4):
+            want = weights(qf[0, 0, :, i], k, 7, 6 * 128 + 9, True, 0.0, 1.0) @ v
+            assert np.linalg.norm(got[0, 0, :, i] - want) <= 2.0 ** -5 * np.linalg.norm(want)
