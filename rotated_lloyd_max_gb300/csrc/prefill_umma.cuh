@@ -9,12 +9,21 @@
 // half as many, columns 256.. hold O.
 //
 // Operands of the records are f16: q~ 2^s (s per row), and centroid * scale
-// with the token's scale folded in, n 2^-(E+1) as f16 with E the exponent of
-// the largest scale of the CTA's run (read ahead; values below 2^-24 of the
-// largest round to zero), so that a logit needs one multiply-add and a weight
-// none.  The ring's operands are bf16 as they are.  The softmax subtracts a
-// reference that follows the maximum only when it is passed by 2^8, so O is
-// rescaled rarely, by the warps that own the rows.
+// with the token's scale folded in, n 2^-(E+1) with E the exponent of the largest
+// scale of the CTA's run (read ahead; values below 2^-24 of the largest round to
+// zero), so that a logit needs one multiply-add and a weight none.  A key's scale
+// is a sum of two f16: rounded to one, it would be off by up to 2^-12 in all of
+// the key's coordinates alike and move a logit of 12 by 3e-3, where the products'
+// own roundings average out (outputs' error 2.0e-3, not 2.6e-3; 1024 tokens over
+// 32768 cached take 590 us, not 563; scaling the f32 scores instead: 694).  The
+// ring's operands are bf16 as they are.
+//
+// The softmax subtracts a reference that is put 2^4 above the first tile's
+// maximum and moves only when a logit passes it by 2^15, so that scores are read
+// once and O is hardly ever rescaled (by the warps that own the rows; a warp that
+// rescales holds the whole CTA up: a reference at the maximum that moves at 2^8
+// takes 5% longer).  Weights are f16, 11 bits down to 2^-14 and to within 2^-25
+// below, which is 2^-21 of the first tile's largest.
 //
 // Warps: 0-3 and 4-7 softmax of tile 0 and 1 (a thread per row), 8-23 decode
 // records (or copy ring tokens) into two stages each of key and value tiles,
@@ -46,7 +55,8 @@ constexpr float kPfMargin = 15.f, kPfAbove = 4.f;
 // Registers per thread: 72 at launch (25 warps: seven on one of the SM's four
 // partitions), then 104 for the softmax and 56 for the decoding warps, no more
 // in sum than at launch.  Sixteen decoding warps rather than eight: what they do
-// is short dependent chains (1024 tokens over 32768 cached: 652 us against 817).
+// is short dependent chains (1024 tokens over 32768 cached: 652 us against 817
+// at that stage).
 constexpr int kPfLaunchRegs = 72, kPfSoftRegs = 104, kPfLoadRegs = 56;
 static_assert(kPfSoft * kPfSoftRegs + kPfLoad * kPfLoadRegs + kPfLaunchRegs <= (kPfSoft + kPfLoad + 1) * kPfLaunchRegs,
               "the registers that some warps take, others gave");
@@ -116,6 +126,10 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, __half2 b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), b);
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, __half2 b, uint32_t c) {
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&a), b, *reinterpret_cast<const __half2*>(&c));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 
 // centroids of up to 16 levels as byte planes; with 8 levels or fewer one lookup a plane is enough
 template <int B>
@@ -170,18 +184,19 @@ __device__ __forceinline__ void load_packed(const uint8_t* rec, Packed<D>& k) {
 // LUT: pairs of 4-bit codes by one shared-memory lookup in a table with a copy per
 // lane (entry e at 128 e + 4 lane, no bank conflicts), two logic operations a
 // pair where the byte planes take six a pair.
-template <int D, int B, bool LUT>
+template <int D, int B, bool LUT, bool KEYS>
 __device__ __forceinline__ void store_decoded(const Packed<D>& k, float n, const Planes& pl, const unsigned char* lut,
                                               unsigned char* st, int w, int lane) {
   using P = Packed<D>;
-  const uint32_t n2 = pack2_f16(n, n);
+  const float lead = __half2float(__float2half_rn(n));
+  const uint32_t n2 = pack2_f16(n, KEYS ? n - lead : n);
   st += w * kPfTok * 128;
   const uint32_t lo = 4 * lane;
 #pragma unroll
   for (int i = 0; i < P::PER; ++i) {
     const int row = (lane + 32 * i) / P::CH, ch = (lane + 32 * i) % P::CH;
     const uint32_t sw = __shfl_sync(0xffffffffu, n2, row);
-    const __half2 s = *reinterpret_cast<const __half2*>(&sw);
+    const __half2 sl = *reinterpret_cast<const __half2*>(&sw), s = __half2half2(__low2half(sl)), l = __high2half2(sl);
     uint4 v;
     if constexpr (LUT) {
       const uint32_t x = k.x[i];
@@ -192,7 +207,12 @@ __device__ __forceinline__ void store_decoded(const Packed<D>& k, float n, const
     } else {
       v = decode_codes<B>(k.x[i], pl);
     }
-    v = make_uint4(hmul2(v.x, s), hmul2(v.y, s), hmul2(v.z, s), hmul2(v.w, s));
+    if constexpr (KEYS) {  // one rounding of centroid * (lead + rest), not two
+      v = make_uint4(hfma2(v.x, s, hmul2(v.x, l)), hfma2(v.y, s, hmul2(v.y, l)), hfma2(v.z, s, hmul2(v.z, l)),
+                     hfma2(v.w, s, hmul2(v.w, l)));
+    } else {
+      v = make_uint4(hmul2(v.x, s), hmul2(v.y, s), hmul2(v.z, s), hmul2(v.w, s));
+    }
     *reinterpret_cast<uint4*>(st + (ch >> 3) * 16384 + row * 128 + (((ch ^ row) & 7) << 4)) = v;
   }
 }
@@ -255,17 +275,17 @@ __device__ __forceinline__ void side_list(const CodecDev& c, const uint8_t* rec,
   }
 }
 
-template <int D>
+template <int D, bool KEYS>
 __device__ __forceinline__ void decode_tile(const CodecDev& c, const uint8_t* rec, const Packed<D>& k, const Planes& pl,
                                             const unsigned char* lut, float nscale, unsigned char* st, int w, int lane) {
   const float n = k.n * nscale;
   switch (c.bits) {
-    case 1: store_decoded<D, 1, false>(k, n, pl, lut, st, w, lane); break;
-    case 2: store_decoded<D, 2, false>(k, n, pl, lut, st, w, lane); break;
-    case 3: store_decoded<D, 3, false>(k, n, pl, lut, st, w, lane); break;
+    case 1: store_decoded<D, 1, false, KEYS>(k, n, pl, lut, st, w, lane); break;
+    case 2: store_decoded<D, 2, false, KEYS>(k, n, pl, lut, st, w, lane); break;
+    case 3: store_decoded<D, 3, false, KEYS>(k, n, pl, lut, st, w, lane); break;
     default:
-      if (lut) store_decoded<D, 4, true>(k, n, pl, lut, st, w, lane);
-      else store_decoded<D, 4, false>(k, n, pl, lut, st, w, lane);
+      if (lut) store_decoded<D, 4, true, KEYS>(k, n, pl, lut, st, w, lane);
+      else store_decoded<D, 4, false, KEYS>(k, n, pl, lut, st, w, lane);
   }
   if (c.has_outl)
     side_list<D>(c, rec, w, lane, n, [&](int row, int j, float y, float nr) {
@@ -549,7 +569,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
       for (int i = 0; i < n; ++i) {
         const int s = i & 1, ph = ((i >> 1) & 1) ^ 1;
         mbar_wait_idle(&ms.k_empty[s], ph, abort_f);
-        decode_tile<D>(p.kc, ks.next, xk, kpl, klut, ek, sm + C::K + s * C::TILE, w, lane);
+        decode_tile<D, true>(p.kc, ks.next, xk, kpl, klut, ek, sm + C::K + s * C::TILE, w, lane);
         fence_async_smem();  // before the next loads, which it would wait for
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.k_full[s]);
@@ -558,7 +578,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
           load_tile<D>(ks, xk);
         }
         mbar_wait_idle(&ms.v_empty[s], ph, abort_f);
-        decode_tile<D>(p.vc, vs.next, xv, vpl, vlut, ev, sm + C::V + s * C::TILE, w, lane);
+        decode_tile<D, false>(p.vc, vs.next, xv, vpl, vlut, ev, sm + C::V + s * C::TILE, w, lane);
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.v_full[s]);
