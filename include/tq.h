@@ -411,6 +411,8 @@ tq_status tq_decode_attn_noalloc(const tq_attn_args* args, const tq_codec* k_cod
  * or a tail_len outside [0, tail_cap]) is not appended and keeps its tail_len,
  * as tq_evict leaves a full record array; its queries are still rotated.
  * Rows t >= T_b of q_out and ring slots of no new token are not touched.
+ * What the call writes may not overlap itself: along axes longer than one the
+ * strides of q_out are at least n_q_heads head_dim, those of layers at least a layer.
  */
 #define TQ_MAX_AXES 4
 typedef struct {
@@ -502,13 +504,14 @@ typedef struct {
  * accumulation and softmax statistics); the ring's bf16 keys, values and
  * queries enter exactly, its weights rounded to bf16: the output is within
  * bf16's own precision of the exact sum.  Scales below 2^-24 of the largest
- * one of the same context split round to zero.  A row that sees no token is
+ * finite one of the same context split round to zero.  A row that sees no token is
  * zero; rows t >= T_b are not touched.  Slots and records that hold no token
- * are never read, and keys of tokens a query does not see do not touch its row,
- * whatever they hold; the VALUES of all tokens below total have to be finite
+ * are never read, and keys of tokens a query does not see do not touch its row
+ * in any other way, NaN and infinities included; the VALUES of all tokens below total have to be finite
  * (a weight of zero times an infinity is NaN, for a later query's token too).
  * The kernels bound every internal wait (about two seconds); if one expires (a
  * fault of the device, not of the arguments) the rows concerned are NaN.
+ * out may not overlap itself (strides as for q_out above).
  * workspace: device, 256-byte aligned; contents need no initialisation.
  * Calls that overlap on the GPU need workspaces of their own.
  */

@@ -463,6 +463,17 @@ def _ready(args, workspace=None):
     _need(workspace is None or workspace.get_device() == dev, "the workspace is on another device")
 
 
+def _scratch(size: int, device, stream):
+    """A workspace that belongs to the stream the call runs on: freed, it serves that stream only."""
+    import torch
+    if stream is None:
+        return torch.empty(size, dtype=torch.uint8, device=device)
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device) if stream else torch.cuda.default_stream(device)
+    with torch.cuda.stream(stream):
+        return torch.empty(size, dtype=torch.uint8, device=device)
+
+
 def _heads_packed(t, name: str, d: int):
     """(layer, batch, token) strides of a [L, B, T, heads, d] view whose heads and dims are packed."""
     _need(t.dim() == 5 and t.shape[4] == d and t.stride(4) == 1 and (t.shape[3] == 1 or t.stride(3) == d),
@@ -657,13 +668,12 @@ def tq_prefill_attn(args: tq_query_args, k_codec: Codec | None, v_codec: Codec |
 
 def prefill_attn(*, k_codec=None, v_codec=None, workspace=None, stream=None, **kw):
     """Convenience: build the arguments, size/allocate the workspace if not given, run."""
-    import torch
     _check_records(k_codec, kw.get("k_rec"), "k_rec")
     _check_records(v_codec, kw.get("v_rec"), "v_rec")
     a = make_query_args(**kw)
     need = tq_prefill_attn_workspace_size(a, k_codec, v_codec)
     if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=kw["q"].device)
+        workspace = _scratch(need, kw["q"].device, stream)
     tq_prefill_attn(a, k_codec, v_codec, workspace, stream)
     return workspace
 
@@ -696,7 +706,7 @@ def attn_mass(*, mass, k_codec=None, decay: float = 1.0, workspace=None, stream=
     a = make_query_args(**kw)
     need = tq_attn_mass_workspace_size(a, k_codec)
     if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=kw["q"].device)
+        workspace = _scratch(need, kw["q"].device, stream)
     tq_attn_mass(a, k_codec, mass, workspace, decay, stream)
     return workspace
 
@@ -777,12 +787,11 @@ def tq_evict_mass(args: tq_evict_mass_args, k_codec: Codec, v_codec: Codec | Non
 
 def evict_mass(*, k_codec, v_codec=None, workspace=None, stream=None, **kw):
     """Convenience: build the arguments, size/allocate the workspace if not given, run."""
-    import torch
     _check_records(k_codec, kw["k_rec"], "k_rec")
     _check_records(v_codec, kw["v_rec"], "v_rec")
     a = make_evict_mass_args(**kw)
     need = tq_evict_mass_workspace_size(a, k_codec, v_codec)
     if workspace is None or workspace.numel() < need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=kw["k_rec"].device)
+        workspace = _scratch(need, kw["k_rec"].device, stream)
     tq_evict_mass(a, k_codec, v_codec, workspace, stream)
     return workspace

@@ -42,6 +42,14 @@ inline bool strides_ok(int64_t a, int64_t b, int64_t c) {
   return a >= 0 && b >= 0 && c >= 0 && a % 8 == 0 && b % 8 == 0 && c % 8 == 0;
 }
 
+// what a call writes must not overlap itself: along every axis longer than one
+// a step is at least a row of `row` elements
+inline bool rows_apart(int64_t ls, int64_t bs, int64_t ts, int L, int B, int T, int64_t row) {
+  return (L == 1 || ls >= row) && (B == 1 || bs >= row) && (T == 1 || ts >= row);
+}
+// nor one layer the next
+inline bool layers_apart(int L, int64_t ls, int64_t layer) { return L == 1 || ls >= layer; }
+
 // ----------------------------------------------------------------- append
 tq_status append_params(const tq_append_args* a, AppendParams* p) {
   if (!a) return TQ_ERR_INVALID_ARG;
@@ -67,6 +75,11 @@ tq_status append_params(const tq_append_args* a, AppendParams* p) {
       !strides_ok(a->q_out_layer_stride, a->q_out_batch_stride, a->q_out_token_stride) ||
       a->tail_layer_stride < 0 || a->tail_layer_stride % 8)
     return TQ_ERR_INVALID_ARG;
+  if (a->q && !rows_apart(a->q_out_layer_stride, a->q_out_batch_stride, a->q_out_token_stride, a->n_layers, a->batch,
+                          a->t_q, (int64_t)a->n_q_heads * d))
+    return TQ_ERR_INVALID_ARG;
+  if (!layers_apart(a->n_layers, a->tail_layer_stride, (int64_t)a->batch * a->n_kv_heads * a->tail_cap * d))
+    return TQ_ERR_INVALID_ARG;
   if (a->q_out == a->q && a->q &&
       (a->q_out_layer_stride != a->q_layer_stride || a->q_out_batch_stride != a->q_batch_stride ||
        a->q_out_token_stride != a->q_token_stride))
@@ -80,7 +93,9 @@ tq_status append_params(const tq_append_args* a, AppendParams* p) {
     for (int i = 0; i < a->rot_dim / 2; ++i)
       if (a->pair_axis[i] >= a->n_axes) return TQ_ERR_INVALID_ARG;
   }
-  if (a->mass && (a->mass_cap <= 0 || a->mass_layer_stride < 0)) return TQ_ERR_INVALID_ARG;
+  if (a->mass && (a->mass_cap <= 0 || a->mass_layer_stride < 0 ||
+                  !layers_apart(a->n_layers, a->mass_layer_stride, (int64_t)a->batch * a->n_kv_heads * a->mass_cap)))
+    return TQ_ERR_INVALID_ARG;
   p->L = a->n_layers;
   p->B = a->batch;
   p->T = a->t_q;
@@ -152,7 +167,9 @@ tq_status query_params(const tq_query_args* a, const tq_codec* kcod, const tq_co
   if (!a->q || !aligned(a->q, 16) || !strides_ok(a->q_layer_stride, a->q_batch_stride, a->q_token_stride))
     return TQ_ERR_INVALID_ARG;
   if (values && (!a->out || !aligned(a->out, 16) ||
-                 !strides_ok(a->out_layer_stride, a->out_batch_stride, a->out_token_stride)))
+                 !strides_ok(a->out_layer_stride, a->out_batch_stride, a->out_token_stride) ||
+                 !rows_apart(a->out_layer_stride, a->out_batch_stride, a->out_token_stride, a->n_layers, a->batch,
+                             a->t_q, (int64_t)a->n_q_heads * d)))
     return TQ_ERR_INVALID_ARG;
   if (!std::isfinite(a->scale) || !std::isfinite(a->softcap) || a->softcap < 0.f) return TQ_ERR_INVALID_ARG;
   if (a->max_chunks < 0 || a->max_tail < 0 || a->splits < 0) return TQ_ERR_INVALID_ARG;
@@ -428,11 +445,19 @@ tq_status evict_mass_params(const tq_evict_mass_args* a, const tq_codec* kcod, c
   if ((int64_t)a->sink + a->recent > (int64_t)TQ_CHUNK * a->keep_chunks) return TQ_ERR_INVALID_ARG;
   const int64_t most = (int64_t)TQ_CHUNK * a->max_chunks + a->max_tail;
   if (most > 0x7FFFFFFFll || (int64_t)TQ_CHUNK * a->keep_chunks > 0x7FFFFFFFll - a->max_tail) return TQ_ERR_UNSUPPORTED;
-  if (a->mass_cap < most || a->mass_layer_stride < 0) return TQ_ERR_INVALID_ARG;
+  if (a->mass_cap < most || a->mass_layer_stride < 0 ||
+      !layers_apart(a->n_layers, a->mass_layer_stride, (int64_t)a->batch * a->n_kv_heads * a->mass_cap))
+    return TQ_ERR_INVALID_ARG;
   const int kept = std::min(a->keep_chunks, std::max(a->max_chunks, 1));  // records that can remain
   if (!in_place) {
     if (a->dst_cap <= 0 || (a->dst_table && a->dst_table_stride <= 0) || a->k_dst_layer_stride % 16 ||
-        a->v_dst_layer_stride % 16 || a->mass_dst_layer_stride < 0)
+        a->v_dst_layer_stride % 16 || a->mass_dst_layer_stride < 0 ||
+        !layers_apart(a->n_layers, a->mass_dst_layer_stride, (int64_t)a->batch * a->n_kv_heads * a->mass_dst_cap))
+      return TQ_ERR_INVALID_ARG;
+    // a layer's records follow one another (pages: at least its destination's blocks are there)
+    const int64_t heads = (a->dst_table ? 1 : (int64_t)a->batch * a->dst_cap) * a->n_kv_heads;
+    if (!layers_apart(a->n_layers, a->k_dst_layer_stride, heads * p->kc.rec_bytes) ||
+        !layers_apart(a->n_layers, a->v_dst_layer_stride, heads * p->vc.rec_bytes))
       return TQ_ERR_INVALID_ARG;
     if ((a->dst_table ? a->dst_table_stride : a->dst_cap) < std::min(a->keep_chunks, a->max_chunks) ||
         a->mass_dst_cap < (int64_t)TQ_CHUNK * std::min(a->keep_chunks, a->max_chunks) + a->max_tail)
@@ -534,6 +559,7 @@ tq_status tq_attn_mass(const tq_query_args* a, const tq_codec* k_codec, float* m
   if (st != TQ_OK) return st;
   MassParams& mp = pl.mp;
   if (!mass || !aligned(mass, 4) || mass_layer_stride < 0 ||
+      !layers_apart(mp.q.L, mass_layer_stride, (int64_t)mp.q.B * mp.q.Hkv * mass_cap) ||
       mass_cap < (int64_t)TQ_CHUNK * mp.q.max_chunks + mp.q.max_tail || !std::isfinite(decay) || decay < 0.f)
     return TQ_ERR_INVALID_ARG;
   if (!workspace || !aligned(workspace, 256)) return TQ_ERR_INVALID_ARG;

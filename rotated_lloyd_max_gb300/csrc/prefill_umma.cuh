@@ -352,14 +352,15 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
     if (p.kc.bits == 4)
       for (int k = 8; k < 16; ++k) vtable = vtable && p.kc.centroids[k] == p.vc.centroids[k];  // tables are symmetric
   }
-  if constexpr (!DENSE) {  // the run's largest scales
+  if constexpr (!DENSE) {  // the run's largest finite scales (an infinite key may be one that no query here sees)
     float mk = 0.f, mv = 0.f;
+    auto mag = [](float x) { return fabsf(x) < INFINITY ? fabsf(x) : 0.f; };
     for (int i = tid; i < n * (kChunk / 4); i += kPfThreads) {
       const int c = c0 + i / (kChunk / 4), o = i % (kChunk / 4);
       const float4 x = __ldg(reinterpret_cast<const float4*>(rec_at(true, c) + p.kc.off_norm) + o);
       const float4 y = __ldg(reinterpret_cast<const float4*>(rec_at(false, c) + p.vc.off_norm) + o);
-      mk = fmaxf(mk, fmaxf(fmaxf(fabsf(x.x), fabsf(x.y)), fmaxf(fabsf(x.z), fabsf(x.w))));
-      mv = fmaxf(mv, fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w))));
+      mk = fmaxf(mk, fmaxf(fmaxf(mag(x.x), mag(x.y)), fmaxf(mag(x.z), mag(x.w))));
+      mv = fmaxf(mv, fmaxf(fmaxf(mag(y.x), mag(y.y)), fmaxf(mag(y.z), mag(y.w))));
     }
     mk = warp_max(mk);
     mv = warp_max(mv);

@@ -236,3 +236,25 @@ def test_binding_refuses_wrong_tensors(tq):
                 dict(dst_table=torch.zeros(2, 3, dtype=i32)), dict(mass=m.double())):
         with pytest.raises(ValueError):
             tq.make_evict_mass_args(**{**good, **bad})
+
+
+def test_outputs_that_overlap_themselves_are_refused(tq):
+    """Two rows, or two layers, of an output in the same place would be written in any order."""
+    L, kc, vc, ws = tq.load(), _codec(tq), _codec(tq, bits=2), ctypes.c_void_p(0x1000000)
+    for kw in (dict(q_out_token_stride=504), dict(q_out_batch_stride=0), dict(n_layers=2, q_out_layer_stride=256, tail_layer_stride=1 << 20),
+               dict(n_layers=2, q_out_layer_stride=4096, tail_layer_stride=2 * 2 * 64 * 128 - 8),
+               dict(n_layers=2, q_out_layer_stride=4096, tail_layer_stride=2 * 2 * 64 * 128, mass=0xB0000, mass_cap=9,
+                    mass_layer_stride=35)):
+        assert L.tq_append(ctypes.byref(_append(tq, **kw)), None) == INV
+    for kw in (dict(out_token_stride=0), dict(out_batch_stride=504), dict(n_layers=2)):
+        a = _query(tq, **kw)
+        assert L.tq_prefill_attn(ctypes.byref(a), ctypes.byref(kc), ctypes.byref(vc), ws, 1 << 40, None) == INV
+    a = _query(tq, n_layers=2, tail_layer_stride=1 << 20)
+    assert L.tq_attn_mass(ctypes.byref(a), ctypes.byref(kc), 0x2000000, 4 * 1088 - 1, 1088, 1.0, ws, 1 << 40, None) == INV
+    two = dict(n_layers=2, mass_layer_stride=4 * (8 * 128 + 16), mass_dst_layer_stride=4 * (4 * 128 + 16),
+               k_dst_layer_stride=1 << 20, v_dst_layer_stride=1 << 20)
+    assert L.tq_evict_mass_workspace_size(ctypes.byref(_evict(tq, **two)), ctypes.byref(kc), ctypes.byref(vc)) > 0
+    for kw in (dict(mass_layer_stride=4159), dict(mass_dst_layer_stride=2111), dict(k_dst_layer_stride=0),
+               dict(v_dst_layer_stride=4 * 4 * (128 * 128 * 2 // 8 + 512) - 16)):
+        a = _evict(tq, **dict(two, **kw))
+        assert L.tq_evict_mass(ctypes.byref(a), ctypes.byref(kc), ctypes.byref(vc), ws, 1 << 40, None) == INV

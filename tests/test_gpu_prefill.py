@@ -215,3 +215,60 @@ def test_growing_logits_move_the_reference(tq, orc):
         for i in range(4):
             want = weights(qf[0, 0, :, i], k, 7, 6 * 128 + 9, True, 0.0, 1.0) @ v
             assert np.linalg.norm(got[0, 0, :, i] - want) <= 2.0 ** -5 * np.linalg.norm(want)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_scales_of_records_a_query_does_not_see_may_be_infinite(tq, orc, d):
+    """The newest tokens already lie in records (no ring): the last one's key scale is infinite or NaN."""
+    import torch
+    c = Cache(tq, orc, B=1, Hkv=2, d=d, kb=3, vb=3, n=3, tail=0, seed=17)
+    q = queries(1, 1, 9, 6, d, 18)
+    clean = _run(tq, c, q, None, 3)
+    for bad in (math.inf, math.nan):
+        off = 128 * d * 3 // 8 + 4 * 127
+        c.rec["k"][0, 0, :, 2, off:off + 4] = torch.tensor([bad], device="cuda").view(torch.uint8)
+        out = _run(tq, c, q, None, 3)
+        assert torch.equal(out[0, 0, :8], clean[0, 0, :8])
+
+
+def test_two_calls_at_once(tq, orc):
+    """Two streams, a workspace each, the same cache: both come out as they do alone."""
+    import torch
+    c = Cache(tq, orc, B=2, Hkv=2, d=128, kb=4, vb=4, n=20, tail=90, seed=19)
+    qs = [tl.to_bf16_tensor(queries(1, 2, t, 8, 128, 20 + t), "cuda") for t in (40, 3)]
+    mk = lambda i, out: tq.make_query_args(q=qs[i], out=out, scale=1.0, **c.kw())  # noqa: E731
+    alone = []
+    for i in (0, 1):
+        alone.append(torch.zeros_like(qs[i]))
+        tq.prefill_attn(k_codec=c.kc, v_codec=c.vc, q=qs[i], out=alone[i], scale=1.0, **c.kw())
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in (0, 1)]
+    both = [torch.zeros_like(x) for x in qs]
+    args = [mk(i, both[i]) for i in (0, 1)]
+    ws = [torch.empty(max(tq.tq_prefill_attn_workspace_size(args[i], c.kc, c.vc), 256), dtype=torch.uint8, device="cuda")
+          for i in (0, 1)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for i in (0, 1):
+            with torch.cuda.stream(streams[i]):
+                tq.tq_prefill_attn(args[i], c.kc, c.vc, ws[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(both[i], alone[i]) for i in (0, 1))
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_dropped_workspace_is_not_handed_out_under_the_call(tq, orc, raw):
+    """A call queued on a busy side stream; its workspace is dropped and memory of its size is filled meanwhile."""
+    import torch
+    c = Cache(tq, orc, B=1, Hkv=2, d=128, kb=4, vb=4, n=16, tail=10, seed=23)
+    q = tl.to_bf16_tensor(queries(1, 1, 30, 8, 128, 24), "cuda")
+    ref, out = torch.zeros_like(q), torch.zeros_like(q)
+    need = tq.prefill_attn(k_codec=c.kc, v_codec=c.vc, q=q, out=ref, scale=1.0, **c.kw()).numel()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    tq.prefill_attn(k_codec=c.kc, v_codec=c.vc, q=q, out=out, scale=1.0, stream=side.cuda_stream if raw else side, **c.kw())
+    junk = [torch.full((need,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref) and len(junk) == 4
