@@ -186,7 +186,9 @@ EVICT_WINDOW, EVICT_MARGIN, EVICT_TQ = 128, 16, 1
 # Captured at commit 54b393f (profiles/phase_traffic.md): small cases
 # (batched --layers 2, V4-Flash-like --layers 8, long context --layers 1,
 # Qwen2-shaped in full), mean over the captured steps, scaled by layers.
-_T = {"tq_encode": "cf493c19144d20f9", "tq_evict": "cb3934c670ca7e8f", "tq_decode_attn": "4990717f4be6d7ec"}
+# Since then abi.cu alone has changed among these sources: three host functions
+# shared with abi_cache.cu; no kernel, launch or plan of the phases.
+_T = {"tq_encode": "4c8a5c91f9ff5e29", "tq_evict": "d1da79bf8cf8b1cf", "tq_decode_attn": "2cac18791acdf967"}
 MEASURED_TRAFFIC: dict = {
     ("batched_b32_ctx32768", "tq_encode"): {"bytes": 181_461_894_758, "sources": _T["tq_encode"]},
     ("batched_b32_ctx32768", "tq_evict"): {"bytes": 538_411_827, "sources": _T["tq_evict"]},

@@ -76,6 +76,29 @@ struct PfMisc {
 };
 static_assert(sizeof(PfMisc) <= 1024, "bookkeeping block");
 
+// mbar_wait for warps that mostly wait: the thread is suspended (for at
+// most about a tenth of a millisecond a time) instead of polling, which leaves the issue
+// slots to the warps that work.
+__device__ __forceinline__ bool mbar_wait_idle(uint64_t* b, uint32_t parity, volatile int* abort) {
+  const uint32_t a = smem_u32(b);
+  if (mbar_try(a, parity)) return true;
+  const uint64_t t0 = global_ns();
+  for (;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(a), "r"(parity), "r"(100000u)
+        : "memory");
+    if (ok) return true;
+    if (*abort) return false;
+    if (global_ns() - t0 > 2000000000ull) {
+      *abort = 1;
+      return false;
+    }
+  }
+}
+
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
