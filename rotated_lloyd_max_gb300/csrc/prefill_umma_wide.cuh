@@ -15,6 +15,13 @@
 // sixteen warps in groups of four, a group a chunk.  Where keys and values share
 // a record (or ring), a chunk serves the scores and, kept, the outputs, so that
 // it is decoded once; otherwise the keys' chunks and the values' follow one another.
+// A chunk is decoded into registers before its slot is waited for (64 tokens of
+// 64 heads over 16384, head dim 512: 357 us, 377 decoding into the slot).
+//
+// Bound by shared memory: 128 tokens at head dim 512 take 640 KB of its traffic (two
+// products of 192 KB, since an MMA of N = 64 reads 6 KB; 128 KB of tiles
+// written; 128 KB of lookups), 5000 of the 9000 cycles measured; the ring holds
+// one such tile, so the decoding of the next runs behind the products of this one.
 #pragma once
 
 #include "prefill_umma.cuh"
@@ -111,34 +118,30 @@ __device__ __forceinline__ void half_planes(uint32_t sel, const Planes& pl, uint
 // 64 e + 4 (lane % 16)), half through the planes: the lookups alone queue for
 // shared memory (two lanes meet in a bank), the planes alone for the ALUs.
 template <int B, bool LUT>
-__device__ __forceinline__ void store_chunk(const Chunk& k, const Planes& pl, const unsigned char* lut,
-                                            unsigned char* st, int w, int lane) {
+__device__ __forceinline__ void decode_chunk(const Chunk& k, const Planes& pl, const unsigned char* lut, uint4 (&v)[8],
+                                             int lane) {
   const uint32_t lo = 4 * (lane & 15);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const int row = 4 * i + (lane >> 3);
-    uint4 v;
     if constexpr (LUT) {
       const uint32_t x = k.x[i];
-      v.x = *reinterpret_cast<const uint32_t*>(lut + (((x << 6) & 0x3FC0u) | lo));
-      v.y = *reinterpret_cast<const uint32_t*>(lut + (((x >> 2) & 0x3FC0u) | lo));
-      half_planes(x >> 16, pl, v.z, v.w);
+      v[i].x = *reinterpret_cast<const uint32_t*>(lut + (((x << 6) & 0x3FC0u) | lo));
+      v[i].y = *reinterpret_cast<const uint32_t*>(lut + (((x >> 2) & 0x3FC0u) | lo));
+      half_planes(x >> 16, pl, v[i].z, v[i].w);
     } else {
-      v = decode_codes<B>(k.x[i], pl);
+      v[i] = decode_codes<B>(k.x[i], pl);
     }
-    *reinterpret_cast<uint4*>(st + sw128_off(32 * w + row, lane & 7)) = v;
   }
 }
-
-__device__ __forceinline__ void store_chunk_b(int bits, const Chunk& k, const Planes& pl, const unsigned char* lut,
-                                              unsigned char* st, int w, int lane) {
+__device__ __forceinline__ void decode_chunk_b(int bits, const Chunk& k, const Planes& pl, const unsigned char* lut,
+                                               uint4 (&v)[8], int lane) {
   switch (bits) {
-    case 1: store_chunk<1, false>(k, pl, lut, st, w, lane); break;
-    case 2: store_chunk<2, false>(k, pl, lut, st, w, lane); break;
-    case 3: store_chunk<3, false>(k, pl, lut, st, w, lane); break;
+    case 1: decode_chunk<1, false>(k, pl, lut, v, lane); break;
+    case 2: decode_chunk<2, false>(k, pl, lut, v, lane); break;
+    case 3: decode_chunk<3, false>(k, pl, lut, v, lane); break;
     default:
-      if (lut) store_chunk<4, true>(k, pl, lut, st, w, lane);
-      else store_chunk<4, false>(k, pl, lut, st, w, lane);
+      if (lut) decode_chunk<4, true>(k, pl, lut, v, lane);
+      else decode_chunk<4, false>(k, pl, lut, v, lane);
   }
 }
 // side list entries of chunk c's coordinates, a lane a token
@@ -382,40 +385,44 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
         load_chunk_b<D>(kbits, krec + kat + 32 * x * kbits, kx[x]);
         if (!one) load_chunk_b<D>(vbits, vrec + vat + 32 * x * vbits, vx[x]);
       }
+      // a chunk is decoded before its slot is waited for
       uint32_t q = grp;
-      auto hand_over = [&](uint32_t s) {
+      uint4 v[8];
+      auto put = [&](const CodecDev& cd, const uint8_t* rec, int x) {
+        const uint32_t s = q % kPwSlots;
+        mbar_wait_idle(&ms.empty[s], ((q / kPwSlots) & 1) ^ 1, abort_f);
+        unsigned char* st = sm + C::RING + s * 16384;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) *reinterpret_cast<uint4*>(st + sw128_off(32 * w + 4 * k + (lane >> 3), lane & 7)) = v[k];
+        if (cd.has_outl) patch_chunk<D>(cd, rec, grp + 4 * x, st, w, lane);
         fence_async_smem();  // before the next loads, which it would wait for
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.full[s]);
         q += 4;
       };
+      decode_chunk_b(kbits, kx[0], kpl, klut, v, lane);
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
         const bool more = i + 1 < n;
         const uint8_t* knext = more ? rec_at(true, c0 + i + 1) : krec;
+        const uint8_t* vnext = one || !more ? vrec : rec_at(false, c0 + i + 1);
 #pragma unroll
         for (int x = 0; x < PER; ++x) {
-          const uint32_t s = q % kPwSlots;
-          mbar_wait_idle(&ms.empty[s], ((q / kPwSlots) & 1) ^ 1, abort_f);
-          unsigned char* st = sm + C::RING + s * 16384;
-          store_chunk_b(kbits, kx[x], kpl, klut, st, w, lane);
-          if (p.kc.has_outl) patch_chunk<D>(p.kc, krec, grp + 4 * x, st, w, lane);
-          hand_over(s);
+          put(p.kc, krec, x);
           if (more) load_chunk_b<D>(kbits, knext + kat + 32 * x * kbits, kx[x]);
+          if (x + 1 < PER) decode_chunk_b(kbits, kx[x + 1 < PER ? x + 1 : 0], kpl, klut, v, lane);
         }
-        krec = knext;
-        if (one) continue;
-        const uint8_t* vnext = more ? rec_at(false, c0 + i + 1) : vrec;
+        if (!one) {
+          decode_chunk_b(vbits, vx[0], vpl, vlut, v, lane);
 #pragma unroll
-        for (int x = 0; x < PER; ++x) {
-          const uint32_t s = q % kPwSlots;
-          mbar_wait_idle(&ms.empty[s], ((q / kPwSlots) & 1) ^ 1, abort_f);
-          unsigned char* st = sm + C::RING + s * 16384;
-          store_chunk_b(vbits, vx[x], vpl, vlut, st, w, lane);
-          if (p.vc.has_outl) patch_chunk<D>(p.vc, vrec, grp + 4 * x, st, w, lane);
-          hand_over(s);
-          if (more) load_chunk_b<D>(vbits, vnext + vat + 32 * x * vbits, vx[x]);
+          for (int x = 0; x < PER; ++x) {
+            put(p.vc, vrec, x);
+            if (more) load_chunk_b<D>(vbits, vnext + vat + 32 * x * vbits, vx[x]);
+            if (x + 1 < PER) decode_chunk_b(vbits, vx[x + 1 < PER ? x + 1 : 0], vpl, vlut, v, lane);
+          }
         }
+        if (more) decode_chunk_b(kbits, kx[0], kpl, klut, v, lane);
+        krec = knext;
         vrec = vnext;
       }
     }
