@@ -77,6 +77,14 @@ __device__ __forceinline__ int row_limit(const QueryParams& p, const CacheLen& c
   return t >= tb ? 0 : p.causal ? min(c.total, c.total - tb + t + 1) : c.total;
 }
 
+// the table's entry (f16 pairs hi, lo) for codes at and at + 1 of a run's words
+template <int KB, int NW>
+__device__ __forceinline__ uint2 pair_at(const ByteTable& tab, const unsigned char* table, const uint32_t (&w)[NW], int at,
+                                         uint32_t loff) {
+  if constexpr (KB == 4) return byte_lookup2(tab, w[at / 8], at % 8 / 2);
+  else return *reinterpret_cast<const uint2*>(table + pair_off(w, at * KB, 2 * KB, loff));
+}
+
 template <int NT>
 struct MassMisc {
   float qsc[8 * NT];      // score scale of a row
@@ -143,6 +151,7 @@ __global__ void __launch_bounds__(kThreads) attn_mass_kernel(const __grid_consta
   const uint16_t* ring = p.ktail + l * p.tail_ls + (int64_t)(b * p.Hkv + h) * cap * D;
   const int rstart = dense && p.tail_start ? ((p.tail_start[lb] % cap) + cap) % cap : 0;
   const uint32_t loff = (lane & 15) * 8;
+  const ByteTable tab = byte_table(sm, loff, 128);
 
   if (!dense) {  // pair table: entry e at byte 128 e + 8 (lane % 16): f16 pairs hi, lo of centroids x 2^16
     if (tid < 16) {
@@ -302,8 +311,7 @@ __global__ void __launch_bounds__(kThreads) attn_mass_kernel(const __grid_consta
             for (int i = 0; i < 4; ++i)
 #pragma unroll
               for (int e = 0; e < 2; ++e) {
-                const uint2 v =
-                    *reinterpret_cast<const uint2*>(sm + pair_off(w[i], (4 * k + 2 * e) * KB, 2 * KB, loff));
+                const uint2 v = pair_at<KB>(tab, sm, w[i], 4 * k + 2 * e, loff);
                 ah[i >> 1][(i & 1) + 2 * e] = v.x;
                 al[i >> 1][(i & 1) + 2 * e] = v.y;
               }

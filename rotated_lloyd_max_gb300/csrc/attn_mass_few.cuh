@@ -67,6 +67,7 @@ __global__ void __launch_bounds__(kThreads) attn_mass_few_kernel(const __grid_co
   const uint16_t* ring = p.ktail + l * p.tail_ls + (int64_t)(b * p.Hkv + h) * cap * D;
   const int rstart = dense && p.tail_start ? ((p.tail_start[lb] % cap) + cap) % cap : 0;
   const uint32_t loff = (lane & 15) * 8;
+  const ByteTable tab = byte_table(sm, loff, 128);
   // the lane's token rows of a record, and the words of one run piece
   const int off0 = (32 * warp + g) * row_bytes;
   auto rec_at = [&](int c) {
@@ -195,7 +196,7 @@ __global__ void __launch_bounds__(kThreads) attn_mass_few_kernel(const __grid_co
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              const uint2 v = *reinterpret_cast<const uint2*>(sm + pair_off(w[i], (4 * k + 2 * e) * KB, 2 * KB, loff));
+              const uint2 v = pair_at<KB>(tab, sm, w[i], 4 * k + 2 * e, loff);
               ah[i >> 1][(i & 1) + 2 * e] = v.x;
               al[i >> 1][(i & 1) + 2 * e] = v.y;
             }

@@ -49,12 +49,17 @@ static_assert(sizeof(MuMisc) <= 11264 && offsetof(MuMisc, nk) % 16 == 0 && offse
 template <int B>
 __device__ __forceinline__ void lookup8(const unsigned char* lut, uint32_t x, uint32_t lo, uint4& vh, uint4& vl) {
   constexpr uint32_t M = ((1u << (2 * B)) - 1u) << 7;
+  const ByteTable tab = byte_table(lut, lo, 128);
   uint2 e[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const int sh = 2 * B * k;
-    const uint32_t o = ((sh >= 7 ? x >> (sh - 7) : x << (7 - sh)) & M) | lo;
-    e[k] = *reinterpret_cast<const uint2*>(lut + o);
+    if constexpr (B == 4) {
+      e[k] = byte_lookup2(tab, x, k);
+    } else {
+      const int sh = 2 * B * k;
+      const uint32_t o = ((sh >= 7 ? x >> (sh - 7) : x << (7 - sh)) & M) | lo;
+      e[k] = *reinterpret_cast<const uint2*>(lut + o);
+    }
   }
   vh = make_uint4(e[0].x, e[1].x, e[2].x, e[3].x);
   vl = make_uint4(e[0].y, e[1].y, e[2].y, e[3].y);

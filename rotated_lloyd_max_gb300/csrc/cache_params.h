@@ -106,6 +106,33 @@ cudaError_t launch_evict_mass(const EvictMassParams& p, cudaStream_t s);
 __device__ __forceinline__ void pdl_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// Lookup of a byte (two 4-bit codes) in a shared-memory table.  The entry's
+// address is one byte extraction and one multiply-add, whose factor sits in a
+// register that the compiler does not see through: shift, mask and sum in its
+// place would take three operations of the ALU pipe, which the decoding fills.
+struct ByteTable {
+  uint32_t at, step;  // the lane's copy of entry 0; bytes from entry to entry
+};
+__device__ __forceinline__ ByteTable byte_table(const void* table, uint32_t lane_off, uint32_t step) {
+  ByteTable t;
+  t.at = (uint32_t)__cvta_generic_to_shared(table) + lane_off;
+  asm volatile("mov.u32 %0, %1;" : "=r"(t.step) : "r"(step));
+  return t;
+}
+__device__ __forceinline__ uint32_t byte_entry(const ByteTable& t, uint32_t x, int k) {
+  return __byte_perm(x, 0, 0x4440 + k) * t.step + t.at;
+}
+__device__ __forceinline__ uint32_t byte_lookup(const ByteTable& t, uint32_t x, int k) {
+  uint32_t r;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(r) : "r"(byte_entry(t, x, k)));
+  return r;
+}
+__device__ __forceinline__ uint2 byte_lookup2(const ByteTable& t, uint32_t x, int k) {
+  uint2 r;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(byte_entry(t, x, k)));
+  return r;
+}
+
 template <class... Args>
 inline cudaError_t launch_after(void (*kern)(Args...), dim3 grid, int block, int smem, cudaStream_t s, int cluster,
                                 const Args&... args) {

@@ -214,7 +214,7 @@ __device__ __forceinline__ void store_decoded(const Packed<D>& k, float n, const
   const float lead = __half2float(__float2half_rn(n));
   const uint32_t n2 = pack2_f16(n, KEYS ? n - lead : n);
   st += w * kPfTok * 128;
-  const uint32_t lo = 4 * lane;
+  const ByteTable tab = byte_table(lut, 4 * lane, 128);
 #pragma unroll
   for (int i = 0; i < P::PER; ++i) {
     const int row = (lane + 32 * i) / P::CH, ch = (lane + 32 * i) % P::CH;
@@ -223,10 +223,7 @@ __device__ __forceinline__ void store_decoded(const Packed<D>& k, float n, const
     uint4 v;
     if constexpr (LUT) {
       const uint32_t x = k.x[i];
-      v.x = *reinterpret_cast<const uint32_t*>(lut + (((x << 7) & 0x7F80u) | lo));
-      v.y = *reinterpret_cast<const uint32_t*>(lut + (((x >> 1) & 0x7F80u) | lo));
-      v.z = *reinterpret_cast<const uint32_t*>(lut + (((x >> 9) & 0x7F80u) | lo));
-      v.w = *reinterpret_cast<const uint32_t*>(lut + (((x >> 17) & 0x7F80u) | lo));
+      v = make_uint4(byte_lookup(tab, x, 0), byte_lookup(tab, x, 1), byte_lookup(tab, x, 2), byte_lookup(tab, x, 3));
     } else {
       v = decode_codes<B>(k.x[i], pl);
     }

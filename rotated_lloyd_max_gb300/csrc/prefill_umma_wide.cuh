@@ -120,13 +120,13 @@ __device__ __forceinline__ void half_planes(uint32_t sel, const Planes& pl, uint
 template <int B, bool LUT>
 __device__ __forceinline__ void decode_chunk(const Chunk& k, const Planes& pl, const unsigned char* lut, uint4 (&v)[8],
                                              int lane) {
-  const uint32_t lo = 4 * (lane & 15);
+  const ByteTable tab = byte_table(lut, 4 * (lane & 15), 64);
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     if constexpr (LUT) {
       const uint32_t x = k.x[i];
-      v[i].x = *reinterpret_cast<const uint32_t*>(lut + (((x << 6) & 0x3FC0u) | lo));
-      v[i].y = *reinterpret_cast<const uint32_t*>(lut + (((x >> 2) & 0x3FC0u) | lo));
+      v[i].x = byte_lookup(tab, x, 0);
+      v[i].y = byte_lookup(tab, x, 1);
       half_planes(x >> 16, pl, v[i].z, v[i].w);
     } else {
       v[i] = decode_codes<B>(k.x[i], pl);
