@@ -10,6 +10,8 @@
 // bytes; the words of the next 32 codes are loaded while this run's are
 // multiplied.  At most four rows share one MMA between their hi and lo parts
 // (columns r and r + 4), two MMAs a k-step instead of three.
+// Five CTAs per SM (a few spilled words; 32 sequences of 32768 tokens, 8 kv heads
+// of 4 query heads: both passes 294 us, four CTAs 305, six 312).
 // Second pass (attn_mass_add_kernel): a thread per token turns its logits into
 // weights with the rows' log-sums and adds them to the mass.
 #pragma once
@@ -31,7 +33,7 @@ __device__ __forceinline__ int64_t few_columns(const MassParams& mp) {
 }
 
 template <int D, int KB, bool OUTL>
-__global__ void __launch_bounds__(kThreads) attn_mass_few_kernel(const __grid_constant__ MassParams mp) {
+__global__ void __launch_bounds__(kThreads, 5) attn_mass_few_kernel(const __grid_constant__ MassParams mp) {
   constexpr int KS = D / 16, RUN = D / 4;
   constexpr int STEP = RUN < 32 ? RUN : 32, NS = RUN / STEP;  // codes of a run taken at a time, such pieces
   constexpr int NB = STEP * KB, NW = (NB + 31) / 32;

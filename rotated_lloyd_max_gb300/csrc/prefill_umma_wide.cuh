@@ -16,7 +16,7 @@
 // a record (or ring), a chunk serves the scores and, kept, the outputs, so that
 // it is decoded once; otherwise the keys' chunks and the values' follow one another.
 // A chunk is decoded into registers before its slot is waited for (64 tokens of
-// 64 heads over 16384, head dim 512: 357 us, 377 decoding into the slot).
+// 64 heads over 16384, head dim 512: 353 us; 5% more when it decodes into the slot).
 //
 // Bound by shared memory: 128 tokens at head dim 512 take 640 KB of its traffic (two
 // products of 192 KB, since an MMA of N = 64 reads 6 KB; 128 KB of tiles
