@@ -70,4 +70,28 @@ __device__ __forceinline__ uint32_t pack2_bf16(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// The soft cap of a logit in log2 units, C tanh(t / C) = C - 2 C / (1 + 2^(t k)),
+// k = 2 log2(e) / C: off by at most 2^-21 C (about half an ulp of each of 2^x, the
+// sum and the quotient), under 2^-13 for C up to 256, where a weight keeps 11
+// bits.  Larger caps go through tanhf.  (1024 tokens over 32768 cached with a cap
+// of 20: 970 us, 3085 through tanhf; without a cap 559.)
+struct SoftCap {
+  float k, c, m2c, ic;
+  bool large;
+};
+__device__ __forceinline__ SoftCap make_cap(float C, float iC) {
+  return SoftCap{2.885390081777927f * iC, C, -2.f * C, iC, C > 256.f};
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float cap_near(float t, const SoftCap& s) {
+  return fmaf(s.m2c, rcp_approx(1.f + ex2(t * s.k)), s.c);
+}
+__device__ __forceinline__ float cap_logit(float t, const SoftCap& s) {
+  return s.large ? soft_cap(t, s.c, s.ic) : cap_near(t, s);
+}
+
 }  // namespace tq

@@ -35,9 +35,9 @@
 // The rotation of the queries is a product with the signed Hadamard matrix
 // (+-1, exact in bf16, as the queries are), one more MMA per tile.
 //
-// Measured: 1024 tokens of 32 heads over 32768 + 1280 (4 bits, head dim 128) 547 us,
-// 1.03 PFLOP/s; bound by the chain softmax -> weights -> MMA of the two tiles and
-// by the ALU pipe, which the decoding fills (lookups by shift and mask: 594 us).
+// Measured: 1024 tokens of 32 heads over 32768 + 1280 (4 bits, head dim 128) 559 us,
+// 1.01 PFLOP/s; bound by the chain softmax -> weights -> MMA of the two tiles and
+// by the ALU pipe, which the decoding fills (lookups by shift and mask took 9% longer).
 //
 // Partials lie as [128-row tile][split][D / 4][128 rows][4], so that the
 // thread that owns a row writes 16 bytes beside its neighbours'.
@@ -318,7 +318,8 @@ __device__ __forceinline__ void decode_tile(const CodecDev& c, const uint8_t* re
     });
 }
 
-template <int D, bool DENSE>
+// CAP: the call caps its logits (a kernel of its own: the branch cost registers).
+template <int D, bool DENSE, bool CAP>
 __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsigned char* sm, int64_t unit, int tile,
                                                   int split) {
   using C = PfCfg<D>;
@@ -623,6 +624,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
     // tokens it sees, counted from the run's first; rows of no query see everything
     const int lim = r < rn ? row_limit(p, cl, tb, r0 + r) - base - k0 : 0x7FFFFFFF;
     float mref = -INFINITY, lsum = 0.f;
+    const SoftCap cap = make_cap(p.scap, p.iscap);
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
       mbar_wait_idle(&ms.s_full[t], i & 1, abort_f);
@@ -632,10 +634,11 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
       uint32_t w[64];  // weights as pairs; chunk c of S becomes columns 16 c .. 16 c + 15
       float mx = -INFINITY;
       float2 sum = f2(0.f, 0.f);
-      bool again = edge || mref == -INFINITY || p.scap > 0.f;
+      bool again = edge || mref == -INFINITY || (CAP && cap.large);
       if (!__any_sync(0xffffffffu, again)) {
         // weights against the reference as it stands; the maximum is found on the way
-        const float2 f2v = f2(f, f), m2 = f2(-mref, -mref);
+        const float fk = CAP ? f * cap.k : f, m0 = CAP ? cap.c - mref : -mref;
+        const float2 f2v = f2(fk, fk), m2 = f2(m0, m0);
         float x0 = -INFINITY;
         uint32_t a[2][16];
         tmem_ld16(tS, a[0]);
@@ -645,7 +648,14 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
           if (c < 7) tmem_ld16(tS + 16 * (c + 1), a[(c + 1) & 1]);
 #pragma unroll
           for (int j = 0; j < 16; j += 2) {
-            float2 v = fma2(f2(__uint_as_float(a[c & 1][j]), __uint_as_float(a[c & 1][j + 1])), f2v, m2);
+            float2 v = f2(__uint_as_float(a[c & 1][j]), __uint_as_float(a[c & 1][j + 1]));
+            if constexpr (CAP) {
+              v = mul2(v, f2v);
+              v = add2(f2(ex2(v.x), ex2(v.y)), f2(1.f, 1.f));
+              v = fma2(f2(rcp_approx(v.x), rcp_approx(v.y)), f2(cap.m2c, cap.m2c), m2);
+            } else {
+              v = fma2(v, f2v, m2);
+            }
             x0 = max3(x0, v.x, v.y);
             v = f2(ex2(v.x), ex2(v.y));
             sum = add2(sum, v);
@@ -668,7 +678,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
           for (int j = 0; j < 16; ++j) mx = fmaxf(mx, 16 * c + j < seen ? __uint_as_float(a[j]) : -INFINITY);
         }
         float tm = mx > -INFINITY ? mx * f : -INFINITY;
-        if (p.scap > 0.f) tm = soft_cap(tm, p.scap, p.iscap);
+        if (CAP && mx > -INFINITY) tm = cap_logit(tm, cap);
         if (__any_sync(0xffffffffu, tm > mref + kPfMargin)) {
           const float mn = tm > mref + kPfMargin ? tm + kPfAbove : mref;
           const float al = mref > -INFINITY ? ex2(mref - mn) : 0.f;  // 1 where the reference stays
@@ -688,15 +698,21 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
           }
         }
         const float ref = mref > -INFINITY ? mref : 0.f;
+        const int top = __reduce_max_sync(0xffffffffu, seen);  // columns that some row of the warp sees
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
+          if (16 * c >= top) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w[8 * c + j] = 0u;
+            continue;
+          }
           uint32_t a[16];
           tmem_ld16(tS + 16 * c, a);
           tmem_ld_wait();
 #pragma unroll
           for (int j = 0; j < 16; j += 2) {
             float2 v = f2(__uint_as_float(a[j]) * f, __uint_as_float(a[j + 1]) * f);
-            if (p.scap > 0.f) v = f2(soft_cap(v.x, p.scap, p.iscap), soft_cap(v.y, p.scap, p.iscap));
+            if constexpr (CAP) v = f2(cap_logit(v.x, cap), cap_logit(v.y, cap));
             v = f2(16 * c + j < seen ? ex2(v.x - ref) : 0.f, 16 * c + j + 1 < seen ? ex2(v.y - ref) : 0.f);
             sum = add2(sum, v);
             w[8 * c + j / 2] = DENSE ? pack2_bf16(v.x, v.y) : pack2_f16(v.x, v.y);
@@ -751,7 +767,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
   }
 }
 
-template <int D>
+template <int D, bool CAP>
 __global__ void __launch_bounds__(kPfThreads, 1) prefill_umma_kernel(const __grid_constant__ PrefillParams pp) {
   pdl_start();
   extern __shared__ __align__(1024) unsigned char smraw[];
@@ -760,21 +776,22 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_umma_kernel(const __gri
   const int64_t U = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv * pp.tiles;
   const int split = (int)(blockIdx.x / U), tile = (int)(blockIdx.x % U % pp.tiles);
   const int64_t unit = blockIdx.x % U / pp.tiles;
-  if (split < pp.Sc) prefill_umma_body<D, false>(pp, sm, unit, tile, split);
-  else prefill_umma_body<D, true>(pp, sm, unit, tile, split - pp.Sc);
+  if (split < pp.Sc) prefill_umma_body<D, false, CAP>(pp, sm, unit, tile, split);
+  else prefill_umma_body<D, true, CAP>(pp, sm, unit, tile, split - pp.Sc);
 }
 
 template <int D>
 cudaError_t prefill_umma_launch(const PrefillParams& pp, cudaStream_t s) {
   if (pp.Sc + pp.St == 0) return cudaSuccess;
-  cudaError_t e = cudaFuncSetAttribute(prefill_umma_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PfCfg<D>::SMEM);
+  auto kern = pp.q.scap > 0.f ? prefill_umma_kernel<D, true> : prefill_umma_kernel<D, false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PfCfg<D>::SMEM);
   if (e != cudaSuccess) return e;
   // the split of the registers counts on this many at launch
   cudaFuncAttributes fa;
-  if ((e = cudaFuncGetAttributes(&fa, prefill_umma_kernel<D>)) != cudaSuccess) return e;
+  if ((e = cudaFuncGetAttributes(&fa, kern)) != cudaSuccess) return e;
   if (fa.numRegs != kPfLaunchRegs) return cudaErrorInvalidConfiguration;
   const int64_t grid = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv * pp.tiles * (pp.Sc + pp.St);
-  prefill_umma_kernel<D><<<(unsigned)grid, kPfThreads, PfCfg<D>::SMEM, s>>>(pp);
+  kern<<<(unsigned)grid, kPfThreads, PfCfg<D>::SMEM, s>>>(pp);
   return cudaGetLastError();
 }
 

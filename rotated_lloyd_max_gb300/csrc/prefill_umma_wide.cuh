@@ -433,6 +433,8 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
     int low = min(ms.lim[lane], ms.lim[32 + lane]);
 #pragma unroll
     for (int m = 16; m; m >>= 1) low = min(low, __shfl_xor_sync(0xffffffffu, low, m));
+    const SoftCap cap = make_cap(p.scap, p.iscap);
+    const bool capped = p.scap > 0.f;
     float lacc[2] = {0.f, 0.f};  // sums of rows lane and 32 + lane over this warp's tokens
     auto scale_at = [&](bool key, int i) {
       if constexpr (DENSE) return 1.f;
@@ -463,9 +465,9 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
           t[j + 2] = __uint_as_float(a[j + 2]) * nk * f.z;
           t[j + 3] = __uint_as_float(a[j + 3]) * nk * f.w;
         }
-        if (p.scap > 0.f) {
+        if (capped) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) t[j] = soft_cap(t[j], p.scap, p.iscap);
+          for (int j = 0; j < 32; ++j) t[j] = cap_logit(t[j], cap);
         }
         if (edge) {
 #pragma unroll
@@ -488,8 +490,8 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
         *reinterpret_cast<uint4*>(sm + C::P + sw128_off(tok, 4 * hh + j / 8)) = make_uint4(u[0], u[1], u[2], u[3]);
       };
       float over = -INFINITY;
-      const bool plain = !edge && !(p.scap > 0.f);
-      if (plain) {
+      const bool plain = !edge && !cap.large;
+      if (plain && !capped) {
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           uint32_t a[32];
@@ -506,6 +508,31 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
               const float2 B = mul2(f2(__uint_as_float(a[j + 2 * k + 2]), __uint_as_float(a[j + 2 * k + 3])), f2(nk, nk));
               x[k] = fma2(A, f2(f.x, f.y), f2(-r.x, -r.y));
               x[k + 1] = fma2(B, f2(f.z, f.w), f2(-r.z, -r.w));
+              over = max3(max3(over, x[k].x, x[k].y), x[k + 1].x, x[k + 1].y);
+              x[k] = f2(ex2(x[k].x), ex2(x[k].y));
+              x[k + 1] = f2(ex2(x[k + 1].x), ex2(x[k + 1].y));
+            }
+            put(hh, j, x);
+          }
+        }
+      } else if (plain) {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+          uint32_t a[32];
+          tmem_ld32(tS + lrow + 32 * hh, a);
+          tmem_ld_wait();
+#pragma unroll
+          for (int j = 0; j < 32; j += 8) {
+            float2 x[4];
+#pragma unroll
+            for (int k = 0; k < 4; k += 2) {
+              const float4 f = *reinterpret_cast<const float4*>(&ms.qf[32 * hh + j + 2 * k]);
+              const float4 r = *reinterpret_cast<const float4*>(&ms.ref[32 * hh + j + 2 * k]);
+              const float2 A = mul2(f2(__uint_as_float(a[j + 2 * k]), __uint_as_float(a[j + 2 * k + 1])), f2(nk, nk));
+              const float2 B = mul2(f2(__uint_as_float(a[j + 2 * k + 2]), __uint_as_float(a[j + 2 * k + 3])), f2(nk, nk));
+              const float2 a2 = mul2(A, f2(f.x, f.y)), b2 = mul2(B, f2(f.z, f.w));
+              x[k] = f2(cap_near(a2.x, cap) - r.x, cap_near(a2.y, cap) - r.y);
+              x[k + 1] = f2(cap_near(b2.x, cap) - r.z, cap_near(b2.y, cap) - r.w);
               over = max3(max3(over, x[k].x, x[k].y), x[k + 1].x, x[k + 1].y);
               x[k] = f2(ex2(x[k].x), ex2(x[k].y));
               x[k + 1] = f2(ex2(x[k + 1].x), ex2(x[k + 1].y));

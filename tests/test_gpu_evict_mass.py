@@ -217,3 +217,55 @@ def test_long_stream_uses_every_pass(tq):
         assert torch.equal(out[:, :1024], rows)
         assert torch.equal(out[:, 1024:], rec[0, 0, 0, :, 1024:].reshape(-1, 4)[best].reshape(keep, 512))
         assert torch.equal(kw.get("mass_dst", m)[0, 0, 0, :128 * keep], mass[0, 0, 0][best])
+
+
+@pytest.mark.parametrize("T", [0.0, 2.0])
+@pytest.mark.parametrize("in_place", [False, True])
+def test_captured_and_replayed(tq, orc, in_place, T):
+    """A captured call, replayed after the weights and counters have changed, does what a fresh call does."""
+    import torch
+    c = Cache(tq, orc, B=2, Hkv=2, d=128, kb=4, vb=3, n=9, tail=33, T=T, seed=41)
+    rec0 = {w: c.rec[w].clone() for w in "kv"}
+    masses = [torch.from_numpy(_mass(c, kind, s)).cuda() for kind, s in (("spread", 1), ("ties", 2))]
+    counts = [torch.tensor([x], dtype=torch.int32, device="cuda") for x in ([9, 4], [7, 9])]
+
+    def buffers():
+        b = dict(rec={w: rec0[w].clone() for w in "kv"}, mass=masses[0].clone(), n=counts[0].clone())
+        if in_place:
+            return b, dict()
+        d = dict(k_dst=torch.zeros_like(rec0["k"][:, :, :, :5]).contiguous(), mass_dst=torch.zeros_like(masses[0]),
+                 v_dst=torch.zeros_like(rec0["v"][:, :, :, :5]).contiguous(), n_chunks_dst=torch.zeros_like(counts[0]))
+        return b, d
+
+    def call(b, d, ws=None):
+        return tq.evict_mass(k_codec=c.kc, v_codec=c.vc, k_rec=b["rec"]["k"], v_rec=b["rec"]["v"], mass=b["mass"],
+                             n_chunks=b["n"], max_chunks=9, keep_chunks=5, tail_len=c.d_len, max_tail=33, sink=3, recent=50,
+                             workspace=ws, **d)
+
+    def results(b, d):
+        return [d["k_dst"], d["v_dst"], d["mass_dst"], d["n_chunks_dst"]] if d else [*b["rec"].values(), b["mass"], b["n"]]
+
+    def refill(b, d, i):
+        for w in "kv":
+            b["rec"][w].copy_(rec0[w])
+        b["mass"].copy_(masses[i])
+        b["n"].copy_(counts[i])
+        for x in d.values():
+            x.zero_()
+
+    b, d = buffers()
+    ws = call(b, d)
+    s, g = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=s):
+        call(b, d, ws)
+    for i in (0, 1):
+        refill(b, d, i)
+        g.replay()
+        torch.cuda.synchronize()
+        got = [x.clone() for x in results(b, d)]
+        fb, fd = buffers()
+        refill(fb, fd, i)
+        call(fb, fd)
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, results(fb, fd)))

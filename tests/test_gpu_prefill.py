@@ -42,7 +42,9 @@ def _check(c, q, lens, G, got, *, causal=True, softcap=0.0, scale=1.0, fill=9.0)
     """Elementwise: a score's operands are off by half an f16 step each (2^-11, the ring's not at all),
     so by 2^-10 sum |q~ c| n <= 2^-10 |q| |k|; a weight by twice that relative to itself and the
     weighted value by 2^-11 (weight; bf16's 2^-8 in the ring) + 2^-11 (centroid); the output by 2^-8 of
-    itself.  The norm of the whole: those errors are independent, 2^-12.8 |q||k| / sqrt(d) a score and
+    itself.  The roundings of a record's values, 2^-11 of a centroid and 2^-11 of its product with the
+    scale, are made in the rotated basis: with errors |e_r| <= 2^-10 |y_r| there, a coordinate is off by
+    at most sum |e_r| / sqrt(d) <= 2^-10 |y| = 2^-10 |v|, however small it is itself.  The norm of the whole: those errors are independent, 2^-12.8 |q||k| / sqrt(d) a score and
     bf16's 2^-9.8 at the end, together under 2^-8 of the output's norm for |q||k| / sqrt(d) <= 3."""
     L, B, T, Hq, d = q.shape
     qf = synth.bf16_bits_to_f32(q).astype(np.float64)
@@ -60,9 +62,10 @@ def _check(c, q, lens, G, got, *, causal=True, softcap=0.0, scale=1.0, fill=9.0)
                     w = weights(qf[l, b, :, hq], k, m, total, causal, softcap, scale)[:m]
                     want = w @ v
                     size = w @ np.abs(v)
+                    turned = 2.0 ** -10 * (w @ np.linalg.norm(v, axis=-1))[:, None]
                     ds = 2.0 ** -10 * scale * np.linalg.norm(qf[l, b, :m, hq], axis=-1) * (
                         np.linalg.norm(k, axis=-1).max() if len(k) else 0.0)
-                    tol = 2.0 ** -8 * np.abs(want) + (np.expm1(2 * ds)[:, None] + 2.0 ** -7.5) * size * 1.01 + 1e-6
+                    tol = 2.0 ** -8 * np.abs(want) + (np.expm1(2 * ds)[:, None] + 2.0 ** -7.5) * size * 1.01 + turned + 1e-6
                     e = np.abs(g[l, b, :m, hq] - want)
                     assert np.all(e <= tol), (l, b, hq, float((e / tol).max()))
                     err2 += float((e ** 2).sum())
@@ -272,3 +275,13 @@ def test_a_dropped_workspace_is_not_handed_out_under_the_call(tq, orc, raw):
     junk = [torch.full((need,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
     torch.cuda.synchronize()
     assert torch.equal(out, ref) and len(junk) == 4
+
+
+@pytest.mark.parametrize("softcap", [0.25, 30.0, 170.0, 1000.0])
+@pytest.mark.parametrize("d", [64, 256])
+def test_caps_from_small_to_large(tq, orc, d, softcap):
+    """The cap's own error, 2^-21 of it below 177 and tanhf's above, is far under an f16 weight's half step."""
+    c = Cache(tq, orc, B=2, Hkv=2, d=d, kb=4, vb=3, n=5, tail=150, seed=27)
+    q = queries(1, 2, 21, 6, d, 28)
+    out = _run(tq, c, q, None, 3, softcap=softcap, splits=1)
+    _check(c, q, None, 3, out, softcap=softcap)
