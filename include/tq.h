@@ -503,7 +503,9 @@ typedef struct {
  * and 128 the per-vector scales, each within half an f16 step; f32
  * accumulation and softmax statistics); the ring's bf16 keys, values and
  * queries enter exactly, its weights rounded to bf16: the output is within
- * bf16's own precision of the exact sum.  Scales below 2^-24 of the largest
+ * bf16's own precision of the exact sum, also where one token holds nearly all
+ * of a row's weight and the others' values make the output (what f16 drops of 128
+ * tokens' weights is under 2^-16 of the row's largest).  Scales below 2^-24 of the largest
  * finite one of the same context split round to zero.  A row that sees no token is
  * zero; rows t >= T_b are not touched.  Slots and records that hold no token
  * are never read, and keys of tokens a query does not see do not touch its row

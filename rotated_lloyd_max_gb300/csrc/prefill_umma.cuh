@@ -18,12 +18,18 @@
 // time; scaling the f32 scores instead took 23%).  The ring's operands are bf16 as
 // they are.
 //
-// The softmax subtracts a reference that is put 2^4 above the first tile's
-// maximum and moves only when a logit passes it by 2^15, so that scores are read
-// once and O is hardly ever rescaled (by the warps that own the rows; a warp that
-// rescales holds the whole CTA up: a reference at the maximum that moves at 2^8
-// takes 5% longer).  Weights are f16, 11 bits down to 2^-14 and to within 2^-25
-// below, which is 2^-21 of the first tile's largest.
+// The softmax subtracts a reference that stays while a tile's largest weight lies
+// between 2^kPfLow and 2^kPfMargin, so that scores are read once and O is hardly
+// ever rescaled (by the warps that own the rows; a warp that rescales holds the
+// whole CTA up for about 3000 cycles), and else moves to where that weight is 2^kPfTop.
+// Weights are f16: 11 bits down to 2^-14, to within 2^-25 below, so that f16 drops at
+// most 128 2^-25 of a tile, 2^-16 of the row's largest weight.  The reference moves down
+// as well, because a token that takes nearly all of a row's weight would push the
+// others, whose values may be the output, below what f16 holds; it stays within
+// 2^kPfFloor of the largest logit, under which no number of tokens counts.  (A wider
+// reach below a reference that only moves up, 2^-33 of the first tile's largest weight, took 782 us
+// where this takes 551: it leaves 2^7 before logits that grow rescale.)  The ring's
+// weights are bf16, of f32's range: there it only moves up.
 //
 // Warps: 0-3 and 4-7 softmax of tile 0 and 1 (a thread per row), 8-23 decode
 // records (or copy ring tokens) into two stages each of key and value tiles,
@@ -52,9 +58,9 @@ constexpr int kPfSoft = 8, kPfLoad = 16;  // softmax and loading warps
 constexpr int kPfThreads = 32 * (kPfSoft + kPfLoad + 1);
 constexpr int kPfRows = 256;
 constexpr int kPfTok = 128 / kPfLoad;  // tokens of a tile that a loading warp decodes
-// log2 of the largest weight kept against an old reference, and how far a new
-// one is put above the maximum it was found for
-constexpr float kPfMargin = 15.f, kPfAbove = 4.f;
+// log2 of a tile's largest weight against an old reference (at most, and at least),
+// and against a new one; how far a reference may lie below the largest logit
+constexpr float kPfMargin = 15.f, kPfLow = -14.f, kPfTop = -2.f, kPfFloor = 24.f;
 
 // Registers per thread: 72 at launch (25 warps: seven on one of the SM's four
 // partitions), then 104 for the softmax and 56 for the decoding warps, no more
@@ -623,7 +629,8 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
     const uint32_t tS = tb0 + 128 * t + lrow, tO = tb0 + 256 + D * t + lrow;
     // tokens it sees, counted from the run's first; rows of no query see everything
     const int lim = r < rn ? row_limit(p, cl, tb, r0 + r) - base - k0 : 0x7FFFFFFF;
-    float mref = -INFINITY, lsum = 0.f;
+    // the largest logit where references moved; how low a tile's maximum may lie against one
+    float mref = -INFINITY, lsum = 0.f, peak = -INFINITY, low = -INFINITY;
     const SoftCap cap = make_cap(p.scap, p.iscap);
 #pragma unroll 1
     for (int i = 0; i < n; ++i) {
@@ -632,7 +639,8 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
       const int seen = lim - i * kChunk;  // columns below it
       const bool edge = __any_sync(0xffffffffu, seen < kChunk);
       uint32_t w[64];  // weights as pairs; chunk c of S becomes columns 16 c .. 16 c + 15
-      float mx = -INFINITY;
+      float mx = -INFINITY, tm = -INFINITY;
+      bool known = false;  // tm is the tile's largest logit
       float2 sum = f2(0.f, 0.f);
       bool again = edge || mref == -INFINITY || (CAP && cap.large);
       if (!__any_sync(0xffffffffu, again)) {
@@ -662,25 +670,32 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
             w[8 * c + j / 2] = DENSE ? pack2_bf16(v.x, v.y) : pack2_f16(v.x, v.y);
           }
         }
-        again = x0 > kPfMargin;
+        again = x0 > kPfMargin || x0 < low;
+        tm = x0 + mref;
+        known = true;
       }
       if (__any_sync(0xffffffffu, again)) {
         // a new reference for the rows that passed theirs by the margin (or have none yet):
         // find the maximum, rescale, and form the weights again
         again = false;
         sum = f2(0.f, 0.f);
+        if (!known) {
 #pragma unroll 1
-        for (int c = 0; c < 8; ++c) {
-          uint32_t a[16];
-          tmem_ld16(tS + 16 * c, a);
-          tmem_ld_wait();
+          for (int c = 0; c < 8; ++c) {
+            uint32_t a[16];
+            tmem_ld16(tS + 16 * c, a);
+            tmem_ld_wait();
 #pragma unroll
-          for (int j = 0; j < 16; ++j) mx = fmaxf(mx, 16 * c + j < seen ? __uint_as_float(a[j]) : -INFINITY);
+            for (int j = 0; j < 16; ++j) mx = fmaxf(mx, 16 * c + j < seen ? __uint_as_float(a[j]) : -INFINITY);
+          }
+          tm = mx > -INFINITY ? mx * f : -INFINITY;
+          if (CAP && mx > -INFINITY) tm = cap_logit(tm, cap);
         }
-        float tm = mx > -INFINITY ? mx * f : -INFINITY;
-        if (CAP && mx > -INFINITY) tm = cap_logit(tm, cap);
-        if (__any_sync(0xffffffffu, tm > mref + kPfMargin)) {
-          const float mn = tm > mref + kPfMargin ? tm + kPfAbove : mref;
+        peak = fmaxf(peak, tm);
+        const bool moves = tm > mref + kPfMargin || (tm < mref + low && tm > -INFINITY);
+        if (__any_sync(0xffffffffu, moves)) {
+          const float mn = !moves ? mref : fmaxf(tm - kPfTop, peak - kPfFloor);
+          if (moves && !DENSE) low = mn > peak - kPfFloor ? kPfLow : -INFINITY;
           const float al = mref > -INFINITY ? ex2(mref - mn) : 0.f;  // 1 where the reference stays
           const float sc = mn > -INFINITY ? al : 1.f;
           lsum *= sc;

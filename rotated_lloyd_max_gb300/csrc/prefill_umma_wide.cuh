@@ -8,8 +8,9 @@
 // A thread owns a token (its lane) for the softmax and a coordinate for the
 // outputs, so that a token's scales are one factor of its thread's logits and one
 // of its weights, and decoding is a table lookup and nothing else.  References
-// of the softmax as in the narrower kernel (prefill_umma.cuh); the ring's
-// tokens are bf16 operands.
+// of the softmax as in the narrower kernel (prefill_umma.cuh), but that a row whose
+// weights have become small is found by their sums, two records late and off the
+// chain of the products; the ring's tokens are bf16 operands.
 //
 // Tokens are decoded in chunks of 64 coordinates (16 KB) into a ring of eight,
 // sixteen warps in groups of four, a group a chunk.  Where keys and values share
@@ -45,6 +46,9 @@ struct PwMisc {
   alignas(16) float ref[64];   // its softmax reference (log2 units)
   int lim[64];                 // tokens it sees, counted from the run's first
   alignas(16) float red[4][64];
+  uint4 small[2][2];           // by record parity, halves of the rows: those whose weights sum to less than
+                               // 2^kPfLow, a word a warp
+  uint32_t bound[2];           // rows whose reference may not move down
 };
 static_assert(sizeof(PwMisc) <= 2048, "bookkeeping block");
 
@@ -435,6 +439,9 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
     for (int m = 16; m; m >>= 1) low = min(low, __shfl_xor_sync(0xffffffffu, low, m));
     const SoftCap cap = make_cap(p.scap, p.iscap);
     const bool capped = p.scap > 0.f;
+    float peak = -INFINITY;      // rows' (thread tid < 64) largest logit where references moved
+    uint32_t bound0 = 0xFFFFFFFFu, bound1 = 0xFFFFFFFFu;
+    bool sunk = false;           // a row's weights have become small and its reference may move down
     float lacc[2] = {0.f, 0.f};  // sums of rows lane and 32 + lane over this warp's tokens
     auto scale_at = [&](bool key, int i) {
       if constexpr (DENSE) return 1.f;
@@ -541,8 +548,7 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
           }
         }
       }
-      const bool need = !plain || over > kPfMargin;
-      if (bar_soft_or(need)) {
+      if (bar_soft_or(!plain || over > kPfMargin || sunk)) {
         // new references for the rows that passed theirs; their outputs and sums rescaled
 #pragma unroll 1
         for (int hh = 0; hh < 2; ++hh) {
@@ -555,8 +561,13 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
         if (tid < 64) {
           const float mx = fmaxf(fmaxf(ms.red[0][tid], ms.red[1][tid]), fmaxf(ms.red[2][tid], ms.red[3][tid]));
           const float mo = ms.ref[tid];
-          mn = mx > mo + kPfMargin ? mx + kPfAbove : mo;
+          peak = fmaxf(peak, mx);
+          const bool up = mx > mo + kPfMargin;
+          const bool down = !DENSE && mx < mo + kPfLow && mx > -INFINITY && mo > peak - kPfFloor;
+          mn = !(up || down) ? mo : fmaxf(mx - kPfTop, peak - kPfFloor);
           sc = mo > -INFINITY ? ex2(mo - mn) : mn > -INFINITY ? 0.f : 1.f;
+          const uint32_t stays = __ballot_sync(0xffffffffu, !(mn > peak - kPfFloor));
+          if (lane == 0) ms.bound[warp] = stays;
         }
         bar_soft();
         if (tid < 64) {
@@ -564,6 +575,8 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
           ms.red[0][tid] = sc;
         }
         bar_soft();
+        bound0 = ms.bound[0];
+        bound1 = ms.bound[1];
         lacc[0] *= ms.red[0][lane];
         lacc[1] *= ms.red[0][32 + lane];
         if (i > 0) {
@@ -610,7 +623,16 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
           t[2 * j] = x.x;
           t[2 * j + 1] = x.y;
         }
-        lacc[hh] += transpose_reduce32<false>(t, lane);
+        const float sum = transpose_reduce32<false>(t, lane);
+        lacc[hh] += sum;
+        if (!DENSE) {
+          const uint32_t m = __ballot_sync(0xffffffffu, sum < exp2f(kPfLow));
+          if (lane == 0) reinterpret_cast<uint32_t*>(&ms.small[i & 1][hh])[warp] = m;
+        }
+      }
+      if (!DENSE && i > 0) {  // the record before: its words are behind this one's barrier
+        const uint4 x = ms.small[(i - 1) & 1][0], y = ms.small[(i - 1) & 1][1];
+        sunk = ((x.x & x.y & x.z & x.w & ~bound0) | (y.x & y.y & y.z & y.w & ~bound1)) != 0;
       }
     }
     mbar_wait_idle(&ms.o_done, (n - 1) & 1, abort_f);

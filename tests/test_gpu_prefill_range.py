@@ -1,0 +1,72 @@
+"""GPU tests of tq_prefill_attn where one token takes nearly all of a row's weight:
+what the other tokens have left counts."""
+import math
+
+import numpy as np
+import pytest
+
+import synth
+import tq_testlib as tl
+from cache_cases import Cache, weights
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def tq():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from rotated_lloyd_max_gb300 import build
+    build.build()
+    import rotated_lloyd_max_gb300 as m
+    m.load()
+    return m
+
+
+def _bits(x):
+    """float array -> bf16 bits, to nearest even."""
+    u = np.ascontiguousarray(x, np.float32).view(np.uint32)
+    return ((u + 0x7FFF + ((u >> 16) & 1)) >> 16).astype(np.uint16)
+
+
+def _scales(c, which, bits):
+    """View of a one-layer, one-sequence, one-head cache's scales [n, 128]."""
+    import torch
+    off = 128 * c.d * bits // 8
+    return c.rec[which][0, 0, 0, :, off:off + 512].view(torch.float32)
+
+
+@pytest.mark.parametrize("place", ["first", "last"])
+@pytest.mark.parametrize("d", [64, 128, 256, 512])
+def test_one_token_takes_most_of_the_weight(tq, orc, d, place):
+    """An attention sink over 32768 tokens in one split: its logit is 13 to 17 nats above a flat context,
+    its value small, and the others' values have a part in common, so that the output is theirs.
+    Bound: bf16's half step of the output's norm, 2^-8 (its own rounding is under 2^-9.5 of the norm; the
+    sink's logit, at most 17, is off by 2^-11 of each of d products of one sign whose operands take 16
+    values, 17 2^-11 / sqrt(8) = 2^-8.4 at the very most and 2^-10 in the mean)."""
+    import torch
+    n = 256
+    c = Cache(tq, orc, B=1, Hkv=1, d=d, kb=4, vb=4, n=n, tail=4, seed=33)
+    g = np.random.default_rng(d)
+    x = 0.5 * g.standard_normal((1, n * 128, d)) + g.standard_normal(d)
+    tq.tq_encode(c.vc, tl.to_bf16_tensor(_bits(x), "cuda"), c.rec["v"].view(1, n, -1))
+    sink = 3 if place == "first" else n * 128 - 7
+    ks, vs = _scales(c, "k", 4), _scales(c, "v", 4)
+    ks *= torch.where(torch.arange(n * 128, device="cuda").view(n, 128) == sink, 1.0, 0.05)
+    vs[sink // 128, sink % 128] *= 0.03
+    c.ring["k"].mul_(0.05)
+    c._host = {w: c.rec[w].cpu().numpy() for w in "kv"}
+    k, v = c.vectors("k", 0, 0, 0), c.vectors("v", 0, 0, 0)
+    gaps = np.array([13.0, 14.0, 15.0, 17.0])
+    q = _bits((gaps[:, None] * k[sink] / (k[sink] @ k[sink]))[None, None].reshape(1, 1, 2, 2, d))
+    out = torch.zeros((1, 1, 2, 2, d), dtype=torch.bfloat16, device="cuda")
+    tq.prefill_attn(k_codec=c.kc, v_codec=c.vc, q=tl.to_bf16_tensor(q, "cuda"), out=out, scale=1.0, splits=1, **c.kw())
+    got = synth.bf16_bits_to_f32(tl.bf16_tensor_bits(out)).astype(np.float64)
+    qf = synth.bf16_bits_to_f32(q).astype(np.float64)
+    for i in range(2):
+        w = weights(qf[0, 0, :, i], k, 2, n * 128 + 4, True, 0.0, 1.0)
+        assert w[:, sink].min() > 0.9
+        want = w @ v
+        e = np.linalg.norm(got[0, 0, :, i] - want, axis=-1) / np.linalg.norm(want, axis=-1)
+        assert np.all(e <= 2.0 ** -8), e
