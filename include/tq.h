@@ -502,7 +502,7 @@ typedef struct {
  * operands are f16 (centroids, rotated queries, weights, and at head dims 64
  * and 128 the per-vector scales, each within half an f16 step; f32
  * accumulation and softmax statistics); the ring's bf16 keys, values and
- * queries enter exactly, its weights rounded to bf16: the output is within
+ * queries enter exactly, its weights rounded to bf16 and summed so: the output is within
  * bf16's own precision of the exact sum, also where one token holds nearly all
  * of a row's weight and the others' values make the output (what f16 drops of 128
  * tokens' weights is under 2^-16 of the row's largest).  Scales below 2^-24 of the largest

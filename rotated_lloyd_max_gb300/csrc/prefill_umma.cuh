@@ -642,6 +642,13 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
       float mx = -INFINITY, tm = -INFINITY;
       bool known = false;  // tm is the tile's largest logit
       float2 sum = f2(0.f, 0.f);
+      // a pair of weights as an operand, and its sum: bf16 ones as rounded, since weights that
+      // are alike round alike and 2^-8 would not average out
+      auto weigh = [&](float2 v) {
+        const uint32_t u = DENSE ? pack2_bf16(v.x, v.y) : pack2_f16(v.x, v.y);
+        sum = add2(sum, DENSE ? f2(bf16_lo(u), bf16_hi(u)) : v);
+        return u;
+      };
       bool again = edge || mref == -INFINITY || (CAP && cap.large);
       if (!__any_sync(0xffffffffu, again)) {
         // weights against the reference as it stands; the maximum is found on the way
@@ -666,8 +673,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
             }
             x0 = max3(x0, v.x, v.y);
             v = f2(ex2(v.x), ex2(v.y));
-            sum = add2(sum, v);
-            w[8 * c + j / 2] = DENSE ? pack2_bf16(v.x, v.y) : pack2_f16(v.x, v.y);
+            w[8 * c + j / 2] = weigh(v);
           }
         }
         again = x0 > kPfMargin || x0 < low;
@@ -729,8 +735,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
             float2 v = f2(__uint_as_float(a[j]) * f, __uint_as_float(a[j + 1]) * f);
             if constexpr (CAP) v = f2(cap_logit(v.x, cap), cap_logit(v.y, cap));
             v = f2(16 * c + j < seen ? ex2(v.x - ref) : 0.f, 16 * c + j + 1 < seen ? ex2(v.y - ref) : 0.f);
-            sum = add2(sum, v);
-            w[8 * c + j / 2] = DENSE ? pack2_bf16(v.x, v.y) : pack2_f16(v.x, v.y);
+            w[8 * c + j / 2] = weigh(v);
           }
         }
       }

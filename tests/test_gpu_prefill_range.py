@@ -1,5 +1,5 @@
-"""GPU tests of tq_prefill_attn where one token takes nearly all of a row's weight:
-what the other tokens have left counts."""
+"""GPU tests of tq_prefill_attn where one token takes nearly all of a row's weight,
+and where many equal weights round alike: what the other tokens have left counts."""
 import math
 
 import numpy as np
@@ -70,3 +70,33 @@ def test_one_token_takes_most_of_the_weight(tq, orc, d, place):
         want = w @ v
         e = np.linalg.norm(got[0, 0, :, i] - want, axis=-1) / np.linalg.norm(want, axis=-1)
         assert np.all(e <= 2.0 ** -8), e
+
+
+@pytest.mark.parametrize("d", [64, 128, 256, 512])
+def test_equal_weights_that_round_alike(tq, orc, d):
+    """Ring tokens whose weights all lie just under the middle of two bf16 numbers (2^-3 (1 + 0.98 2^-8) of
+    the largest): the sum they are divided by counts them as rounded.  Exactly, they hold 0.99 of the weight, so
+    a common factor moves the output by a hundredth of itself: 2^-8 (the output's rounding) + 2^-10."""
+    import torch
+    t = math.log(0.125 * (1 + 0.98 * 2.0 ** -8))
+    tail = 700
+    c = Cache(tq, orc, B=1, Hkv=1, d=d, n=0, tail=tail, seed=34)
+    g = np.random.default_rng(d)
+    k, v = np.zeros((c.cap, d), np.float32), np.tile(g.standard_normal(d).astype(np.float32), (c.cap, 1))
+    a = synth.bf16_bits_to_f32(_bits(np.float32(t)).reshape(1))[0]
+    k[:, 0], k[:, 1] = a, t - a
+    first = int(c.start[0, 0])
+    k[first] = 0
+    v[first] = 0
+    c.ring["k"].copy_(tl.to_bf16_tensor(_bits(k), "cuda").view_as(c.ring["k"]))
+    c.ring["v"].copy_(tl.to_bf16_tensor(_bits(v), "cuda").view_as(c.ring["v"]))
+    q = np.zeros((1, 1, 1, 2, d), np.float32)
+    q[..., :2] = 1
+    out = torch.zeros((1, 1, 1, 2, d), dtype=torch.bfloat16, device="cuda")
+    tq.prefill_attn(q=tl.to_bf16_tensor(_bits(q), "cuda"), out=out, scale=1.0, splits=1, **c.kw())
+    got = synth.bf16_bits_to_f32(tl.bf16_tensor_bits(out)).astype(np.float64)
+    kf, vf = c.vectors("k", 0, 0, 0), c.vectors("v", 0, 0, 0)
+    want = weights(q[0, 0, :, 0].astype(np.float64), kf, 1, tail, True, 0.0, 1.0) @ vf
+    for i in range(2):
+        e = np.abs(got[0, 0, :, i] - want) / np.abs(want)
+        assert np.all(e <= 2.0 ** -8 + 2.0 ** -10), float(e.max())
