@@ -163,3 +163,27 @@ def test_same_bits_every_time_and_from_a_graph(tq, orc):
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(one, two)
+
+
+MORE = {
+    "decode_d256": dict(d=256, G=5, T=1, kb=3, n=4, L=2, B=3),
+    "decode_d256_side_lists": dict(d=256, G=4, T=2, T_out=2.0, n=3),
+    "window_d256_paged": dict(d=256, G=4, T=21, kb=4, paged=True, n=4, B=3, L=2),
+    "window_d512_side_lists": dict(d=512, G=8, T=9, T_out=2.0, Hkv=1, kb=2, n=3),
+}
+
+
+@pytest.mark.parametrize("splits", [0, 2])
+@pytest.mark.parametrize("name", MORE)
+def test_more_layouts_against_the_formula(tq, orc, name, splits):
+    kw = dict(MORE[name])
+    call = {k: kw.pop(k) for k in ("G", "T", "lens", "causal", "softcap") if k in kw}
+    c = Cache(tq, orc, T=kw.pop("T_out", 0.0), seed=14, **kw)
+    _check(tq, c, splits=splits, **call)
+
+
+@pytest.mark.parametrize("T,G", [(1, 4), (6, 4), (23, 4)])
+def test_runs_longer_than_a_split_may_be(tq, orc, T, G):
+    """One split is asked for over 101 records: the routes that keep a split's sums in shared memory take as many as they need."""
+    c = Cache(tq, orc, B=1, Hkv=1, d=64, kb=2, n=101, tail=100, seed=15)
+    _check(tq, c, T, G, splits=1)

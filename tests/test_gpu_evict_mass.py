@@ -269,3 +269,39 @@ def test_captured_and_replayed(tq, orc, in_place, T):
         call(fb, fd)
         torch.cuda.synchronize()
         assert all(torch.equal(x, y) for x, y in zip(got, results(fb, fd)))
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("n", [3073, 3207])
+def test_streams_longer_than_a_cluster_keeps(tq, in_place, n):
+    """More than 3072 records: the weights are read again in every pass; the last of the cluster's CTAs have fewer records."""
+    import torch
+    keep, d = 1500, 64
+    kc = tq.tq_make_codebook(1, d)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(n)
+    rec = torch.randint(0, 256, (1, 1, 1, n, kc.record_bytes), dtype=torch.uint8, device="cuda", generator=g)
+    mass = 1.0 + torch.rand((1, 1, 1, 128 * n + 77), device="cuda", generator=g) * 2.0 ** -12
+    mass[..., 5:128 * n:3] = mass[..., 5:6]  # a third of the weights are equal
+    cnt = torch.full((1, 1), n, dtype=torch.int32, device="cuda")
+    ln = torch.full((1, 1), 77, dtype=torch.int32, device="cuda")
+    m, r = mass.clone(), rec.clone()
+    kept = torch.zeros((1, 1, 1, 128 * keep), dtype=torch.int32, device="cuda")
+    kw = {}
+    if not in_place:
+        kw = dict(k_dst=torch.zeros_like(rec[:, :, :, :keep]), mass_dst=torch.zeros((1, 1, 1, 128 * keep + 77), device="cuda"),
+                  n_chunks_dst=torch.zeros_like(cnt))
+        kw["v_dst"] = kw["k_dst"]
+    tq.evict_mass(k_codec=kc, v_codec=kc, k_rec=r, v_rec=r, mass=m, n_chunks=cnt, max_chunks=n, keep_chunks=keep,
+                  kept=kept, tail_len=ln, max_tail=77, sink=9, recent=200, **kw)
+    rank = mass[0, 0, 0, :128 * n].clone()
+    rank[:9] = rank[-200:] = math.inf
+    best = torch.sort(rank, descending=True, stable=True).indices[:128 * keep].sort().values
+    assert torch.equal(kept[0, 0, 0].long(), best)
+    out = kw.get("k_dst", r)[0, 0, 0, :keep]
+    assert torch.equal(out[:, :1024], rec[0, 0, 0, :, :1024].reshape(-1, 8)[best].reshape(keep, 1024))
+    assert torch.equal(out[:, 1024:], rec[0, 0, 0, :, 1024:].reshape(-1, 4)[best].reshape(keep, 512))
+    md = kw.get("mass_dst", m)[0, 0, 0]
+    assert torch.equal(md[:128 * keep], mass[0, 0, 0, best])
+    assert torch.equal(md[128 * keep:128 * keep + 77], mass[0, 0, 0, 128 * n:])
+    assert torch.all(md[128 * keep + 77:128 * n + 77] == 0)

@@ -285,3 +285,24 @@ def test_caps_from_small_to_large(tq, orc, d, softcap):
     q = queries(1, 2, 21, 6, d, 28)
     out = _run(tq, c, q, None, 3, softcap=softcap, splits=1)
     _check(c, q, None, 3, out, softcap=softcap)
+
+
+MORE = {
+    "side_lists_d256": dict(d=256, G=4, T=9, T_out=2.0, kb=4, vb=3, n=3),
+    "side_lists_d512_shared": dict(d=512, G=8, T=5, T_out=2.0, kb=4, shared=True, Hkv=1, n=2),
+    "side_lists_d512_paged": dict(d=512, G=3, T=7, T_out=1.5, kb=3, vb=2, paged=True, n=4, B=2, L=2),
+    "paged_d256": dict(d=256, G=5, T=30, kb=2, vb=4, paged=True, n=5, B=3, L=2, lens=[30, 7, 19]),
+    "paged_d512_shared": dict(d=512, G=16, T=9, kb=4, shared=True, Hkv=1, paged=True, n=3, B=3, L=2),
+    "one_bit_side_lists": dict(d=128, G=2, T=6, T_out=1.5, kb=1, vb=1, n=3),
+}
+
+
+@pytest.mark.parametrize("splits", [0, 1])
+@pytest.mark.parametrize("name", MORE)
+def test_more_layouts_against_the_formula(tq, orc, name, splits):
+    kw = dict(MORE[name])
+    G, T, lens, T_out = kw.pop("G"), kw.pop("T"), kw.pop("lens", None), kw.pop("T_out", 0.0)
+    c = Cache(tq, orc, T=T_out, seed=5, **kw)
+    q = queries(c.L, c.B, T, c.Hkv * G, c.d, 78)
+    out = _run(tq, c, q, lens, G, splits=splits)
+    _check(c, q, lens, G, out)
