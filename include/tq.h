@@ -510,7 +510,10 @@ typedef struct {
  * zero; rows t >= T_b are not touched.  Slots and records that hold no token
  * are never read, and keys of tokens a query does not see do not touch its row
  * in any other way, NaN and infinities included; the VALUES of all tokens below total have to be finite
- * (a weight of zero times an infinity is NaN, for a later query's token too).
+ * (a weight of zero times an infinity is NaN, for a later query's token too).  A row whose
+ * query holds a NaN or an infinity, or that sees a key of a NaN or of a scale that is not finite, is NaN, and so is one
+ * that sees tokens of no finite logit (infinities of queries and keys in the ring under a soft cap may count
+ * as the cap).
  * The kernels bound every internal wait (about two seconds); if one expires (a
  * fault of the device, not of the arguments) the rows concerned are NaN.
  * out may not overlap itself (strides as for q_out above).

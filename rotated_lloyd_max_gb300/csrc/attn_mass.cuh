@@ -57,6 +57,10 @@ __device__ __forceinline__ float ex2(float x) {
   return r;
 }
 
+// x, or NaN in the place of an infinity: an infinite scale makes coordinates of both signs infinite,
+// and a product with them no number
+__device__ __forceinline__ float finite_or_nan(float x) { return fmaf(x, 0.f, x); }
+
 // new tokens of sequence b
 __device__ __forceinline__ int query_len(const QueryParams& p, int b) {
   return p.q_lens ? min(max(p.q_lens[b], 0), p.T) : p.T;

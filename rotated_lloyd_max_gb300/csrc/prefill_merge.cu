@@ -6,6 +6,12 @@
 
 namespace tq {
 
+// 1 / W; NaN where it is or where a row sees tokens of no finite logit, 0 where it sees no token
+__device__ __forceinline__ float inverse_weight(const QueryParams& p, int lb, int tb, int row, float W) {
+  if (W > 0.f || W != W) return 1.f / W;
+  return row_limit(p, cache_len(p, lb), tb, row) > 0 ? __int_as_float(0x7fc00000) : 0.f;
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads) prefill_merge_kernel(const __grid_constant__ PrefillParams pp) {
   constexpr int E = D / 32;
@@ -18,7 +24,8 @@ __global__ void __launch_bounds__(kThreads) prefill_merge_kernel(const __grid_co
   const int64_t unit = wrow / pp.rows;
   const int row = (int)(wrow % pp.rows), tok = row / p.G;
   const int h = (int)(unit % p.Hkv), lb = (int)(unit / p.Hkv), b = lb % p.B, l = lb / p.B;
-  if (tok >= query_len(p, b)) return;
+  const int tb = query_len(p, b);
+  if (tok >= tb) return;
   const int S = pp.Sc + pp.St;
   const float2* ml = pp.ws_ml + wrow * S;
   const float* acc = pp.ws_acc + wrow * S * D + lane * E;
@@ -52,7 +59,7 @@ __global__ void __launch_bounds__(kThreads) prefill_merge_kernel(const __grid_co
     fwht_regs<E>(c);
     fwht_lanes<E>(c, lane, 32);
   }
-  const float iw = W > 0.f || W != W ? 1.f / W : 0.f;  // a row that sees no token is zero
+  const float iw = inverse_weight(p, lb, tb, row, W);
   uint16_t* out = pp.out + l * pp.o_ls + b * pp.o_bs + (int64_t)tok * pp.o_ts + (int64_t)(h * p.G + row % p.G) * D +
                   lane * E;
 #pragma unroll
@@ -163,7 +170,7 @@ __global__ void __launch_bounds__(256) prefill_merge_tiles_kernel(const __grid_c
     for (int g = 1; g < SL; ++g) W += wsum[g * 4 * ROWS + 4 * lr + qd];
   }
   if (!live) return;
-  const float iw = W > 0.f || W != W ? 1.f / W : 0.f;  // a row that sees no token is zero
+  const float iw = inverse_weight(p, lb, tb, row, W);
   uint16_t* out = pp.out + l * pp.o_ls + b * pp.o_bs + (int64_t)tok * pp.o_ts + (int64_t)(h * p.G + row % p.G) * D + qd * E;
 #pragma unroll
   for (int e = 0; e < E; e += 8)

@@ -740,6 +740,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
         }
       }
       lsum += sum.x + sum.y;
+      if (lsum != lsum && mref == -INFINITY) mref = 0.f;  // a NaN row has no maximum to wait for
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
         uint32_t u[16];
@@ -772,7 +773,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
     }
     if (r < rn) {
       const float bad = __int_as_float(0x7fc00000);
-      pp.ws_ml[at + (r & 127)] = *abort_f ? make_float2(bad, bad)
+      pp.ws_ml[at + (r & 127)] = *abort_f || lsum != lsum ? make_float2(bad, bad)
                                  : lsum > 0.f ? make_float2(mref, lsum) : make_float2(-INFINITY, 0.f);
     }
     tc_fence_before();

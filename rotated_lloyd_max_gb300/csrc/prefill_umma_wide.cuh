@@ -445,7 +445,8 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
     float lacc[2] = {0.f, 0.f};  // sums of rows lane and 32 + lane over this warp's tokens
     auto scale_at = [&](bool key, int i) {
       if constexpr (DENSE) return 1.f;
-      return __ldg(reinterpret_cast<const float*>(rec_at(key, c0 + i) + (key ? p.kc.off_norm : p.vc.off_norm)) + tok);
+      const float n = __ldg(reinterpret_cast<const float*>(rec_at(key, c0 + i) + (key ? p.kc.off_norm : p.vc.off_norm)) + tok);
+      return finite_or_nan(n);
     };
     float nk1 = scale_at(true, 0), nv1 = scale_at(false, 0);
 #pragma unroll 1
@@ -656,7 +657,7 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
       const float bad = __int_as_float(0x7fc00000);
       const float sum = (ms.red[0][tid] + ms.red[1][tid]) + (ms.red[2][tid] + ms.red[3][tid]);
       pp.ws_ml[(wrow + tid) * S + sidx] =
-          *abort_f ? make_float2(bad, bad) : sum > 0.f ? make_float2(ms.ref[tid], sum) : make_float2(-INFINITY, 0.f);
+          *abort_f || sum != sum ? make_float2(bad, bad) : sum > 0.f ? make_float2(ms.ref[tid], sum) : make_float2(-INFINITY, 0.f);
     }
     tc_fence_before();
   }

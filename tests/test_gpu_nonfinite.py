@@ -1,0 +1,108 @@
+"""GPU tests of NaN and infinities that a query does see, in the several-query attention: the rows
+concerned come out NaN, the others as with clean inputs."""
+import math
+
+import pytest
+
+import tq_testlib as tl
+from cache_cases import Cache, queries
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def tq():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from rotated_lloyd_max_gb300 import build
+    build.build()
+    import rotated_lloyd_max_gb300 as m
+    m.load()
+    return m
+
+
+def _put_scale(c, which, bits, h, record, slot, value):
+    import torch
+    off = 128 * c.d * bits // 8 + 4 * slot
+    c.rec[which][0, 0, h, record, off:off + 4] = torch.tensor([value], device="cuda").view(torch.uint8)
+
+
+def _attend(tq, c, q, **kw):
+    import torch
+    out = torch.full_like(q, 5.0)
+    tq.prefill_attn(k_codec=c.kc, v_codec=c.vc, q=q, out=out, scale=1.0, **kw, **c.kw())
+    torch.cuda.synchronize()
+    return out
+
+
+T, G = 12, 3
+
+
+def _cache(tq, orc, d, **kw):
+    return Cache(tq, orc, **dict(dict(B=1, Hkv=2, d=d, kb=3, vb=4, n=7, tail=150, seed=51), **kw))
+
+
+@pytest.mark.parametrize("splits", [0, 1, 4])
+@pytest.mark.parametrize("softcap", [0.0, 20.0])
+@pytest.mark.parametrize("d", [64, 128, 256, 512])
+def test_attention_of_a_query_with_nan(tq, orc, d, softcap, splits):
+    import torch
+    c = _cache(tq, orc, d)
+    q = tl.to_bf16_tensor(queries(1, 1, T, 2 * G, d, 5), "cuda")
+    clean = _attend(tq, c, q, splits=splits, softcap=softcap)
+    bad = q.clone()
+    bad[0, 0, 4, 1, d // 2] = math.nan
+    bad[0, 0, 9, 5, 0] = math.nan
+    out = _attend(tq, c, bad, splits=splits, softcap=softcap)
+    hit = torch.zeros((T, 2 * G), dtype=torch.bool, device="cuda")
+    hit[4, 1] = hit[9, 5] = True
+    assert torch.isnan(out[0, 0][hit]).all()
+    assert torch.equal(out[0, 0][~hit], clean[0, 0][~hit])
+
+
+@pytest.mark.parametrize("splits", [0, 1, 4])
+@pytest.mark.parametrize("value", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("d", [64, 128, 256, 512])
+def test_attention_over_a_scale_that_is_not_finite(tq, orc, d, value, splits):
+    """One record of seven; the other kv head is untouched.  A key's scale, then a value's."""
+    import torch
+    c = _cache(tq, orc, d)
+    q = tl.to_bf16_tensor(queries(1, 1, T, 2 * G, d, 6), "cuda")
+    clean = _attend(tq, c, q, splits=splits)
+    saved = {w: c.rec[w].clone() for w in "kv"}
+    for which, bits in (("k", 3), ("v", 4)):
+        c.rec[which].copy_(saved[which])
+        _put_scale(c, which, bits, 1, 2, 77, value)
+        out = _attend(tq, c, q, splits=splits)
+        assert not torch.isfinite(out[0, 0, :, G:]).any()
+        assert torch.isnan(out[0, 0, :, G:]).all() or which == "v"
+        assert torch.equal(out[0, 0, :, :G], clean[0, 0, :, :G])
+        c.rec[which].copy_(saved[which])
+
+
+@pytest.mark.parametrize("splits", [0, 1])
+@pytest.mark.parametrize("d", [64, 128, 256, 512])
+def test_attention_over_a_ring_key_with_nan(tq, orc, d, splits):
+    """The key of new token 7: queries from it on see it."""
+    import torch
+    c = _cache(tq, orc, d)
+    q = tl.to_bf16_tensor(queries(1, 1, T, 2 * G, d, 7), "cuda")
+    clean = _attend(tq, c, q, splits=splits)
+    slot = (int(c.start[0, 0]) + 150 - T + 7) % c.cap
+    c.ring["k"][0, 0, 0, slot, 3] = math.nan
+    out = _attend(tq, c, q, splits=splits)
+    assert torch.isnan(out[0, 0, 7:, :G]).all()
+    assert torch.equal(out[0, 0, :7], clean[0, 0, :7]) and torch.equal(out[0, 0, :, G:], clean[0, 0, :, G:])
+
+
+@pytest.mark.parametrize("d", [64, 256])
+def test_attention_whose_logits_are_all_minus_infinity(tq, orc, d):
+    """A row that sees tokens, but none of a finite logit, is NaN; one that sees no token is zero."""
+    import torch
+    c = _cache(tq, orc, d, n=0, tail=40)
+    q = torch.zeros((1, 1, 50, 2, d), dtype=torch.bfloat16, device="cuda")
+    q[..., 3] = -math.inf
+    c.ring["k"].fill_(1.0)
+    out = _attend(tq, c, q)
+    assert torch.all(out[0, 0, :10] == 0) and torch.isnan(out[0, 0, 10:]).all()
