@@ -536,7 +536,8 @@ tq_status tq_prefill_attn(const tq_query_args* args, const tq_codec* k_codec, co
  * fixed order (no atomics); logits are f32-accurate (operands of 22 bits or
  * exact), on every route: up to 8 rows (query heads of a kv head x t_q), up to
  * 40 or head dims 256 and 512 (mma.sync), more (tcgen05; a wait of its that
- * expires leaves NaN).  decay: finite, >= 0.  workspace as for tq_prefill_attn.
+ * expires leaves NaN).  A row (query) that tq_prefill_attn would leave NaN leaves NaN in
+ * every entry below total of its kv head, on every route.  decay: finite, >= 0.  workspace as for tq_prefill_attn.
  */
 size_t tq_attn_mass_workspace_size(const tq_query_args* args, const tq_codec* k_codec);
 tq_status tq_attn_mass(const tq_query_args* args, const tq_codec* k_codec, float* mass,

@@ -101,6 +101,12 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float a, float b) {
   const __nv_bfloat162 v = __floats2bfloat162_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&v);
 }
+// log2 of a row's sum W 2^M: INFINITY for a row that sees no token and weighs nothing, NaN for one of
+// no finite softmax, which leaves NaN in every entry
+__device__ __forceinline__ float log_sum(float M, float W, int limit) {
+  if (W > 0.f) return M + log2f(W);
+  return W != W || limit > 0 ? __int_as_float(0x7fc00000) : INFINITY;
+}
 // a logit in log2 units, -inf past the row's limit
 __device__ __forceinline__ float mass_logit(const QueryParams& p, float acc, float f, bool seen) {
   float t = acc * f;
@@ -272,8 +278,9 @@ __global__ void __launch_bounds__(kThreads) attn_mass_kernel(const __grid_consta
         for (int s = 0; s < S; ++s) {
           const float2 v = ml[(int64_t)s * rows_pad];
           if (v.y > 0.f) W += v.y * exp2f(v.x - M);
+          else if (v.y != v.y) W = v.y;
         }
-        ms.lse[tid] = W > 0.f ? M + log2f(W) : INFINITY;  // a row that sees nothing weighs nothing
+        ms.lse[tid] = log_sum(M, W, ms.lim[tid]);
       }
       __syncthreads();
     }
@@ -391,6 +398,8 @@ __global__ void __launch_bounds__(kThreads) attn_mass_kernel(const __grid_consta
         }
       }
       // element e of tile mi: token 32 warp + 16 mi + 8 (e / 2) + g, row 8 nt + 2 t + e % 2
+#pragma unroll
+      for (int i = 0; i < 4; ++i) nk[i] = finite_or_nan(nk[i]);
       const int tok0 = base + c * kChunk + 32 * warp + g;
       float w4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -411,11 +420,10 @@ __global__ void __launch_bounds__(kThreads) attn_mass_kernel(const __grid_consta
           }
           if (mp.pass == 0) {
             const float mx = fmaxf(fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])), m_[nt][e1]);
-            if (mx > -INFINITY) {
-              l_[nt][e1] = l_[nt][e1] * ex2(m_[nt][e1] - mx) + ((ex2(x[0] - mx) + ex2(x[1] - mx)) +
-                                                               (ex2(x[2] - mx) + ex2(x[3] - mx)));
-              m_[nt][e1] = mx;
-            }
+            const float rf = mx > -INFINITY ? mx : 0.f;  // a NaN reaches the sum, whatever the maximum is
+            l_[nt][e1] = l_[nt][e1] * ex2(m_[nt][e1] - rf) + ((ex2(x[0] - rf) + ex2(x[1] - rf)) +
+                                                             (ex2(x[2] - rf) + ex2(x[3] - rf)));
+            m_[nt][e1] = mx;
           } else {
             const float lse = ms.lse[r];
 #pragma unroll
@@ -442,7 +450,7 @@ __global__ void __launch_bounds__(kThreads) attn_mass_kernel(const __grid_consta
           for (int x = 4; x < 32; x <<= 1) {
             const float mo = __shfl_xor_sync(0xffffffffu, m, x), so = __shfl_xor_sync(0xffffffffu, s, x);
             const float mx = fmaxf(m, mo);
-            s = mx > -INFINITY ? s * ex2(m - mx) + so * ex2(mo - mx) : 0.f;
+            s = mx > -INFINITY ? s * ex2(m - mx) + so * ex2(mo - mx) : s + so;
             m = mx;
           }
           if (g == 0) ms.part[warp][8 * nt + 2 * t + e1] = make_float2(m, s);
@@ -451,8 +459,7 @@ __global__ void __launch_bounds__(kThreads) attn_mass_kernel(const __grid_consta
       if (tid < R) {
         float m = -INFINITY, s = 0.f;
         for (int w = 0; w < 4; ++w) m = fmaxf(m, ms.part[w][tid].x);
-        if (m > -INFINITY)
-          for (int w = 0; w < 4; ++w) s += ms.part[w][tid].y * ex2(ms.part[w][tid].x - m);
+        for (int w = 0; w < 4; ++w) s += ms.part[w][tid].y * (m > -INFINITY ? ex2(ms.part[w][tid].x - m) : 1.f);
         mp.ml[(unit * S + split) * rows_pad + rb * R + tid] = make_float2(m, s);
       }
     }

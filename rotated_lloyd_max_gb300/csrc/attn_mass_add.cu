@@ -48,9 +48,10 @@ __global__ void __launch_bounds__(kAddThreads) attn_mass_add_kernel(const __grid
     for (int s = lane; s < S; s += 32) {
       const float2 v = ml[s * 8];
       if (v.y > 0.f) W += v.y * exp2f(v.x - M);
+      else if (v.y != v.y) W = v.y;
     }
     W = warp_sum(W);
-    if (lane == 0) lse[warp] = W > 0.f ? M + log2f(W) : INFINITY;  // a row that sees nothing weighs nothing
+    if (lane == 0) lse[warp] = log_sum(M, W, row_limit(p, cl, query_len(p, b), warp));
   }
   __syncthreads();
 #pragma unroll
@@ -60,7 +61,7 @@ __global__ void __launch_bounds__(kAddThreads) attn_mass_add_kernel(const __grid
     float s = 0.f;
 #pragma unroll
     for (int q = 0; q < P; ++q)
-      if (q < mp.rows && lse[q] < INFINITY) s += ex2(x[k][q] - lse[q]);
+      if (q < mp.rows && lse[q] != INFINITY) s += ex2(x[k][q] - lse[q]);
     m[i] = fmaf(mp.decay, old[k], s);
   }
 }

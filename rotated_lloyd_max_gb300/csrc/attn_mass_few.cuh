@@ -281,13 +281,14 @@ __global__ void __launch_bounds__(kThreads, 5) attn_mass_few_kernel(const __grid
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int tok = c * kChunk + 32 * warp + 8 * i + g;
+      const float n = finite_or_nan(nk[i]);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         float v = acc[i >> 1][2 * (i & 1) + e] * (e ? q1 : q0);
         if constexpr (OUTL) {
           if (!dense) v = fmaf(reinterpret_cast<const float*>(sm + mp.sm_corr)[(warp * 32 + 8 * i + g) * 9 + r0 + e], p.sscale, v);
         }
-        x[i][e] = mass_logit(p, v, nk[i], base + tok < (e ? lim1 : lim0));
+        x[i][e] = mass_logit(p, v, n, base + tok < (e ? lim1 : lim0));
       }
       if (writes) {
         float* dst = keep + (int64_t)tok * pitch;
@@ -297,13 +298,20 @@ __global__ void __launch_bounds__(kThreads, 5) attn_mass_few_kernel(const __grid
     }
     const float a0 = fmaxf(fmaxf(fmaxf(x[0][0], x[1][0]), fmaxf(x[2][0], x[3][0])), m0);
     const float a1 = fmaxf(fmaxf(fmaxf(x[0][1], x[1][1]), fmaxf(x[2][1], x[3][1])), m1);
+    // a NaN reaches the sums, whatever the maxima are
     if (a0 > -INFINITY) {
       l0 = l0 * ex2(m0 - a0) + ((ex2(x[0][0] - a0) + ex2(x[1][0] - a0)) + (ex2(x[2][0] - a0) + ex2(x[3][0] - a0)));
       m0 = a0;
+    } else {
+      const float y = (x[0][0] + x[1][0]) + (x[2][0] + x[3][0]);
+      if (y != y) l0 = y;
     }
     if (a1 > -INFINITY) {
       l1 = l1 * ex2(m1 - a1) + ((ex2(x[0][1] - a1) + ex2(x[1][1] - a1)) + (ex2(x[2][1] - a1) + ex2(x[3][1] - a1)));
       m1 = a1;
+    } else {
+      const float y = (x[0][1] + x[1][1]) + (x[2][1] + x[3][1]);
+      if (y != y) l1 = y;
     }
     if (!dense) {
 #pragma unroll
@@ -319,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 5) attn_mass_few_kernel(const __grid
     for (int k = 4; k < 32; k <<= 1) {
       const float mo = __shfl_xor_sync(0xffffffffu, m, k), so = __shfl_xor_sync(0xffffffffu, s, k);
       const float mx = fmaxf(m, mo);
-      s = mx > -INFINITY ? s * ex2(m - mx) + so * ex2(mo - mx) : 0.f;
+      s = mx > -INFINITY ? s * ex2(m - mx) + so * ex2(mo - mx) : s + so;
       m = mx;
     }
     if (g == 0 && (!packed || t < 2)) ms.part[warp][r0 + e] = make_float2(m, s);
@@ -329,8 +337,7 @@ __global__ void __launch_bounds__(kThreads, 5) attn_mass_few_kernel(const __grid
     float m = -INFINITY, s = 0.f;
     if (!packed || tid < 4) {
       for (int k = 0; k < 4; ++k) m = fmaxf(m, ms.part[k][tid].x);
-      if (m > -INFINITY)
-        for (int k = 0; k < 4; ++k) s += ms.part[k][tid].y * ex2(ms.part[k][tid].x - m);
+      for (int k = 0; k < 4; ++k) s += ms.part[k][tid].y * (m > -INFINITY ? ex2(ms.part[k][tid].x - m) : 1.f);
     }
     ml[tid] = make_float2(m, s);
   }

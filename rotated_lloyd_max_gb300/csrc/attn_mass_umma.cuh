@@ -202,8 +202,7 @@ __device__ __forceinline__ void mass_umma_body(const MassParams& mp, unsigned ch
       }
       W += __shfl_xor_sync(0xffffffffu, W, 1);
       W += __shfl_xor_sync(0xffffffffu, W, 2);
-      // a row of no query, or one that sees nothing, weighs nothing
-      if ((tid & 3) == 0) ms.st[0][r].x = row < tb * p.G && (W > 0.f || W != W) ? M + log2f(W) : INFINITY;
+      if ((tid & 3) == 0) ms.st[0][r].x = log_sum(M, W, row < tb * p.G ? row_limit(p, cl, tb, row) : 0);
     }
     fence_async_smem();
     tc_fence_before();
@@ -388,7 +387,8 @@ __device__ __forceinline__ void mass_umma_body(const MassParams& mp, unsigned ch
         const uint32_t g = done + i, sb = g % 3;
         const uint32_t tB = tS + 128 * sb + lrow;
         __syncwarp();
-        *reinterpret_cast<float4*>(&ms.nk[warp][4 * lane]) = nk;
+        *reinterpret_cast<float4*>(&ms.nk[warp][4 * lane]) =
+            make_float4(finite_or_nan(nk.x), finite_or_nan(nk.y), finite_or_nan(nk.z), finite_or_nan(nk.w));
         __syncwarp();
         if (i + 2 < n) nk = norms(i + 2);
         mbar_wait_idle(&ms.s_full[sb], (g / 3) & 1, abort_f);
@@ -431,7 +431,7 @@ __device__ __forceinline__ void mass_umma_body(const MassParams& mp, unsigned ch
             m = fmaxf(m, v[31]);
             m = m > -INFINITY ? m * ff : -INFINITY;
             if (m > ref + kMuMargin) {
-              lsum = ref > -INFINITY ? lsum * ex2(ref - m) : 0.f;
+              if (ref > -INFINITY) lsum *= ex2(ref - m);  // else it is zero or NaN
               ref = m;
             }
             const float rr = ref > -INFINITY ? ref : 0.f;
@@ -477,7 +477,7 @@ __device__ __forceinline__ void mass_umma_body(const MassParams& mp, unsigned ch
     if (mp.pass == 0 && tid < 128) {
       const float2 x = ms.st[0][tid], y = ms.st[1][tid];
       const float m = fmaxf(x.x, y.x);
-      float w = m > -INFINITY ? x.y * ex2(x.x - m) + y.y * ex2(y.x - m) : 0.f;
+      float w = m > -INFINITY ? x.y * ex2(x.x - m) + y.y * ex2(y.x - m) : x.y + y.y;
       if (*abort_f) w = __int_as_float(0x7fc00000);
       mp.ml[((unit * mp.nrb + tile) * S + sidx) * 128 + tid] = make_float2(m, tid < rn ? w : 0.f);
     }

@@ -1,7 +1,8 @@
-"""GPU tests of NaN and infinities that a query does see, in the several-query attention: the rows
-concerned come out NaN, the others as with clean inputs."""
+"""GPU tests of NaN and infinities that a query does see, in the several-query attention and the
+accumulated weights: the rows concerned come out NaN on every route, the others as with clean inputs."""
 import math
 
+import numpy as np
 import pytest
 
 import tq_testlib as tl
@@ -106,3 +107,61 @@ def test_attention_whose_logits_are_all_minus_infinity(tq, orc, d):
     c.ring["k"].fill_(1.0)
     out = _attend(tq, c, q)
     assert torch.all(out[0, 0, :10] == 0) and torch.isnan(out[0, 0, 10:]).all()
+
+
+# rows of a kv head: up to 8, 9 to 40, more; head dim 256 has no tcgen05 route
+ROUTES = [(128, 1, 4), (128, 2, 4), (512, 1, 6), (64, 5, 4), (128, 5, 4), (256, 20, 3), (64, 30, 3), (128, 30, 3)]
+
+
+def _weigh(tq, c, q, mass0, **kw):
+    import torch
+    mass = mass0.clone()
+    tq.attn_mass(k_codec=c.kc, mass=mass, q=q, scale=1.0, decay=0.5, **kw, **c.kw(values=False))
+    torch.cuda.synchronize()
+    return mass
+
+
+@pytest.mark.parametrize("outliers", [0.0, 2.0])
+@pytest.mark.parametrize("splits", [0, 1, 4])
+@pytest.mark.parametrize("d,rows_t,group", ROUTES)
+def test_weights_of_what_is_not_finite(tq, orc, d, rows_t, group, splits, outliers):
+    """A row without a finite softmax leaves NaN in every entry of its kv head below total, whichever way
+    the rows are laid out; entries behind it and the other kv heads are as with clean inputs."""
+    import torch
+    c = _cache(tq, orc, d, T=outliers)
+    total = 7 * 128 + 150
+    g = np.random.default_rng(3)
+    mass0 = torch.from_numpy(g.random((1, 1, 2, total + 9)).astype(np.float32)).cuda()
+    q = tl.to_bf16_tensor(queries(1, 1, rows_t, 2 * group, d, 8), "cuda")
+    clean = _weigh(tq, c, q, mass0, splits=splits)
+    assert torch.isfinite(clean).all()
+
+    def check(mass, h):
+        assert torch.isnan(mass[0, 0, h, :total]).all()
+        assert torch.equal(mass[0, 0, h, total:], mass0[0, 0, h, total:])
+        assert torch.equal(mass[0, 0, 1 - h], clean[0, 0, 1 - h])
+
+    bad = q.clone()
+    bad[0, 0, rows_t - 1, 1, d - 1] = math.nan
+    check(_weigh(tq, c, bad, mass0, splits=splits), 0)
+    keys = c.rec["k"].clone()
+    for value in (math.nan, math.inf, -math.inf):
+        for record, slot in ((0, 0), (3, 100)):
+            c.rec["k"].copy_(keys)
+            _put_scale(c, "k", 3, 1, record, slot, value)
+            check(_weigh(tq, c, q, mass0, splits=splits), 1)
+    c.rec["k"].copy_(keys)
+    c.ring["k"][0, 0, 0, (int(c.start[0, 0]) + 140) % c.cap, 1] = math.nan
+    check(_weigh(tq, c, q, mass0, splits=splits), 0)
+
+
+@pytest.mark.parametrize("d,rows_t,group", [(128, 1, 4), (128, 5, 4), (128, 30, 3)])
+def test_weights_whose_logits_are_all_minus_infinity(tq, orc, d, rows_t, group):
+    """Rows that see tokens of no finite logit leave NaN; where no row sees a token, the decay alone is applied."""
+    import torch
+    c = _cache(tq, orc, d, n=0, tail=40, B=2, lens=(0, [[40, 0]]))
+    q = torch.zeros((1, 2, rows_t, 2 * group, d), dtype=torch.bfloat16, device="cuda")
+    q[..., 3] = -math.inf
+    c.ring["k"].fill_(1.0)
+    mass = _weigh(tq, c, q, torch.ones((1, 2, 2, 41), device="cuda"))
+    assert torch.isnan(mass[0, 0, :, :40]).all() and torch.all(mass[0, 0, :, 40:] == 1) and torch.all(mass[0, 1] == 1)
