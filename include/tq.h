@@ -559,7 +559,8 @@ tq_status tq_attn_mass(const tq_query_args* args, const tq_codec* k_codec, float
  * In place (k_dst == k_rec, and v_dst, mass_dst, n_chunks_dst likewise equal
  * to their sources, dst fields of the layout ignored): the entries of mass
  * behind the remaining tokens become 0, dropped records keep their bytes;
- * with a block table every block named must belong to one sequence only.
+ * with a block table every block named must belong to one sequence only; the
+ * layers of the records may not overlap.
  * Out of place: the destination must not overlap the source; only records
  * below n_chunks_dst and entries of remaining tokens are written.
  */

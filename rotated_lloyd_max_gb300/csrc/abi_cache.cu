@@ -449,16 +449,21 @@ tq_status evict_mass_params(const tq_evict_mass_args* a, const tq_codec* kcod, c
       !layers_apart(a->n_layers, a->mass_layer_stride, (int64_t)a->batch * a->n_kv_heads * a->mass_cap))
     return TQ_ERR_INVALID_ARG;
   const int kept = std::min(a->keep_chunks, std::max(a->max_chunks, 1));  // records that can remain
-  if (!in_place) {
+  // a layer's records follow one another (pages: at least its own blocks are there)
+  auto records_apart = [&](const int32_t* table, int cap, int64_t k_ls, int64_t v_ls) {
+    const int64_t heads = (table ? 1 : (int64_t)a->batch * cap) * a->n_kv_heads;
+    return layers_apart(a->n_layers, k_ls, heads * p->kc.rec_bytes) &&
+           (shared || layers_apart(a->n_layers, v_ls, heads * p->vc.rec_bytes));
+  };
+  if (in_place) {  // the source is written
+    if (!records_apart(a->block_table, a->rec_cap, a->k_rec_layer_stride, a->v_rec_layer_stride))
+      return TQ_ERR_INVALID_ARG;
+  } else {
     if (a->dst_cap <= 0 || (a->dst_table && a->dst_table_stride <= 0) || a->k_dst_layer_stride % 16 ||
         a->v_dst_layer_stride % 16 || a->mass_dst_layer_stride < 0 ||
         !layers_apart(a->n_layers, a->mass_dst_layer_stride, (int64_t)a->batch * a->n_kv_heads * a->mass_dst_cap))
       return TQ_ERR_INVALID_ARG;
-    // a layer's records follow one another (pages: at least its destination's blocks are there)
-    const int64_t heads = (a->dst_table ? 1 : (int64_t)a->batch * a->dst_cap) * a->n_kv_heads;
-    if (!layers_apart(a->n_layers, a->k_dst_layer_stride, heads * p->kc.rec_bytes) ||
-        !layers_apart(a->n_layers, a->v_dst_layer_stride, heads * p->vc.rec_bytes))
-      return TQ_ERR_INVALID_ARG;
+    if (!records_apart(a->dst_table, a->dst_cap, a->k_dst_layer_stride, a->v_dst_layer_stride)) return TQ_ERR_INVALID_ARG;
     if ((a->dst_table ? a->dst_table_stride : a->dst_cap) < std::min(a->keep_chunks, a->max_chunks) ||
         a->mass_dst_cap < (int64_t)TQ_CHUNK * std::min(a->keep_chunks, a->max_chunks) + a->max_tail)
       return TQ_ERR_INVALID_ARG;

@@ -258,3 +258,30 @@ def test_outputs_that_overlap_themselves_are_refused(tq):
                dict(v_dst_layer_stride=4 * 4 * (128 * 128 * 2 // 8 + 512) - 16)):
         a = _evict(tq, **dict(two, **kw))
         assert L.tq_evict_mass(ctypes.byref(a), ctypes.byref(kc), ctypes.byref(vc), ws, 1 << 40, None) == INV
+
+
+@pytest.mark.parametrize("shared", [False, True])
+@pytest.mark.parametrize("paged", [False, True])
+def test_layers_that_overlap_in_place_are_refused(tq, shared, paged):
+    """In place the source is the destination: two layers in the same records would be compacted at once."""
+    L, kc, vc, ws = tq.load(), _codec(tq), _codec(tq, bits=3 if shared else 2), ctypes.c_void_p(0x1000000)
+    heads = 2 if paged else 2 * 8 * 2
+    kb, vb = ((128 * 128 * b // 8 + 512) * heads for b in (3, 3 if shared else 2))
+    kw = dict(n_layers=2, mass_layer_stride=4 * (8 * 128 + 16), k_rec_layer_stride=kb, v_rec_layer_stride=vb)
+    if paged:
+        kw.update(block_table=0x800000, table_stride=8)
+    if shared:
+        kw.update(v_rec=0x100000, v_dst=0x100000)
+
+    def size(**more):
+        a = _evict(tq, True, **dict(kw, **more))
+        n = L.tq_evict_mass_workspace_size(ctypes.byref(a), ctypes.byref(kc), ctypes.byref(vc))
+        if n == 0:
+            assert L.tq_evict_mass(ctypes.byref(a), ctypes.byref(kc), ctypes.byref(vc), ws, 1 << 40, None) == INV
+        return n
+
+    assert size() > 0
+    assert size(k_rec_layer_stride=kb - 16) == 0 and size(k_rec_layer_stride=0) == 0
+    if not shared:
+        assert size(v_rec_layer_stride=vb - 16) == 0 and size(v_rec_layer_stride=0) == 0
+    assert size(n_layers=1, k_rec_layer_stride=0, v_rec_layer_stride=0) > 0
