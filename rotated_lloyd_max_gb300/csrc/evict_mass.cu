@@ -329,18 +329,19 @@ __global__ void __launch_bounds__(kMoveThreads) mass_compact_kernel(const __grid
     const int live = left * kChunk, all = live + len, was = n * kChunk;
     auto source = [&](int i) { return i < live ? list[i] : was + (i - live); };
     constexpr int PER = 8;
-    const int step = (int)gridDim.x * kMoveThreads * PER;
-    for (int i0 = 0; i0 < all; i0 += step) {
+    const int64_t step = (int64_t)gridDim.x * kMoveThreads * PER;  // past 32 bits from 2^20 records on
+    for (int64_t i0 = 0; i0 < all; i0 += step) {
+      const int64_t at = i0 + (int64_t)blockIdx.x * PER * kMoveThreads + tid;
       float v[PER];
 #pragma unroll
       for (int k = 0; k < PER; ++k) {
-        const int i = i0 + (blockIdx.x * PER + k) * kMoveThreads + tid;
-        v[k] = i < all ? m[source(i)] : 0.f;
+        const int64_t i = at + k * kMoveThreads;
+        v[k] = i < all ? m[source((int)i)] : 0.f;
       }
       if constexpr (INPLACE) cg::this_cluster().sync();
 #pragma unroll
       for (int k = 0; k < PER; ++k) {
-        const int i = i0 + (blockIdx.x * PER + k) * kMoveThreads + tid;
+        const int64_t i = at + k * kMoveThreads;
         if (i < all) d[i] = v[k];
       }
     }

@@ -305,3 +305,32 @@ def test_streams_longer_than_a_cluster_keeps(tq, in_place, n):
     assert torch.equal(md[:128 * keep], mass[0, 0, 0, best])
     assert torch.equal(md[128 * keep:128 * keep + 77], mass[0, 0, 0, 128 * n:])
     assert torch.all(md[128 * keep + 77:128 * n + 77] == 0)
+
+
+def test_more_than_a_million_records_remain(tq):
+    """2^20 + 2 records of one stream with side lists, into another cache: 134 million tokens remain."""
+    import torch
+    n, keep, d = (1 << 20) + 5, (1 << 20) + 2, 64
+    kc = tq.tq_make_codebook(1, d, outlier_T=3.0, outlier_cap=8)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(1)
+    rec = torch.zeros((1, 1, 1, n, kc.record_bytes), dtype=torch.uint8, device="cuda")
+    rec[..., :1536].random_(0, 256, generator=g)  # codes and scales; no entries
+    mass = torch.ones((1, 1, 1, 128 * n + 9), device="cuda")
+    gone = torch.randperm(128 * n, device="cuda", generator=g)[:128 * (n - keep)]
+    mass[0, 0, 0, gone] = 0.0
+    cnt = torch.full((1, 1), n, dtype=torch.int32, device="cuda")
+    ln = torch.full((1, 1), 9, dtype=torch.int32, device="cuda")
+    dst = torch.zeros((1, 1, 1, keep, kc.record_bytes), dtype=torch.uint8, device="cuda")
+    mass_dst = torch.zeros((1, 1, 1, 128 * keep + 9), device="cuda")
+    n_dst = torch.zeros_like(cnt)
+    kept = torch.zeros((1, 1, 1, 128 * keep), dtype=torch.int32, device="cuda")
+    tq.evict_mass(k_codec=kc, k_rec=rec, v_rec=rec, mass=mass, n_chunks=cnt, max_chunks=n, keep_chunks=keep, kept=kept,
+                  tail_len=ln, max_tail=9, k_dst=dst, v_dst=dst, mass_dst=mass_dst, n_chunks_dst=n_dst)
+    assert int(n_dst) == keep and torch.all(mass_dst == 1)
+    best = mass[0, 0, 0, :128 * n].nonzero().view(-1)
+    assert torch.equal(kept[0, 0, 0].long(), best)
+    for lo, hi, row in ((0, 1024, 8), (1024, 1536, 4)):
+        rows = rec[0, 0, 0, :, lo:hi].reshape(-1, row)[best].view(keep, hi - lo)
+        assert torch.equal(dst[0, 0, 0, :, lo:hi], rows)
+    assert not dst[0, 0, 0, :, 1536:1664].any()
