@@ -42,6 +42,11 @@ inline bool strides_ok(int64_t a, int64_t b, int64_t c) {
   return a >= 0 && b >= 0 && c >= 0 && a % 8 == 0 && b % 8 == 0 && c % 8 == 0;
 }
 
+// Tokens of a sequence.  Indices are 32-bit, and kernels count past the last
+// token by less than 2^20: to the end of the last split (fewer than 128 records
+// behind, the split counts being at most 128) or of a block's last batch (8192).
+constexpr int64_t kMostTokens = (1ll << 31) - (1 << 20);
+
 // what a call writes must not overlap itself: along every axis longer than one
 // a step is at least a row of `row` elements
 inline bool rows_apart(int64_t ls, int64_t bs, int64_t ts, int L, int B, int T, int64_t row) {
@@ -202,8 +207,7 @@ tq_status query_params(const tq_query_args* a, const tq_codec* kcod, const tq_co
   } else if (a->v_tail || a->tail_len || a->tail_start || a->max_tail) {
     return TQ_ERR_INVALID_ARG;
   }
-  // token indices are 32-bit
-  if ((int64_t)a->max_chunks * TQ_CHUNK + a->max_tail > 0x7FFFFFFFll - 2 * TQ_CHUNK) return TQ_ERR_UNSUPPORTED;
+  if ((int64_t)a->max_chunks * TQ_CHUNK + a->max_tail > kMostTokens) return TQ_ERR_UNSUPPORTED;
   p->L = a->n_layers;
   p->B = a->batch;
   p->T = a->t_q;
@@ -280,7 +284,9 @@ tq_status prefill_plan(const tq_query_args* a, const tq_codec* kcod, const tq_co
       pp.St = (int)st;
     }
   }
-  if (U * (pp.Sc + pp.St) > 0x7FFFFFFFll || units * pp.rows > (1ll << 32)) return TQ_ERR_UNSUPPORTED;
+  // the grids of the attention and of the merge of its splits
+  const int64_t merges = d <= 128 ? 16 * units * cdiv(pp.rows, 128) : cdiv(units * pp.rows, 4);
+  if (U * (pp.Sc + pp.St) > 0x7FFFFFFFll || merges > 0x7FFFFFFFll) return TQ_ERR_UNSUPPORTED;
   pp.out = (uint16_t*)a->out;
   pp.o_ls = a->out_layer_stride;
   pp.o_bs = a->out_batch_stride;
@@ -444,7 +450,7 @@ tq_status evict_mass_params(const tq_evict_mass_args* a, const tq_codec* kcod, c
   if (a->max_chunks > limit) return TQ_ERR_INVALID_ARG;
   if ((int64_t)a->sink + a->recent > (int64_t)TQ_CHUNK * a->keep_chunks) return TQ_ERR_INVALID_ARG;
   const int64_t most = (int64_t)TQ_CHUNK * a->max_chunks + a->max_tail;
-  if (most > 0x7FFFFFFFll || (int64_t)TQ_CHUNK * a->keep_chunks > 0x7FFFFFFFll - a->max_tail) return TQ_ERR_UNSUPPORTED;
+  if (most > kMostTokens || (int64_t)TQ_CHUNK * a->keep_chunks > 0x7FFFFFFFll - a->max_tail) return TQ_ERR_UNSUPPORTED;
   if (a->mass_cap < most || a->mass_layer_stride < 0 ||
       !layers_apart(a->n_layers, a->mass_layer_stride, (int64_t)a->batch * a->n_kv_heads * a->mass_cap))
     return TQ_ERR_INVALID_ARG;

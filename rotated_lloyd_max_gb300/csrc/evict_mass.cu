@@ -453,21 +453,21 @@ cudaError_t launch_evict_mass(const EvictMassParams& p, cudaStream_t s) {
   // memory does not hold the keys.  (256 streams of 32768 tokens: 8 CTAs each
   // took 217 us, mostly for meetings of the histograms.)
   const int64_t streams = (int64_t)p.L * p.B * p.Hkv;
-  auto bytes = [&](int c) { return (p.max_chunks + c - 1) / c * kChunk * 4; };
+  auto bytes = [&](int c) { return (int64_t)((p.max_chunks + c - 1) / c) * kChunk * 4; };
   int C = 1;
   while (C < 8 && ((p.max_chunks > 32 * C && streams * C < sm_count()) || bytes(C) > 192 * 1024)) C *= 2;
-  const int smem = bytes(C);
-  const bool cached = smem <= 192 * 1024;
+  const bool cached = bytes(C) <= 192 * 1024;
+  const int smem = cached ? (int)bytes(C) : 0;
   auto kern = C > 1 ? (cached ? mass_select_kernel<true, true> : mass_select_kernel<false, true>)
                     : (cached ? mass_select_kernel<true, false> : mass_select_kernel<false, false>);
-  if (cached && smem + (int)sizeof(SelShared) > 48 * 1024) {
+  if (smem + (int)sizeof(SelShared) > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)(streams * C));
   cfg.blockDim = dim3(kSelThreads);
-  cfg.dynamicSmemBytes = cached ? smem : 0;
+  cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;

@@ -285,3 +285,36 @@ def test_layers_that_overlap_in_place_are_refused(tq, shared, paged):
     if not shared:
         assert size(v_rec_layer_stride=vb - 16) == 0 and size(v_rec_layer_stride=0) == 0
     assert size(n_layers=1, k_rec_layer_stride=0, v_rec_layer_stride=0) > 0
+
+
+def test_sizes_whose_indices_would_wrap_are_refused(tq):
+    """Token indices are 32-bit, with room for a launch's last threads and a split's length behind them; a
+    merge's grid has 2^31 - 1 blocks at most."""
+    L, kc, vc = tq.load(), _codec(tq, d=64, bits=1), _codec(tq, d=64, bits=1)
+    most = ((1 << 31) - (1 << 20)) // 128
+
+    def sizes(a):
+        return (L.tq_prefill_attn_workspace_size(ctypes.byref(a), ctypes.byref(kc), ctypes.byref(vc)),
+                L.tq_attn_mass_workspace_size(ctypes.byref(a), ctypes.byref(kc)))
+
+    def query(n, tail, **kw):
+        return _query(tq, **dict(dict(head_dim=64, batch=1, n_kv_heads=1, n_q_heads=1, t_q=1, max_chunks=n, rec_cap=max(n, 1),
+                                      max_tail=tail, tail_cap=max(tail, 1)), **kw))
+
+    assert all(sizes(query(most - 1, 0))) and all(sizes(query(most - 1, 128)))
+    assert sizes(query(most, 1)) == (0, 0) and sizes(query(most + 1, 0)) == (0, 0)
+    assert all(sizes(query(0, 128 * most))) and sizes(query(0, 128 * most + 1)) == (0, 0)
+    a = query(most + 1, 0)
+    ws = ctypes.c_void_p(0x1000000)
+    assert L.tq_prefill_attn(ctypes.byref(a), ctypes.byref(kc), ctypes.byref(vc), ws, 1 << 60, None) == UNS
+    # nothing cached, rows of 2^32 - 2^17 (layer, sequence, kv head) units: the merge alone would run
+    none = dict(k_rec=None, v_rec=None, n_chunks=None, k_tail=None, v_tail=None, tail_start=None, tail_len=None, rec_cap=0,
+                tail_cap=0, out_batch_stride=64, out_layer_stride=1 << 22, q_batch_stride=64, q_token_stride=64)
+    a = query(0, 0, n_layers=65535, batch=65535, **none)
+    assert L.tq_prefill_attn_workspace_size(ctypes.byref(a), ctypes.byref(kc), ctypes.byref(vc)) == 0
+    assert L.tq_prefill_attn(ctypes.byref(a), ctypes.byref(kc), ctypes.byref(vc), ws, 1 << 60, None) == UNS
+    b = dict(n_kv_heads=1, batch=1, max_tail=0, tail_len=None, keep_chunks=1, recent=0, sink=0, dst_cap=1)
+    ev = lambda n, **kw: L.tq_evict_mass_workspace_size(  # noqa: E731
+        ctypes.byref(_evict(tq, False, **dict(b, max_chunks=n, rec_cap=n, mass_cap=128 * n, mass_dst_cap=128, **kw))),
+        ctypes.byref(kc), ctypes.byref(vc))
+    assert ev(most) > 0 and ev(most + 1) == 0
