@@ -58,8 +58,8 @@ struct SelShared {
   uint32_t cta_gt, cta_eq;
 };
 
-// CACHED: the CTA's keys stay in shared memory (otherwise each pass reads the
-// weights again).  CLUSTER: several CTAs hold a stream; their histograms meet
+// CACHED: the CTA's keys stay in shared memory (otherwise, above 3072 records and
+// with a cluster, each pass reads the weights again).  CLUSTER: several CTAs hold a stream; their histograms meet
 // slice by slice, CTA r summing the r-th slice of the bins over all of them.
 template <bool CACHED, bool CLUSTER>
 __global__ void __launch_bounds__(kSelThreads, 1) mass_select_kernel(const __grid_constant__ EvictMassParams p) {
@@ -459,7 +459,7 @@ cudaError_t launch_evict_mass(const EvictMassParams& p, cudaStream_t s) {
   const bool cached = bytes(C) <= 192 * 1024;
   const int smem = cached ? (int)bytes(C) : 0;
   auto kern = C > 1 ? (cached ? mass_select_kernel<true, true> : mass_select_kernel<false, true>)
-                    : (cached ? mass_select_kernel<true, false> : mass_select_kernel<false, false>);
+                    : mass_select_kernel<true, false>;
   if (smem + (int)sizeof(SelShared) > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
