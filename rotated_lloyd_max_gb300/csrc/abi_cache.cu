@@ -27,7 +27,6 @@ TQ_DECL_DIM(512)
 cudaError_t launch_prefill_merge(const PrefillParams& pp, cudaStream_t s);
 cudaError_t launch_attn_mass_umma_d64(const MassParams& mp, cudaStream_t s);
 cudaError_t launch_attn_mass_umma_d128(const MassParams& mp, cudaStream_t s);
-constexpr int kMassUmmaPer = 48;  // 128-token tiles of a split of theirs at most
 cudaError_t launch_attn_mass_add(const MassParams& mp, cudaStream_t s);
 
 }  // namespace tq

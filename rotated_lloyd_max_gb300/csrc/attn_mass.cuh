@@ -30,6 +30,9 @@
 
 namespace tq {
 
+// 128-token tiles of a split on tcgen05 at most: their sums lie in shared memory (24 KB)
+constexpr int kMassUmmaPer = 48;
+
 struct MassParams {
   QueryParams q;
   int Sc, St;         // context splits over records and over ring tokens

@@ -34,8 +34,7 @@ template <int D>
 struct MuCfg {
   static constexpr int TILE = 128 * D * 2;  // one operand tile
   static constexpr int K = 0, LUT = 4 * TILE, MISC = LUT + 32768, SUMS = MISC + 11264;
-  static constexpr int MAXPER = 48;         // 128-token tiles per split (their sums: 24 KB)
-  static constexpr int SMEM = SUMS + MAXPER * 512 + 1024;
+  static constexpr int SMEM = SUMS + kMassUmmaPer * 512 + 1024;
 };
 
 struct MuMisc {
