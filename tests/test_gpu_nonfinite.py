@@ -165,3 +165,24 @@ def test_weights_whose_logits_are_all_minus_infinity(tq, orc, d, rows_t, group):
     c.ring["k"].fill_(1.0)
     mass = _weigh(tq, c, q, torch.ones((1, 2, 2, 41), device="cuda"))
     assert torch.isnan(mass[0, 0, :, :40]).all() and torch.all(mass[0, 0, :, 40:] == 1) and torch.all(mass[0, 1] == 1)
+
+
+@pytest.mark.parametrize("value", [math.inf, -math.inf])
+@pytest.mark.parametrize("d", [64, 128, 256, 512])
+def test_a_query_with_an_infinity(tq, orc, d, value):
+    """Its row is NaN in the attention, its kv head's entries in the weights (few rows and many); others as before."""
+    import torch
+    c = _cache(tq, orc, d)
+    q = tl.to_bf16_tensor(queries(1, 1, T, 2 * G, d, 9), "cuda")
+    bad = q.clone()
+    bad[0, 0, T - 1, 1, 5] = value
+    hit = torch.zeros((T, 2 * G), dtype=torch.bool, device="cuda")
+    hit[T - 1, 1] = True
+    clean, out = _attend(tq, c, q), _attend(tq, c, bad)
+    assert torch.isnan(out[0, 0][hit]).all() and torch.equal(out[0, 0][~hit], clean[0, 0][~hit])
+    total = 7 * 128 + 150
+    mass0 = torch.ones((1, 1, 2, total + 3), device="cuda")
+    for t in (2, 4, T):  # rows of a kv head: 6, 12, 36
+        x, y = _weigh(tq, c, q[:, :, -t:], mass0), _weigh(tq, c, bad[:, :, -t:], mass0)
+        assert torch.isnan(y[0, 0, 0, :total]).all() and torch.equal(y[0, 0, 1], x[0, 0, 1])
+        assert torch.all(y[0, 0, :, total:] == 1)

@@ -100,3 +100,57 @@ def test_equal_weights_that_round_alike(tq, orc, d):
     for i in range(2):
         e = np.abs(got[0, 0, :, i] - want) / np.abs(want)
         assert np.all(e <= 2.0 ** -8 + 2.0 ** -10), float(e.max())
+
+
+def _sinks(tq, orc, d, n, places, seed):
+    """A cache of one head, n records and 4 ring tokens: at `places` one token's key, at its full length times
+    a factor, and values of 0.03 of the others' norm; elsewhere keys of 0.05 and values with a part in common."""
+    import torch
+    c = Cache(tq, orc, B=1, Hkv=1, d=d, kb=4, vb=4, n=n, tail=4, seed=seed)
+    g = np.random.default_rng(d + seed)
+    x = 0.5 * g.standard_normal((1, n * 128, d)) + g.standard_normal(d)
+    tq.tq_encode(c.vc, tl.to_bf16_tensor(_bits(x), "cuda"), c.rec["v"].view(1, n, -1))
+    ks, vs, row = _scales(c, "k", 4), _scales(c, "v", 4), d // 2
+    first, full = next(iter(places)), ks.clone()
+    ks *= 0.05
+    for at, factor in places.items():
+        c.rec["k"][0, 0, 0, at // 128, at % 128 * row:(at % 128 + 1) * row] = c.rec["k"][0, 0, 0, first // 128, first % 128 * row:(first % 128 + 1) * row]
+        ks[at // 128, at % 128] = full[first // 128, first % 128] * factor
+        vs[at // 128, at % 128] *= 0.03
+    c.ring["k"].mul_(0.05)
+    c._host = {w: c.rec[w].cpu().numpy() for w in "kv"}
+    return c, first
+
+
+def _against(tq, c, at, gaps, softcap, splits):
+    import torch
+    d = c.d
+    k, v = c.vectors("k", 0, 0, 0), c.vectors("v", 0, 0, 0)
+    q = _bits((np.array(gaps)[:, None] * k[at] / (k[at] @ k[at])).reshape(1, 1, 2, 2, d))
+    out = torch.zeros((1, 1, 2, 2, d), dtype=torch.bfloat16, device="cuda")
+    tq.prefill_attn(k_codec=c.kc, v_codec=c.vc, q=tl.to_bf16_tensor(q, "cuda"), out=out, scale=1.0, softcap=softcap,
+                    splits=splits, **c.kw())
+    got = synth.bf16_bits_to_f32(tl.bf16_tensor_bits(out)).astype(np.float64)
+    qf = synth.bf16_bits_to_f32(q).astype(np.float64)
+    for i in range(2):
+        w = weights(qf[0, 0, :, i], k, 2, len(k), True, softcap, 1.0)
+        want = w @ v
+        e = np.linalg.norm(got[0, 0, :, i] - want, axis=-1) / np.linalg.norm(want, axis=-1)
+        assert np.all(e <= 2.0 ** -8), (e, w[:, at])
+
+
+@pytest.mark.parametrize("softcap", [40.0, 400.0])
+@pytest.mark.parametrize("d", [64, 128, 256, 512])
+def test_one_token_takes_most_of_the_weight_under_a_cap(tq, orc, d, softcap):
+    """As the first test, over 8192 tokens and with logits capped (below and above 177, two forms of the cap)."""
+    c, at = _sinks(tq, orc, d, 64, {40: 1.0}, 35)
+    _against(tq, c, at, [12.0, 13.0, 14.0, 16.0], softcap, 1)
+
+
+@pytest.mark.parametrize("splits", [0, 1, 2])
+@pytest.mark.parametrize("d", [64, 128, 256, 512])
+def test_references_move_up_and_down(tq, orc, d, splits):
+    """Tokens that dominate come and go: logits of 9, 12, 10 and 13 times a row's gain of 0.9 to 1.2 above 6144
+    flat ones, in single records far apart and in neighbouring ones."""
+    c, at = _sinks(tq, orc, d, 48, {5: 0.75, 900: 1.0, 4000: 0.83, 4001: 0.5, 4130: 1.08}, 36)
+    _against(tq, c, at, [10.0, 11.0, 12.0, 13.3], 0.0, splits)
