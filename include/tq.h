@@ -498,22 +498,25 @@ typedef struct {
 /*
  * Attention of several query tokens per sequence over records and ring:
  *   out[l][b][t][h] = sum_i softmax_i(cap(scale q . k_i)) v_i
- * over the tokens that query sees, rounded once to bf16.  The records'
- * operands are f16 (centroids, rotated queries, weights, and at head dims 64
- * and 128 the per-vector scales, each within half an f16 step; f32
- * accumulation and softmax statistics); the ring's bf16 keys, values and
- * queries enter exactly, its weights rounded to bf16 and summed so: the output is within
- * bf16's own precision of the exact sum, also where one token holds nearly all
- * of a row's weight and the others' values make the output (what f16 drops of 128
- * tokens' weights is under 2^-16 of the row's largest).  Scales below 2^-24 of the largest
- * finite one of the same context split round to zero.  A row that sees no token is
- * zero; rows t >= T_b are not touched.  Slots and records that hold no token
- * are never read, and keys of tokens a query does not see do not touch its row
- * in any other way, NaN and infinities included; the VALUES of all tokens below total have to be finite
- * (a weight of zero times an infinity is NaN, for a later query's token too).  A row whose
- * query holds a NaN or an infinity, or that sees a key of a NaN or of a scale that is not finite, is NaN, and so is one
- * that sees tokens of no finite logit (infinities of queries and keys in the ring under a soft cap may count
- * as the cap).
+ * over the tokens that query sees, rounded once to bf16. The records' operands
+ * are f16 (centroids, rotated queries, weights, and at head dims 64 and 128 the
+ * per-vector scales, each within half an f16 step; f32 accumulation and softmax
+ * statistics); the ring's bf16 keys, values and queries enter exactly, its
+ * weights rounded to bf16 and summed so: the output is within bf16's own
+ * precision of the exact sum, also where one token holds nearly all of a row's
+ * weight and the others' values make the output (what f16 drops of 128 tokens'
+ * weights is under 2^-16 of the row's largest). Scales below 2^-24 of the
+ * largest finite one of the same context split round to zero, and at head dims
+ * 256 and 512, where a weight enters times its value's scale, values whose scale
+ * is far below the largest (2^-8 and less) lose bits with it.
+ * A row that sees no token is zero; rows t >= T_b are not touched. Slots and
+ * records that hold no token are never read, and keys of tokens a query does not
+ * see do not touch its row in any other way, NaN and infinities included; the
+ * VALUES of all tokens below total have to be finite (a weight of zero times an
+ * infinity is NaN, for a later query's token too). A row whose query holds a NaN
+ * or an infinity, or that sees a key of a NaN or of a scale that is not finite,
+ * is NaN, and so is one that sees tokens of no finite logit (infinities of
+ * queries and keys in the ring under a soft cap may count as the cap).
  * The kernels bound every internal wait (about two seconds); if one expires (a
  * fault of the device, not of the arguments) the rows concerned are NaN.
  * out may not overlap itself (strides as for q_out above).

@@ -317,7 +317,11 @@ tq_status mass_plan(const tq_query_args* a, const tq_codec* kcod, MassPlan* pl) 
   const int64_t units = (int64_t)q.L * q.B * q.Hkv, sms = sm_count();
   const int bits = q.krec ? q.kc.bits : 1;
   pl->few = mp.rows <= 8;
-  // 128 rows cost the tensor cores as much as 40 do on mma.sync (four times slower a product)
+  // Up to 8 rows the logits are kept (8 sequences of 32768, 8 kv heads: 8 rows 95 us, 461
+  // with the scores formed twice).  A tile of 128 rows costs the tensor cores what
+  // 40 rows cost mma.sync (a quarter of the rate), beside a set-up of its own: 18 rows of 2 kv heads
+  // over 4096 take 25 us on mma.sync and 29 on tcgen05, 36 rows 40 and 29, 54 rows 46 and 31;
+  // over 32768 with 8 kv heads, 12 rows 116 and 69, 40 rows 218 and 69, 48 rows 221 and 69.
   pl->umma = mp.rows > 40 && q.D <= 128;
   const int64_t ring = cdiv(q.max_tail, TQ_CHUNK);
   if (pl->few) {
@@ -366,8 +370,11 @@ tq_status mass_plan(const tq_query_args* a, const tq_codec* kcod, MassPlan* pl) 
   } else {
     pl->NT = outl ? 2 : mp.rows <= 32 ? 4 : 8;
     mp.nrb = (int)cdiv(mp.rows, 8 * pl->NT);
-    // CTAs of the first pass for about two waves of four per SM; at most 32
-    // records or ring tiles of 128 tokens a split (their sums sit in shared memory)
+    // Eight CTAs per SM for the first pass (splits x row blocks), of which shared
+    // memory holds one (head dim 512, 170 KB) to four at a time; at most 32 records or
+    // ring tiles of 128 tokens a split (their sums sit in shared memory).  The second
+    // pass has a CTA a split, which walks the row blocks: few where those are many
+    // (32 tokens of one kv head of 64, head dim 512, over 32768: 1280 CTAs, then 40; 4.6 ms).
     const int64_t want = a->splits > 0 ? a->splits : cdiv(8 * sms, units * mp.nrb);
     if (q.max_chunks > 0) {
       mp.cps = (int)std::min<int64_t>(32, cdiv(q.max_chunks, std::min<int64_t>(want, q.max_chunks)));

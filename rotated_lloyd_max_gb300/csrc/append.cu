@@ -14,7 +14,9 @@
 // tokens to fill the SMs) and keeps the table in shared memory.  A thread
 // moves units of two 16-byte chunks, the two halves of eight pairs, so that
 // the rotation needs no exchange and may run in place.  Four prompts of up to 4099
-// tokens, 48 heads of 128: 54 us, 5.6 TB/s; one token 4.6 us, two launches' latency.
+// tokens, 48 heads of 128: 54 us, 5.6 TB/s.  One token: 3.0 us from a graph, a launch
+// and one chain behind it (lengths, inv_freq, angle, barrier, and only then the loads);
+// with the counters in place, which a second launch moves, 3.7 us.
 #include "cache_params.h"
 #include "tq_common.cuh"
 

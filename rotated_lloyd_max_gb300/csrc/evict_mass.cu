@@ -58,9 +58,10 @@ struct SelShared {
   uint32_t cta_gt, cta_eq;
 };
 
-// CACHED: the CTA's keys stay in shared memory (otherwise, above 3072 records and
-// with a cluster, each pass reads the weights again).  CLUSTER: several CTAs hold a stream; their histograms meet
-// slice by slice, CTA r summing the r-th slice of the bins over all of them.
+// CACHED: the CTA's keys stay in shared memory (otherwise, where a cluster of eight
+// cannot keep them, each pass reads the weights again).  CLUSTER: several CTAs hold
+// a stream; their histograms meet slice by slice, CTA r summing the r-th slice of
+// the bins over all of them.
 template <bool CACHED, bool CLUSTER>
 __global__ void __launch_bounds__(kSelThreads, 1) mass_select_kernel(const __grid_constant__ EvictMassParams p) {
   __shared__ SelShared sh;

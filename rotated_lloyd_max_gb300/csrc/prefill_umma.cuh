@@ -21,15 +21,16 @@
 // The softmax subtracts a reference that stays while a tile's largest weight lies
 // between 2^kPfLow and 2^kPfMargin, so that scores are read once and O is hardly
 // ever rescaled (by the warps that own the rows; a warp that rescales holds the
-// whole CTA up for about 3000 cycles), and else moves to where that weight is 2^kPfTop.
-// Weights are f16: 11 bits down to 2^-14, to within 2^-25 below, so that f16 drops at
-// most 128 2^-25 of a tile, 2^-16 of the row's largest weight.  The reference moves down
-// as well, because a token that takes nearly all of a row's weight would push the
-// others, whose values may be the output, below what f16 holds; it stays within
-// 2^kPfFloor of the largest logit, under which no number of tokens counts.  (A wider
-// reach below a reference that only moves up, 2^-33 of the first tile's largest weight, took 782 us
-// where this takes 551: it leaves 2^7 before logits that grow rescale.)  The ring's
-// weights are bf16, of f32's range: there it only moves up.
+// whole CTA up for about 3000 cycles), and else moves to where that weight is
+// 2^kPfTop. Weights are f16: 11 bits down to 2^-14, to within 2^-25 below, so that
+// f16 drops at most 128 2^-25 of a tile, 2^-16 of the row's largest weight.  The
+// reference moves down as well, because a token that takes nearly all of a row's
+// weight would push the others, whose values may be the output, below what f16
+// holds; it stays within 2^kPfFloor of the largest logit, under which no number of
+// tokens counts.  (A wider reach below a reference that only moves up, 2^-33 of
+// the first tile's largest weight, took 782 us where this takes 550: it leaves 2^7
+// before logits that grow rescale.)  The ring's weights are bf16, of f32's range:
+// there it only moves up.
 //
 // Warps: 0-3 and 4-7 softmax of tile 0 and 1 (a thread per row), 8-23 decode
 // records (or copy ring tokens) into two stages each of key and value tiles,
@@ -41,9 +42,10 @@
 // The rotation of the queries is a product with the signed Hadamard matrix
 // (+-1, exact in bf16, as the queries are), one more MMA per tile.
 //
-// Measured: 1024 tokens of 32 heads over 32768 + 1280 (4 bits, head dim 128) 559 us,
-// 1.01 PFLOP/s; bound by the chain softmax -> weights -> MMA of the two tiles and
-// by the ALU pipe, which the decoding fills (lookups by shift and mask took 9% longer).
+// Measured: 1024 tokens of 32 heads over 32768 + 1280 (4 bits, head dim 128) 550 us,
+// 1.02 PFLOP/s.  Neither the tensor pipe (48%) nor the issue slots (58%) are full: the
+// two tiles' chains softmax -> weights -> MMA cover one another only in part.  Instructions
+// count (lookups by shift and mask took 9% longer).
 //
 // Partials lie as [128-row tile][split][D / 4][128 rows][4], so that the
 // thread that owns a row writes 16 bytes beside its neighbours'.

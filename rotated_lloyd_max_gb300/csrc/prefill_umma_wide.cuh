@@ -16,13 +16,14 @@
 // sixteen warps in groups of four, a group a chunk.  Where keys and values share
 // a record (or ring), a chunk serves the scores and, kept, the outputs, so that
 // it is decoded once; otherwise the keys' chunks and the values' follow one another.
-// A chunk is decoded into registers before its slot is waited for (64 tokens of
-// 64 heads over 16384, head dim 512: 353 us; 5% more when it decodes into the slot).
+// A chunk is decoded into registers before its slot is waited for (5% more when it
+// decodes into the slot).  64 tokens of 64 heads over 16384, head dim 512: 376 us.
 //
-// Bound by shared memory: 128 tokens at head dim 512 take 640 KB of its traffic (two
+// 128 tokens at head dim 512 take 640 KB of shared memory's traffic (two
 // products of 192 KB, since an MMA of N = 64 reads 6 KB; 128 KB of tiles
-// written; 128 KB of lookups), 5000 of the 9000 cycles measured; the ring holds
-// one such tile, so the decoding of the next runs behind the products of this one.
+// written; 128 KB of lookups), 5000 of the 9600 cycles measured.  The rest is
+// waiting: the ring holds one such tile, so that the decoding of the next runs
+// behind the products of this one, and scores, softmax and outputs follow one another.
 #pragma once
 
 #include "prefill_umma.cuh"

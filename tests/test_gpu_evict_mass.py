@@ -272,9 +272,10 @@ def test_captured_and_replayed(tq, orc, in_place, T):
 
 
 @pytest.mark.parametrize("in_place", [False, True])
-@pytest.mark.parametrize("n", [3073, 3207])
+@pytest.mark.parametrize("n", [3104, 3207])
 def test_streams_longer_than_a_cluster_keeps(tq, in_place, n):
-    """More than 3072 records: the weights are read again in every pass; the last of the cluster's CTAs have fewer records."""
+    """More records than a cluster of eight CTAs keeps in shared memory (192 KB each): the weights are read again in
+    every pass; the last CTA has fewer records, or all have the same number."""
     import torch
     keep, d = 1500, 64
     kc = tq.tq_make_codebook(1, d)
