@@ -460,7 +460,16 @@ def _ready(args, workspace=None):
     import torch
     dev = args._tensors[args._lead].device.index
     _need(dev == torch.cuda.current_device(), f"the tensors are on device {dev}, not on the current one")
-    _need(workspace is None or workspace.get_device() == dev, "the workspace is on another device")
+    _need(workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()),
+          "the workspace is on another device, or not contiguous")
+
+
+def _fits(args, k_codec, v_codec):
+    """The records are of the codecs' size (looked at once for an argument block and its codecs)."""
+    if args._fit is None or args._fit[0] is not k_codec or args._fit[1] is not v_codec:
+        for codec, rec, name in ((k_codec, args._records[0], "k_rec"), (v_codec, args._records[1], "v_rec")):
+            _check_records(codec, rec, name)
+        args._fit = (k_codec, v_codec)
 
 
 def _scratch(size: int, device, stream):
@@ -638,7 +647,7 @@ def make_query_args(*, q, scale: float, out=None, softcap: float = 0.0, causal: 
     _need(q_lens is None or (q_lens.is_contiguous() and tuple(q_lens.shape) == (B,)), "q_lens: expected int32 [B]")
     a.n_chunks, a.tail_start, a.tail_len, a.q_lens = _ptr(n_chunks), _ptr(tail_start), _ptr(tail_len), _ptr(q_lens)
     a.max_chunks, a.max_tail = max_chunks, max_tail
-    a._lead = 0
+    a._lead, a._records, a._fit = 0, (k_rec, v_rec), None
     a._tensors = (q, out, k_rec, v_rec, k_tail, v_tail, n_chunks, tail_start, tail_len, q_lens, block_table)
     return a
 
@@ -662,14 +671,13 @@ def tq_prefill_attn_workspace_size(args: tq_query_args, k_codec: Codec | None, v
 def tq_prefill_attn(args: tq_query_args, k_codec: Codec | None, v_codec: Codec | None, workspace, stream=None):
     """Attention of several query tokens per sequence over records and ring, bf16 out (include/tq.h)."""
     _ready(args, workspace)
+    _fits(args, k_codec, v_codec)
     _check("tq_prefill_attn", load().tq_prefill_attn(ctypes.byref(args), _raw(k_codec), _raw(v_codec), _ptr(workspace),
                                                      workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def prefill_attn(*, k_codec=None, v_codec=None, workspace=None, stream=None, **kw):
     """Convenience: build the arguments, size/allocate the workspace if not given, run."""
-    _check_records(k_codec, kw.get("k_rec"), "k_rec")
-    _check_records(v_codec, kw.get("v_rec"), "v_rec")
     a = make_query_args(**kw)
     need = tq_prefill_attn_workspace_size(a, k_codec, v_codec)
     if workspace is None or workspace.numel() < need:
@@ -689,6 +697,7 @@ def tq_attn_mass(args: tq_query_args, k_codec: Codec | None, mass, workspace, de
     """mass (f32 [L, B, Hkv, cap]) = decay * mass + the attention weight each cached token receives
     from the queries (include/tq.h)."""
     _ready(args, workspace)
+    _fits(args, k_codec, None)
     import torch
     _need(mass.dtype == torch.float32 and mass.device == args._tensors[0].device,
           "mass: expected f32 on the queries' device")
@@ -702,7 +711,6 @@ def attn_mass(*, mass, k_codec=None, decay: float = 1.0, workspace=None, stream=
     """Convenience: build the arguments, size/allocate the workspace if not given, run."""
     import torch
     _check_tensors(dict(mass=(mass, torch.float32)))
-    _check_records(k_codec, kw.get("k_rec"), "k_rec")
     a = make_query_args(**kw)
     need = tq_attn_mass_workspace_size(a, k_codec)
     if workspace is None or workspace.numel() < need:
@@ -765,7 +773,7 @@ def make_evict_mass_args(*, k_rec, v_rec, mass, n_chunks, max_chunks: int, keep_
           "kept: expected contiguous int32 [L, B, Hkv, 128 * keep_chunks]")
     a.kept = _ptr(kept)
     a.max_chunks, a.max_tail, a.keep_chunks, a.sink, a.recent = max_chunks, max_tail, keep_chunks, sink, recent
-    a._lead = 0
+    a._lead, a._records, a._fit = 0, (k_rec, v_rec), None
     a._tensors = (k_rec, v_rec, k_dst, v_dst, mass, mass_dst, n_chunks, n_chunks_dst, tail_len, kept, block_table,
                   dst_table)
     return a
@@ -781,14 +789,13 @@ def tq_evict_mass_workspace_size(args: tq_evict_mass_args, k_codec: Codec, v_cod
 def tq_evict_mass(args: tq_evict_mass_args, k_codec: Codec, v_codec: Codec | None, workspace, stream=None):
     """Keep the tokens of the largest accumulated weight and compact the records (include/tq.h)."""
     _ready(args, workspace)
+    _fits(args, k_codec, v_codec)
     _check("tq_evict_mass", load().tq_evict_mass(ctypes.byref(args), _raw(k_codec), _raw(v_codec), _ptr(workspace),
                                                  workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def evict_mass(*, k_codec, v_codec=None, workspace=None, stream=None, **kw):
     """Convenience: build the arguments, size/allocate the workspace if not given, run."""
-    _check_records(k_codec, kw["k_rec"], "k_rec")
-    _check_records(v_codec, kw["v_rec"], "v_rec")
     a = make_evict_mass_args(**kw)
     need = tq_evict_mass_workspace_size(a, k_codec, v_codec)
     if workspace is None or workspace.numel() < need:
