@@ -456,6 +456,26 @@ typedef struct {
 tq_status tq_append(const tq_append_args* args, void* stream);
 
 /*
+ * Append with norms of queries and keys: as tq_append, but that every head x of
+ * the queries (q_weight not NULL) and of the keys (k_weight not NULL) is first
+ * normalised over its head_dim coordinates,
+ *   x_j -> x_j w_j / sqrt(sum_i x_i^2 / head_dim + eps),
+ * in f32, and rounded once, after the rotation.  Values are copied as they are.
+ * Weights: device f32, 16-byte aligned, head h's at weight + h*head_stride
+ * (elements, a multiple of 4; 0 = one row for all heads).  At least one of the
+ * two; q_weight only with queries.  eps: finite, >= 0 (with 0 a head of zeros
+ * becomes NaN).
+ */
+typedef struct {
+  const float* q_weight;
+  const float* k_weight;
+  int64_t q_head_stride, k_head_stride;
+  float eps;
+} tq_head_norm;
+
+tq_status tq_norm_append(const tq_append_args* args, const tq_head_norm* norm, void* stream);
+
+/*
  * Queries of up to t_q new tokens per sequence against a cache.  With
  * total = 128 n_chunks + tail_len (the new tokens' own keys included) query t
  * of sequence b sees the tokens of index < total, and when `causal` is set of
@@ -599,6 +619,106 @@ size_t tq_evict_mass_workspace_size(const tq_evict_mass_args* args, const tq_cod
                                     const tq_codec* v_codec);
 tq_status tq_evict_mass(const tq_evict_mass_args* args, const tq_codec* k_codec, const tq_codec* v_codec,
                         void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Attention to a part of a long cache: bounds of every record's keys, records
+ * chosen by them for blocks of queries, attention over the chosen ones.
+ *
+ * Bounds of the keys.  For coordinate j of record r of (l, b, kv head h), over
+ * the record's 128 decoded keys (tq_decode's, in f32: off by at most a few ulp
+ * of a key's norm) in the keys' own basis,
+ *   lo_j = min_i khat_ij rounded down, hi_j = max_i khat_ij rounded up, to bf16.
+ * Bounds lie as the records do: bf16 [2][head_dim] (lo, then hi) in the place
+ * of a record's bytes, at
+ *   bounds + l*bounds_layer_stride + ((b*n_kv_heads + h)*rec_cap + r)*2*head_dim,
+ * or, with a block table, at block (block_table[b][r]*n_kv_heads + h) of the layer's pool.
+ * Records first[l][b] <= r < min(n_chunks[l][b], first[l][b] + max_new) are
+ * bounded (first NULL = 0), the others' bounds left as they are: a caller that
+ * bounds what it encodes passes the count it had before.  A record that holds
+ * a scale which is not finite has NaN bounds.
+ */
+typedef struct {
+  int32_t n_layers, batch, n_kv_heads;
+  const void* k_rec; /* records as in tq_evict_args */
+  int64_t k_rec_layer_stride;
+  int32_t rec_cap;
+  const int32_t* block_table;
+  int32_t table_stride;
+  const int32_t* n_chunks; /* device [L][B] */
+  const int32_t* first;    /* device [L][B]; NULL = 0 */
+  int32_t max_chunks;      /* host upper bound of n_chunks */
+  int32_t max_new;         /* records bounded per sequence at most, >= 1 */
+  void* bounds;            /* 16-byte aligned */
+  int64_t bounds_layer_stride; /* elements, a multiple of 8 */
+} tq_bounds_args;
+
+tq_status tq_key_bounds(const tq_codec* k_codec, const tq_bounds_args* args, void* stream);
+
+/*
+ * Records chosen for blocks of queries.  Block j holds the tokens
+ * j*q_block <= t < min((j + 1)*q_block, T_b), T_b as in tq_append; n_blocks =
+ * ceil(t_q / q_block).  It may read the m = min(n_chunks, ceil(limit / 128))
+ * first records, limit the tokens its last query sees (as in tq_query_args),
+ * m = 0 where it has no query.  Record r's score is the largest
+ *   sum_j max(q_j lo_rj, q_j hi_rj)
+ * over the kv head's query heads and the block's tokens, no logit q . k of the
+ * block in the record being above it.  The list holds min(m, keep) records in
+ * ascending order: the first `sink`, the newest `recent` of the m, and the
+ * rest by score.  Scores are compared exactly (those too near to be told apart
+ * in f32 are formed again with twice the bits); ties go to the lower index.  A
+ * query row or a record whose sum is not finite does not count; records without
+ * a score come last.
+ *   list: [L][B][n_blocks][Hkv][keep], -1 behind the chosen; count: [L][B][n_blocks][Hkv].
+ * max_chunks <= TQ_SELECT_MAX_CHUNKS.  workspace as for tq_prefill_attn.
+ */
+#define TQ_SELECT_MAX_CHUNKS 16384
+typedef struct {
+  int32_t n_layers, batch, t_q, n_q_heads, n_kv_heads, head_dim;
+  int32_t causal;
+  const void* q; /* as in tq_query_args */
+  int64_t q_layer_stride, q_batch_stride, q_token_stride;
+  const int32_t* q_lens;
+  const void* bounds; /* as tq_key_bounds leaves them */
+  int64_t bounds_layer_stride;
+  int32_t rec_cap;
+  const int32_t* block_table;
+  int32_t table_stride;
+  const int32_t* n_chunks; /* device [L][B] */
+  const int32_t* tail_len; /* device [L][B]; NULL = 0 */
+  int32_t max_chunks, max_tail;
+  int32_t q_block; /* >= 1 */
+  int32_t keep;    /* >= 1 */
+  int32_t sink, recent; /* >= 0, sink + recent <= keep */
+  int32_t* list;
+  int32_t* count;
+} tq_select_args;
+
+size_t tq_select_records_workspace_size(const tq_select_args* args);
+tq_status tq_select_records(const tq_select_args* args, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * Attention over listed records and the ring: tq_prefill_attn, but that the
+ * queries of block j of kv head h see, of the records, those that its list
+ * names (and of these, when `causal` is set, the tokens of index <= total -
+ * T_b + t).  Entries from count on are not read; entries outside [0, n_chunks)
+ * name nothing; an entry that comes twice weighs twice.  Order is free.
+ * Precision, rows that see nothing, what is not finite and the workspace as
+ * for tq_prefill_attn; the values of listed records and of the ring have to be
+ * finite.  Lists are as tq_select_records leaves them.
+ * Up to 16 rows a list (query heads of a kv head x q_block) at head dims 64 and
+ * 128 without side lists run on mma.sync, everything else on tcgen05.
+ */
+typedef struct {
+  const int32_t* list;  /* device [L][B][n_blocks][Hkv][list_stride] */
+  const int32_t* count; /* device [L][B][n_blocks][Hkv] */
+  int32_t list_stride;  /* >= 1 */
+  int32_t q_block;      /* >= 1 */
+} tq_record_lists;
+
+size_t tq_sparse_attn_workspace_size(const tq_query_args* args, const tq_record_lists* lists, const tq_codec* k_codec,
+                                     const tq_codec* v_codec);
+tq_status tq_sparse_attn(const tq_query_args* args, const tq_record_lists* lists, const tq_codec* k_codec,
+                         const tq_codec* v_codec, void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus
 }

@@ -100,6 +100,30 @@ class tq_evict_mass_args(ctypes.Structure):
                 ("recent", c_i32), ("kept", c_p)]
 
 
+class tq_head_norm(ctypes.Structure):
+    _fields_ = [("q_weight", c_p), ("k_weight", c_p), ("q_head_stride", c_i64), ("k_head_stride", c_i64), ("eps", c_f32)]
+
+
+class tq_bounds_args(ctypes.Structure):
+    _fields_ = [("n_layers", c_i32), ("batch", c_i32), ("n_kv_heads", c_i32),
+                ("k_rec", c_p), ("k_rec_layer_stride", c_i64), ("rec_cap", c_i32),
+                ("block_table", c_p), ("table_stride", c_i32), ("n_chunks", c_p), ("first", c_p),
+                ("max_chunks", c_i32), ("max_new", c_i32), ("bounds", c_p), ("bounds_layer_stride", c_i64)]
+
+
+class tq_select_args(ctypes.Structure):
+    _fields_ = [("n_layers", c_i32), ("batch", c_i32), ("t_q", c_i32), ("n_q_heads", c_i32), ("n_kv_heads", c_i32),
+                ("head_dim", c_i32), ("causal", c_i32), ("q", c_p), ("q_layer_stride", c_i64),
+                ("q_batch_stride", c_i64), ("q_token_stride", c_i64), ("q_lens", c_p), ("bounds", c_p),
+                ("bounds_layer_stride", c_i64), ("rec_cap", c_i32), ("block_table", c_p), ("table_stride", c_i32),
+                ("n_chunks", c_p), ("tail_len", c_p), ("max_chunks", c_i32), ("max_tail", c_i32), ("q_block", c_i32),
+                ("keep", c_i32), ("sink", c_i32), ("recent", c_i32), ("list", c_p), ("count", c_p)]
+
+
+class tq_record_lists(ctypes.Structure):
+    _fields_ = [("list", c_p), ("count", c_p), ("list_stride", c_i32), ("q_block", c_i32)]
+
+
 ATTN_KERNELS = {0: "none", 1: "cuda_core", 2: "cuda_core_warp", 3: "mma", 4: "mma512", 5: "tcgen05"}
 
 _SIGS = {
@@ -140,6 +164,14 @@ _SIGS = {
                                                        ctypes.POINTER(tq_codec)]),
     "tq_evict_mass": (ctypes.c_int, [ctypes.POINTER(tq_evict_mass_args), ctypes.POINTER(tq_codec),
                                      ctypes.POINTER(tq_codec), c_p, ctypes.c_size_t, c_p]),
+    "tq_norm_append": (ctypes.c_int, [ctypes.POINTER(tq_append_args), ctypes.POINTER(tq_head_norm), c_p]),
+    "tq_key_bounds": (ctypes.c_int, [ctypes.POINTER(tq_codec), ctypes.POINTER(tq_bounds_args), c_p]),
+    "tq_select_records_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(tq_select_args)]),
+    "tq_select_records": (ctypes.c_int, [ctypes.POINTER(tq_select_args), c_p, ctypes.c_size_t, c_p]),
+    "tq_sparse_attn_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(tq_query_args), ctypes.POINTER(tq_record_lists),
+                                                        ctypes.POINTER(tq_codec), ctypes.POINTER(tq_codec)]),
+    "tq_sparse_attn": (ctypes.c_int, [ctypes.POINTER(tq_query_args), ctypes.POINTER(tq_record_lists),
+                                      ctypes.POINTER(tq_codec), ctypes.POINTER(tq_codec), c_p, ctypes.c_size_t, c_p]),
 }
 
 NOALLOC_WORKSPACE_BYTES = 8 << 20
@@ -801,4 +833,199 @@ def evict_mass(*, k_codec, v_codec=None, workspace=None, stream=None, **kw):
     if workspace is None or workspace.numel() < need:
         workspace = _scratch(need, kw["k_rec"].device, stream)
     tq_evict_mass(a, k_codec, v_codec, workspace, stream)
+    return workspace
+
+
+# ---------------------------------------------------------------------------
+# attention to a part of a long cache: head norms, key bounds, selection, listed records
+# ---------------------------------------------------------------------------
+def _bounds_layout(bounds, rec_cap: int, L: int, B: int, Hkv: int, d: int, paged: bool) -> int:
+    """Layer stride of bounds that lie as the records do."""
+    import torch
+    want = (L, rec_cap, Hkv, 2, d) if paged else (L, B, Hkv, rec_cap, 2, d)
+    _need(tuple(bounds.shape) == want and bounds[0].is_contiguous(),
+          f"bounds: expected {torch.bfloat16} {list(want)}, contiguous within a layer")
+    return _layer_stride(bounds)
+
+
+def _table(a, block_table, B: int):
+    if block_table is not None:
+        _need(block_table.is_contiguous() and block_table.dim() == 2 and block_table.shape[0] == B,
+              "block_table: expected contiguous int32 [B, stride]")
+        a.block_table, a.table_stride = block_table.data_ptr(), block_table.shape[1]
+
+
+def make_head_norm(*, q_weight=None, k_weight=None, eps: float = 1e-6) -> tq_head_norm:
+    """tq_head_norm from tensors: f32 [d] for all heads or [heads, d] (rows packed within a head); None: that side
+    is not normalised."""
+    import torch
+    _check_tensors(dict(q_weight=(q_weight, torch.float32), k_weight=(k_weight, torch.float32)))
+    n = tq_head_norm()
+    for name, w in (("q", q_weight), ("k", k_weight)):
+        if w is not None:
+            _need(w.dim() in (1, 2) and w.stride(-1) == 1, f"{name}_weight: expected f32 [d] or [heads, d]")
+            setattr(n, name + "_weight", w.data_ptr())
+            setattr(n, name + "_head_stride", w.stride(0) if w.dim() == 2 and w.shape[0] > 1 else 0)
+    n.eps = eps
+    n._tensors = (q_weight, k_weight)
+    return n
+
+
+def tq_norm_append(args: tq_append_args, norm: tq_head_norm, stream=None):
+    """tq_append with the queries' and keys' heads normalised before the rotation (include/tq.h)."""
+    _ready(args)
+    for w, heads in zip(norm._tensors, (args.n_q_heads, args.n_kv_heads)):
+        _need(w is None or (w.shape[-1] == args.head_dim and (w.dim() == 1 or w.shape[0] == heads) and
+                            w.device == args._tensors[args._lead].device),
+              "norm weights: expected [d] or [heads, d] on the tensors' device")
+    _check("tq_norm_append", load().tq_norm_append(ctypes.byref(args), ctypes.byref(norm), _stream(stream)))
+
+
+def make_bounds_args(*, k_rec, bounds, n_chunks, max_chunks: int, first=None, max_new: int | None = None,
+                     block_table=None) -> tq_bounds_args:
+    """tq_bounds_args from tensors.  k_rec: uint8 [L, B, Hkv, cap, bytes], or with block_table (int32 [B, stride])
+    pools [L, blocks, Hkv, bytes]; bounds: bf16 [L, B, Hkv, cap, 2, d] or [L, blocks, Hkv, 2, d]; n_chunks, first:
+    int32 [L, B] (records from first on are bounded, max_new at most; default: all up to max_chunks)."""
+    import torch
+    i32 = torch.int32
+    _check_tensors(dict(k_rec=(k_rec, torch.uint8), bounds=(bounds, torch.bfloat16), n_chunks=(n_chunks, i32),
+                        first=(first, i32), block_table=(block_table, i32)))
+    paged = block_table is not None
+    _need(k_rec.dim() == (4 if paged else 5) and k_rec[0].is_contiguous(),
+          "k_rec: expected records [L, B, Hkv, cap, bytes] or a pool [L, blocks, Hkv, bytes], contiguous within a layer")
+    a = tq_bounds_args()
+    if paged:
+        (L, cap, Hkv), B = k_rec.shape[:3], block_table.shape[0]
+    else:
+        L, B, Hkv, cap = k_rec.shape[:4]
+    _table(a, block_table, B)
+    a.n_layers, a.batch, a.n_kv_heads, a.rec_cap = L, B, Hkv, cap
+    a.k_rec, a.k_rec_layer_stride = k_rec.data_ptr(), _layer_stride(k_rec)
+    a.bounds, a.bounds_layer_stride = bounds.data_ptr(), _bounds_layout(bounds, cap, L, B, Hkv, bounds.shape[-1], paged)
+    _counts(n_chunks, "n_chunks", L, B)
+    _counts(first, "first", L, B)
+    a.n_chunks, a.first = n_chunks.data_ptr(), _ptr(first)
+    a.max_chunks, a.max_new = max_chunks, max(max_chunks, 1) if max_new is None else max_new
+    a._lead, a._records, a._fit = 0, (k_rec, None), None
+    a._tensors = (k_rec, bounds, n_chunks, first, block_table)
+    return a
+
+
+def tq_key_bounds(args: tq_bounds_args, k_codec: Codec, stream=None):
+    """Smallest and largest value of each coordinate of every record's keys (include/tq.h)."""
+    _ready(args)
+    _fits(args, k_codec, None)
+    _need(args._tensors[1].shape[-1] == k_codec.head_dim, "bounds: expected the codec's head dim")
+    _check("tq_key_bounds", load().tq_key_bounds(_raw(k_codec), ctypes.byref(args), _stream(stream)))
+
+
+def key_bounds(*, k_codec, stream=None, **kw):
+    """Convenience: build the arguments, run."""
+    tq_key_bounds(make_bounds_args(**kw), k_codec, stream)
+
+
+def make_select_args(*, q, bounds, n_chunks, max_chunks: int, list, count, keep: int, q_block: int = 1, sink: int = 1,
+                     recent: int = 1, causal: bool = True, q_lens=None, tail_len=None, max_tail: int = 0,
+                     block_table=None) -> tq_select_args:
+    """tq_select_args from tensors.  q: bf16 view [L, B, T, Hq, d]; bounds as for make_bounds_args; list: int32
+    [L, B, blocks, Hkv, keep], count: int32 [L, B, blocks, Hkv], blocks = ceil(T / q_block); counters int32 [L, B]."""
+    import torch
+    i32, bf = torch.int32, torch.bfloat16
+    _check_tensors(dict(q=(q, bf), bounds=(bounds, bf), n_chunks=(n_chunks, i32), tail_len=(tail_len, i32),
+                        q_lens=(q_lens, i32), block_table=(block_table, i32), list=(list, i32), count=(count, i32)))
+    L, B, T, Hq, d = q.shape
+    paged = block_table is not None
+    _need(bounds.dim() == (5 if paged else 6), "bounds: expected [L, B, Hkv, cap, 2, d] or a pool [L, blocks, Hkv, 2, d]")
+    Hkv, cap = bounds.shape[2], bounds.shape[1] if paged else bounds.shape[3]
+    a = tq_select_args()
+    a.n_layers, a.batch, a.t_q, a.n_q_heads, a.n_kv_heads, a.head_dim, a.causal = L, B, T, Hq, Hkv, d, int(causal)
+    a.q, (a.q_layer_stride, a.q_batch_stride, a.q_token_stride) = q.data_ptr(), _heads_packed(q, "q", d)
+    a.bounds, a.bounds_layer_stride = bounds.data_ptr(), _bounds_layout(bounds, cap, L, B, Hkv, d, paged)
+    a.rec_cap = cap
+    _table(a, block_table, B)
+    for name, t in (("n_chunks", n_chunks), ("tail_len", tail_len)):
+        _counts(t, name, L, B)
+    _need(q_lens is None or (q_lens.is_contiguous() and tuple(q_lens.shape) == (B,)), "q_lens: expected int32 [B]")
+    _need(q_block >= 1 and keep >= 1, "q_block, keep: expected at least 1")
+    blocks = -(-T // q_block)
+    _need(tuple(list.shape) == (L, B, blocks, Hkv, keep) and list.is_contiguous() and
+          tuple(count.shape) == (L, B, blocks, Hkv) and count.is_contiguous(),
+          f"list, count: expected contiguous int32 {[L, B, blocks, Hkv, keep]} and {[L, B, blocks, Hkv]}")
+    a.q_lens, a.n_chunks, a.tail_len = _ptr(q_lens), n_chunks.data_ptr(), _ptr(tail_len)
+    a.max_chunks, a.max_tail, a.q_block, a.keep, a.sink, a.recent = max_chunks, max_tail, q_block, keep, sink, recent
+    a.list, a.count = list.data_ptr(), count.data_ptr()
+    a._lead = 0
+    a._tensors = (q, bounds, n_chunks, tail_len, q_lens, block_table, list, count)
+    return a
+
+
+def tq_select_records_workspace_size(args: tq_select_args) -> int:
+    n = load().tq_select_records_workspace_size(ctypes.byref(args))
+    if n == 0:
+        raise TqError("tq_select_records_workspace_size", TQ_ERR_INVALID_ARG)
+    return int(n)
+
+
+def tq_select_records(args: tq_select_args, workspace, stream=None):
+    """Records chosen for blocks of queries by an upper bound of their logits (include/tq.h)."""
+    _ready(args, workspace)
+    _check("tq_select_records", load().tq_select_records(ctypes.byref(args), _ptr(workspace),
+                                                         workspace.numel() * workspace.element_size(), _stream(stream)))
+
+
+def select_records(*, workspace=None, stream=None, **kw):
+    """Convenience: build the arguments, size/allocate the workspace if not given, run."""
+    a = make_select_args(**kw)
+    need = tq_select_records_workspace_size(a)
+    if workspace is None or workspace.numel() < need:
+        workspace = _scratch(need, kw["q"].device, stream)
+    tq_select_records(a, workspace, stream)
+    return workspace
+
+
+def make_record_lists(*, list, count, q_block: int = 1) -> tq_record_lists:
+    """tq_record_lists from tensors: int32 [L, B, blocks, Hkv, entries] and [L, B, blocks, Hkv]."""
+    import torch
+    _check_tensors(dict(list=(list, torch.int32), count=(count, torch.int32)))
+    _need(list.dim() == 5 and list.is_contiguous() and count.is_contiguous() and tuple(count.shape) == tuple(list.shape[:4]),
+          "list, count: expected contiguous int32 [L, B, blocks, Hkv, entries] and [L, B, blocks, Hkv]")
+    r = tq_record_lists(list.data_ptr(), count.data_ptr(), list.shape[4], q_block)
+    r._tensors = (list, count)
+    return r
+
+
+def _lists_fit(args: tq_query_args, lists: tq_record_lists):
+    _need(lists.q_block >= 1, "q_block: expected at least 1")
+    want = (args.n_layers, args.batch, -(-args.t_q // lists.q_block), args.n_kv_heads)
+    _need(tuple(lists._tensors[1].shape) == want and lists._tensors[0].device == args._tensors[0].device,
+          f"list, count: expected {list(want)} lists on the queries' device")
+
+
+def tq_sparse_attn_workspace_size(args: tq_query_args, lists: tq_record_lists, k_codec: Codec,
+                                  v_codec: Codec | None) -> int:
+    n = load().tq_sparse_attn_workspace_size(ctypes.byref(args), ctypes.byref(lists), _raw(k_codec), _raw(v_codec))
+    if n == 0:
+        raise TqError("tq_sparse_attn_workspace_size", TQ_ERR_INVALID_ARG)
+    return int(n)
+
+
+def tq_sparse_attn(args: tq_query_args, lists: tq_record_lists, k_codec: Codec, v_codec: Codec | None, workspace,
+                   stream=None):
+    """Attention over listed records and the ring, bf16 out (include/tq.h)."""
+    _ready(args, workspace)
+    _fits(args, k_codec, v_codec)
+    _lists_fit(args, lists)
+    _check("tq_sparse_attn", load().tq_sparse_attn(ctypes.byref(args), ctypes.byref(lists), _raw(k_codec), _raw(v_codec),
+                                                   _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                                   _stream(stream)))
+
+
+def sparse_attn(*, list, count, q_block: int = 1, k_codec=None, v_codec=None, workspace=None, stream=None, **kw):
+    """Convenience: build the arguments, size/allocate the workspace if not given, run."""
+    a = make_query_args(**kw)
+    lists = make_record_lists(list=list, count=count, q_block=q_block)
+    need = tq_sparse_attn_workspace_size(a, lists, k_codec, v_codec)
+    if workspace is None or workspace.numel() < need:
+        workspace = _scratch(need, kw["q"].device, stream)
+    tq_sparse_attn(a, lists, k_codec, v_codec, workspace, stream)
     return workspace

@@ -16,10 +16,6 @@ namespace {
 
 constexpr int kVersion = 10000;  // 1.0.0
 
-inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-inline bool dim_ok(int d) { return d == 64 || d == 128 || d == 256 || d == 512; }
-
 int default_cap(int d) { return 4 * ((8 * TQ_CHUNK * d + 399) / 400); }
 
 // record layout: codes, norms, [counts, entries]

@@ -33,26 +33,14 @@ cudaError_t launch_attn_mass_add(const MassParams& mp, cudaStream_t s);
 
 namespace {
 
-inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
-inline size_t pad256(size_t x) { return (x + 255) / 256 * 256; }
-inline bool dim_ok(int d) { return d == 64 || d == 128 || d == 256 || d == 512; }
-inline bool strides_ok(int64_t a, int64_t b, int64_t c) {
-  return a >= 0 && b >= 0 && c >= 0 && a % 8 == 0 && b % 8 == 0 && c % 8 == 0;
-}
-
-// Tokens of a sequence.  Indices are 32-bit, and kernels count past the last
-// token by less than 2^20: to the end of the last split (fewer than 128 records
-// behind, the split counts being at most 128) or of a block's last batch (8192).
-constexpr int64_t kMostTokens = (1ll << 31) - (1 << 20);
-
 // what a call writes must not overlap itself: along every axis longer than one
 // a step is at least a row of `row` elements
 inline bool rows_apart(int64_t ls, int64_t bs, int64_t ts, int L, int B, int T, int64_t row) {
   return (L == 1 || ls >= row) && (B == 1 || bs >= row) && (T == 1 || ts >= row);
 }
-// nor one layer the next
-inline bool layers_apart(int L, int64_t ls, int64_t layer) { return L == 1 || ls >= layer; }
+}  // namespace
+
+namespace tq {
 
 // ----------------------------------------------------------------- append
 tq_status append_params(const tq_append_args* a, AppendParams* p) {
@@ -243,6 +231,10 @@ tq_status query_params(const tq_query_args* a, const tq_codec* kcod, const tq_co
   p->max_tail = a->max_tail;
   return TQ_OK;
 }
+
+}  // namespace tq
+
+namespace {
 
 struct PrefillPlan {
   PrefillParams pp;

@@ -17,6 +17,11 @@
 // tokens, 48 heads of 128: 54 us, 5.6 TB/s.  One token: 3.0 us from a graph, a launch
 // and one chain behind it (lengths, inv_freq, angle, barrier, and only then the loads);
 // with the counters in place, which a second launch moves, 3.7 us.
+//
+// With norms (tq_norm_append) the lanes that hold a head, d / 16 neighbours of one
+// warp, add up its squares by shuffles; norm, weights and rotation follow in f32
+// on the values in registers and are rounded once, so that the norm costs no
+// second read.
 #include "cache_params.h"
 #include "tq_common.cuh"
 
@@ -59,7 +64,35 @@ __device__ __forceinline__ void turn_adjacent(uint4& a, const float2* cs) {
   }
 }
 
-template <int D>
+__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = bf16_lo(w[i]);
+    x[2 * i + 1] = bf16_hi(w[i]);
+  }
+}
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+}
+__device__ __forceinline__ void scale8(float (&x)[8], float r, const float* w) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(w)), b = __ldg(reinterpret_cast<const float4*>(w) + 1);
+  const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] *= r * v[i];
+}
+// four pairs of neighbours
+__device__ __forceinline__ void turn_adjacent(float (&x)[8], const float2* cs) {
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    const float2 c = cs[i / 2];
+    const float x0 = x[i], x1 = x[i + 1];
+    x[i] = x0 * c.x - x1 * c.y;
+    x[i + 1] = x1 * c.x + x0 * c.y;
+  }
+}
+
+template <int D, bool NORM>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int UPH = D / 16;  // two-chunk units per head
   extern __shared__ __align__(16) float2 table[];  // [tile][rot_dim / 2] cos, sin (times rot_scale)
@@ -143,6 +176,43 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     }
     uint4 x = *reinterpret_cast<const uint4*>(src + 8 * c0), y = *reinterpret_cast<const uint4*>(src + 8 * c1);
     const float2* cs = table + t * half;
+    if constexpr (NORM) {
+      const bool query = h < p.Hq;
+      const float* wt = query ? p.q_weight : turns ? p.k_weight : nullptr;  // values have no norm
+      if (wt) {  // the same for the UPH neighbouring lanes that hold the head
+        wt += query ? h * p.q_hs : (h - p.Hq) * p.k_hs;
+        float a[8], b[8];
+        unpack8(x, a);
+        unpack8(y, b);
+        float2 ss = f2(0.f, 0.f);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fma2(f2(a[j], b[j]), f2(a[j], b[j]), ss);
+        float sum = ss.x + ss.y;
+        const uint32_t team = UPH == 32 ? 0xffffffffu : ((1u << (UPH & 31)) - 1u) << (threadIdx.x & 31 & ~(UPH - 1));
+#pragma unroll
+        for (int m = 1; m < UPH; m <<= 1) sum += __shfl_xor_sync(team, sum, m);
+        const float r = rsqrtf(fmaf(sum, 1.f / D, p.eps));
+        scale8(a, r, wt + 8 * c0);
+        scale8(b, r, wt + 8 * c1);
+        if (pairs) {
+          cs += 8 * u;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float2 c = cs[j];
+            const float y0 = a[j] * c.x - b[j] * c.y, y1 = b[j] * c.x + a[j] * c.y;
+            a[j] = y0;
+            b[j] = y1;
+          }
+        } else if (p.adjacent) {
+          const int r0 = 8 * c0 - p.rot_start, r1 = 8 * c1 - p.rot_start;
+          if (r0 >= 0 && r0 < p.rot_dim) turn_adjacent(a, cs + (r0 >> 1));
+          if (r1 >= 0 && r1 < p.rot_dim) turn_adjacent(b, cs + (r1 >> 1));
+        }
+        *reinterpret_cast<uint4*>(dst + 8 * c0) = pack8(a);
+        *reinterpret_cast<uint4*>(dst + 8 * c1) = pack8(b);
+        continue;
+      }
+    }
     if (pairs) {
       turn_halves(x, y, cs + 8 * u);
     } else if (turns && p.adjacent) {
@@ -162,18 +232,22 @@ __global__ void append_commit_kernel(const __grid_constant__ AppendParams p) {
   }
 }
 
-cudaError_t launch_append(const AppendParams& p, cudaStream_t s) {
+template <bool NORM>
+static cudaError_t append_launch(const AppendParams& p, cudaStream_t s) {
   const dim3 grid((unsigned)((int64_t)p.L * p.B * p.tiles), (p.heads + p.group - 1) / p.group);
   const int smem = p.tile * (p.rot_dim / 2) * (int)sizeof(float2);
   switch (p.D) {
-    case 64: append_kernel<64><<<grid, kAppendThreads, smem, s>>>(p); break;
-    case 128: append_kernel<128><<<grid, kAppendThreads, smem, s>>>(p); break;
-    case 256: append_kernel<256><<<grid, kAppendThreads, smem, s>>>(p); break;
-    case 512: append_kernel<512><<<grid, kAppendThreads, smem, s>>>(p); break;
+    case 64: append_kernel<64, NORM><<<grid, kAppendThreads, smem, s>>>(p); break;
+    case 128: append_kernel<128, NORM><<<grid, kAppendThreads, smem, s>>>(p); break;
+    case 256: append_kernel<256, NORM><<<grid, kAppendThreads, smem, s>>>(p); break;
+    case 512: append_kernel<512, NORM><<<grid, kAppendThreads, smem, s>>>(p); break;
     default: return cudaErrorInvalidValue;
   }
   return cudaGetLastError();
 }
+
+cudaError_t launch_append(const AppendParams& p, cudaStream_t s) { return append_launch<false>(p, s); }
+cudaError_t launch_norm_append(const AppendParams& p, cudaStream_t s) { return append_launch<true>(p, s); }
 
 cudaError_t launch_append_commit(const AppendParams& p, cudaStream_t s) {
   const int n = p.L * p.B;

@@ -35,6 +35,10 @@ struct AppendParams {
   int64_t mass_ls;
   int mass_cap;
   const int32_t* n_chunks;
+  // norms (tq_norm_append)
+  const float *q_weight, *k_weight;
+  int64_t q_hs, k_hs;
+  float eps;
 };
 
 struct EvictMassParams {
@@ -91,7 +95,40 @@ struct QueryParams {
   int max_chunks, max_tail;
 };
 
+struct BoundsParams {
+  int L, B, Hkv;
+  CodecDev c;
+  const uint8_t* rec;
+  int64_t rec_ls;
+  int rec_cap;
+  const int32_t* table;
+  int table_stride, rec_limit;
+  const int32_t* n_chunks;
+  const int32_t* first;
+  int max_chunks, max_new;
+  uint16_t* bounds;
+  int64_t bounds_ls;
+};
+
+struct SelectParams {
+  QueryParams q;      // of its records the counts and the table; krec is not read
+  const uint16_t* bounds;
+  int64_t bounds_ls;
+  int qb, blocks;     // tokens of a block, blocks of a sequence
+  int keep, sink, recent;
+  int32_t* list;
+  int32_t* count;
+  // workspace
+  int tiles, tile;    // CTAs of a list's scores; records of one
+  float* scores;      // [lists][max_chunks]
+  float2* limits;     // [lists][tiles]: largest 1-norm of a query, largest bound
+  uint64_t* exact;    // [lists][max_chunks]
+};
+
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
+cudaError_t launch_norm_append(const AppendParams& p, cudaStream_t s);
+cudaError_t launch_key_bounds(const BoundsParams& p, cudaStream_t s);
+cudaError_t launch_select_records(const SelectParams& p, cudaStream_t s);
 cudaError_t launch_append_commit(const AppendParams& p, cudaStream_t s);
 cudaError_t launch_evict_mass(const EvictMassParams& p, cudaStream_t s);
 
@@ -157,5 +194,21 @@ inline cudaError_t launch_after(void (*kern)(Args...), dim3 grid, int block, int
 int sm_count();
 int max_dynamic_smem();
 tq_status resolve_codec_dev(const tq_codec* c, CodecDev* o);
+// abi_cache.cu: the checks that calls with tq_append_args and tq_query_args share (values: whether the call reads them)
+tq_status append_params(const tq_append_args* a, AppendParams* p);
+tq_status query_params(const tq_query_args* a, const tq_codec* kcod, const tq_codec* vcod, bool values, QueryParams* p);
+// what a call writes must not overlap itself: one layer the next
+inline bool layers_apart(int L, int64_t ls, int64_t layer) { return L == 1 || ls >= layer; }
+inline int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+inline size_t pad256(size_t x) { return (x + 255) / 256 * 256; }
+inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline bool dim_ok(int d) { return d == 64 || d == 128 || d == 256 || d == 512; }
+inline bool strides_ok(int64_t a, int64_t b, int64_t c) {
+  return a >= 0 && b >= 0 && c >= 0 && a % 8 == 0 && b % 8 == 0 && c % 8 == 0;
+}
+// Tokens of a sequence.  Indices are 32-bit, and kernels count past the last
+// token by less than 2^20: to the end of the last split (fewer than 128 records
+// behind, the split counts being at most 128) or of a block's last batch (8192).
+constexpr int64_t kMostTokens = (1ll << 31) - (1 << 20);
 
 }  // namespace tq

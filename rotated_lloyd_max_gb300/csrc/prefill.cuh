@@ -24,7 +24,34 @@ struct PrefillParams {
   uint16_t* out;
   int64_t o_ls, o_bs, o_ts;
   float inv_sqrt_d;
+  // listed records (tq_sparse_attn; q_block 0: every record).  A block of q_block
+  // tokens shares a list; its rows make sub row tiles, tiles = blocks * sub.
+  const int32_t* list;
+  const int32_t* list_count;
+  int list_stride, q_block, sub;
 };
+
+// The records of a row tile's split: c0, c0 + 1, .., or (LISTED) the entries c0,
+// c0 + 1, .. of its list, of which those that name no record stand for record 0
+// with no token seen.
+struct RecordRun {
+  const int32_t* list;
+  int c0, n;  // first record or entry; records of the sequence
+};
+template <bool LISTED>
+__device__ __forceinline__ int run_entry(const RecordRun& r, int i) {
+  return LISTED ? __ldg(r.list + r.c0 + i) : r.c0 + i;
+}
+template <bool LISTED>
+__device__ __forceinline__ int run_record(const RecordRun& r, int i) {
+  const int e = run_entry<LISTED>(r, i);
+  return LISTED && (e < 0 || e >= r.n) ? 0 : e;
+}
+// of entry i's 128 tokens, those below `lim` (a row's limit in the sequence), counted from the record's first
+__device__ __forceinline__ int listed_seen(const RecordRun& r, int i, int lim) {
+  const int e = run_entry<true>(r, i);
+  return e < 0 || e >= r.n ? 0 : lim - e * kChunk;
+}
 
 // byte planes of a 16-entry f16 table: low and high bytes of entries 4 w .. 4 w + 3
 struct Planes {

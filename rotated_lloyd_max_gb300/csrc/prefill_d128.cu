@@ -4,6 +4,6 @@
 namespace tq {
 
 int prefill_rows_d128() { return kPfRows; }
-cudaError_t launch_prefill_d128(const PrefillParams& pp, cudaStream_t s) { return prefill_umma_launch<128>(pp, s); }
+cudaError_t launch_prefill_d128(const PrefillParams& pp, cudaStream_t s) { return prefill_umma_launch<128, false>(pp, s); }
 
 }  // namespace tq

@@ -4,6 +4,6 @@
 namespace tq {
 
 int prefill_rows_d256() { return kPwRows; }
-cudaError_t launch_prefill_d256(const PrefillParams& pp, cudaStream_t s) { return prefill_wide_launch<256>(pp, s); }
+cudaError_t launch_prefill_d256(const PrefillParams& pp, cudaStream_t s) { return prefill_wide_launch<256, false>(pp, s); }
 
 }  // namespace tq

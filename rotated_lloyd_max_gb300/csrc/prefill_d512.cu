@@ -4,6 +4,6 @@
 namespace tq {
 
 int prefill_rows_d512() { return kPwRows; }
-cudaError_t launch_prefill_d512(const PrefillParams& pp, cudaStream_t s) { return prefill_wide_launch<512>(pp, s); }
+cudaError_t launch_prefill_d512(const PrefillParams& pp, cudaStream_t s) { return prefill_wide_launch<512, false>(pp, s); }
 
 }  // namespace tq

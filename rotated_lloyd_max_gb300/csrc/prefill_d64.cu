@@ -4,6 +4,6 @@
 namespace tq {
 
 int prefill_rows_d64() { return kPfRows; }
-cudaError_t launch_prefill_d64(const PrefillParams& pp, cudaStream_t s) { return prefill_umma_launch<64>(pp, s); }
+cudaError_t launch_prefill_d64(const PrefillParams& pp, cudaStream_t s) { return prefill_umma_launch<64, false>(pp, s); }
 
 }  // namespace tq

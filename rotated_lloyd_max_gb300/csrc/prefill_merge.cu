@@ -6,10 +6,25 @@
 
 namespace tq {
 
+// whether a row sees a token at all
+__device__ __noinline__ bool sees_token(const PrefillParams& pp, int lb, int h, int tb, int row) {
+  const QueryParams& p = pp.q;
+  const CacheLen cl = cache_len(p, lb);
+  const int limit = row_limit(p, cl, tb, row);
+  if (!pp.q_block || limit > cl.n * kChunk) return limit > 0;  // every token, or one of the ring's
+  const int blocks = (p.T + pp.q_block - 1) / pp.q_block;
+  const int64_t at = ((int64_t)lb * blocks + row / p.G / pp.q_block) * p.Hkv + h;
+  const int cnt = min(pp.list_count[at], pp.list_stride);
+  for (int i = 0; i < cnt; ++i) {
+    const int e = pp.list[at * pp.list_stride + i];
+    if (e >= 0 && e < cl.n && e * kChunk < limit) return true;
+  }
+  return false;
+}
 // 1 / W; NaN where it is or where a row sees tokens of no finite logit, 0 where it sees no token
-__device__ __forceinline__ float inverse_weight(const QueryParams& p, int lb, int tb, int row, float W) {
+__device__ __forceinline__ float inverse_weight(const PrefillParams& pp, int lb, int h, int tb, int row, float W) {
   if (W > 0.f || W != W) return 1.f / W;
-  return row_limit(p, cache_len(p, lb), tb, row) > 0 ? __int_as_float(0x7fc00000) : 0.f;
+  return sees_token(pp, lb, h, tb, row) ? __int_as_float(0x7fc00000) : 0.f;
 }
 
 template <int D>
@@ -59,7 +74,7 @@ __global__ void __launch_bounds__(kThreads) prefill_merge_kernel(const __grid_co
     fwht_regs<E>(c);
     fwht_lanes<E>(c, lane, 32);
   }
-  const float iw = inverse_weight(p, lb, tb, row, W);
+  const float iw = inverse_weight(pp, lb, h, tb, row, W);
   uint16_t* out = pp.out + l * pp.o_ls + b * pp.o_bs + (int64_t)tok * pp.o_ts + (int64_t)(h * p.G + row % p.G) * D +
                   lane * E;
 #pragma unroll
@@ -88,16 +103,23 @@ __global__ void __launch_bounds__(256) prefill_merge_tiles_kernel(const __grid_c
   pdl_wait();
   const QueryParams& p = pp.q;
   const int tid = threadIdx.x, qd = tid & 3, sl = SL > 1 ? tid / (4 * ROWS) : 0, lr = (tid >> 2) % ROWS;
-  const int ntile = (pp.rows + 127) / 128, per = 128 / ROWS;  // CTAs of a tile
+  // listed records: whole row tiles of 256 for every block of queries
+  const int ntile = pp.q_block ? 2 * pp.tiles : (pp.rows + 127) / 128, per = 128 / ROWS;  // CTAs of a tile
   const int64_t blk = blockIdx.x / per;
   const int r = (int)(blockIdx.x % per) * ROWS + lr;
   const int tile = (int)(blk % ntile);
   const int64_t unit = blk / ntile;
-  const int row = tile * 128 + r, tok = row / p.G;
+  int first = tile * 128, rows_left = 0x7FFFFFFF;  // the tile's first row, rows of its block from there
+  if (pp.q_block) {
+    const int block = (tile >> 1) / pp.sub, off = ((tile >> 1) % pp.sub) * 256 + (tile & 1) * 128;
+    first = block * pp.q_block * p.G + off;
+    rows_left = pp.q_block * p.G - off;
+  }
+  const int row = first + r, tok = row / p.G;
   const int h = (int)(unit % p.Hkv), lb = (int)(unit / p.Hkv), b = lb % p.B, l = lb / p.B;
   const int tb = query_len(p, b);
-  if (tile * 128 + (int)(blockIdx.x % per) * ROWS >= tb * p.G) return;
-  const bool live = row < tb * p.G;
+  if ((int)(blockIdx.x % per) * ROWS >= min(rows_left, tb * p.G - first)) return;
+  const bool live = r < min(rows_left, tb * p.G - first);
   const int S = pp.Sc + pp.St;
   const float2* ml = pp.ws_ml + blk * S * 128 + r;
   const float4* acc = reinterpret_cast<const float4*>(pp.ws_acc) + (blk * S * (D / 4) + qd * (E / 4)) * 128 + r;
@@ -170,7 +192,7 @@ __global__ void __launch_bounds__(256) prefill_merge_tiles_kernel(const __grid_c
     for (int g = 1; g < SL; ++g) W += wsum[g * 4 * ROWS + 4 * lr + qd];
   }
   if (!live) return;
-  const float iw = inverse_weight(p, lb, tb, row, W);
+  const float iw = inverse_weight(pp, lb, h, tb, row, W);
   uint16_t* out = pp.out + l * pp.o_ls + b * pp.o_bs + (int64_t)tok * pp.o_ts + (int64_t)(h * p.G + row % p.G) * D + qd * E;
 #pragma unroll
   for (int e = 0; e < E; e += 8)
@@ -186,9 +208,8 @@ static cudaError_t merge_tiles_launch(const PrefillParams& pp, int64_t tiles, cu
 }
 
 cudaError_t launch_prefill_merge(const PrefillParams& pp, cudaStream_t s) {
-  const int64_t rows = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv * pp.rows;
-  const unsigned grid = (unsigned)((rows + 3) / 4);
-  const int64_t tiles = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv * ((pp.rows + 127) / 128);
+  const unsigned grid = (unsigned)cdiv((int64_t)pp.q.L * pp.q.B * pp.q.Hkv * pp.rows, 4);
+  const int64_t tiles = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv * (pp.q_block ? 2 * pp.tiles : (pp.rows + 127) / 128);
   switch (pp.q.D) {
     case 64: return merge_tiles_launch<64>(pp, tiles, s);
     case 128: return merge_tiles_launch<128>(pp, tiles, s);
@@ -196,6 +217,13 @@ cudaError_t launch_prefill_merge(const PrefillParams& pp, cudaStream_t s) {
     case 512: return launch_after(prefill_merge_kernel<512>, dim3(grid), kThreads, 0, s, 1, pp);
     default: return cudaErrorInvalidValue;
   }
+}
+
+// partials of a row each, as the kernel for few rows leaves them
+cudaError_t launch_prefill_merge_rows(const PrefillParams& pp, cudaStream_t s) {
+  const unsigned grid = (unsigned)cdiv((int64_t)pp.q.L * pp.q.B * pp.q.Hkv * pp.rows, 4);
+  if (pp.q.D == 64) return launch_after(prefill_merge_kernel<64>, dim3(grid), kThreads, 0, s, 1, pp);
+  return launch_after(prefill_merge_kernel<128>, dim3(grid), kThreads, 0, s, 1, pp);
 }
 
 }  // namespace tq

@@ -327,7 +327,8 @@ __device__ __forceinline__ void decode_tile(const CodecDev& c, const uint8_t* re
 }
 
 // CAP: the call caps its logits (a kernel of its own: the branch cost registers).
-template <int D, bool DENSE, bool CAP>
+// LISTED: the row tile's records are those that its block's list names.
+template <int D, bool DENSE, bool CAP, bool LISTED>
 __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsigned char* sm, int64_t unit, int tile,
                                                   int split) {
   using C = PfCfg<D>;
@@ -338,15 +339,24 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
   const int S = pp.Sc + pp.St;
   const CacheLen cl = cache_len(p, lb);
   const int tb = query_len(p, b);
-  const int r0 = tile * kPfRows, rn = min(kPfRows, tb * p.G - r0);
+  const int block = LISTED ? tile / pp.sub : 0, off = LISTED ? tile % pp.sub * kPfRows : 0;
+  const int r0 = LISTED ? block * pp.q_block * p.G + off : tile * kPfRows;
+  const int rn = min(LISTED ? min(kPfRows, pp.q_block * p.G - off) : kPfRows, tb * p.G - r0);
   if (rn <= 0) return;
   const int base = DENSE ? cl.n * kChunk : 0;
   const int top = row_limit(p, cl, tb, r0 + rn - 1) - base;
   const int k0 = split * (DENSE ? pp.tps : pp.cps * kChunk);
-  const int k1 = min(min(k0 + (DENSE ? pp.tps : pp.cps * kChunk), DENSE ? cl.len : cl.n * kChunk), top);
+  int k1 = min(min(k0 + (DENSE ? pp.tps : pp.cps * kChunk), DENSE ? cl.len : cl.n * kChunk), top);
+  RecordRun run = {nullptr, k0 / kChunk, cl.n};
+  if constexpr (LISTED && !DENSE) {  // entries stand for whole records; what of them a row sees is its softmax's
+    const int64_t at = ((int64_t)lb * (pp.tiles / pp.sub) + block) * p.Hkv + h;
+    run.list = pp.list + at * pp.list_stride;
+    const int cnt = cl.n > 0 && top > 0 ? min(max(__ldg(pp.list_count + at), 0), pp.list_stride) : 0;
+    k1 = min(run.c0 + pp.cps, cnt) * kChunk;
+  }
   const int sidx = DENSE ? pp.Sc + split : split;
   // partials of the CTA's first 128-row tile (a second one follows S blocks later)
-  const int64_t blk = ((unit * ((pp.rows + 127) / 128) + 2 * tile) * S + sidx) * 128;
+  const int64_t blk = ((unit * (LISTED ? 2 * pp.tiles : (pp.rows + 127) / 128) + 2 * tile) * S + sidx) * 128;
   if (k0 >= k1) {
     for (int r = tid; r < rn; r += kPfThreads)
       pp.ws_ml[blk + (r >> 7) * S * 128 + (r & 127)] = make_float2(-INFINITY, 0.f);
@@ -354,10 +364,10 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
   }
   const int n = (k1 - k0 + kChunk - 1) / kChunk;  // 128-token tiles
   const int nt = rn > 128 ? 2 : 1;                // row tiles in use
-  const int c0 = k0 / kChunk;
   const uint8_t* kl = p.krec + l * p.krec_ls;
   const uint8_t* vl = p.vrec + l * p.vrec_ls;
-  auto rec_at = [&](bool key, int c) {
+  auto rec_at = [&](bool key, int i) {  // record i of the run
+    const int c = run_record<LISTED>(run, i);
     const int bytes = key ? p.kc.rec_bytes : p.vc.rec_bytes;
     return (key ? kl : vl) + rec_offset(p.table, p.table_stride, p.rec_cap, p.Hkv, b, h, c, bytes);
   };
@@ -389,7 +399,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
     float mk = 0.f, mv = 0.f;
     auto mag = [](float x) { return fabsf(x) < INFINITY ? fabsf(x) : 0.f; };
     for (int i = tid; i < n * (kChunk / 4); i += kPfThreads) {
-      const int c = c0 + i / (kChunk / 4), o = i % (kChunk / 4);
+      const int c = i / (kChunk / 4), o = i % (kChunk / 4);
       const float4 x = __ldg(reinterpret_cast<const float4*>(rec_at(true, c) + p.kc.off_norm) + o);
       const float4 y = __ldg(reinterpret_cast<const float4*>(rec_at(false, c) + p.vc.off_norm) + o);
       mk = fmaxf(mk, fmaxf(fmaxf(mag(x.x), mag(x.y)), fmaxf(mag(x.z), mag(x.w))));
@@ -590,14 +600,15 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
       const unsigned char* klut = p.kc.bits == 4 ? sm + C::LUT : nullptr;
       const unsigned char* vlut = vtable ? sm + C::LUT : nullptr;
       RecSource ks = rec_source<D>(p.kc, kl, w, lane), vs = rec_source<D>(p.vc, vl, w, lane);
-      auto seek = [&](RecSource& r, int c) {  // contiguous records follow one another
-        if (p.table || c == c0) r.next = r.layer + rec_offset(p.table, p.table_stride, p.rec_cap, p.Hkv, b, h, c, r.bytes);
+      auto seek = [&](RecSource& r, int i) {  // contiguous records follow one another
+        if (LISTED || p.table || i == 0)
+          r.next = r.layer + rec_offset(p.table, p.table_stride, p.rec_cap, p.Hkv, b, h, run_record<LISTED>(run, i), r.bytes);
         else r.next += r.bytes;
       };
       Packed<D> xk, xv;
-      seek(ks, c0);
+      seek(ks, 0);
       load_tile<D>(ks, xk);
-      seek(vs, c0);
+      seek(vs, 0);
       load_tile<D>(vs, xv);
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
@@ -608,7 +619,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.k_full[s]);
         if (i + 1 < n) {
-          seek(ks, c0 + i + 1);
+          seek(ks, i + 1);
           load_tile<D>(ks, xk);
         }
         mbar_wait_idle(&ms.v_empty[s], ph, abort_f);
@@ -617,7 +628,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
         __syncwarp();
         if (lane == 0) mbar_arrive(&ms.v_full[s]);
         if (i + 1 < n) {
-          seek(vs, c0 + i + 1);
+          seek(vs, i + 1);
           load_tile<D>(vs, xv);
         }
       }
@@ -630,7 +641,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
     const uint32_t lrow = (uint32_t)(32 * q) << 16;
     const uint32_t tS = tb0 + 128 * t + lrow, tO = tb0 + 256 + D * t + lrow;
     // tokens it sees, counted from the run's first; rows of no query see everything
-    const int lim = r < rn ? row_limit(p, cl, tb, r0 + r) - base - k0 : 0x7FFFFFFF;
+    const int lim = r < rn ? row_limit(p, cl, tb, r0 + r) - base - (LISTED && !DENSE ? 0 : k0) : 0x7FFFFFFF;
     // the largest logit where references moved; how low a tile's maximum may lie against one
     float mref = -INFINITY, lsum = 0.f, peak = -INFINITY, low = -INFINITY;
     const SoftCap cap = make_cap(p.scap, p.iscap);
@@ -638,7 +649,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
     for (int i = 0; i < n; ++i) {
       mbar_wait_idle(&ms.s_full[t], i & 1, abort_f);
       tc_fence_after();
-      const int seen = lim - i * kChunk;  // columns below it
+      const int seen = LISTED && !DENSE ? listed_seen(run, i, lim) : lim - i * kChunk;  // columns below it
       const bool edge = __any_sync(0xffffffffu, seen < kChunk);
       uint32_t w[64];  // weights as pairs; chunk c of S becomes columns 16 c .. 16 c + 15
       float mx = -INFINITY, tm = -INFINITY;
@@ -790,7 +801,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
   }
 }
 
-template <int D, bool CAP>
+template <int D, bool CAP, bool LISTED>
 __global__ void __launch_bounds__(kPfThreads, 1) prefill_umma_kernel(const __grid_constant__ PrefillParams pp) {
   pdl_start();
   extern __shared__ __align__(1024) unsigned char smraw[];
@@ -799,14 +810,14 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_umma_kernel(const __gri
   const int64_t U = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv * pp.tiles;
   const int split = (int)(blockIdx.x / U), tile = (int)(blockIdx.x % U % pp.tiles);
   const int64_t unit = blockIdx.x % U / pp.tiles;
-  if (split < pp.Sc) prefill_umma_body<D, false, CAP>(pp, sm, unit, tile, split);
-  else prefill_umma_body<D, true, CAP>(pp, sm, unit, tile, split - pp.Sc);
+  if (split < pp.Sc) prefill_umma_body<D, false, CAP, LISTED>(pp, sm, unit, tile, split);
+  else prefill_umma_body<D, true, CAP, LISTED>(pp, sm, unit, tile, split - pp.Sc);
 }
 
-template <int D>
+template <int D, bool LISTED>
 cudaError_t prefill_umma_launch(const PrefillParams& pp, cudaStream_t s) {
   if (pp.Sc + pp.St == 0) return cudaSuccess;
-  auto kern = pp.q.scap > 0.f ? prefill_umma_kernel<D, true> : prefill_umma_kernel<D, false>;
+  auto kern = pp.q.scap > 0.f ? prefill_umma_kernel<D, true, LISTED> : prefill_umma_kernel<D, false, LISTED>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PfCfg<D>::SMEM);
   if (e != cudaSuccess) return e;
   // the split of the registers counts on this many at launch

@@ -165,7 +165,7 @@ __device__ __forceinline__ void patch_chunk(const CodecDev& cd, const uint8_t* r
   }
 }
 
-template <int D, bool DENSE>
+template <int D, bool DENSE, bool LISTED>
 __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsigned char* sm, int64_t unit, int tile,
                                                   int split) {
   using C = PwCfg<D>;
@@ -177,24 +177,33 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
   const int S = pp.Sc + pp.St;
   const CacheLen cl = cache_len(p, lb);
   const int tb = query_len(p, b);
-  const int r0 = tile * kPwRows, rn = min(kPwRows, tb * p.G - r0);
+  const int block = LISTED ? tile / pp.sub : 0, off = LISTED ? tile % pp.sub * kPwRows : 0;
+  const int r0 = LISTED ? block * pp.q_block * p.G + off : tile * kPwRows;
+  const int rn = min(LISTED ? min(kPwRows, pp.q_block * p.G - off) : kPwRows, tb * p.G - r0);
   if (rn <= 0) return;
   const int base = DENSE ? cl.n * kChunk : 0;
   const int top = row_limit(p, cl, tb, r0 + rn - 1) - base;
   const int k0 = split * (DENSE ? pp.tps : pp.cps * kChunk);
-  const int k1 = min(min(k0 + (DENSE ? pp.tps : pp.cps * kChunk), DENSE ? cl.len : cl.n * kChunk), top);
+  int k1 = min(min(k0 + (DENSE ? pp.tps : pp.cps * kChunk), DENSE ? cl.len : cl.n * kChunk), top);
+  RecordRun run = {nullptr, k0 / kChunk, cl.n};
+  if constexpr (LISTED && !DENSE) {  // entries stand for whole records
+    const int64_t at = ((int64_t)lb * (pp.tiles / pp.sub) + block) * p.Hkv + h;
+    run.list = pp.list + at * pp.list_stride;
+    const int cnt = cl.n > 0 && top > 0 ? min(max(__ldg(pp.list_count + at), 0), pp.list_stride) : 0;
+    k1 = min(run.c0 + pp.cps, cnt) * kChunk;
+  }
   const int sidx = DENSE ? pp.Sc + split : split;
   const int64_t wrow = unit * pp.rows + r0;
   if (k0 >= k1) {
     for (int r = tid; r < rn; r += kPwThreads) pp.ws_ml[(wrow + r) * S + sidx] = make_float2(-INFINITY, 0.f);
     return;
   }
-  const int n = (k1 - k0 + kChunk - 1) / kChunk, c0 = k0 / kChunk;
+  const int n = (k1 - k0 + kChunk - 1) / kChunk;
   const bool one = DENSE ? p.ktail == p.vtail : p.shared_kv != 0;  // keys are the values
   const uint8_t* kl = p.krec + l * p.krec_ls;
   const uint8_t* vl = p.vrec + l * p.vrec_ls;
-  auto rec_at = [&](bool key, int c) {
-    return (key ? kl : vl) + rec_offset(p.table, p.table_stride, p.rec_cap, p.Hkv, b, h, c,
+  auto rec_at = [&](bool key, int i) {  // record i of the run
+    return (key ? kl : vl) + rec_offset(p.table, p.table_stride, p.rec_cap, p.Hkv, b, h, run_record<LISTED>(run, i),
                                         key ? p.kc.rec_bytes : p.vc.rec_bytes);
   };
   // ---------------------------------------------------------------- set-up
@@ -218,7 +227,7 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
       for (int k = 8; k < 16; ++k) vtable = vtable && p.kc.centroids[k] == p.vc.centroids[k];
     float mv = 0.f;  // the run's largest value scale
     for (int i = tid; i < n * (kChunk / 4); i += kPwThreads) {
-      const float4 y = __ldg(reinterpret_cast<const float4*>(rec_at(false, c0 + i / (kChunk / 4)) + p.vc.off_norm) + i % (kChunk / 4));
+      const float4 y = __ldg(reinterpret_cast<const float4*>(rec_at(false, i / (kChunk / 4)) + p.vc.off_norm) + i % (kChunk / 4));
       mv = fmaxf(mv, fmaxf(fmaxf(fabsf(y.x), fabsf(y.y)), fmaxf(fabsf(y.z), fabsf(y.w))));
     }
     mv = warp_max(mv);
@@ -288,7 +297,7 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
       if (lane == 0) {
         ms.qf[r] = f;
         ms.ref[r] = -INFINITY;
-        ms.lim[r] = r < rn ? row_limit(p, cl, tb, row) - base - k0 : 0x7FFFFFFF;
+        ms.lim[r] = r < rn ? row_limit(p, cl, tb, row) - base - (LISTED && !DENSE ? 0 : k0) : 0x7FFFFFFF;
       }
     }
   }
@@ -384,7 +393,7 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
       const int kat = (32 * w + (lane >> 3)) * (D * kbits / 8) + (8 * grp + (lane & 7)) * kbits;
       const int vat = (32 * w + (lane >> 3)) * (D * vbits / 8) + (8 * grp + (lane & 7)) * vbits;
       Chunk kx[PER], vx[PER];
-      const uint8_t *krec = rec_at(true, c0), *vrec = rec_at(false, c0);
+      const uint8_t *krec = rec_at(true, 0), *vrec = rec_at(false, 0);
 #pragma unroll
       for (int x = 0; x < PER; ++x) {
         load_chunk_b<D>(kbits, krec + kat + 32 * x * kbits, kx[x]);
@@ -409,8 +418,8 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
 #pragma unroll 1
       for (int i = 0; i < n; ++i) {
         const bool more = i + 1 < n;
-        const uint8_t* knext = more ? rec_at(true, c0 + i + 1) : krec;
-        const uint8_t* vnext = one || !more ? vrec : rec_at(false, c0 + i + 1);
+        const uint8_t* knext = more ? rec_at(true, i + 1) : krec;
+        const uint8_t* vnext = one || !more ? vrec : rec_at(false, i + 1);
 #pragma unroll
         for (int x = 0; x < PER; ++x) {
           put(p.kc, krec, x);
@@ -446,7 +455,7 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
     float lacc[2] = {0.f, 0.f};  // sums of rows lane and 32 + lane over this warp's tokens
     auto scale_at = [&](bool key, int i) {
       if constexpr (DENSE) return 1.f;
-      const float n = __ldg(reinterpret_cast<const float*>(rec_at(key, c0 + i) + (key ? p.kc.off_norm : p.vc.off_norm)) + tok);
+      const float n = __ldg(reinterpret_cast<const float*>(rec_at(key, i) + (key ? p.kc.off_norm : p.vc.off_norm)) + tok);
       return finite_or_nan(n);
     };
     float nk1 = scale_at(true, 0), nv1 = scale_at(false, 0);
@@ -459,8 +468,15 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
       }
       mbar_wait_idle(&ms.s_full, i & 1, abort_f);
       tc_fence_after();
-      const int at = i * kChunk + tok;
-      const bool edge = (i + 1) * kChunk > low;
+      // the tile's first token as limits count: from the run's, or (LISTED) the sequence's first on;
+      // an entry that names no record is past them all
+      int from = i * kChunk;
+      if constexpr (LISTED && !DENSE) {
+        const int e = run_entry<true>(run, i);
+        from = e < 0 || e >= run.n ? 0x7FFFFFFF - kChunk : e * kChunk;
+      }
+      const int at = from + tok;
+      const bool edge = from + kChunk > low;
       // logits of rows 32 hh .. (log2 units, -inf where the row does not see the token)
       auto logits = [&](int hh, float (&t)[32]) {
         uint32_t a[32];
@@ -671,7 +687,7 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
   }
 }
 
-template <int D>
+template <int D, bool LISTED>
 __global__ void __launch_bounds__(kPwThreads, 1) prefill_wide_kernel(const __grid_constant__ PrefillParams pp) {
   pdl_start();
   extern __shared__ __align__(1024) unsigned char smraw[];
@@ -679,17 +695,17 @@ __global__ void __launch_bounds__(kPwThreads, 1) prefill_wide_kernel(const __gri
   const int64_t U = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv * pp.tiles;
   const int split = (int)(blockIdx.x / U), tile = (int)(blockIdx.x % U % pp.tiles);
   const int64_t unit = blockIdx.x % U / pp.tiles;
-  if (split < pp.Sc) prefill_wide_body<D, false>(pp, sm, unit, tile, split);
-  else prefill_wide_body<D, true>(pp, sm, unit, tile, split - pp.Sc);
+  if (split < pp.Sc) prefill_wide_body<D, false, LISTED>(pp, sm, unit, tile, split);
+  else prefill_wide_body<D, true, LISTED>(pp, sm, unit, tile, split - pp.Sc);
 }
 
-template <int D>
+template <int D, bool LISTED>
 cudaError_t prefill_wide_launch(const PrefillParams& pp, cudaStream_t s) {
   if (pp.Sc + pp.St == 0) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(prefill_wide_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, PwCfg<D>::SMEM);
+  const cudaError_t e = cudaFuncSetAttribute(prefill_wide_kernel<D, LISTED>, cudaFuncAttributeMaxDynamicSharedMemorySize, PwCfg<D>::SMEM);
   if (e != cudaSuccess) return e;
   const int64_t grid = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv * pp.tiles * (pp.Sc + pp.St);
-  prefill_wide_kernel<D><<<(unsigned)grid, kPwThreads, PwCfg<D>::SMEM, s>>>(pp);
+  prefill_wide_kernel<D, LISTED><<<(unsigned)grid, kPwThreads, PwCfg<D>::SMEM, s>>>(pp);
   return cudaGetLastError();
 }
 

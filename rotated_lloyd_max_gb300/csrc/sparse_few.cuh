@@ -1,0 +1,584 @@
+// Attention over listed records and the ring for at most 16 query rows a list
+// (query heads of a kv head x tokens of a block), head dims 64 and 128, codecs
+// without side lists: the decode step of a long cache.
+//
+// Eight warps a CTA; four share a record (32 tokens each), the two groups take
+// every other one of the split's list.  Tokens are the M dimension of the scores
+// (K q~^T, rows as N), coordinates that of the outputs (V^T p), so that 8 rows
+// fill the N of mma.sync and both operands A are decoded from the packed codes
+// straight into registers: a lane holds d / 4 neighbouring codes of four keys, and
+// d / 8 codes of eight values, whose nibbles are paired by token before the lookup.
+// Every pair of codes is one lookup in a table with a copy per lane (no bank
+// conflicts).  The words of the next record are loaded as soon as this one's are
+// used; warps share nothing until the end, so that no barrier holds up the loads.
+//
+// Centroids and rotated queries are f16 (11 bits), logits take the key's scale and
+// sums in f32.  A weight enters times its value's scale, relative to the running
+// maxima of both and 2^14 above f16's 1: what lies within 2^-28 of the largest
+// keeps 11 bits, so that a token with nearly all of a row's weight leaves the
+// others theirs.  The ring's weights are two bf16 (16 bits) against exact values.
+#pragma once
+
+#include "prefill.cuh"
+
+namespace tq {
+
+constexpr int kFewThreads = 256;
+constexpr int kFewIds = 256;  // records of a split at most
+
+template <int D, int KB, int VB, int NT>
+struct FewCfg {
+  static constexpr int KTAB = (1 << (2 * KB)) * 128, VTAB = VIdx<VB>::ENTRIES * 128;
+  static constexpr int QF = KTAB + VTAB, QFB = D / 16 * NT * 32 * 8;
+  static constexpr int IDS = QF + QFB, MISC = IDS + kFewIds * 4;
+  static constexpr int MISCB = 8 * NT * 8 + 64;
+  static constexpr int RED = 8 * 8 * (D + D / 8) * 4;  // the warps' outputs of eight rows
+  static constexpr int ML = (RED > MISC + MISCB ? RED : MISC + MISCB);
+  static constexpr int SMEM = ML + 8 * 8 * NT * 8;
+};
+
+// NB bits of a packed row from bit `off` on, loaded now and aligned when used
+template <int NB>
+struct Run {
+  static constexpr bool AL = NB % 32 == 0;
+  static constexpr int NW = (NB + 31) / 32, RAW = AL ? NW : NW + 1;
+  uint32_t r[RAW];
+  __device__ __forceinline__ void load(const uint8_t* row, int off) {
+    const uint32_t* p = reinterpret_cast<const uint32_t*>(row) + (off >> 5);
+    if constexpr (RAW == 4 && AL) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
+      r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
+    } else if constexpr (RAW == 2 && AL) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+      r[0] = v.x; r[1] = v.y;
+    } else {
+#pragma unroll
+      for (int i = 0; i < RAW; ++i) r[i] = __ldg(p + i);
+    }
+  }
+  __device__ __forceinline__ void get(int off, uint32_t (&w)[NW]) const {
+#pragma unroll
+    for (int i = 0; i < NW; ++i) w[i] = AL ? r[i] : __funnelshift_r(r[i], r[i + (AL ? 0 : 1)], off & 31);
+  }
+};
+
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t r;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+// A warp's softmax state: rows 8 nt + 2 t + e, and its outputs: coordinates
+// (d / 8) g + 2 mc (+ 1 for elements 2, 3), rows 2 t (+ 1 for odd elements).
+template <int D, int NT>
+struct FewState {
+  float m[NT][2], l[NT][2];
+  float acc[NT][D / 16][4];
+  int ev;  // exponent of the largest value scale so far
+
+  __device__ __forceinline__ void init() {
+    ev = -100;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        m[nt][e] = -INFINITY;
+        l[nt][e] = 0.f;
+      }
+#pragma unroll
+      for (int mc = 0; mc < D / 16; ++mc)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[nt][mc][e] = 0.f;
+    }
+  }
+  // x[mi][nt][2 half + e]: logits (log2 units) of token 16 mi + 8 half + g; becomes weights
+  // against the running maxima.  grow: factor of the outputs that the scales ask for.
+  __device__ __forceinline__ void weigh(float (&x)[2][NT][4], float grow) {
+    bool moved = grow != 1.f;
+    float mn[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float v = fmaxf(fmaxf(x[0][nt][e], x[0][nt][2 + e]), fmaxf(x[1][nt][e], x[1][nt][2 + e]));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+        mn[nt][e] = v > m[nt][e] + 1.f ? v : m[nt][e];  // weights of up to 2 spare a rescaling
+        moved = moved || mn[nt][e] != m[nt][e];
+      }
+    if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float f[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          f[e] = mn[nt][e] != m[nt][e] ? ex2(m[nt][e] - mn[nt][e]) : 1.f;
+          l[nt][e] *= f[e];
+          m[nt][e] = mn[nt][e];
+          f[e] *= grow;
+        }
+#pragma unroll
+        for (int mc = 0; mc < D / 16; ++mc)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[nt][mc][e] *= f[e & 1];
+      }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float ref = m[nt][e] > -INFINITY ? m[nt][e] : 0.f;
+#pragma unroll
+        for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            const float w = ex2(x[mi][nt][2 * half + e] - ref);
+            x[mi][nt][2 * half + e] = w;
+            l[nt][e] += w;
+          }
+      }
+  }
+};
+
+// The records of a split.
+template <int D, int KB, int VB, int NT>
+__device__ __forceinline__ void few_records(const PrefillParams& pp, unsigned char* sm, const int* ids, int n, int l, int b,
+                                            int h, const float* qf, const int* lim, int low, FewState<D, NT>& st) {
+  using C = FewCfg<D, KB, VB, NT>;
+  constexpr int KS = D / 16, KR = D / 4, VR = D / 8, KNB = KR * KB, VNB = VR * VB;
+  constexpr int FW = VIdx<VB>::FW, KROW = D * KB / 8, VROW = D * VB / 8;
+  constexpr int VNW = Run<VNB>::NW, ZW = VB == 3 ? 2 * VNW : VNW;
+  const QueryParams& p = pp.q;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int w4 = warp & 3;
+  const uint32_t loff = lane * 4;
+  const unsigned char *ktab = sm, *vtab = sm + C::KTAB;
+  const ByteTable kbt = byte_table(ktab, loff, 128), vbt = byte_table(vtab, loff, 128);
+  const uint2* qfrag = reinterpret_cast<const uint2*>(sm + C::QF) + lane;
+  const uint8_t* kl = p.krec + l * p.krec_ls;
+  const uint8_t* vl = p.vrec + l * p.vrec_ls;
+  Run<KNB> kr[4];
+  Run<VNB> vr[8];
+  float nk[4], nv[4], nk1[4], nv1[4];
+  auto load_keys = [&](int c) {
+    const uint8_t* rec = kl + rec_offset(p.table, p.table_stride, p.rec_cap, p.Hkv, b, h, c, p.kc.rec_bytes);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      kr[i].load(rec + (32 * w4 + 8 * i + g) * KROW, KNB * t);
+      nk1[i] = __ldg(reinterpret_cast<const float*>(rec + p.kc.off_norm) + 32 * w4 + 8 * i + g);
+    }
+  };
+  auto load_values = [&](int c) {
+    const uint8_t* rec = vl + rec_offset(p.table, p.table_stride, p.rec_cap, p.Hkv, b, h, c, p.vc.rec_bytes);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)  // tokens 16 (i / 4) + 2 t + {0, 1, 8, 9}
+      vr[i].load(rec + (32 * w4 + 16 * (i >> 2) + 2 * t + (i & 1) + 8 * ((i >> 1) & 1)) * VROW, VNB * g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      nv1[i] = __ldg(reinterpret_cast<const float*>(rec + p.vc.off_norm) + 32 * w4 + 8 * i + g);
+  };
+  int i = warp >> 2;
+  if (i >= n) return;
+  load_keys(ids[i]);
+  load_values(ids[i]);
+#pragma unroll 1
+  for (; i < n; i += 2) {
+    const int c = ids[i], next = i + 2 < n ? ids[i + 2] : c;
+    // ---------------------------------------------------------------- scores
+    float x[2][NT][4];
+#pragma unroll
+    for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[mi][nt][e] = 0.f;
+    {
+      uint32_t w[4][Run<KNB>::NW];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        kr[k].get(KNB * t, w[k]);
+        nk[k] = finite_or_nan(nk1[k]);
+      }
+#pragma unroll
+      for (int kk = 0; kk < KS; ++kk) {
+        uint32_t a[2][4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int at = 4 * kk + 2 * e;
+            uint32_t v;
+            if constexpr (KB == 4) v = byte_lookup(kbt, w[k][at / 8], at % 8 / 2);
+            else v = *reinterpret_cast<const uint32_t*>(ktab + pair_off(w[k], at * KB, 2 * KB, loff));
+            a[k >> 1][(k & 1) + 2 * e] = v;
+          }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint2 q = qfrag[(kk * NT + nt) * 32];
+          mma_f16(x[0][nt], a[0], q.x, q.y);
+          mma_f16(x[1][nt], a[1], q.x, q.y);
+        }
+      }
+    }
+    load_keys(next);
+    // ---------------------------------------------------------------- weights
+    const bool edge = (c + 1) * kChunk > low;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float f = qf[8 * nt + 2 * t + e];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float& v = x[k >> 1][nt][2 * (k & 1) + e];
+          v *= nk[k] * f;
+          if (p.scap > 0.f) v = soft_cap(v, p.scap, p.iscap);
+          if (edge) v = c * kChunk + 32 * w4 + 8 * k + g < lim[8 * nt + 2 * t + e] ? v : -INFINITY;
+        }
+      }
+    // the values' scales against the largest so far
+    uint32_t nb = 0u;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      nv[k] = nv1[k];
+      const uint32_t u = __float_as_uint(nv[k]) & 0x7FFFFFFFu;
+      nb = max(nb, u < 0x7F800000u ? u : 0u);
+    }
+    const int en = exp_of(__uint_as_float(__reduce_max_sync(0xffffffffu, nb)));
+    float grow = 1.f;
+    if (en > st.ev) {
+      grow = pow2i(st.ev - en);
+      st.ev = en;
+    }
+    st.weigh(x, grow);
+    const float up = pow2i(13 - st.ev);  // 2^14 2^-(ev + 1)
+#pragma unroll
+    for (int k = 0; k < 4; ++k) nv[k] *= up;
+    // ---------------------------------------------------------------- values
+#pragma unroll
+    for (int mt = 0; mt < 2; ++mt) {
+      uint32_t b0[NT], b1[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        b0[nt] = transpose8(pack2_f16(x[mt][nt][0] * nv[2 * mt], x[mt][nt][1] * nv[2 * mt]));
+        b1[nt] = transpose8(pack2_f16(x[mt][nt][2] * nv[2 * mt + 1], x[mt][nt][3] * nv[2 * mt + 1]));
+      }
+      uint32_t z[4][ZW];  // even and odd coordinates of tokens 2 t, 2 t + 1; of 2 t + 8, 2 t + 9
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint32_t r0[VNW], r1[VNW];
+        vr[4 * mt + 2 * k].get(VNB * g, r0);
+        vr[4 * mt + 2 * k + 1].get(VNB * g, r1);
+        v_pair_words<VB, VNW>(r0, r1, z[2 * k], z[2 * k + 1]);
+      }
+#pragma unroll
+      for (int mc = 0; mc < KS; ++mc) {
+        uint32_t a[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (2 * FW == 8) a[k] = byte_lookup(vbt, z[k][mc / 4], mc % 4);
+          else a[k] = *reinterpret_cast<const uint32_t*>(vtab + pair_off(z[k], mc * 2 * FW, 2 * FW, loff));
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma_f16(st.acc[nt][mc], a, b0[nt], b1[nt]);
+      }
+    }
+    load_values(next);
+  }
+}
+
+// The ring's tokens [k0, k1) of a split.
+template <int D, int NT>
+__device__ __forceinline__ void few_ring(const PrefillParams& pp, const uint2* qfrag, int k0, int k1, int len, int l, int b,
+                                         int h, int start, const float* qf, const int* lim, int low, FewState<D, NT>& st) {
+  constexpr int KS = D / 16, KR = D / 4, VR = D / 8;
+  const QueryParams& p = pp.q;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int64_t ring = l * p.tail_ls + (int64_t)(b * p.Hkv + h) * p.tail_cap * D;
+  const uint16_t *kt = p.ktail + ring, *vt = p.vtail + ring;
+  // clamped to the last token: its values are finite, its weights zero
+  auto row = [&](int tok) {
+    int s = start + min(tok, len - 1);
+    if (s >= p.tail_cap) s -= p.tail_cap;
+    return (int64_t)s * D;
+  };
+#pragma unroll 1
+  for (int a0 = k0 + 32 * warp; a0 < k1; a0 += kFewThreads) {
+    float x[2][NT][4];
+#pragma unroll
+    for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[mi][nt][e] = 0.f;
+    const uint16_t* rows[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) rows[i] = kt + row(a0 + 8 * i + g) + KR * t;
+#pragma unroll 2
+    for (int kk = 0; kk < KS; kk += 2) {
+      uint4 w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(rows[i] + 4 * kk));
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        uint32_t a[2][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          a[i >> 1][i & 1] = k ? w[i].z : w[i].x;
+          a[i >> 1][(i & 1) + 2] = k ? w[i].w : w[i].y;
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint2 q = qfrag[((kk + k) * NT + nt) * 32 + lane];
+          mma_bf16(x[0][nt], a[0], q.x, q.y);
+          mma_bf16(x[1][nt], a[1], q.x, q.y);
+        }
+      }
+    }
+    const bool edge = a0 + 32 > low;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float f = qf[8 * nt + 2 * t + e];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          float& v = x[k >> 1][nt][2 * (k & 1) + e];
+          v *= f;
+          if (p.scap > 0.f) v = soft_cap(v, p.scap, p.iscap);
+          if (edge) v = a0 + 8 * k + g < lim[8 * nt + 2 * t + e] ? v : -INFINITY;
+        }
+      }
+    st.weigh(x, 1.f);
+#pragma unroll 1
+    for (int mt = 0; mt < 2; ++mt) {
+      uint32_t bh[2][NT], bl[2][NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          const float u = mt ? x[1][nt][2 * k] : x[0][nt][2 * k], v = mt ? x[1][nt][2 * k + 1] : x[0][nt][2 * k + 1];
+          const uint32_t hi = pack2_bf16(u, v);
+          bh[k][nt] = transpose8(hi);
+          bl[k][nt] = transpose8(pack2_bf16(u - bf16_lo(hi), v - bf16_hi(hi)));
+        }
+      const uint16_t* vrow[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) vrow[k] = vt + row(a0 + 16 * mt + 2 * t + (k & 1) + 8 * (k >> 1)) + VR * g;
+#pragma unroll
+      for (int mc = 0; mc < KS; mc += 4) {
+        uint4 w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) w[k] = __ldg(reinterpret_cast<const uint4*>(vrow[k] + 2 * mc));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          auto at = [&](int k) { return j == 0 ? w[k].x : j == 1 ? w[k].y : j == 2 ? w[k].z : w[k].w; };
+          const uint32_t a[4] = {__byte_perm(at(0), at(1), 0x5410), __byte_perm(at(0), at(1), 0x7632),
+                                 __byte_perm(at(2), at(3), 0x5410), __byte_perm(at(2), at(3), 0x7632)};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_bf16(st.acc[nt][mc + j], a, bh[0][nt], bh[1][nt]);
+            mma_bf16(st.acc[nt][mc + j], a, bl[0][nt], bl[1][nt]);
+          }
+        }
+      }
+    }
+  }
+}
+
+template <int D, int KB, int VB, int NT>
+__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) sparse_few_kernel(const __grid_constant__ PrefillParams pp) {
+  using C = FewCfg<D, KB, VB, NT>;
+  constexpr int R = 8 * NT, E = D / 32, KR = D / 4;
+  const QueryParams& p = pp.q;
+  pdl_start();
+  extern __shared__ __align__(128) unsigned char sm[];
+  int* ids = reinterpret_cast<int*>(sm + C::IDS);
+  float* qf = reinterpret_cast<float*>(sm + C::MISC);  // logit factor of a row
+  int* lim = reinterpret_cast<int*>(qf + R);           // tokens it sees (dense: of the ring)
+  int* head = lim + R;                                 // records of the split
+  float2* wml = reinterpret_cast<float2*>(sm + C::ML); // the warps' statistics
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  // records' splits first, the ring's shorter ones behind them
+  const int64_t U = (int64_t)p.L * p.B * p.Hkv * pp.tiles;
+  const int split = (int)(blockIdx.x / U);
+  const bool dense = split >= pp.Sc;
+  const int64_t x = blockIdx.x % U;
+  const int h = (int)(x % p.Hkv), j = (int)(x / p.Hkv % pp.tiles), lb = (int)(x / p.Hkv / pp.tiles), b = lb % p.B, l = lb / p.B;
+  const int64_t unit = (int64_t)lb * p.Hkv + h;
+  const CacheLen cl = cache_len(p, lb);
+  const int tb = query_len(p, b);
+  const int r0 = j * pp.q_block * p.G, rn = min(pp.q_block, tb - j * pp.q_block) * p.G;
+  if (rn <= 0) return;
+  const int S = pp.Sc + pp.St;
+  const int64_t wrow = unit * pp.rows + r0;
+  const int base = dense ? cl.n * kChunk : 0;
+  int k0 = 0, k1 = 0, n = 0;
+  if (dense) {
+    k0 = (split - pp.Sc) * pp.tps;
+    k1 = min(min(k0 + pp.tps, cl.len), row_limit(p, cl, tb, r0 + rn - 1) - base);
+  } else if (warp == 0) {  // the split's entries that name a record, in their order
+    const int cnt = cl.n > 0 ? min(max(__ldg(pp.list_count + x), 0), pp.list_stride) : 0;
+    const int c0 = split * pp.cps, c1 = min(c0 + pp.cps, cnt);
+    int at = 0;
+    for (int c = c0; c < c1; c += 32) {
+      const int v = c + lane < c1 ? __ldg(pp.list + x * pp.list_stride + c + lane) : -1;
+      const bool on = v >= 0 && v < cl.n;
+      const uint32_t m = __ballot_sync(0xffffffffu, on);
+      if (on) ids[at + __popc(m & ((1u << lane) - 1u))] = v;
+      at += __popc(m);
+    }
+    if (lane == 0) *head = at;
+  }
+  // ---------------------------------------------------------------- queries: a warp a row
+  for (int r = warp; r < R; r += kFewThreads / 32) {
+    const int row = r0 + r;
+    float v[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) v[e] = 0.f;
+    if (r < rn) {
+      const uint16_t* qp = p.q + l * p.q_ls + b * p.q_bs + (int64_t)(row / p.G) * p.q_ts +
+                           (int64_t)(h * p.G + row % p.G) * D + lane * E;
+#pragma unroll
+      for (int e = 0; e < E; e += 2) {
+        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(qp + e));
+        v[e] = bf16_lo(w);
+        v[e + 1] = bf16_hi(w);
+      }
+    }
+    float f = p.sscale, sc = 1.f;
+    if (!dense) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const int c = lane * E + e;
+        if ((p.kc.signs[c >> 5] >> (c & 31)) & 1u) v[e] = -v[e];
+      }
+      fwht_regs<E>(v);
+      fwht_lanes<E>(v, lane, 32);
+      float mx = 0.f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        v[e] *= inv_sqrt_dim<D>();
+        mx = fmaxf(mx, fabsf(v[e]));
+      }
+      mx = warp_max(mx);
+      const int s = mx > 0.f ? 13 - exp_of(mx) : 0;  // largest in [2^13, 2^14)
+      sc = pow2i(s);
+      f *= pow2i(-15 - s);
+    }
+    if (lane == 0) {
+      qf[r] = f;
+      lim[r] = r < rn ? row_limit(p, cl, tb, row) - base : 0x7FFFFFFF;
+    }
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {  // coordinate c: lane c / KR's word of k-step (c % KR) / 4
+      const int c = lane * E + e, kk = c % KR / 4;
+      reinterpret_cast<uint32_t*>(sm + C::QF)[((kk * NT + (r >> 3)) * 32 + (r & 7) * 4 + c / KR) * 2 + (c & 2) / 2] =
+          dense ? pack2_bf16(v[e], v[e + 1]) : pack2_f16(v[e] * sc, v[e + 1] * sc);
+    }
+  }
+  if (!dense) {  // pair tables: entry i at 128 i, a copy of four bytes a lane
+    constexpr int KM = (1 << KB) - 1;
+    for (int i = tid; i < (1 << (2 * KB)) * 8; i += kFewThreads) {
+      const int e = i >> 3;
+      const uint32_t v = pack2_f16(p.kc.centroids[e & KM] * kTableScale, p.kc.centroids[e >> KB] * kTableScale);
+      reinterpret_cast<uint4*>(sm)[i] = make_uint4(v, v, v, v);
+    }
+    constexpr int FW = VIdx<VB>::FW, VM = (1 << VB) - 1;
+    for (int i = tid; i < VIdx<VB>::ENTRIES * 8; i += kFewThreads) {
+      const int e = i >> 3;
+      const uint32_t v = pack2_f16(p.vc.centroids[e & VM] * kTableScale, p.vc.centroids[(e >> FW) & VM] * kTableScale);
+      reinterpret_cast<uint4*>(sm + C::KTAB)[i] = make_uint4(v, v, v, v);
+    }
+  }
+  __syncthreads();
+  if (!dense) n = *head;
+  if (dense ? k0 >= k1 : n == 0) {
+    if (tid < rn) pp.ws_ml[(wrow + tid) * S + split] = make_float2(-INFINITY, 0.f);
+    return;
+  }
+  int low = 0x7FFFFFFF;
+#pragma unroll
+  for (int r = 0; r < R; ++r) low = min(low, lim[r]);
+  FewState<D, NT> st;
+  st.init();
+  if (dense) {
+    const int cap = p.tail_cap, start = p.tail_start ? ((p.tail_start[lb] % cap) + cap) % cap : 0;
+    few_ring<D, NT>(pp, reinterpret_cast<const uint2*>(sm + C::QF), k0, k1, cl.len, l, b, h, start, qf, lim, low, st);
+  } else {
+    few_records<D, KB, VB, NT>(pp, sm, ids, n, l, b, h, qf, lim, low, st);
+  }
+  // ---------------------------------------------------------------- the warps' partials: one of the split
+  const float un = dense ? 1.f : pow2i(-15) * pow2i(st.ev - 13);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float s = st.l[nt][e];
+#pragma unroll
+      for (int m = 4; m < 32; m <<= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
+      if (g == 0) wml[warp * R + 8 * nt + 2 * t + e] = make_float2(st.m[nt][e], s);
+    }
+  constexpr int RS = D + D / 8;
+  float* red = reinterpret_cast<float*>(sm);
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    __syncthreads();  // tables and lists, or the rows before, are done with
+    // element (row r, coordinate c) of a warp at r RS + c + 4 (c / 32) + r / 2: 32 stores, 32 banks
+#pragma unroll
+    for (int mc = 0; mc < D / 16; ++mc)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int c = D / 8 * g + 2 * mc + (e >> 1), r = 2 * t + (e & 1);
+        red[warp * 8 * RS + r * RS + c + 4 * (c >> 5) + (r >> 1)] = st.acc[nt][mc][e] * un;
+      }
+    __syncthreads();
+    for (int i = tid; i < 8 * D; i += kFewThreads) {
+      const int r = i / D, c = i % D, row = 8 * nt + r;
+      if (row >= rn) break;
+      float M = -INFINITY, W = 0.f, v = 0.f;
+#pragma unroll
+      for (int w = 0; w < 8; ++w) M = fmaxf(M, wml[w * R + row].x);
+#pragma unroll
+      for (int w = 0; w < 8; ++w) {
+        const float2 ml = wml[w * R + row];
+        // a NaN sum stays one, whatever the maximum is
+        const float f = ml.x > -INFINITY ? ex2(ml.x - M) : ml.y != ml.y ? 1.f : 0.f;
+        W = fmaf(f, ml.y, W);
+        v = fmaf(f, red[w * 8 * RS + r * RS + c + 4 * (c >> 5) + (r >> 1)], v);
+      }
+      pp.ws_acc[((wrow + row) * S + split) * D + c] = v;
+      if (c == 0) pp.ws_ml[(wrow + row) * S + split] = W != W ? make_float2(W, W) : make_float2(M, W);
+    }
+  }
+}
+
+template <int D, int KB, int VB, int NT>
+cudaError_t sparse_few_launch_t(const PrefillParams& pp, cudaStream_t s) {
+  auto kern = sparse_few_kernel<D, KB, VB, NT>;
+  constexpr int smem = FewCfg<D, KB, VB, NT>::SMEM;
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+  }
+  const int64_t grid = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv * pp.tiles * (pp.Sc + pp.St);
+  kern<<<(unsigned)grid, kFewThreads, smem, s>>>(pp);
+  return cudaGetLastError();
+}
+template <int D, int KB, int VB>
+cudaError_t sparse_few_launch_n(const PrefillParams& pp, cudaStream_t s) {
+  return pp.q_block * pp.q.G <= 8 ? sparse_few_launch_t<D, KB, VB, 1>(pp, s) : sparse_few_launch_t<D, KB, VB, 2>(pp, s);
+}
+template <int D, int KB>
+cudaError_t sparse_few_launch(const PrefillParams& pp, cudaStream_t s) {
+  switch (pp.q.vc.bits) {
+    case 1: return sparse_few_launch_n<D, KB, 1>(pp, s);
+    case 2: return sparse_few_launch_n<D, KB, 2>(pp, s);
+    case 3: return sparse_few_launch_n<D, KB, 3>(pp, s);
+    case 4: return sparse_few_launch_n<D, KB, 4>(pp, s);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace tq

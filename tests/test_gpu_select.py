@@ -1,0 +1,225 @@
+"""GPU tests of tq_select_records: lists equal those of the scores in 64 bits,
+entry by entry; ties, near ties, scores that are not finite, blocks of queries,
+sinks and newest records, causal limits, pages, long caches."""
+import math
+
+import numpy as np
+import pytest
+
+import synth
+import tq_testlib as tl
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def tq():
+    import torch
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from rotated_lloyd_max_gb300 import build
+    build.build()
+    import rotated_lloyd_max_gb300 as m
+    m.load()
+    return m
+
+
+def chosen(score, m, keep, sink, recent):
+    """The list of a block with scores [m]: numbers, or -inf where there is none."""
+    at = np.arange(m)
+    safe = (at < sink) | (at >= m - recent)
+    order = np.lexsort((at, -np.where(safe, np.inf, score[:m])))
+    best = np.sort(order[: min(m, keep)])
+    return np.concatenate([best, np.full(keep - len(best), -1)]).astype(np.int32)
+
+
+def want(q, lo, hi, n, ln, lens, G, qb, keep, sink, recent, causal=True):
+    """Lists [blocks][Hkv][keep] of one sequence: q [T][Hq][d], lo, hi [Hkv][n][d] float64."""
+    T, Hkv = q.shape[0], lo.shape[0]
+    out = []
+    for t0 in range(0, T, qb):
+        t1 = min(t0 + qb, lens)
+        row = []
+        for h in range(Hkv):
+            m = 0
+            score = np.full(n, -np.inf)
+            if t1 > t0:
+                total = 128 * n + ln
+                limit = total - lens + t1 if causal else total
+                m = max(0, min(n, -(-limit // 128)))
+                x = q[t0:t1, h * G:(h + 1) * G].reshape(-1, q.shape[-1])
+                with np.errstate(all="ignore"):
+                    s = np.maximum(x, 0) @ hi[h].T + np.minimum(x, 0) @ lo[h].T
+                s = np.where(np.isfinite(s), s, -np.inf)
+                score = s.max(0)
+            row.append(chosen(score, m, keep, sink, recent))
+        out.append(row)
+    return np.array(out)
+
+
+class Case:
+    def __init__(self, *, L=1, B=2, T=1, Hkv=2, G=4, d=128, n=40, tail=90, qb=1, keep=8, sink=1, recent=2, causal=True,
+                 lens=None, counts=None, paged=False, seed=0):
+        import torch
+        self.__dict__.update(L=L, B=B, T=T, Hkv=Hkv, G=G, d=d, n=n, tail=tail, qb=qb, keep=keep, sink=sink, recent=recent,
+                             causal=causal)
+        g = np.random.default_rng(seed)
+        self.lens = np.full(B, T) if lens is None else np.asarray(lens)
+        self.counts = np.full((L, B), n) if counts is None else np.broadcast_to(counts, (L, B))
+        self.ragged = lens is not None
+        self.q = synth.gaussian_bf16((L, B, T, Hkv * G, d), seed + 1)
+        wide = np.where(g.random(d) < 0.05, 6.0, 1.0)
+        mid = 0.4 * g.normal(size=(L, B, Hkv, n, d)) * wide
+        half = (2.0 + g.random((L, B, Hkv, n, d))) * wide
+        self.bounds = np.stack([mid - half, mid + half], -2).astype(np.float32)
+        self.bounds = (self.bounds.view(np.uint32) >> 16).astype(np.uint16)
+        self.paged, self.perm = paged, None
+        if paged:
+            self.perm = g.permutation(B * n + 3)[: B * n].reshape(B, n).astype(np.int32)
+
+    def run(self, tq, **kw):
+        import torch
+        i32 = lambda a: torch.from_numpy(np.ascontiguousarray(a, np.int32)).cuda()  # noqa: E731
+        bounds, table = tl.to_bf16_tensor(self.bounds, "cuda"), None
+        if self.paged:
+            pool = torch.full((self.L, self.B * self.n + 3, self.Hkv, 2, self.d), math.nan, dtype=torch.bfloat16, device="cuda")
+            for b in range(self.B):
+                for r in range(self.n):
+                    pool[:, int(self.perm[b, r])] = bounds[:, b, :, r]
+            bounds, table = pool, i32(self.perm)
+        blocks = -(-self.T // self.qb)
+        self.list = torch.full((self.L, self.B, blocks, self.Hkv, self.keep), 77, dtype=torch.int32, device="cuda")
+        self.count = torch.full((self.L, self.B, blocks, self.Hkv), 77, dtype=torch.int32, device="cuda")
+        self.kw = dict(q=tl.to_bf16_tensor(self.q, "cuda"), bounds=bounds, n_chunks=i32(self.counts), max_chunks=self.n,
+                       tail_len=i32(np.full((self.L, self.B), self.tail)), max_tail=self.tail,
+                       q_lens=i32(self.lens) if self.ragged else None, block_table=table, q_block=self.qb, keep=self.keep,
+                       sink=self.sink, recent=self.recent, causal=self.causal, list=self.list, count=self.count)
+        self.kw.update(kw)
+        tq.select_records(**self.kw)
+        torch.cuda.synchronize()
+        return self.list.cpu().numpy(), self.count.cpu().numpy()
+
+    def check(self, tq):
+        got, count = self.run(tq)
+        q = synth.bf16_bits_to_f32(self.q).astype(np.float64)
+        lo, hi = (synth.bf16_bits_to_f32(np.ascontiguousarray(self.bounds[..., i, :])).astype(np.float64) for i in (0, 1))
+        for l in range(self.L):
+            for b in range(self.B):
+                n = int(self.counts[l, b])
+                w = want(q[l, b], lo[l, b][:, :n], hi[l, b][:, :n], n, self.tail, int(self.lens[b]), self.G, self.qb,
+                         self.keep, self.sink, self.recent, self.causal)
+                np.testing.assert_array_equal(got[l, b], w)
+                np.testing.assert_array_equal(count[l, b], (w >= 0).sum(-1))
+
+
+CASES = {
+    "one_token": dict(),
+    "one_row": dict(G=1, B=1, Hkv=1, n=9, keep=3),
+    "d64_blocks": dict(d=64, T=37, qb=8, G=3, n=70, keep=11, lens=[37, 20], B=2),
+    "d256": dict(d=256, T=5, qb=2, G=5, n=33, keep=7),
+    "d512_many_rows": dict(d=512, T=9, qb=4, G=64, Hkv=1, B=1, n=30, keep=6),
+    "all_of_them": dict(n=6, keep=8),
+    "as_many_as_there_are": dict(n=8, keep=8),
+    "only_sinks_and_newest": dict(keep=5, sink=2, recent=3),
+    "no_sinks": dict(keep=4, sink=0, recent=0),
+    "long": dict(B=1, Hkv=1, n=2000, keep=100),
+    "longest": dict(B=1, Hkv=1, n=16384, keep=33, d=64),
+    "ragged_counts": dict(B=4, counts=[[40, 0, 1, 17]], lens=[3, 3, 0, 2], T=3, qb=2),
+    "paged": dict(paged=True, L=2, B=3, T=2, n=21, keep=5),
+    "queries_in_the_records": dict(T=300, qb=64, tail=20, n=12, keep=4, G=2),
+    "not_causal": dict(T=300, qb=64, tail=20, n=12, keep=4, G=2, causal=False),
+    "block_longer_than_the_queries": dict(T=5, qb=64, G=7, n=20),
+    "rows_past_a_tile": dict(T=41, qb=41, G=7, n=100, keep=20, B=1),
+    "more_queries_than_tokens": dict(T=200, qb=16, tail=3, n=1, keep=2, B=1, sink=0),
+}
+
+
+@pytest.mark.parametrize("name", CASES)
+def test_lists_against_64_bits(tq, name):
+    Case(seed=3, **CASES[name]).check(tq)
+
+
+def test_equal_scores_go_to_the_lower_index(tq):
+    """Records in groups of equal bounds, and queries of zeros (every score is 0)."""
+    c = Case(seed=4, n=90, keep=20)
+    c.bounds[..., 1:, :, :] = c.bounds[..., 0:1, :, :]
+    c.check(tq)
+    c = Case(seed=5, n=90, keep=20)
+    for r in range(90):
+        c.bounds[:, :, :, r] = c.bounds[:, :, :, r - r % 7]
+    c.check(tq)
+    c.q[:] = 0
+    c.check(tq)
+
+
+@pytest.mark.parametrize("d,G,qb,T", [(64, 1, 1, 1), (128, 4, 1, 2), (128, 5, 9, 9), (512, 16, 1, 1)])
+def test_scores_that_f32_cannot_tell_apart(tq, d, G, qb, T):
+    """Records that differ in one small coordinate beside large ones: the sums differ by 2^-30 of
+    themselves, in an order that is not the records'.  The values are few bits wide, so that 64 bits
+    hold every sum exactly."""
+    g = np.random.default_rng(6)
+    c = Case(seed=7, d=d, G=G, qb=qb, T=T, n=64, keep=17, sink=0, recent=1)
+    bf = lambda x: (np.float32(x).view(np.uint32) >> 16).astype(np.uint16)  # noqa: E731
+    c.q[:] = bf(np.float32(g.integers(1, 4, c.q.shape) * 64))
+    c.q[..., 3] = bf(np.full(c.q.shape[:-1], 2.0 ** -12, np.float32))
+    base = g.integers(1, 100, (1, 1, 1, 1, 2, d)).astype(np.float32)
+    b = np.broadcast_to(base, c.bounds.shape).copy()
+    b[..., 3] = g.integers(-60, 60, b.shape[:-1]) * 2.0 ** -6
+    c.bounds = bf(b)
+    c.check(tq)
+
+
+def test_scores_that_are_not_finite_come_last(tq):
+    """A record with NaN bounds and one with infinite ones, a query row of NaN, one of infinities: rows
+    are left out, records without a score come last, by index."""
+    c = Case(seed=8, n=12, keep=6, G=3, T=2, qb=2, sink=0, recent=0)
+    c.bounds[0, 0, :, 3] = 0x7FC0
+    c.bounds[0, 0, :, 7, 1] = 0x7F80
+    c.bounds[0, 1, :, :9] = 0x7FC0   # more than may be left out
+    c.q[0, 0, 1, 2] = 0x7FC0
+    c.q[0, 1, 0, 1, 5] = 0x7F80
+    c.check(tq)
+    c.q[0, 0] = 0x7FC0               # no row at all
+    c.check(tq)
+
+
+def test_captured_and_replayed_with_another_calls_workspace(tq):
+    import torch
+    c, other = Case(seed=9, n=64, T=3, qb=2, keep=9), Case(seed=10, n=64, T=3, qb=2, keep=9)
+    eager = c.run(tq)
+    other.run(tq)
+    a, b = tq.make_select_args(**c.kw), tq.make_select_args(**other.kw)
+    ws = torch.empty(tq.tq_select_records_workspace_size(a), dtype=torch.uint8, device="cuda")
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=s):
+        tq.tq_select_records(a, ws)
+    for _ in range(2):
+        c.list.fill_(5)
+        ws.fill_(0xFF)  # nothing is left from the call before
+        tq.tq_select_records(b, ws)
+        g.replay()
+        torch.cuda.synchronize()
+        np.testing.assert_array_equal(c.list.cpu().numpy(), eager[0])
+        np.testing.assert_array_equal(c.count.cpu().numpy(), eager[1])
+
+
+def test_strided_and_broadcast_queries(tq):
+    import torch
+    c = Case(seed=11, B=3, T=4, Hkv=1, G=5, n=30)
+    c.run(tq)
+    wide = tl.to_bf16_tensor(synth.gaussian_bf16((1, 1, 4, 9, 128), 12), "cuda")
+    view = wide[:, :, :, 2:7].expand(1, 3, 4, 5, 128)
+    tq.select_records(**{**c.kw, "q": view})
+    got = c.list.clone()
+    tq.select_records(**{**c.kw, "q": view.contiguous()})
+    assert torch.equal(got, c.list)
+
+
+def test_without_a_ring(tq):
+    """No tail_len: the records are all there is, and the newest of them hold the queries' own tokens."""
+    c = Case(seed=13, T=3, n=20, tail=0, qb=2)
+    c.check(tq)
+    got = c.list.clone()
+    tq.select_records(**{**c.kw, "tail_len": None, "max_tail": 0})
+    assert (got == c.list).all()
