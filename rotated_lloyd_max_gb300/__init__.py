@@ -212,19 +212,27 @@ def _check(fn: str, status: int):
 
 
 _raw_stream = None  # torch's handle of the current stream by device (a Stream object costs microseconds)
+_raw_device = None  # the current device's index (torch.cuda.current_device looks at torch's state first)
+
+
+def _current_device() -> int:
+    global _raw_device
+    if _raw_device is None:
+        import torch
+        torch.cuda.current_device()  # CUDA is up from here on
+        _raw_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    return _raw_device()
 
 
 def _stream(stream):
     global _raw_stream
-    import torch
     if stream is None:
         if _raw_stream is None:
+            import torch
             _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                                   lambda dev: torch.cuda.current_stream(dev).cuda_stream)
-        return c_p(_raw_stream(torch.cuda.current_device()))
-    if isinstance(stream, int):
-        return c_p(stream)
-    return c_p(stream.cuda_stream)
+        return _raw_stream(_current_device())
+    return stream if isinstance(stream, int) else stream.cuda_stream
 
 
 def _ptr(t):
@@ -489,11 +497,11 @@ def _check_tensors(dtype_of: dict):
 
 def _ready(args, workspace=None):
     """The call runs where its tensors are (they may have been checked under another current device)."""
-    import torch
-    dev = args._tensors[args._lead].device.index
-    _need(dev == torch.cuda.current_device(), f"the tensors are on device {dev}, not on the current one")
-    _need(workspace is None or (workspace.get_device() == dev and workspace.is_contiguous()),
-          "the workspace is on another device, or not contiguous")
+    dev = args._tensors[args._lead].get_device()
+    if dev != _current_device():
+        raise ValueError(f"the tensors are on device {dev}, not on the current one")
+    if workspace is not None and not (workspace.get_device() == dev and workspace.is_contiguous()):
+        raise ValueError("the workspace is on another device, or not contiguous")
 
 
 def _fits(args, k_codec, v_codec):
@@ -868,16 +876,19 @@ def make_head_norm(*, q_weight=None, k_weight=None, eps: float = 1e-6) -> tq_hea
             setattr(n, name + "_head_stride", w.stride(0) if w.dim() == 2 and w.shape[0] > 1 else 0)
     n.eps = eps
     n._tensors = (q_weight, k_weight)
+    n._fit = None
     return n
 
 
 def tq_norm_append(args: tq_append_args, norm: tq_head_norm, stream=None):
     """tq_append with the queries' and keys' heads normalised before the rotation (include/tq.h)."""
     _ready(args)
-    for w, heads in zip(norm._tensors, (args.n_q_heads, args.n_kv_heads)):
-        _need(w is None or (w.shape[-1] == args.head_dim and (w.dim() == 1 or w.shape[0] == heads) and
-                            w.device == args._tensors[args._lead].device),
-              "norm weights: expected [d] or [heads, d] on the tensors' device")
+    if norm._fit is not args:  # looked at once for two argument blocks
+        for w, heads in zip(norm._tensors, (args.n_q_heads, args.n_kv_heads)):
+            _need(w is None or (w.shape[-1] == args.head_dim and (w.dim() == 1 or w.shape[0] == heads) and
+                                w.device == args._tensors[args._lead].device),
+                  "norm weights: expected [d] or [heads, d] on the tensors' device")
+        norm._fit = args
     _check("tq_norm_append", load().tq_norm_append(ctypes.byref(args), ctypes.byref(norm), _stream(stream)))
 
 
@@ -991,14 +1002,19 @@ def make_record_lists(*, list, count, q_block: int = 1) -> tq_record_lists:
           "list, count: expected contiguous int32 [L, B, blocks, Hkv, entries] and [L, B, blocks, Hkv]")
     r = tq_record_lists(list.data_ptr(), count.data_ptr(), list.shape[4], q_block)
     r._tensors = (list, count)
+    r._fit = None
     return r
 
 
 def _lists_fit(args: tq_query_args, lists: tq_record_lists):
+    """The lists are those of the queries (looked at once for two argument blocks)."""
+    if lists._fit is args:
+        return
     _need(lists.q_block >= 1, "q_block: expected at least 1")
     want = (args.n_layers, args.batch, -(-args.t_q // lists.q_block), args.n_kv_heads)
     _need(tuple(lists._tensors[1].shape) == want and lists._tensors[0].device == args._tensors[0].device,
           f"list, count: expected {list(want)} lists on the queries' device")
+    lists._fit = args
 
 
 def tq_sparse_attn_workspace_size(args: tq_query_args, lists: tq_record_lists, k_codec: Codec,

@@ -140,18 +140,19 @@ tq_status select_plan(const tq_select_args* a, SelectPlan* pl) {
   p.bounds_ls = a->bounds_layer_stride;
   p.qb = std::min(a->q_block, a->t_q);
   p.blocks = (int)cdiv(a->t_q, p.qb);
+  p.group = make_fast_div((uint32_t)q.G);
   p.keep = a->keep;
   p.sink = a->sink;
   p.recent = a->recent;
   p.list = a->list;
   p.count = a->count;
-  p.tile = 64;  // 16 records a warp
+  p.tile = 128;  // 16 records a warp (select_records.cu)
   p.tiles = (int)std::max<int64_t>(1, cdiv(q.max_chunks, p.tile));
   const double lists = (double)q.L * q.B * q.Hkv * p.blocks;
   if (lists * p.tiles > 2147483647.0) return TQ_ERR_UNSUPPORTED;
   const size_t n = (size_t)lists;
   pl->limits = pad256(n * q.max_chunks * 4);
-  pl->exact = pl->limits + pad256(n * p.tiles * 8);
+  pl->exact = pl->limits + pad256(n * p.tiles * 4);
   pl->bytes = pl->exact + pad256(n * q.max_chunks * 8) + 256;
   return TQ_OK;
 }
@@ -288,7 +289,7 @@ tq_status tq_select_records(const tq_select_args* a, void* workspace, size_t wor
   if (workspace_bytes < pl.bytes) return TQ_ERR_WORKSPACE;
   char* ws = (char*)workspace;
   pl.p.scores = (float*)ws;
-  pl.p.limits = (float2*)(ws + pl.limits);
+  pl.p.limits = (float*)(ws + pl.limits);
   pl.p.exact = (uint64_t*)(ws + pl.exact);
   return launch_select_records(pl.p, (cudaStream_t)stream) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }

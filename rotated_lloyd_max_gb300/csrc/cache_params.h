@@ -115,13 +115,14 @@ struct SelectParams {
   const uint16_t* bounds;
   int64_t bounds_ls;
   int qb, blocks;     // tokens of a block, blocks of a sequence
+  FastDiv group;      // division by the query heads of a kv head
   int keep, sink, recent;
   int32_t* list;
   int32_t* count;
   // workspace
   int tiles, tile;    // CTAs of a list's scores; records of one
   float* scores;      // [lists][max_chunks]
-  float2* limits;     // [lists][tiles]: largest 1-norm of a query, largest bound
+  float* limits;      // [lists][tiles]: the largest sum of a row's |terms|
   uint64_t* exact;    // [lists][max_chunks]
 };
 

@@ -14,154 +14,240 @@
 // are exact in f32, and a sum kept as two f32 has twice the bits.  So the list
 // depends on neither the order of the sums nor the split of the work.
 //
-// e: the tensor core adds 16 products and the accumulator with a relative error
-// of at most 2^-21 of the largest partial sum (f32 accumulation with truncated
-// alignment is within 2^-22); 2 d / 16 such steps, partial sums at most
-// |q|_1 max|bound|: e = d 2^-24 |q|_1 max|bound|, of the list's largest |q|_1 and
-// bound.
+// e = 2^-22 a step of the tensor core's 2 d / 16, of the largest sum of a row's
+// |terms|: measured, its f32 accumulation (16 products and the accumulator, cut off
+// below the largest) is off by at most 2.5 2^-24 of that sum after one step and
+// 1.5 2^-24 a step after 64.
 #include "attn_mass.cuh"
 
 namespace tq {
 
-constexpr int kSelThreads = 128;  // scores: four warps, 16 records a warp at a time
-constexpr int kPickThreads = 256;
+constexpr int kSelThreads = 256;
+constexpr int kPickThreads = 512;
 
 // what a list covers
 struct SelList {
   int l, b, h, t0, rows, m;  // first token, query rows, records it may read
 };
-__device__ __forceinline__ SelList select_list(const SelectParams& p, int64_t list) {
-  SelList s;
-  const QueryParams& q = p.q;
-  s.h = (int)(list % q.Hkv);
-  const int64_t x = list / q.Hkv;
-  const int j = (int)(x % p.blocks);
+__device__ __forceinline__ void select_place(const SelectParams& p, int64_t list, SelList& s) {
+  s.h = (int)(list % p.q.Hkv);
+  const int64_t x = list / p.q.Hkv;
   const int lb = (int)(x / p.blocks);
-  s.b = lb % q.B;
-  s.l = lb / q.B;
-  const int tb = query_len(q, s.b);
-  s.t0 = j * p.qb;
-  const int nt = min(p.qb, tb - s.t0);
+  s.t0 = (int)(x % p.blocks) * p.qb;
+  s.b = lb % p.q.B;
+  s.l = lb / p.q.B;
+}
+// from the sequence's counters as they are
+__device__ __forceinline__ void select_extent(const SelectParams& p, SelList& s, int chunks, int tail, int queries) {
+  const QueryParams& q = p.q;
+  CacheLen cl;
+  cl.n = min(max(chunks, 0), min(q.max_chunks, q.rec_limit));
+  cl.len = min(max(tail, 0), q.max_tail);
+  cl.total = cl.n * kChunk + cl.len;
+  const int tb = min(max(queries, 0), q.T), nt = min(p.qb, tb - s.t0);
   s.rows = max(nt, 0) * q.G;
   s.m = 0;
   if (nt > 0) {
-    const CacheLen cl = cache_len(q, lb);
     const int limit = row_limit(q, cl, tb, (s.t0 + nt - 1) * q.G);
     s.m = max(0, min(cl.n, (limit + kChunk - 1) / kChunk));
   }
+}
+__device__ __forceinline__ SelList select_list(const SelectParams& p, int64_t list) {
+  SelList s;
+  select_place(p, list, s);
+  const int lb = s.l * p.q.B + s.b;
+  select_extent(p, s, __ldg(p.q.n_chunks + lb), p.q.tail_len ? __ldg(p.q.tail_len + lb) : 0,
+                p.q.q_lens ? __ldg(p.q.q_lens + s.b) : p.q.T);
   return s;
 }
 // query row r of a list: head r % G of token t0 + r / G
 __device__ __forceinline__ const uint16_t* query_row(const SelectParams& p, const SelList& s, int r) {
-  return p.q.q + s.l * p.q.q_ls + s.b * p.q.q_bs + (int64_t)(s.t0 + r / p.q.G) * p.q.q_ts +
-         (int64_t)(s.h * p.q.G + r % p.q.G) * p.q.D;
+  const int tok = (int)fast_div((uint32_t)r, p.group), head = r - tok * p.q.G;
+  return p.q.q + s.l * p.q.q_ls + s.b * p.q.q_bs + (int64_t)(s.t0 + tok) * p.q.q_ts + (int64_t)(s.h * p.q.G + head) * p.q.D;
 }
 __device__ __forceinline__ const uint16_t* bounds_row(const SelectParams& p, const SelList& s, int r) {
   return p.bounds + s.l * p.bounds_ls +
          rec_offset(p.q.table, p.q.table_stride, p.q.rec_cap, p.q.Hkv, s.b, s.h, r, 2 * p.q.D);
 }
-// the negative of a bf16 pair's halves, the others zero
-__device__ __forceinline__ uint32_t negative_halves(uint32_t w) { return w & (((w & 0x80008000u) >> 15) * 0xFFFFu); }
-__device__ __forceinline__ uint32_t abs_max2(uint32_t a, uint32_t w) {
-  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&a), __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w)));
-  return *reinterpret_cast<const uint32_t*>(&r);
+// all ones in the halves of a bf16 pair that are negative: one byte permutation that spreads the signs
+__device__ __forceinline__ uint32_t sign_mask2(uint32_t w) {
+  uint32_t r;
+  asm("prmt.b32 %0, %1, 0, 0xBB99;" : "=r"(r) : "r"(w));
+  return r;
+}
+// the negative halves (LOW) or the others, zero in their place
+template <bool LOW>
+__device__ __forceinline__ uint4 halves_of(const uint4& q) {
+  const uint32_t x = sign_mask2(q.x), y = sign_mask2(q.y), z = sign_mask2(q.z), w = sign_mask2(q.w);
+  return LOW ? make_uint4(q.x & x, q.y & y, q.z & z, q.w & w) : make_uint4(q.x & ~x, q.y & ~y, q.z & ~z, q.w & ~w);
+}
+// by halves, the larger magnitude; what is not finite counts as 0 (an exponent of ones carries into the sign)
+__device__ __forceinline__ uint32_t finite_abs2(uint32_t w) {
+  w &= 0x7FFF7FFFu;
+  return w & ~sign_mask2(w + 0x00800080u);
+}
+__device__ __forceinline__ uint4 max8(const uint4& a, const uint4& b) {
+  return make_uint4(__vmaxu2(a.x, b.x), __vmaxu2(a.y, b.y), __vmaxu2(a.z, b.z), __vmaxu2(a.w, b.w));
+}
+__device__ __forceinline__ uint4 abs4(const uint4& v) {
+  return make_uint4(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu, v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu);
+}
+// twice the error of an f32 score whose terms' magnitudes add up to at most `size`: 4 2^-24 a step (above)
+__device__ __forceinline__ float score_error2(int D, float size) { return size * ((float)D * 5.9604644775390625e-8f); }
+
+// Where query rows r0 .. lie as fragments: lane (g, t) of k-step pair k holds coordinates
+// 32 k + 8 t .. + 7 of row g.  [n-tile][pair][lane]; rows from nr on are zeros.
+template <int D, int T>
+__device__ __forceinline__ void query_fragments(const SelectParams& p, const SelList& s, int r0, int nr, uint4* frag) {
+  constexpr int KP = D / 32;
+  for (int i = threadIdx.x; i < (nr + 7) / 8 * KP * 32; i += T) {
+    const int ln = i & 31, k = (i >> 5) % KP, r = i / (32 * KP) * 8 + (ln >> 2);
+    if (r < nr) cp_async16(frag + i, reinterpret_cast<const uint4*>(query_row(p, s, r0 + r)) + 4 * k + (ln & 3));
+    else frag[i] = make_uint4(0, 0, 0, 0);
+  }
+  cp_async_commit();
+  cp_async_wait<0>();
+}
+// the largest finite one of a score fragment's rows below nr; rows 2 t, 2 t + 1 of an n-tile in c[0], c[1] (c[2], c[3])
+__device__ __forceinline__ void keep_best(float (&best)[2], const float (&c)[4], int at, int nr) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    best[e >> 1] = fmaxf(best[e >> 1], at + (e & 1) < nr && c[e] < INFINITY ? c[e] : -INFINITY);  // NaN is neither
+}
+// c += bounds x queries over 32 coordinates: u, v the bounds of records g, g + 8
+__device__ __forceinline__ void score_step(float (&c)[4], const uint4& u, const uint4& v, const uint4& w) {
+  const uint32_t a0[4] = {u.x, v.x, u.y, v.y}, a1[4] = {u.z, v.z, u.w, v.w};
+  mma_bf16(c, a0, w.x, w.y);
+  mma_bf16(c, a1, w.z, w.w);
 }
 
-// NT: n-tiles of eight query rows at a time
-template <int D, int NT>
-__global__ void __launch_bounds__(kSelThreads) select_scores_kernel(const __grid_constant__ SelectParams p) {
-  constexpr int KP = D / 32;  // pairs of k-steps of one half (q+ . hi or q- . lo)
-  extern __shared__ __align__(16) uint4 frag[];  // [n-tile][KP][half][lane]
-  __shared__ float red[2][kSelThreads / 32];
+// Scores of p.tile = 128 records a CTA, 16 a warp, against the list's query rows, which
+// lie in shared memory (64 KB of them at a time).  Up to head dim 128 a warp's bounds stay
+// in registers; the wider ones are read again (from L1) for every 8 NT rows.  The sum of
+// |terms| is bounded by that of |q_j| and the CTA's largest |bound| of coordinate j,
+// formed the same way.  1024 tokens of 32 heads in blocks of 64, 256 records: xx us.
+template <int D>
+struct ScoreCfg {
+  static constexpr bool HELD = D <= 128;
+  static constexpr int ROWS = 65536 / (2 * D), NT = HELD ? 2 : 4;  // query rows in shared memory; n-tiles at a time
+  static constexpr int SMEM = 65536;
+};
+template <int D>
+__global__ void __launch_bounds__(kSelThreads, 2) select_scores_kernel(const __grid_constant__ SelectParams p) {
+  using C = ScoreCfg<D>;
+  constexpr int KP = D / 32, NT = C::NT;  // pairs of k-steps of one half (q+ . hi or q- . lo)
+  extern __shared__ __align__(16) uint4 frag[];
+  __shared__ uint4 top[kSelThreads / 32][D / 8];  // the warps' largest |bound| by coordinate
+  __shared__ float red[kSelThreads / 32];
   pdl_start();
   const int64_t list = blockIdx.x / p.tiles;
   const int tile = (int)(blockIdx.x % p.tiles);
   const SelList s = select_list(p, list);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  const int c0 = tile * p.tile, c1 = min(c0 + p.tile, s.m);
-  if (c0 >= c1 || s.m <= p.keep) return;  // all of them are chosen
-  float qmax = 0.f;
-  uint32_t bmax = 0u;
-  for (int r0 = 0; r0 < s.rows; r0 += 8 * NT) {
-    const int nr = min(8 * NT, s.rows - r0);
-    if (r0) __syncthreads();
-    // fragments: lane (g, t) of k-step pair k holds coordinates 32 k + 8 t .. + 7 of row g
-    for (int i = tid; i < NT * KP * 32; i += kSelThreads) {
-      const int ln = i & 31, k = (i >> 5) % KP, nt = i / (32 * KP), r = 8 * nt + (ln >> 2);
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < nr) v = __ldg(reinterpret_cast<const uint4*>(query_row(p, s, r0 + r)) + 4 * k + (ln & 3));
-      const uint4 n = make_uint4(negative_halves(v.x), negative_halves(v.y), negative_halves(v.z), negative_halves(v.w));
-      frag[(nt * KP + k) * 64 + ln] = make_uint4(v.x ^ n.x, v.y ^ n.y, v.z ^ n.z, v.w ^ n.w);
-      frag[(nt * KP + k) * 64 + 32 + ln] = n;
-    }
-    for (int r = warp; r < nr; r += kSelThreads / 32) {  // 1-norms of the finite rows
-      const uint16_t* q = query_row(p, s, r0 + r);
-      float a = 0.f;
-      for (int j = 2 * lane; j < D; j += 64) {
-        const uint32_t w = __ldg(reinterpret_cast<const uint32_t*>(q + j));
-        a += fabsf(bf16_lo(w)) + fabsf(bf16_hi(w));
-      }
-      a = warp_sum(a);
-      if (a < INFINITY) qmax = fmaxf(qmax, a);
-    }
-    __syncthreads();
-    for (int c = c0 + 16 * warp; c < c1; c += 16 * (kSelThreads / 32)) {
-      const uint4* rows[2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int c0 = tile * p.tile, c1 = min(c0 + p.tile, s.m), c = c0 + 16 * warp;
+  if (c0 >= c1 || s.m <= p.keep) return;  // nothing here, or all of them are chosen
+  const uint4* rows[2];
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        rows[i] = reinterpret_cast<const uint4*>(bounds_row(p, s, min(c + 8 * i + g, c1 - 1))) + t;
-      float acc[NT][4];
+  for (int i = 0; i < 2; ++i) rows[i] = reinterpret_cast<const uint4*>(bounds_row(p, s, min(c + 8 * i + g, c1 - 1))) + t;
+  auto bound = [&](int i, int half, int k) { return __ldg(rows[i] + (half ? 0 : D / 8) + 4 * k); };  // hi, then lo
+  uint4 held[C::HELD ? KP : 1][2][2];
+  if constexpr (C::HELD) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+    for (int k = 0; k < KP; ++k)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
-#pragma unroll 4
-      for (int k = 0; k < KP; ++k)
+      for (int half = 0; half < 2; ++half)
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {  // hi with q+, lo with q-
-          const int at = (half ? 0 : D / 8) + 4 * k;
-          const uint4 x = __ldg(rows[0] + at), y = __ldg(rows[1] + at);
-          if (r0 == 0) {
-            bmax = abs_max2(abs_max2(abs_max2(abs_max2(bmax, x.x), x.y), x.z), x.w);
-            bmax = abs_max2(abs_max2(abs_max2(abs_max2(bmax, y.x), y.y), y.z), y.w);
-          }
-          const uint32_t a0[4] = {x.x, y.x, x.y, y.y}, a1[4] = {x.z, y.z, x.w, y.w};
+        for (int i = 0; i < 2; ++i) held[k][half][i] = bound(i, half, k);
+  }
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint4 q = frag[(nt * KP + k) * 64 + 32 * half + lane];
-            mma_bf16(acc[nt], a0, q.x, q.y);
-            mma_bf16(acc[nt], a1, q.z, q.w);
-          }
-        }
-      float best[2] = {-INFINITY, -INFINITY};
+  for (int k = 0; k < KP; ++k) {  // coordinates 32 k + 8 t .. of all the warp's records
+    uint4 m = make_uint4(0, 0, 0, 0);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (8 * nt + 2 * t + (e & 1) < nr && fabsf(acc[nt][e]) < INFINITY) best[e >> 1] = fmaxf(best[e >> 1], acc[nt][e]);
+    for (int half = 0; half < 2; ++half)
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], 1));
-        best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], 2));
-        const int r = c + 8 * i + g;
-        if (t == 0 && r < c1) {
-          float* at = p.scores + list * p.q.max_chunks + r;
-          *at = r0 ? fmaxf(*at, best[i]) : best[i];
+        uint4 x;
+        if constexpr (C::HELD) x = held[k][half][i];
+        else x = bound(i, half, k);
+        m = max8(m, make_uint4(finite_abs2(x.x), finite_abs2(x.y), finite_abs2(x.z), finite_abs2(x.w)));
+      }
+#pragma unroll
+    for (int j = 4; j < 32; j <<= 1)
+      m = max8(m, make_uint4(__shfl_xor_sync(0xffffffffu, m.x, j), __shfl_xor_sync(0xffffffffu, m.y, j),
+                             __shfl_xor_sync(0xffffffffu, m.z, j), __shfl_xor_sync(0xffffffffu, m.w, j)));
+    if (g == 0) top[warp][4 * k + t] = m;
+  }
+  float best[2] = {-INFINITY, -INFINITY}, size[2] = {0.f, 0.f};
+  for (int r0 = 0; r0 < s.rows; r0 += C::ROWS) {
+    const int nr = min(C::ROWS, s.rows - r0);
+    if (r0) __syncthreads();
+    query_fragments<D, kSelThreads>(p, s, r0, nr, frag);
+    __syncthreads();
+    if (r0 == 0) {  // of all the warps'
+      if (threadIdx.x < D / 2) {
+        uint32_t m = 0u;
+        for (int w = 0; w < kSelThreads / 32; ++w) m = __vmaxu2(m, reinterpret_cast<const uint32_t*>(top[w])[threadIdx.x]);
+        reinterpret_cast<uint32_t*>(top[0])[threadIdx.x] = m;
+      }
+      __syncthreads();
+    }
+    if (c < c1) {
+      for (int n0 = 0; n0 < nr; n0 += 8 * NT) {
+        const uint4* fr = frag + n0 / 8 * KP * 32 + lane;
+        float acc[NT][4];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
+#pragma unroll C::HELD ? KP : 2
+        for (int k = 0; k < KP; ++k) {
+          uint4 x[2][2];
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              if constexpr (C::HELD) x[half][i] = held[k][half][i];
+              else x[half][i] = bound(i, half, k);
+            }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if (nt && n0 + 8 * nt >= nr) break;
+            const uint4 q = fr[(nt * KP + k) * 32];
+            score_step(acc[nt], x[0][0], x[0][1], halves_of<false>(q));
+            score_step(acc[nt], x[1][0], x[1][1], halves_of<true>(q));
+          }
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) keep_best(best, acc[nt], n0 + 8 * nt + 2 * t, nr);
       }
     }
+    // the rows' sizes, a warp every eighth n-tile
+    for (int n0 = 8 * warp; n0 < nr; n0 += 8 * (kSelThreads / 32)) {
+      const uint4* fr = frag + n0 / 8 * KP * 32 + lane;
+      float acc[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+      for (int k = 0; k < KP; ++k) {
+        const uint4 m = top[0][4 * k + t];
+        score_step(acc, m, m, abs4(fr[k * 32]));
+      }
+      keep_best(size, acc, n0 + 2 * t, nr);
+    }
   }
-  float b = fmaxf(bf16_lo(bmax), bf16_hi(bmax));
-  b = warp_max(b);
-  qmax = warp_max(qmax);
-  if (lane == 0) {
-    red[0][warp] = qmax;
-    red[1][warp] = b;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], 1));
+    best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], 2));
+    const int r = c + 8 * i + g;
+    if (t == 0 && r < c1) p.scores[list * p.q.max_chunks + r] = best[i];
   }
+  const float sz = warp_max(size[0]);
+  if (lane == 0) red[warp] = sz;
   __syncthreads();
-  if (tid == 0)
-    p.limits[list * p.tiles + tile] = make_float2(fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3])),
-                                                  fmaxf(fmaxf(red[1][0], red[1][1]), fmaxf(red[1][2], red[1][3])));
+  if (threadIdx.x == 0) {
+    float m = 0.f;
+    for (int w = 0; w < kSelThreads / 32; ++w) m = fmaxf(m, red[w]);
+    p.limits[list * p.tiles + tile] = m;
+  }
 }
 
 // a float's order as an unsigned number's, and back
@@ -182,84 +268,109 @@ __device__ __forceinline__ void add_exact(float& a, float& c, float x) {
   a = s;
 }
 
+// (x, its rounding errors) of two sums in one, the larger part first
+__device__ __forceinline__ float2 join_exact(float2 a, float2 b) {
+  float s = a.x, c = __fadd_rn(a.y, b.y);
+  add_exact(s, c, b.x);
+  const float h = __fadd_rn(s, c);
+  return make_float2(h, __fadd_rn(c, __fsub_rn(s, h)));
+}
+
+constexpr int kPrune = 16;    // query rows from which on the exact scores ask for the f32 ones first
+constexpr int kSearch = 256;  // records up to which a warp's search finds the threshold
 struct PickMisc {
   uint32_t hist[256];
-  uint32_t warp[kPickThreads / 32];
-  uint32_t prefix, left, above, cand;
+  uint32_t warp[32];
+  uint32_t x, prefix, left, above, cand;
 };
 
-__global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const __grid_constant__ SelectParams p) {
-  extern __shared__ __align__(16) uint32_t keys[];  // [max_chunks], then candidates [max_chunks], then chosen records' bits
-  __shared__ PickMisc ms;
-  pdl_wait();
-  const int64_t list = blockIdx.x;
-  const SelList s = select_list(p, list);
+// The list of one block from its keys (smem, one a record), of T threads.  e2: twice the error of a score.
+// cand: room for every record; bits: a bit a record.  Starts and ends with every thread past its use of keys.
+template <int T>
+__device__ __forceinline__ void pick_list(const SelectParams& p, const SelList& s, int64_t list, const uint32_t* keys,
+                                          uint32_t* cand, uint32_t* bits, PickMisc& ms, float e2) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int32_t* out = p.list + list * p.keep;
-  const int take = min(s.m, p.keep);
-  if (tid == 0) p.count[list] = take;
-  for (int i = tid; i < p.keep; i += kPickThreads)
-    if (i >= take || s.m <= p.keep) out[i] = i < take ? i : -1;
-  if (s.m <= p.keep) return;
   const int M = p.q.max_chunks, words = (s.m + 31) / 32;
-  uint32_t* cand = keys + M;
-  uint32_t* bits = cand + M;
   // records that the scores decide on
   const int a = min(p.sink, s.m), z = max(a, s.m - p.recent), need = p.keep - a - (s.m - z);
-  for (int w = tid; w < words; w += kPickThreads) {
-    uint32_t v = 0u;
-    for (int i = 0; i < 32; ++i) {
-      const int r = 32 * w + i;
-      if (r < a || (r >= z && r < s.m)) v |= 1u << i;
-    }
+  for (int w = tid; w < words; w += T) {
+    const int lo = a - 32 * w, hi = z - 32 * w;  // chosen: bits below lo, and from hi to m
+    uint32_t v = lo >= 32 ? ~0u : lo > 0 ? (1u << lo) - 1u : 0u;
+    v |= hi >= 32 ? 0u : hi > 0 ? ~0u << hi : ~0u;
+    if (s.m - 32 * w < 32) v &= (1u << (s.m - 32 * w)) - 1u;
     bits[w] = v;
   }
-  const float* score = p.scores + list * M;
-  for (int i = a + tid; i < z; i += kPickThreads) keys[i] = order_key(__ldcg(score + i));
   if (tid == 0) {
     ms.prefix = 0u;
     ms.left = (uint32_t)need;
     ms.above = ms.cand = 0u;
   }
   if (need > 0) {
-    // ------------------------------------------------------------ the need-th largest key, eight bits at a time
-    for (int sh = 24; sh >= 0; sh -= 8) {
-      ms.hist[tid] = 0u;
-      __syncthreads();
-      const uint32_t prefix = ms.prefix, left = ms.left;
-      for (int i = a + tid; i < z; i += kPickThreads)
-        if (sh == 24 || (keys[i] >> (sh + 8)) == prefix) atomicAdd(&ms.hist[(keys[i] >> sh) & 255u], 1u);
-      __syncthreads();
-      // keys in bins from this thread's upwards: thread t looks at bin 255 - t
-      const uint32_t mine = ms.hist[255 - tid];
-      uint32_t inc = mine;
+    uint32_t x;
+    __syncthreads();
+    if (z - a <= kSearch) {
+      // ---------------------------------------------------------- the largest number that need keys reach, four bits at a
+      // time below what all keys have in common: every warp holds all keys and tries one of 16 numbers (a bit at a
+      // time by barriers, or by one warp, takes 2 us, this 0.5)
+      static_assert(T == 512, "16 warps");
+      uint32_t k[kSearch / 32], most = 0u, least = 0xFFFFFFFFu;
 #pragma unroll
-      for (int k = 1; k < 32; k <<= 1) {
-        const uint32_t o = __shfl_up_sync(0xffffffffu, inc, k);
-        if (lane >= k) inc += o;
+      for (int i = 0; i < kSearch / 32; ++i) {
+        const int j = a + 32 * i + lane;
+        k[i] = j < z ? keys[j] : 0u;
+        most = max(most, k[i]);
+        least = min(least, j < z ? k[i] : 0xFFFFFFFFu);
       }
-      if (lane == 31) ms.warp[warp] = inc;
-      __syncthreads();
-      for (int w = 0; w < warp; ++w) inc += ms.warp[w];
-      if (inc >= left && inc - mine < left) {
-        ms.prefix = prefix << 8 | (uint32_t)(255 - tid);
-        ms.left = left - (inc - mine);
+      most = __reduce_max_sync(0xffffffffu, most);
+      least = __reduce_min_sync(0xffffffffu, least);
+      x = least;
+      if (most != least) {
+        int sh = (31 - __clz((int)(most ^ least))) & ~3;
+        x = sh == 28 ? 0u : least >> (sh + 4) << (sh + 4);
+        for (; sh >= 0; sh -= 4) {
+          const uint32_t trial = x | (uint32_t)warp << sh;
+          int n[2] = {0, 0};
+#pragma unroll
+          for (int i = 0; i < kSearch / 32; i += 2) {
+            n[0] += k[i] >= trial;
+            n[1] += k[i + 1] >= trial;
+          }
+          const bool reached = (int)__reduce_add_sync(0xffffffffu, (unsigned)(n[0] + n[1])) >= need;
+          x |= (uint32_t)(__syncthreads_count(lane == 0 && reached) - 1) << sh;  // the numbers reached are the lower ones
+        }
       }
-      __syncthreads();
+    } else {
+      // ---------------------------------------------------------- eight bits at a time
+      for (int sh = 24; sh >= 0; sh -= 8) {
+        if (tid < 256) ms.hist[tid] = 0u;
+        __syncthreads();
+        const uint32_t prefix = ms.prefix, left = ms.left;
+        for (int i = a + tid; i < z; i += T)
+          if (sh == 24 || (keys[i] >> (sh + 8)) == prefix) atomicAdd(&ms.hist[(keys[i] >> sh) & 255u], 1u);
+        __syncthreads();
+        // keys in bins from this thread's upwards: thread t looks at bin 255 - t
+        const uint32_t mine = tid < 256 ? ms.hist[255 - tid] : 0u;
+        uint32_t inc = mine;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+          const uint32_t o = __shfl_up_sync(0xffffffffu, inc, k);
+          if (lane >= k) inc += o;
+        }
+        if (lane == 31) ms.warp[warp] = inc;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) inc += ms.warp[w];
+        if (tid < 256 && inc >= left && inc - mine < left) {
+          ms.prefix = prefix << 8 | (uint32_t)(255 - tid);
+          ms.left = left - (inc - mine);
+        }
+        __syncthreads();
+      }
+      x = ms.prefix;
     }
     // ------------------------------------------------------------ records that f32 cannot tell from it
-    float q1 = 0.f, bm = 0.f;
-    const int used = (s.m + p.tile - 1) / p.tile;
-    for (int i = lane; i < used; i += 32) {
-      const float2 v = __ldcg(p.limits + list * p.tiles + i);
-      q1 = fmaxf(q1, v.x);
-      bm = fmaxf(bm, v.y);
-    }
-    float e = warp_max(q1) * warp_max(bm) * ((float)p.q.D * 1.1920929e-7f);  // 2 e: d 2^-23
-    if (!(e < INFINITY)) e = 0.f;
-    const float x = key_value(ms.prefix);
-    const uint32_t lo = order_key(x - e), hi = order_key(x + e);
-    for (int i = a + tid; i < z; i += kPickThreads) {
+    const uint32_t lo = order_key(key_value(x) - e2), hi = order_key(key_value(x) + e2);
+    for (int i = a + tid; i < z; i += T) {
       const uint32_t k = keys[i];
       if (k > hi) {
         atomicOr(&bits[i >> 5], 1u << (i & 31));
@@ -272,104 +383,236 @@ __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const __grid_
     const int nc = (int)ms.cand, places = need - (int)ms.above;
     if (nc > places) {
       // ---------------------------------------------------------- their scores with twice the bits
-      uint64_t* exact = p.exact + list * M;
-      for (int i = tid; i < nc; i += kPickThreads) exact[i] = order_key(-(double)INFINITY);
+      unsigned long long* exact = reinterpret_cast<unsigned long long*>(p.exact) + list * M;
+      for (int i = tid; i < nc; i += T) exact[i] = 0ull;
       __syncthreads();
-      const int D = p.q.D, sub = lane & 7;  // eight lanes a candidate and row
+      const int D = p.q.D, sub = lane & 7, grp = tid >> 3;  // eight lanes a (candidate, row), four of them at a time
+      constexpr int NG = T / 8;
       const int64_t pairs = (int64_t)nc * s.rows;
-      for (int64_t i0 = warp * 4; i0 < pairs; i0 += kPickThreads / 8) {
-        const int64_t i = i0 + (lane >> 3);
-        const bool on = i < pairs;
-        const int c = on ? (int)(i / s.rows) : 0, r = on ? (int)(i % s.rows) : 0;
-        const uint4* q = reinterpret_cast<const uint4*>(query_row(p, s, r));
-        const uint4* bnd = reinterpret_cast<const uint4*>(bounds_row(p, s, (int)cand[c]));
-        float sum[2] = {0.f, 0.f}, err[2] = {0.f, 0.f};
-        for (int k = sub; k < D / 8; k += 8) {
-          const uint4 qv = __ldg(q + k), lv = __ldg(bnd + k), hv = __ldg(bnd + D / 8 + k);
-          const uint32_t qw[4] = {qv.x, qv.y, qv.z, qv.w}, lw[4] = {lv.x, lv.y, lv.z, lv.w}, hw[4] = {hv.x, hv.y, hv.z, hv.w};
+      for (int64_t i0 = 0; i0 < pairs; i0 += 4 * NG) {
+        const uint4 *q[4], *bnd[4];
+        int c[4];
+        bool far[4];
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t n = (qw[w] & 0x80008000u) >> 15, pick = n * 0xFFFFu, bw = (lw[w] & pick) | (hw[w] & ~pick);
-            add_exact(sum[0], err[0], bf16_lo(qw[w]) * bf16_lo(bw));
-            add_exact(sum[1], err[1], bf16_hi(qw[w]) * bf16_hi(bw));
+        for (int u = 0; u < 4; ++u) {
+          const int64_t i = i0 + u * NG + grp;
+          far[u] = i >= pairs;
+          c[u] = far[u] ? 0 : (int)(i / s.rows);
+          q[u] = reinterpret_cast<const uint4*>(query_row(p, s, far[u] ? 0 : (int)(i - (int64_t)c[u] * s.rows)));
+          bnd[u] = reinterpret_cast<const uint4*>(bounds_row(p, s, (int)cand[c[u]]));
+        }
+        if (s.rows > kPrune) {
+          // many rows: their sums in f32 first; a row further than e2 below the record's f32 score is not its maximum
+          float f[4] = {0.f, 0.f, 0.f, 0.f};
+          for (int k = sub; k < D / 8; k += 8)
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const uint4 qv = __ldg(q[u] + k), lv = __ldg(bnd[u] + k), hv = __ldg(bnd[u] + D / 8 + k);
+              const uint32_t qw[4] = {qv.x, qv.y, qv.z, qv.w}, lw[4] = {lv.x, lv.y, lv.z, lv.w}, hw[4] = {hv.x, hv.y, hv.z, hv.w};
+#pragma unroll
+              for (int w = 0; w < 4; ++w) {
+                const uint32_t pick = sign_mask2(qw[w]), bw = (lw[w] & pick) | (hw[w] & ~pick);
+                f[u] = fmaf(bf16_lo(qw[w]), bf16_lo(bw), f[u]);
+                f[u] = fmaf(bf16_hi(qw[w]), bf16_hi(bw), f[u]);
+              }
+            }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+#pragma unroll
+            for (int k = 1; k < 8; k <<= 1) f[u] += __shfl_xor_sync(0xffffffffu, f[u], k);
+            far[u] = far[u] || f[u] < key_value(keys[cand[c[u]]]) - e2;
           }
         }
-        double v = ((double)sum[0] + (double)sum[1]) + ((double)err[0] + (double)err[1]);
 #pragma unroll
-        for (int k = 1; k < 8; k <<= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
-        if (on && sub == 0 && fabs(v) < (double)INFINITY)
-          atomicMax(reinterpret_cast<unsigned long long*>(exact + c), (unsigned long long)order_key(v));
+        for (int u = 0; u < 4; ++u) {
+          if (__all_sync(0xffffffffu, far[u])) continue;
+          float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          for (int k = sub; k < D / 8; k += 8) {
+            const uint4 qv = __ldg(q[u] + k), lv = __ldg(bnd[u] + k), hv = __ldg(bnd[u] + D / 8 + k);
+            const uint32_t qw[4] = {qv.x, qv.y, qv.z, qv.w}, lw[4] = {lv.x, lv.y, lv.z, lv.w}, hw[4] = {hv.x, hv.y, hv.z, hv.w};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const uint32_t pick = sign_mask2(qw[w]), bw = (lw[w] & pick) | (hw[w] & ~pick);
+              add_exact(part[0].x, part[0].y, bf16_lo(qw[w]) * bf16_lo(bw));
+              add_exact(part[1].x, part[1].y, bf16_hi(qw[w]) * bf16_hi(bw));
+            }
+          }
+          float2 sum = join_exact(part[0], part[1]);
+#pragma unroll
+          for (int k = 1; k < 8; k <<= 1)
+            sum = join_exact(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, k), __shfl_xor_sync(0xffffffffu, sum.y, k)));
+          sum = join_exact(sum, make_float2(0.f, 0.f));
+          // the order of the pairs (sum to the nearest f32, what is left) is that of the sums
+          if (!far[u] && sub == 0 && fabsf(sum.x) < INFINITY)
+            atomicMax(exact + c[u], (unsigned long long)order_key(sum.x + 0.f) << 32 | order_key(sum.y + 0.f));
+        }
       }
       __syncthreads();
-      for (int i = tid; i < nc; i += kPickThreads) {
+      for (int i = tid; i < nc; i += T) {
         // the maxima were formed in L2: no line of L1 is asked for them
-        const uint64_t k = __ldcg(reinterpret_cast<const unsigned long long*>(exact) + i);
+        const unsigned long long k = __ldcg(exact + i);
         const uint32_t r = cand[i];
         int before = 0;
         for (int j = 0; j < nc; ++j) {
-          const uint64_t o = __ldcg(reinterpret_cast<const unsigned long long*>(exact) + j);
+          const unsigned long long o = __ldcg(exact + j);
           before += o > k || (o == k && cand[j] < r);
         }
         if (before < places) atomicOr(&bits[r >> 5], 1u << (r & 31));
       }
     } else {
-      for (int i = tid; i < nc; i += kPickThreads) atomicOr(&bits[cand[i] >> 5], 1u << (cand[i] & 31));
+      for (int i = tid; i < nc; i += T) atomicOr(&bits[cand[i] >> 5], 1u << (cand[i] & 31));
     }
   }
   __syncthreads();
   // ---------------------------------------------------------------- the chosen ones in ascending order
   uint32_t base = 0;
-  for (int w0 = 0; w0 < words; w0 += kPickThreads) {
-    const int w = w0 + tid;
-    uint32_t v = w < words ? bits[w] : 0u, inc = __popc(v);
-    const uint32_t mine = inc;
-#pragma unroll
-    for (int k = 1; k < 32; k <<= 1) {
-      const uint32_t o = __shfl_up_sync(0xffffffffu, inc, k);
-      if (lane >= k) inc += o;
-    }
-    __syncthreads();
-    if (lane == 31) ms.warp[warp] = inc;
+  for (int w0 = 0; w0 < words; w0 += T / 32) {  // a warp a word, a lane a record
+    const int w = w0 + warp;
+    const uint32_t v = w < words ? bits[w] : 0u;
+    if (w0) __syncthreads();
+    if (lane == 0) ms.warp[warp] = __popc(v);
     __syncthreads();
     uint32_t before = 0, all = 0;
-    for (int k = 0; k < kPickThreads / 32; ++k) {
-      if (k < warp) before += ms.warp[k];
-      all += ms.warp[k];
+#pragma unroll
+    for (int k = 0; k < T / 32; ++k) {
+      const uint32_t n = ms.warp[k];
+      if (k < warp) before += n;
+      all += n;
     }
-    uint32_t at = base + before + inc - mine;
-    for (; v; v &= v - 1) out[at++] = 32 * w + __ffs(v) - 1;
+    if ((v >> lane) & 1u) out[base + before + __popc(v & ((1u << lane) - 1u))] = 32 * w + lane;
     base += all;
   }
 }
 
-template <int D, int NT>
-static cudaError_t scores_launch(const SelectParams& p, int64_t lists, cudaStream_t s) {
-  const int smem = NT * (D / 32) * 64 * 16;
-  auto kern = select_scores_kernel<D, NT>;
-  if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess) return e;
+// what of a list needs no scores: all of it where it takes every record (returns true), else the count
+template <int T>
+__device__ __forceinline__ bool list_is_all(const SelectParams& p, const SelList& s, int64_t list) {
+  int32_t* out = p.list + list * p.keep;
+  if (threadIdx.x == 0) p.count[list] = min(s.m, p.keep);
+  if (s.m > p.keep) return false;
+  for (int i = threadIdx.x; i < p.keep; i += T) out[i] = i < s.m ? i : -1;
+  return true;
+}
+
+__global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const __grid_constant__ SelectParams p) {
+  extern __shared__ __align__(16) uint32_t keys[];  // [max_chunks], then candidates [max_chunks], then chosen records' bits
+  __shared__ PickMisc ms;
+  pdl_wait();
+  const int64_t list = blockIdx.x;
+  const SelList s = select_list(p, list);
+  if (list_is_all<kPickThreads>(p, s, list)) return;
+  const int M = p.q.max_chunks, lane = threadIdx.x & 31, Mp = (M + 3) & ~3;
+  const float* score = p.scores + list * M;
+  for (int i = threadIdx.x; i < s.m; i += kPickThreads) keys[i] = order_key(__ldcg(score + i));
+  float bm = 0.f;
+  const int used = (s.m + p.tile - 1) / p.tile;
+  for (int i = lane; i < used; i += 32) bm = fmaxf(bm, __ldcg(p.limits + list * p.tiles + i));
+  const float e2 = score_error2(p.q.D, warp_max(bm));
+  pick_list<kPickThreads>(p, s, list, keys, keys + Mp, keys + 2 * Mp, ms, e2);
+}
+
+// Scores and list in one CTA, for up to 256 records and eight query rows a list: 16
+// warps take 16 records each, whose bounds are on their way at once.
+constexpr int kOneThreads = 512, kOneRecords = 256;
+template <int D>
+__global__ void __launch_bounds__(kOneThreads, 2) select_one_kernel(const __grid_constant__ SelectParams p) {
+  constexpr int KP = D / 32;
+  __shared__ __align__(16) uint4 frag[KP * 32];
+  __shared__ __align__(16) uint32_t keys[2 * kOneRecords + kOneRecords / 32];
+  __shared__ PickMisc ms;
+  __shared__ float red[kOneThreads / 32];
+  const int64_t list = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int c = 16 * warp;
+  constexpr int AHEAD = 2;  // k-step pairs whose bounds are loaded ahead
+  uint4 x[AHEAD][2][2];
+  const uint4* rows[2];
+  SelList s;
+  select_place(p, list, s);
+  const int lb = s.l * p.q.B + s.b;
+  const int n0 = __ldg(p.q.n_chunks + lb), l0 = p.q.tail_len ? __ldg(p.q.tail_len + lb) : 0, t0 = p.q.q_lens ? __ldg(p.q.q_lens + s.b) : p.q.T;
+  if (c < p.q.max_chunks) {  // the first ones are on their way before the sequence's counts are known
+#pragma unroll
+    for (int i = 0; i < 2; ++i) rows[i] = reinterpret_cast<const uint4*>(bounds_row(p, s, min(c + 8 * i + g, p.q.max_chunks - 1))) + t;
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k)
+#pragma unroll
+      for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) x[k][half][i] = __ldg(rows[i] + (half ? 0 : D / 8) + 4 * k);
   }
-  kern<<<(unsigned)(lists * p.tiles), kSelThreads, smem, s>>>(p);
+  select_extent(p, s, n0, l0, t0);
+  if (list_is_all<kOneThreads>(p, s, list)) return;
+  const bool work = c < s.m;
+  query_fragments<D, kOneThreads>(p, s, 0, s.rows, frag);
+  __syncthreads();
+  float best[2] = {-INFINITY, -INFINITY}, size[2] = {0.f, 0.f};
+  if (work) {
+    float acc[4] = {0.f, 0.f, 0.f, 0.f}, sz[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int k = 0; k < KP; ++k) {
+      const uint4 q = frag[k * 32 + lane];
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        const uint4 u = x[k % AHEAD][half][0], v = x[k % AHEAD][half][1];
+        if (k + AHEAD < KP) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) x[k % AHEAD][half][i] = __ldg(rows[i] + (half ? 0 : D / 8) + 4 * (k + AHEAD));
+        }
+        const uint4 w = half ? halves_of<true>(q) : halves_of<false>(q);
+        score_step(acc, u, v, w);
+        score_step(sz, abs4(u), abs4(v), abs4(w));  // |terms|: |lo| where q is negative, |hi| where it is not
+      }
+    }
+    keep_best(best, acc, 2 * t, s.rows);
+    keep_best(size, sz, 2 * t, s.rows);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], 1));
+      best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], 2));
+      if (t == 0) keys[c + 8 * i + g] = order_key(best[i]);
+      if (c + 8 * i + g >= s.m) size[i] = 0.f;
+    }
+  }
+  const float sw = warp_max(fmaxf(size[0], size[1]));
+  if (lane == 0) red[warp] = sw;
+  __syncthreads();
+  const float e2 = score_error2(D, warp_max(red[lane & 15]));
+  pick_list<kOneThreads>(p, s, list, keys, keys + kOneRecords, keys + 2 * kOneRecords, ms, e2);
+}
+
+template <int D>
+static cudaError_t scores_launch(const SelectParams& p, int64_t lists, cudaStream_t s) {
+  const cudaError_t e = cudaFuncSetAttribute(select_scores_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, ScoreCfg<D>::SMEM);
+  if (e != cudaSuccess) return e;
+  select_scores_kernel<D><<<(unsigned)(lists * p.tiles), kSelThreads, ScoreCfg<D>::SMEM, s>>>(p);
   return cudaGetLastError();
 }
-template <int D>
-static cudaError_t scores_launch_d(const SelectParams& p, int64_t lists, cudaStream_t s) {
-  return p.qb * p.q.G <= 8 ? scores_launch<D, 1>(p, lists, s) : scores_launch<D, 4>(p, lists, s);
-}
+
+static bool select_in_one(const SelectParams& p) { return p.q.max_chunks <= kOneRecords && p.qb * p.q.G <= 8; }
 
 cudaError_t launch_select_records(const SelectParams& p, cudaStream_t s) {
   const int64_t lists = (int64_t)p.q.L * p.q.B * p.q.Hkv * p.blocks;
+  if (select_in_one(p)) {
+    switch (p.q.D) {
+      case 64: select_one_kernel<64><<<(unsigned)lists, kOneThreads, 0, s>>>(p); break;
+      case 128: select_one_kernel<128><<<(unsigned)lists, kOneThreads, 0, s>>>(p); break;
+      case 256: select_one_kernel<256><<<(unsigned)lists, kOneThreads, 0, s>>>(p); break;
+      case 512: select_one_kernel<512><<<(unsigned)lists, kOneThreads, 0, s>>>(p); break;
+      default: return cudaErrorInvalidValue;
+    }
+    return cudaGetLastError();
+  }
   cudaError_t e;
   switch (p.q.D) {
-    case 64: e = scores_launch_d<64>(p, lists, s); break;
-    case 128: e = scores_launch_d<128>(p, lists, s); break;
-    case 256: e = scores_launch_d<256>(p, lists, s); break;
-    case 512: e = scores_launch_d<512>(p, lists, s); break;
+    case 64: e = scores_launch<64>(p, lists, s); break;
+    case 128: e = scores_launch<128>(p, lists, s); break;
+    case 256: e = scores_launch<256>(p, lists, s); break;
+    case 512: e = scores_launch<512>(p, lists, s); break;
     default: return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess) return e;
-  const int smem = p.q.max_chunks * 8 + (p.q.max_chunks + 31) / 32 * 4;
+  const int smem = (p.q.max_chunks + 3) / 4 * 32 + (p.q.max_chunks + 31) / 32 * 4;
   if (smem > 48 * 1024) {
     e = cudaFuncSetAttribute(select_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;

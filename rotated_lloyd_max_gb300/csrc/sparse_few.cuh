@@ -19,6 +19,7 @@
 // others theirs.  The ring's weights are two bf16 (16 bits) against exact values.
 #pragma once
 
+#include "packed_run.cuh"
 #include "prefill.cuh"
 
 namespace tq {
@@ -35,31 +36,6 @@ struct FewCfg {
   static constexpr int RED = 8 * 8 * (D + D / 8) * 4;  // the warps' outputs of eight rows
   static constexpr int ML = (RED > MISC + MISCB ? RED : MISC + MISCB);
   static constexpr int SMEM = ML + 8 * 8 * NT * 8;
-};
-
-// NB bits of a packed row from bit `off` on, loaded now and aligned when used
-template <int NB>
-struct Run {
-  static constexpr bool AL = NB % 32 == 0;
-  static constexpr int NW = (NB + 31) / 32, RAW = AL ? NW : NW + 1;
-  uint32_t r[RAW];
-  __device__ __forceinline__ void load(const uint8_t* row, int off) {
-    const uint32_t* p = reinterpret_cast<const uint32_t*>(row) + (off >> 5);
-    if constexpr (RAW == 4 && AL) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p));
-      r[0] = v.x; r[1] = v.y; r[2] = v.z; r[3] = v.w;
-    } else if constexpr (RAW == 2 && AL) {
-      const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-      r[0] = v.x; r[1] = v.y;
-    } else {
-#pragma unroll
-      for (int i = 0; i < RAW; ++i) r[i] = __ldg(p + i);
-    }
-  }
-  __device__ __forceinline__ void get(int off, uint32_t (&w)[NW]) const {
-#pragma unroll
-    for (int i = 0; i < NW; ++i) w[i] = AL ? r[i] : __funnelshift_r(r[i], r[i + (AL ? 0 : 1)], off & 31);
-  }
 };
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
