@@ -33,14 +33,15 @@ int prefill_rows_d128();
 int prefill_rows_d256();
 int prefill_rows_d512();
 cudaError_t launch_prefill_merge(const PrefillParams& pp, cudaStream_t s);
-cudaError_t launch_prefill_merge_rows(const PrefillParams& pp, cudaStream_t s);
+cudaError_t launch_merge_rows(const PrefillParams& pp, cudaStream_t s);
 
 }  // namespace tq
 
 namespace {
 
 constexpr int kFewRows = 16;   // rows of a list on mma.sync at most
-constexpr int kFewRecords = 256;  // records of a split there at most
+constexpr int kFewRecords = 256;  // records of a CTA's part of a list there at most
+constexpr double kFewTile = 2, kFewPart = 3;  // a tile of 128 ring tokens, a list's part, in records
 
 // ----------------------------------------------------------------- bounds
 // where bounds or records lie: contiguous or a pool
@@ -80,7 +81,10 @@ tq_status bounds_params(const tq_codec* kcod, const tq_bounds_args* a, BoundsPar
   p->max_new = std::min(a->max_new, std::max(a->max_chunks, 1));
   p->bounds = (uint16_t*)a->bounds;
   p->bounds_ls = a->bounds_layer_stride;
-  if ((double)a->n_layers * a->batch * a->n_kv_heads * p->max_new > 2147483647.0) return TQ_ERR_UNSUPPORTED;
+  if ((double)a->n_layers * a->batch * a->n_kv_heads * p->max_new > 2000000000.0) return TQ_ERR_UNSUPPORTED;
+  p->by_new = make_fast_div((uint32_t)p->max_new);
+  p->by_heads = make_fast_div((uint32_t)p->Hkv);
+  p->by_batch = make_fast_div((uint32_t)p->B);
   return TQ_OK;
 }
 
@@ -190,37 +194,80 @@ tq_status sparse_plan(const tq_query_args* a, const tq_record_lists* r, const tq
   const int64_t units = (int64_t)q.L * q.B * q.Hkv, U = units * tiles, sms = sm_count();
   if (tiles > 0x3FFFFFFF || U > 0x7FFFFFFFll) return TQ_ERR_UNSUPPORTED;
   pp.tiles = (int)tiles;
-  // The split count that minimises, in 128-token tiles' time, waves of records'
-  // CTAs with their set-up and epilogue, the ring's CTAs in the last wave's idle
-  // slots or after it, and the partials' traffic.
   const int64_t keep = r->list_stride, ring = cdiv(q.max_tail, TQ_CHUNK), most = std::max(keep, ring);
-  const int64_t slots = pl->few ? 2 * sms : sms;
-  const double setup = 6, part = 0.03;
-  double best = 1e300;
-  for (int64_t s = 1; s <= std::min<int64_t>(most, 128); ++s) {
-    if (a->splits > 0 && s != std::min<int64_t>(a->splits, std::min<int64_t>(most, 128))) continue;
-    const int64_t per = cdiv(most, s);
-    const int64_t sc = cdiv(keep, per), sr = cdiv(ring, per);
-    const int64_t waves = cdiv(U * sc, slots);
-    const double one = (double)cdiv(keep, sc) + setup, rest = (double)(sr ? cdiv(ring, sr) : 0) + setup;
-    const double idle = (double)(waves * slots - U * sc) * one, dense = (double)(U * sr) * rest;
-    double cost = (double)waves * one + part * (double)(U * (sc + sr));
-    if (dense > 0.9 * idle) cost += std::max(rest, (dense - 0.9 * idle) / (double)slots);
-    if (cost < best) {
-      best = cost;
-      pp.cps = (int)per;
-      pp.Sc = (int)sc;
-      pp.tps = (int)(TQ_CHUNK * per);
-      pp.St = (int)sr;
+  if (pl->few) {
+    // One wave of two CTAs per SM, shared between records and ring.  A CTA's time, in
+    // records: its entries, kFewTile for a tile of 128 ring tokens, and kFewPart for every
+    // list it has a part of (query set-up, first loads, joining its warps).  Of the
+    // entries per CTA that fill the wave, or fit the lists' ends, the best are taken.
+    const int64_t slots = 2 * sms;
+    auto most_parts = [](int64_t len, int64_t n) -> int64_t {  // CTAs that share a list of len, n a CTA
+      return len == 0 ? 0 : n % len == 0 ? 1 : len % n == 0 ? len / n : (len - 1) / n + 2;
+    };
+    auto parts_of = [](int64_t len, int64_t n) -> int64_t {  // lists that a CTA has a part of
+      return len == 0 ? 0 : n % len == 0 ? n / len : len % n == 0 ? 1 : (n - 1) / len + 2;
+    };
+    double best = 1e300;
+    auto consider = [&](int64_t per) {
+      per = std::max<int64_t>(1, std::min<int64_t>(per, keep > kFewRecords ? kFewRecords : U * keep));
+      const int64_t ctas = cdiv(U * keep, per), waves = cdiv(ctas, slots);
+      const int64_t left = std::max<int64_t>(waves * slots - ctas, std::max<int64_t>(1, slots / 16));
+      int64_t tiles_per = std::max<int64_t>(1, cdiv(U * ring, left));
+      if (tiles_per > ring && ring) tiles_per = cdiv(tiles_per, ring) * ring;
+      const double a1 = (double)waves * ((double)per + kFewPart * (double)parts_of(keep, per));
+      const double b1 = ring ? kFewTile * (double)tiles_per + kFewPart * (double)parts_of(ring, tiles_per) : 0;
+      const double cost = std::max(a1, b1) + 0.05 * (a1 + b1);
+      if (cost < best) {
+        best = cost;
+        pp.cps = (int)per;
+        pp.tps = (int)tiles_per;
+      }
+    };
+    if (a->splits > 0) {
+      consider(cdiv(keep, std::min<int64_t>(a->splits, keep)));
+    } else {
+      const double share = (keep + kFewPart) / (keep + kFewPart + (ring ? kFewTile * ring + kFewPart : 0));
+      const int64_t even = std::max<int64_t>(2, (int64_t)((double)(U * keep) / (share * (double)slots)) + 1);
+      for (const int64_t per : {even, even + 1, even + even / 8, 2 * cdiv(even, 2)}) consider(per);
+      if (even >= keep)
+        for (int64_t k = even / keep; k <= even / keep + 1; ++k) consider(k * keep);
+      else
+        for (int64_t k = std::max<int64_t>(1, keep / even); k >= std::max<int64_t>(1, keep / even - 1); --k) consider(cdiv(keep, k));
     }
-  }
-  if (pl->few && pp.cps > kFewRecords) {
-    pp.cps = kFewRecords;
-    pp.Sc = (int)cdiv(keep, pp.cps);
+    pp.ring = (int)ring;
+    pp.Sc = (int)most_parts(keep, pp.cps);
+    pp.St = (int)most_parts(ring, pp.tps);
+    if (cdiv(U * keep, pp.cps) + cdiv(U * ring, pp.tps) > 0x7FFFFFFFll) return TQ_ERR_UNSUPPORTED;
+    pp.rec_ctas = (int)cdiv(U * keep, pp.cps);
+    pp.ring_ctas = (int)cdiv(U * ring, pp.tps);
+  } else {
+    // The split count that minimises, in 128-token tiles' time, waves of records'
+    // CTAs with their set-up and epilogue, the ring's CTAs in the last wave's idle
+    // slots or after it, and the partials' traffic.
+    const double setup = 6, part = 0.03;
+    double best = 1e300;
+    for (int64_t s = 1; s <= std::min<int64_t>(most, 128); ++s) {
+      if (a->splits > 0 && s != std::min<int64_t>(a->splits, std::min<int64_t>(most, 128))) continue;
+      const int64_t per = cdiv(most, s);
+      const int64_t sc = cdiv(keep, per), sr = cdiv(ring, per);
+      const int64_t waves = cdiv(U * sc, sms);
+      const double one = (double)cdiv(keep, sc) + setup, rest = (double)(sr ? cdiv(ring, sr) : 0) + setup;
+      const double idle = (double)(waves * sms - U * sc) * one, dense = (double)(U * sr) * rest;
+      double cost = (double)waves * one + part * (double)(U * (sc + sr));
+      if (dense > 0.9 * idle) cost += std::max(rest, (dense - 0.9 * idle) / (double)sms);
+      if (cost < best) {
+        best = cost;
+        pp.cps = (int)per;
+        pp.Sc = (int)sc;
+        pp.tps = (int)(TQ_CHUNK * per);
+        pp.St = (int)sr;
+      }
+    }
+    if (U * (pp.Sc + pp.St) > 0x7FFFFFFFll) return TQ_ERR_UNSUPPORTED;
   }
   const bool by_tile = !pl->few && d <= 128;  // partials of whole 128-row tiles
-  const int64_t merges = by_tile ? 16 * units * 2 * tiles : cdiv(units * pp.rows, 4);
-  if (U * (pp.Sc + pp.St) > 0x7FFFFFFFll || merges > 0x7FFFFFFFll) return TQ_ERR_UNSUPPORTED;
+  const int64_t merges = by_tile ? 16 * units * 2 * tiles : units * pp.rows;
+  if (merges > 0x7FFFFFFFll) return TQ_ERR_UNSUPPORTED;
   pp.out = (uint16_t*)a->out;
   pp.o_ls = a->out_layer_stride;
   pp.o_bs = a->out_batch_stride;
@@ -314,17 +361,17 @@ tq_status tq_sparse_attn(const tq_query_args* a, const tq_record_lists* lists, c
   cudaError_t e;
   if (pl.few) {
     e = launch_few(pp, s);
-    if (e != cudaSuccess) return TQ_ERR_CUDA;
-    return launch_prefill_merge_rows(pp, s) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
-  }
-  switch (pp.q.D) {
-    case 64: e = launch_prefill_listed_d64(pp, s); break;
-    case 128: e = launch_prefill_listed_d128(pp, s); break;
-    case 256: e = launch_prefill_listed_d256(pp, s); break;
-    default: e = launch_prefill_listed_d512(pp, s); break;
+  } else {
+    switch (pp.q.D) {
+      case 64: e = launch_prefill_listed_d64(pp, s); break;
+      case 128: e = launch_prefill_listed_d128(pp, s); break;
+      case 256: e = launch_prefill_listed_d256(pp, s); break;
+      default: e = launch_prefill_listed_d512(pp, s); break;
+    }
   }
   if (e != cudaSuccess) return TQ_ERR_CUDA;
-  return launch_prefill_merge(pp, s) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+  e = pl.few || pp.q.D > 128 ? launch_merge_rows(pp, s) : launch_prefill_merge(pp, s);
+  return e == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
 }
 
 }  // extern "C"

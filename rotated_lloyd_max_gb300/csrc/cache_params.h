@@ -106,6 +106,7 @@ struct BoundsParams {
   const int32_t* n_chunks;
   const int32_t* first;
   int max_chunks, max_new;
+  FastDiv by_new, by_heads, by_batch;  // divisions by max_new, Hkv, B
   uint16_t* bounds;
   int64_t bounds_ls;
 };

@@ -12,8 +12,8 @@
 // bank conflicts); sums are f32.  At head dim 512 a warp forms half of the outputs
 // (the top k-step bit's sum or difference by the sign of A).
 //
-// A warp takes a record, or, where there are fewer records than warps on the GPU,
-// the four warps of a CTA share one.
+// A warp takes a record at a time as long as there is one for every warp; those
+// that are left (or all of a short call) are shared by the four warps of a CTA.
 //
 // Codecs with side lists go through f32 butterflies on the CUDA cores, a vector
 // spread over d / 32 lanes as in the decoder, which replaces single coordinates easily.
@@ -76,9 +76,10 @@ struct BoundsCfg {
   static constexpr int SMEM = TAB + 4 * 4 * D;      // and the warps' bounds, bf16 [2][D]
 };
 
-// W: warps that share a record
-template <int D, int B, int W>
-__global__ void __launch_bounds__(kThreads, D <= 128 ? 4 : 3) key_bounds_mma_kernel(const __grid_constant__ BoundsParams p, int64_t tasks) {
+// tasks: records, or at head dim 512 halves of their outputs; the first `solo` of them a warp each
+template <int D, int B>
+__global__ void __launch_bounds__(kThreads, D <= 128 ? 4 : 3)
+    key_bounds_mma_kernel(const __grid_constant__ BoundsParams p, uint32_t tasks, uint32_t solo) {
   constexpr int KK = D / 16, RUN = D / 4, STEP = RUN < 32 ? RUN : 32, NS = RUN / STEP, NB = STEP * B;
   constexpr int HALVES = D == 512 ? 2 : 1, ACC = KK / HALVES, ROW = D * B / 8;
   extern __shared__ __align__(128) unsigned char sm[];
@@ -102,17 +103,45 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 4 : 3) key_bounds_mma_ker
     const uint32_t s0 = __popc(t & (row >> 2)) + __popc(j & row & 3), s1 = __popc(t & (row >> 2)) + __popc((j + 1) & row & 3);
     h16[i] = 0x3C003C00u | (s0 & 1u) << 15 | (s1 & 1u) << 31;
   }
-  // a task: a record, or at head dim 512 half of one's outputs
-  const int64_t per = W == 1 ? 4 : 1;
-  for (int64_t q = blockIdx.x * per + (W == 1 ? warp : 0); q < tasks; q += gridDim.x * per) {
-    const int half = HALVES == 1 ? 0 : (int)(q & 1);
-    const int64_t unit = (HALVES == 1 ? q : q >> 1) / p.max_new;
-    const int h = (int)(unit % p.Hkv), lb = (int)(unit / p.Hkv), b = lb % p.B, l = lb / p.B;
-    const int n = min(max(__ldg(p.n_chunks + lb), 0), min(p.max_chunks, p.rec_limit));
-    const int64_t r = (int64_t)(p.first ? max(__ldg(p.first + lb), 0) : 0) + (HALVES == 1 ? q : q >> 1) % p.max_new;
-    if (r >= n) continue;
-    const uint8_t* rec = p.rec + l * p.rec_ls +
-                         rec_offset(p.table, p.table_stride, p.rec_cap, p.Hkv, b, h, (int)r, p.c.rec_bytes);
+  struct Task {
+    uint32_t q;
+    int64_t out;  // place of its bounds
+    const uint8_t* rec;
+  };
+  // the first task from k.q on that names a record; false where there is none before `end`
+  auto seek = [&](Task& k, uint32_t stride, uint32_t end) {
+    for (; k.q < end; k.q += stride) {
+      const uint32_t x = HALVES == 1 ? k.q : k.q >> 1, unit = fast_div(x, p.by_new), lb = fast_div(unit, p.by_heads);
+      const int h = (int)(unit - lb * p.Hkv), l = (int)fast_div(lb, p.by_batch), b = (int)lb - l * p.B;
+      const int n = min(max(__ldg(p.n_chunks + lb), 0), min(p.max_chunks, p.rec_limit));
+      const int64_t r = (int64_t)(p.first ? max(__ldg(p.first + lb), 0) : 0) + (x - unit * p.max_new);
+      if (r >= n) continue;
+      const int64_t at = rec_offset(p.table, p.table_stride, p.rec_cap, p.Hkv, b, h, (int)r, 1);
+      k.rec = p.rec + l * p.rec_ls + at * p.c.rec_bytes;
+      k.out = l * p.bounds_ls + at * 2 * D;
+      return true;
+    }
+    return false;
+  };
+#pragma unroll 1
+  for (int team = 0; team < 2; ++team) {  // warps alone, then four together
+  const uint32_t stride = team ? gridDim.x : 4 * gridDim.x, end = team ? tasks : solo;
+  const int tiles = team ? kChunk / 32 : kChunk / 8, first = team ? warp * tiles : 0;
+  Task cur, nxt;
+  cur.q = team ? solo + blockIdx.x : 4 * blockIdx.x + warp;
+  bool more = seek(cur, stride, end);
+  Run<NB> run;
+  float2 nn = f2(0.f, 0.f);
+  if (more) {
+    run.load(cur.rec + (8 * first + g) * ROW, t * RUN * B);
+    nn = __ldg(reinterpret_cast<const float2*>(cur.rec + p.c.off_norm) + 4 * first + t);
+  }
+  for (; more; cur = nxt) {
+    nxt.q = cur.q + stride;
+    nxt.rec = cur.rec;
+    more = seek(nxt, stride, end);
+    const int half = HALVES == 1 ? 0 : (int)(cur.q & 1);
+    const uint8_t* rec = cur.rec;
     uint32_t sign = 0u;  // of A for the k-steps of the upper half
     if (HALVES == 2 && half) sign = 0x80008000u;
     float lo[ACC][2], hi[ACC][2];
@@ -124,19 +153,15 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 4 : 3) key_bounds_mma_ker
         hi[k][e] = -INFINITY;
       }
     bool bad = false;
-    constexpr int TILES = kChunk / 8 / W;
-    const int first = W == 1 ? 0 : warp * TILES;
     const uint8_t* row = rec + (8 * first + g) * ROW;
-    Run<NB> run;
-    run.load(row, t * RUN * B);
-    float2 nn = __ldg(reinterpret_cast<const float2*>(rec + p.c.off_norm) + 4 * first + t);
 #pragma unroll 1
-    for (int i = 0; i < TILES; ++i) {
+    for (int i = 0; i < tiles; ++i) {
       float acc[ACC][4];
       const float2 f = f2(nn.x * p.c.inv_sqrt_d, nn.y * p.c.inv_sqrt_d);
       bad = bad || !(fabsf(nn.x) < INFINITY) || !(fabsf(nn.y) < INFINITY);
-      const uint8_t* next = i + 1 < TILES ? row + 8 * ROW : row;
-      if (i + 1 < TILES) nn = __ldg(reinterpret_cast<const float2*>(rec + p.c.off_norm) + 4 * (first + i + 1) + t);
+      const bool last = i + 1 == tiles;
+      const uint8_t* next = last ? nxt.rec + (8 * first + g) * ROW : row + 8 * ROW;
+      nn = __ldg(reinterpret_cast<const float2*>((last ? nxt.rec : rec) + p.c.off_norm) + 4 * (last ? first : first + i + 1) + t);
 #pragma unroll
       for (int s = 0; s < NS; ++s) {
         uint32_t w[Run<NB>::NW];
@@ -183,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 4 : 3) key_bounds_mma_ker
     // over the four lanes of a quad (tokens), of which lane t keeps k-steps = t modulo 4: half of them go over at
     // a time; then to the keys' signs and bf16
     bad = __any_sync(0xffffffffu, bad);
-    if (W > 1) __syncthreads();  // the bounds of the record before are written
+    if (team) __syncthreads();  // the bounds of the record before are written
     else __syncwarp();
 #pragma unroll
     for (int m = 1; m < 4; m <<= 1)
@@ -217,12 +242,11 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 4 : 3) key_bounds_mma_ker
         mine[D + c] = bound_bits<false>(y, bad);
       }
     }
-    uint16_t* out = p.bounds + l * p.bounds_ls +
-                    rec_offset(p.table, p.table_stride, p.rec_cap, p.Hkv, b, h, (int)r, 2 * D);
+    uint16_t* out = p.bounds + cur.out;
     // coordinates come in runs of 4 ACC at steps of RUN: 16-byte chunks
     constexpr int CH = 4 * ACC / 8;  // chunks of a run
     auto chunk = [&](int i) { return (i / CH) * (RUN / 8) + half * CH + i % CH; };
-    if constexpr (W == 1) {
+    if (!team) {
       __syncwarp();
       for (int i = lane; i < 8 * CH; i += 32) {
         const int c = chunk(i);
@@ -234,7 +258,7 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 4 : 3) key_bounds_mma_ker
         const int c = chunk(i);
         uint4 v = reinterpret_cast<const uint4*>(sm + BoundsCfg<D, B>::TAB)[c];
 #pragma unroll
-        for (int w = 1; w < W; ++w) {
+        for (int w = 1; w < 4; ++w) {
           const uint4 x = reinterpret_cast<const uint4*>(sm + BoundsCfg<D, B>::TAB)[w * (D / 4) + c];
           v = c < D / 8 ? make_uint4(join2<true>(v.x, x.x), join2<true>(v.y, x.y), join2<true>(v.z, x.z), join2<true>(v.w, x.w))
                         : make_uint4(join2<false>(v.x, x.x), join2<false>(v.y, x.y), join2<false>(v.z, x.z), join2<false>(v.w, x.w));
@@ -242,6 +266,8 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 4 : 3) key_bounds_mma_ker
         reinterpret_cast<uint4*>(out)[c] = v;
       }
     }
+  }
+  __syncthreads();
   }
 }
 
@@ -350,17 +376,6 @@ __global__ void __launch_bounds__(kThreads) key_bounds_kernel(const __grid_const
   }
 }
 
-template <int D, int B, int W>
-static cudaError_t bounds_launch_mma(const BoundsParams& p, int64_t records, cudaStream_t s) {
-  const int64_t tasks = records * (D == 512 ? 2 : 1), per = W == 1 ? 4 : 1;
-  auto kern = key_bounds_mma_kernel<D, B, W>;
-  constexpr int smem = BoundsCfg<D, B>::SMEM;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  const int64_t grid = min(cdiv(tasks, per), (int64_t)sm_count() * (D <= 128 ? 4 : 3));
-  kern<<<(unsigned)grid, kThreads, smem, s>>>(p, tasks);
-  return cudaGetLastError();
-}
 template <int D, int B>
 static cudaError_t bounds_launch(const BoundsParams& p, cudaStream_t s) {
   const int64_t records = (int64_t)p.L * p.B * p.Hkv * p.max_new;
@@ -368,8 +383,13 @@ static cudaError_t bounds_launch(const BoundsParams& p, cudaStream_t s) {
     key_bounds_kernel<D, B><<<(unsigned)records, kThreads, 0, s>>>(p);
     return cudaGetLastError();
   }
-  if (records <= 12 * (int64_t)sm_count()) return bounds_launch_mma<D, B, 4>(p, records, s);
-  return bounds_launch_mma<D, B, 1>(p, records, s);
+  auto kern = key_bounds_mma_kernel<D, B>;
+  constexpr int smem = BoundsCfg<D, B>::SMEM;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  const int64_t tasks = records * (D == 512 ? 2 : 1), grid = min(tasks, (int64_t)sm_count() * (D <= 128 ? 4 : 3));
+  kern<<<(unsigned)grid, kThreads, smem, s>>>(p, (uint32_t)tasks, (uint32_t)(tasks / (4 * grid) * (4 * grid)));
+  return cudaGetLastError();
 }
 
 cudaError_t launch_key_bounds(const BoundsParams& p, cudaStream_t s) {

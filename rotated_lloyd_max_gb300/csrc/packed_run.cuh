@@ -5,11 +5,12 @@
 
 namespace tq {
 
-// NB bits of a packed row from bit `off` on, loaded now and aligned when used
+// NB bits of a packed row from bit `off` on, a multiple of NB, loaded now and aligned when used
 template <int NB>
 struct Run {
   static constexpr bool AL = NB % 32 == 0;
-  static constexpr int NW = (NB + 31) / 32, RAW = AL ? NW : NW + 1;
+  static constexpr int STEP = NB % 16 ? 8 : 16;  // what an unaligned run's offset is a multiple of
+  static constexpr int NW = (NB + 31) / 32, RAW = AL ? NW : (32 - STEP + NB + 31) / 32;
   uint32_t r[RAW];
   __device__ __forceinline__ void load(const uint8_t* row, int off) {
     const uint32_t* p = reinterpret_cast<const uint32_t*>(row) + (off >> 5);
@@ -26,7 +27,7 @@ struct Run {
   }
   __device__ __forceinline__ void get(int off, uint32_t (&w)[NW]) const {
 #pragma unroll
-    for (int i = 0; i < NW; ++i) w[i] = AL ? r[i] : __funnelshift_r(r[i], r[i + (AL ? 0 : 1)], off & 31);
+    for (int i = 0; i < NW; ++i) w[i] = AL ? r[i] : __funnelshift_r(r[i], i + 1 < RAW ? r[i + 1 < RAW ? i + 1 : i] : 0u, off & 31);
   }
 };
 

@@ -219,11 +219,108 @@ cudaError_t launch_prefill_merge(const PrefillParams& pp, cudaStream_t s) {
   }
 }
 
-// partials of a row each, as the kernel for few rows leaves them
-cudaError_t launch_prefill_merge_rows(const PrefillParams& pp, cudaStream_t s) {
-  const unsigned grid = (unsigned)cdiv((int64_t)pp.q.L * pp.q.B * pp.q.Hkv * pp.rows, 4);
-  if (pp.q.D == 64) return launch_after(prefill_merge_kernel<64>, dim3(grid), kThreads, 0, s, 1, pp);
-  return launch_after(prefill_merge_kernel<128>, dim3(grid), kThreads, 0, s, 1, pp);
+// Merge of partials of a row each by a CTA of W warps a row, which share the
+// splits: few rows with many splits (a decode step of one sequence: 12 rows, 10
+// splits) would otherwise wait for one load after another.
+template <int D, int W>
+__global__ void __launch_bounds__(32 * W) merge_shared_kernel(const __grid_constant__ PrefillParams pp) {
+  constexpr int E = D / 32;
+  __shared__ float part[W > 1 ? W - 1 : 1][2][D];
+  __shared__ float wsum[W];
+  pdl_wait();
+  const QueryParams& p = pp.q;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t wrow = blockIdx.x;
+  const int64_t unit = wrow / pp.rows;
+  const int row = (int)(wrow % pp.rows), tok = row / p.G;
+  const int h = (int)(unit % p.Hkv), lb = (int)(unit / p.Hkv), b = lb % p.B, l = lb / p.B;
+  const int tb = query_len(p, b);
+  if (tok >= tb) return;
+  const int S = pp.Sc + pp.St;
+  const float2* ml = pp.ws_ml + wrow * S;
+  const float* acc = pp.ws_acc + wrow * S * D + lane * E;
+  float M = -INFINITY;
+  for (int s = lane; s < S; s += 32) M = fmaxf(M, ml[s].y > 0.f ? ml[s].x : -INFINITY);
+  M = warp_max(M);
+  float c[E], d[E], sum = 0.f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) c[e] = d[e] = 0.f;
+#pragma unroll 2
+  for (int s = warp; s < S; s += W) {
+    const float2 v = ml[s];
+    if (v.y != v.y) sum = v.y;  // no softmax in a split: the row comes out NaN
+    if (!(v.y > 0.f)) continue;
+    const float w = exp2f(v.x - M);
+    sum = fmaf(w, v.y, sum);
+    const float* a = acc + (int64_t)s * D;
+#pragma unroll
+    for (int e = 0; e < E; e += 2) {
+      const float2 x = *reinterpret_cast<const float2*>(a + e);
+      if (s < pp.Sc) {
+        c[e] = fmaf(w, x.x, c[e]);
+        c[e + 1] = fmaf(w, x.y, c[e + 1]);
+      } else {
+        d[e] = fmaf(w, x.x, d[e]);
+        d[e + 1] = fmaf(w, x.y, d[e + 1]);
+      }
+    }
+  }
+  if constexpr (W > 1) {
+    if (warp > 0) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        part[warp - 1][0][e * 32 + lane] = c[e];
+        part[warp - 1][1][e * 32 + lane] = d[e];
+      }
+      if (lane == 0) wsum[warp] = sum;
+    }
+    __syncthreads();
+    if (warp > 0) return;
+#pragma unroll
+    for (int w = 1; w < W; ++w) {
+      sum += wsum[w];
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        c[e] += part[w - 1][0][e * 32 + lane];
+        d[e] += part[w - 1][1][e * 32 + lane];
+      }
+    }
+  }
+  if (pp.Sc > 0) {
+    fwht_regs<E>(c);
+    fwht_lanes<E>(c, lane, 32);
+  }
+  const float iw = inverse_weight(pp, lb, h, tb, row, sum);
+  uint16_t* out = pp.out + l * pp.o_ls + b * pp.o_bs + (int64_t)tok * pp.o_ts + (int64_t)(h * p.G + row % p.G) * D + lane * E;
+#pragma unroll
+  for (int e = 0; e < E; e += 2) {
+    const int j = lane * E + e;
+    const uint32_t sg = p.vc.signs[j >> 5] >> (j & 31);
+    const float x = c[e] * ((sg & 1u) ? -pp.inv_sqrt_d : pp.inv_sqrt_d) + d[e];
+    const float y = c[e + 1] * ((sg & 2u) ? -pp.inv_sqrt_d : pp.inv_sqrt_d) + d[e + 1];
+    *reinterpret_cast<uint32_t*>(out + e) = pack2_bf16(x * iw, y * iw);
+  }
+}
+
+template <int D>
+static cudaError_t merge_rows_launch(const PrefillParams& pp, int64_t rows, cudaStream_t s) {
+  // a warp for every two splits, up to eight
+  const int S = pp.Sc + pp.St;
+  if (S <= 2) return launch_after(merge_shared_kernel<D, 1>, dim3((unsigned)rows), 32, 0, s, 1, pp);
+  if (S <= 4) return launch_after(merge_shared_kernel<D, 2>, dim3((unsigned)rows), 64, 0, s, 1, pp);
+  return launch_after(merge_shared_kernel<D, 8>, dim3((unsigned)rows), 256, 0, s, 1, pp);
+}
+
+// of listed records: the kernel's for few rows, and the wide kernel's
+cudaError_t launch_merge_rows(const PrefillParams& pp, cudaStream_t s) {
+  const int64_t rows = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv * pp.rows;
+  switch (pp.q.D) {
+    case 64: return merge_rows_launch<64>(pp, rows, s);
+    case 128: return merge_rows_launch<128>(pp, rows, s);
+    case 256: return merge_rows_launch<256>(pp, rows, s);
+    case 512: return merge_rows_launch<512>(pp, rows, s);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace tq

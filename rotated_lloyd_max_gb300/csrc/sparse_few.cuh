@@ -2,14 +2,17 @@
 // (query heads of a kv head x tokens of a block), head dims 64 and 128, codecs
 // without side lists: the decode step of a long cache.
 //
-// Eight warps a CTA; four share a record (32 tokens each), the two groups take
-// every other one of the split's list.  Tokens are the M dimension of the scores
+// One wave of CTAs: the lists' entries, one list after the other, are cut into equal
+// runs, a run a CTA, and so are the rings' tiles for the CTAs behind, so that a CTA
+// works on the ends of two lists and the lists between; what it has of each is a
+// partial for the merge.  Eight warps a CTA; four share a record (32 tokens each),
+// the two groups take every other one of a run.  Tokens are the M dimension of the scores
 // (K q~^T, rows as N), coordinates that of the outputs (V^T p), so that 8 rows
 // fill the N of mma.sync and both operands A are decoded from the packed codes
 // straight into registers: a lane holds d / 4 neighbouring codes of four keys, and
-// d / 8 codes of eight values, whose nibbles are paired by token before the lookup.
-// Every pair of codes is one lookup in a table with a copy per lane (no bank
-// conflicts).  The words of the next record are loaded as soon as this one's are
+// d / 8 codes of eight values, whose codes are paired by token before the lookup
+// (3-bit ones after it).  Every pair of codes is one lookup in a table with a copy
+// per lane (no bank conflicts).  The words of the next record are loaded as soon as this one's are
 // used; warps share nothing until the end, so that no barrier holds up the loads.
 //
 // Centroids and rotated queries are f16 (11 bits), logits take the key's scale and
@@ -25,17 +28,16 @@
 namespace tq {
 
 constexpr int kFewThreads = 256;
-constexpr int kFewIds = 256;  // records of a split at most
+constexpr int kFewIds = 256;  // records that are listed at a time
 
 template <int D, int KB, int VB, int NT>
 struct FewCfg {
-  static constexpr int KTAB = (1 << (2 * KB)) * 128, VTAB = VIdx<VB>::ENTRIES * 128;
+  static constexpr int KTAB = (1 << (2 * KB)) * 128, VTAB = (1 << (2 * VB)) * 128;
   static constexpr int QF = KTAB + VTAB, QFB = D / 16 * NT * 32 * 8;
   static constexpr int IDS = QF + QFB, MISC = IDS + kFewIds * 4;
-  static constexpr int MISCB = 8 * NT * 8 + 64;
-  static constexpr int RED = 8 * 8 * (D + D / 8) * 4;  // the warps' outputs of eight rows
-  static constexpr int ML = (RED > MISC + MISCB ? RED : MISC + MISCB);
-  static constexpr int SMEM = ML + 8 * 8 * NT * 8;
+  static constexpr int MISCB = 8 * NT * 8 + 64, ML = MISC + MISCB;
+  static constexpr int RED = ML + 8 * 8 * NT * 8;           // the warps' outputs of eight rows
+  static constexpr int SMEM = RED + 8 * 8 * (D + D / 8) * 4;
 };
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -67,53 +69,47 @@ struct FewState {
         for (int e = 0; e < 4; ++e) acc[nt][mc][e] = 0.f;
     }
   }
-  // x[mi][nt][2 half + e]: logits (log2 units) of token 16 mi + 8 half + g; becomes weights
-  // against the running maxima.  grow: factor of the outputs that the scales ask for.
-  __device__ __forceinline__ void weigh(float (&x)[2][NT][4], float grow) {
-    bool moved = grow != 1.f;
-    float mn[NT][2];
+  // x[mi][nt][2 half + e]: logits (log2 units) of token 16 mi + 8 half + g.  New maxima where a row's logits pass
+  // the old one by more than 1 (weights of up to 2 spare a rescaling); grow: what the values' scales ask of the outputs.
+  template <int MI>
+  __device__ __forceinline__ void raise(const float (&x)[MI][NT][4], float grow) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt) {
+      float f[2];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        float v = fmaxf(fmaxf(x[0][nt][e], x[0][nt][2 + e]), fmaxf(x[1][nt][e], x[1][nt][2 + e]));
+        float v = fmaxf(x[0][nt][e], x[0][nt][2 + e]);
+#pragma unroll
+        for (int mi = 1; mi < MI; ++mi) v = fmaxf(v, fmaxf(x[mi][nt][e], x[mi][nt][2 + e]));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-        mn[nt][e] = v > m[nt][e] + 1.f ? v : m[nt][e];  // weights of up to 2 spare a rescaling
-        moved = moved || mn[nt][e] != m[nt][e];
+        const bool up = v > m[nt][e] + 1.f;
+        f[e] = up ? ex2(m[nt][e] - v) : 1.f;
+        if (up) m[nt][e] = v;
+        l[nt][e] *= f[e];
+        f[e] *= grow;
       }
-    if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float f[2];
+      for (int mc = 0; mc < D / 16; ++mc)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          f[e] = mn[nt][e] != m[nt][e] ? ex2(m[nt][e] - mn[nt][e]) : 1.f;
-          l[nt][e] *= f[e];
-          m[nt][e] = mn[nt][e];
-          f[e] *= grow;
-        }
-#pragma unroll
-        for (int mc = 0; mc < D / 16; ++mc)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[nt][mc][e] *= f[e & 1];
-      }
+        for (int e = 0; e < 4; ++e) acc[nt][mc][e] *= f[e & 1];
     }
+  }
+  __device__ __forceinline__ float ref(int nt, int e) const { return m[nt][e] > -INFINITY ? m[nt][e] : 0.f; }
+  // logits less their rows' references become weights
+  template <int MI>
+  __device__ __forceinline__ void weigh(float (&x)[MI][NT][4]) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float ref = m[nt][e] > -INFINITY ? m[nt][e] : 0.f;
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
-        for (int mi = 0; mi < 2; ++mi)
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const float w = ex2(x[mi][nt][2 * half + e] - ref);
-            x[mi][nt][2 * half + e] = w;
-            l[nt][e] += w;
-          }
-      }
+        for (int mi = 0; mi < MI; ++mi) {
+          x[mi][nt][e] = ex2(x[mi][nt][e]);
+          x[mi][nt][2 + e] = ex2(x[mi][nt][2 + e]);
+          l[nt][e] += x[mi][nt][e] + x[mi][nt][2 + e];
+        }
   }
 };
 
@@ -123,8 +119,7 @@ __device__ __forceinline__ void few_records(const PrefillParams& pp, unsigned ch
                                             int h, const float* qf, const int* lim, int low, FewState<D, NT>& st) {
   using C = FewCfg<D, KB, VB, NT>;
   constexpr int KS = D / 16, KR = D / 4, VR = D / 8, KNB = KR * KB, VNB = VR * VB;
-  constexpr int FW = VIdx<VB>::FW, KROW = D * KB / 8, VROW = D * VB / 8;
-  constexpr int VNW = Run<VNB>::NW, ZW = VB == 3 ? 2 * VNW : VNW;
+  constexpr int KROW = D * KB / 8, VROW = D * VB / 8, VNW = Run<VNB>::NW;
   const QueryParams& p = pp.q;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int w4 = warp & 3;
@@ -137,30 +132,52 @@ __device__ __forceinline__ void few_records(const PrefillParams& pp, unsigned ch
   Run<KNB> kr[4];
   Run<VNB> vr[8];
   float nk[4], nv[4], nk1[4], nv1[4];
+  // contiguous records follow one another behind a base; pages are looked up
+  const uint8_t* kbase = kl + (p.table ? (int64_t)h : ((int64_t)b * p.Hkv + h) * p.rec_cap) * p.kc.rec_bytes;
+  const uint8_t* vbase = vl + (p.table ? (int64_t)h : ((int64_t)b * p.Hkv + h) * p.rec_cap) * p.vc.rec_bytes;
+  const int32_t* table = p.table ? p.table + (int64_t)b * p.table_stride : nullptr;
+  const int kat = (32 * w4 + g) * KROW, vat = (32 * w4 + 2 * t) * VROW;
+  const int knorm = p.kc.off_norm + 4 * (32 * w4 + g), vnorm = p.vc.off_norm + 4 * (32 * w4 + g);
+  const int kstep = (table ? p.Hkv : 1) * p.kc.rec_bytes, vstep = (table ? p.Hkv : 1) * p.vc.rec_bytes;
+  auto index = [&](int i) {  // the i-th record's place behind a base
+    const int c = ids[i];
+    return table ? min(max(__ldg(table + c), 0), p.rec_cap - 1) : c;
+  };
   auto load_keys = [&](int c) {
-    const uint8_t* rec = kl + rec_offset(p.table, p.table_stride, p.rec_cap, p.Hkv, b, h, c, p.kc.rec_bytes);
+    const uint8_t* rec = kbase + (int64_t)c * kstep;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      kr[i].load(rec + (32 * w4 + 8 * i + g) * KROW, KNB * t);
-      nk1[i] = __ldg(reinterpret_cast<const float*>(rec + p.kc.off_norm) + 32 * w4 + 8 * i + g);
+      kr[i].load(rec + kat + 8 * i * KROW, KNB * t);
+      nk1[i] = __ldg(reinterpret_cast<const float*>(rec + knorm) + 8 * i);
     }
   };
   auto load_values = [&](int c) {
-    const uint8_t* rec = vl + rec_offset(p.table, p.table_stride, p.rec_cap, p.Hkv, b, h, c, p.vc.rec_bytes);
+    const uint8_t* rec = vbase + (int64_t)c * vstep;
 #pragma unroll
     for (int i = 0; i < 8; ++i)  // tokens 16 (i / 4) + 2 t + {0, 1, 8, 9}
-      vr[i].load(rec + (32 * w4 + 16 * (i >> 2) + 2 * t + (i & 1) + 8 * ((i >> 1) & 1)) * VROW, VNB * g);
+      vr[i].load(rec + vat + (16 * (i >> 2) + (i & 1) + 8 * ((i >> 1) & 1)) * VROW, VNB * g);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      nv1[i] = __ldg(reinterpret_cast<const float*>(rec + p.vc.off_norm) + 32 * w4 + 8 * i + g);
+    for (int i = 0; i < 4; ++i) nv1[i] = __ldg(reinterpret_cast<const float*>(rec + vnorm) + 8 * i);
   };
+  const bool capped = p.scap > 0.f;
+  float f[NT][2], rf[NT][2];  // logit factors and references of the lane's rows
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      f[nt][e] = qf[8 * nt + 2 * t + e];
+      rf[nt][e] = 0.f;
+    }
+  bool none = true;  // a row has no reference yet
+  float reach = 0.f, up = 0.f;  // scales that the exponent of the values' covers; 2^14 2^-(ev + 1)
   int i = warp >> 2;
   if (i >= n) return;
-  load_keys(ids[i]);
-  load_values(ids[i]);
+  int at = index(i);
+  load_keys(at);
+  load_values(at);
 #pragma unroll 1
   for (; i < n; i += 2) {
-    const int c = ids[i], next = i + 2 < n ? ids[i + 2] : c;
+    const int next = i + 2 < n ? index(i + 2) : at;
     // ---------------------------------------------------------------- scores
     float x[2][NT][4];
 #pragma unroll
@@ -183,10 +200,10 @@ __device__ __forceinline__ void few_records(const PrefillParams& pp, unsigned ch
         for (int k = 0; k < 4; ++k)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const int at = 4 * kk + 2 * e;
+            const int o = 4 * kk + 2 * e;
             uint32_t v;
-            if constexpr (KB == 4) v = byte_lookup(kbt, w[k][at / 8], at % 8 / 2);
-            else v = *reinterpret_cast<const uint32_t*>(ktab + pair_off(w[k], at * KB, 2 * KB, loff));
+            if constexpr (KB == 4) v = byte_lookup(kbt, w[k][o / 8], o % 8 / 2);
+            else v = *reinterpret_cast<const uint32_t*>(ktab + pair_off(w[k], o * KB, 2 * KB, loff));
             a[k >> 1][(k & 1) + 2 * e] = v;
           }
 #pragma unroll
@@ -199,36 +216,57 @@ __device__ __forceinline__ void few_records(const PrefillParams& pp, unsigned ch
     }
     load_keys(next);
     // ---------------------------------------------------------------- weights
-    const bool edge = (c + 1) * kChunk > low;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float f = qf[8 * nt + 2 * t + e];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float& v = x[k >> 1][nt][2 * (k & 1) + e];
-          v *= nk[k] * f;
-          if (p.scap > 0.f) v = soft_cap(v, p.scap, p.iscap);
-          if (edge) v = c * kChunk + 32 * w4 + 8 * k + g < lim[8 * nt + 2 * t + e] ? v : -INFINITY;
-        }
-      }
-    // the values' scales against the largest so far
-    uint32_t nb = 0u;
+    // against the references as they stand, unless a row has none, a logit passes its by more than 1, a value's
+    // scale the exponent, a row does not see a token, or logits are capped
+    const int token = ids[i] * kChunk + 32 * w4 + g;  // of k = 0
+    const bool edge = (ids[i] + 1) * kChunk > low;
+    float over = -INFINITY, big = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       nv[k] = nv1[k];
-      const uint32_t u = __float_as_uint(nv[k]) & 0x7FFFFFFFu;
-      nb = max(nb, u < 0x7F800000u ? u : 0u);
+      big = fmaxf(big, fabsf(nv[k]));
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float& v = x[k >> 1][nt][2 * (k & 1) + e];
+          v = fmaf(v, nk[k] * f[nt][e], -rf[nt][e]);
+          over = fmaxf(over, v);
+        }
     }
-    const int en = exp_of(__uint_as_float(__reduce_max_sync(0xffffffffu, nb)));
-    float grow = 1.f;
-    if (en > st.ev) {
-      grow = pow2i(st.ev - en);
-      st.ev = en;
+    if (__any_sync(0xffffffffu, over > 1.f || big >= reach || edge || none)) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            float& v = x[k >> 1][nt][2 * (k & 1) + e];
+            v += rf[nt][e];
+            if (capped) v = soft_cap(v, p.scap, p.iscap);
+            if (edge) v = token + 8 * k < lim[8 * nt + 2 * t + e] ? v : -INFINITY;
+          }
+      const int en = exp_of(__uint_as_float(__reduce_max_sync(0xffffffffu, big < INFINITY ? __float_as_uint(big) : 0u)));
+      float grow = 1.f;
+      if (en > st.ev) {
+        grow = pow2i(st.ev - en);
+        st.ev = en;
+      }
+      reach = pow2i(st.ev + 1);
+      up = pow2i(13 - st.ev);
+      st.raise(x, grow);
+      none = capped;  // capped logits take this way always
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          none = none || st.m[nt][e] == -INFINITY;
+          rf[nt][e] = capped ? 0.f : st.ref(nt, e);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) x[k >> 1][nt][2 * (k & 1) + e] -= st.ref(nt, e);
+        }
     }
-    st.weigh(x, grow);
-    const float up = pow2i(13 - st.ev);  // 2^14 2^-(ev + 1)
+    st.weigh(x);
 #pragma unroll
     for (int k = 0; k < 4; ++k) nv[k] *= up;
     // ---------------------------------------------------------------- values
@@ -240,31 +278,52 @@ __device__ __forceinline__ void few_records(const PrefillParams& pp, unsigned ch
         b0[nt] = transpose8(pack2_f16(x[mt][nt][0] * nv[2 * mt], x[mt][nt][1] * nv[2 * mt]));
         b1[nt] = transpose8(pack2_f16(x[mt][nt][2] * nv[2 * mt + 1], x[mt][nt][3] * nv[2 * mt + 1]));
       }
-      uint32_t z[4][ZW];  // even and odd coordinates of tokens 2 t, 2 t + 1; of 2 t + 8, 2 t + 9
+      if constexpr (VB == 3) {
+        // a field of two 3-bit codes would have to be put together for two tokens: cheaper to look up each
+        // token's pairs of neighbours and to pair the results (8 instructions for two operands; 12)
+        uint32_t r[4][VNW];
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t r0[VNW], r1[VNW];
-        vr[4 * mt + 2 * k].get(VNB * g, r0);
-        vr[4 * mt + 2 * k + 1].get(VNB * g, r1);
-        v_pair_words<VB, VNW>(r0, r1, z[2 * k], z[2 * k + 1]);
-      }
+        for (int k = 0; k < 4; ++k) vr[4 * mt + k].get(VNB * g, r[k]);
 #pragma unroll
-      for (int mc = 0; mc < KS; ++mc) {
-        uint32_t a[4];
+        for (int mc = 0; mc < KS; ++mc) {
+          uint32_t y[4], a[4];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if constexpr (2 * FW == 8) a[k] = byte_lookup(vbt, z[k][mc / 4], mc % 4);
-          else a[k] = *reinterpret_cast<const uint32_t*>(vtab + pair_off(z[k], mc * 2 * FW, 2 * FW, loff));
+          for (int k = 0; k < 4; ++k) y[k] = *reinterpret_cast<const uint32_t*>(vtab + pair_off(r[k], mc * 6, 6, loff));
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            a[2 * k] = __byte_perm(y[2 * k], y[2 * k + 1], 0x5410);
+            a[2 * k + 1] = __byte_perm(y[2 * k], y[2 * k + 1], 0x7632);
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_f16(st.acc[nt][mc], a, b0[nt], b1[nt]);
+        }
+      } else {
+        uint32_t z[4][VNW];  // even and odd coordinates of tokens 2 t, 2 t + 1; of 2 t + 8, 2 t + 9
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          uint32_t r0[VNW], r1[VNW];
+          vr[4 * mt + 2 * k].get(VNB * g, r0);
+          vr[4 * mt + 2 * k + 1].get(VNB * g, r1);
+          v_pair_words<VB, VNW>(r0, r1, z[2 * k], z[2 * k + 1]);
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16(st.acc[nt][mc], a, b0[nt], b1[nt]);
+        for (int mc = 0; mc < KS; ++mc) {
+          uint32_t a[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if constexpr (VB == 4) a[k] = byte_lookup(vbt, z[k][mc / 4], mc % 4);
+            else a[k] = *reinterpret_cast<const uint32_t*>(vtab + pair_off(z[k], mc * 2 * VB, 2 * VB, loff));
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_f16(st.acc[nt][mc], a, b0[nt], b1[nt]);
+        }
       }
     }
     load_values(next);
   }
 }
 
-// The ring's tokens [k0, k1) of a split.
+// The ring's tokens [k0, k1) of a split: a warp takes 16 at a time, whose keys and values are asked for together.
 template <int D, int NT>
 __device__ __forceinline__ void few_ring(const PrefillParams& pp, const uint2* qfrag, int k0, int k1, int len, int l, int b,
                                          int h, int start, const float* qf, const int* lim, int low, FewState<D, NT>& st) {
@@ -280,125 +339,120 @@ __device__ __forceinline__ void few_ring(const PrefillParams& pp, const uint2* q
     return (int64_t)s * D;
   };
 #pragma unroll 1
-  for (int a0 = k0 + 32 * warp; a0 < k1; a0 += kFewThreads) {
-    float x[2][NT][4];
+  for (int a0 = k0 + 16 * warp; a0 < k1; a0 += 16 * (kFewThreads / 32)) {
+    uint4 kw[2][KS / 2], vw[4][VR / 8];
 #pragma unroll
-    for (int mi = 0; mi < 2; ++mi)
+    for (int i = 0; i < 2; ++i) {
+      const uint4* r = reinterpret_cast<const uint4*>(kt + row(a0 + 8 * i + g) + KR * t);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int k = 0; k < KS / 2; ++k) kw[i][k] = __ldg(r + k);
+    }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[mi][nt][e] = 0.f;
-    const uint16_t* rows[4];
+    for (int k = 0; k < 4; ++k) {  // tokens 2 t + {0, 1, 8, 9}
+      const uint4* r = reinterpret_cast<const uint4*>(vt + row(a0 + 2 * t + (k & 1) + 8 * (k >> 1)) + VR * g);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) rows[i] = kt + row(a0 + 8 * i + g) + KR * t;
-#pragma unroll 2
-    for (int kk = 0; kk < KS; kk += 2) {
-      uint4 w[4];
+      for (int j = 0; j < VR / 8; ++j) vw[k][j] = __ldg(r + j);
+    }
+    float x[1][NT][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[i] = __ldg(reinterpret_cast<const uint4*>(rows[i] + 4 * kk));
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        uint32_t a[2][4];
+      for (int e = 0; e < 4; ++e) x[0][nt][e] = 0.f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[i >> 1][i & 1] = k ? w[i].z : w[i].x;
-          a[i >> 1][(i & 1) + 2] = k ? w[i].w : w[i].y;
-        }
+    for (int k = 0; k < KS / 2; ++k) {
+      const uint32_t a[2][4] = {{kw[0][k].x, kw[1][k].x, kw[0][k].y, kw[1][k].y}, {kw[0][k].z, kw[1][k].z, kw[0][k].w, kw[1][k].w}};
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const uint2 q = qfrag[((kk + k) * NT + nt) * 32 + lane];
-          mma_bf16(x[0][nt], a[0], q.x, q.y);
-          mma_bf16(x[1][nt], a[1], q.x, q.y);
+          const uint2 q = qfrag[((2 * k + j) * NT + nt) * 32 + lane];
+          mma_bf16(x[0][nt], a[j], q.x, q.y);
         }
-      }
     }
-    const bool edge = a0 + 32 > low;
+    const bool edge = a0 + 16 > low;
+    float over = -INFINITY;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const float f = qf[8 * nt + 2 * t + e];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          float& v = x[k >> 1][nt][2 * (k & 1) + e];
+        for (int k = 0; k < 2; ++k) {
+          float& v = x[0][nt][2 * k + e];
           v *= f;
           if (p.scap > 0.f) v = soft_cap(v, p.scap, p.iscap);
           if (edge) v = a0 + 8 * k + g < lim[8 * nt + 2 * t + e] ? v : -INFINITY;
+          over = fmaxf(over, v - st.m[nt][e]);
         }
       }
-    st.weigh(x, 1.f);
-#pragma unroll 1
-    for (int mt = 0; mt < 2; ++mt) {
-      uint32_t bh[2][NT], bl[2][NT];
+    if (__any_sync(0xffffffffu, over > 1.f)) st.raise(x, 1.f);
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 2; ++k) {
-          const float u = mt ? x[1][nt][2 * k] : x[0][nt][2 * k], v = mt ? x[1][nt][2 * k + 1] : x[0][nt][2 * k + 1];
-          const uint32_t hi = pack2_bf16(u, v);
-          bh[k][nt] = transpose8(hi);
-          bl[k][nt] = transpose8(pack2_bf16(u - bf16_lo(hi), v - bf16_hi(hi)));
-        }
-      const uint16_t* vrow[4];
+      for (int e = 0; e < 2; ++e)
 #pragma unroll
-      for (int k = 0; k < 4; ++k) vrow[k] = vt + row(a0 + 16 * mt + 2 * t + (k & 1) + 8 * (k >> 1)) + VR * g;
+        for (int k = 0; k < 2; ++k) x[0][nt][2 * k + e] -= st.ref(nt, e);
+    st.weigh(x);
+    uint32_t bh[2][NT], bl[2][NT];
 #pragma unroll
-      for (int mc = 0; mc < KS; mc += 4) {
-        uint4 w[4];
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) w[k] = __ldg(reinterpret_cast<const uint4*>(vrow[k] + 2 * mc));
+      for (int k = 0; k < 2; ++k) {
+        const float u = x[0][nt][2 * k], v = x[0][nt][2 * k + 1];
+        const uint32_t hi = pack2_bf16(u, v);
+        bh[k][nt] = transpose8(hi);
+        bl[k][nt] = transpose8(pack2_bf16(u - bf16_lo(hi), v - bf16_hi(hi)));
+      }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          auto at = [&](int k) { return j == 0 ? w[k].x : j == 1 ? w[k].y : j == 2 ? w[k].z : w[k].w; };
-          const uint32_t a[4] = {__byte_perm(at(0), at(1), 0x5410), __byte_perm(at(0), at(1), 0x7632),
-                                 __byte_perm(at(2), at(3), 0x5410), __byte_perm(at(2), at(3), 0x7632)};
+    for (int mc = 0; mc < KS; ++mc) {
+      auto at = [&](int k) { return mc % 4 == 0 ? vw[k][mc / 4].x : mc % 4 == 1 ? vw[k][mc / 4].y : mc % 4 == 2 ? vw[k][mc / 4].z : vw[k][mc / 4].w; };
+      const uint32_t a[4] = {__byte_perm(at(0), at(1), 0x5410), __byte_perm(at(0), at(1), 0x7632),
+                             __byte_perm(at(2), at(3), 0x5410), __byte_perm(at(2), at(3), 0x7632)};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            mma_bf16(st.acc[nt][mc + j], a, bh[0][nt], bh[1][nt]);
-            mma_bf16(st.acc[nt][mc + j], a, bl[0][nt], bl[1][nt]);
-          }
-        }
+      for (int nt = 0; nt < NT; ++nt) {
+        mma_bf16(st.acc[nt][mc], a, bh[0][nt], bh[1][nt]);
+        mma_bf16(st.acc[nt][mc], a, bl[0][nt], bl[1][nt]);
       }
     }
   }
 }
 
+// One list's part of a CTA's run: entries [k0, k1) of it, or (dense) tiles of 128 ring tokens.
+// split: the partial's place; the first one marks the `gaps` places behind the list's last as empty.
 template <int D, int KB, int VB, int NT>
-__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) sparse_few_kernel(const __grid_constant__ PrefillParams pp) {
+__device__ __forceinline__ void few_segment(const PrefillParams& pp, unsigned char* sm, bool dense, int64_t x, int k0, int k1,
+                                            int split, int last, int slots) {
   using C = FewCfg<D, KB, VB, NT>;
   constexpr int R = 8 * NT, E = D / 32, KR = D / 4;
   const QueryParams& p = pp.q;
-  pdl_start();
-  extern __shared__ __align__(128) unsigned char sm[];
   int* ids = reinterpret_cast<int*>(sm + C::IDS);
   float* qf = reinterpret_cast<float*>(sm + C::MISC);  // logit factor of a row
   int* lim = reinterpret_cast<int*>(qf + R);           // tokens it sees (dense: of the ring)
-  int* head = lim + R;                                 // records of the split
+  int* head = lim + R;                                 // records of the segment
   float2* wml = reinterpret_cast<float2*>(sm + C::ML); // the warps' statistics
+  float* red = reinterpret_cast<float*>(sm + C::RED);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  // records' splits first, the ring's shorter ones behind them
-  const int64_t U = (int64_t)p.L * p.B * p.Hkv * pp.tiles;
-  const int split = (int)(blockIdx.x / U);
-  const bool dense = split >= pp.Sc;
-  const int64_t x = blockIdx.x % U;
   const int h = (int)(x % p.Hkv), j = (int)(x / p.Hkv % pp.tiles), lb = (int)(x / p.Hkv / pp.tiles), b = lb % p.B, l = lb / p.B;
-  const int64_t unit = (int64_t)lb * p.Hkv + h;
   const CacheLen cl = cache_len(p, lb);
   const int tb = query_len(p, b);
   const int r0 = j * pp.q_block * p.G, rn = min(pp.q_block, tb - j * pp.q_block) * p.G;
   if (rn <= 0) return;
   const int S = pp.Sc + pp.St;
-  const int64_t wrow = unit * pp.rows + r0;
-  const int base = dense ? cl.n * kChunk : 0;
-  int k0 = 0, k1 = 0, n = 0;
+  const int64_t wrow = ((int64_t)lb * p.Hkv + h) * pp.rows + r0;
+  const int base = dense ? cl.n * kChunk : 0, place = (dense ? pp.Sc : 0) + split;
+  if (split == 0)  // places that no part of this list fills
+    for (int i = tid; i < rn * (slots - 1 - last); i += kFewThreads)
+      pp.ws_ml[(wrow + i % rn) * S + (dense ? pp.Sc : 0) + last + 1 + i / rn] = make_float2(-INFINITY, 0.f);
+  int t0 = 0, t1 = 0, n = 0;
+  __syncthreads();  // the segment before is done with what lies in shared memory
   if (dense) {
-    k0 = (split - pp.Sc) * pp.tps;
-    k1 = min(min(k0 + pp.tps, cl.len), row_limit(p, cl, tb, r0 + rn - 1) - base);
-  } else if (warp == 0) {  // the split's entries that name a record, in their order
+    t0 = k0 * kChunk;
+    t1 = min(min(k1 * kChunk, cl.len), row_limit(p, cl, tb, r0 + rn - 1) - base);
+  } else if (warp == 0) {  // the entries that name a record, in their order
     const int cnt = cl.n > 0 ? min(max(__ldg(pp.list_count + x), 0), pp.list_stride) : 0;
-    const int c0 = split * pp.cps, c1 = min(c0 + pp.cps, cnt);
+    const int c1 = min(k1, cnt);
     int at = 0;
-    for (int c = c0; c < c1; c += 32) {
+    for (int c = k0; c < c1; c += 32) {
       const int v = c + lane < c1 ? __ldg(pp.list + x * pp.list_stride + c + lane) : -1;
       const bool on = v >= 0 && v < cl.n;
       const uint32_t m = __ballot_sync(0xffffffffu, on);
@@ -454,24 +508,10 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) sparse_few_kerne
           dense ? pack2_bf16(v[e], v[e + 1]) : pack2_f16(v[e] * sc, v[e + 1] * sc);
     }
   }
-  if (!dense) {  // pair tables: entry i at 128 i, a copy of four bytes a lane
-    constexpr int KM = (1 << KB) - 1;
-    for (int i = tid; i < (1 << (2 * KB)) * 8; i += kFewThreads) {
-      const int e = i >> 3;
-      const uint32_t v = pack2_f16(p.kc.centroids[e & KM] * kTableScale, p.kc.centroids[e >> KB] * kTableScale);
-      reinterpret_cast<uint4*>(sm)[i] = make_uint4(v, v, v, v);
-    }
-    constexpr int FW = VIdx<VB>::FW, VM = (1 << VB) - 1;
-    for (int i = tid; i < VIdx<VB>::ENTRIES * 8; i += kFewThreads) {
-      const int e = i >> 3;
-      const uint32_t v = pack2_f16(p.vc.centroids[e & VM] * kTableScale, p.vc.centroids[(e >> FW) & VM] * kTableScale);
-      reinterpret_cast<uint4*>(sm + C::KTAB)[i] = make_uint4(v, v, v, v);
-    }
-  }
   __syncthreads();
   if (!dense) n = *head;
-  if (dense ? k0 >= k1 : n == 0) {
-    if (tid < rn) pp.ws_ml[(wrow + tid) * S + split] = make_float2(-INFINITY, 0.f);
+  if (dense ? t0 >= t1 : n == 0) {
+    if (tid < rn) pp.ws_ml[(wrow + tid) * S + place] = make_float2(-INFINITY, 0.f);
     return;
   }
   int low = 0x7FFFFFFF;
@@ -481,11 +521,11 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) sparse_few_kerne
   st.init();
   if (dense) {
     const int cap = p.tail_cap, start = p.tail_start ? ((p.tail_start[lb] % cap) + cap) % cap : 0;
-    few_ring<D, NT>(pp, reinterpret_cast<const uint2*>(sm + C::QF), k0, k1, cl.len, l, b, h, start, qf, lim, low, st);
+    few_ring<D, NT>(pp, reinterpret_cast<const uint2*>(sm + C::QF), t0, t1, cl.len, l, b, h, start, qf, lim, low, st);
   } else {
     few_records<D, KB, VB, NT>(pp, sm, ids, n, l, b, h, qf, lim, low, st);
   }
-  // ---------------------------------------------------------------- the warps' partials: one of the split
+  // ---------------------------------------------------------------- the warps' partials: one of the segment
   const float un = dense ? 1.f : pow2i(-15) * pow2i(st.ev - 13);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -497,10 +537,9 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) sparse_few_kerne
       if (g == 0) wml[warp * R + 8 * nt + 2 * t + e] = make_float2(st.m[nt][e], s);
     }
   constexpr int RS = D + D / 8;
-  float* red = reinterpret_cast<float*>(sm);
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    __syncthreads();  // tables and lists, or the rows before, are done with
+    if (nt) __syncthreads();  // the rows before are done with
     // element (row r, coordinate c) of a warp at r RS + c + 4 (c / 32) + r / 2: 32 stores, 32 banks
 #pragma unroll
     for (int mc = 0; mc < D / 16; ++mc)
@@ -524,9 +563,42 @@ __global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) sparse_few_kerne
         W = fmaf(f, ml.y, W);
         v = fmaf(f, red[w * 8 * RS + r * RS + c + 4 * (c >> 5) + (r >> 1)], v);
       }
-      pp.ws_acc[((wrow + row) * S + split) * D + c] = v;
-      if (c == 0) pp.ws_ml[(wrow + row) * S + split] = W != W ? make_float2(W, W) : make_float2(M, W);
+      pp.ws_acc[((wrow + row) * S + place) * D + c] = v;
+      if (c == 0) pp.ws_ml[(wrow + row) * S + place] = W != W ? make_float2(W, W) : make_float2(M, W);
     }
+  }
+}
+
+template <int D, int KB, int VB, int NT>
+__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) sparse_few_kernel(const __grid_constant__ PrefillParams pp) {
+  using C = FewCfg<D, KB, VB, NT>;
+  const QueryParams& p = pp.q;
+  pdl_start();
+  extern __shared__ __align__(128) unsigned char sm[];
+  const bool dense = (int)blockIdx.x >= pp.rec_ctas;
+  if (!dense) {  // pair tables: entry i at 128 i, a copy of four bytes a lane
+    constexpr int KM = (1 << KB) - 1, VM = (1 << VB) - 1;
+    for (int i = threadIdx.x; i < (1 << (2 * KB)) * 8; i += kFewThreads) {
+      const int e = i >> 3;
+      const uint32_t v = pack2_f16(p.kc.centroids[e & KM] * kTableScale, p.kc.centroids[e >> KB] * kTableScale);
+      reinterpret_cast<uint4*>(sm)[i] = make_uint4(v, v, v, v);
+    }
+    for (int i = threadIdx.x; i < (1 << (2 * VB)) * 8; i += kFewThreads) {
+      const int e = i >> 3;
+      const uint32_t v = pack2_f16(p.vc.centroids[e & VM] * kTableScale, p.vc.centroids[e >> VB] * kTableScale);
+      reinterpret_cast<uint4*>(sm + C::KTAB)[i] = make_uint4(v, v, v, v);
+    }
+  }
+  // the CTA's run of all lists' entries (or of all rings' tiles), list by list
+  const int64_t U = (int64_t)p.L * p.B * p.Hkv * pp.tiles;
+  const int per = dense ? pp.tps : pp.cps, len = dense ? pp.ring : pp.list_stride, slots = dense ? pp.St : pp.Sc;
+  const int64_t u0 = (int64_t)((int)blockIdx.x - (dense ? pp.rec_ctas : 0)) * per, u1 = min(u0 + per, U * len);
+  for (int64_t u = u0; u < u1;) {
+    const int64_t x = u / len, first = x * len;  // the list, and where its entries begin
+    const int k0 = (int)(u - first), k1 = (int)min((int64_t)len, u1 - first);
+    const int c = (int)(first / per);  // the CTA that has its first entry
+    few_segment<D, KB, VB, NT>(pp, sm, dense, x, k0, k1, (int)(u / per) - c, (int)((first + len - 1) / per) - c, slots);
+    u = first + k1;
   }
 }
 
@@ -538,8 +610,7 @@ cudaError_t sparse_few_launch_t(const PrefillParams& pp, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  const int64_t grid = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv * pp.tiles * (pp.Sc + pp.St);
-  kern<<<(unsigned)grid, kFewThreads, smem, s>>>(pp);
+  kern<<<pp.rec_ctas + pp.ring_ctas, kFewThreads, smem, s>>>(pp);
   return cudaGetLastError();
 }
 template <int D, int KB, int VB>
