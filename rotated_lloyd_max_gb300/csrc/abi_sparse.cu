@@ -41,7 +41,7 @@ namespace {
 
 constexpr int kFewRows = 16;   // rows of a list on mma.sync at most
 constexpr int kFewRecords = 256;  // records of a CTA's part of a list there at most
-constexpr double kFewTile = 2, kFewPart = 3;  // a tile of 128 ring tokens, a list's part, in records
+constexpr double kFewTile = 2, kFewPart = 1.5;  // a tile of 128 ring tokens, a list's part, in records
 
 // ----------------------------------------------------------------- bounds
 // where bounds or records lie: contiguous or a pool
@@ -196,15 +196,15 @@ tq_status sparse_plan(const tq_query_args* a, const tq_record_lists* r, const tq
   pp.tiles = (int)tiles;
   const int64_t keep = r->list_stride, ring = cdiv(q.max_tail, TQ_CHUNK), most = std::max(keep, ring);
   if (pl->few) {
-    // One wave of two CTAs per SM, shared between records and ring.  A CTA's time, in
-    // records: its entries, kFewTile for a tile of 128 ring tokens, and kFewPart for every
-    // list it has a part of (query set-up, first loads, joining its warps).  Of the
-    // entries per CTA that fill the wave, or fit the lists' ends, the best are taken.
-    const int64_t slots = 2 * sms;
-    auto most_parts = [](int64_t len, int64_t n) -> int64_t {  // CTAs that share a list of len, n a CTA
+    // A run for each team of an SM (sparse_few.cuh), shared between records and ring.  A run's time,
+    // in records: its entries, kFewTile for a tile of 128 ring tokens, and kFewPart for every
+    // list it has a part of (query set-up, first loads, joining the warps).  Of the
+    // entries per run that fill the teams, or fit the lists' ends, the best are taken.
+    const int64_t slots = (rows <= 8 ? 4 : 2) * sms;
+    auto most_parts = [](int64_t len, int64_t n) -> int64_t {  // runs that share a list of len, n a run
       return len == 0 ? 0 : n % len == 0 ? 1 : len % n == 0 ? len / n : (len - 1) / n + 2;
     };
-    auto parts_of = [](int64_t len, int64_t n) -> int64_t {  // lists that a CTA has a part of
+    auto parts_of = [](int64_t len, int64_t n) -> int64_t {  // lists that a run has a part of
       return len == 0 ? 0 : n % len == 0 ? n / len : len % n == 0 ? 1 : (n - 1) / len + 2;
     };
     double best = 1e300;
@@ -227,7 +227,7 @@ tq_status sparse_plan(const tq_query_args* a, const tq_record_lists* r, const tq
       consider(cdiv(keep, std::min<int64_t>(a->splits, keep)));
     } else {
       const double share = (keep + kFewPart) / (keep + kFewPart + (ring ? kFewTile * ring + kFewPart : 0));
-      const int64_t even = std::max<int64_t>(2, (int64_t)((double)(U * keep) / (share * (double)slots)) + 1);
+      const int64_t even = std::max<int64_t>(1, (int64_t)((double)(U * keep) / (share * (double)slots)) + 1);
       for (const int64_t per : {even, even + 1, even + even / 8, 2 * cdiv(even, 2)}) consider(per);
       if (even >= keep)
         for (int64_t k = even / keep; k <= even / keep + 1; ++k) consider(k * keep);
@@ -238,8 +238,8 @@ tq_status sparse_plan(const tq_query_args* a, const tq_record_lists* r, const tq
     pp.Sc = (int)most_parts(keep, pp.cps);
     pp.St = (int)most_parts(ring, pp.tps);
     if (cdiv(U * keep, pp.cps) + cdiv(U * ring, pp.tps) > 0x7FFFFFFFll) return TQ_ERR_UNSUPPORTED;
-    pp.rec_ctas = (int)cdiv(U * keep, pp.cps);
-    pp.ring_ctas = (int)cdiv(U * ring, pp.tps);
+    pp.rec_runs = (int)cdiv(U * keep, pp.cps);
+    pp.ring_runs = (int)cdiv(U * ring, pp.tps);
   } else {
     // The split count that minimises, in 128-token tiles' time, waves of records'
     // CTAs with their set-up and epilogue, the ring's CTAs in the last wave's idle

@@ -29,8 +29,8 @@ struct PrefillParams {
   const int32_t* list;
   const int32_t* list_count;
   int list_stride, q_block, sub;
-  // few rows: CTAs that share the lists' entries (cps each) and the rings' tiles of 128 tokens (tps each, ring a list)
-  int rec_ctas, ring_ctas, ring;
+  // few rows: runs of the lists' entries (cps each) and of the rings' tiles of 128 tokens (tps each, ring a list)
+  int rec_runs, ring_runs, ring;
 };
 
 // The records of a row tile's split: c0, c0 + 1, .., or (LISTED) the entries c0,

@@ -2,18 +2,20 @@
 // (query heads of a kv head x tokens of a block), head dims 64 and 128, codecs
 // without side lists: the decode step of a long cache.
 //
-// One wave of CTAs: the lists' entries, one list after the other, are cut into equal
-// runs, a run a CTA, and so are the rings' tiles for the CTAs behind, so that a CTA
-// works on the ends of two lists and the lists between; what it has of each is a
-// partial for the merge.  Eight warps a CTA; four share a record (32 tokens each),
-// the two groups take every other one of a run.  Tokens are the M dimension of the scores
-// (K q~^T, rows as N), coordinates that of the outputs (V^T p), so that 8 rows
-// fill the N of mma.sync and both operands A are decoded from the packed codes
-// straight into registers: a lane holds d / 4 neighbouring codes of four keys, and
-// d / 8 codes of eight values, whose codes are paired by token before the lookup
-// (3-bit ones after it).  Every pair of codes is one lookup in a table with a copy
-// per lane (no bank conflicts).  The words of the next record are loaded as soon as this one's are
-// used; warps share nothing until the end, so that no barrier holds up the loads.
+// The lists' entries, one list after the other, are cut into equal runs, and so are
+// the rings' tiles behind them; a run is worked off by a team of four warps, which
+// has parts of one or more lists, each a partial for the merge.  A CTA per SM holds
+// four teams that share nothing but the lookup tables, so that one team's set-up,
+// first loads and joining of its warps run under the others' records.  A warp takes
+// 32 tokens of a record and copies its tokens of the next record but one into shared
+// memory while it works (cp.async, two stages): no barrier between records.
+//
+// Tokens are the M dimension of the scores (K q~^T, rows as N), coordinates that of
+// the outputs (V^T p), so that 8 rows fill the N of mma.sync and both operands A are
+// decoded from the packed codes straight into registers: a lane holds d / 4
+// neighbouring codes of four keys, and d / 8 codes of eight values, paired by token
+// before the lookup (3-bit codes after it).  Every pair of codes is one lookup in a
+// table with a copy per lane (no bank conflicts).
 //
 // Centroids and rotated queries are f16 (11 bits), logits take the key's scale and
 // sums in f32.  A weight enters times its value's scale, relative to the running
@@ -27,18 +29,39 @@
 
 namespace tq {
 
-constexpr int kFewThreads = 256;
+// teams of a CTA: four of up to 8 rows; two of 16, whose accumulators take 255 registers a
+// thread (four with 128 spill: 256 records of 32 sequences, 4 kv heads of 16: 433 us, 237 with two)
+constexpr int few_teams(int rows) { return rows <= 8 ? 4 : 2; }
+__device__ __forceinline__ void team_sync() { asm volatile("bar.sync %0, 128;" ::"r"(1 + (int)(threadIdx.x >> 7)) : "memory"); }
+
 constexpr int kFewIds = 256;  // records that are listed at a time
 
 template <int D, int KB, int VB, int NT>
 struct FewCfg {
   static constexpr int KTAB = (1 << (2 * KB)) * 128, VTAB = (1 << (2 * VB)) * 128;
-  static constexpr int QF = KTAB + VTAB, QFB = D / 16 * NT * 32 * 8;
+  // of a team:
+  static constexpr int QF = 0, QFB = D / 16 * NT * 32 * 8;
   static constexpr int IDS = QF + QFB, MISC = IDS + kFewIds * 4;
   static constexpr int MISCB = 8 * NT * 8 + 64, ML = MISC + MISCB;
-  static constexpr int RED = ML + 8 * 8 * NT * 8;           // the warps' outputs of eight rows
-  static constexpr int SMEM = RED + 8 * 8 * (D + D / 8) * 4;
+  static constexpr int STAGE = ML + 4 * 8 * NT * 8;  // two a warp: 32 keys, 32 values, their scales
+  static constexpr int VAT = 32 * (D * KB / 8), NAT = VAT + 32 * (D * VB / 8), STAGEB = NAT + 256;
+  static constexpr int RED = 4 * 8 * (D + D / 8) * 4;  // in the stages' place: the warps' outputs of eight rows
+  static constexpr int TEAM = STAGE + (8 * STAGEB > RED ? 8 * STAGEB : RED);
+  static constexpr int TEAMS = few_teams(8 * NT), THREADS = 128 * TEAMS, SMEM = KTAB + VTAB + TEAMS * TEAM;
+  static_assert(STAGE % 16 == 0 && STAGEB % 16 == 0 && TEAM % 16 == 0 && SMEM <= 232448, "one CTA per SM");
 };
+
+// Where 16-byte chunk c of a row lies in a warp's 32 rows: rows of 64 bytes two to a line of 128, in which the
+// chunks move on by two from line to line, so that the eight lanes of a key's and the sixteen of a value's
+// access meet no bank twice; other rows one behind the other.
+template <int ROW>
+__device__ __forceinline__ int few_chunk(int i) {
+  if constexpr (ROW == 64) {
+    const int line = i >> 3;
+    return line * 128 + (((i & 7) + 2 * line) & 7) * 16;
+  }
+  return 16 * i;
+}
 
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t r;
@@ -115,49 +138,53 @@ struct FewState {
 
 // The records of a split.
 template <int D, int KB, int VB, int NT>
-__device__ __forceinline__ void few_records(const PrefillParams& pp, unsigned char* sm, const int* ids, int n, int l, int b,
+__device__ __forceinline__ void few_records(const PrefillParams& pp, const unsigned char* tables, unsigned char* sm, const int* ids, int n, int l, int b,
                                             int h, const float* qf, const int* lim, int low, FewState<D, NT>& st) {
   using C = FewCfg<D, KB, VB, NT>;
   constexpr int KS = D / 16, KR = D / 4, VR = D / 8, KNB = KR * KB, VNB = VR * VB;
   constexpr int KROW = D * KB / 8, VROW = D * VB / 8, VNW = Run<VNB>::NW;
   const QueryParams& p = pp.q;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-  const int w4 = warp & 3;
+  const int lane = threadIdx.x & 31, w4 = (threadIdx.x >> 5) & 3, g = lane >> 2, t = lane & 3;
   const uint32_t loff = lane * 4;
-  const unsigned char *ktab = sm, *vtab = sm + C::KTAB;
+  const unsigned char *ktab = tables, *vtab = tables + C::KTAB;
   const ByteTable kbt = byte_table(ktab, loff, 128), vbt = byte_table(vtab, loff, 128);
   const uint2* qfrag = reinterpret_cast<const uint2*>(sm + C::QF) + lane;
-  const uint8_t* kl = p.krec + l * p.krec_ls;
-  const uint8_t* vl = p.vrec + l * p.vrec_ls;
-  Run<KNB> kr[4];
-  Run<VNB> vr[8];
-  float nk[4], nv[4], nk1[4], nv1[4];
+  float nk[4], nv[4];
   // contiguous records follow one another behind a base; pages are looked up
-  const uint8_t* kbase = kl + (p.table ? (int64_t)h : ((int64_t)b * p.Hkv + h) * p.rec_cap) * p.kc.rec_bytes;
-  const uint8_t* vbase = vl + (p.table ? (int64_t)h : ((int64_t)b * p.Hkv + h) * p.rec_cap) * p.vc.rec_bytes;
   const int32_t* table = p.table ? p.table + (int64_t)b * p.table_stride : nullptr;
-  const int kat = (32 * w4 + g) * KROW, vat = (32 * w4 + 2 * t) * VROW;
-  const int knorm = p.kc.off_norm + 4 * (32 * w4 + g), vnorm = p.vc.off_norm + 4 * (32 * w4 + g);
+  const int64_t unit = table ? (int64_t)h : ((int64_t)b * p.Hkv + h) * p.rec_cap;
   const int kstep = (table ? p.Hkv : 1) * p.kc.rec_bytes, vstep = (table ? p.Hkv : 1) * p.vc.rec_bytes;
-  auto index = [&](int i) {  // the i-th record's place behind a base
-    const int c = ids[i];
-    return table ? min(max(__ldg(table + c), 0), p.rec_cap - 1) : c;
+  const uint8_t* kbase = p.krec + l * p.krec_ls + unit * p.kc.rec_bytes + 32 * w4 * KROW + 16 * lane;
+  const uint8_t* vbase = p.vrec + l * p.vrec_ls + unit * p.vc.rec_bytes + 32 * w4 * VROW + 16 * lane;
+  const int norm = (lane < 8 ? p.kc.off_norm - 32 * w4 * KROW : p.vc.off_norm - 32 * w4 * VROW - 128) + 128 * w4;
+  unsigned char* stages = sm + C::STAGE + w4 * 2 * C::STAGEB;
+  // the warp's tokens of entry i into a stage
+  auto ask = [&](int i, int s) {
+    const int e = ids[i], c = table ? min(max(__ldg(table + e), 0), p.rec_cap - 1) : e;
+    unsigned char* st_ = stages + s * C::STAGEB;
+    const uint8_t *k = kbase + (int64_t)c * kstep, *v = vbase + (int64_t)c * vstep;
+#pragma unroll
+    for (int j = 0; j < 2 * KROW; j += 32)
+      if (j + 32 <= 2 * KROW || j + lane < 2 * KROW) cp_async16(st_ + few_chunk<KROW>(j + lane), k + 16 * j);
+#pragma unroll
+    for (int j = 0; j < 2 * VROW; j += 32)
+      if (j + 32 <= 2 * VROW || j + lane < 2 * VROW) cp_async16(st_ + C::VAT + few_chunk<VROW>(j + lane), v + 16 * j);
+    if (lane < 16) cp_async16(st_ + C::NAT + 16 * lane, (lane < 8 ? k : v) + norm);
   };
-  auto load_keys = [&](int c) {
-    const uint8_t* rec = kbase + (int64_t)c * kstep;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      kr[i].load(rec + kat + 8 * i * KROW, KNB * t);
-      nk1[i] = __ldg(reinterpret_cast<const float*>(rec + knorm) + 8 * i);
-    }
+  // a key's run of codes: token 8 i + g, run t; a value's: token 16 mt + 2 t + {0, 1, 8, 9}, run g
+  const int kat = KROW == 64 ? (g >> 1) * 128 + (((g & 1) * 4 + t + 2 * (g >> 1)) & 7) * 16 : g * KROW;
+  auto key_run = [&](const unsigned char* st_, int i, uint32_t (&w)[Run<KNB>::NW]) {
+    Run<KNB> r;
+    if constexpr (KROW == 64) r.fetch(st_ + kat + 512 * i, 0);
+    else r.fetch(st_ + kat + 8 * i * KROW, KNB * t);
+    r.get(KNB * t, w);
   };
-  auto load_values = [&](int c) {
-    const uint8_t* rec = vbase + (int64_t)c * vstep;
-#pragma unroll
-    for (int i = 0; i < 8; ++i)  // tokens 16 (i / 4) + 2 t + {0, 1, 8, 9}
-      vr[i].load(rec + vat + (16 * (i >> 2) + (i & 1) + 8 * ((i >> 1) & 1)) * VROW, VNB * g);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) nv1[i] = __ldg(reinterpret_cast<const float*>(rec + vnorm) + 8 * i);
+  auto value_run = [&](const unsigned char* st_, int mt, int k, uint32_t (&w)[VNW]) {
+    Run<VNB> r;
+    if constexpr (VROW == 64)
+      r.fetch(st_ + C::VAT + (8 * mt + t + 4 * (k >> 1)) * 128 + (((k & 1) * 4 + (g >> 1) + 2 * t) & 7) * 16 + (g & 1) * 8, 0);
+    else r.fetch(st_ + C::VAT + (16 * mt + 2 * t + (k & 1) + 8 * (k >> 1)) * VROW, VNB * g);
+    r.get(VNB * g, w);
   };
   const bool capped = p.scap > 0.f;
   float f[NT][2], rf[NT][2];  // logit factors and references of the lane's rows
@@ -170,14 +197,16 @@ __device__ __forceinline__ void few_records(const PrefillParams& pp, unsigned ch
     }
   bool none = true;  // a row has no reference yet
   float reach = 0.f, up = 0.f;  // scales that the exponent of the values' covers; 2^14 2^-(ev + 1)
-  int i = warp >> 2;
-  if (i >= n) return;
-  int at = index(i);
-  load_keys(at);
-  load_values(at);
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+    if (s < n) ask(s, s);
+    cp_async_commit();
+  }
 #pragma unroll 1
-  for (; i < n; i += 2) {
-    const int next = i + 2 < n ? index(i + 2) : at;
+  for (int i = 0, s = 0; i < n; ++i, s ^= 1) {
+    cp_async_wait<1>();
+    __syncwarp();
+    const unsigned char* stage = stages + s * C::STAGEB;
     // ---------------------------------------------------------------- scores
     float x[2][NT][4];
 #pragma unroll
@@ -190,8 +219,8 @@ __device__ __forceinline__ void few_records(const PrefillParams& pp, unsigned ch
       uint32_t w[4][Run<KNB>::NW];
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        kr[k].get(KNB * t, w[k]);
-        nk[k] = finite_or_nan(nk1[k]);
+        key_run(stage, k, w[k]);
+        nk[k] = finite_or_nan(reinterpret_cast<const float*>(stage + C::NAT)[8 * k + g]);
       }
 #pragma unroll
       for (int kk = 0; kk < KS; ++kk) {
@@ -214,7 +243,6 @@ __device__ __forceinline__ void few_records(const PrefillParams& pp, unsigned ch
         }
       }
     }
-    load_keys(next);
     // ---------------------------------------------------------------- weights
     // against the references as they stand, unless a row has none, a logit passes its by more than 1, a value's
     // scale the exponent, a row does not see a token, or logits are capped
@@ -223,7 +251,7 @@ __device__ __forceinline__ void few_records(const PrefillParams& pp, unsigned ch
     float over = -INFINITY, big = 0.f;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
-      nv[k] = nv1[k];
+      nv[k] = reinterpret_cast<const float*>(stage + C::NAT)[32 + 8 * k + g];
       big = fmaxf(big, fabsf(nv[k]));
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -283,7 +311,7 @@ __device__ __forceinline__ void few_records(const PrefillParams& pp, unsigned ch
         // token's pairs of neighbours and to pair the results (8 instructions for two operands; 12)
         uint32_t r[4][VNW];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) vr[4 * mt + k].get(VNB * g, r[k]);
+        for (int k = 0; k < 4; ++k) value_run(stage, mt, k, r[k]);
 #pragma unroll
         for (int mc = 0; mc < KS; ++mc) {
           uint32_t y[4], a[4];
@@ -302,8 +330,8 @@ __device__ __forceinline__ void few_records(const PrefillParams& pp, unsigned ch
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
           uint32_t r0[VNW], r1[VNW];
-          vr[4 * mt + 2 * k].get(VNB * g, r0);
-          vr[4 * mt + 2 * k + 1].get(VNB * g, r1);
+          value_run(stage, mt, 2 * k, r0);
+          value_run(stage, mt, 2 * k + 1, r1);
           v_pair_words<VB, VNW>(r0, r1, z[2 * k], z[2 * k + 1]);
         }
 #pragma unroll
@@ -319,8 +347,11 @@ __device__ __forceinline__ void few_records(const PrefillParams& pp, unsigned ch
         }
       }
     }
-    load_values(next);
+    __syncwarp();  // the stage has been read
+    if (i + 2 < n) ask(i + 2, s);
+    cp_async_commit();
   }
+  cp_async_wait<0>();
 }
 
 // The ring's tokens [k0, k1) of a split: a warp takes 16 at a time, whose keys and values are asked for together.
@@ -329,7 +360,7 @@ __device__ __forceinline__ void few_ring(const PrefillParams& pp, const uint2* q
                                          int h, int start, const float* qf, const int* lim, int low, FewState<D, NT>& st) {
   constexpr int KS = D / 16, KR = D / 4, VR = D / 8;
   const QueryParams& p = pp.q;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) & 3, g = lane >> 2, t = lane & 3;
   const int64_t ring = l * p.tail_ls + (int64_t)(b * p.Hkv + h) * p.tail_cap * D;
   const uint16_t *kt = p.ktail + ring, *vt = p.vtail + ring;
   // clamped to the last token: its values are finite, its weights zero
@@ -339,7 +370,7 @@ __device__ __forceinline__ void few_ring(const PrefillParams& pp, const uint2* q
     return (int64_t)s * D;
   };
 #pragma unroll 1
-  for (int a0 = k0 + 16 * warp; a0 < k1; a0 += 16 * (kFewThreads / 32)) {
+  for (int a0 = k0 + 16 * warp; a0 < k1; a0 += 64) {
     uint4 kw[2][KS / 2], vw[4][VR / 8];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
@@ -417,10 +448,10 @@ __device__ __forceinline__ void few_ring(const PrefillParams& pp, const uint2* q
   }
 }
 
-// One list's part of a CTA's run: entries [k0, k1) of it, or (dense) tiles of 128 ring tokens.
+// One list's part of a team's run: entries [k0, k1) of it, or (dense) tiles of 128 ring tokens.
 // split: the partial's place; the first one marks the `gaps` places behind the list's last as empty.
 template <int D, int KB, int VB, int NT>
-__device__ __forceinline__ void few_segment(const PrefillParams& pp, unsigned char* sm, bool dense, int64_t x, int k0, int k1,
+__device__ __forceinline__ void few_segment(const PrefillParams& pp, const unsigned char* tables, unsigned char* sm, bool dense, int64_t x, int k0, int k1,
                                             int split, int last, int slots) {
   using C = FewCfg<D, KB, VB, NT>;
   constexpr int R = 8 * NT, E = D / 32, KR = D / 4;
@@ -430,8 +461,9 @@ __device__ __forceinline__ void few_segment(const PrefillParams& pp, unsigned ch
   int* lim = reinterpret_cast<int*>(qf + R);           // tokens it sees (dense: of the ring)
   int* head = lim + R;                                 // records of the segment
   float2* wml = reinterpret_cast<float2*>(sm + C::ML); // the warps' statistics
-  float* red = reinterpret_cast<float*>(sm + C::RED);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  float* red = reinterpret_cast<float*>(sm + C::STAGE);
+  constexpr int WARPS = 4, T = 128;
+  const int tid = threadIdx.x & (T - 1), lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int h = (int)(x % p.Hkv), j = (int)(x / p.Hkv % pp.tiles), lb = (int)(x / p.Hkv / pp.tiles), b = lb % p.B, l = lb / p.B;
   const CacheLen cl = cache_len(p, lb);
   const int tb = query_len(p, b);
@@ -441,10 +473,10 @@ __device__ __forceinline__ void few_segment(const PrefillParams& pp, unsigned ch
   const int64_t wrow = ((int64_t)lb * p.Hkv + h) * pp.rows + r0;
   const int base = dense ? cl.n * kChunk : 0, place = (dense ? pp.Sc : 0) + split;
   if (split == 0)  // places that no part of this list fills
-    for (int i = tid; i < rn * (slots - 1 - last); i += kFewThreads)
+    for (int i = tid; i < rn * (slots - 1 - last); i += T)
       pp.ws_ml[(wrow + i % rn) * S + (dense ? pp.Sc : 0) + last + 1 + i / rn] = make_float2(-INFINITY, 0.f);
   int t0 = 0, t1 = 0, n = 0;
-  __syncthreads();  // the segment before is done with what lies in shared memory
+  team_sync();  // the segment before is done with what lies in shared memory
   if (dense) {
     t0 = k0 * kChunk;
     t1 = min(min(k1 * kChunk, cl.len), row_limit(p, cl, tb, r0 + rn - 1) - base);
@@ -462,7 +494,7 @@ __device__ __forceinline__ void few_segment(const PrefillParams& pp, unsigned ch
     if (lane == 0) *head = at;
   }
   // ---------------------------------------------------------------- queries: a warp a row
-  for (int r = warp; r < R; r += kFewThreads / 32) {
+  for (int r = warp; r < R; r += WARPS) {
     const int row = r0 + r;
     float v[E];
 #pragma unroll
@@ -508,7 +540,7 @@ __device__ __forceinline__ void few_segment(const PrefillParams& pp, unsigned ch
           dense ? pack2_bf16(v[e], v[e + 1]) : pack2_f16(v[e] * sc, v[e + 1] * sc);
     }
   }
-  __syncthreads();
+  team_sync();
   if (!dense) n = *head;
   if (dense ? t0 >= t1 : n == 0) {
     if (tid < rn) pp.ws_ml[(wrow + tid) * S + place] = make_float2(-INFINITY, 0.f);
@@ -523,7 +555,7 @@ __device__ __forceinline__ void few_segment(const PrefillParams& pp, unsigned ch
     const int cap = p.tail_cap, start = p.tail_start ? ((p.tail_start[lb] % cap) + cap) % cap : 0;
     few_ring<D, NT>(pp, reinterpret_cast<const uint2*>(sm + C::QF), t0, t1, cl.len, l, b, h, start, qf, lim, low, st);
   } else {
-    few_records<D, KB, VB, NT>(pp, sm, ids, n, l, b, h, qf, lim, low, st);
+    few_records<D, KB, VB, NT>(pp, tables, sm, ids, n, l, b, h, qf, lim, low, st);
   }
   // ---------------------------------------------------------------- the warps' partials: one of the segment
   const float un = dense ? 1.f : pow2i(-15) * pow2i(st.ev - 13);
@@ -539,7 +571,7 @@ __device__ __forceinline__ void few_segment(const PrefillParams& pp, unsigned ch
   constexpr int RS = D + D / 8;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt) {
-    if (nt) __syncthreads();  // the rows before are done with
+    team_sync();  // stages, or the rows before, are done with
     // element (row r, coordinate c) of a warp at r RS + c + 4 (c / 32) + r / 2: 32 stores, 32 banks
 #pragma unroll
     for (int mc = 0; mc < D / 16; ++mc)
@@ -548,15 +580,15 @@ __device__ __forceinline__ void few_segment(const PrefillParams& pp, unsigned ch
         const int c = D / 8 * g + 2 * mc + (e >> 1), r = 2 * t + (e & 1);
         red[warp * 8 * RS + r * RS + c + 4 * (c >> 5) + (r >> 1)] = st.acc[nt][mc][e] * un;
       }
-    __syncthreads();
-    for (int i = tid; i < 8 * D; i += kFewThreads) {
+    team_sync();
+    for (int i = tid; i < 8 * D; i += T) {
       const int r = i / D, c = i % D, row = 8 * nt + r;
       if (row >= rn) break;
       float M = -INFINITY, W = 0.f, v = 0.f;
 #pragma unroll
-      for (int w = 0; w < 8; ++w) M = fmaxf(M, wml[w * R + row].x);
+      for (int w = 0; w < WARPS; ++w) M = fmaxf(M, wml[w * R + row].x);
 #pragma unroll
-      for (int w = 0; w < 8; ++w) {
+      for (int w = 0; w < WARPS; ++w) {
         const float2 ml = wml[w * R + row];
         // a NaN sum stays one, whatever the maximum is
         const float f = ml.x > -INFINITY ? ex2(ml.x - M) : ml.y != ml.y ? 1.f : 0.f;
@@ -570,34 +602,39 @@ __device__ __forceinline__ void few_segment(const PrefillParams& pp, unsigned ch
 }
 
 template <int D, int KB, int VB, int NT>
-__global__ void __launch_bounds__(kFewThreads, NT == 1 ? 2 : 1) sparse_few_kernel(const __grid_constant__ PrefillParams pp) {
+__global__ void __launch_bounds__(128 * few_teams(8 * NT), 1) sparse_few_kernel(const __grid_constant__ PrefillParams pp) {
   using C = FewCfg<D, KB, VB, NT>;
   const QueryParams& p = pp.q;
   pdl_start();
   extern __shared__ __align__(128) unsigned char sm[];
-  const bool dense = (int)blockIdx.x >= pp.rec_ctas;
-  if (!dense) {  // pair tables: entry i at 128 i, a copy of four bytes a lane
+  {  // pair tables: entry i at 128 i, a copy of four bytes a lane
     constexpr int KM = (1 << KB) - 1, VM = (1 << VB) - 1;
-    for (int i = threadIdx.x; i < (1 << (2 * KB)) * 8; i += kFewThreads) {
+    for (int i = threadIdx.x; i < (1 << (2 * KB)) * 8; i += C::THREADS) {
       const int e = i >> 3;
       const uint32_t v = pack2_f16(p.kc.centroids[e & KM] * kTableScale, p.kc.centroids[e >> KB] * kTableScale);
       reinterpret_cast<uint4*>(sm)[i] = make_uint4(v, v, v, v);
     }
-    for (int i = threadIdx.x; i < (1 << (2 * VB)) * 8; i += kFewThreads) {
+    for (int i = threadIdx.x; i < (1 << (2 * VB)) * 8; i += C::THREADS) {
       const int e = i >> 3;
       const uint32_t v = pack2_f16(p.vc.centroids[e & VM] * kTableScale, p.vc.centroids[e >> VB] * kTableScale);
       reinterpret_cast<uint4*>(sm + C::KTAB)[i] = make_uint4(v, v, v, v);
     }
   }
-  // the CTA's run of all lists' entries (or of all rings' tiles), list by list
+  __syncthreads();
+  // the team's run of all lists' entries (or of all rings' tiles), list by list; the teams of an SM take
+  // runs far apart, so that records and ring meet there
+  const int team = threadIdx.x >> 7, slot = team * (int)gridDim.x + (int)blockIdx.x;
+  const bool dense = slot >= pp.rec_runs;
+  if (slot >= pp.rec_runs + pp.ring_runs) return;
   const int64_t U = (int64_t)p.L * p.B * p.Hkv * pp.tiles;
   const int per = dense ? pp.tps : pp.cps, len = dense ? pp.ring : pp.list_stride, slots = dense ? pp.St : pp.Sc;
-  const int64_t u0 = (int64_t)((int)blockIdx.x - (dense ? pp.rec_ctas : 0)) * per, u1 = min(u0 + per, U * len);
+  const int64_t u0 = (int64_t)(slot - (dense ? pp.rec_runs : 0)) * per, u1 = min(u0 + per, U * len);
   for (int64_t u = u0; u < u1;) {
     const int64_t x = u / len, first = x * len;  // the list, and where its entries begin
     const int k0 = (int)(u - first), k1 = (int)min((int64_t)len, u1 - first);
-    const int c = (int)(first / per);  // the CTA that has its first entry
-    few_segment<D, KB, VB, NT>(pp, sm, dense, x, k0, k1, (int)(u / per) - c, (int)((first + len - 1) / per) - c, slots);
+    const int c = (int)(first / per);  // the run that has its first entry
+    few_segment<D, KB, VB, NT>(pp, sm, sm + C::KTAB + C::VTAB + team * C::TEAM, dense, x, k0, k1, (int)(u / per) - c,
+                               (int)((first + len - 1) / per) - c, slots);
     u = first + k1;
   }
 }
@@ -610,7 +647,9 @@ cudaError_t sparse_few_launch_t(const PrefillParams& pp, cudaStream_t s) {
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
   }
-  kern<<<pp.rec_ctas + pp.ring_ctas, kFewThreads, smem, s>>>(pp);
+  const int runs = pp.rec_runs + pp.ring_runs;
+  constexpr int teams = few_teams(8 * NT);
+  kern<<<(unsigned)(runs <= teams * sm_count() ? min(runs, sm_count()) : cdiv(runs, teams)), 128 * teams, smem, s>>>(pp);
   return cudaGetLastError();
 }
 template <int D, int KB, int VB>
