@@ -310,6 +310,14 @@ tq_status tq_norm_append(const tq_append_args* a, const tq_head_norm* n, void* s
   p.q_hs = n->q_head_stride;
   p.k_hs = n->k_head_stride;
   p.eps = n->eps;
+  // with many tokens eight a CTA, all their heads: a CTA's angles and first loads are a chain of 2 to 3 us
+  // (4 prompts of 2049 tokens, 48 heads of 128: 42 us with two tokens a CTA)
+  const int64_t eights = (int64_t)p.L * p.B * cdiv(p.T, 8);
+  if (eights >= 2 * sm_count()) {
+    p.tile = 8;
+    p.tiles = (int)cdiv(p.T, 8);
+    p.group = p.heads;
+  }
   cudaStream_t s = (cudaStream_t)stream;
   if (launch_norm_append(p, s) != cudaSuccess) return TQ_ERR_CUDA;
   if (p.in_place && launch_append_commit(p, s) != cudaSuccess) return TQ_ERR_CUDA;

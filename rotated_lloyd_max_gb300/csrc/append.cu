@@ -18,10 +18,11 @@
 // and one chain behind it (lengths, inv_freq, angle, barrier, and only then the loads);
 // with the counters in place, which a second launch moves, 3.7 us.
 //
-// With norms (tq_norm_append) the lanes that hold a head, d / 16 neighbours of one
-// warp, add up its squares by shuffles; norm, weights and rotation follow in f32
-// on the values in registers and are rounded once, so that the norm costs no
-// second read.
+// With norms (norm_append_kernel) the lanes that hold a head, d / 16 neighbours of
+// one warp, add up its squares by shuffles; norm, weights and rotation follow in f32
+// on the values in registers and are rounded once, so that the norm costs no second
+// read.  The next unit is asked for before this one is worked on, and cosines and
+// sines lie in planes, so that two pairs turn by packed instructions.
 #include "cache_params.h"
 #include "tq_common.cuh"
 
@@ -64,35 +65,29 @@ __device__ __forceinline__ void turn_adjacent(uint4& a, const float2* cs) {
   }
 }
 
-__device__ __forceinline__ void unpack8(const uint4& v, float (&x)[8]) {
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    x[2 * i] = bf16_lo(w[i]);
-    x[2 * i + 1] = bf16_hi(w[i]);
-  }
+// the fraction of a turn that a position adds, as a multiple of 2^-64, and the cosine and sine of part 2^-64 turns
+__device__ __forceinline__ uint64_t turn_fraction(float inv_freq) {
+  double turns = (double)inv_freq * 0.15915494309189533577;
+  turns -= floor(turns);
+  // turns in [0, 1]; the product with a position only needs it modulo 1
+  return turns < 1.0 ? (uint64_t)(turns * 18446744073709551616.0) : 0ull;
 }
-__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
-  return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
+__device__ __forceinline__ void turn_angle(int32_t pos, uint64_t frac, float* s, float* c) {
+  const int64_t part = (int64_t)((uint64_t)(int64_t)pos * frac);
+  sincospif((float)(int32_t)(part >> 32) * 4.656612873077393e-10f, s, c);  // 2^-31: half turns
 }
-__device__ __forceinline__ void scale8(float (&x)[8], float r, const float* w) {
-  const float4 a = __ldg(reinterpret_cast<const float4*>(w)), b = __ldg(reinterpret_cast<const float4*>(w) + 1);
-  const float v[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] *= r * v[i];
-}
-// four pairs of neighbours
-__device__ __forceinline__ void turn_adjacent(float (&x)[8], const float2* cs) {
-#pragma unroll
-  for (int i = 0; i < 8; i += 2) {
-    const float2 c = cs[i / 2];
-    const float x0 = x[i], x1 = x[i + 1];
-    x[i] = x0 * c.x - x1 * c.y;
-    x[i + 1] = x1 * c.x + x0 * c.y;
+
+// the new tokens' accumulated weights start at 0
+__device__ __forceinline__ void clear_mass(const AppendParams& p, int l, int b, int len, int t0, int nt) {
+  const int64_t first = (int64_t)kChunk * (p.n_chunks ? max(p.n_chunks[l * p.B + b], 0) : 0) + len + t0;
+  float* m = p.mass + l * p.mass_ls + (int64_t)b * p.Hkv * p.mass_cap;
+  for (int i = threadIdx.x; i < nt * p.Hkv; i += kAppendThreads) {
+    const int64_t at = first + i % nt;
+    if (at < p.mass_cap) m[(int64_t)(i / nt) * p.mass_cap + at] = 0.f;
   }
 }
 
-template <int D, bool NORM>
+template <int D>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int UPH = D / 16;  // two-chunk units per head
   extern __shared__ __align__(16) float2 table[];  // [tile][rot_dim / 2] cos, sin (times rot_scale)
@@ -109,26 +104,15 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
   const int start = p.tail_start ? ((p.tail_start[lb] % cap) + cap) % cap : 0;
   const int half = p.rot_dim >> 1;
   for (int i = threadIdx.x; i < half; i += kAppendThreads) {
-    double turns = (double)p.inv_freq[i] * 0.15915494309189533577;
-    turns -= floor(turns);
-    // turns in [0, 1]; the product below only needs it modulo 1
-    const uint64_t frac = turns < 1.0 ? (uint64_t)(turns * 18446744073709551616.0) : 0ull;
+    const uint64_t frac = turn_fraction(p.inv_freq[i]);
     const int32_t* pos = p.positions + ((int64_t)p.pair_axis[i] * p.B + b) * p.T + t0;
     for (int t = 0; t < nt; ++t) {
-      const int64_t part = (int64_t)((uint64_t)(int64_t)pos[t] * frac);
       float s, c;
-      sincospif((float)(int32_t)(part >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
+      turn_angle(pos[t], frac, &s, &c);
       table[t * half + i] = f2(c * p.rot_scale, s * p.rot_scale);
     }
   }
-  if (p.mass && fits && blockIdx.y == 0) {
-    const int64_t first = (int64_t)kChunk * (p.n_chunks ? max(p.n_chunks[lb], 0) : 0) + len + t0;
-    float* m = p.mass + l * p.mass_ls + (int64_t)b * p.Hkv * p.mass_cap;
-    for (int i = threadIdx.x; i < nt * p.Hkv; i += kAppendThreads) {
-      const int64_t at = first + i % nt;
-      if (at < p.mass_cap) m[(int64_t)(i / nt) * p.mass_cap + at] = 0.f;
-    }
-  }
+  if (p.mass && fits && blockIdx.y == 0) clear_mass(p, l, b, len, t0, nt);
   __syncthreads();
   const uint16_t* q = p.q + l * p.q_ls + b * p.q_bs;
   const uint16_t* k = p.k + l * p.kv_ls + b * p.kv_bs;
@@ -176,43 +160,6 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     }
     uint4 x = *reinterpret_cast<const uint4*>(src + 8 * c0), y = *reinterpret_cast<const uint4*>(src + 8 * c1);
     const float2* cs = table + t * half;
-    if constexpr (NORM) {
-      const bool query = h < p.Hq;
-      const float* wt = query ? p.q_weight : turns ? p.k_weight : nullptr;  // values have no norm
-      if (wt) {  // the same for the UPH neighbouring lanes that hold the head
-        wt += query ? h * p.q_hs : (h - p.Hq) * p.k_hs;
-        float a[8], b[8];
-        unpack8(x, a);
-        unpack8(y, b);
-        float2 ss = f2(0.f, 0.f);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fma2(f2(a[j], b[j]), f2(a[j], b[j]), ss);
-        float sum = ss.x + ss.y;
-        const uint32_t team = UPH == 32 ? 0xffffffffu : ((1u << (UPH & 31)) - 1u) << (threadIdx.x & 31 & ~(UPH - 1));
-#pragma unroll
-        for (int m = 1; m < UPH; m <<= 1) sum += __shfl_xor_sync(team, sum, m);
-        const float r = rsqrtf(fmaf(sum, 1.f / D, p.eps));
-        scale8(a, r, wt + 8 * c0);
-        scale8(b, r, wt + 8 * c1);
-        if (pairs) {
-          cs += 8 * u;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float2 c = cs[j];
-            const float y0 = a[j] * c.x - b[j] * c.y, y1 = b[j] * c.x + a[j] * c.y;
-            a[j] = y0;
-            b[j] = y1;
-          }
-        } else if (p.adjacent) {
-          const int r0 = 8 * c0 - p.rot_start, r1 = 8 * c1 - p.rot_start;
-          if (r0 >= 0 && r0 < p.rot_dim) turn_adjacent(a, cs + (r0 >> 1));
-          if (r1 >= 0 && r1 < p.rot_dim) turn_adjacent(b, cs + (r1 >> 1));
-        }
-        *reinterpret_cast<uint4*>(dst + 8 * c0) = pack8(a);
-        *reinterpret_cast<uint4*>(dst + 8 * c1) = pack8(b);
-        continue;
-      }
-    }
     if (pairs) {
       turn_halves(x, y, cs + 8 * u);
     } else if (turns && p.adjacent) {
@@ -225,6 +172,173 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
   }
 }
 
+// ---------------------------------------------------------------- with norms
+struct Eight {
+  float2 v[4];
+};
+__device__ __forceinline__ Eight unpack8(const uint4& w) {
+  return Eight{{f2(bf16_lo(w.x), bf16_hi(w.x)), f2(bf16_lo(w.y), bf16_hi(w.y)), f2(bf16_lo(w.z), bf16_hi(w.z)),
+                f2(bf16_lo(w.w), bf16_hi(w.w))}};
+}
+__device__ __forceinline__ uint4 pack8(const Eight& x) {
+  return make_uint4(pack_bf16(x.v[0].x, x.v[0].y), pack_bf16(x.v[1].x, x.v[1].y), pack_bf16(x.v[2].x, x.v[2].y),
+                    pack_bf16(x.v[3].x, x.v[3].y));
+}
+__device__ __forceinline__ Eight load8(const float* p) {
+  const float4 a = *reinterpret_cast<const float4*>(p), b = *(reinterpret_cast<const float4*>(p) + 1);
+  return Eight{{f2(a.x, a.y), f2(a.z, a.w), f2(b.x, b.y), f2(b.z, b.w)}};
+}
+__device__ __forceinline__ void scale8(Eight& x, float r, const float* w) {
+  const Eight k = load8(w);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x.v[i] = mul2(x.v[i], mul2(k.v[i], f2(r, r)));
+}
+// four pairs of neighbours; their cosines and sines
+__device__ __forceinline__ void turn_neighbours(Eight& x, const float* c, const float* s) {
+  const float4 cc = *reinterpret_cast<const float4*>(c), ss = *reinterpret_cast<const float4*>(s);
+  const float cv[4] = {cc.x, cc.y, cc.z, cc.w}, sv[4] = {ss.x, ss.y, ss.z, ss.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x.v[i] = f2(x.v[i].x * cv[i] - x.v[i].y * sv[i], x.v[i].y * cv[i] + x.v[i].x * sv[i]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kAppendThreads) norm_append_kernel(const __grid_constant__ AppendParams p) {
+  constexpr int UPH = D / 16;  // two-chunk units per head
+  extern __shared__ __align__(16) float planes[];  // cosines [tile][rot_dim / 2], then sines (times rot_scale)
+  const int lb = blockIdx.x / p.tiles, t0 = (blockIdx.x % p.tiles) * p.tile;
+  const int l = lb / p.B, b = lb % p.B;
+  const int h0 = blockIdx.y * p.group, nh = min(p.group, p.heads - h0);
+  const int tb = append_len(p, b);
+  const int cap = p.tail_cap;
+  const int len = p.tail_len[lb];
+  const bool fits = append_fits(p, len, tb);
+  if (blockIdx.y == 0 && t0 == 0 && threadIdx.x == 0 && !p.in_place) p.tail_len_out[lb] = fits ? len + tb : len;
+  const int nt = min(p.tile, tb - t0);
+  if (nt <= 0) return;
+  const int start = p.tail_start ? ((p.tail_start[lb] % cap) + cap) % cap : 0;
+  const uint32_t first = (uint32_t)(((int64_t)start + (fits ? len : 0)) % cap) + t0;  // of a token's slot, before it wraps
+  const int half = p.rot_dim >> 1;
+  float *cosines = planes, *sines = planes + p.tile * half;
+  // a thread's units: unit u of every kAppendThreads / UPH-th head, token after token
+  constexpr int STEP = kAppendThreads / UPH;
+  const int u = threadIdx.x % UPH;
+  const uint16_t* q = p.q + l * p.q_ls + b * p.q_bs + t0 * p.q_ts;
+  const uint16_t* k = p.k + l * p.kv_ls + b * p.kv_bs + t0 * p.kv_ts;
+  const uint16_t* v = p.v + l * p.kv_ls + b * p.kv_bs + t0 * p.kv_ts;
+  uint16_t* qo = p.q_out + l * p.o_ls + b * p.o_bs + t0 * p.o_ts;
+  const int64_t ring = l * p.tail_ls + (int64_t)b * p.Hkv * cap * D;
+  uint16_t *kr = p.k_tail + ring, *vr = p.v_tail + ring;
+  // the unit's chunks of eight coordinates in a head that turns: pairs, or the chunks that do not turn, in two
+  // runs around the rotated ones; a value's, and neighbours' pairs, are chunks u and u + UPH
+  int c0 = u, c1 = u + UPH;
+  bool pairs = false;
+  if (!p.adjacent) {
+    const int rc = half >> 3, a = p.rot_start >> 3;
+    pairs = u < rc;
+    if (pairs) {
+      c0 = a + u;
+      c1 = c0 + rc;
+    } else {
+      c0 = u - rc;
+      c1 = c0 + UPH - rc;
+      if (c0 >= a) c0 += 2 * rc;
+      if (c1 >= a) c1 += 2 * rc;
+    }
+  }
+  c0 *= 8;
+  c1 *= 8;
+  int t = 0, hh = threadIdx.x / UPH;  // token, head of the group
+  auto settle = [&] {
+    while (hh >= p.group) {
+      hh -= p.group;
+      ++t;
+    }
+  };
+  uint4 x = make_uint4(0, 0, 0, 0), y = x;
+  auto ask = [&](uint4& a, uint4& b_) {
+    const int head = h0 + hh;
+    if (t >= nt || hh >= nh) return;
+    const bool query = head < p.Hq, value = head >= p.Hq + p.Hkv;
+    if (!query && !fits) return;
+    const uint16_t* src = query ? q + t * p.q_ts + (int64_t)head * D
+                                : (value ? v : k) + t * p.kv_ts + (int64_t)(head - p.Hq - (value ? p.Hkv : 0)) * D;
+    a = *reinterpret_cast<const uint4*>(src + (value ? 8 * u : c0));
+    b_ = *reinterpret_cast<const uint4*>(src + (value ? 8 * (u + UPH) : c1));
+  };
+  settle();
+  ask(x, y);
+  const int teams = max(1, kAppendThreads / max(half, 1));  // threads of a pair, which share the tokens
+  for (int i = threadIdx.x; i < half * teams; i += kAppendThreads) {
+    const int pair = i % half;
+    const uint64_t frac = turn_fraction(p.inv_freq[pair]);
+    const int32_t* pos = p.positions + ((int64_t)p.pair_axis[pair] * p.B + b) * p.T + t0;
+    for (int t = i / half; t < nt; t += teams) {
+      float s, c;
+      turn_angle(pos[t], frac, &s, &c);
+      cosines[t * half + pair] = c * p.rot_scale;
+      sines[t * half + pair] = s * p.rot_scale;
+    }
+  }
+  if (p.mass && fits && blockIdx.y == 0) clear_mass(p, l, b, len, t0, nt);
+  __syncthreads();
+  const uint32_t team = UPH == 32 ? 0xffffffffu : ((1u << (UPH & 31)) - 1u) << (threadIdx.x & 31 & ~(UPH - 1));
+  const float* wq = p.q_weight;
+  while (t < nt) {
+    const int tt = t, head = h0 + hh;
+    const bool mine = hh < nh && (head < p.Hq || fits);
+    uint4 nx = x, ny = y;
+    hh += STEP;
+    settle();
+    // in place a unit's lanes write what no other unit reads: the next one may be read before
+    ask(nx, ny);
+    if (mine) {
+      const bool query = head < p.Hq, value = head >= p.Hq + p.Hkv;
+      const int kv = head - p.Hq - (value ? p.Hkv : 0);
+      uint32_t slot = first + tt;
+      if (slot >= (uint32_t)cap) slot -= cap;
+      uint16_t* dst = query ? qo + tt * p.o_ts + (int64_t)head * D : (value ? vr : kr) + ((int64_t)kv * cap + slot) * D;
+      if (!value) {
+        const float* weight = query ? wq : p.k_weight;
+        Eight a = unpack8(x), b_ = unpack8(y);
+        if (weight) {  // the same for the UPH neighbouring lanes that hold the head
+          weight += query ? head * p.q_hs : kv * p.k_hs;
+          float2 ss = mul2(a.v[0], a.v[0]);
+#pragma unroll
+          for (int j = 1; j < 4; ++j) ss = fma2(a.v[j], a.v[j], ss);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) ss = fma2(b_.v[j], b_.v[j], ss);
+          float sum = ss.x + ss.y;
+#pragma unroll
+          for (int m = 1; m < UPH; m <<= 1) sum += __shfl_xor_sync(team, sum, m);
+          const float r = rsqrtf(fmaf(sum, 1.f / D, p.eps));
+          scale8(a, r, weight + c0);
+          scale8(b_, r, weight + c1);
+        }
+        if (pairs) {
+          const Eight c = load8(cosines + tt * half + 8 * u), s = load8(sines + tt * half + 8 * u);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 m = mul2(b_.v[j], s.v[j]), o = mul2(a.v[j], s.v[j]);
+            a.v[j] = fma2(a.v[j], c.v[j], f2(-m.x, -m.y));
+            b_.v[j] = fma2(b_.v[j], c.v[j], o);
+          }
+        } else if (p.adjacent) {
+          const int r0 = c0 - p.rot_start, r1 = c1 - p.rot_start;
+          const float *c = cosines + tt * half, *s = sines + tt * half;
+          if (r0 >= 0 && r0 < p.rot_dim) turn_neighbours(a, c + (r0 >> 1), s + (r0 >> 1));
+          if (r1 >= 0 && r1 < p.rot_dim) turn_neighbours(b_, c + (r1 >> 1), s + (r1 >> 1));
+        }
+        x = pack8(a);
+        y = pack8(b_);
+      }
+      *reinterpret_cast<uint4*>(dst + (value ? 8 * u : c0)) = x;
+      *reinterpret_cast<uint4*>(dst + (value ? 8 * (u + UPH) : c1)) = y;
+    }
+    x = nx;
+    y = ny;
+  }
+}
+
 __global__ void append_commit_kernel(const __grid_constant__ AppendParams p) {
   for (int lb = blockIdx.x * blockDim.x + threadIdx.x; lb < p.L * p.B; lb += gridDim.x * blockDim.x) {
     const int len = p.tail_len[lb], tb = append_len(p, lb % p.B);
@@ -232,22 +346,31 @@ __global__ void append_commit_kernel(const __grid_constant__ AppendParams p) {
   }
 }
 
-template <bool NORM>
-static cudaError_t append_launch(const AppendParams& p, cudaStream_t s) {
+cudaError_t launch_append(const AppendParams& p, cudaStream_t s) {
   const dim3 grid((unsigned)((int64_t)p.L * p.B * p.tiles), (p.heads + p.group - 1) / p.group);
   const int smem = p.tile * (p.rot_dim / 2) * (int)sizeof(float2);
   switch (p.D) {
-    case 64: append_kernel<64, NORM><<<grid, kAppendThreads, smem, s>>>(p); break;
-    case 128: append_kernel<128, NORM><<<grid, kAppendThreads, smem, s>>>(p); break;
-    case 256: append_kernel<256, NORM><<<grid, kAppendThreads, smem, s>>>(p); break;
-    case 512: append_kernel<512, NORM><<<grid, kAppendThreads, smem, s>>>(p); break;
+    case 64: append_kernel<64><<<grid, kAppendThreads, smem, s>>>(p); break;
+    case 128: append_kernel<128><<<grid, kAppendThreads, smem, s>>>(p); break;
+    case 256: append_kernel<256><<<grid, kAppendThreads, smem, s>>>(p); break;
+    case 512: append_kernel<512><<<grid, kAppendThreads, smem, s>>>(p); break;
     default: return cudaErrorInvalidValue;
   }
   return cudaGetLastError();
 }
 
-cudaError_t launch_append(const AppendParams& p, cudaStream_t s) { return append_launch<false>(p, s); }
-cudaError_t launch_norm_append(const AppendParams& p, cudaStream_t s) { return append_launch<true>(p, s); }
+cudaError_t launch_norm_append(const AppendParams& p, cudaStream_t s) {
+  const dim3 grid((unsigned)((int64_t)p.L * p.B * p.tiles), (p.heads + p.group - 1) / p.group);
+  const int smem = p.tile * (p.rot_dim / 2) * 2 * (int)sizeof(float);
+  switch (p.D) {
+    case 64: norm_append_kernel<64><<<grid, kAppendThreads, smem, s>>>(p); break;
+    case 128: norm_append_kernel<128><<<grid, kAppendThreads, smem, s>>>(p); break;
+    case 256: norm_append_kernel<256><<<grid, kAppendThreads, smem, s>>>(p); break;
+    case 512: norm_append_kernel<512><<<grid, kAppendThreads, smem, s>>>(p); break;
+    default: return cudaErrorInvalidValue;
+  }
+  return cudaGetLastError();
+}
 
 cudaError_t launch_append_commit(const AppendParams& p, cudaStream_t s) {
   const int n = p.L * p.B;

@@ -241,63 +241,82 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
   }
   float ev = 1.f;  // 2^-(E+1) of the values' scales: weights times scales stay in f16's range
   if constexpr (!DENSE) ev = pow2i(-1 - exp_of(warp_max(ms.red[0][lane < 21 ? lane : 0])));
-  {  // query rows, a warp each; lane holds E coordinates
-    const float sgn = p.sscale < 0.f ? -1.f : 1.f;
-    for (int r = warp; r < kPwRows; r += kPwThreads / 32) {
-      const int row = r0 + r;
-      float x[E];
+  {  // query rows, a warp each, two at a time (one after the other they take 13 us, so 6); lane holds E coordinates
+    constexpr int NW = kPwThreads / 32;
+    const uint32_t flip = p.sscale < 0.f ? 0x80008000u : 0u;
+    const uint32_t sg = DENSE ? 0u : p.kc.signs[lane * E >> 5] >> (lane * E & 31);  // of the lane's coordinates
+    for (int r0_ = warp; r0_ < kPwRows; r0_ += 2 * NW) {
+      uint4 v[2][E / 8];
 #pragma unroll
-      for (int e = 0; e < E; ++e) x[e] = 0.f;
-      if (r < rn) {
-        const uint16_t* qp = p.q + l * p.q_ls + b * p.q_bs + (int64_t)(row / p.G) * p.q_ts +
-                             (int64_t)(h * p.G + row % p.G) * D + lane * E;
+      for (int u = 0; u < 2; ++u) {
+        const int r = r0_ + u * NW, row = r0 + r;
+#pragma unroll
+        for (int e = 0; e < E / 8; ++e) v[u][e] = make_uint4(0, 0, 0, 0);
+        if (r < rn) {
+          const uint4* qp = reinterpret_cast<const uint4*>(p.q + l * p.q_ls + b * p.q_bs + (int64_t)(row / p.G) * p.q_ts +
+                                                           (int64_t)(h * p.G + row % p.G) * D + lane * E);
+#pragma unroll
+          for (int e = 0; e < E / 8; ++e) v[u][e] = __ldg(qp + e);
+        }
+      }
+      float x[2][E];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
 #pragma unroll
         for (int e = 0; e < E; e += 8) {
-          const uint4 v = *reinterpret_cast<const uint4*>(qp + e);
-          const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          const uint32_t w[4] = {v[u][e / 8].x ^ flip, v[u][e / 8].y ^ flip, v[u][e / 8].z ^ flip, v[u][e / 8].w ^ flip};
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            x[e + 2 * k] = bf16_lo(w[k]) * sgn;
-            x[e + 2 * k + 1] = bf16_hi(w[k]) * sgn;
+            x[u][e + 2 * k] = bf16_lo(w[k]);
+            x[u][e + 2 * k + 1] = bf16_hi(w[k]);
           }
         }
-      }
-      float f = fabsf(p.sscale);
-      uint32_t w[E / 2];
+      float f[2] = {fabsf(p.sscale), fabsf(p.sscale)};
+      uint32_t w[2][E / 2];
       if constexpr (DENSE) {
 #pragma unroll
-        for (int e = 0; e < E; e += 2) w[e / 2] = pack2_bf16(x[e], x[e + 1]);
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int e = 0; e < E; e += 2) w[u][e / 2] = pack2_bf16(x[u][e], x[u][e + 1]);
       } else {
+        float mx[2] = {0.f, 0.f};
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
+        for (int u = 0; u < 2; ++u) {
+#pragma unroll
+          for (int e = 0; e < E; ++e) x[u][e] = __uint_as_float(__float_as_uint(x[u][e]) ^ ((sg >> e) << 31));
+          fwht_regs<E>(x[u]);
+          fwht_lanes<E>(x[u], lane, 32);
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            x[u][e] *= inv_sqrt_dim<D>();
+            mx[u] = fmaxf(mx[u], fabsf(x[u][e]));
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const float m = warp_max(mx[u]);
+          const int s = m > 0.f ? 13 - exp_of(m) : 0;
+          const float sc = pow2i(s);
+          f[u] *= pow2i(-15 - s);
+#pragma unroll
+          for (int e = 0; e < E; e += 2) w[u][e / 2] = pack2_f16(x[u][e] * sc, x[u][e + 1] * sc);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const int r = r0_ + u * NW;
+        if (r >= kPwRows) break;
+#pragma unroll
+        for (int e = 0; e < E; e += 8) {
           const int j = lane * E + e;
-          if ((p.kc.signs[j >> 5] >> (j & 31)) & 1u) x[e] = -x[e];
+          *reinterpret_cast<uint4*>(sm + C::Q + (j >> 6) * 8192 + sw128_off(r, (j >> 3) & 7)) =
+              make_uint4(w[u][e / 2], w[u][e / 2 + 1], w[u][e / 2 + 2], w[u][e / 2 + 3]);
         }
-        fwht_regs<E>(x);
-        fwht_lanes<E>(x, lane, 32);
-        float mx = 0.f;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          x[e] *= inv_sqrt_dim<D>();
-          mx = fmaxf(mx, fabsf(x[e]));
+        if (lane == 0) {
+          ms.qf[r] = f[u];
+          ms.ref[r] = -INFINITY;
+          ms.lim[r] = r < rn ? row_limit(p, cl, tb, r0 + r) - base - (LISTED && !DENSE ? 0 : k0) : 0x7FFFFFFF;
         }
-        mx = warp_max(mx);
-        const int s = mx > 0.f ? 13 - exp_of(mx) : 0;
-        const float sc = pow2i(s);
-        f *= pow2i(-15 - s);
-#pragma unroll
-        for (int e = 0; e < E; e += 2) w[e / 2] = pack2_f16(x[e] * sc, x[e + 1] * sc);
-      }
-#pragma unroll
-      for (int e = 0; e < E; e += 8) {
-        const int j = lane * E + e;
-        *reinterpret_cast<uint4*>(sm + C::Q + (j >> 6) * 8192 + sw128_off(r, (j >> 3) & 7)) =
-            make_uint4(w[e / 2], w[e / 2 + 1], w[e / 2 + 2], w[e / 2 + 3]);
-      }
-      if (lane == 0) {
-        ms.qf[r] = f;
-        ms.ref[r] = -INFINITY;
-        ms.lim[r] = r < rn ? row_limit(p, cl, tb, row) - base - (LISTED && !DENSE ? 0 : k0) : 0x7FFFFFFF;
       }
     }
   }
