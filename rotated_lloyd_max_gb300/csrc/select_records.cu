@@ -388,19 +388,25 @@ __device__ __forceinline__ void pick_list(const SelectParams& p, const SelList& 
       __syncthreads();
       const int D = p.q.D, sub = lane & 7, grp = tid >> 3;  // eight lanes a (candidate, row), four of them at a time
       constexpr int NG = T / 8;
-      const int64_t pairs = (int64_t)nc * s.rows;
-      for (int64_t i0 = 0; i0 < pairs; i0 += 4 * NG) {
+      // pair i = candidate i / rows, row i % rows; from one round to the next both move by fixed steps
+      const int stepc = 4 * NG / s.rows, stepr = 4 * NG - stepc * s.rows;
+      int c[4], row[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        c[u] = (u * NG + grp) / s.rows;
+        row[u] = u * NG + grp - c[u] * s.rows;
+      }
+      for (;;) {
         const uint4 *q[4], *bnd[4];
-        int c[4];
         bool far[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const int64_t i = i0 + u * NG + grp;
-          far[u] = i >= pairs;
-          c[u] = far[u] ? 0 : (int)(i / s.rows);
-          q[u] = reinterpret_cast<const uint4*>(query_row(p, s, far[u] ? 0 : (int)(i - (int64_t)c[u] * s.rows)));
-          bnd[u] = reinterpret_cast<const uint4*>(bounds_row(p, s, (int)cand[c[u]]));
+          far[u] = c[u] >= nc;
+          c[u] = min(c[u], nc);
+          q[u] = reinterpret_cast<const uint4*>(query_row(p, s, far[u] ? 0 : row[u]));
+          bnd[u] = reinterpret_cast<const uint4*>(bounds_row(p, s, (int)cand[far[u] ? 0 : c[u]]));
         }
+        if (__all_sync(0xffffffffu, far[0] && far[1] && far[2] && far[3])) break;
         if (s.rows > kPrune) {
           // many rows: their sums in f32 first; a row further than e2 below the record's f32 score is not its maximum
           float f[4] = {0.f, 0.f, 0.f, 0.f};
@@ -420,7 +426,7 @@ __device__ __forceinline__ void pick_list(const SelectParams& p, const SelList& 
           for (int u = 0; u < 4; ++u) {
 #pragma unroll
             for (int k = 1; k < 8; k <<= 1) f[u] += __shfl_xor_sync(0xffffffffu, f[u], k);
-            far[u] = far[u] || f[u] < key_value(keys[cand[c[u]]]) - e2;
+            far[u] = far[u] || f[u] < key_value(keys[cand[c[u]]]) - e2;  // (c is below nc where far is not set)
           }
         }
 #pragma unroll
@@ -445,6 +451,15 @@ __device__ __forceinline__ void pick_list(const SelectParams& p, const SelList& 
           // the order of the pairs (sum to the nearest f32, what is left) is that of the sums
           if (!far[u] && sub == 0 && fabsf(sum.x) < INFINITY)
             atomicMax(exact + c[u], (unsigned long long)order_key(sum.x + 0.f) << 32 | order_key(sum.y + 0.f));
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          c[u] += stepc;
+          row[u] += stepr;
+          if (row[u] >= s.rows) {
+            row[u] -= s.rows;
+            ++c[u];
+          }
         }
       }
       __syncthreads();
