@@ -257,6 +257,7 @@ tq_status sparse_plan(const tq_query_args* a, const tq_record_lists* r, const tq
       if (dense > 0.9 * idle) cost += std::max(rest, (dense - 0.9 * idle) / (double)sms);
       if (cost < best) {
         best = cost;
+        pp.ring = dense > 0.9 * idle;
         pp.cps = (int)per;
         pp.Sc = (int)sc;
         pp.tps = (int)(TQ_CHUNK * per);

@@ -95,8 +95,10 @@ __global__ void __launch_bounds__(kThreads) prefill_merge_kernel(const __grid_co
 // groups of threads, whose sums meet in shared memory (a few rows with many
 // splits would otherwise wait for one load after another: the call for 30 rows of
 // 2 kv heads takes 33 us with SL = 1 and 23 with 8 over 18 splits, 25 and 21 over 7).
+// Of the CTAs with SL = 1 four share an SM, at the cost of a few spilled bytes, so that
+// 512 of them (32768 rows) run at once.
 template <int D, int SL>
-__global__ void __launch_bounds__(256) prefill_merge_tiles_kernel(const __grid_constant__ PrefillParams pp) {
+__global__ void __launch_bounds__(256, SL > 1 ? 1 : 4) prefill_merge_tiles_kernel(const __grid_constant__ PrefillParams pp) {
   constexpr int E = D / 4, ROWS = 256 / (4 * SL);
   __shared__ float part[SL > 1 ? (SL - 1) * 4 * ROWS : 1][E + 1];
   __shared__ float wsum[SL > 1 ? SL * 4 * ROWS : 1];

@@ -806,9 +806,12 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_umma_kernel(const __gri
   pdl_start();
   extern __shared__ __align__(1024) unsigned char smraw[];
   unsigned char* sm = smraw + ((1024u - (smem_u32(smraw) & 1023u)) & 1023u);
-  // records first, the ring's shorter runs behind them
+  // records first, the ring's shorter runs behind them or (listed records, where they would
+  // outlast the last wave's idle slots) before them
   const int64_t U = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv * pp.tiles;
-  const int split = (int)(blockIdx.x / U), tile = (int)(blockIdx.x % U % pp.tiles);
+  int split = (int)(blockIdx.x / U);
+  if (LISTED && pp.ring) split = split < pp.St ? split + pp.Sc : split - pp.St;
+  const int tile = (int)(blockIdx.x % U % pp.tiles);
   const int64_t unit = blockIdx.x % U / pp.tiles;
   if (split < pp.Sc) prefill_umma_body<D, false, CAP, LISTED>(pp, sm, unit, tile, split);
   else prefill_umma_body<D, true, CAP, LISTED>(pp, sm, unit, tile, split - pp.Sc);
