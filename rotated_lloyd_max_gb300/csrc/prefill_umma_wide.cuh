@@ -534,7 +534,7 @@ __device__ __forceinline__ void prefill_wide_body(const PrefillParams& pp, unsig
         *reinterpret_cast<uint4*>(sm + C::P + sw128_off(tok, 4 * hh + j / 8)) = make_uint4(u[0], u[1], u[2], u[3]);
       };
       float over = -INFINITY;
-      const bool plain = !edge && !cap.large;
+      const bool plain = i > 0 && !edge && !cap.large;  // (the first has no references yet)
       if (plain && !capped) {
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
