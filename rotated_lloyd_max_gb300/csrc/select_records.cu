@@ -311,8 +311,8 @@ __device__ __forceinline__ void pick_list(const SelectParams& p, const SelList& 
     __syncthreads();
     if (z - a <= kSearch) {
       // ---------------------------------------------------------- the largest number that need keys reach, four bits at a
-      // time below what all keys have in common: every warp holds all keys and tries one of 16 numbers (a bit at a
-      // time by barriers, or by one warp, takes 2 us, this 0.5)
+      // time below what all keys have in common: every warp holds all keys and tries one of 16 numbers.  Where one is
+      // reached by just `need` keys, the least of those is it.
       static_assert(T == 512, "16 warps");
       uint32_t k[kSearch / 32], most = 0u, least = 0xFFFFFFFFu;
 #pragma unroll
@@ -336,8 +336,20 @@ __device__ __forceinline__ void pick_list(const SelectParams& p, const SelList& 
             n[0] += k[i] >= trial;
             n[1] += k[i + 1] >= trial;
           }
-          const bool reached = (int)__reduce_add_sync(0xffffffffu, (unsigned)(n[0] + n[1])) >= need;
-          x |= (uint32_t)(__syncthreads_count(lane == 0 && reached) - 1) << sh;  // the numbers reached are the lower ones
+          const int reach = (int)__reduce_add_sync(0xffffffffu, (unsigned)(n[0] + n[1]));
+          if (reach == need) {
+            least = 0xFFFFFFFFu;
+#pragma unroll
+            for (int i = 0; i < kSearch / 32; ++i) least = min(least, k[i] >= trial ? k[i] : 0xFFFFFFFFu);
+            least = __reduce_min_sync(0xffffffffu, least);
+            if (lane == 0) ms.x = least;
+          }
+          const int votes = __syncthreads_count(lane == 0 ? reach >= need : reach == need);
+          if (votes >= 31) {
+            x = ms.x;
+            break;
+          }
+          x |= (uint32_t)(votes - 1) << sh;  // the numbers reached are the lower ones
         }
       }
     } else {
