@@ -12,8 +12,11 @@
 // bank conflicts); sums are f32.  At head dim 512 a warp forms half of the outputs
 // (the top k-step bit's sum or difference by the sign of A).
 //
-// A warp takes a record at a time as long as there is one for every warp; those
-// that are left (or all of a short call) are shared by the four warps of a CTA.
+// A warp takes a record at a time as long as there is one for every warp (8192 of
+// 3 bits at head dim 128: 53 us, 64 with four warps a record); those that are left
+// (or all of a short call) are shared by the four warps of a CTA (256 records: 5.2 us,
+// 7.0 a warp each; 512 of head dim 512: 26 and 39).  The instructions bound it, about 2.2
+// a cycle and SM: lookups, butterflies, minima and maxima of 128 d values a record.
 //
 // Codecs with side lists go through f32 butterflies on the CUDA cores, a vector
 // spread over d / 32 lanes as in the decoder, which replaces single coordinates easily.
@@ -53,7 +56,7 @@ __device__ __forceinline__ float min3(float a, float b, float c) {
   asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-__device__ __forceinline__ float max3_(float a, float b, float c) {
+__device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
@@ -125,149 +128,149 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 4 : 3)
   };
 #pragma unroll 1
   for (int team = 0; team < 2; ++team) {  // warps alone, then four together
-  const uint32_t stride = team ? gridDim.x : 4 * gridDim.x, end = team ? tasks : solo;
-  const int tiles = team ? kChunk / 32 : kChunk / 8, first = team ? warp * tiles : 0;
-  Task cur, nxt;
-  cur.q = team ? solo + blockIdx.x : 4 * blockIdx.x + warp;
-  bool more = seek(cur, stride, end);
-  Run<NB> run;
-  float2 nn = f2(0.f, 0.f);
-  if (more) {
-    run.load(cur.rec + (8 * first + g) * ROW, t * RUN * B);
-    nn = __ldg(reinterpret_cast<const float2*>(cur.rec + p.c.off_norm) + 4 * first + t);
-  }
-  for (; more; cur = nxt) {
-    nxt.q = cur.q + stride;
-    nxt.rec = cur.rec;
-    more = seek(nxt, stride, end);
-    const int half = HALVES == 1 ? 0 : (int)(cur.q & 1);
-    const uint8_t* rec = cur.rec;
-    uint32_t sign = 0u;  // of A for the k-steps of the upper half
-    if (HALVES == 2 && half) sign = 0x80008000u;
-    float lo[ACC][2], hi[ACC][2];
-#pragma unroll
-    for (int k = 0; k < ACC; ++k)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        lo[k][e] = INFINITY;
-        hi[k][e] = -INFINITY;
-      }
-    bool bad = false;
-    const uint8_t* row = rec + (8 * first + g) * ROW;
-#pragma unroll 1
-    for (int i = 0; i < tiles; ++i) {
-      float acc[ACC][4];
-      const float2 f = f2(nn.x * p.c.inv_sqrt_d, nn.y * p.c.inv_sqrt_d);
-      bad = bad || !(fabsf(nn.x) < INFINITY) || !(fabsf(nn.y) < INFINITY);
-      const bool last = i + 1 == tiles;
-      const uint8_t* next = last ? nxt.rec + (8 * first + g) * ROW : row + 8 * ROW;
-      nn = __ldg(reinterpret_cast<const float2*>((last ? nxt.rec : rec) + p.c.off_norm) + 4 * (last ? first : first + i + 1) + t);
-#pragma unroll
-      for (int s = 0; s < NS; ++s) {
-        uint32_t w[Run<NB>::NW];
-        run.get((t * RUN + s * STEP) * B, w);
-        run.load(s + 1 < NS ? row : next, (t * RUN + (s + 1 < NS ? s + 1 : 0) * STEP) * B);
-        const bool upper = HALVES == 2 && s >= NS / 2;
-        const uint32_t a[4] = {h16[0] ^ (upper ? sign : 0u), h16[1] ^ (upper ? sign : 0u), h16[2] ^ (upper ? sign : 0u),
-                               h16[3] ^ (upper ? sign : 0u)};
-#pragma unroll
-        for (int k = 0; k < STEP / 4; ++k) {
-          const uint2 e0 = pair_at<B>(tab, sm, w, 4 * k, loff), e1 = pair_at<B>(tab, sm, w, 4 * k + 2, loff);
-          const int kk = s * (STEP / 4) + k;
-          if (kk < ACC) mma_f16_first(acc[kk % ACC], a, e0.x, e1.x);
-          else mma_f16(acc[kk % ACC], a, e0.x, e1.x);
-          mma_f16(acc[kk % ACC], a, e0.y, e1.y);
-        }
-      }
-      // the k-steps' bits
-#pragma unroll
-      for (int m = 1; m < ACC; m <<= 1)
-#pragma unroll
-        for (int k = 0; k < ACC; ++k)
-          if (!(k & m)) {
-#pragma unroll
-            for (int e = 0; e < 4; e += 2) {
-              const float2 x = f2(acc[k][e], acc[k][e + 1]), y = f2(acc[k | m][e], acc[k | m][e + 1]);
-              const float2 u = add2(x, y), v = fma2(y, f2(-1.f, -1.f), x);
-              acc[k][e] = u.x;
-              acc[k][e + 1] = u.y;
-              acc[k | m][e] = v.x;
-              acc[k | m][e + 1] = v.y;
-            }
-          }
+    const uint32_t stride = team ? gridDim.x : 4 * gridDim.x, end = team ? tasks : solo;
+    const int tiles = team ? kChunk / 32 : kChunk / 8, first = team ? warp * tiles : 0;
+    Task cur, nxt;
+    cur.q = team ? solo + blockIdx.x : 4 * blockIdx.x + warp;
+    bool more = seek(cur, stride, end);
+    Run<NB> run;
+    float2 nn = f2(0.f, 0.f);
+    if (more) {
+      run.load(cur.rec + (8 * first + g) * ROW, t * RUN * B);
+      nn = __ldg(reinterpret_cast<const float2*>(cur.rec + p.c.off_norm) + 4 * first + t);
+    }
+    for (; more; cur = nxt) {
+      nxt.q = cur.q + stride;
+      nxt.rec = cur.rec;
+      more = seek(nxt, stride, end);
+      const int half = HALVES == 1 ? 0 : (int)(cur.q & 1);
+      const uint8_t* rec = cur.rec;
+      uint32_t sign = 0u;  // of A for the k-steps of the upper half
+      if (HALVES == 2 && half) sign = 0x80008000u;
+      float lo[ACC][2], hi[ACC][2];
 #pragma unroll
       for (int k = 0; k < ACC; ++k)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const float2 y = mul2(f2(acc[k][2 * e], acc[k][2 * e + 1]), f);
-          lo[k][e] = min3(lo[k][e], y.x, y.y);
-          hi[k][e] = max3_(hi[k][e], y.x, y.y);
+          lo[k][e] = INFINITY;
+          hi[k][e] = -INFINITY;
         }
-      row = next;
-    }
-    // over the four lanes of a quad (tokens), of which lane t keeps k-steps = t modulo 4: half of them go over at
-    // a time; then to the keys' signs and bf16
-    bad = __any_sync(0xffffffffu, bad);
-    if (team) __syncthreads();  // the bounds of the record before are written
-    else __syncwarp();
+      bool bad = false;
+      const uint8_t* row = rec + (8 * first + g) * ROW;
+#pragma unroll 1
+      for (int i = 0; i < tiles; ++i) {
+        float acc[ACC][4];
+        const float2 f = f2(nn.x * p.c.inv_sqrt_d, nn.y * p.c.inv_sqrt_d);
+        bad = bad || !(fabsf(nn.x) < INFINITY) || !(fabsf(nn.y) < INFINITY);
+        const bool last = i + 1 == tiles;
+        const uint8_t* next = last ? nxt.rec + (8 * first + g) * ROW : row + 8 * ROW;
+        nn = __ldg(reinterpret_cast<const float2*>((last ? nxt.rec : rec) + p.c.off_norm) + 4 * (last ? first : first + i + 1) + t);
 #pragma unroll
-    for (int m = 1; m < 4; m <<= 1)
+        for (int s = 0; s < NS; ++s) {
+          uint32_t w[Run<NB>::NW];
+          run.get((t * RUN + s * STEP) * B, w);
+          run.load(s + 1 < NS ? row : next, (t * RUN + (s + 1 < NS ? s + 1 : 0) * STEP) * B);
+          const bool upper = HALVES == 2 && s >= NS / 2;
+          const uint32_t a[4] = {h16[0] ^ (upper ? sign : 0u), h16[1] ^ (upper ? sign : 0u), h16[2] ^ (upper ? sign : 0u),
+                                 h16[3] ^ (upper ? sign : 0u)};
 #pragma unroll
-      for (int k = 0; k < ACC; ++k)
-        if (m == 1 ? !(k & 1) : (k & 3) < 2) {  // after the first round, what a lane keeps lies in even places
-          if (m == 2 && (k & 1)) continue;
-          const int o = k + m;
-          const bool up = (t & m) != 0;
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float x = __shfl_xor_sync(0xffffffffu, up ? lo[k][e] : lo[o][e], m);
-            const float y = __shfl_xor_sync(0xffffffffu, up ? hi[k][e] : hi[o][e], m);
-            lo[k][e] = fminf(up ? lo[o][e] : lo[k][e], x);
-            hi[k][e] = fmaxf(up ? hi[o][e] : hi[k][e], y);
+          for (int k = 0; k < STEP / 4; ++k) {
+            const uint2 e0 = pair_at<B>(tab, sm, w, 4 * k, loff), e1 = pair_at<B>(tab, sm, w, 4 * k + 2, loff);
+            const int kk = s * (STEP / 4) + k;
+            if (kk < ACC) mma_f16_first(acc[kk % ACC], a, e0.x, e1.x);
+            else mma_f16(acc[kk % ACC], a, e0.x, e1.x);
+            mma_f16(acc[kk % ACC], a, e0.y, e1.y);
           }
         }
+        // the k-steps' bits
 #pragma unroll
-    for (int k0 = 0; k0 < ACC; k0 += 4) {
-      const int k = k0 + t;  // the k-step that lane t keeps in place k0
+        for (int m = 1; m < ACC; m <<= 1)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int o = g + 8 * e, c = (o >> 2) * RUN + 4 * (half * ACC + k) + (o & 3);
-        float x = lo[k0][e] * (1.f / 65536.f), y = hi[k0][e] * (1.f / 65536.f);
-        if ((p.c.signs[c >> 5] >> (c & 31)) & 1u) {
-          const float z = x;
-          x = -y;
-          y = -z;
+          for (int k = 0; k < ACC; ++k)
+            if (!(k & m)) {
+#pragma unroll
+              for (int e = 0; e < 4; e += 2) {
+                const float2 x = f2(acc[k][e], acc[k][e + 1]), y = f2(acc[k | m][e], acc[k | m][e + 1]);
+                const float2 u = add2(x, y), v = fma2(y, f2(-1.f, -1.f), x);
+                acc[k][e] = u.x;
+                acc[k][e + 1] = u.y;
+                acc[k | m][e] = v.x;
+                acc[k | m][e + 1] = v.y;
+              }
+            }
+#pragma unroll
+        for (int k = 0; k < ACC; ++k)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float2 y = mul2(f2(acc[k][2 * e], acc[k][2 * e + 1]), f);
+            lo[k][e] = min3(lo[k][e], y.x, y.y);
+            hi[k][e] = max3(hi[k][e], y.x, y.y);
+          }
+        row = next;
+      }
+      // over the four lanes of a quad (tokens), of which lane t keeps k-steps = t modulo 4: half of them go over at
+      // a time; then to the keys' signs and bf16
+      bad = __any_sync(0xffffffffu, bad);
+      if (team) __syncthreads();  // the bounds of the record before are written
+      else __syncwarp();
+#pragma unroll
+      for (int m = 1; m < 4; m <<= 1)
+#pragma unroll
+        for (int k = 0; k < ACC; ++k)
+          if (m == 1 ? !(k & 1) : (k & 3) < 2) {  // after the first round, what a lane keeps lies in even places
+            if (m == 2 && (k & 1)) continue;
+            const int o = k + m;
+            const bool up = (t & m) != 0;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float x = __shfl_xor_sync(0xffffffffu, up ? lo[k][e] : lo[o][e], m);
+              const float y = __shfl_xor_sync(0xffffffffu, up ? hi[k][e] : hi[o][e], m);
+              lo[k][e] = fminf(up ? lo[o][e] : lo[k][e], x);
+              hi[k][e] = fmaxf(up ? hi[o][e] : hi[k][e], y);
+            }
+          }
+#pragma unroll
+      for (int k0 = 0; k0 < ACC; k0 += 4) {
+        const int k = k0 + t;  // the k-step that lane t keeps in place k0
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int o = g + 8 * e, c = (o >> 2) * RUN + 4 * (half * ACC + k) + (o & 3);
+          float x = lo[k0][e] * (1.f / 65536.f), y = hi[k0][e] * (1.f / 65536.f);
+          if ((p.c.signs[c >> 5] >> (c & 31)) & 1u) {
+            const float z = x;
+            x = -y;
+            y = -z;
+          }
+          mine[c] = bound_bits<true>(x, bad);
+          mine[D + c] = bound_bits<false>(y, bad);
         }
-        mine[c] = bound_bits<true>(x, bad);
-        mine[D + c] = bound_bits<false>(y, bad);
+      }
+      uint16_t* out = p.bounds + cur.out;
+      // coordinates come in runs of 4 ACC at steps of RUN: 16-byte chunks
+      constexpr int CH = 4 * ACC / 8;  // chunks of a run
+      auto chunk = [&](int i) { return (i / CH) * (RUN / 8) + half * CH + i % CH; };
+      if (!team) {
+        __syncwarp();
+        for (int i = lane; i < 8 * CH; i += 32) {
+          const int c = chunk(i);
+          reinterpret_cast<uint4*>(out)[c] = reinterpret_cast<const uint4*>(mine)[c];
+        }
+      } else {
+        __syncthreads();
+        for (int i = tid; i < 8 * CH; i += kThreads) {
+          const int c = chunk(i);
+          uint4 v = reinterpret_cast<const uint4*>(sm + BoundsCfg<D, B>::TAB)[c];
+#pragma unroll
+          for (int w = 1; w < 4; ++w) {
+            const uint4 x = reinterpret_cast<const uint4*>(sm + BoundsCfg<D, B>::TAB)[w * (D / 4) + c];
+            v = c < D / 8 ? make_uint4(join2<true>(v.x, x.x), join2<true>(v.y, x.y), join2<true>(v.z, x.z), join2<true>(v.w, x.w))
+                          : make_uint4(join2<false>(v.x, x.x), join2<false>(v.y, x.y), join2<false>(v.z, x.z), join2<false>(v.w, x.w));
+          }
+          reinterpret_cast<uint4*>(out)[c] = v;
+        }
       }
     }
-    uint16_t* out = p.bounds + cur.out;
-    // coordinates come in runs of 4 ACC at steps of RUN: 16-byte chunks
-    constexpr int CH = 4 * ACC / 8;  // chunks of a run
-    auto chunk = [&](int i) { return (i / CH) * (RUN / 8) + half * CH + i % CH; };
-    if (!team) {
-      __syncwarp();
-      for (int i = lane; i < 8 * CH; i += 32) {
-        const int c = chunk(i);
-        reinterpret_cast<uint4*>(out)[c] = reinterpret_cast<const uint4*>(mine)[c];
-      }
-    } else {
-      __syncthreads();
-      for (int i = tid; i < 8 * CH; i += kThreads) {
-        const int c = chunk(i);
-        uint4 v = reinterpret_cast<const uint4*>(sm + BoundsCfg<D, B>::TAB)[c];
-#pragma unroll
-        for (int w = 1; w < 4; ++w) {
-          const uint4 x = reinterpret_cast<const uint4*>(sm + BoundsCfg<D, B>::TAB)[w * (D / 4) + c];
-          v = c < D / 8 ? make_uint4(join2<true>(v.x, x.x), join2<true>(v.y, x.y), join2<true>(v.z, x.z), join2<true>(v.w, x.w))
-                        : make_uint4(join2<false>(v.x, x.x), join2<false>(v.y, x.y), join2<false>(v.z, x.z), join2<false>(v.w, x.w));
-        }
-        reinterpret_cast<uint4*>(out)[c] = v;
-      }
-    }
-  }
-  __syncthreads();
+    __syncthreads();
   }
 }
 

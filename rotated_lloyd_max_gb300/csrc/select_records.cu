@@ -125,7 +125,8 @@ __device__ __forceinline__ void score_step(float (&c)[4], const uint4& u, const 
 // lie in shared memory (64 KB of them at a time).  Up to head dim 128 a warp's bounds stay
 // in registers; the wider ones are read again (from L1) for every 8 NT rows.  The sum of
 // |terms| is bounded by that of |q_j| and the CTA's largest |bound| of coordinate j,
-// formed the same way.  1024 tokens of 32 heads in blocks of 64, 256 records: xx us.
+// formed the same way.  1024 tokens of 32 heads in blocks of 64, 256 records: 21 us of
+// the call's 37, 13 to 16 of them in mma.sync's loop (256 CTAs, two on most SMs).
 template <int D>
 struct ScoreCfg {
   static constexpr bool HELD = D <= 128;
@@ -276,8 +277,12 @@ __device__ __forceinline__ float2 join_exact(float2 a, float2 b) {
   return make_float2(h, __fadd_rn(c, __fsub_rn(s, h)));
 }
 
-constexpr int kPrune = 16;    // query rows from which on the exact scores ask for the f32 ones first
-constexpr int kSearch = 256;  // records up to which a warp's search finds the threshold
+// Query rows above which the exact sums of a row ask for its f32 score first: few rows of a candidate can be its
+// best, many cannot (256 rows of 256 records 42 us without asking, 37 with; 32 lists of 4 rows 12.6 and 13.2).
+constexpr int kPrune = 16;
+// Records up to which the warps search for the threshold in registers; beyond that its bytes are counted, which
+// takes four rounds of shared memory's atomics (2048 lists of 256 records 56 us by search, 68 by counting).
+constexpr int kSearch = 256;
 struct PickMisc {
   uint32_t hist[256];
   uint32_t warp[32];
@@ -332,9 +337,16 @@ __device__ __forceinline__ void pick_list(const SelectParams& p, const SelList& 
           const uint32_t trial = x | (uint32_t)warp << sh;
           int n[2] = {0, 0};
 #pragma unroll
-          for (int i = 0; i < kSearch / 32; i += 2) {
+          for (int i = 0; i < kSearch / 64; i += 2) {
             n[0] += k[i] >= trial;
             n[1] += k[i + 1] >= trial;
+          }
+          if (z - a > kSearch / 2) {
+#pragma unroll
+            for (int i = kSearch / 64; i < kSearch / 32; i += 2) {
+              n[0] += k[i] >= trial;
+              n[1] += k[i + 1] >= trial;
+            }
           }
           const int reach = (int)__reduce_add_sync(0xffffffffu, (unsigned)(n[0] + n[1]));
           if (reach == need) {

@@ -365,8 +365,8 @@ __device__ __forceinline__ void few_ring(const PrefillParams& pp, const uint2* q
   const uint16_t *kt = p.ktail + ring, *vt = p.vtail + ring;
   // clamped to the last token: its values are finite, its weights zero
   auto row = [&](int tok) {
-    int s = start + min(tok, len - 1);
-    if (s >= p.tail_cap) s -= p.tail_cap;
+    uint32_t s = (uint32_t)start + (uint32_t)min(tok, len - 1);  // (up to twice the capacity: 32 bits)
+    if (s >= (uint32_t)p.tail_cap) s -= (uint32_t)p.tail_cap;
     return (int64_t)s * D;
   };
 #pragma unroll 1
@@ -552,7 +552,8 @@ __device__ __forceinline__ void few_segment(const PrefillParams& pp, const unsig
   FewState<D, NT> st;
   st.init();
   if (dense) {
-    const int cap = p.tail_cap, start = p.tail_start ? ((p.tail_start[lb] % cap) + cap) % cap : 0;
+    int start = p.tail_start ? p.tail_start[lb] % p.tail_cap : 0;
+    if (start < 0) start += p.tail_cap;
     few_ring<D, NT>(pp, reinterpret_cast<const uint2*>(sm + C::QF), t0, t1, cl.len, l, b, h, start, qf, lim, low, st);
   } else {
     few_records<D, KB, VB, NT>(pp, tables, sm, ids, n, l, b, h, qf, lim, low, st);

@@ -137,6 +137,41 @@ def test_captured_and_replayed(tq, orc):
     assert torch.equal(out, eager)
 
 
+@pytest.mark.parametrize("d,B,n", [(64, 4, 100), (512, 3, 90)])
+def test_more_records_than_warps_at_work(tq, orc, d, B, n):
+    """Enough records for a warp each, and some that are left; every one as in a call of its own sequence and few
+    records, every fiftieth against the oracle."""
+    import torch
+    Hkv = 8
+    c = Cache(tq, orc, B=B, Hkv=Hkv, d=d, kb=3, vb=1, n=n, seed=37)
+    bounds, few = place(c), place(c)
+    tq.key_bounds(k_codec=c.kc, k_rec=c.rec["k"], bounds=bounds, n_chunks=c.d_n, max_chunks=n)
+    for r in range(0, n, 30):  # 30 records of every sequence at a time
+        tq.key_bounds(k_codec=c.kc, k_rec=c.rec["k"], bounds=few, n_chunks=c.d_n, max_chunks=n, max_new=30,
+                      first=torch.full((1, B), r, dtype=torch.int32, device="cuda"))
+    assert torch.equal(bounds.view(torch.int16), few.view(torch.int16))
+    for i, (b, h, r) in enumerate(np.ndindex(B, Hkv, n)):
+        if i % 50 == 0 and r < c.n[0, b]:
+            check(c, bounds, 0, b, h, r)
+        elif r >= c.n[0, b] and h == 0:
+            assert torch.all(bounds[0, b, :, r] == 7.0)
+
+
+def test_records_and_bounds_past_32_bits_of_their_pools(tq, orc):
+    import torch
+    c = Cache(tq, orc, B=2, Hkv=1, d=512, kb=1, vb=1, n=3, paged=True, seed=38)
+    near, pool = place(c), c.rec["k"]
+    kw = dict(k_codec=c.kc, n_chunks=c.d_n, max_chunks=3)
+    tq.key_bounds(k_rec=pool, bounds=near, block_table=c.table, **kw)
+    blocks = (1 << 32) // 2048 + 50  # a record's bounds are 2048 bytes, and it more
+    far = torch.empty((1, blocks, 1, pool.shape[-1]), dtype=torch.uint8, device="cuda")
+    far[:, -pool.shape[1]:] = pool
+    out = torch.empty((1, blocks, 1, 2, 512), dtype=torch.bfloat16, device="cuda")
+    out[:, -pool.shape[1]:] = 7.0
+    tq.key_bounds(k_rec=far, bounds=out, block_table=c.table + (blocks - pool.shape[1]), **kw)
+    assert torch.equal(out[:, -pool.shape[1]:], near)
+
+
 def test_a_codec_of_another_size_is_refused(tq, orc):
     c = Cache(tq, orc, B=1, Hkv=1, d=128, kb=4, vb=4, n=2, seed=36)
     a = tq.make_bounds_args(k_rec=c.rec["k"], bounds=place(c), n_chunks=c.d_n, max_chunks=2)

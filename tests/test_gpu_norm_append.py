@@ -34,6 +34,10 @@ CASES = [  # d, rot, rs, adjacent, L, B, T, Hkv, G, far, scale, sides, per head,
     (512, 64, 448, False, 1, 2, 4, 1, 16, 70000, 1.25, "qk", False, 1e-6),
     (128, 48, 16, False, 2, 2, 130, 1, 2, 4000, 1.0, "qk", True, 1e-6),
     (64, 0, 0, False, 1, 2, 4, 2, 2, 10, 1.0, "qk", False, 1e-6),
+    (64, 64, 0, False, 2, 2, 1211, 1, 2, 5000, 1.0, "qk", True, 1e-6),  # tokens enough for eight a CTA
+    (128, 96, 32, True, 1, 3, 811, 2, 3, 5000, 1.0, "k", False, 1e-6),
+    (256, 128, 0, False, 1, 1, 2437, 1, 1, 5000, 1.0, "q", False, 1e-6),
+    (512, 64, 448, True, 1, 2, 1217, 1, 2, 5000, 1.0, "qk", False, 1e-6),
 ]
 
 

@@ -130,6 +130,13 @@ CASES = {
     "not_causal": dict(T=300, qb=64, tail=20, n=12, keep=4, G=2, causal=False),
     "block_longer_than_the_queries": dict(T=5, qb=64, G=7, n=20),
     "rows_past_a_tile": dict(T=41, qb=41, G=7, n=100, keep=20, B=1),
+    "eight_rows_of_256": dict(n=256, G=8, keep=32, B=1),
+    "nine_rows_of_256": dict(n=256, G=9, keep=32, B=1),
+    "eight_rows_of_257": dict(n=257, G=8, keep=32, B=1, Hkv=1),
+    "most_but_one": dict(n=257, G=4, keep=256, B=1, sink=0, recent=0),
+    "one_of_many": dict(n=256, G=4, keep=1, B=1, sink=0, recent=0),
+    "many_decided_by_few": dict(n=300, G=4, keep=290, B=1, sink=280, recent=8),
+    "sixteen_and_seventeen_rows": dict(T=33, qb=16, G=1, n=140, keep=20, B=1, sink=0),
     "more_queries_than_tokens": dict(T=200, qb=16, tail=3, n=1, keep=2, B=1, sink=0),
 }
 
@@ -202,6 +209,59 @@ def test_captured_and_replayed_with_another_calls_workspace(tq):
         torch.cuda.synchronize()
         np.testing.assert_array_equal(c.list.cpu().numpy(), eager[0])
         np.testing.assert_array_equal(c.count.cpu().numpy(), eager[1])
+
+
+@pytest.mark.parametrize("n", [200, 400])
+@pytest.mark.parametrize("raw", [False, True])
+def test_a_dropped_workspace_is_not_handed_out_under_the_call(tq, n, raw):
+    """A call queued on a busy side stream; its workspace is dropped and memory of its size is filled meanwhile."""
+    import torch
+    c = Case(seed=14, n=n, T=4, qb=2, G=5)
+    ref = c.run(tq)
+    need = tq.tq_select_records_workspace_size(tq.make_select_args(**c.kw))
+    c.list.fill_(5)
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    tq.select_records(stream=side.cuda_stream if raw else side, **c.kw)
+    junk = [torch.full((max(need, 1),), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(c.list.cpu().numpy(), ref[0])
+    assert len(junk) == 4
+
+
+@pytest.mark.parametrize("n,qb", [(200, 1), (400, 2)])
+def test_two_calls_at_once(tq, n, qb):
+    """Calls of two streams, each with its own workspace: both as if alone."""
+    import torch
+    cs = [Case(seed=s, n=n, T=8, qb=qb, G=6) for s in (15, 16)]
+    alone = [c.run(tq)[0] for c in cs]
+    outs = [[torch.empty_like(c.list) for _ in range(8)] for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for k in range(8):
+        for c, o, s in zip(cs, outs, streams):
+            with torch.cuda.stream(s):
+                tq.select_records(**{**c.kw, "list": o[k]})
+    torch.cuda.synchronize()
+    for o, a in zip(outs, alone):
+        for x in o:
+            np.testing.assert_array_equal(x.cpu().numpy(), a)
+
+
+@pytest.mark.parametrize("n", [200, 300])
+def test_bounds_past_32_bits_of_their_pool(tq, n):
+    import torch
+    c = Case(seed=17, d=512, Hkv=1, G=3, n=n, paged=True)
+    near = c.run(tq)[0]
+    pool = c.kw["bounds"]
+    blocks = (1 << 32) // 2048 + 50
+    far = torch.empty((1, blocks + pool.shape[1], 1, 2, 512), dtype=torch.bfloat16, device="cuda")
+    far[:, blocks:] = pool
+    c.list.fill_(5)
+    tq.select_records(**{**c.kw, "bounds": far, "block_table": c.kw["block_table"] + blocks})
+    np.testing.assert_array_equal(c.list.cpu().numpy(), near)
 
 
 def test_strided_and_broadcast_queries(tq):

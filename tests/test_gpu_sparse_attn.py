@@ -139,6 +139,9 @@ CASES = {
     "queries_in_the_records_blocks": dict(d=128, G=3, T=200, qb=50, n=4, keep=3, tail=60),
     "queries_in_the_records_d256": dict(d=256, G=3, T=200, qb=50, n=4, keep=3, tail=60),
     "long_ring": dict(d=128, G=4, T=2, n=2, keep=1, tail=700),
+    "long_lists_d64": dict(d=64, G=2, T=2, n=300, keep=290, Hkv=1, lens=[2, 1]),
+    "long_lists_blocks_d64": dict(d=64, G=10, T=4, qb=2, n=300, keep=290, Hkv=1, B=1),
+    "long_lists_d256": dict(d=256, G=3, T=1, n=270, keep=265, Hkv=1, B=1, kb=2, shared=True),
 }
 
 
@@ -356,6 +359,70 @@ def test_captured_and_replayed(tq, orc, name):
         g.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, eager)
+
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("name", ROUTES)
+def test_a_dropped_workspace_is_not_handed_out_under_the_call(tq, orc, name, raw):
+    """A call queued on a busy side stream; its workspace is dropped and memory of its size is filled meanwhile."""
+    import torch
+    r = ROUTES[name]
+    c = Cache(tq, orc, B=1, Hkv=2, d=r["d"], kb=4, vb=4, n=16, tail=40, seed=30)
+    q = tl.to_bf16_tensor(queries(1, 1, r["T"], 2 * r["G"], r["d"], 31), "cuda")
+    ls = [torch.from_numpy(x).cuda() for x in lists(c, r["T"], r["qb"], 12, 32)]
+    ref, out = torch.zeros_like(q), torch.zeros_like(q)
+    kw = dict(k_codec=c.kc, v_codec=c.vc, q=q, scale=1.0, list=ls[0], count=ls[1], q_block=r["qb"], **c.kw())
+    need = tq.sparse_attn(out=ref, **kw).numel()
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+    tq.sparse_attn(out=out, stream=side.cuda_stream if raw else side, **kw)
+    junk = [torch.full((need,), 255, dtype=torch.uint8, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(out, ref) and len(junk) == 4
+
+
+@pytest.mark.parametrize("name", ROUTES)
+def test_two_calls_at_once(tq, orc, name):
+    """Calls of two streams over one cache, each with its own workspace: both as if alone."""
+    import torch
+    r = ROUTES[name]
+    c = Cache(tq, orc, B=2, Hkv=2, d=r["d"], kb=4, vb=3, n=30, tail=64, seed=33)
+    qs = [tl.to_bf16_tensor(queries(1, 2, r["T"], 2 * r["G"], r["d"], s), "cuda") for s in (34, 35)]
+    ls = [[torch.from_numpy(x).cuda() for x in lists(c, r["T"], r["qb"], 20, s)] for s in (36, 37)]
+    call = lambda i, out: tq.sparse_attn(k_codec=c.kc, v_codec=c.vc, q=qs[i], out=out, scale=1.0, list=ls[i][0],  # noqa: E731
+                                         count=ls[i][1], q_block=r["qb"], **c.kw())
+    alone = [torch.zeros_like(q) for q in qs]
+    for i in range(2):
+        call(i, alone[i])
+    outs = [[torch.zeros_like(qs[i]) for _ in range(8)] for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for k in range(8):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                call(i, outs[i][k])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, alone[i]) for i in range(2) for o in outs[i])
+
+
+@pytest.mark.parametrize("name", ROUTES)
+def test_records_past_32_bits_of_a_pool(tq, orc, name):
+    """Pages more than 2^32 bytes into their pool."""
+    import torch
+    r = ROUTES[name]
+    c = Cache(tq, orc, B=2, Hkv=1, d=r["d"], kb=4, vb=4, n=4, tail=30, shared=True, paged=True, seed=38)
+    q = queries(1, 2, r["T"], r["G"], r["d"], 39)
+    ls = lists(c, r["T"], r["qb"], 3, 40)
+    near = run(tq, c, q, ls, r["qb"])
+    pool = c.rec["k"]
+    blocks = (1 << 32) // pool.shape[-1] + 100
+    far = torch.empty((1, blocks, 1, pool.shape[-1]), dtype=torch.uint8, device="cuda")
+    far[:, -pool.shape[1]:] = pool
+    c.rec = dict(k=far, v=far)
+    c.table = c.table + (blocks - pool.shape[1])
+    assert torch.equal(run(tq, c, q, ls, r["qb"]), near)
 
 
 def test_lists_of_another_shape_are_refused(tq, orc):
