@@ -153,10 +153,16 @@ tq_status select_plan(const tq_select_args* a, SelectPlan* pl) {
   p.tile = 128;  // 16 records a warp (select_records.cu)
   p.tiles = (int)std::max<int64_t>(1, cdiv(q.max_chunks, p.tile));
   const double lists = (double)q.L * q.B * q.Hkv * p.blocks;
-  if (lists * p.tiles > 2147483647.0) return TQ_ERR_UNSUPPORTED;
+  // A list's rows are cut into at most 16 parts, of 32 rows or more; few lists share their parts among CTAs.
+  const int rows = p.qb * q.G;
+  p.part = (int)cdiv(cdiv(rows, 16), 32) * 32;
+  p.parts = (int)cdiv(rows, p.part);
+  p.share = (int)cdiv(p.parts, std::max<int64_t>(1, (int64_t)(2.0 * sm_count() / (lists * p.tiles))));
+  p.shares = (int)cdiv(p.parts, p.share);
+  if (lists * p.tiles * p.shares > 2147483647.0) return TQ_ERR_UNSUPPORTED;
   const size_t n = (size_t)lists;
-  pl->limits = pad256(n * q.max_chunks * 4);
-  pl->exact = pl->limits + pad256(n * p.tiles * 4);
+  pl->limits = pad256(n * p.parts * q.max_chunks * 4);
+  pl->exact = pl->limits + pad256(n * p.tiles * p.shares * 4);
   pl->bytes = pl->exact + pad256(n * q.max_chunks * 8) + 256;
   return TQ_OK;
 }

@@ -121,9 +121,11 @@ struct SelectParams {
   int32_t* list;
   int32_t* count;
   // workspace
-  int tiles, tile;    // CTAs of a list's scores; records of one
-  float* scores;      // [lists][max_chunks]
-  float* limits;      // [lists][tiles]: the largest sum of a row's |terms|
+  int tiles, tile;    // tiles of a list's records; records of one
+  int part, parts;    // query rows whose largest score is kept, and of those parts a list's
+  int shares, share;  // CTAs of a tile, and parts of one
+  float* scores;      // [lists][parts][max_chunks]
+  float* limits;      // [lists][tiles][shares]: the largest sum of a row's |terms|
   uint64_t* exact;    // [lists][max_chunks]
 };
 

@@ -141,12 +141,13 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_scores_kernel(const __g
   __shared__ uint4 top[kSelThreads / 32][D / 8];  // the warps' largest |bound| by coordinate
   __shared__ float red[kSelThreads / 32];
   pdl_start();
-  const int64_t list = blockIdx.x / p.tiles;
-  const int tile = (int)(blockIdx.x % p.tiles);
+  const int64_t at = blockIdx.x / p.shares, list = at / p.tiles;
+  const int tile = (int)(at % p.tiles);
   const SelList s = select_list(p, list);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
   const int c0 = tile * p.tile, c1 = min(c0 + p.tile, s.m), c = c0 + 16 * warp;
-  if (c0 >= c1 || s.m <= p.keep) return;  // nothing here, or all of them are chosen
+  const int first = (int)(blockIdx.x % p.shares) * p.share * p.part, end = min(first + p.share * p.part, s.rows);
+  if (c0 >= c1 || s.m <= p.keep || first >= end) return;  // nothing here, or all of them are chosen
   const uint4* rows[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) rows[i] = reinterpret_cast<const uint4*>(bounds_row(p, s, min(c + 8 * i + g, c1 - 1))) + t;
@@ -179,12 +180,14 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_scores_kernel(const __g
     if (g == 0) top[warp][4 * k + t] = m;
   }
   float best[2] = {-INFINITY, -INFINITY}, size[2] = {0.f, 0.f};
-  for (int r0 = 0; r0 < s.rows; r0 += C::ROWS) {
-    const int nr = min(C::ROWS, s.rows - r0);
-    if (r0) __syncthreads();
+  int left = p.part;  // rows to the end of a part
+  float* scores = p.scores + (list * p.parts + first / p.part) * p.q.max_chunks + c + g;
+  for (int r0 = first; r0 < end; r0 += C::ROWS) {
+    const int nr = min(C::ROWS, end - r0);
+    if (r0 != first) __syncthreads();
     query_fragments<D, kSelThreads>(p, s, r0, nr, frag);
     __syncthreads();
-    if (r0 == 0) {  // of all the warps'
+    if (r0 == first) {  // of all the warps'
       if (threadIdx.x < D / 2) {
         uint32_t m = 0u;
         for (int w = 0; w < kSelThreads / 32; ++w) m = __vmaxu2(m, reinterpret_cast<const uint32_t*>(top[w])[threadIdx.x]);
@@ -220,6 +223,18 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_scores_kernel(const __g
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) keep_best(best, acc[nt], n0 + 8 * nt + 2 * t, nr);
+        left -= 8 * NT;
+        if (left == 0 || r0 + n0 + 8 * NT >= end) {  // parts are a multiple of 8 NT rows
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], 1));
+            best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], 2));
+            if (t == 0 && c + 8 * i + g < c1) scores[8 * i] = best[i];
+            best[i] = -INFINITY;
+          }
+          left = p.part;
+          scores += p.q.max_chunks;
+        }
       }
     }
     // the rows' sizes, a warp every eighth n-tile
@@ -234,20 +249,13 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_scores_kernel(const __g
       keep_best(size, acc, n0 + 2 * t, nr);
     }
   }
-#pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], 1));
-    best[i] = fmaxf(best[i], __shfl_xor_sync(0xffffffffu, best[i], 2));
-    const int r = c + 8 * i + g;
-    if (t == 0 && r < c1) p.scores[list * p.q.max_chunks + r] = best[i];
-  }
   const float sz = warp_max(size[0]);
   if (lane == 0) red[warp] = sz;
   __syncthreads();
   if (threadIdx.x == 0) {
     float m = 0.f;
     for (int w = 0; w < kSelThreads / 32; ++w) m = fmaxf(m, red[w]);
-    p.limits[list * p.tiles + tile] = m;
+    p.limits[blockIdx.x] = m;
   }
 }
 
@@ -286,7 +294,8 @@ constexpr int kSearch = 256;
 struct PickMisc {
   uint32_t hist[256];
   uint32_t warp[32];
-  uint32_t x, prefix, left, above, cand;
+  uint32_t x, prefix, left, above, cand, items;
+  uint32_t item[512];  // candidates' parts that may hold their best row: index << 4 | part
 };
 
 // The list of one block from its keys (smem, one a record), of T threads.  e2: twice the error of a score.
@@ -412,25 +421,40 @@ __device__ __forceinline__ void pick_list(const SelectParams& p, const SelList& 
       __syncthreads();
       const int D = p.q.D, sub = lane & 7, grp = tid >> 3;  // eight lanes a (candidate, row), four of them at a time
       constexpr int NG = T / 8;
-      // pair i = candidate i / rows, row i % rows; from one round to the next both move by fixed steps
-      const int stepc = 4 * NG / s.rows, stepr = 4 * NG - stepc * s.rows;
-      int c[4], row[4];
+      for (int c0 = 0; c0 < nc; c0 += T / 16) {  // 32 candidates with up to 16 parts at a time
+      if (tid == 0) ms.items = 0u;
+      __syncthreads();
+      {
+        const int i = c0 + (tid >> 4), part = tid & 15;
+        if (i < nc && part < p.parts && part * p.part < s.rows &&
+            (p.parts == 1 ||
+             !(__ldcg(p.scores + (list * p.parts + part) * M + cand[i]) < key_value(keys[cand[i]]) - e2)))
+          ms.item[atomicAdd(&ms.items, 1u)] = (uint32_t)i << 4 | (uint32_t)part;
+      }
+      __syncthreads();
+      const int ni = (int)ms.items, per = min(p.part, s.rows);
+      // pair i = item i / per, row i % per of its part; from one round to the next both move by fixed steps
+      const int stepi = 4 * NG / per, stepr = 4 * NG - stepi * per;
+      int it[4], row[4];
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
-        c[u] = (u * NG + grp) / s.rows;
-        row[u] = u * NG + grp - c[u] * s.rows;
+        it[u] = (u * NG + grp) / per;
+        row[u] = u * NG + grp - it[u] * per;
       }
       for (;;) {
         const uint4 *q[4], *bnd[4];
         bool far[4];
+        int c[4];
+        if (__all_sync(0xffffffffu, it[0] >= ni)) break;  // (the others are further)
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          far[u] = c[u] >= nc;
-          c[u] = min(c[u], nc);
-          q[u] = reinterpret_cast<const uint4*>(query_row(p, s, far[u] ? 0 : row[u]));
-          bnd[u] = reinterpret_cast<const uint4*>(bounds_row(p, s, (int)cand[far[u] ? 0 : c[u]]));
+          const uint32_t e = ms.item[min(it[u], ni - 1)];
+          const int r = (int)(e & 15u) * p.part + row[u];
+          c[u] = (int)(e >> 4);
+          far[u] = it[u] >= ni || r >= s.rows;
+          q[u] = reinterpret_cast<const uint4*>(query_row(p, s, far[u] ? 0 : r));
+          bnd[u] = reinterpret_cast<const uint4*>(bounds_row(p, s, (int)cand[c[u]]));
         }
-        if (__all_sync(0xffffffffu, far[0] && far[1] && far[2] && far[3])) break;
         if (s.rows > kPrune) {
           // many rows: their sums in f32 first; a row further than e2 below the record's f32 score is not its maximum
           float f[4] = {0.f, 0.f, 0.f, 0.f};
@@ -450,7 +474,7 @@ __device__ __forceinline__ void pick_list(const SelectParams& p, const SelList& 
           for (int u = 0; u < 4; ++u) {
 #pragma unroll
             for (int k = 1; k < 8; k <<= 1) f[u] += __shfl_xor_sync(0xffffffffu, f[u], k);
-            far[u] = far[u] || f[u] < key_value(keys[cand[c[u]]]) - e2;  // (c is below nc where far is not set)
+            far[u] = far[u] || f[u] < key_value(keys[cand[c[u]]]) - e2;
           }
         }
 #pragma unroll
@@ -478,13 +502,15 @@ __device__ __forceinline__ void pick_list(const SelectParams& p, const SelList& 
         }
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          c[u] += stepc;
+          it[u] += stepi;
           row[u] += stepr;
-          if (row[u] >= s.rows) {
-            row[u] -= s.rows;
-            ++c[u];
+          if (row[u] >= per) {
+            row[u] -= per;
+            ++it[u];
           }
         }
+      }
+      __syncthreads();
       }
       __syncthreads();
       for (int i = tid; i < nc; i += T) {
@@ -541,11 +567,20 @@ __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const __grid_
   const SelList s = select_list(p, list);
   if (list_is_all<kPickThreads>(p, s, list)) return;
   const int M = p.q.max_chunks, lane = threadIdx.x & 31, Mp = (M + 3) & ~3;
-  const float* score = p.scores + list * M;
-  for (int i = threadIdx.x; i < s.m; i += kPickThreads) keys[i] = order_key(__ldcg(score + i));
+  const float* score = p.scores + list * p.parts * M;
+  const int parts = (s.rows + p.part - 1) / p.part, shares = (parts + p.share - 1) / p.share;
+  for (int i = threadIdx.x; i < s.m; i += kPickThreads) {
+    float v[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = k < parts ? __ldcg(score + (int64_t)k * M + i) : -INFINITY;
+#pragma unroll
+    for (int k = 1; k < 16; ++k) v[0] = fmaxf(v[0], v[k]);
+    keys[i] = order_key(v[0]);
+  }
   float bm = 0.f;
-  const int used = (s.m + p.tile - 1) / p.tile;
-  for (int i = lane; i < used; i += 32) bm = fmaxf(bm, __ldcg(p.limits + list * p.tiles + i));
+  const int used = (s.m + p.tile - 1) / p.tile * p.shares;
+  for (int i = lane; i < used; i += 32)
+    if (i % p.shares < shares) bm = fmaxf(bm, __ldcg(p.limits + list * p.tiles * p.shares + i));
   const float e2 = score_error2(p.q.D, warp_max(bm));
   pick_list<kPickThreads>(p, s, list, keys, keys + Mp, keys + 2 * Mp, ms, e2);
 }
@@ -624,7 +659,7 @@ template <int D>
 static cudaError_t scores_launch(const SelectParams& p, int64_t lists, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(select_scores_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, ScoreCfg<D>::SMEM);
   if (e != cudaSuccess) return e;
-  select_scores_kernel<D><<<(unsigned)(lists * p.tiles), kSelThreads, ScoreCfg<D>::SMEM, s>>>(p);
+  select_scores_kernel<D><<<(unsigned)(lists * p.tiles * p.shares), kSelThreads, ScoreCfg<D>::SMEM, s>>>(p);
   return cudaGetLastError();
 }
 
