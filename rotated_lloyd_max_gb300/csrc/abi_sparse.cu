@@ -153,9 +153,9 @@ tq_status select_plan(const tq_select_args* a, SelectPlan* pl) {
   p.tile = 128;  // 16 records a warp (select_records.cu)
   p.tiles = (int)std::max<int64_t>(1, cdiv(q.max_chunks, p.tile));
   const double lists = (double)q.L * q.B * q.Hkv * p.blocks;
-  // A list's rows are cut into at most 16 parts, of 32 rows or more; few lists share their parts among CTAs.
+  // A list's rows are cut into at most 64 parts, of 32 rows or more; few lists share their parts among CTAs.
   const int rows = p.qb * q.G;
-  p.part = (int)cdiv(cdiv(rows, 16), 32) * 32;
+  p.part = (int)cdiv(cdiv(rows, 64), 32) * 32;
   p.parts = (int)cdiv(rows, p.part);
   p.share = (int)cdiv(p.parts, std::max<int64_t>(1, (int64_t)(2.0 * sm_count() / (lists * p.tiles))));
   p.shares = (int)cdiv(p.parts, p.share);

@@ -295,7 +295,7 @@ struct PickMisc {
   uint32_t hist[256];
   uint32_t warp[32];
   uint32_t x, prefix, left, above, cand, items;
-  uint32_t item[512];  // candidates' parts that may hold their best row: index << 4 | part
+  uint32_t item[512];  // candidates' parts that may hold their best row: index << 6 | part
 };
 
 // The list of one block from its keys (smem, one a record), of T threads.  e2: twice the error of a score.
@@ -421,15 +421,15 @@ __device__ __forceinline__ void pick_list(const SelectParams& p, const SelList& 
       __syncthreads();
       const int D = p.q.D, sub = lane & 7, grp = tid >> 3;  // eight lanes a (candidate, row), four of them at a time
       constexpr int NG = T / 8;
-      for (int c0 = 0; c0 < nc; c0 += T / 16) {  // 32 candidates with up to 16 parts at a time
+      for (int c0 = 0; c0 < nc; c0 += T / 64) {  // eight candidates with up to 64 parts at a time
       if (tid == 0) ms.items = 0u;
       __syncthreads();
       {
-        const int i = c0 + (tid >> 4), part = tid & 15;
+        const int i = c0 + (tid >> 6), part = tid & 63;
         if (i < nc && part < p.parts && part * p.part < s.rows &&
             (p.parts == 1 ||
              !(__ldcg(p.scores + (list * p.parts + part) * M + cand[i]) < key_value(keys[cand[i]]) - e2)))
-          ms.item[atomicAdd(&ms.items, 1u)] = (uint32_t)i << 4 | (uint32_t)part;
+          ms.item[atomicAdd(&ms.items, 1u)] = (uint32_t)i << 6 | (uint32_t)part;
       }
       __syncthreads();
       const int ni = (int)ms.items, per = min(p.part, s.rows);
@@ -449,8 +449,8 @@ __device__ __forceinline__ void pick_list(const SelectParams& p, const SelList& 
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const uint32_t e = ms.item[min(it[u], ni - 1)];
-          const int r = (int)(e & 15u) * p.part + row[u];
-          c[u] = (int)(e >> 4);
+          const int r = (int)(e & 63u) * p.part + row[u];
+          c[u] = (int)(e >> 6);
           far[u] = it[u] >= ni || r >= s.rows;
           q[u] = reinterpret_cast<const uint4*>(query_row(p, s, far[u] ? 0 : r));
           bnd[u] = reinterpret_cast<const uint4*>(bounds_row(p, s, (int)cand[c[u]]));
@@ -570,12 +570,15 @@ __global__ void __launch_bounds__(kPickThreads) select_pick_kernel(const __grid_
   const float* score = p.scores + list * p.parts * M;
   const int parts = (s.rows + p.part - 1) / p.part, shares = (parts + p.share - 1) / p.share;
   for (int i = threadIdx.x; i < s.m; i += kPickThreads) {
-    float v[16];
+    float best = -INFINITY;
+    for (int k0 = 0; k0 < parts; k0 += 8) {
+      float v[8];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) v[k] = k < parts ? __ldcg(score + (int64_t)k * M + i) : -INFINITY;
+      for (int k = 0; k < 8; ++k) v[k] = k0 + k < parts ? __ldcg(score + (int64_t)(k0 + k) * M + i) : -INFINITY;
 #pragma unroll
-    for (int k = 1; k < 16; ++k) v[0] = fmaxf(v[0], v[k]);
-    keys[i] = order_key(v[0]);
+      for (int k = 0; k < 8; ++k) best = fmaxf(best, v[k]);
+    }
+    keys[i] = order_key(best);
   }
   float bm = 0.f;
   const int used = (s.m + p.tile - 1) / p.tile * p.shares;
