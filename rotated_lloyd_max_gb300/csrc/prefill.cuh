@@ -34,12 +34,22 @@ struct PrefillParams {
 };
 
 // The records of a row tile's split: c0, c0 + 1, .., or (LISTED) the entries c0,
-// c0 + 1, .. of its list, of which those that name no record stand for record 0
-// with no token seen.
+// c0 + 1, .. of its list, of which those that name no record stand for the run's
+// first that does (its values are finite, as weights of zero need them) with no token seen.
 struct RecordRun {
   const int32_t* list;
-  int c0, n;  // first record or entry; records of the sequence
+  int c0, n, stand;  // first record or entry; records of the sequence; what entries that name none stand for
 };
+// the first of entries c0 .. c1 - 1 that names a record; -1 where there is none.  By whole warps.
+__device__ __forceinline__ int first_entry(const RecordRun& r, int c1) {
+  const int lane = threadIdx.x & 31;
+  for (int c = r.c0; c < c1; c += 32) {
+    const int v = c + lane < c1 ? __ldg(r.list + c + lane) : -1;
+    const uint32_t m = __ballot_sync(0xffffffffu, v >= 0 && v < r.n);
+    if (m) return __shfl_sync(0xffffffffu, v, __ffs((int)m) - 1);
+  }
+  return -1;
+}
 template <bool LISTED>
 __device__ __forceinline__ int run_entry(const RecordRun& r, int i) {
   return LISTED ? __ldg(r.list + r.c0 + i) : r.c0 + i;
@@ -47,7 +57,7 @@ __device__ __forceinline__ int run_entry(const RecordRun& r, int i) {
 template <bool LISTED>
 __device__ __forceinline__ int run_record(const RecordRun& r, int i) {
   const int e = run_entry<LISTED>(r, i);
-  return LISTED && (e < 0 || e >= r.n) ? 0 : e;
+  return LISTED && (e < 0 || e >= r.n) ? r.stand : e;
 }
 // of entry i's 128 tokens, those below `lim` (a row's limit in the sequence), counted from the record's first
 __device__ __forceinline__ int listed_seen(const RecordRun& r, int i, int lim) {

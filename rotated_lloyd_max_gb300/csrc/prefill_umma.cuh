@@ -347,12 +347,14 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
   const int top = row_limit(p, cl, tb, r0 + rn - 1) - base;
   const int k0 = split * (DENSE ? pp.tps : pp.cps * kChunk);
   int k1 = min(min(k0 + (DENSE ? pp.tps : pp.cps * kChunk), DENSE ? cl.len : cl.n * kChunk), top);
-  RecordRun run = {nullptr, k0 / kChunk, cl.n};
+  RecordRun run = {nullptr, k0 / kChunk, cl.n, 0};
   if constexpr (LISTED && !DENSE) {  // entries stand for whole records; what of them a row sees is its softmax's
     const int64_t at = ((int64_t)lb * (pp.tiles / pp.sub) + block) * p.Hkv + h;
     run.list = pp.list + at * pp.list_stride;
     const int cnt = cl.n > 0 && top > 0 ? min(max(__ldg(pp.list_count + at), 0), pp.list_stride) : 0;
     k1 = min(run.c0 + pp.cps, cnt) * kChunk;
+    run.stand = first_entry(run, k1 / kChunk);
+    if (run.stand < 0) k1 = k0;
   }
   const int sidx = DENSE ? pp.Sc + split : split;
   // partials of the CTA's first 128-row tile (a second one follows S blocks later)

@@ -422,95 +422,95 @@ __device__ __forceinline__ void pick_list(const SelectParams& p, const SelList& 
       const int D = p.q.D, sub = lane & 7, grp = tid >> 3;  // eight lanes a (candidate, row), four of them at a time
       constexpr int NG = T / 8;
       for (int c0 = 0; c0 < nc; c0 += T / 64) {  // eight candidates with up to 64 parts at a time
-      if (tid == 0) ms.items = 0u;
-      __syncthreads();
-      {
-        const int i = c0 + (tid >> 6), part = tid & 63;
-        if (i < nc && part < p.parts && part * p.part < s.rows &&
-            (p.parts == 1 ||
-             !(__ldcg(p.scores + (list * p.parts + part) * M + cand[i]) < key_value(keys[cand[i]]) - e2)))
-          ms.item[atomicAdd(&ms.items, 1u)] = (uint32_t)i << 6 | (uint32_t)part;
-      }
-      __syncthreads();
-      const int ni = (int)ms.items, per = min(p.part, s.rows);
-      // pair i = item i / per, row i % per of its part; from one round to the next both move by fixed steps
-      const int stepi = 4 * NG / per, stepr = 4 * NG - stepi * per;
-      int it[4], row[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        it[u] = (u * NG + grp) / per;
-        row[u] = u * NG + grp - it[u] * per;
-      }
-      for (;;) {
-        const uint4 *q[4], *bnd[4];
-        bool far[4];
-        int c[4];
-        if (__all_sync(0xffffffffu, it[0] >= ni)) break;  // (the others are further)
+        if (tid == 0) ms.items = 0u;
+        __syncthreads();
+        {
+          const int i = c0 + (tid >> 6), part = tid & 63;
+          if (i < nc && part < p.parts && part * p.part < s.rows &&
+              (p.parts == 1 ||
+               !(__ldcg(p.scores + (list * p.parts + part) * M + cand[i]) < key_value(keys[cand[i]]) - e2)))
+            ms.item[atomicAdd(&ms.items, 1u)] = (uint32_t)i << 6 | (uint32_t)part;
+        }
+        __syncthreads();
+        const int ni = (int)ms.items, per = min(p.part, s.rows);
+        // pair i = item i / per, row i % per of its part; from one round to the next both move by fixed steps
+        const int stepi = 4 * NG / per, stepr = 4 * NG - stepi * per;
+        int it[4], row[4];
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
-          const uint32_t e = ms.item[min(it[u], ni - 1)];
-          const int r = (int)(e & 63u) * p.part + row[u];
-          c[u] = (int)(e >> 6);
-          far[u] = it[u] >= ni || r >= s.rows;
-          q[u] = reinterpret_cast<const uint4*>(query_row(p, s, far[u] ? 0 : r));
-          bnd[u] = reinterpret_cast<const uint4*>(bounds_row(p, s, (int)cand[c[u]]));
+          it[u] = (u * NG + grp) / per;
+          row[u] = u * NG + grp - it[u] * per;
         }
-        if (s.rows > kPrune) {
-          // many rows: their sums in f32 first; a row further than e2 below the record's f32 score is not its maximum
-          float f[4] = {0.f, 0.f, 0.f, 0.f};
-          for (int k = sub; k < D / 8; k += 8)
+        for (;;) {
+          const uint4 *q[4], *bnd[4];
+          bool far[4];
+          int c[4];
+          if (__all_sync(0xffffffffu, it[0] >= ni)) break;  // (the others are further)
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const uint32_t e = ms.item[min(it[u], ni - 1)];
+            const int r = (int)(e & 63u) * p.part + row[u];
+            c[u] = (int)(e >> 6);
+            far[u] = it[u] >= ni || r >= s.rows;
+            q[u] = reinterpret_cast<const uint4*>(query_row(p, s, far[u] ? 0 : r));
+            bnd[u] = reinterpret_cast<const uint4*>(bounds_row(p, s, (int)cand[c[u]]));
+          }
+          if (s.rows > kPrune) {
+            // many rows: their sums in f32 first; a row further than e2 below the record's f32 score is not its maximum
+            float f[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int k = sub; k < D / 8; k += 8)
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const uint4 qv = __ldg(q[u] + k), lv = __ldg(bnd[u] + k), hv = __ldg(bnd[u] + D / 8 + k);
+                const uint32_t qw[4] = {qv.x, qv.y, qv.z, qv.w}, lw[4] = {lv.x, lv.y, lv.z, lv.w}, hw[4] = {hv.x, hv.y, hv.z, hv.w};
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                  const uint32_t pick = sign_mask2(qw[w]), bw = (lw[w] & pick) | (hw[w] & ~pick);
+                  f[u] = fmaf(bf16_lo(qw[w]), bf16_lo(bw), f[u]);
+                  f[u] = fmaf(bf16_hi(qw[w]), bf16_hi(bw), f[u]);
+                }
+              }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
+#pragma unroll
+              for (int k = 1; k < 8; k <<= 1) f[u] += __shfl_xor_sync(0xffffffffu, f[u], k);
+              far[u] = far[u] || f[u] < key_value(keys[cand[c[u]]]) - e2;
+            }
+          }
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            if (__all_sync(0xffffffffu, far[u])) continue;
+            float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            for (int k = sub; k < D / 8; k += 8) {
               const uint4 qv = __ldg(q[u] + k), lv = __ldg(bnd[u] + k), hv = __ldg(bnd[u] + D / 8 + k);
               const uint32_t qw[4] = {qv.x, qv.y, qv.z, qv.w}, lw[4] = {lv.x, lv.y, lv.z, lv.w}, hw[4] = {hv.x, hv.y, hv.z, hv.w};
 #pragma unroll
               for (int w = 0; w < 4; ++w) {
                 const uint32_t pick = sign_mask2(qw[w]), bw = (lw[w] & pick) | (hw[w] & ~pick);
-                f[u] = fmaf(bf16_lo(qw[w]), bf16_lo(bw), f[u]);
-                f[u] = fmaf(bf16_hi(qw[w]), bf16_hi(bw), f[u]);
+                add_exact(part[0].x, part[0].y, bf16_lo(qw[w]) * bf16_lo(bw));
+                add_exact(part[1].x, part[1].y, bf16_hi(qw[w]) * bf16_hi(bw));
               }
             }
+            float2 sum = join_exact(part[0], part[1]);
+#pragma unroll
+            for (int k = 1; k < 8; k <<= 1)
+              sum = join_exact(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, k), __shfl_xor_sync(0xffffffffu, sum.y, k)));
+            sum = join_exact(sum, make_float2(0.f, 0.f));
+            // the order of the pairs (sum to the nearest f32, what is left) is that of the sums
+            if (!far[u] && sub == 0 && fabsf(sum.x) < INFINITY)
+              atomicMax(exact + c[u], (unsigned long long)order_key(sum.x + 0.f) << 32 | order_key(sum.y + 0.f));
+          }
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
-#pragma unroll
-            for (int k = 1; k < 8; k <<= 1) f[u] += __shfl_xor_sync(0xffffffffu, f[u], k);
-            far[u] = far[u] || f[u] < key_value(keys[cand[c[u]]]) - e2;
-          }
-        }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          if (__all_sync(0xffffffffu, far[u])) continue;
-          float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          for (int k = sub; k < D / 8; k += 8) {
-            const uint4 qv = __ldg(q[u] + k), lv = __ldg(bnd[u] + k), hv = __ldg(bnd[u] + D / 8 + k);
-            const uint32_t qw[4] = {qv.x, qv.y, qv.z, qv.w}, lw[4] = {lv.x, lv.y, lv.z, lv.w}, hw[4] = {hv.x, hv.y, hv.z, hv.w};
-#pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const uint32_t pick = sign_mask2(qw[w]), bw = (lw[w] & pick) | (hw[w] & ~pick);
-              add_exact(part[0].x, part[0].y, bf16_lo(qw[w]) * bf16_lo(bw));
-              add_exact(part[1].x, part[1].y, bf16_hi(qw[w]) * bf16_hi(bw));
+            it[u] += stepi;
+            row[u] += stepr;
+            if (row[u] >= per) {
+              row[u] -= per;
+              ++it[u];
             }
           }
-          float2 sum = join_exact(part[0], part[1]);
-#pragma unroll
-          for (int k = 1; k < 8; k <<= 1)
-            sum = join_exact(sum, make_float2(__shfl_xor_sync(0xffffffffu, sum.x, k), __shfl_xor_sync(0xffffffffu, sum.y, k)));
-          sum = join_exact(sum, make_float2(0.f, 0.f));
-          // the order of the pairs (sum to the nearest f32, what is left) is that of the sums
-          if (!far[u] && sub == 0 && fabsf(sum.x) < INFINITY)
-            atomicMax(exact + c[u], (unsigned long long)order_key(sum.x + 0.f) << 32 | order_key(sum.y + 0.f));
         }
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          it[u] += stepi;
-          row[u] += stepr;
-          if (row[u] >= per) {
-            row[u] -= per;
-            ++it[u];
-          }
-        }
-      }
-      __syncthreads();
+        __syncthreads();
       }
       __syncthreads();
       for (int i = tid; i < nc; i += T) {
@@ -607,10 +607,14 @@ __global__ void __launch_bounds__(kOneThreads, 2) select_one_kernel(const __grid
   SelList s;
   select_place(p, list, s);
   const int lb = s.l * p.q.B + s.b;
-  const int n0 = __ldg(p.q.n_chunks + lb), l0 = p.q.tail_len ? __ldg(p.q.tail_len + lb) : 0, t0 = p.q.q_lens ? __ldg(p.q.q_lens + s.b) : p.q.T;
-  if (c < p.q.max_chunks) {  // the first ones are on their way before the sequence's counts are known
+  const int n0 = __ldg(p.q.n_chunks + lb), l0 = p.q.tail_len ? __ldg(p.q.tail_len + lb) : 0;
+  const int t0 = p.q.q_lens ? __ldg(p.q.q_lens + s.b) : p.q.T;
+  // the first ones are on their way before the sequence's counts are known: up to max_chunks they lie in the buffer
+  // (a table's entries are taken as blocks of the pool, whatever they hold)
+  if (c < p.q.max_chunks) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) rows[i] = reinterpret_cast<const uint4*>(bounds_row(p, s, min(c + 8 * i + g, p.q.max_chunks - 1))) + t;
+    for (int i = 0; i < 2; ++i)
+      rows[i] = reinterpret_cast<const uint4*>(bounds_row(p, s, min(c + 8 * i + g, p.q.max_chunks - 1))) + t;
 #pragma unroll
     for (int k = 0; k < AHEAD; ++k)
 #pragma unroll

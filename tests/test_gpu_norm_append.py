@@ -145,6 +145,18 @@ def test_in_place_full_rings_and_counters(tq):
     assert torch.equal(u["q"], t["q_out"])
 
 
+def test_many_tokens_in_place(tq):
+    """Eight tokens a CTA, the queries' own buffer taking the normalised ones, counters moving in place."""
+    import torch
+    T, ln = 700, (0, 3, 1, 2)
+    far, here = _small(tq, T=T, cap=800, ln=ln), _small(tq, T=T, cap=800, ln=ln)
+    here["q_out"] = here["q"]
+    for t in (far, here):
+        tq.tq_norm_append(tq.make_append_args(**t), _ones(tq))
+    assert torch.equal(here["q"], far["q_out"]) and torch.equal(here["k_tail"], far["k_tail"])
+    assert here["tail_len"].tolist() == [[T + n for n in ln]]
+
+
 def test_captured_and_replayed_on_another_stream(tq):
     import torch
     t, u = _small(tq, ln=(0, 1, 2, 3)), _small(tq, ln=(0, 1, 2, 3))

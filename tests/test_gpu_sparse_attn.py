@@ -327,6 +327,32 @@ def test_rows_that_are_not_finite(tq, orc, name):
         c.rec["k"].copy_(keep)
 
 
+@pytest.mark.parametrize("name", ROUTES)
+def test_entries_that_name_nothing_read_no_other_record(tq, orc, name):
+    """Holes in a list beside records that it does not name and that hold NaN and infinities, keys and values; the
+    first of a run's entries, the last, and all of them."""
+    import torch
+    r = ROUTES[name]
+    d, T, G = r["d"], r["T"], r["G"]
+    c = Cache(tq, orc, B=1, Hkv=1, d=d, kb=4, vb=4, n=5, tail=30, seed=41)
+    q = queries(1, 1, T, G, d, 42)
+    blocks = -(-T // r["qb"])
+    same = lambda e: (np.broadcast_to(np.array(e, np.int32), (1, 1, blocks, 1, len(e))).copy(),  # noqa: E731
+                      np.full((1, 1, blocks, 1), len(e), np.int32))
+    clean, alone = run(tq, c, q, same([1, 3]), r["qb"], splits=1), run(tq, c, q, same([-1]), r["qb"], splits=1)
+    off = 128 * d * 4 // 8
+    bad = torch.tensor([math.nan, math.inf, -math.inf, math.nan], device="cuda").view(torch.uint8)
+    for w in "kv":
+        for x in (0, 2, 4):
+            c.rec[w][0, 0, 0, x, off:off + 16] = bad
+    for e in ([-1, 1, 3], [1, 9, 3], [-1, 5, 1, 1 << 30, 3, -1, -2, 7]):
+        for splits in (0, 1, 2):
+            out = run(tq, c, q, same(e), r["qb"], splits=splits)
+            assert float((out.float() - clean.float()).norm() / clean.float().norm()) <= 2.0 ** -8
+    for splits in (0, 1, 3):
+        assert torch.equal(run(tq, c, q, same([-1, 5, -3]), r["qb"], splits=splits), alone)
+
+
 @pytest.mark.parametrize("scale", [-1.0, 0.0])
 @pytest.mark.parametrize("name", ROUTES)
 def test_negative_and_zero_scales(tq, orc, name, scale):
