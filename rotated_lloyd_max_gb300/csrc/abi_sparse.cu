@@ -312,11 +312,7 @@ tq_status tq_norm_append(const tq_append_args* a, const tq_head_norm* n, void* s
       !aligned(n->k_weight, 16) || n->q_head_stride < 0 || n->k_head_stride < 0 || n->q_head_stride % 4 ||
       n->k_head_stride % 4 || !std::isfinite(n->eps) || n->eps < 0.f)
     return TQ_ERR_INVALID_ARG;
-  p.q_weight = n->q_weight;
-  p.k_weight = n->k_weight;
-  p.q_hs = n->q_head_stride;
-  p.k_hs = n->k_head_stride;
-  p.eps = n->eps;
+  const HeadNorm norm = {n->q_weight, n->k_weight, n->q_head_stride, n->k_head_stride, n->eps};
   // With many tokens eight a CTA, all their heads, since a CTA's angles and first loads are a chain of 2 to 3 us: 4864
   // tokens of 48 heads of 128 24 us, 29 with the two tokens a CTA of the plain append; but 1024 tokens 11.1 and 8.5.
   const int64_t eights = (int64_t)p.L * p.B * cdiv(p.T, 8);
@@ -326,7 +322,7 @@ tq_status tq_norm_append(const tq_append_args* a, const tq_head_norm* n, void* s
     p.group = p.heads;
   }
   cudaStream_t s = (cudaStream_t)stream;
-  if (launch_norm_append(p, s) != cudaSuccess) return TQ_ERR_CUDA;
+  if (launch_norm_append(p, norm, s) != cudaSuccess) return TQ_ERR_CUDA;
   if (p.in_place && launch_append_commit(p, s) != cudaSuccess) return TQ_ERR_CUDA;
   return TQ_OK;
 }

@@ -78,8 +78,8 @@ __device__ __forceinline__ void turn_angle(int32_t pos, uint64_t frac, float* s,
 }
 
 // the new tokens' accumulated weights start at 0
-__device__ __forceinline__ void clear_mass(const AppendParams& p, int l, int b, int len, int t0, int nt) {
-  const int64_t first = (int64_t)kChunk * (p.n_chunks ? max(p.n_chunks[l * p.B + b], 0) : 0) + len + t0;
+__device__ __forceinline__ void clear_mass(const AppendParams& p, int lb, int l, int b, int len, int t0, int nt) {
+  const int64_t first = (int64_t)kChunk * (p.n_chunks ? max(p.n_chunks[lb], 0) : 0) + len + t0;
   float* m = p.mass + l * p.mass_ls + (int64_t)b * p.Hkv * p.mass_cap;
   for (int i = threadIdx.x; i < nt * p.Hkv; i += kAppendThreads) {
     const int64_t at = first + i % nt;
@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
       table[t * half + i] = f2(c * p.rot_scale, s * p.rot_scale);
     }
   }
-  if (p.mass && fits && blockIdx.y == 0) clear_mass(p, l, b, len, t0, nt);
+  if (p.mass && fits && blockIdx.y == 0) clear_mass(p, lb, l, b, len, t0, nt);
   __syncthreads();
   const uint16_t* q = p.q + l * p.q_ls + b * p.q_bs;
   const uint16_t* k = p.k + l * p.kv_ls + b * p.kv_bs;
@@ -202,7 +202,8 @@ __device__ __forceinline__ void turn_neighbours(Eight& x, const float* c, const 
 }
 
 template <int D>
-__global__ void __launch_bounds__(kAppendThreads) norm_append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kAppendThreads)
+    norm_append_kernel(const __grid_constant__ AppendParams p, const __grid_constant__ HeadNorm n) {
   constexpr int UPH = D / 16;  // two-chunk units per head
   extern __shared__ __align__(16) float planes[];  // cosines [tile][rot_dim / 2], then sines (times rot_scale)
   const int lb = blockIdx.x / p.tiles, t0 = (blockIdx.x % p.tiles) * p.tile;
@@ -279,10 +280,10 @@ __global__ void __launch_bounds__(kAppendThreads) norm_append_kernel(const __gri
       sines[t * half + pair] = s * p.rot_scale;
     }
   }
-  if (p.mass && fits && blockIdx.y == 0) clear_mass(p, l, b, len, t0, nt);
+  if (p.mass && fits && blockIdx.y == 0) clear_mass(p, lb, l, b, len, t0, nt);
   __syncthreads();
   const uint32_t team = UPH == 32 ? 0xffffffffu : ((1u << (UPH & 31)) - 1u) << (threadIdx.x & 31 & ~(UPH - 1));
-  const float* wq = p.q_weight;
+  const float* wq = n.q_weight;
   while (t < nt) {
     const int tt = t, head = h0 + hh;
     const bool mine = hh < nh && (head < p.Hq || fits);
@@ -298,10 +299,10 @@ __global__ void __launch_bounds__(kAppendThreads) norm_append_kernel(const __gri
       if (slot >= (uint32_t)cap) slot -= cap;
       uint16_t* dst = query ? qo + tt * p.o_ts + (int64_t)head * D : (value ? vr : kr) + ((int64_t)kv * cap + slot) * D;
       if (!value) {
-        const float* weight = query ? wq : p.k_weight;
+        const float* weight = query ? wq : n.k_weight;
         Eight a = unpack8(x), b_ = unpack8(y);
         if (weight) {  // the same for the UPH neighbouring lanes that hold the head
-          weight += query ? head * p.q_hs : kv * p.k_hs;
+          weight += query ? head * n.q_hs : kv * n.k_hs;
           float2 ss = mul2(a.v[0], a.v[0]);
 #pragma unroll
           for (int j = 1; j < 4; ++j) ss = fma2(a.v[j], a.v[j], ss);
@@ -310,7 +311,7 @@ __global__ void __launch_bounds__(kAppendThreads) norm_append_kernel(const __gri
           float sum = ss.x + ss.y;
 #pragma unroll
           for (int m = 1; m < UPH; m <<= 1) sum += __shfl_xor_sync(team, sum, m);
-          const float r = rsqrtf(fmaf(sum, 1.f / D, p.eps));
+          const float r = rsqrtf(fmaf(sum, 1.f / D, n.eps));
           scale8(a, r, weight + c0);
           scale8(b_, r, weight + c1);
         }
@@ -359,14 +360,14 @@ cudaError_t launch_append(const AppendParams& p, cudaStream_t s) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_norm_append(const AppendParams& p, cudaStream_t s) {
+cudaError_t launch_norm_append(const AppendParams& p, const HeadNorm& n, cudaStream_t s) {
   const dim3 grid((unsigned)((int64_t)p.L * p.B * p.tiles), (p.heads + p.group - 1) / p.group);
   const int smem = p.tile * (p.rot_dim / 2) * 2 * (int)sizeof(float);
   switch (p.D) {
-    case 64: norm_append_kernel<64><<<grid, kAppendThreads, smem, s>>>(p); break;
-    case 128: norm_append_kernel<128><<<grid, kAppendThreads, smem, s>>>(p); break;
-    case 256: norm_append_kernel<256><<<grid, kAppendThreads, smem, s>>>(p); break;
-    case 512: norm_append_kernel<512><<<grid, kAppendThreads, smem, s>>>(p); break;
+    case 64: norm_append_kernel<64><<<grid, kAppendThreads, smem, s>>>(p, n); break;
+    case 128: norm_append_kernel<128><<<grid, kAppendThreads, smem, s>>>(p, n); break;
+    case 256: norm_append_kernel<256><<<grid, kAppendThreads, smem, s>>>(p, n); break;
+    case 512: norm_append_kernel<512><<<grid, kAppendThreads, smem, s>>>(p, n); break;
     default: return cudaErrorInvalidValue;
   }
   return cudaGetLastError();

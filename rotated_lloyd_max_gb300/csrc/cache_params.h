@@ -35,7 +35,9 @@ struct AppendParams {
   int64_t mass_ls;
   int mass_cap;
   const int32_t* n_chunks;
-  // norms (tq_norm_append)
+};
+// the norms of tq_norm_append
+struct HeadNorm {
   const float *q_weight, *k_weight;
   int64_t q_hs, k_hs;
   float eps;
@@ -130,7 +132,7 @@ struct SelectParams {
 };
 
 cudaError_t launch_append(const AppendParams& p, cudaStream_t s);
-cudaError_t launch_norm_append(const AppendParams& p, cudaStream_t s);
+cudaError_t launch_norm_append(const AppendParams& p, const HeadNorm& n, cudaStream_t s);
 cudaError_t launch_key_bounds(const BoundsParams& p, cudaStream_t s);
 cudaError_t launch_select_records(const SelectParams& p, cudaStream_t s);
 cudaError_t launch_append_commit(const AppendParams& p, cudaStream_t s);
