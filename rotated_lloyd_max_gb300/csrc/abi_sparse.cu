@@ -247,17 +247,18 @@ tq_status sparse_plan(const tq_query_args* a, const tq_record_lists* r, const tq
     pp.rec_runs = (int)cdiv(U * keep, pp.cps);
     pp.ring_runs = (int)cdiv(U * ring, pp.tps);
   } else {
-    // The split count that minimises, in 128-token tiles' time, waves of records'
-    // CTAs with their set-up and epilogue, the ring's CTAs in the last wave's idle
-    // slots or after it, and the partials' traffic.
-    const double setup = 6, part = 0.03;
+    // The split count that minimises, in the time of a record's tile, waves of records'
+    // CTAs with their set-up and epilogue, the ring's CTAs (whose tiles need no decoding)
+    // in the last wave's idle slots or after it, and the partials' traffic.
+    const double setup = d <= 128 ? 4 : 3, ringtile = 0.45;
+    const double part = d <= 128 ? 0.03 * std::min(rows, bm) / bm : 0.015;
     double best = 1e300;
     for (int64_t s = 1; s <= std::min<int64_t>(most, 128); ++s) {
       if (a->splits > 0 && s != std::min<int64_t>(a->splits, std::min<int64_t>(most, 128))) continue;
       const int64_t per = cdiv(most, s);
       const int64_t sc = cdiv(keep, per), sr = cdiv(ring, per);
       const int64_t waves = cdiv(U * sc, sms);
-      const double one = (double)cdiv(keep, sc) + setup, rest = (double)(sr ? cdiv(ring, sr) : 0) + setup;
+      const double one = (double)cdiv(keep, sc) + setup, rest = ringtile * (double)(sr ? cdiv(ring, sr) : 0) + setup;
       const double idle = (double)(waves * sms - U * sc) * one, dense = (double)(U * sr) * rest;
       double cost = (double)waves * one + part * (double)(U * (sc + sr));
       if (dense > 0.9 * idle) cost += std::max(rest, (dense - 0.9 * idle) / (double)sms);
