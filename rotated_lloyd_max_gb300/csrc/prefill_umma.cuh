@@ -391,6 +391,17 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   if (warp == kPfSoft + kPfLoad) tmem_alloc(&ms.tbase, 512);
+  // queries on their way while the scales are looked through: chunk i % CH of row i / CH
+  constexpr int CH = D / 8, QN = (kPfRows * CH + kPfThreads - 1) / kPfThreads;
+  uint4 qv[QN];
+#pragma unroll
+  for (int k = 0; k < QN; ++k) {
+    const int i = tid + k * kPfThreads, r = i / CH, row = r0 + r;
+    qv[k] = make_uint4(0, 0, 0, 0);
+    if (r < rn)
+      qv[k] = __ldg(reinterpret_cast<const uint4*>(p.q + l * p.q_ls + b * p.q_bs + (int64_t)(row / p.G) * p.q_ts +
+                                                   (int64_t)(h * p.G + row % p.G) * D) + i % CH);
+  }
   bool vtable = false;  // the values are decoded through the lookup table
   if constexpr (!DENSE) {
     vtable = p.vc.bits == 4;
@@ -415,15 +426,12 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
     }
   }
   {  // queries, bf16 as they are (the softmax scale's sign folded in)
-    constexpr int CH = D / 8;
     const uint32_t flip = p.sscale < 0.f ? 0x80008000u : 0u;
-    for (int i = tid; i < 128 * nt * CH; i += kPfThreads) {
-      const int r = i / CH, ch = i % CH, row = r0 + r;
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < rn)
-        v = __ldg(reinterpret_cast<const uint4*>(p.q + l * p.q_ls + b * p.q_bs + (int64_t)(row / p.G) * p.q_ts +
-                                                 (int64_t)(h * p.G + row % p.G) * D) + ch);
-      v = make_uint4(v.x ^ flip, v.y ^ flip, v.z ^ flip, v.w ^ flip);
+#pragma unroll
+    for (int k = 0; k < QN; ++k) {
+      const int i = tid + k * kPfThreads, r = i / CH, ch = i % CH;
+      if (i >= 128 * nt * CH) break;
+      const uint4 v = make_uint4(qv[k].x ^ flip, qv[k].y ^ flip, qv[k].z ^ flip, qv[k].w ^ flip);
       *reinterpret_cast<uint4*>(sm + C::Q + (r >> 7) * C::TILE + (ch >> 3) * 16384 + sw128_off(r & 127, ch & 7)) = v;
     }
     if constexpr (!DENSE) {
