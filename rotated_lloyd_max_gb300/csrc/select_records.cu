@@ -96,7 +96,7 @@ __device__ __forceinline__ uint4 abs4(const uint4& v) {
 __device__ __forceinline__ float score_error2(int D, float size) { return size * ((float)D * 5.9604644775390625e-8f); }
 
 // Where query rows r0 .. lie as fragments: lane (g, t) of k-step pair k holds coordinates
-// 32 k + 8 t .. + 7 of row g.  [n-tile][pair][lane]; rows from nr on are zeros.
+// 32 k + 8 t .. + 7 of row g.  [n-tile][pair][lane]; rows from nr on are zeros.  Asked for, not waited for.
 template <int D, int T>
 __device__ __forceinline__ void query_fragments(const SelectParams& p, const SelList& s, int r0, int nr, uint4* frag) {
   constexpr int KP = D / 32;
@@ -106,7 +106,6 @@ __device__ __forceinline__ void query_fragments(const SelectParams& p, const Sel
     else frag[i] = make_uint4(0, 0, 0, 0);
   }
   cp_async_commit();
-  cp_async_wait<0>();
 }
 // the largest finite one of a score fragment's rows below nr; rows 2 t, 2 t + 1 of an n-tile in c[0], c[1] (c[2], c[3])
 __device__ __forceinline__ void keep_best(float (&best)[2], const float (&c)[4], int at, int nr) {
@@ -148,6 +147,7 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_scores_kernel(const __g
   const int c0 = tile * p.tile, c1 = min(c0 + p.tile, s.m), c = c0 + 16 * warp;
   const int first = (int)(blockIdx.x % p.shares) * p.share * p.part, end = min(first + p.share * p.part, s.rows);
   if (c0 >= c1 || s.m <= p.keep || first >= end) return;  // nothing here, or all of them are chosen
+  query_fragments<D, kSelThreads>(p, s, first, min(C::ROWS, end - first), frag);
   const uint4* rows[2];
 #pragma unroll
   for (int i = 0; i < 2; ++i) rows[i] = reinterpret_cast<const uint4*>(bounds_row(p, s, min(c + 8 * i + g, c1 - 1))) + t;
@@ -184,8 +184,11 @@ __global__ void __launch_bounds__(kSelThreads, 2) select_scores_kernel(const __g
   float* scores = p.scores + (list * p.parts + first / p.part) * p.q.max_chunks + c + g;
   for (int r0 = first; r0 < end; r0 += C::ROWS) {
     const int nr = min(C::ROWS, end - r0);
-    if (r0 != first) __syncthreads();
-    query_fragments<D, kSelThreads>(p, s, r0, nr, frag);
+    if (r0 != first) {
+      __syncthreads();
+      query_fragments<D, kSelThreads>(p, s, r0, nr, frag);
+    }
+    cp_async_wait<0>();
     __syncthreads();
     if (r0 == first) {  // of all the warps'
       if (threadIdx.x < D / 2) {
@@ -626,6 +629,7 @@ __global__ void __launch_bounds__(kOneThreads, 2) select_one_kernel(const __grid
   if (list_is_all<kOneThreads>(p, s, list)) return;
   const bool work = c < s.m;
   query_fragments<D, kOneThreads>(p, s, 0, s.rows, frag);
+  cp_async_wait<0>();
   __syncthreads();
   float best[2] = {-INFINITY, -INFINITY}, size[2] = {0.f, 0.f};
   if (work) {
