@@ -39,9 +39,13 @@ cudaError_t launch_merge_rows(const PrefillParams& pp, cudaStream_t s);
 
 namespace {
 
-constexpr int kFewRows = 16;   // rows of a list on mma.sync at most
-constexpr int kFewRecords = 256;  // records of a CTA's part of a list there at most
-constexpr double kFewTile = 2, kFewPart = 1.5;  // a tile of 128 ring tokens, a list's part, in records
+// Rows of a list on mma.sync at most, two of its tiles (32 of 256 records of 32 sequences, 4 kv heads of 16: 39 us, 90
+// on tcgen05; one sequence of 8 kv heads of 16: 17 and 27).
+constexpr int kFewRows = 16;
+constexpr int kFewRecords = 256;  // records of a team's part of a list there at most
+// A tile of 128 ring tokens and a list's part, in records (8 sequences over 16 records + 4096 tokens: 47 us, 51 with a
+// tile as one record, 50 as four; 32 of 256 records + 144: 51.5 us, 57.5 with a part as three).
+constexpr double kFewTile = 2, kFewPart = 1.5;
 
 // ----------------------------------------------------------------- bounds
 // where bounds or records lie: contiguous or a pool
@@ -153,7 +157,9 @@ tq_status select_plan(const tq_select_args* a, SelectPlan* pl) {
   p.tile = 128;  // 16 records a warp (select_records.cu)
   p.tiles = (int)std::max<int64_t>(1, cdiv(q.max_chunks, p.tile));
   const double lists = (double)q.L * q.B * q.Hkv * p.blocks;
-  // A list's rows are cut into at most 64 parts, of 32 rows or more; few lists share their parts among CTAs.
+  // A list's rows are cut into at most 64 parts, of 32 rows or more, and few lists share their parts among CTAs: two
+  // blocks of 4096 rows of 512 take 29 us, 76 with 16 parts, 1076 with one.  Two CTAs an SM: with four, 1024 tokens of
+  // 32 heads take 36 us instead of 34.
   const int rows = p.qb * q.G;
   p.part = (int)cdiv(cdiv(rows, 64), 32) * 32;
   p.parts = (int)cdiv(rows, p.part);

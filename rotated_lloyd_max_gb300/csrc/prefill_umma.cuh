@@ -42,7 +42,7 @@
 // The rotation of the queries is a product with the signed Hadamard matrix
 // (+-1, exact in bf16, as the queries are), one more MMA per tile.
 //
-// Measured: 1024 tokens of 32 heads over 32768 + 1280 (4 bits, head dim 128) 550 us,
+// Measured: 1024 tokens of 32 heads over 32768 + 1280 (4 bits, head dim 128) 530 us,
 // 1.02 PFLOP/s.  Neither the tensor pipe (48%) nor the issue slots (58%) are full: the
 // two tiles' chains softmax -> weights -> MMA cover one another only in part.  Instructions
 // count (lookups by shift and mask took 9% longer).

@@ -17,7 +17,7 @@
 // a record (or ring), a chunk serves the scores and, kept, the outputs, so that
 // it is decoded once; otherwise the keys' chunks and the values' follow one another.
 // A chunk is decoded into registers before its slot is waited for (5% more when it
-// decodes into the slot).  64 tokens of 64 heads over 16384, head dim 512: 376 us.
+// decodes into the slot).  64 tokens of 64 heads over 16384, head dim 512: 362 us.
 //
 // 128 tokens at head dim 512 take 640 KB of shared memory's traffic (two
 // products of 192 KB, since an MMA of N = 64 reads 6 KB; 128 KB of tiles

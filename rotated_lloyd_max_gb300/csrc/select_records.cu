@@ -124,8 +124,10 @@ __device__ __forceinline__ void score_step(float (&c)[4], const uint4& u, const 
 // lie in shared memory (64 KB of them at a time).  Up to head dim 128 a warp's bounds stay
 // in registers; the wider ones are read again (from L1) for every 8 NT rows.  The sum of
 // |terms| is bounded by that of |q_j| and the CTA's largest |bound| of coordinate j,
-// formed the same way.  1024 tokens of 32 heads in blocks of 64, 256 records: 21 us of
-// the call's 37, 13 to 16 of them in mma.sync's loop (256 CTAs, two on most SMs).
+// formed the same way.  A part's largest score of each record is kept, so that the exact
+// sums ask only the parts that may hold it.  1024 tokens of 32 heads in blocks of 64, 256
+// records: 21 us of the call's 33, 13 to 16 of them in mma.sync's loop (256 CTAs, two on
+// most SMs); 4096 tokens over 1024 records 306 us, 224 TFLOP/s.
 template <int D>
 struct ScoreCfg {
   static constexpr bool HELD = D <= 128;
@@ -288,9 +290,6 @@ __device__ __forceinline__ float2 join_exact(float2 a, float2 b) {
   return make_float2(h, __fadd_rn(c, __fsub_rn(s, h)));
 }
 
-// Query rows above which the exact sums of a row ask for its f32 score first: few rows of a candidate can be its
-// best, many cannot (256 rows of 256 records 42 us without asking, 37 with; 32 lists of 4 rows 12.6 and 13.2).
-constexpr int kPrune = 16;
 // Records up to which the warps search for the threshold in registers; beyond that its bytes are counted, which
 // takes four rounds of shared memory's atomics (2048 lists of 256 records 56 us by search, 68 by counting).
 constexpr int kSearch = 256;
@@ -457,28 +456,6 @@ __device__ __forceinline__ void pick_list(const SelectParams& p, const SelList& 
             far[u] = it[u] >= ni || r >= s.rows;
             q[u] = reinterpret_cast<const uint4*>(query_row(p, s, far[u] ? 0 : r));
             bnd[u] = reinterpret_cast<const uint4*>(bounds_row(p, s, (int)cand[c[u]]));
-          }
-          if (s.rows > kPrune) {
-            // many rows: their sums in f32 first; a row further than e2 below the record's f32 score is not its maximum
-            float f[4] = {0.f, 0.f, 0.f, 0.f};
-            for (int k = sub; k < D / 8; k += 8)
-#pragma unroll
-              for (int u = 0; u < 4; ++u) {
-                const uint4 qv = __ldg(q[u] + k), lv = __ldg(bnd[u] + k), hv = __ldg(bnd[u] + D / 8 + k);
-                const uint32_t qw[4] = {qv.x, qv.y, qv.z, qv.w}, lw[4] = {lv.x, lv.y, lv.z, lv.w}, hw[4] = {hv.x, hv.y, hv.z, hv.w};
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                  const uint32_t pick = sign_mask2(qw[w]), bw = (lw[w] & pick) | (hw[w] & ~pick);
-                  f[u] = fmaf(bf16_lo(qw[w]), bf16_lo(bw), f[u]);
-                  f[u] = fmaf(bf16_hi(qw[w]), bf16_hi(bw), f[u]);
-                }
-              }
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-#pragma unroll
-              for (int k = 1; k < 8; k <<= 1) f[u] += __shfl_xor_sync(0xffffffffu, f[u], k);
-              far[u] = far[u] || f[u] < key_value(keys[cand[c[u]]]) - e2;
-            }
           }
 #pragma unroll
           for (int u = 0; u < 4; ++u) {

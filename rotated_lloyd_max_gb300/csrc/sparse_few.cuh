@@ -22,6 +22,9 @@
 // maxima of both and 2^14 above f16's 1: what lies within 2^-28 of the largest
 // keeps 11 bits, so that a token with nearly all of a row's weight leaves the
 // others theirs.  The ring's weights are two bf16 (16 bits) against exact values.
+//
+// 32 of 256 records (4 and 3 bits) + 144 tokens of 32 sequences, 8 kv heads of 4: 51.7 us, of which the
+// merge 5; 145 MB at 2.8 TB/s.  Issue 63%, shared memory 55% and ALU 56% of what they can: the lookups.
 #pragma once
 
 #include "packed_run.cuh"
