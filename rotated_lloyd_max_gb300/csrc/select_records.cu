@@ -423,7 +423,9 @@ __device__ __forceinline__ void pick_list(const SelectParams& p, const SelList& 
       __syncthreads();
       const int D = p.q.D, sub = lane & 7, grp = tid >> 3;  // eight lanes a (candidate, row), four of them at a time
       constexpr int NG = T / 8;
-      for (int c0 = 0; c0 < nc; c0 += T / 64) {  // eight candidates with up to 64 parts at a time
+      // Eight candidates with up to 64 parts at a time; none where every product is zero (queries of zeros, which would
+      // make candidates of all records): their sums are alike as they are.
+      for (int c0 = 0; c0 < nc && e2 != 0.f; c0 += T / 64) {
         if (tid == 0) ms.items = 0u;
         __syncthreads();
         {

@@ -159,6 +159,16 @@ def test_equal_scores_go_to_the_lower_index(tq):
     c.check(tq)
 
 
+@pytest.mark.parametrize("n,T,qb", [(70, 1, 1), (700, 3, 1), (700, 40, 20)])
+def test_queries_of_zeros(tq, n, T, qb):
+    """Every score is zero, or none where bounds are not finite: the lower index, those without a score last."""
+    c = Case(seed=18, B=1, T=T, qb=qb, G=6, n=n, keep=20, sink=1, recent=1, tail=T + 5)
+    c.q[:] = 0
+    c.check(tq)
+    c.bounds[0, 0, :, 1:n - 9, 1, 7] = 0x7F80  # zero times an infinity is none
+    c.check(tq)
+
+
 @pytest.mark.parametrize("d,G,qb,T", [(64, 1, 1, 1), (128, 4, 1, 2), (128, 5, 9, 9), (512, 16, 1, 1)])
 def test_scores_that_f32_cannot_tell_apart(tq, d, G, qb, T):
     """Records that differ in one small coordinate beside large ones: the sums differ by 2^-30 of
