@@ -3,13 +3,15 @@
 //
 // H_d = H_16 x H_{d/16} over a split of the index bits.  A lane holds d / 4
 // neighbouring codes of a token, four of them a k-step: the top two and the low two
-// bits of the index are the sixteen columns of mma.sync's k, on which H_16 (+-1,
+// bits of the index are the sixteen columns of mma.sync's k, on which H_16 (+-2^-14,
 // exact) works as operand A with eight tokens as N; the bits between count the
 // k-steps, whose butterflies stay in registers.  So a lane ends with two outputs a
 // k-step for two tokens each, and a running minimum and maximum of d / 8
 // coordinates, which four lanes join at the end of a record.  Centroids enter as
 // f16 hi + lo (22 bits, two MMAs), looked up in pairs in a table with 16 copies (no
-// bank conflicts); sums are f32.  At head dim 512 a warp forms half of the outputs
+// bank conflicts); sums are f32.  The table holds them times 2^14, so that lo parts keep
+// their bits, and A takes the factor out again: sums times 2^14 would leave f32's range for
+// keys above 2^114.  At head dim 512 a warp forms half of the outputs
 // (the top k-step bit's sum or difference by the sign of A).
 //
 // A warp takes a record at a time as long as there is one for every warp (8192 of
@@ -73,6 +75,8 @@ __device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 
+constexpr float kBoundsTable = 16384.f;
+
 template <int D, int B>
 struct BoundsCfg {
   static constexpr int TAB = (1 << (2 * B)) * 128;  // pair table: entry i at 128 i, 16 copies of (hi, lo)
@@ -89,7 +93,7 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 4 : 3)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   for (int i = tid; i < (1 << (2 * B)) * 16; i += kThreads) {
     const int e = i >> 4;
-    const float x = p.c.centroids[e & ((1 << B) - 1)] * 65536.f, y = p.c.centroids[e >> B] * 65536.f;
+    const float x = p.c.centroids[e & ((1 << B) - 1)] * kBoundsTable, y = p.c.centroids[e >> B] * kBoundsTable;
     uint32_t hi, lo;
     split_f16x2(x, y, hi, lo);
     reinterpret_cast<uint2*>(sm)[i] = make_uint2(hi, lo);
@@ -98,13 +102,13 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 4 : 3)
   const uint32_t loff = (lane & 15) * 8;
   const ByteTable tab = byte_table(sm, loff, 128);
   uint16_t* mine = reinterpret_cast<uint16_t*>(sm + BoundsCfg<D, B>::TAB) + warp * 2 * D;  // [2][D]
-  // H_16: rows g, g + 8 (t' = row / 4, j' = row % 4), columns (t, j): the sign is the parity of t & t' and j & j'
+  // H_16 / kBoundsTable: rows g, g + 8 (t' = row / 4, j' = row % 4), columns (t, j): the sign is the parity of t & t' and j & j'
   uint32_t h16[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = g + 8 * (i & 1), j = 2 * (i >> 1);
     const uint32_t s0 = __popc(t & (row >> 2)) + __popc(j & row & 3), s1 = __popc(t & (row >> 2)) + __popc((j + 1) & row & 3);
-    h16[i] = 0x3C003C00u | (s0 & 1u) << 15 | (s1 & 1u) << 31;
+    h16[i] = 0x04000400u | (s0 & 1u) << 15 | (s1 & 1u) << 31;  // +-1 / kBoundsTable
   }
   struct Task {
     uint32_t q;
@@ -235,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, D <= 128 ? 4 : 3)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int o = g + 8 * e, c = (o >> 2) * RUN + 4 * (half * ACC + k) + (o & 3);
-          float x = lo[k0][e] * (1.f / 65536.f), y = hi[k0][e] * (1.f / 65536.f);
+          float x = lo[k0][e], y = hi[k0][e];
           if ((p.c.signs[c >> 5] >> (c & 31)) & 1u) {
             const float z = x;
             x = -y;

@@ -178,3 +178,21 @@ def test_a_codec_of_another_size_is_refused(tq, orc):
     for codec in (tq.tq_make_codebook(3, 128), tq.tq_make_codebook(4, 64)):
         with pytest.raises(ValueError):
             tq.tq_key_bounds(a, codec)
+
+
+@pytest.mark.parametrize("T", [0.0, 1.8])
+@pytest.mark.parametrize("d,bits", [(64, 1), (128, 4), (256, 3), (512, 2)])
+def test_bounds_of_the_largest_and_the_smallest_keys(tq, orc, d, bits, T):
+    """Keys of norms near both ends of f32: their bounds are finite and as exact as any (1e-32: a bf16 of a
+    coordinate near zero has a subnormal's step there, under 2^-20 norms)."""
+    import torch
+    c = Cache(tq, orc, B=1, Hkv=1, d=d, kb=bits, vb=1, n=3, T=T, seed=39)
+    off = 128 * d * bits // 8
+    sc = c.rec["k"][0, 0, 0, :, off:off + 512].contiguous().view(torch.float32)
+    c.rec["k"][0, 0, 0, :, off:off + 512] = (sc * torch.tensor([1e36, 1e-32, 1.0], device="cuda")[:, None]).view(torch.uint8)
+    c._host["k"] = c.rec["k"].cpu().numpy()
+    bounds = place(c)
+    tq.key_bounds(k_codec=c.kc, k_rec=c.rec["k"], bounds=bounds, n_chunks=c.d_n, max_chunks=3)
+    assert torch.all(bounds.isfinite())
+    for r in range(3):
+        check(c, bounds, 0, 0, 0, r)
