@@ -665,9 +665,10 @@ tq_status tq_key_bounds(const tq_codec* k_codec, const tq_bounds_args* args, voi
  * block in the record being above it.  The list holds min(m, keep) records in
  * ascending order: the first `sink`, the newest `recent` of the m, and the
  * rest by score.  Scores are compared exactly (those too near to be told apart
- * in f32 are formed again with twice the bits); ties go to the lower index.  A
- * query row or a record whose sum is not finite does not count; records without
- * a score come last.
+ * in f32 are formed again with twice the bits), as far as the magnitudes of the
+ * products and their sums stay in f32's normal range; ties go to the lower index.
+ * A query row or a record that holds a value which is not finite does not count;
+ * records without a score come last.
  *   list: [L][B][n_blocks][Hkv][keep], -1 behind the chosen; count: [L][B][n_blocks][Hkv].
  * max_chunks <= TQ_SELECT_MAX_CHUNKS.  workspace as for tq_prefill_attn.
  */

@@ -81,7 +81,9 @@ __device__ __forceinline__ uint4 halves_of(const uint4& q) {
   const uint32_t x = sign_mask2(q.x), y = sign_mask2(q.y), z = sign_mask2(q.z), w = sign_mask2(q.w);
   return LOW ? make_uint4(q.x & x, q.y & y, q.z & z, q.w & w) : make_uint4(q.x & ~x, q.y & ~y, q.z & ~z, q.w & ~w);
 }
-// by halves, the larger magnitude; what is not finite counts as 0 (an exponent of ones carries into the sign)
+// by halves, the sign bit where a bf16 is not finite (an exponent of ones carries into it)
+__device__ __forceinline__ uint32_t infinite2(uint32_t w) { return ((w & 0x7FFF7FFFu) + 0x00800080u) & 0x80008000u; }
+// by halves, the magnitude; what is not finite counts as 0
 __device__ __forceinline__ uint32_t finite_abs2(uint32_t w) {
   w &= 0x7FFF7FFFu;
   return w & ~sign_mask2(w + 0x00800080u);
@@ -463,16 +465,19 @@ __device__ __forceinline__ void pick_list(const SelectParams& p, const SelList& 
           for (int u = 0; u < 4; ++u) {
             if (__all_sync(0xffffffffu, far[u])) continue;
             float2 part[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            uint32_t none = 0u;  // a bound that is not finite: 0 times it is no number in the scores either
             for (int k = sub; k < D / 8; k += 8) {
               const uint4 qv = __ldg(q[u] + k), lv = __ldg(bnd[u] + k), hv = __ldg(bnd[u] + D / 8 + k);
               const uint32_t qw[4] = {qv.x, qv.y, qv.z, qv.w}, lw[4] = {lv.x, lv.y, lv.z, lv.w}, hw[4] = {hv.x, hv.y, hv.z, hv.w};
 #pragma unroll
               for (int w = 0; w < 4; ++w) {
+                none |= infinite2(lw[w]) | infinite2(hw[w]);
                 const uint32_t pick = sign_mask2(qw[w]), bw = (lw[w] & pick) | (hw[w] & ~pick);
                 add_exact(part[0].x, part[0].y, bf16_lo(qw[w]) * bf16_lo(bw));
                 add_exact(part[1].x, part[1].y, bf16_hi(qw[w]) * bf16_hi(bw));
               }
             }
+            if (none) part[0].x = INFINITY;
             float2 sum = join_exact(part[0], part[1]);
 #pragma unroll
             for (int k = 1; k < 8; k <<= 1)

@@ -293,3 +293,17 @@ def test_without_a_ring(tq):
     got = c.list.clone()
     tq.select_records(**{**c.kw, "tail_len": None, "max_tail": 0})
     assert (got == c.list).all()
+
+
+@pytest.mark.parametrize("G", [1, 9])
+def test_an_infinite_bound_leaves_its_record_without_a_score(tq, G):
+    """Whatever the queries' signs, so that max(q lo, q hi) would be finite: such records come last too, by index, beside
+    those of NaN bounds."""
+    for sign, half, inf in ((1, 0, 0xFF80), (-1, 1, 0x7F80), (1, 1, 0x7F80), (-1, 0, 0xFF80)):
+        c = Case(seed=19, B=1, G=G, n=12, keep=5, sink=0, recent=0)
+        c.q[:] = (c.q & 0x7FFF) | (0x8000 if sign < 0 else 0)
+        c.bounds[0, 0, :, :8] = 0x7FC0
+        for r in (4, 6):
+            c.bounds[0, 0, :, r] = c.bounds[0, 0, :, 9]
+            c.bounds[0, 0, :, r, half, 7] = inf
+        c.check(tq)
