@@ -279,15 +279,16 @@ tq_status sparse_plan(const tq_query_args* a, const tq_record_lists* r, const tq
     }
     if (U * (pp.Sc + pp.St) > 0x7FFFFFFFll) return TQ_ERR_UNSUPPORTED;
   }
-  const bool by_tile = !pl->few && d <= 128;  // partials of whole 128-row tiles
-  const int64_t merges = by_tile ? 16 * units * 2 * tiles : units * pp.rows;
+  const int64_t padded = cdiv(pp.rows, 128) * 128;
+  const bool by_tile = !pl->few && d <= 128;  // partials in tiles of 128 of a unit's rows
+  const int64_t merges = by_tile ? units * padded / 8 : units * pp.rows;
   if (merges > 0x7FFFFFFFll) return TQ_ERR_UNSUPPORTED;
   pp.out = (uint16_t*)a->out;
   pp.o_ls = a->out_layer_stride;
   pp.o_bs = a->out_batch_stride;
   pp.o_ts = a->out_token_stride;
   pp.inv_sqrt_d = (float)(1.0 / std::sqrt((double)d));
-  const size_t parts = (size_t)(by_tile ? units * tiles * 256 : units * pp.rows) * (pp.Sc + pp.St);
+  const size_t parts = (size_t)(units * (by_tile ? padded : pp.rows)) * (pp.Sc + pp.St);
   pl->ml_off = pad256(parts * d * 4);
   pl->bytes = pl->ml_off + pad256(parts * 8) + 256;
   return TQ_OK;

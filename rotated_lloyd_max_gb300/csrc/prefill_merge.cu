@@ -105,23 +105,16 @@ __global__ void __launch_bounds__(256, SL > 1 ? 1 : 4) prefill_merge_tiles_kerne
   pdl_wait();
   const QueryParams& p = pp.q;
   const int tid = threadIdx.x, qd = tid & 3, sl = SL > 1 ? tid / (4 * ROWS) : 0, lr = (tid >> 2) % ROWS;
-  // listed records: whole row tiles of 256 for every block of queries
-  const int ntile = pp.q_block ? 2 * pp.tiles : (pp.rows + 127) / 128, per = 128 / ROWS;  // CTAs of a tile
+  const int ntile = (pp.rows + 127) / 128, per = 128 / ROWS;  // CTAs of a tile
   const int64_t blk = blockIdx.x / per;
   const int r = (int)(blockIdx.x % per) * ROWS + lr;
   const int tile = (int)(blk % ntile);
   const int64_t unit = blk / ntile;
-  int first = tile * 128, rows_left = 0x7FFFFFFF;  // the tile's first row, rows of its block from there
-  if (pp.q_block) {
-    const int block = (tile >> 1) / pp.sub, off = ((tile >> 1) % pp.sub) * 256 + (tile & 1) * 128;
-    first = block * pp.q_block * p.G + off;
-    rows_left = pp.q_block * p.G - off;
-  }
-  const int row = first + r, tok = row / p.G;
+  const int row = tile * 128 + r, tok = row / p.G;
   const int h = (int)(unit % p.Hkv), lb = (int)(unit / p.Hkv), b = lb % p.B, l = lb / p.B;
   const int tb = query_len(p, b);
-  if ((int)(blockIdx.x % per) * ROWS >= min(rows_left, tb * p.G - first)) return;
-  const bool live = r < min(rows_left, tb * p.G - first);
+  if (tile * 128 + (int)(blockIdx.x % per) * ROWS >= tb * p.G) return;
+  const bool live = row < tb * p.G;
   const int S = pp.Sc + pp.St;
   const float2* ml = pp.ws_ml + blk * S * 128 + r;
   const float4* acc = reinterpret_cast<const float4*>(pp.ws_acc) + (blk * S * (D / 4) + qd * (E / 4)) * 128 + r;
@@ -211,7 +204,7 @@ static cudaError_t merge_tiles_launch(const PrefillParams& pp, int64_t tiles, cu
 
 cudaError_t launch_prefill_merge(const PrefillParams& pp, cudaStream_t s) {
   const unsigned grid = (unsigned)cdiv((int64_t)pp.q.L * pp.q.B * pp.q.Hkv * pp.rows, 4);
-  const int64_t tiles = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv * (pp.q_block ? 2 * pp.tiles : (pp.rows + 127) / 128);
+  const int64_t tiles = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv * ((pp.rows + 127) / 128);
   switch (pp.q.D) {
     case 64: return merge_tiles_launch<64>(pp, tiles, s);
     case 128: return merge_tiles_launch<128>(pp, tiles, s);

@@ -357,11 +357,22 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
     if (run.stand < 0) k1 = k0;
   }
   const int sidx = DENSE ? pp.Sc + split : split;
-  // partials of the CTA's first 128-row tile (a second one follows S blocks later)
-  const int64_t blk = ((unit * (LISTED ? 2 * pp.tiles : (pp.rows + 127) / 128) + 2 * tile) * S + sidx) * 128;
+  // Partials lie in tiles of 128 of the unit's rows, whatever the blocks of queries are: the place of the CTA's first row
+  // (a next tile follows S tiles later)
+  const int64_t blk = ((unit * ((pp.rows + 127) / 128) + (LISTED ? r0 >> 7 : 2 * tile)) * S + sidx) * 128 +
+                      (LISTED ? r0 & 127 : 0);
+  // where row r's tile begins, and which of its rows it is
+  auto place = [&](int r, int& row) {
+    const int x = (LISTED ? (int)blk & 127 : 0) + r;
+    row = x & 127;
+    return (LISTED ? blk & ~(int64_t)127 : blk) + (int64_t)(x >> 7) * S * 128;
+  };
   if (k0 >= k1) {
-    for (int r = tid; r < rn; r += kPfThreads)
-      pp.ws_ml[blk + (r >> 7) * S * 128 + (r & 127)] = make_float2(-INFINITY, 0.f);
+    for (int r = tid; r < rn; r += kPfThreads) {
+      int row;
+      const int64_t at = place(r, row);
+      pp.ws_ml[at + row] = make_float2(-INFINITY, 0.f);
+    }
     return;
   }
   const int n = (k1 - k0 + kChunk - 1) / kChunk;  // 128-token tiles
@@ -779,8 +790,9 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
     mbar_wait_idle(&ms.o_done[t], (n - 1) & 1, abort_f);
     tc_fence_after();
     const float un = DENSE ? 1.f : pow2i(-15) * (1.f / ev);
-    const int64_t at = blk + (int64_t)t * S * 128;
-    float4* dst = reinterpret_cast<float4*>(pp.ws_acc) + at * (D / 4) + (r & 127);
+    int row;
+    const int64_t at = place(r, row);
+    float4* dst = reinterpret_cast<float4*>(pp.ws_acc) + at * (D / 4) + row;
 #pragma unroll 1
     for (int c = 0; c < D / 32; ++c) {
       uint32_t o[32];
@@ -796,7 +808,7 @@ __device__ __forceinline__ void prefill_umma_body(const PrefillParams& pp, unsig
     }
     if (r < rn) {
       const float bad = __int_as_float(0x7fc00000);
-      pp.ws_ml[at + (r & 127)] = *abort_f || lsum != lsum ? make_float2(bad, bad)
+      pp.ws_ml[at + row] = *abort_f || lsum != lsum ? make_float2(bad, bad)
                                  : lsum > 0.f ? make_float2(mref, lsum) : make_float2(-INFINITY, 0.f);
     }
     tc_fence_before();

@@ -460,3 +460,16 @@ def test_lists_of_another_shape_are_refused(tq, orc):
         with pytest.raises((ValueError, tq.TqError)):
             tq.sparse_attn(k_codec=c.kc, v_codec=c.vc, q=q, out=torch.empty_like(q), scale=1.0, list=z(*shape, 3),
                            count=z(*shape), q_block=qb, **c.kw())
+
+
+@pytest.mark.parametrize("splits", [1, 7])
+@pytest.mark.parametrize("G,qb,d", [(17, 1, 64), (5, 7, 128), (16, 4, 128), (64, 2, 64), (43, 3, 128), (65, 3, 64), (128, 2, 128),
+                                    (43, 7, 64), (65, 8, 64)])
+def test_blocks_of_17_to_520_rows(tq, orc, G, qb, d, splits):
+    """Blocks whose rows end inside the partials' tiles of 128, or take several; the last one is short."""
+    c = Cache(tq, orc, B=2, Hkv=1, d=d, kb=4, vb=3, n=9, tail=40, seed=43, lens=([9, 4], [40, 17]))
+    T = 2 * qb + 1
+    q = queries(1, 2, T, G, d, 44)
+    ls = lists(c, T, qb, 8, 45)
+    lens = [T, max(1, qb - 1)]
+    check(c, q, ls, qb, run(tq, c, q, ls, qb, lens, splits=splits), lens)

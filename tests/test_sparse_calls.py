@@ -209,3 +209,21 @@ def test_binding_refuses_wrong_tensors(tq):
     for bad in (dict(count=lists["count"][:, :1]), dict(list=lists["list"][..., 0]), dict(count=lists["count"].long())):
         with pytest.raises(ValueError):
             tq.make_record_lists(**{**lists, **bad})
+
+
+@pytest.mark.parametrize("d", [64, 128, 256, 512])
+@pytest.mark.parametrize("T_out", [0.0, 2.0])
+@pytest.mark.parametrize("T,G,q_block", [(2048, 4, 1), (2048, 1, 1), (2047, 4, 5), (300, 5, 4), (1000, 16, 8), (513, 4, 64),
+                                         (300, 5, 100), (5, 64, 5), (1, 4, 1)])
+def test_partials_take_the_rows_that_there_are(tq, d, T_out, T, G, q_block):
+    """One split of the records and one of the ring: the workspace holds two partials of every row (f32 outputs, two
+    numbers), a unit's rows (not a block's) padded to 128."""
+    B, Hkv = 2, 8
+    outl = dict(T=T_out, cap=4 * math.ceil(0.08 * 128 * d / 4)) if T_out else {}
+    kc, vc = _codec(tq, d=d, **outl), _codec(tq, d=d, bits=2, **outl)
+    row = Hkv * G * d
+    a = _query(tq, batch=B, t_q=T, n_q_heads=Hkv * G, n_kv_heads=Hkv, head_dim=d, q_batch_stride=T * row, q_token_stride=row,
+               out_batch_stride=T * row, out_token_stride=row, splits=1, max_tail=60)
+    r = _lists(tq, list_stride=1, q_block=q_block)
+    need = tq.load().tq_sparse_attn_workspace_size(*[ctypes.byref(x) for x in (a, r, kc, vc)])
+    assert 0 < need <= B * Hkv * (-(-T * G // 128) * 128) * 2 * (4 * d + 8) + 1024
