@@ -295,6 +295,10 @@ __device__ __forceinline__ float2 join_exact(float2 a, float2 b) {
 // Records up to which the warps search for the threshold in registers; beyond that its bytes are counted, which
 // takes four rounds of shared memory's atomics (2048 lists of 256 records 56 us by search, 68 by counting).
 constexpr int kSearch = 256;
+// Candidates up to which each sum is compared with all the others; beyond that the border is searched for, whose rounds
+// cost about as much as 64 comparisons (32, 64, 128, 256 candidates: 11.2, 14.3, 22.0, 35.7 us by pairs, 13.6, 14.3, 16.0,
+// 19.4 by search; 16384: 45.5 ms and 0.46).
+constexpr int kPairs = 64;
 struct PickMisc {
   uint32_t hist[256];
   uint32_t warp[32];
@@ -302,10 +306,46 @@ struct PickMisc {
   uint32_t item[512];  // candidates' parts that may hold their best row: index << 6 | part
 };
 
-// The list of one block from its keys (smem, one a record), of T threads.  e2: twice the error of a score.
-// cand: room for every record; bits: a bit a record.  Starts and ends with every thread past its use of keys.
+// The left-th largest of n numbers, eight bits at a time: key(i, k) says whether number i counts, and sets it.
+// left becomes how many of those that equal it are among the left largest.  By all T threads.
+template <int T, class K>
+__device__ __forceinline__ uint32_t nth_largest(PickMisc& ms, int n, uint32_t& left, K key) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  uint32_t prefix = 0u;
+  for (int sh = 24; sh >= 0; sh -= 8) {
+    if (tid < 256) ms.hist[tid] = 0u;
+    __syncthreads();
+    for (int i = tid; i < n; i += T) {
+      uint32_t k;
+      if (key(i, k) && (sh == 24 || (k >> (sh + 8)) == prefix)) atomicAdd(&ms.hist[(k >> sh) & 255u], 1u);
+    }
+    __syncthreads();
+    // numbers in bins from this thread's upwards: thread t looks at bin 255 - t
+    const uint32_t mine = tid < 256 ? ms.hist[255 - tid] : 0u;
+    uint32_t inc = mine;
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+      const uint32_t o = __shfl_up_sync(0xffffffffu, inc, k);
+      if (lane >= k) inc += o;
+    }
+    if (lane == 31) ms.warp[warp] = inc;
+    __syncthreads();
+    for (int w = 0; w < warp; ++w) inc += ms.warp[w];
+    if (tid < 256 && inc >= left && inc - mine < left) {
+      ms.prefix = prefix << 8 | (uint32_t)(255 - tid);
+      ms.left = left - (inc - mine);
+    }
+    __syncthreads();
+    prefix = ms.prefix;
+    left = ms.left;
+  }
+  return prefix;
+}
+
+// The list of one block from its keys (smem, one a record; later other uses), of T threads.  e2: twice the error of a
+// score.  cand: room for every record; bits: a bit a record.  Starts and ends with every thread past its use of keys.
 template <int T>
-__device__ __forceinline__ void pick_list(const SelectParams& p, const SelList& s, int64_t list, const uint32_t* keys,
+__device__ __forceinline__ void pick_list(const SelectParams& p, const SelList& s, int64_t list, uint32_t* keys,
                                           uint32_t* cand, uint32_t* bits, PickMisc& ms, float e2) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int32_t* out = p.list + list * p.keep;
@@ -319,11 +359,7 @@ __device__ __forceinline__ void pick_list(const SelectParams& p, const SelList& 
     if (s.m - 32 * w < 32) v &= (1u << (s.m - 32 * w)) - 1u;
     bits[w] = v;
   }
-  if (tid == 0) {
-    ms.prefix = 0u;
-    ms.left = (uint32_t)need;
-    ms.above = ms.cand = 0u;
-  }
+  if (tid == 0) ms.above = ms.cand = 0u;
   if (need > 0) {
     uint32_t x;
     __syncthreads();
@@ -378,32 +414,11 @@ __device__ __forceinline__ void pick_list(const SelectParams& p, const SelList& 
         }
       }
     } else {
-      // ---------------------------------------------------------- eight bits at a time
-      for (int sh = 24; sh >= 0; sh -= 8) {
-        if (tid < 256) ms.hist[tid] = 0u;
-        __syncthreads();
-        const uint32_t prefix = ms.prefix, left = ms.left;
-        for (int i = a + tid; i < z; i += T)
-          if (sh == 24 || (keys[i] >> (sh + 8)) == prefix) atomicAdd(&ms.hist[(keys[i] >> sh) & 255u], 1u);
-        __syncthreads();
-        // keys in bins from this thread's upwards: thread t looks at bin 255 - t
-        const uint32_t mine = tid < 256 ? ms.hist[255 - tid] : 0u;
-        uint32_t inc = mine;
-#pragma unroll
-        for (int k = 1; k < 32; k <<= 1) {
-          const uint32_t o = __shfl_up_sync(0xffffffffu, inc, k);
-          if (lane >= k) inc += o;
-        }
-        if (lane == 31) ms.warp[warp] = inc;
-        __syncthreads();
-        for (int w = 0; w < warp; ++w) inc += ms.warp[w];
-        if (tid < 256 && inc >= left && inc - mine < left) {
-          ms.prefix = prefix << 8 | (uint32_t)(255 - tid);
-          ms.left = left - (inc - mine);
-        }
-        __syncthreads();
-      }
-      x = ms.prefix;
+      uint32_t left = (uint32_t)need;
+      x = nth_largest<T>(ms, z - a, left, [&](int i, uint32_t& k) {
+        k = keys[a + i];
+        return true;
+      });
     }
     // ------------------------------------------------------------ records that f32 cannot tell from it
     const uint32_t lo = order_key(key_value(x) - e2), hi = order_key(key_value(x) + e2);
@@ -425,13 +440,14 @@ __device__ __forceinline__ void pick_list(const SelectParams& p, const SelList& 
       __syncthreads();
       const int D = p.q.D, sub = lane & 7, grp = tid >> 3;  // eight lanes a (candidate, row), four of them at a time
       constexpr int NG = T / 8;
-      // Eight candidates with up to 64 parts at a time; none where every product is zero (queries of zeros, which would
-      // make candidates of all records): their sums are alike as they are.
-      for (int c0 = 0; c0 < nc && e2 != 0.f; c0 += T / 64) {
+      // T candidates' parts at a time (a list has 64 at most); none where every product is zero (queries of zeros, which
+      // would make candidates of all records): their sums are alike as they are.
+      const int lg = 32 - __clz(p.parts - 1);
+      for (int c0 = 0; c0 < nc && e2 != 0.f; c0 += T >> lg) {
         if (tid == 0) ms.items = 0u;
         __syncthreads();
         {
-          const int i = c0 + (tid >> 6), part = tid & 63;
+          const int i = c0 + (tid >> lg), part = tid & ((1 << lg) - 1);
           if (i < nc && part < p.parts && part * p.part < s.rows &&
               (p.parts == 1 ||
                !(__ldcg(p.scores + (list * p.parts + part) * M + cand[i]) < key_value(keys[cand[i]]) - e2)))
@@ -500,16 +516,56 @@ __device__ __forceinline__ void pick_list(const SelectParams& p, const SelList& 
         __syncthreads();
       }
       __syncthreads();
-      for (int i = tid; i < nc; i += T) {
-        // the maxima were formed in L2: no line of L1 is asked for them
-        const unsigned long long k = __ldcg(exact + i);
-        const uint32_t r = cand[i];
-        int before = 0;
-        for (int j = 0; j < nc; ++j) {
-          const unsigned long long o = __ldcg(exact + j);
-          before += o > k || (o == k && cand[j] < r);
+      // (the maxima were formed in L2: no line of L1 is asked for them)
+      if (nc <= kPairs && e2 != 0.f) {
+        for (int i = tid; i < nc; i += T) {
+          const unsigned long long k = __ldcg(exact + i);
+          const uint32_t r = cand[i];
+          int before = 0;
+          for (int j = 0; j < nc; ++j) {
+            const unsigned long long o = __ldcg(exact + j);
+            before += o > k || (o == k && cand[j] < r);
+          }
+          if (before < places) atomicOr(&bits[r >> 5], 1u << (r & 31));
         }
-        if (before < places) atomicOr(&bits[r >> 5], 1u << (r & 31));
+      } else {
+        // the places-th largest sum; of the records that have it, the lowest
+        uint32_t left = (uint32_t)places, high = 0u, low = 0u;
+        if (e2 != 0.f) {
+          high = nth_largest<T>(ms, nc, left, [&](int i, uint32_t& k) {
+            k = (uint32_t)(__ldcg(exact + i) >> 32);
+            return true;
+          });
+          low = nth_largest<T>(ms, nc, left, [&](int i, uint32_t& k) {
+            const unsigned long long v = __ldcg(exact + i);
+            k = (uint32_t)v;
+            return (uint32_t)(v >> 32) == high;
+          });
+        }
+        const unsigned long long border = (unsigned long long)high << 32 | low;
+        static_assert(TQ_SELECT_MAX_CHUNKS <= 32 * T, "a word of ties a thread");
+        uint32_t* ties = keys;  // whose keys have served
+        if (tid < words) ties[tid] = 0u;
+        __syncthreads();
+        for (int i = tid; i < nc; i += T) {
+          const unsigned long long k = e2 != 0.f ? __ldcg(exact + i) : 0ull;
+          if (k >= border) atomicOr((k > border ? bits : ties) + (cand[i] >> 5), 1u << (cand[i] & 31));
+        }
+        __syncthreads();
+        uint32_t v = tid < words ? ties[tid] : 0u, inc = __popc(v);
+        const uint32_t mine = inc;
+#pragma unroll
+        for (int k = 1; k < 32; k <<= 1) {
+          const uint32_t o = __shfl_up_sync(0xffffffffu, inc, k);
+          if (lane >= k) inc += o;
+        }
+        if (lane == 31) ms.warp[warp] = inc;
+        __syncthreads();
+        for (int w = 0; w < warp; ++w) inc += ms.warp[w];
+        for (uint32_t at = inc - mine; v && at < left; ++at) {
+          bits[tid] |= v & (0u - v);
+          v &= v - 1u;
+        }
       }
     } else {
       for (int i = tid; i < nc; i += T) atomicOr(&bits[cand[i] >> 5], 1u << (cand[i] & 31));

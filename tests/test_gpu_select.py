@@ -307,3 +307,53 @@ def test_an_infinite_bound_leaves_its_record_without_a_score(tq, G):
             c.bounds[0, 0, :, r] = c.bounds[0, 0, :, 9]
             c.bounds[0, 0, :, r, half, 7] = inf
         c.check(tq)
+
+
+def few_apart(c, seed, near):
+    """Scores that f32 cannot tell apart: records of one base that differ in one small coordinate, `near` values of it."""
+    g = np.random.default_rng(seed)
+    bf = lambda x: (np.float32(x).view(np.uint32) >> 16).astype(np.uint16)  # noqa: E731
+    c.q[:] = bf(np.float32(g.integers(1, 4, c.q.shape) * 64))
+    c.q[..., 3] = bf(np.full(c.q.shape[:-1], 2.0 ** -12, np.float32))
+    b = np.broadcast_to(g.integers(1, 100, (1, 1, 1, 1, 2, c.d)).astype(np.float32), c.bounds.shape).copy()
+    b[..., 3] = g.integers(-near, near + 1, b.shape[:-1]) * 2.0 ** -6
+    c.bounds = bf(b)
+
+
+@pytest.mark.parametrize("G,T,qb", [(2, 1, 1), (5, 8, 8), (40, 4, 4)])
+@pytest.mark.parametrize("n,keep,near", [(200, 120, 60), (700, 33, 1), (700, 350, 100), (5000, 1, 3), (5000, 4000, 100),
+                                         (5000, 2500, 0)])
+def test_many_candidates(tq, n, keep, near, G, T, qb):
+    """Every record is a candidate for the exact sums; few distinct ones (ties go to the lower index), many, one."""
+    c = Case(seed=20, B=1, Hkv=1, d=64, G=G, T=T, qb=qb, n=n, keep=keep, sink=0, recent=0)
+    few_apart(c, 21, near)
+    c.check(tq)
+
+
+@pytest.mark.parametrize("kind", ["zero_queries", "equal_bounds", "nan_bounds"])
+def test_ties_of_a_long_cache_take_no_square_of_it(tq, kind):
+    """Records that all tie: the lowest indices, in a time that grows with their number: 16384 take less than eight times
+    what 4096 do (pairwise comparisons take sixteen times as long)."""
+    import torch
+    best = {}
+    for n in (4096, 16384):
+        c = Case(seed=22, B=1, Hkv=1, d=64, n=n, keep=64, sink=1, recent=1)
+        if kind == "zero_queries":
+            c.q[:] = 0
+        elif kind == "equal_bounds":
+            c.bounds[:] = c.bounds[:, :, :, :1]
+        else:
+            c.bounds[:] = 0x7FC0
+        c.check(tq)
+        a = tq.make_select_args(**c.kw)
+        ws = torch.empty(tq.tq_select_records_workspace_size(a), dtype=torch.uint8, device="cuda")
+        times = []
+        for _ in range(6):
+            t0, t1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            t0.record()
+            tq.tq_select_records(a, ws)
+            t1.record()
+            torch.cuda.synchronize()
+            times.append(t0.elapsed_time(t1))
+        best[n] = min(times)
+    assert best[16384] < 8 * best[4096]
