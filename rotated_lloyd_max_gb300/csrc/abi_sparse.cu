@@ -46,6 +46,7 @@ constexpr int kFewRecords = 256;  // records of a team's part of a list there at
 // A tile of 128 ring tokens and a list's part, in records (8 sequences over 16 records + 4096 tokens: 47 us, 51 with a
 // tile as one record, 50 as four; 32 of 256 records + 144: 51.5 us, 57.5 with a part as three).
 constexpr double kFewTile = 2, kFewPart = 1.5;
+constexpr int64_t kMostInt = 0x7FFFFFFF;
 
 // ----------------------------------------------------------------- bounds
 // where bounds or records lie: contiguous or a pool
@@ -204,7 +205,7 @@ tq_status sparse_plan(const tq_query_args* a, const tq_record_lists* r, const tq
   pp.sub = (int)cdiv(rows, bm);
   const int64_t tiles = (int64_t)blocks * pp.sub;
   const int64_t units = (int64_t)q.L * q.B * q.Hkv, U = units * tiles, sms = sm_count();
-  if (tiles > 0x3FFFFFFF || U > 0x7FFFFFFFll) return TQ_ERR_UNSUPPORTED;
+  if (tiles > 0x3FFFFFFF || U > kMostInt) return TQ_ERR_UNSUPPORTED;
   pp.tiles = (int)tiles;
   const int64_t keep = r->list_stride, ring = cdiv(q.max_tail, TQ_CHUNK), most = std::max(keep, ring);
   if (pl->few) {
@@ -221,11 +222,11 @@ tq_status sparse_plan(const tq_query_args* a, const tq_record_lists* r, const tq
     };
     double best = 1e300;
     auto consider = [&](int64_t per) {
-      per = std::max<int64_t>(1, std::min<int64_t>(per, keep > kFewRecords ? kFewRecords : U * keep));
+      per = std::max<int64_t>(1, std::min<int64_t>(per, keep > kFewRecords ? kFewRecords : std::min(U * keep, kMostInt)));
       const int64_t ctas = cdiv(U * keep, per), waves = cdiv(ctas, slots);
       const int64_t left = std::max<int64_t>(waves * slots - ctas, std::max<int64_t>(1, slots / 16));
       int64_t tiles_per = std::max<int64_t>(1, cdiv(U * ring, left));
-      if (tiles_per > ring && ring) tiles_per = cdiv(tiles_per, ring) * ring;
+      if (tiles_per > ring && ring) tiles_per = std::min(cdiv(tiles_per, ring), kMostInt / ring) * ring;
       const double a1 = (double)waves * ((double)per + kFewPart * (double)parts_of(keep, per));
       const double b1 = ring ? kFewTile * (double)tiles_per + kFewPart * (double)parts_of(ring, tiles_per) : 0;
       const double cost = std::max(a1, b1) + 0.05 * (a1 + b1);
@@ -249,7 +250,8 @@ tq_status sparse_plan(const tq_query_args* a, const tq_record_lists* r, const tq
     pp.ring = (int)ring;
     pp.Sc = (int)most_parts(keep, pp.cps);
     pp.St = (int)most_parts(ring, pp.tps);
-    if (cdiv(U * keep, pp.cps) + cdiv(U * ring, pp.tps) > 0x7FFFFFFFll) return TQ_ERR_UNSUPPORTED;
+    // (the last CTA's teams count past the runs)
+    if (cdiv(U * keep, pp.cps) + cdiv(U * ring, pp.tps) > kMostInt - 4) return TQ_ERR_UNSUPPORTED;
     pp.rec_runs = (int)cdiv(U * keep, pp.cps);
     pp.ring_runs = (int)cdiv(U * ring, pp.tps);
   } else {
@@ -277,12 +279,12 @@ tq_status sparse_plan(const tq_query_args* a, const tq_record_lists* r, const tq
         pp.St = (int)sr;
       }
     }
-    if (U * (pp.Sc + pp.St) > 0x7FFFFFFFll) return TQ_ERR_UNSUPPORTED;
+    if (U * (pp.Sc + pp.St) > kMostInt) return TQ_ERR_UNSUPPORTED;
   }
   const int64_t padded = cdiv(pp.rows, 128) * 128;
   const bool by_tile = !pl->few && d <= 128;  // partials in tiles of 128 of a unit's rows
   const int64_t merges = by_tile ? units * padded / 8 : units * pp.rows;
-  if (merges > 0x7FFFFFFFll) return TQ_ERR_UNSUPPORTED;
+  if (merges > kMostInt) return TQ_ERR_UNSUPPORTED;
   pp.out = (uint16_t*)a->out;
   pp.o_ls = a->out_layer_stride;
   pp.o_bs = a->out_batch_stride;

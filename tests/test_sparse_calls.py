@@ -227,3 +227,19 @@ def test_partials_take_the_rows_that_there_are(tq, d, T_out, T, G, q_block):
     r = _lists(tq, list_stride=1, q_block=q_block)
     need = tq.load().tq_sparse_attn_workspace_size(*[ctypes.byref(x) for x in (a, r, kc, vc)])
     assert 0 < need <= B * Hkv * (-(-T * G // 128) * 128) * 2 * (4 * d + 8) + 1024
+
+
+@pytest.mark.parametrize("T,layers,max_tail,keep", [(1 << 20, 64, 1 << 30, 32), (1 << 20, 64, 1 << 29, 256),
+                                                    (1 << 20, 64, 1 << 30, 1), (1 << 17, 1, 1 << 20, 32), (1, 1, 1 << 30, 1)])
+def test_runs_of_very_long_rings_are_planned(tq, T, layers, max_tail, keep):
+    """Lists x ring tiles past 2^31 a run (a division by zero ended the process): the workspace holds one partial of the
+    records and one of the ring for every row, and few more."""
+    Hkv, d = 8, 64
+    row = Hkv * d
+    a = _query(tq, n_layers=layers, batch=1, t_q=T, n_q_heads=Hkv, n_kv_heads=Hkv, head_dim=d, q_layer_stride=T * row,
+               q_batch_stride=T * row, q_token_stride=row, out_layer_stride=T * row, out_batch_stride=T * row,
+               out_token_stride=row, max_tail=max_tail, tail_cap=max_tail)
+    kc, vc, r = _codec(tq, d=d), _codec(tq, d=d, bits=2), _lists(tq, list_stride=keep, q_block=1)
+    need = tq.load().tq_sparse_attn_workspace_size(*[ctypes.byref(x) for x in (a, r, kc, vc)])
+    one = layers * T * Hkv * (4 * d + 8)
+    assert 2 * one <= need <= (4 if T > 1 else 700) * one + 1024
