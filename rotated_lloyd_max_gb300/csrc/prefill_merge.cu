@@ -95,10 +95,9 @@ __global__ void __launch_bounds__(kThreads) prefill_merge_kernel(const __grid_co
 // groups of threads, whose sums meet in shared memory (a few rows with many
 // splits would otherwise wait for one load after another: the call for 30 rows of
 // 2 kv heads takes 33 us with SL = 1 and 23 with 8 over 18 splits, 25 and 21 over 7).
-// Of the CTAs with SL = 1 four share an SM, at the cost of a few spilled bytes, so that
-// 512 of them (32768 rows) run at once.
-template <int D, int SL>
-__global__ void __launch_bounds__(256, SL > 1 ? 1 : 4) prefill_merge_tiles_kernel(const __grid_constant__ PrefillParams pp) {
+// CTAS share an SM, which bounds the registers and with them the loads in flight (the launch has the rule).
+template <int D, int SL, int CTAS>
+__global__ void __launch_bounds__(256, CTAS) prefill_merge_tiles_kernel(const __grid_constant__ PrefillParams pp) {
   constexpr int E = D / 4, ROWS = 256 / (4 * SL);
   __shared__ float part[SL > 1 ? (SL - 1) * 4 * ROWS : 1][E + 1];
   __shared__ float wsum[SL > 1 ? SL * 4 * ROWS : 1];
@@ -198,8 +197,15 @@ __global__ void __launch_bounds__(256, SL > 1 ? 1 : 4) prefill_merge_tiles_kerne
 
 template <int D>
 static cudaError_t merge_tiles_launch(const PrefillParams& pp, int64_t tiles, cudaStream_t s) {
-  if (pp.Sc + pp.St > 6) return launch_after(prefill_merge_tiles_kernel<D, 8>, dim3((unsigned)(tiles * 16)), 256, 0, s, 1, pp);
-  return launch_after(prefill_merge_tiles_kernel<D, 1>, dim3((unsigned)(tiles * 2)), 256, 0, s, 1, pp);
+  if (pp.Sc + pp.St > 6) return launch_after(prefill_merge_tiles_kernel<D, 8, 1>, dim3((unsigned)(tiles * 16)), 256, 0, s, 1, pp);
+  // One CTA more an SM, with fewer registers, only where it lets all of them run at once (512 CTAs at head dim 128: the
+  // call for 1024 tokens over 32 of 256 listed records 139.6 us, 140.8 without; but 128 CTAs, 4 times 64 tokens over 4096,
+  // 52.9 us, 56.4 with it, and 720 at head dim 64, 6 prompts of 257 over 6144, 151.2 and 153.4).
+  constexpr int CTAS = D == 64 ? 4 : 3;
+  const int64_t ctas = 2 * tiles, sms = sm_count();
+  const auto kern = ctas > CTAS * sms && ctas <= (CTAS + 1) * sms ? prefill_merge_tiles_kernel<D, 1, CTAS + 1>
+                                                                  : prefill_merge_tiles_kernel<D, 1, CTAS>;
+  return launch_after(kern, dim3((unsigned)ctas), 256, 0, s, 1, pp);
 }
 
 cudaError_t launch_prefill_merge(const PrefillParams& pp, cudaStream_t s) {
