@@ -257,7 +257,10 @@ tq_status sparse_plan(const tq_query_args* a, const tq_record_lists* r, const tq
   } else {
     // The split count that minimises, in the time of a record's tile, waves of records'
     // CTAs with their set-up and epilogue, the ring's CTAs (whose tiles need no decoding)
-    // in the last wave's idle slots or after it, and the partials' traffic.
+    // in the last wave's idle slots or after it, and the partials' traffic.  Where the ring's
+    // outlast those slots they go first, at head dims 64 and 128 (1024 tokens of 32 heads over 32 records
+    // 150 us, 153 behind; at 256 and 512 they stay behind: 512 tokens of 64 heads of 512 over 32
+    // records + 2048 1071 us, 1122 first; 512 of 16 heads of 256 208 us, 226).
     const double setup = d <= 128 ? 4 : 3, ringtile = 0.45;
     const double part = d <= 128 ? 0.03 * std::min(rows, bm) / bm : 0.015;
     double best = 1e300;
@@ -272,7 +275,7 @@ tq_status sparse_plan(const tq_query_args* a, const tq_record_lists* r, const tq
       if (dense > 0.9 * idle) cost += std::max(rest, (dense - 0.9 * idle) / (double)sms);
       if (cost < best) {
         best = cost;
-        pp.ring = dense > 0.9 * idle;
+        pp.ring_first = d <= 128 && dense > 0.9 * idle;
         pp.cps = (int)per;
         pp.Sc = (int)sc;
         pp.tps = (int)(TQ_CHUNK * per);

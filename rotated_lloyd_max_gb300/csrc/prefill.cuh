@@ -29,6 +29,7 @@ struct PrefillParams {
   const int32_t* list;
   const int32_t* list_count;
   int list_stride, q_block, sub;
+  bool ring_first;  // the ring's CTAs before the records' (head dims 64 and 128)
   // few rows: runs of the lists' entries (cps each) and of the rings' tiles of 128 tokens (tps each, ring a list)
   int rec_runs, ring_runs, ring;
 };

@@ -839,7 +839,7 @@ __global__ void __launch_bounds__(kPfThreads, 1) prefill_umma_kernel(const __gri
   // outlast the last wave's idle slots) before them
   const int64_t U = (int64_t)pp.q.L * pp.q.B * pp.q.Hkv * pp.tiles;
   int split = (int)(blockIdx.x / U);
-  if (LISTED && pp.ring) split = split < pp.St ? split + pp.Sc : split - pp.St;
+  if (LISTED && pp.ring_first) split = split < pp.St ? split + pp.Sc : split - pp.St;
   const int tile = (int)(blockIdx.x % U % pp.tiles);
   const int64_t unit = blockIdx.x % U / pp.tiles;
   if (split < pp.Sc) prefill_umma_body<D, false, CAP, LISTED>(pp, sm, unit, tile, split);

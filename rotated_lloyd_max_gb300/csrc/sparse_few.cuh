@@ -452,7 +452,7 @@ __device__ __forceinline__ void few_ring(const PrefillParams& pp, const uint2* q
 }
 
 // One list's part of a team's run: entries [k0, k1) of it, or (dense) tiles of 128 ring tokens.
-// split: the partial's place; the first one marks the `gaps` places behind the list's last as empty.
+// split: the partial's place of the list's `slots`; the first one marks those behind the list's last one as empty.
 template <int D, int KB, int VB, int NT>
 __device__ __forceinline__ void few_segment(const PrefillParams& pp, const unsigned char* tables, unsigned char* sm, bool dense, int64_t x, int k0, int k1,
                                             int split, int last, int slots) {
