@@ -636,6 +636,16 @@ tq_status tq_evict_mass(const tq_evict_mass_args* args, const tq_codec* k_codec,
  * bounded (first NULL = 0), the others' bounds left as they are: a caller that
  * bounds what it encodes passes the count it had before.  A record that holds
  * a scale which is not finite has NaN bounds.
+ *
+ * Bounds are those of the records' bytes at the time of the call, and nothing
+ * tells a later selection that the bytes have changed:
+ *   tq_evict adds records behind the others, whose bounds stay;
+ *   tq_evict_mass moves tokens between records: all of the destination's are
+ *     to be bounded again (first NULL or 0);
+ *   tq_rollback drops records, and evictions after it write others in their
+ *     places: a count of bounded records kept for `first` has to go down with it,
+ *     to n_chunks as the rollback leaves it;
+ *   a block of a pool that another record takes is to be bounded for that one.
  */
 typedef struct {
   int32_t n_layers, batch, n_kv_heads;

@@ -923,7 +923,8 @@ def make_bounds_args(*, k_rec, bounds, n_chunks, max_chunks: int, first=None, ma
 
 
 def tq_key_bounds(args: tq_bounds_args, k_codec: Codec, stream=None):
-    """Smallest and largest value of each coordinate of every record's keys (include/tq.h)."""
+    """Smallest and largest value of each coordinate of every record's keys; to be formed again where records have
+    changed, as tq_evict_mass and evictions after tq_rollback change them (include/tq.h)."""
     _ready(args)
     _fits(args, k_codec, None)
     _need(args._tensors[1].shape[-1] == k_codec.head_dim, "bounds: expected the codec's head dim")

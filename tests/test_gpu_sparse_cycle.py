@@ -8,8 +8,9 @@ import pytest
 
 import synth
 import tq_testlib as tl
-from cache_cases import ocodec
+from cache_cases import Cache, ocodec, queries
 from test_gpu_append import _turned
+from test_gpu_key_bounds import at, check, place
 from test_gpu_select import want as wanted
 
 pytestmark = pytest.mark.gpu
@@ -121,3 +122,64 @@ def test_append_age_bound_choose_attend(tq, orc, d, G, paged):
                       max_new=4, block_table=table)
         cnt["bounded"].copy_(cnt["n"])
     assert int(cnt["n"].min()) >= 4
+
+
+@pytest.mark.parametrize("paged", [False, True])
+def test_bounds_and_lists_after_an_eviction_by_weight_and_a_rollback(tq, orc, paged):
+    """When bounds expire: all of them after an eviction by weight; from the records that a rollback leaves on, where
+    others have been written in the dropped ones' places."""
+    import torch
+    c = Cache(tq, orc, B=2, Hkv=2, d=128, kb=4, vb=3, n=9, tail=40, cap=700, paged=paged, seed=51, lens=([9, 7], [40, 21]))
+    bounds = place(c)
+    ring = dict(k_tail=c.ring["k"], v_tail=c.ring["v"])
+    counts = dict(n_chunks=c.d_n, tail_start=c.d_start, tail_len=c.d_len)
+    recs = dict(k_rec=c.rec["k"], v_rec=c.rec["v"], block_table=c.table)
+    q = queries(1, 2, 3, 8, 128, 52)
+
+    def bound(first=None):
+        tq.key_bounds(k_codec=c.kc, k_rec=c.rec["k"], bounds=bounds, n_chunks=c.d_n, first=first, max_chunks=9,
+                      block_table=c.table)
+
+    def agree():
+        """Every record's bounds are those of its keys, and the lists those of its bounds."""
+        c.n[:], c.len[:] = c.d_n.cpu().numpy(), c.d_len.cpu().numpy()
+        k = c.rec["k"]
+        if c.table is not None:
+            k = torch.stack([torch.stack([k[0, c.table[b].long()] for b in range(2)])]).transpose(2, 3)
+        c._host["k"] = k.contiguous().cpu().numpy()
+        lst = torch.zeros((1, 2, 3, 2, 4), dtype=torch.int32, device="cuda")
+        tq.select_records(q=tl.to_bf16_tensor(q, "cuda"), bounds=bounds, n_chunks=c.d_n, max_chunks=9, tail_len=c.d_len,
+                          max_tail=c.cap, keep=4, sink=1, recent=1, list=lst, count=lst[..., 0].clone(), block_table=c.table)
+        qf = synth.bf16_bits_to_f32(q).astype(np.float64)[0]
+        for b in range(2):
+            n = int(c.n[0, b])
+            for h in range(2):
+                for r in range(n):
+                    check(c, bounds, 0, b, h, r)
+            bb = np.array([[at(c, bounds, 0, b, h, r) for r in range(n)] for h in range(2)])
+            w = wanted(qf[b], bb[:, :, 0], bb[:, :, 1], n, int(c.len[0, b]), 3, 4, 1, 4, 1, 1)
+            np.testing.assert_array_equal(lst[0, b].cpu().numpy(), w)
+
+    bound()
+    agree()
+    old = bounds.clone()
+    mass = torch.rand((1, 2, 2, 9 * 128 + c.cap), device="cuda")
+    tq.evict_mass(k_codec=c.kc, v_codec=c.vc, mass=mass, n_chunks=c.d_n, max_chunks=9, tail_len=c.d_len, max_tail=c.cap,
+                  keep_chunks=5, sink=4, recent=128, **recs)
+    bound()
+    assert int(c.d_n.max()) == 5 and not torch.equal(old, bounds)
+    agree()
+    bounded = c.d_n.clone()
+    tq.tq_rollback(c.kc, c.vc, torch.tensor([[2 * 128 + 50, 3 * 128 + 7]], dtype=torch.int32, device="cuda"),
+                   max_evict=1, **recs, **ring, **counts)
+    assert c.d_n.tolist() == [[2, 3]] and c.d_len.tolist() == [[50, 7]]
+    bounded = torch.minimum(bounded, c.d_n)  # (5 would skip the next ones)
+    x = tl.to_bf16_tensor(queries(1, 2, 400, 4, 128, 53, gain=5.0), "cuda")
+    tq.tq_append(tq.make_append_args(q=None, q_out=None, k=x[..., :2, :], v=x[..., 2:, :],
+                                     positions=torch.zeros((1, 2, 400), dtype=torch.int32, device="cuda"),
+                                     inv_freq=torch.ones(64, device="cuda"), **ring,
+                                     **{w: counts[w] for w in ("tail_start", "tail_len")}))
+    tq.tq_evict(c.kc, c.vc, window=0, margin=0, max_evict=4, **recs, **ring, **counts)
+    assert c.d_n.tolist() == [[5, 6]]
+    bound(bounded)
+    agree()
