@@ -357,3 +357,65 @@ def test_ties_of_a_long_cache_take_no_square_of_it(tq, kind):
             times.append(t0.elapsed_time(t1))
         best[n] = min(times)
     assert best[16384] < 8 * best[4096]
+
+
+@pytest.mark.parametrize("d,G,T,qb,n", [(64, 3, 1, 1, 200), (128, 8, 1, 1, 256), (128, 4, 40, 16, 300), (256, 6, 2, 2, 300),
+                                        (512, 16, 4, 4, 150), (128, 64, 8, 8, 40)])
+def test_near_ties_of_full_width_operands(tq, d, G, T, qb, n):
+    """Operands of eight significant bits, queries of magnitudes 2^-16 to 1, sums that lie within a few f32 roundings
+    of one another: what the f32 scores' error bound has to cover.  Products are multiples of 2^-30 and sums below
+    2^12, so that 64 bits hold every one exactly."""
+    g = np.random.default_rng(23)
+    c = Case(seed=24, B=1, Hkv=1, d=d, G=G, T=T, qb=qb, n=n, keep=max(3, n // 3), sink=0, recent=0)
+    bf = lambda x: (np.float32(x).view(np.uint32) >> 16).astype(np.uint16)  # noqa: E731
+    size = 2.0 ** -g.integers(0, 17, d)
+    row = (1 + g.random(d)) * size * np.where(g.random(d) < 0.3, -1, 1)
+    small = np.argsort(size)[: d // 4]  # rows and records differ in the last bits of these coordinates
+    c.q[:] = bf(row.astype(np.float32))
+    c.q[..., small] += g.integers(0, 3, (*c.q.shape[:-1], len(small))).astype(np.uint16)
+    base = (1 + g.random((2, d))) * np.array([[-1.0], [1.0]])
+    c.bounds = np.broadcast_to(bf(base.astype(np.float32)), c.bounds.shape).copy()
+    c.bounds[..., small] += g.integers(0, 4, (*c.bounds.shape[:-1], len(small))).astype(np.uint16)
+    c.check(tq)
+    q = synth.bf16_bits_to_f32(c.q).astype(np.float64)[0, 0, :qb].reshape(-1, d)
+    lo, hi = (synth.bf16_bits_to_f32(np.ascontiguousarray(c.bounds[0, 0, 0, :, i])).astype(np.float64) for i in (0, 1))
+    s = (np.maximum(q, 0) @ hi.T + np.minimum(q, 0) @ lo.T).max(0)
+    terms = (np.abs(q) @ np.maximum(np.abs(lo), np.abs(hi)).T).max()
+    border = np.sort(s)[-c.keep]
+    assert (np.abs(s - border) < 2.0 ** -22 * terms).sum() >= 5  # what f32 sums may confuse
+
+
+TWO_KERNELS = {"more_than_256_records": dict(n=400, T=1, G=4, keep=32), "parts_and_shares": dict(n=90, d=128, G=16, T=300, qb=150, keep=9),
+               "ragged_parts": dict(n=60, d=512, G=64, Hkv=1, B=3, T=40, qb=40, keep=9, lens=[40, 3, 17]),
+               "ragged_counts": dict(n=300, B=4, T=3, qb=2, keep=20, counts=[[300, 0, 15, 140]], lens=[3, 3, 2, 0])}
+
+
+@pytest.mark.parametrize("name", TWO_KERNELS)
+def test_two_kernels_captured_and_replayed_over_another_calls_workspace(tq, name):
+    """Scores of parts and shares that a block does not fill are not read: a workspace of NaN bytes, then of another
+    call's scores, leaves the lists as they are."""
+    import torch
+    kw = TWO_KERNELS[name]
+    c, other = Case(seed=25, **kw), Case(seed=26, **{k: v for k, v in kw.items() if k not in ("lens", "counts")})
+    c.check(tq)
+    eager = c.list.cpu().numpy(), c.count.cpu().numpy()
+    other.run(tq)
+    a, b = tq.make_select_args(**c.kw), tq.make_select_args(**other.kw)
+    ws = torch.empty(tq.tq_select_records_workspace_size(a), dtype=torch.uint8, device="cuda")
+    assert tq.tq_select_records_workspace_size(b) == ws.numel()
+    g, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(g, stream=s):
+        tq.tq_select_records(a, ws)
+    for fill in (0xFF, 0x7F, None):
+        c.list.fill_(5)
+        c.count.fill_(5)
+        if fill is None:
+            tq.tq_select_records(b, ws)
+        else:
+            ws.fill_(fill)
+        for _ in range(2):
+            g.replay()
+        torch.cuda.synchronize()
+        np.testing.assert_array_equal(c.list.cpu().numpy(), eager[0])
+        np.testing.assert_array_equal(c.count.cpu().numpy(), eager[1])
