@@ -627,7 +627,8 @@ tq_status tq_evict_mass(const tq_evict_mass_args* args, const tq_codec* k_codec,
  * Bounds of the keys.  For coordinate j of record r of (l, b, kv head h), over
  * the record's 128 decoded keys (tq_decode's, in f32: off by at most a few ulp
  * of a key's norm) in the keys' own basis,
- *   lo_j = min_i khat_ij rounded down, hi_j = max_i khat_ij rounded up, to bf16.
+ *   lo_j = min_i khat_ij rounded down, hi_j = max_i khat_ij rounded up, to bf16
+ * (an infinity past its largest number).
  * Bounds lie as the records do: bf16 [2][head_dim] (lo, then hi) in the place
  * of a record's bytes, at
  *   bounds + l*bounds_layer_stride + ((b*n_kv_heads + h)*rec_cap + r)*2*head_dim,

@@ -12,7 +12,10 @@
 // x + 2 e are chosen, those below x - 2 e are not, and only where the records in
 // between are more than the places left are they formed again: bf16 products
 // are exact in f32, and a sum kept as two f32 has twice the bits.  So the list
-// depends on neither the order of the sums nor the split of the work.
+// depends on neither the order of the sums nor the split of the work.  The largest
+// of them are found by comparing pairs, or, of more than 64, by a selection as
+// before over 64-bit keys, whose ties a bit a record puts in order: the time grows with the
+// records however many tie (16384 of them: 53 us with queries of zeros, 0.5 ms where exact sums are formed).
 //
 // e = 2^-22 a step of the tensor core's 2 d / 16, of the largest sum of a row's
 // |terms|: measured, its f32 accumulation (16 products and the accumulator, cut off
